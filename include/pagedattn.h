@@ -68,6 +68,7 @@ typedef enum pa_status {
 #define PA_DEV_ERR_LENGTH 2u   /* a length did not fit: seq_len < 0 or > bt_stride*16, q_len > seq_len, ... */
 #define PA_DEV_ERR_TIMEOUT 4u  /* a bounded wait inside a kernel gave up (the kernel returned early) */
 #define PA_DEV_ERR_INTERNAL 8u /* a kernel found the GPU's layout not as built for (it did nothing) */
+#define PA_DEV_ERR_NO_PAGES 16u /* paged_step_plan: fewer free pages than the step's requests need */
 
 typedef struct pa_dims {
   int32_t num_q_heads;  /* Hq  (16) */
@@ -269,6 +270,115 @@ pa_status attn_prefill_chunk_ex(pa_dims dims, const void* q, const int32_t* cu_q
 pa_status attn_merge_lse(int32_t num_parts, int32_t rows, int32_t heads, int32_t head_dim,
                          const float* o_parts, const float* lse_parts, void* out,
                          float* lse_out, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * paged_step_plan / paged_release — block tables, positions and slot maps of one step, built on
+ * the GPU from request lengths, so that a step's page bookkeeping needs no host round trip and
+ * can be captured in a CUDA graph with the calls that use it.
+ *
+ * Source: the pages name KV-cache management as the runner's part ("Optimizing ASR Models to
+ * Transcribe 90-Minute Multi-Speaker Audio", "Optimization Strategies"); they give no layout.
+ *
+ * paged_step_plan: request b has cached_lens[b] tokens in the cache and gets new_lens[b] more. It
+ * needs ceil((cached + new) / 16) - ceil(cached / 16) pages, popped from the end of the free list
+ * in request order. A request is served when it needs none, or when the pages needed by it and
+ * by all requests before it do not exceed the free ones. A request that is not served keeps its
+ * rows in the packing but gets no page, its rows get slot -1 and its seq_lens stays cached_lens;
+ * PA_DEV_ERR_NO_PAGES is flagged. So is (PA_DEV_ERR_LENGTH, not served) a request with a negative
+ * length or more tokens than its table row holds.
+ *   cached_lens, new_lens  int32 [batch], batch <= 4096
+ *   block_table     int32 [batch][bt_stride], in place: entries of the new pages are written,
+ *                   the ones of cached tokens read, nothing else is touched
+ *   free_pages      int32 [free_capacity]: entries 0 .. *free_count - 1 are free
+ *   free_count      device int32; free_count_out  device int32, the count after the step (may be
+ *                   the same address)
+ *   total_rows      rows of positions and slot_map (>= the packed rows; fewer is flagged
+ *                   PA_DEV_ERR_LENGTH and the rest is not written); rows past the last request's
+ *                   are padding: position 0, slot -1
+ *   cu_new_lens     int32 [batch+1]: packed row offsets (the cu_new_lens / cu_q_lens of the calls)
+ *   seq_lens        int32 [batch]: tokens after the step (may be cached_lens itself)
+ *   positions       int32 [total_rows];  slot_map  int64 [total_rows]: page * 16 + position % 16
+ * A page outside [0, num_pages) is flagged PA_DEV_ERR_PAGE_OOB and its rows get slot -1.
+ *
+ * paged_release: the entries of logical pages [begin_pages[b], end_pages[b]) of each request are
+ * appended to the free list in (request, page) order and become -1 in the table; entries that are
+ * -1 already are skipped. (0, ceil(seq_len / 16)) gives back a finished request, a range in the
+ * middle what a sliding window has left behind. If the list has no room for all of them nothing is
+ * released (PA_DEV_ERR_LENGTH). Each page must be held by one request only.
+ * ------------------------------------------------------------------------------------------ */
+pa_status paged_step_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                          int32_t* block_table, int32_t bt_stride, const int32_t* free_pages,
+                          int32_t free_capacity, const int32_t* free_count, int64_t num_pages,
+                          int32_t total_rows, int32_t* free_count_out, int32_t* cu_new_lens,
+                          int32_t* seq_lens, int32_t* positions, int64_t* slot_map,
+                          int32_t* status, pa_stream_t stream);
+
+pa_status paged_release(const int32_t* begin_pages, const int32_t* end_pages, int32_t batch,
+                        int32_t* block_table, int32_t bt_stride, int32_t* free_pages,
+                        int32_t free_capacity, const int32_t* free_count, int64_t num_pages,
+                        int32_t* free_count_out, int32_t* status, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * rope_append_paged — rotary positions of the new tokens' q and k, and their K/V into the cache.
+ *
+ * Source: the decoder's attention takes rotated q and k, and the new tokens' K/V are in the cache
+ * before it runs (component table and "ASR Model Primer" of "Optimizing ASR Models to Transcribe
+ * 90-Minute Multi-Speaker Audio": a Qwen3 text decoder); the pages do not describe the rotation.
+ *
+ * Per row t and head of q and k, in this order: (if gamma) x <- x / sqrt(mean(x^2) + eps) * gamma
+ * over the head's 128 dims; then each pair (x1, x2) of the first rot_dim dims becomes
+ * ((x1 cos a - x2 sin a), (x2 cos a + x1 sin a)) * attn_factor with a = positions[t] * inv_freq[i];
+ * the pair i is dims (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved != 0. Dims from rot_dim
+ * on are not rotated. fp32 arithmetic, angles exact to 64-bit fractions of a turn, one rounding
+ * to bf16. v is copied bit for bit.
+ *   rot_dim      multiple of 16 in [16, 128], else PA_ERR_UNSUPPORTED
+ *   inv_freq     double [rot_dim / 2] on the device (pa_rope_inv_freq fills a host array)
+ *   q            bf16, row t at q + t * q_stride elements: [Hq][128]; k_new and v_new likewise with
+ *                [Hkv][128]. Strides are multiples of 8 and at least a row (slices of one fused
+ *                projection are fine).
+ *   positions    int32 [rows], any value;  slot_map  int64 [rows]: page * 16 + slot of each row.
+ *                A negative slot marks padding: the row is not read into anything and nothing is
+ *                written for it. A slot past the pool is flagged PA_DEV_ERR_PAGE_OOB and treated
+ *                the same way. Two rows must not have the same slot.
+ *   q_gamma, k_gamma  fp32 [128] or NULL (no norm)
+ *   q_out        bf16 [rows][Hq][128]; may be q itself if q_stride is Hq * 128, and must not
+ *                overlap the inputs otherwise
+ *   k_pool, v_pool  written in place at the slots; nothing else changes
+ * q, k_new, v_new, q_out, pools and gammas 16-byte aligned.
+ *
+ * pa_rope_inv_freq — frequencies theta^(-2i / rot_dim), stretched for contexts longer than the
+ * model's, into the host array inv_freq [rot_dim / 2], and the factor for cos and sin.
+ *   PA_ROPE_NONE (or scaling NULL);  PA_ROPE_LINEAR: divided by factor;  PA_ROPE_NTK: theta *
+ *   factor^(rot_dim / (rot_dim - 2));  PA_ROPE_LLAMA3: divided by factor where a pair makes fewer
+ *   than low_freq_factor turns over original_max_position, kept where more than high_freq_factor,
+ *   blended between;  PA_ROPE_YARN: the same with a ramp over the pair index between the pairs
+ *   that make beta_fast and beta_slow turns, and attn_factor (0: 0.1 ln(factor) + 1).
+ * ------------------------------------------------------------------------------------------ */
+#define PA_ROPE_NONE 0
+#define PA_ROPE_LINEAR 1
+#define PA_ROPE_NTK 2
+#define PA_ROPE_LLAMA3 3
+#define PA_ROPE_YARN 4
+
+typedef struct pa_rope_scaling {
+  int32_t kind;
+  double factor;
+  double original_max_position;             /* llama3, yarn */
+  double low_freq_factor, high_freq_factor; /* llama3 */
+  double beta_fast, beta_slow, attn_factor; /* yarn */
+} pa_rope_scaling;
+
+pa_status pa_rope_inv_freq(int32_t rot_dim, double theta, const pa_rope_scaling* scaling,
+                           double* inv_freq, float* attn_factor);
+
+pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t interleaved,
+                            const double* inv_freq, float attn_factor, const void* q,
+                            int64_t q_stride, const void* k_new, int64_t k_stride,
+                            const void* v_new, int64_t v_stride, int32_t rows,
+                            const int32_t* positions, const int64_t* slot_map,
+                            const float* q_gamma, const float* k_gamma, float eps, void* q_out,
+                            void* k_pool, void* v_pool, int64_t num_pages, int32_t* status,
+                            pa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * adaptor_mlp_merge4 — the audio-text bridge that turns encoder frames into decoder embeddings.

@@ -10,9 +10,13 @@ Calls (same names as the C ABI):
 * ``attn_decode_paged`` one decode step over a paged KV cache (split-KV + log-sum-exp merge)
 * ``attn_prefill_chunk`` causal attention of query chunks over their cached prefix + themselves
 * ``attn_merge_lse``    combine partial results over disjoint key sets
+* ``paged_step_plan``   block tables, positions and slot maps of a step from request lengths
+* ``paged_release``     give pages of finished or windowed requests back to the free list
+* ``rope_append_paged`` rotary positions of new q and k rows, K/V written into their slots
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -24,13 +28,17 @@ __all__ = [
     "attn_merge_lse", "adaptor_mlp_merge4", "adaptor_workspace_size", "LaunchOpts",
     "decode_workspace_size", "decode_kernels_per_call", "prefill_workspace_size",
     "read_device_status", "debug_decode_starve",
-    "DEV_ERR_PAGE_OOB", "DEV_ERR_LENGTH", "DEV_ERR_TIMEOUT", "DEV_ERR_INTERNAL", "lib_path",
+    "paged_step_plan", "StepPlan", "paged_release", "rope_append_paged", "rope_inv_freq",
+    "RopeScaling",
+    "DEV_ERR_PAGE_OOB", "DEV_ERR_LENGTH", "DEV_ERR_TIMEOUT", "DEV_ERR_INTERNAL",
+    "DEV_ERR_NO_PAGES", "lib_path",
 ]
 
 DEV_ERR_PAGE_OOB = 1
 DEV_ERR_LENGTH = 2
 DEV_ERR_TIMEOUT = 4
 DEV_ERR_INTERNAL = 8
+DEV_ERR_NO_PAGES = 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -68,6 +76,15 @@ class LaunchOpts(ctypes.Structure):
     _fields_ = [("max_ctas", ctypes.c_int32)]
 
 
+class RopeScaling(ctypes.Structure):
+    """pa_rope_scaling."""
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_max_position", ctypes.c_double),
+                ("low_freq_factor", ctypes.c_double), ("high_freq_factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attn_factor", ctypes.c_double)]
+
+
 def _opts(max_ctas):
     if max_ctas is None:
         return None, None
@@ -97,6 +114,13 @@ _SIGS = {
     "attn_merge_lse": (_I32, [_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "pa_adaptor_workspace_size": (_SZ, [_I32]),
     "adaptor_mlp_merge4": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _SZ, _P, _P]),
+    "paged_step_plan": (_I32, [_P, _P, _I32, _P, _I32, _P, _I32, _P, _I64, _I32, _P, _P, _P, _P, _P,
+                               _P, _P]),
+    "paged_release": (_I32, [_P, _P, _I32, _P, _I32, _P, _I32, _P, _I64, _P, _P, _P]),
+    "pa_rope_inv_freq": (_I32, [_I32, ctypes.c_double, ctypes.POINTER(RopeScaling), _P,
+                                ctypes.POINTER(_F)]),
+    "rope_append_paged": (_I32, [Dims, _I32, _I32, _P, _F, _P, _I64, _P, _I64, _P, _I64, _I32, _P,
+                                 _P, _P, _P, _F, _P, _P, _P, _I64, _P, _P]),
     "pa_read_device_status": (_I32, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
     "pa_status_string": (ctypes.c_char_p, [_I32]),
     "pa_last_error": (ctypes.c_char_p, []),
@@ -399,6 +423,174 @@ def attn_merge_lse(o_parts, lse_parts, *, out=None, lse_out=None, stream=None):
     _check("attn_merge_lse", lib.attn_merge_lse(S, R, H, D, _ptr(o_parts), _ptr(lse_parts),
                                                 _ptr(out), _ptr(lse_out), _stream(stream)))
     return out, lse_out
+
+
+# ----------------------------------------------------------------------------------------------
+# page tables and rotary positions
+# ----------------------------------------------------------------------------------------------
+StepPlan = collections.namedtuple("StepPlan",
+                                  "cu_new_lens seq_lens positions slot_map free_count")
+
+
+def _new_or_given(t, name, dtype, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _given(t, name, dtype, shape)
+    return t
+
+
+def paged_step_plan(cached_lens, new_lens, block_table, free_pages, free_count, num_pages: int, *,
+                    total_rows: int, free_count_out=None, cu_new_lens=None, seq_lens=None,
+                    positions=None, slot_map=None, status=None, stream=None) -> StepPlan:
+    """Pages, positions and slots of a step that adds new_lens[b] tokens to request b's
+    cached_lens[b]. block_table is updated in place; returns StepPlan(cu_new_lens [B+1],
+    seq_lens [B], positions [total_rows], slot_map int64 [total_rows], free_count [1]).
+
+    free_pages[:free_count] are free; pages are taken from its end, in request order. Requests
+    that the free pages do not cover are left as they are (their rows get slot -1,
+    DEV_ERR_NO_PAGES). free_count_out may be free_count, seq_lens may be cached_lens."""
+    for t, n, d in ((cached_lens, "cached_lens", 1), (new_lens, "new_lens", 1),
+                    (block_table, "block_table", 2), (free_pages, "free_pages", 1),
+                    (free_count, "free_count", 1)):
+        _need(t, n, torch.int32, d)
+    B = cached_lens.shape[0]
+    _shape("new_lens", new_lens, (B,))
+    _rows_at_least("block_table", block_table, B)
+    _rows_at_least("free_count", free_count, 1)
+    dev = cached_lens.device
+    total_rows = int(total_rows)
+    if total_rows < 0:
+        raise ValueError("total_rows must be >= 0")
+    free_count_out = _new_or_given(free_count_out, "free_count_out", torch.int32, (1,), dev)
+    cu_new_lens = _new_or_given(cu_new_lens, "cu_new_lens", torch.int32, (B + 1,), dev)
+    seq_lens = _new_or_given(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    positions = _new_or_given(positions, "positions", torch.int32, (total_rows,), dev)
+    slot_map = _new_or_given(slot_map, "slot_map", torch.int64, (total_rows,), dev)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _on_device("paged_step_plan", cached_lens, new_lens, block_table, free_pages, free_count,
+               free_count_out, cu_new_lens, seq_lens, positions, slot_map, status)
+    _check("paged_step_plan", load().paged_step_plan(
+        _ptr(cached_lens), _ptr(new_lens), B, _ptr(block_table), block_table.shape[1],
+        _ptr(free_pages), free_pages.shape[0], _ptr(free_count), int(num_pages), total_rows,
+        _ptr(free_count_out), _ptr(cu_new_lens), _ptr(seq_lens), _ptr(positions), _ptr(slot_map),
+        _ptr(status), _stream(stream)))
+    return StepPlan(cu_new_lens, seq_lens, positions, slot_map, free_count_out)
+
+
+def paged_release(begin_pages, end_pages, block_table, free_pages, free_count, num_pages: int, *,
+                  free_count_out=None, status=None, stream=None):
+    """Append the pages of each request's logical range [begin_pages[b], end_pages[b]) to
+    free_pages and set their block_table entries to -1 (entries that are -1 are skipped).
+    Returns the new free count [1] (free_count_out, which may be free_count)."""
+    for t, n, d in ((begin_pages, "begin_pages", 1), (end_pages, "end_pages", 1),
+                    (block_table, "block_table", 2), (free_pages, "free_pages", 1),
+                    (free_count, "free_count", 1)):
+        _need(t, n, torch.int32, d)
+    B = begin_pages.shape[0]
+    _shape("end_pages", end_pages, (B,))
+    _rows_at_least("block_table", block_table, B)
+    _rows_at_least("free_count", free_count, 1)
+    free_count_out = _new_or_given(free_count_out, "free_count_out", torch.int32, (1,),
+                                   begin_pages.device)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _on_device("paged_release", begin_pages, end_pages, block_table, free_pages, free_count,
+               free_count_out, status)
+    _check("paged_release", load().paged_release(
+        _ptr(begin_pages), _ptr(end_pages), B, _ptr(block_table), block_table.shape[1],
+        _ptr(free_pages), free_pages.shape[0], _ptr(free_count), int(num_pages),
+        _ptr(free_count_out), _ptr(status), _stream(stream)))
+    return free_count_out
+
+
+_ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
+
+
+def rope_inv_freq(rot_dim: int = 128, theta: float = 1e6, *, scaling: str = "none",
+                  factor: float = 1.0, original_max_position: float = 32768,
+                  low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0, attn_factor: float = 0.0,
+                  device=None):
+    """Rotary frequencies in 64 bits [rot_dim / 2], stretched for long contexts, and the factor for
+    cos and sin: (inv_freq, attn_factor) for rope_append_paged. scaling: none, linear, ntk, llama3
+    or yarn (pa_rope_inv_freq). On the current CUDA device unless device says otherwise."""
+    if scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_KINDS)}, got {scaling!r}")
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be a positive even number")
+    sc = RopeScaling(_ROPE_KINDS[scaling], factor, original_max_position, low_freq_factor,
+                     high_freq_factor, beta_fast, beta_slow, attn_factor)
+    host = (ctypes.c_double * (rot_dim // 2))()
+    a = ctypes.c_float(0.0)
+    _check("pa_rope_inv_freq", load().pa_rope_inv_freq(rot_dim, theta, ctypes.byref(sc), host,
+                                                       ctypes.byref(a)))
+    freq = torch.tensor(list(host), dtype=torch.float64,
+                        device="cuda" if device is None else device)
+    return freq, float(a.value)
+
+
+def _rows_strided(t, name, heads):
+    """A [T, heads, 128] bf16 tensor whose rows may lie apart; returns their stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
+    T, h, d = t.shape
+    if heads is not None and (h, d) != (heads, 128):
+        raise ValueError(f"{name} must have shape ('*', {heads}, 128), got {tuple(t.shape)}")
+    row, head, dim = t.stride()
+    if (dim != 1 and d > 1) or (head != d and h > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return row if T > 1 else h * d
+
+
+def rope_append_paged(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq, *,
+                      interleaved: bool = False, attn_factor: float = 1.0, q_gamma=None,
+                      k_gamma=None, eps: float = 1e-6, q_out=None, status=None, stream=None,
+                      dims=None):
+    """Rotate (and, with gammas, RMS-normalise per head) q [T, Hq, 128] and k_new [T, Hkv, 128] at
+    their positions, write k and v into the pools at slot_map (negative: padding row, left
+    alone). Returns q_out [T, Hq, 128]. rot_dim is 2 * len(inv_freq); rows of q, k_new and v_new
+    may be strided (slices of one projection)."""
+    heads = _heads(dims)
+    qs = _rows_strided(q, "q", None if heads is None else heads[0])
+    ks = _rows_strided(k_new, "k_new", None if heads is None else heads[1])
+    vs = _rows_strided(v_new, "v_new", None if heads is None else heads[1])
+    T = q.shape[0]
+    _need(positions, "positions", torch.int32, 1)
+    _need(slot_map, "slot_map", torch.int64, 1)
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    for t, n in ((k_new, "k_new"), (v_new, "v_new"), (positions, "positions"),
+                 (slot_map, "slot_map")):
+        if t.shape[0] != T:
+            raise ValueError(f"{n} must have {T} rows, got {t.shape[0]}")
+    _need(k_pool, "k_pool", torch.bfloat16, 4)
+    _need(v_pool, "v_pool", torch.bfloat16, 4)
+    if heads is not None:
+        _pools(k_pool, v_pool, heads[1])
+    for t, n in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
+        if t is not None:
+            _need(t, n, torch.float32, 1)
+            _shape(n, t, (128,))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _given(q_out, "q_out", torch.bfloat16, tuple(q.shape))
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _on_device("rope_append_paged", q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq,
+               q_gamma, k_gamma, q_out, status)
+    _check("rope_append_paged", load().rope_append_paged(
+        _dims(dims), 2 * inv_freq.shape[0], 1 if interleaved else 0, _ptr(inv_freq),
+        float(attn_factor), _ptr(q), qs, _ptr(k_new), ks, _ptr(v_new), vs, T, _ptr(positions),
+        _ptr(slot_map), _ptr(q_gamma), _ptr(k_gamma), float(eps), _ptr(q_out), _ptr(k_pool),
+        _ptr(v_pool), k_pool.shape[0], _ptr(status), _stream(stream)))
+    return q_out
 
 
 def adaptor_workspace_size(num_frames: int) -> int:
