@@ -861,7 +861,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
                  : "memory");
   };
   auto page_entry = [&](int lp) {
-    int e = preload ? s.pages[lp] : bt_row[lp];
+    // (a device length past the host's bound, flagged above, has pages that were not preloaded)
+    int e = preload && lp < pmax ? s.pages[lp] : bt_row[lp];
     if (e < 0 || e >= p.num_pages) {
       if (lane == 0) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
       e = 0;
