@@ -254,6 +254,56 @@ pa_status attn_prefill_chunk_ex(pa_dims dims, const void* q, const int32_t* cu_q
                                 pa_stream_t stream, const pa_launch_opts* opts);
 
 /* ------------------------------------------------------------------------------------------
+ * attn_decode_paged_score / attn_prefill_chunk_score — the two attention calls with score
+ * options: capped scores, a distance bias, and masks beyond the causal one.
+ *
+ * Source: long recordings are decoded with the audio prompt in front of the transcript
+ * ("Optimizing ASR Models to Transcribe 90-Minute Multi-Speaker Audio", "ASR Model Primer"); the
+ * pages describe no mask or bias beyond the causal one.
+ *
+ * The arguments are those of the _ex calls plus score (NULL = the _ex call). The query row at
+ * position i (decode: the sequence's last key) sees key j of its sequence's L keys when
+ *     j < prefix_lens[b],   or   max(row_start[row], i - window + 1) <= j <= i
+ * and its score is, in this order,
+ *     s = softmax_scale <q, k_j>;  softcap > 0: s <- softcap tanh(s / softcap);
+ *     alibi_slopes: s <- s - alibi_slopes[h] |i - j|.
+ * A row that sees no key, or whose visible scores are all -inf, gets o = 0, lse = -inf.
+ * K and V of keys that no row of the call sees are never used, whatever they hold; pages whose
+ * keys no row of a sequence (decode) or of a 128-row tile of its chunk (prefill) sees are not
+ * read, and their block-table entries may be anything (-1 after paged_release).
+ *   softcap         >= 0; 0: no cap
+ *   alibi_slopes    fp32 [Hq] on the device, or NULL
+ *   window          >= 0; 0: no limit. A row sees its own position and the window - 1 before it
+ *   prefix_lens     int32 [batch] on the device, or NULL: keys seen by every row of the sequence,
+ *                   before or after it (a key that is not in the cache yet is not seen: a prompt
+ *                   longer than a chunk is seen as far as it has been appended)
+ *   max_prefix_len  host upper bound of prefix_lens (<= 131072); larger values and negative ones
+ *                   are cut and flagged PA_DEV_ERR_LENGTH; 0: no prefix
+ *   row_start       int32 on the device, per query row ([batch] / [total_q]), or NULL: first key
+ *                   of the row's document; past i: the row sees the prefix only
+ * attn_prefill_chunk_score takes its workspace size from pa_prefill_score_workspace_size; the
+ * decode's is pa_decode_workspace_size. Scores without options give what the plain call gives
+ * up to rounding.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct pa_score_opts {
+  float softcap;
+  const float* alibi_slopes;
+  int32_t window;
+  const int32_t* prefix_lens;
+  int32_t max_prefix_len;
+  const int32_t* row_start;
+} pa_score_opts;
+
+pa_status attn_decode_paged_score(pa_dims dims, const void* q, const void* k_pool,
+                                  const void* v_pool, int64_t num_pages,
+                                  const int32_t* block_table, int32_t bt_stride,
+                                  const int32_t* seq_lens, int32_t batch, int32_t max_seq_len,
+                                  float softmax_scale, int32_t split_tokens, void* out,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  int32_t* status, pa_stream_t stream, const pa_launch_opts* opts,
+                                  const pa_score_opts* score);
+
+/* ------------------------------------------------------------------------------------------
  * attn_merge_lse — combine attention results computed over disjoint key sets.
  *
  * Source: the split-KV form of the decode step (long caches are cut into key ranges whose

@@ -29,7 +29,7 @@ __all__ = [
     "decode_workspace_size", "decode_kernels_per_call", "prefill_workspace_size",
     "read_device_status", "debug_decode_starve",
     "paged_step_plan", "StepPlan", "paged_release", "rope_append_paged", "rope_inv_freq",
-    "RopeScaling",
+    "RopeScaling", "ScoreOpts",
     "DEV_ERR_PAGE_OOB", "DEV_ERR_LENGTH", "DEV_ERR_TIMEOUT", "DEV_ERR_INTERNAL",
     "DEV_ERR_NO_PAGES", "lib_path",
 ]
@@ -76,6 +76,13 @@ class LaunchOpts(ctypes.Structure):
     _fields_ = [("max_ctas", ctypes.c_int32)]
 
 
+class ScoreOpts(ctypes.Structure):
+    """pa_score_opts (device pointers as integers)."""
+    _fields_ = [("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int32), ("prefix_lens", ctypes.c_void_p),
+                ("max_prefix_len", ctypes.c_int32), ("row_start", ctypes.c_void_p)]
+
+
 class RopeScaling(ctypes.Structure):
     """pa_rope_scaling."""
     _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
@@ -111,6 +118,8 @@ _SIGS = {
                                     _P, _P, _SZ, _P, _P, _P]),
     "attn_prefill_chunk_ex": (_I32, [Dims, _P, _P, _I32, _P, _P, _I64, _P, _I32, _P, _I32, _I32,
                                      _I32, _F, _P, _P, _P, _SZ, _P, _P, _P]),
+    "attn_decode_paged_score": (_I32, [Dims, _P, _P, _P, _I64, _P, _I32, _P, _I32, _I32, _F, _I32,
+                                       _P, _P, _P, _SZ, _P, _P, _P, ctypes.POINTER(ScoreOpts)]),
     "attn_merge_lse": (_I32, [_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "pa_adaptor_workspace_size": (_SZ, [_I32]),
     "adaptor_mlp_merge4": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _SZ, _P, _P]),
@@ -275,14 +284,43 @@ def _workspace(nbytes, device, workspace):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _score(call, hq, batch, rows, max_seq_len, softcap, alibi_slopes, window, prefix_lens,
+           max_prefix_len, row_start):
+    """The score options as a ScoreOpts, or None when none is set. Tensors are checked here; the
+    caller keeps them alive until the call has been made."""
+    if (not softcap and alibi_slopes is None and not window and prefix_lens is None
+            and row_start is None):
+        return None
+    for t, n, d, shape in ((alibi_slopes, "alibi_slopes", torch.float32, hq),
+                           (prefix_lens, "prefix_lens", torch.int32, batch),
+                           (row_start, "row_start", torch.int32, rows)):
+        if t is not None:
+            _need(t, n, d, 1)
+            if n == "alibi_slopes":
+                _shape(n, t, (shape,))
+            else:
+                _rows_at_least(n, t, shape)
+    _on_device(call, alibi_slopes, prefix_lens, row_start)
+    if max_prefix_len is None:
+        max_prefix_len = max_seq_len if prefix_lens is not None else 0
+    return ScoreOpts(float(softcap), 0 if alibi_slopes is None else alibi_slopes.data_ptr(),
+                     int(window), 0 if prefix_lens is None else prefix_lens.data_ptr(),
+                     int(max_prefix_len), 0 if row_start is None else row_start.data_ptr())
+
+
 def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int,
                       softmax_scale: float, *, split_tokens: int = 0, out=None, lse=None,
                       workspace=None, status=None, stream=None, want_lse=True, dims=None,
-                      max_ctas=None):
+                      max_ctas=None, softcap: float = 0.0, alibi_slopes=None, window: int = 0,
+                      prefix_lens=None, max_prefix_len=None, row_start=None):
     """Decode attention: q [B, Hq, D] over each sequence's cached keys. Returns (out, lse).
 
     split_tokens: keys per split-KV range (whole pages); 0 = one equal share per SM.
-    max_ctas: cap on the persistent grid (attn_decode_paged_ex); None = the plain call."""
+    max_ctas: cap on the persistent grid (attn_decode_paged_ex); None = the plain call.
+
+    Score options (attn_decode_paged_score). Key j is seen from position i when j < prefix_lens[b]
+    or max(row_start[b], i - window + 1) <= j <= i; its score is softcap * tanh(s / softcap) minus
+    alibi_slopes[h] * |i - j|. max_prefix_len: host bound of prefix_lens (default max_seq_len)."""
     _need(q, "q", torch.bfloat16, 3)
     _need(k_pool, "k_pool", torch.bfloat16, 4)
     _need(v_pool, "v_pool", torch.bfloat16, 4)
@@ -313,7 +351,12 @@ def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int
             int(split_tokens), _ptr(out), _ptr(lse), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
     keep, ref = _opts(max_ctas)
-    if ref is None:
+    score = _score("attn_decode_paged", q.shape[1], B, B, int(max_seq_len), softcap, alibi_slopes,
+                   window, prefix_lens, max_prefix_len, row_start)
+    if score is not None:
+        _check("attn_decode_paged_score", lib.attn_decode_paged_score(*args, ref,
+                                                                      ctypes.byref(score)))
+    elif ref is None:
         _check("attn_decode_paged", lib.attn_decode_paged(*args))
     else:
         _check("attn_decode_paged_ex", lib.attn_decode_paged_ex(*args, ref))

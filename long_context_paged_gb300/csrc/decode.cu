@@ -36,6 +36,7 @@
 
 #include "cluster_common.cuh"
 #include "pa_common.cuh"
+#include "score_common.cuh"
 
 namespace pa {
 namespace {
@@ -75,6 +76,7 @@ struct DecodeSmem {
 static_assert(sizeof(DecodeSmem) <= 227 * 1024, "decode shared memory beyond the per-CTA limit");
 
 struct DecodeParams {
+  static constexpr bool kScore = false;
   int32_t hq;           // query heads of the call (2 x its KV heads)
   int32_t stage_pages;  // pages per ring stage: 8 / KV heads
   const uint16_t* q;
@@ -100,6 +102,13 @@ struct DecodeParams {
   int32_t starve;          // test hook: CTA 0 never fills its first ring stage
 };
 
+// The same call with score options (attn_decode_paged_score). scale_log2 then is what q is
+// multiplied by: softmax_scale * log2 e, or with a cap softmax_scale / cap (the tanh's argument).
+struct DecodeScoreParams : DecodeParams {
+  static constexpr bool kScore = true;
+  ScoreParams score;
+};
+
 // Maximum of v over the 32 lanes of the warp, in every lane (redux.sync on fp32, sm_100 and
 // later; like fmaxf, a NaN operand is ignored when another lane holds a number).
 __device__ __forceinline__ float warp_max(float v) {
@@ -120,6 +129,62 @@ __device__ __forceinline__ int clamp_len(const DecodeParams& p, int b, bool repo
   return L;
 }
 
+// The pages of sequence b that hold a visible key, as a list: the whole cache (page i of the list is
+// page i), or with score options the prefix's pages [0, n1) and then the own keys' from page w0 on.
+template <class P>
+struct SeqView {
+  int L, pages;
+  __device__ __forceinline__ int page_at(int i) const { return i; }
+};
+template <>
+struct SeqView<DecodeScoreParams> {
+  int L, pages;
+  int prefix, lo;  // visible: key < prefix, or lo <= key < L
+  int n1, w0;
+  __device__ __forceinline__ int page_at(int i) const { return i < n1 ? i : i - n1 + w0; }
+  // visible keys of page pg, bit t = key 16 pg + t
+  __device__ __forceinline__ uint32_t mask(int pg) const {
+    const int k0 = pg * kPage;
+    auto below = [](int n) { return n >= kPage ? 0xffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+    return below(prefix - k0) | (below(L - k0) & ~below(lo - k0));
+  }
+  // distance of the nearest visible key (0 when the row sees its own position)
+  __device__ __forceinline__ int nearest() const { return lo < L ? 0 : L - prefix; }
+};
+
+__device__ __forceinline__ SeqView<DecodeParams> seq_view(const DecodeParams& p, int b, bool report) {
+  SeqView<DecodeParams> v;
+  v.L = clamp_len(p, b, report);
+  v.pages = (v.L + kPage - 1) / kPage;
+  return v;
+}
+__device__ __forceinline__ SeqView<DecodeScoreParams> seq_view(const DecodeScoreParams& p, int b,
+                                                               bool report) {
+  SeqView<DecodeScoreParams> v;
+  v.L = clamp_len(p, b, report);
+  v.prefix = min(score_prefix(p.score, b, p.status, report), v.L);
+  v.lo = min(score_first_key(p.score, b, v.L - 1), v.L);
+  const int np = (v.L + kPage - 1) / kPage;
+  v.n1 = (v.prefix + kPage - 1) / kPage;
+  v.w0 = v.lo < v.L ? max(v.lo / kPage, v.n1) : np;
+  v.pages = v.n1 + np - v.w0;
+  return v;
+}
+
+// 1 / l of a softmax sum: 0 when nothing carried weight (no key visible, or every score -inf)
+__device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.f ? 0.f : 1.0f / l; }
+
+// The part of the log-sum-exp that the kernels leave out: they count a bias's distances from the
+// nearest visible key (see ScoreParams).
+template <class P>
+__device__ __forceinline__ float lse_shift(const P& p, int b, int h) {
+  if constexpr (P::kScore) {
+    if (p.score.slopes != nullptr && p.score.row_start != nullptr)
+      return -p.score.slopes[h] * static_cast<float>(seq_view(p, b, false).nearest());
+  }
+  return 0.f;
+}
+
 __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -130,12 +195,13 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
 }
 
 // prefix[b] = first global page of sequence b, prefix[batch] = total pages.
-__device__ void build_prefix(const DecodeParams& p, DecodeSmem& s) {
+template <class P>
+__device__ void build_prefix(const P& p, DecodeSmem& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   int local = 0;
-  for (int b = b0; b < b1; ++b) local += (clamp_len(p, b, blockIdx.x == 0) + kPage - 1) / kPage;
+  for (int b = b0; b < b1; ++b) local += seq_view(p, b, blockIdx.x == 0).pages;
   const int incl = warp_incl_scan(local, lane);
   if (lane == 31) s.warp_tot[warp] = incl;
   __syncthreads();
@@ -149,7 +215,7 @@ __device__ void build_prefix(const DecodeParams& p, DecodeSmem& s) {
   int run = s.warp_tot[warp] + incl - local;
   for (int b = b0; b < b1; ++b) {
     s.prefix[b] = run;
-    run += (clamp_len(p, b, false) + kPage - 1) / kPage;
+    run += seq_view(p, b, false).pages;
   }
   if (tid == 0) s.prefix[p.batch] = s.total;
   __syncthreads();
@@ -168,8 +234,8 @@ __device__ __forceinline__ int find_seq(const int32_t* prefix, int batch, int x)
 // kHkvT: KV heads of the call (8 for the decoder; 1, 2 or 4 for a device's share of them).
 // Consumer warp w serves KV head (w % 8) % kHkvT of page slot (w % 8) / kHkvT of each stage, tokens
 // 8 * (w / 8) .. +7 of each page.
-template <int kHkvT>
-__global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const DecodeParams p) {
+template <int kHkvT, class P>
+__global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const P p) {
   constexpr int kSlots = kHkv / kHkvT;                        // pages per stage
   constexpr int kHqT = kGroup * kHkvT;
   constexpr uint32_t kPageBytes = kPage * kHkvT * kHeadDim * 2;  // K (or V) of one page
@@ -207,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
   // beside the length instead of after it, and used only once the length confirms them.
   const int total_spec = (p.max_seq_len + kPage - 1) / kPage;
   int spec_entry = 0;
-  if (p.batch == 1 && warp == kConsumerWarps) {
+  if (!P::kScore && p.batch == 1 && warp == kConsumerWarps) {
     const int W_s = max((total_spec + p.max_ranges - 1) / p.max_ranges, base);
     const int P0_s = static_cast<int>(blockIdx.x) * W_s;
     if (lane < min(W_s, total_spec - P0_s) && P0_s + lane < p.bt_stride)
@@ -243,15 +309,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
         const int lp0 = max(P0, s.prefix[b]) - s.prefix[b];
         const int lp1 = min(P1, s.prefix[b + 1]) - s.prefix[b];
         const int32_t* bt_row = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
+        const auto view = seq_view(p, b, false);
         for (int lp = lp0; ok && lp < lp1; lp += 32) {
           const int n = min(32, lp1 - lp);
           // the entries loaded before the length are this CTA's first 32 when the length gave
           // the same page count as the bound (then W and this range are the ones assumed)
-          const bool spec = p.batch == 1 && total == total_spec && rg == static_cast<int>(blockIdx.x) &&
+          const bool spec = !P::kScore && p.batch == 1 && total == total_spec && rg == static_cast<int>(blockIdx.x) &&
                             lp == lp0;
           int entry = 0;
           if (lane < n) {
-            entry = spec ? spec_entry : bt_row[lp + lane];
+            entry = spec ? spec_entry : bt_row[view.page_at(lp + lane)];
             if (entry < 0 || entry >= p.num_pages) {
               flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
               entry = 0;
@@ -333,7 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
       const int lp0 = max(P0, s.prefix[b]) - s.prefix[b];
       const int lp1 = min(P1, s.prefix[b + 1]) - s.prefix[b];
       if (lp0 >= lp1) continue;
-      const int L = clamp_len(p, b, false);
+      const auto view = seq_view(p, b, false);
+      const int L = view.L;
+      float slope2 = 0.f;  // of the head whose score this lane keeps
+      if constexpr (P::kScore) {
+        if (p.score.slopes != nullptr) slope2 = slope_log2(p.score, 2 * g + (hi_head ? 1 : 0));
+      }
 
       // q of the two heads in this lane's order: its own head (the one whose score it keeps
       // after the scatter) first
@@ -359,7 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
       for (int lp0s = lp0; lp0s < lp1; lp0s += kSlots) {
         const int lp = lp0s + slot;               // this warp's page of the stage
         const bool active = lp < lp1;             // (a stage may hold fewer than kSlots pages)
-        const int n_valid = active ? min(kPage, L - lp * kPage) : 0;
+        const int pg = view.page_at(lp);
+        int n_valid = active ? min(kPage, L - lp * kPage) : 0;
+        uint32_t seen = 0;  // visible keys of the page (score options; else the first n_valid)
+        if constexpr (P::kScore) {
+          seen = active ? view.mask(pg) : 0u;
+          n_valid = __popc(seen);
+        }
         bool ok = true;
         if (!mbar_wait_bounded(&s.full[stage], phase, p.wait_limit_ns)) {
           flag_error(p.status, PA_DEV_ERR_TIMEOUT);
@@ -404,7 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
             for (int i = 0; i < w; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[w + i], w);
           }
           v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
-          const float sc = (kFull || tok0 + (c & 3) < n_valid) ? v[0] : -CUDART_INF_F;
+          float sc;
+          if constexpr (P::kScore) {
+            const int tok = tok0 + (c & 3);
+            sc = kFull || (seen >> tok & 1u)
+                     ? score_of(p.score, v[0], slope2, L - 1 - (pg * kPage + tok) - view.nearest())
+                     : -CUDART_INF_F;
+          } else {
+            sc = (kFull || tok0 + (c & 3) < n_valid) ? v[0] : -CUDART_INF_F;
+          }
 
           // ---- page max per head over this warp's 8 tokens (one warp-wide max reduction per
           //      head), lazily moved running max
@@ -428,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
           // empty: its max is still -inf and the probability is 0; on a full page the max is
           // finite by now)
           const float mh = hi_head ? m_b : m_a;
-          const float pr = (!kFull && sc == -CUDART_INF_F) ? 0.f : fast_exp2(sc - mh);
+          // (with a bias, a visible key's score may be -inf as well)
+          const float pr = ((!kFull || P::kScore) && sc == -CUDART_INF_F) ? 0.f : fast_exp2(sc - mh);
           l_part += pr;
 
           // ---- hand probabilities to the lanes that own the V dims, each stored twice (the
@@ -449,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
           // ---- o += p v over this lane's 4 tokens (invalid slots of a partial page skipped)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (kFull || tok0 + j < n_valid) {
+            if (kFull || (P::kScore ? (seen >> (tok0 + j) & 1u) != 0 : tok0 + j < n_valid)) {
               const uint4 vr = lds128(Vs + (tok0 + j) * kTokenBytes);
               const float2 v0 = make_float2(bf16lo(vr.x), bf16hi(vr.x));
               const float2 v1 = make_float2(bf16lo(vr.y), bf16hi(vr.y));
@@ -541,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
 
       // (with several pages per stage a warp pair may have seen no page of this range: l = 0,
       // and its record is o = 0, lse = -inf, which the merge weighs by 0)
-      const float inv = (kSlots == 1 || l_h > 0.f) ? 1.0f / l_h : 0.f;
+      const float inv = P::kScore ? inverse_or_zero(l_h) : (kSlots == 1 || l_h > 0.f) ? 1.0f / l_h : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] *= inv;
       const float lse_h = (m_h + log2f(l_h)) * kLn2;
@@ -552,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const Decod
         w.z = pack_bf16x2(o[4], o[5]);
         w.w = pack_bf16x2(o[6], o[7]);
         *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * kHqT + head) * kHeadDim + 8 * c) = w;
-        if (c == 0 && p.lse != nullptr) p.lse[b * kHqT + head] = lse_h;
+        if (c == 0 && p.lse != nullptr) p.lse[b * kHqT + head] = lse_h + lse_shift(p, b, head);
       } else {
         // unique per (sequence, range, page slot): the records of sequence b are
         // b * kSlots + k for k = range * kSlots + slot over the ranges that touch it
@@ -584,13 +671,14 @@ constexpr int kMergePrefixBatch = 64;  // batches this small: page range compute
 // computed them. For a small batch every warp derives them from the lengths with the split
 // kernel's own arithmetic while the split kernel still runs; a large batch reads them from the
 // workspace after the wait. Contains the grid dependency wait.
-__device__ __forceinline__ void merge_seq_range(const DecodeParams& p, int b, int lane, int& p0,
+template <class P>
+__device__ __forceinline__ void merge_seq_range(const P& p, int b, int lane, int& p0,
                                                 int& p1, int& W) {
   p0 = p1 = W = 0;
   const bool early = p.batch <= kMergePrefixBatch;
   if (early) {
-    const int n0 = lane < p.batch ? (clamp_len(p, lane, false) + kPage - 1) / kPage : 0;
-    const int n1 = lane + 32 < p.batch ? (clamp_len(p, lane + 32, false) + kPage - 1) / kPage : 0;
+    const int n0 = lane < p.batch ? seq_view(p, lane, false).pages : 0;
+    const int n1 = lane + 32 < p.batch ? seq_view(p, lane + 32, false).pages : 0;
     int before = (lane < b ? n0 : 0) + (lane + 32 < b ? n1 : 0), total = n0 + n1;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
@@ -611,8 +699,8 @@ __device__ __forceinline__ void merge_seq_range(const DecodeParams& p, int b, in
   }
 }
 
-template <int kWarps>
-__global__ void __launch_bounds__(kWarps * 32) decode_merge_kernel(const DecodeParams p) {
+template <int kWarps, class P>
+__global__ void __launch_bounds__(kWarps * 32) decode_merge_kernel(const P p) {
   // the next kernel on the stream may launch now; it waits for this grid before reading anything
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ float red_m[kWarps], red_w[kWarps];
@@ -683,10 +771,10 @@ __global__ void __launch_bounds__(kWarps * 32) decode_merge_kernel(const DecodeP
     acc.x += s * o.x; acc.y += s * o.y; acc.z += s * o.z; acc.w += s * o.w;
     wsum += s * red_w[k];
   }
-  const float inv = 1.0f / wsum;
+  const float inv = P::kScore ? inverse_or_zero(wsum) : 1.0f / wsum;
   *reinterpret_cast<uint2*>(orow) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0 && p.lse != nullptr) p.lse[b * hq + h] = (M + log2f(wsum)) * kLn2;
+  if (lane == 0 && p.lse != nullptr) p.lse[b * hq + h] = (M + log2f(wsum)) * kLn2 + lse_shift(p, b, h);
 }
 
 // The same merge for sequences cut into many partials (more than 64: a few sequences over all
@@ -695,7 +783,8 @@ __global__ void __launch_bounds__(kWarps * 32) decode_merge_kernel(const DecodeP
 // each warp keeps eight partials' loads in flight: up to 256 partials in one round of loads.
 constexpr int kMergeDimParts = 4;
 constexpr int kMergeManyPartials = 64;
-__global__ void __launch_bounds__(kMergeWarpsSmall * 32) decode_merge_dims_kernel(const DecodeParams p) {
+template <class P>
+__global__ void __launch_bounds__(kMergeWarpsSmall * 32) decode_merge_dims_kernel(const P p) {
   constexpr int kWarps = kMergeWarpsSmall, kInFlight = 8;
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ float red_m[kWarps], red_w[kWarps];
@@ -762,8 +851,10 @@ __global__ void __launch_bounds__(kMergeWarpsSmall * 32) decode_merge_dims_kerne
     a += sk * red_o[k][lane];
     wsum += sk * red_w[k];
   }
-  orow[d] = static_cast<uint16_t>(pack_bf16x2(a / wsum, 0.f) & 0xffffu);
-  if (blockIdx.z == 0 && lane == 0 && p.lse != nullptr) p.lse[b * hq + h] = (M + log2f(wsum)) * kLn2;
+  const float o_d = P::kScore ? a * inverse_or_zero(wsum) : a / wsum;
+  orow[d] = static_cast<uint16_t>(pack_bf16x2(o_d, 0.f) & 0xffffu);
+  if (blockIdx.z == 0 && lane == 0 && p.lse != nullptr)
+    p.lse[b * hq + h] = (M + log2f(wsum)) * kLn2 + lse_shift(p, b, h);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -802,8 +893,8 @@ struct SmallSmem {  // dynamic shared memory, 128-byte aligned
 
 // kHpc KV heads per CTA (1, or 2 when a batch has more (sequence, KV head) pairs than resident
 // clusters allow): warp w serves the CTA's head w / (8 / kHpc).
-template <int kHkvT, int kHpc>
-__global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const DecodeParams p) {
+template <int kHkvT, int kHpc, class P>
+__global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const P p) {
   static_assert(kHpc == 1 || kHpc == 2, "one or two KV heads per CTA");
   constexpr int kHqT = kGroup * kHkvT;
   constexpr int kWph = kSmallWarps / kHpc;  // warps per KV head
@@ -830,12 +921,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
   const int32_t* bt_row = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
   const int pmax = min((p.max_seq_len + kPage - 1) / kPage, p.bt_stride);
   const bool preload = pmax <= kSmallPreload;
-  if (preload)
+  if (!P::kScore && preload)
     for (int i = tid; i < pmax; i += kSmallThreads) s.pages[i] = bt_row[i];
-  const int L = clamp_len(p, b, rank == 0 && g0 == 0 && tid == 0);
-  const int P = (L + kPage - 1) / kPage;
-  const int p0 = static_cast<int>(static_cast<int64_t>(rank) * P / C);
-  const int p1 = static_cast<int>(static_cast<int64_t>(rank + 1) * P / C);
+  const auto view = seq_view(p, b, rank == 0 && g0 == 0 && tid == 0);
+  const int L = view.L;
+  const int p0 = static_cast<int>(static_cast<int64_t>(rank) * view.pages / C);
+  const int p1 = static_cast<int>(static_cast<int64_t>(rank + 1) * view.pages / C);
+  // with score options the pages follow from the lengths: this rank's share, loaded at once
+  if (P::kScore)
+    for (int i = tid; i < min(p1 - p0, kSmallPreload); i += kSmallThreads) s.pages[i] = bt_row[view.page_at(p0 + i)];
 
   // ---- this lane's share of the group's two query rows (dims 8c .. 8c+7), in log2 units
   const int c = lane & 15, th = lane >> 4;
@@ -862,7 +956,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
   };
   auto page_entry = [&](int lp) {
     // (a device length past the host's bound, flagged above, has pages that were not preloaded)
-    int e = preload && lp < pmax ? s.pages[lp] : bt_row[lp];
+    int e;
+    if constexpr (P::kScore) e = lp - p0 < kSmallPreload ? s.pages[lp - p0] : bt_row[view.page_at(lp)];
+    else e = preload && lp < pmax ? s.pages[lp] : bt_row[lp];
     if (e < 0 || e >= p.num_pages) {
       if (lane == 0) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
       e = 0;
@@ -898,6 +994,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
   for (int i = 0; i < 4; ++i) acc_a[i] = acc_b[i] = make_float2(0.f, 0.f);
   float m_a = -CUDART_INF_F, m_b = -CUDART_INF_F;  // max used for the exponent, per head
   float l_part = 0.f;                               // this lane's share of its head's sum
+  float slope2 = 0.f;                               // of the head whose score this lane keeps
+  if constexpr (P::kScore) {
+    if (p.score.slopes != nullptr) slope2 = slope_log2(p.score, 2 * g + (hi_head ? 1 : 0));
+  }
   for (int k = 0; k < n_my; ++k) {
     const int st = k % kRingStages, lp = p0 + wl + k * kWph;
     // page k has landed once at most the pages issued after it are still pending
@@ -906,6 +1006,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
     else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
     const int n_valid = min(kPage, L - lp * kPage);
+    const int pg = view.page_at(lp);
+    uint32_t seen = 0;  // visible keys of the page (score options; else the first n_valid)
+    if constexpr (P::kScore) seen = view.mask(pg);
     // ---- scores: partial dot products over this lane's 8 dims, for 8 tokens x 2 heads.
     //      Register i holds value k = i ^ (c & 15) (k = head * 8 + token, head 0 = 2g): the lane
     //      visits its tokens as j ^ (c & 7) and its own head first, so that every lane keeps the
@@ -933,7 +1036,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
 #pragma unroll
       for (int i = 0; i < w; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[w + i], w);
     }
-    const float sc = (th * 8 + (c & 7) < n_valid) ? v[0] : -CUDART_INF_F;
+    float sc;
+    if constexpr (P::kScore) {
+      const int tok = th * 8 + (c & 7);
+      sc = (seen >> tok & 1u) ? score_of(p.score, v[0], slope2, L - 1 - (pg * kPage + tok) - view.nearest())
+                              : -CUDART_INF_F;
+    } else {
+      sc = (th * 8 + (c & 7) < n_valid) ? v[0] : -CUDART_INF_F;
+    }
     // ---- page max per head (one warp-wide max reduction per head), lazily moved running max
     //      (at least one key of a page is valid)
     const float pmax_a = warp_max(hi_head ? -CUDART_INF_F : sc);
@@ -952,7 +1062,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
       m_a = na;
       m_b = nb;
     }
-    const float pr = fast_exp2(sc - (hi_head ? m_b : m_a));
+    // (with a bias every visible key's score may be -inf: its max still is, and the weight is 0)
+    const float pr = P::kScore && sc == -CUDART_INF_F ? 0.f : fast_exp2(sc - (hi_head ? m_b : m_a));
     l_part += pr;
     // ---- hand probabilities to the lanes that own the V dims
     s.p[warp][lane] = pr;
@@ -967,7 +1078,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
     // ---- o += p v over this lane's 8 tokens (invalid slots of a partial page skipped)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (th * 8 + j < n_valid) {
+      if (P::kScore ? (seen >> (th * 8 + j) & 1u) != 0 : th * 8 + j < n_valid) {
         const uint4 vr = lds128(slot(st, 1, j));
         const float2 ppa = make_float2(pav[j], pav[j]);
         const float2 ppb = make_float2(pbv[j], pbv[j]);
@@ -1079,10 +1190,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
   for (int k = 0; k < kHpc; ++k) {
     const int qh = (tid + k * kSmallThreads) >> 7, d = tid & (kHeadDim - 1);
     const int head = 2 * g0 + qh;
-    const float inv = l[k] > 0.f ? 1.0f / l[k] : 0.f;
+    const float inv = P::kScore ? inverse_or_zero(l[k]) : l[k] > 0.f ? 1.0f / l[k] : 0.f;
     p.out[(static_cast<int64_t>(b) * kHqT + head) * kHeadDim + d] =
         static_cast<uint16_t>(pack_bf16x2(o[k] * inv, 0.f) & 0xffffu);
-    if (d == 0 && p.lse != nullptr) p.lse[b * kHqT + head] = (M[k] + log2f(l[k])) * kLn2;
+    if (d == 0 && p.lse != nullptr)
+      p.lse[b * kHqT + head] = (M[k] + log2f(l[k])) * kLn2 + lse_shift(p, b, head);
   }
 }
 
@@ -1147,18 +1259,24 @@ DecodePlan decode_plan(int batch, int max_seq_len, int split_tokens, int sm_grid
 // call); cached per device and size.
 // The single-launch kernels' shared memory is above the 48 KB default: allowed once per device
 // for every instance (under the capacity cache's lock).
+template <class P>
+cudaError_t configure_small_kernels() {
+  const int bytes = static_cast<int>(sizeof(SmallSmem));
+  const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(decode_cluster_kernel<8, 1, P>, a, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<8, 2, P>, a, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<4, 1, P>, a, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<4, 2, P>, a, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<2, 1, P>, a, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<2, 2, P>, a, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<1, 1, P>, a, bytes);
+  return e;
+}
 bool configure_small_kernels_locked(int dev) {
   static bool done[64] = {};
   if (done[dev]) return true;
-  const int bytes = static_cast<int>(sizeof(SmallSmem));
-  const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(decode_cluster_kernel<8, 1>, a, bytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<8, 2>, a, bytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<4, 1>, a, bytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<4, 2>, a, bytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<2, 1>, a, bytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<2, 2>, a, bytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_cluster_kernel<1, 1>, a, bytes);
+  cudaError_t e = configure_small_kernels<DecodeParams>();
+  if (e == cudaSuccess) e = configure_small_kernels<DecodeScoreParams>();
   if (e != cudaSuccess) {
     cudaGetLastError();
     return false;
@@ -1189,10 +1307,11 @@ int small_cluster_capacity(int C, int hpc) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    // the instances for other KV-head counts use the same registers and shared memory
+    // the instances for other KV-head counts and with score options use the same shared memory,
+    // which allows one CTA per SM whatever their registers (256 threads)
     const cudaError_t e = hpc == 2
-        ? cudaOccupancyMaxActiveClusters(&n, decode_cluster_kernel<8, 2>, &cfg)
-        : cudaOccupancyMaxActiveClusters(&n, decode_cluster_kernel<8, 1>, &cfg);
+        ? cudaOccupancyMaxActiveClusters(&n, decode_cluster_kernel<8, 2, DecodeParams>, &cfg)
+        : cudaOccupancyMaxActiveClusters(&n, decode_cluster_kernel<8, 1, DecodeParams>, &cfg);
     if (e != cudaSuccess) {
       cudaGetLastError();  // not sticky: clear it; the split path serves this call, and the
       return 0;            // query is repeated on the next call
@@ -1265,17 +1384,136 @@ extern "C" int32_t pa_decode_kernels_per_call(pa_dims dims, int32_t batch, int32
 
 namespace pa {
 namespace {
+// The launches of one call: the single-launch path, or the split kernel and its merge.
+// max_visible: host bound of the keys a row sees.
+template <class P>
+pa_status launch_decode(const P& p, const DecodePlan& plan, int hkv, int max_visible, int split_tokens,
+                        int32_t max_ctas, cudaStream_t st) {
+  const int batch = p.batch;
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_device != dev) {
+    const int smem = static_cast<int>(sizeof(DecodeSmem));
+    cudaError_t e = cudaFuncSetAttribute(decode_splitkv_kernel<8, P>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_splitkv_kernel<4, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_splitkv_kernel<2, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_splitkv_kernel<1, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(decode)");
+    // the merge kernel uses no shared memory; giving it the split kernel's carveout keeps the
+    // SMs from reconfiguring shared memory / L1 between the two launches of every call
+    e = cudaFuncSetAttribute(decode_merge_kernel<kMergeWarpsSmall, P>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_merge_kernel<kMergeWarpsLarge, P>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_merge_dims_kernel<P>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(decode merge)");
+    configured_device = dev;
+  }
+
+  // Short batches in one launch (decode_cluster_kernel; see small_path)
+  {
+    const SmallPath sp = small_path(hkv, batch, max_visible, split_tokens);
+    if (sp.C > 0 && (max_ctas <= 0 || static_cast<int64_t>(batch) * (hkv / sp.hpc * sp.C) <= max_ctas)) {
+      const int C = sp.C;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(batch) * static_cast<unsigned>(hkv / sp.hpc * C));
+      cfg.blockDim = dim3(kSmallThreads);
+      cfg.dynamicSmemBytes = sizeof(SmallSmem);  // allowed by small_path's capacity query
+      cfg.stream = st;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[1].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 2;
+      cudaError_t e;
+      const bool two = sp.hpc == 2;
+      switch (hkv) {
+        case 8: e = two ? cudaLaunchKernelEx(&cfg, decode_cluster_kernel<8, 2, P>, p)
+                        : cudaLaunchKernelEx(&cfg, decode_cluster_kernel<8, 1, P>, p); break;
+        case 4: e = two ? cudaLaunchKernelEx(&cfg, decode_cluster_kernel<4, 2, P>, p)
+                        : cudaLaunchKernelEx(&cfg, decode_cluster_kernel<4, 1, P>, p); break;
+        case 2: e = two ? cudaLaunchKernelEx(&cfg, decode_cluster_kernel<2, 2, P>, p)
+                        : cudaLaunchKernelEx(&cfg, decode_cluster_kernel<2, 1, P>, p); break;
+        default: e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<1, 1, P>, p); break;
+      }
+      if (e != cudaSuccess) return record_cuda_error(e, "decode_cluster_kernel");
+      return PA_OK;
+    }
+  }
+  {
+    // a programmatic dependent of the previous work on the stream: it may launch during that
+    // work's tail and waits (griddepcontrol.wait) before reading any input
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(DecodeSmem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    switch (hkv) {
+      case 8: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<8, P>, p); break;
+      case 4: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<4, P>, p); break;
+      case 2: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<2, P>, p); break;
+      default: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<1, P>, p); break;
+    }
+    if (e != cudaSuccess) return record_cuda_error(e, "decode_splitkv_kernel");
+  }
+  {
+    cudaLaunchConfig_t cfg = {};
+    // partials per sequence when the lengths are equal: ceil(ranges / batch), plus one for a
+    // cut at each end, times the page slots per range; more than 4 warps take in one round of
+    // 4 loads -> 16 warps per head
+    const int partials = ((plan.max_ranges + batch - 1) / batch + 1) * p.stage_pages;
+    const bool many = partials > kMergeManyPartials;
+    const bool small = partials > 4 * kMergeWarpsLarge;
+    cfg.gridDim = dim3(batch, p.hq, many ? kMergeDimParts : 1);
+    cfg.blockDim = dim3((small ? kMergeWarpsSmall : kMergeWarpsLarge) * 32);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = many ? cudaLaunchKernelEx(&cfg, decode_merge_dims_kernel<P>, p)
+                  : small ? cudaLaunchKernelEx(&cfg, decode_merge_kernel<kMergeWarpsSmall, P>, p)
+                          : cudaLaunchKernelEx(&cfg, decode_merge_kernel<kMergeWarpsLarge, P>, p);
+    if (e != cudaSuccess) return record_cuda_error(e, "decode_merge_kernel");
+  }
+  return PA_OK;
+}
+
+
 // attn_decode_paged with a cap on the grid (max_ctas > 0; 0 = one CTA per SM)
 pa_status decode_call(pa_dims dims, const void* q, const void* k_pool, const void* v_pool,
                       int64_t num_pages, const int32_t* block_table, int32_t bt_stride,
                       const int32_t* seq_lens, int32_t batch, int32_t max_seq_len,
                       float softmax_scale, int32_t split_tokens, void* out, float* lse,
                       void* workspace, size_t workspace_bytes, int32_t* status,
-                      pa_stream_t stream, int32_t max_ctas) {
+                      pa_stream_t stream, int32_t max_ctas, const pa_score_opts* score = nullptr) {
   if (!gqa_dims_supported(dims)) return PA_ERR_UNSUPPORTED;
   if (batch < 0 || batch > kMaxBatch || bt_stride <= 0 || num_pages <= 0 || max_seq_len < 0 ||
       max_seq_len > 131072 || !(softmax_scale == softmax_scale) || split_tokens < 0)
     return PA_ERR_INVALID_ARG;
+  if (score != nullptr && !score_opts_valid(*score)) return PA_ERR_INVALID_ARG;
   if (batch == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out || !workspace)
     return PA_ERR_INVALID_ARG;
@@ -1286,42 +1524,13 @@ pa_status decode_call(pa_dims dims, const void* q, const void* k_pool, const voi
   const int full_grid = decode_grid_size();
   if (full_grid <= 0) return PA_ERR_CUDA;
   const int sm_grid = max_ctas > 0 ? std::min(full_grid, static_cast<int>(max_ctas)) : full_grid;
-  const DecodePlan plan = decode_plan(batch, max_seq_len, split_tokens, sm_grid);
+  const int max_visible = score != nullptr ? score_max_visible(*score, max_seq_len) : max_seq_len;
+  const DecodePlan plan = decode_plan(batch, max_visible, split_tokens, sm_grid);
   const int hkv = dims.num_kv_heads;
   if (workspace_bytes < ws_layout(batch, plan.ws_ranges, hkv).total) return PA_ERR_WORKSPACE_TOO_SMALL;
   const WsLayout w = ws_layout(batch, plan.max_ranges, hkv);
 
-  static thread_local int configured_device = -1;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (configured_device != dev) {
-    const int smem = static_cast<int>(sizeof(DecodeSmem));
-    cudaError_t e = cudaFuncSetAttribute(decode_splitkv_kernel<8>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_splitkv_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_splitkv_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_splitkv_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(decode)");
-    // the merge kernel uses no shared memory; giving it the split kernel's carveout keeps the
-    // SMs from reconfiguring shared memory / L1 between the two launches of every call
-    e = cudaFuncSetAttribute(decode_merge_kernel<kMergeWarpsSmall>,
-                             cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_merge_kernel<kMergeWarpsLarge>,
-                               cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_merge_dims_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(decode merge)");
-    configured_device = dev;
-  }
-
-  DecodeParams p;
+  DecodeScoreParams p;  // the plain call launches with its base part
   p.hq = dims.num_q_heads;
   p.stage_pages = kHkv / hkv;
   p.q = static_cast<const uint16_t*>(q);
@@ -1348,85 +1557,10 @@ pa_status decode_call(pa_dims dims, const void* q, const void* k_pool, const voi
   p.starve = g_debug_starve ? 1 : 0;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Short batches in one launch (decode_cluster_kernel; see small_path)
-  {
-    const SmallPath sp = small_path(hkv, batch, max_seq_len, split_tokens);
-    if (sp.C > 0 && (max_ctas <= 0 || static_cast<int64_t>(batch) * (hkv / sp.hpc * sp.C) <= max_ctas)) {
-      const int C = sp.C;
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(batch) * static_cast<unsigned>(hkv / sp.hpc * C));
-      cfg.blockDim = dim3(kSmallThreads);
-      cfg.dynamicSmemBytes = sizeof(SmallSmem);  // allowed by small_path's capacity query
-      cfg.stream = st;
-      cudaLaunchAttribute attr[2];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = static_cast<unsigned>(C);
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[1].val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 2;
-      cudaError_t e;
-      const bool two = sp.hpc == 2;
-      switch (hkv) {
-        case 8: e = two ? cudaLaunchKernelEx(&cfg, decode_cluster_kernel<8, 2>, p)
-                        : cudaLaunchKernelEx(&cfg, decode_cluster_kernel<8, 1>, p); break;
-        case 4: e = two ? cudaLaunchKernelEx(&cfg, decode_cluster_kernel<4, 2>, p)
-                        : cudaLaunchKernelEx(&cfg, decode_cluster_kernel<4, 1>, p); break;
-        case 2: e = two ? cudaLaunchKernelEx(&cfg, decode_cluster_kernel<2, 2>, p)
-                        : cudaLaunchKernelEx(&cfg, decode_cluster_kernel<2, 1>, p); break;
-        default: e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<1, 1>, p); break;
-      }
-      if (e != cudaSuccess) return record_cuda_error(e, "decode_cluster_kernel");
-      return PA_OK;
-    }
-  }
-  {
-    // a programmatic dependent of the previous work on the stream: it may launch during that
-    // work's tail and waits (griddepcontrol.wait) before reading any input
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(DecodeSmem);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e;
-    switch (hkv) {
-      case 8: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<8>, p); break;
-      case 4: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<4>, p); break;
-      case 2: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<2>, p); break;
-      default: e = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<1>, p); break;
-    }
-    if (e != cudaSuccess) return record_cuda_error(e, "decode_splitkv_kernel");
-  }
-  {
-    cudaLaunchConfig_t cfg = {};
-    // partials per sequence when the lengths are equal: ceil(ranges / batch), plus one for a
-    // cut at each end, times the page slots per range; more than 4 warps take in one round of
-    // 4 loads -> 16 warps per head
-    const int partials = ((plan.max_ranges + batch - 1) / batch + 1) * p.stage_pages;
-    const bool many = partials > kMergeManyPartials;
-    const bool small = partials > 4 * kMergeWarpsLarge;
-    cfg.gridDim = dim3(batch, dims.num_q_heads, many ? kMergeDimParts : 1);
-    cfg.blockDim = dim3((small ? kMergeWarpsSmall : kMergeWarpsLarge) * 32);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = many ? cudaLaunchKernelEx(&cfg, decode_merge_dims_kernel, p)
-                  : small ? cudaLaunchKernelEx(&cfg, decode_merge_kernel<kMergeWarpsSmall>, p)
-                          : cudaLaunchKernelEx(&cfg, decode_merge_kernel<kMergeWarpsLarge>, p);
-    if (e != cudaSuccess) return record_cuda_error(e, "decode_merge_kernel");
-  }
-  return PA_OK;
+  if (score == nullptr)
+    return launch_decode(static_cast<const DecodeParams&>(p), plan, hkv, max_visible, split_tokens, max_ctas, st);
+  p.score = score_params(*score, softmax_scale, &p.scale_log2);
+  return launch_decode(p, plan, hkv, max_visible, split_tokens, max_ctas, st);
 }
 
 }  // namespace
@@ -1459,6 +1593,22 @@ extern "C" pa_status attn_decode_paged_ex(pa_dims dims, const void* q, const voi
   return pa::decode_call(dims, q, k_pool, v_pool, num_pages, block_table, bt_stride, seq_lens,
                          batch, max_seq_len, softmax_scale, split_tokens, out, lse, workspace,
                          workspace_bytes, status, stream, cap);
+}
+
+extern "C" pa_status attn_decode_paged_score(pa_dims dims, const void* q, const void* k_pool,
+                                             const void* v_pool, int64_t num_pages,
+                                             const int32_t* block_table, int32_t bt_stride,
+                                             const int32_t* seq_lens, int32_t batch,
+                                             int32_t max_seq_len, float softmax_scale,
+                                             int32_t split_tokens, void* out, float* lse,
+                                             void* workspace, size_t workspace_bytes,
+                                             int32_t* status, pa_stream_t stream,
+                                             const pa_launch_opts* opts, const pa_score_opts* score) {
+  const int32_t cap = opts != nullptr ? opts->max_ctas : 0;
+  if (cap < 0) return PA_ERR_INVALID_ARG;
+  return pa::decode_call(dims, q, k_pool, v_pool, num_pages, block_table, bt_stride, seq_lens,
+                         batch, max_seq_len, softmax_scale, split_tokens, out, lse, workspace,
+                         workspace_bytes, status, stream, cap, score);
 }
 
 // ---------------------------------------------------------------------------------------------
