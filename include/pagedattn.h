@@ -271,7 +271,7 @@ pa_status attn_prefill_chunk_ex(pa_dims dims, const void* q, const int32_t* cu_q
  * K and V of keys that no row of the call sees are never used, whatever they hold; pages whose
  * keys no row of a sequence (decode) or of a 128-row tile of its chunk (prefill) sees are not
  * read, and their block-table entries may be anything (-1 after paged_release).
- *   softcap         >= 0; 0: no cap
+ *   softcap         0 (no cap) or in [1e-6, 1e30)
  *   alibi_slopes    fp32 [Hq] on the device, or NULL
  *   window          >= 0; 0: no limit. A row sees its own position and the window - 1 before it
  *   prefix_lens     int32 [batch] on the device, or NULL: keys seen by every row of the sequence,
@@ -302,6 +302,17 @@ pa_status attn_decode_paged_score(pa_dims dims, const void* q, const void* k_poo
                                   float* lse, void* workspace, size_t workspace_bytes,
                                   int32_t* status, pa_stream_t stream, const pa_launch_opts* opts,
                                   const pa_score_opts* score);
+
+size_t pa_prefill_score_workspace_size(pa_dims dims, int32_t batch, int32_t total_q);
+
+pa_status attn_prefill_chunk_score(pa_dims dims, const void* q, const int32_t* cu_q_lens,
+                                   int32_t total_q, const void* k_pool, const void* v_pool,
+                                   int64_t num_pages, const int32_t* block_table,
+                                   int32_t bt_stride, const int32_t* seq_lens, int32_t batch,
+                                   int32_t max_q_len, int32_t max_seq_len, float softmax_scale,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   int32_t* status, pa_stream_t stream, const pa_launch_opts* opts,
+                                   const pa_score_opts* score);
 
 /* ------------------------------------------------------------------------------------------
  * attn_merge_lse — combine attention results computed over disjoint key sets.

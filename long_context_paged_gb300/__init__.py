@@ -27,6 +27,7 @@ __all__ = [
     "kv_append_paged", "attn_decode_paged", "attn_decode_paged_noalloc", "attn_prefill_chunk",
     "attn_merge_lse", "adaptor_mlp_merge4", "adaptor_workspace_size", "LaunchOpts",
     "decode_workspace_size", "decode_kernels_per_call", "prefill_workspace_size",
+    "prefill_score_workspace_size",
     "read_device_status", "debug_decode_starve",
     "paged_step_plan", "StepPlan", "paged_release", "rope_append_paged", "rope_inv_freq",
     "RopeScaling", "ScoreOpts",
@@ -120,6 +121,10 @@ _SIGS = {
                                      _I32, _F, _P, _P, _P, _SZ, _P, _P, _P]),
     "attn_decode_paged_score": (_I32, [Dims, _P, _P, _P, _I64, _P, _I32, _P, _I32, _I32, _F, _I32,
                                        _P, _P, _P, _SZ, _P, _P, _P, ctypes.POINTER(ScoreOpts)]),
+    "pa_prefill_score_workspace_size": (_SZ, [Dims, _I32, _I32]),
+    "attn_prefill_chunk_score": (_I32, [Dims, _P, _P, _I32, _P, _P, _I64, _P, _I32, _P, _I32, _I32,
+                                        _I32, _F, _P, _P, _P, _SZ, _P, _P, _P,
+                                        ctypes.POINTER(ScoreOpts)]),
     "attn_merge_lse": (_I32, [_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "pa_adaptor_workspace_size": (_SZ, [_I32]),
     "adaptor_mlp_merge4": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _SZ, _P, _P]),
@@ -278,6 +283,11 @@ def prefill_workspace_size(batch: int, max_q_len: int, max_seq_len: int, dims=No
     return int(load().pa_prefill_workspace_size(_dims(dims), batch, max_q_len, max_seq_len))
 
 
+def prefill_score_workspace_size(batch: int, total_q: int, dims=None) -> int:
+    """Workspace of attn_prefill_chunk with score options."""
+    return int(load().pa_prefill_score_workspace_size(_dims(dims), batch, total_q))
+
+
 def _workspace(nbytes, device, workspace):
     if workspace is not None:
         return workspace
@@ -402,10 +412,14 @@ def attn_decode_paged_noalloc(q, k_pool, v_pool, block_table, seq_lens, max_seq_
 def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_q_len: int,
                        max_seq_len: int, softmax_scale: float, *, out=None, lse=None,
                        workspace=None, status=None, stream=None, want_lse=True, dims=None,
-                       max_ctas=None):
+                       max_ctas=None, softcap: float = 0.0, alibi_slopes=None, window: int = 0,
+                       prefix_lens=None, max_prefix_len=None, row_start=None):
     """Chunked prefill: q [Tq, Hq, D] packed by cu_q_lens. Returns (out, lse).
 
-    max_ctas: cap on the persistent grid (attn_prefill_chunk_ex); None = the plain call."""
+    max_ctas: cap on the persistent grid (attn_prefill_chunk_ex); None = the plain call.
+    Score options as in attn_decode_paged, row_start per query row [Tq]
+    (attn_prefill_chunk_score; a workspace passed in then has prefill_score_workspace_size
+    bytes)."""
     _need(q, "q", torch.bfloat16, 3)
     _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
     _need(k_pool, "k_pool", torch.bfloat16, 4)
@@ -426,7 +440,10 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
-    ws_bytes = prefill_workspace_size(B, max_q_len, max_seq_len, dims)
+    score = _score("attn_prefill_chunk", q.shape[1], B, Tq, int(max_seq_len), softcap, alibi_slopes,
+                   window, prefix_lens, max_prefix_len, row_start)
+    ws_bytes = (prefill_workspace_size(B, max_q_len, max_seq_len, dims) if score is None
+                else prefill_score_workspace_size(B, Tq, dims))
     if ws_bytes > 0:
         workspace = _workspace(ws_bytes, q.device, workspace)
     if status is not None:
@@ -441,7 +458,10 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
             0 if workspace is None else workspace.numel() * workspace.element_size(),
             _ptr(status), _stream(stream))
     keep, ref = _opts(max_ctas)
-    if ref is None:
+    if score is not None:
+        _check("attn_prefill_chunk_score", lib.attn_prefill_chunk_score(*args, ref,
+                                                                        ctypes.byref(score)))
+    elif ref is None:
         _check("attn_prefill_chunk", lib.attn_prefill_chunk(*args))
     else:
         _check("attn_prefill_chunk_ex", lib.attn_prefill_chunk_ex(*args, ref))

@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const P p) 
       const int L = view.L;
       float slope2 = 0.f;  // of the head whose score this lane keeps
       if constexpr (P::kScore) {
-        if (p.score.slopes != nullptr) slope2 = slope_log2(p.score, 2 * g + (hi_head ? 1 : 0));
+        if (p.score.slopes != nullptr) slope2 = slope_over(p.score, 2 * g + (hi_head ? 1 : 0), 1.0f);
       }
 
       // q of the two heads in this lane's order: its own head (the one whose score it keeps
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
   float l_part = 0.f;                               // this lane's share of its head's sum
   float slope2 = 0.f;                               // of the head whose score this lane keeps
   if constexpr (P::kScore) {
-    if (p.score.slopes != nullptr) slope2 = slope_log2(p.score, 2 * g + (hi_head ? 1 : 0));
+    if (p.score.slopes != nullptr) slope2 = slope_over(p.score, 2 * g + (hi_head ? 1 : 0), 1.0f);
   }
   for (int k = 0; k < n_my; ++k) {
     const int st = k % kRingStages, lp = p0 + wl + k * kWph;

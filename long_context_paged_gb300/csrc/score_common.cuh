@@ -29,7 +29,7 @@ struct ScoreParams {
 };
 
 inline bool score_opts_valid(const pa_score_opts& o) {
-  return o.softcap >= 0.f && o.softcap < 1e30f && o.window >= 0 && o.max_prefix_len >= 0 &&
+  return (o.softcap == 0.f || (o.softcap >= 1e-6f && o.softcap < 1e30f)) && o.window >= 0 && o.max_prefix_len >= 0 &&
          o.max_prefix_len <= 131072;
 }
 
@@ -71,9 +71,10 @@ __device__ __forceinline__ int score_first_key(const ScoreParams& s, int row, in
   return lo;
 }
 
-// A head's slope in log2 units. A finite slope stays finite: at distance 0 its bias is 0.
-__device__ __forceinline__ float slope_log2(const ScoreParams& s, int head) {
-  const float a = s.slopes[head], r = a * kLog2e;
+// A head's slope in log2 units, over `scale`. A finite slope stays finite: at distance 0 its bias
+// is 0.
+__device__ __forceinline__ float slope_over(const ScoreParams& s, int head, float scale) {
+  const float a = s.slopes[head], r = a * kLog2e / scale;
   return isinf(r) && !isinf(a) ? copysignf(3.402823466e38f, a) : r;
 }
 
