@@ -785,18 +785,45 @@ __device__ void plan_split(const PrefillTcParams& p, PrefillTcSmem& s, int G, in
   U1 = s.plan_u1;
 }
 
-// Cap and bias of a row's 128 raw products, in place, and the row max before the bias (which moves
-// it: the caller takes it afterwards). Capped scores come out in log2 units; uncapped ones stay raw
-// products, with the bias in their units (`slope` = the head's slope over the softmax scale).
+// cap * tanh of 128 raw products as s P(s^2) with N terms, in place.
+template <int N>
+__device__ __forceinline__ void cap_poly(const float (&a)[N], uint32_t (&sb)[128]) {
+#pragma unroll
+  for (int c = 0; c < 128; c += 2) {
+    const float2 s = make_float2(__uint_as_float(sb[c]), __uint_as_float(sb[c + 1]));
+    const float2 t = mul2(s, s);
+    float2 y = make_float2(a[N - 1], a[N - 1]);
+#pragma unroll
+    for (int k = N - 2; k >= 0; --k) y = fma2(y, t, make_float2(a[k], a[k]));
+    y = mul2(y, s);
+    sb[c] = __float_as_uint(y.x);
+    sb[c + 1] = __float_as_uint(y.y);
+  }
+}
+
+// Cap and bias of a row's 128 raw products, in place. mx: the largest magnitude of the products on
+// entry with a cap, their max without one; on return a max of the scores before the bias, or an
+// upper bound of it (a bias moves the maximum: the caller takes it afterwards). Capped scores come
+// out in log2 units; uncapped ones stay raw products, with the bias in their units (`slope` = the
+// head's slope over the softmax scale).
+// The tanh: an exponential and a quotient per score would take three trips through the MUFU unit
+// instead of one, which then bounds the kernel (3.15 ms for 4,096 queries at 61,440); while a
+// warp's products are small against the cap, FMA-pipe polynomials serve (two ranges).
 template <class P>
 __device__ __forceinline__ void score_tile(const P& p, uint32_t (&sb)[128], const RowMask& rm, int k0,
                                            float slope, float& mx) {
   if constexpr (P::kCap) {
     const float cap = p.score.cap_log2;
+    if (__all_sync(0xffffffffu, mx <= p.score.poly_max[0])) {
+      cap_poly<4>(p.score.poly4, sb);
+    } else if (__all_sync(0xffffffffu, mx <= p.score.poly_max[1])) {
+      cap_poly<6>(p.score.poly6, sb);
+    } else {
 #pragma unroll
-    for (int c = 0; c < 128; ++c)
-      sb[c] = __float_as_uint(cap * tanh_exp(__uint_as_float(sb[c]) * p.scale_log2));
-    mx = cap * tanh_exp(mx * p.scale_log2);  // tanh is monotone: the max of the raw products
+      for (int c = 0; c < 128; ++c)
+        sb[c] = __float_as_uint(cap * tanh_exp(__uint_as_float(sb[c]) * p.scale_log2));
+    }
+    mx = cap * tanh_exp(mx * p.scale_log2);  // tanh is odd and monotone
   }
   if constexpr (P::kBias) {
     // - slope * distance, the distance (an exact small integer) counted from the nearest visible key
@@ -1205,8 +1232,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         uint32_t sb[128];  // raw scores (fp32 bits) of this row
         float cm[4];       // the maximum of each 32-column piece, from the TMEM load itself
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (P::kCap) tc::tmem_ld32_absmax(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
+          else tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
+        }
         tc::tmem_wait_ld();
         int k0 = (pjb + i) * kTileN;
         float mx = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
@@ -1218,7 +1247,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         } else {
           partial = k0 + kTileN - 1 > qpos;
         }
-        if (partial || P::kBias) {
+        // With a cap, mx is the capped largest magnitude: it bounds the max from above, and as the
+        // exponents' reference it leaves every weight that matters in fp32's range while the max,
+        // at least -mx, is within 2^-100 of it; beyond that the max itself is taken.
+        const bool need_max = P::kBias || (P::kCap && mx > 50.f);
+        if (partial || need_max) {
           // mask the keys this row does not see, then take the row max over what is left (8
           // independent partial maxima, two new elements per three-input max)
           if constexpr (P::kScore) {

@@ -285,3 +285,20 @@ def test_replayed_from_a_graph_with_new_masks(cuda_lib):
         g.replay()
         torch.cuda.synchronize()
         close(out, lse, *reference(inp, o))
+
+
+@pytest.mark.parametrize("cap", [8.0, 50.0, 300.0])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_large_capped_scores_of_one_sign(cuda_lib, cap, sign):
+    """Scores near +-60 (all of one sign): the exponents' reference is the largest magnitude's score
+    while that stays near the max, else the max itself."""
+    n, off = 70, 180
+    inp = W.make_paged(67, [off + n], [n], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    u = torch.randn(16, 128, generator=g, device="cuda")
+    k = u[::2] + 0.2 * torch.randn(inp.num_pages, 16, 8, 128, generator=g, device="cuda")
+    inp.k_pools[0] = k.to(torch.bfloat16)
+    q = sign * 5.0 * u[::2].repeat_interleave(2, 0) * (0.5 + torch.rand(n, 16, 1, generator=g, device="cuda"))
+    inp.q[0] = q.to(torch.bfloat16)
+    check(cuda_lib, inp, dict(softcap=cap))
+    check(cuda_lib, inp, dict(softcap=cap, slopes=SLOPES, window=150), poison=False)
