@@ -1,4 +1,5 @@
-// attn_prefill_chunk: argument checks of the C ABI; the work runs in prefill_tc.cu.
+// attn_prefill_chunk: argument checks of the C ABI; the work runs in prefill_tc.cu
+// and, with score options, in prefill_score.cu.
 //
 // Source: chunked prefill of long audio prompts, 4096 tokens per scheduling step, each chunk
 // attending to the KV cache of the earlier chunks plus its own tokens ("Optimizing ASR
@@ -17,7 +18,14 @@ pa_status launch_prefill_tc(int32_t hkv, const void* q, int32_t total_q, const i
                             const int32_t* seq_lens, int32_t batch, int32_t max_q_len,
                             float softmax_scale, void* out, float* lse, void* workspace,
                             size_t workspace_bytes, int32_t* status, cudaStream_t stream,
-                            int32_t max_ctas, const pa_score_opts* score);
+                            int32_t max_ctas);
+pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, const int32_t* cu_q_lens,
+                               const void* k_pool, const void* v_pool, int64_t num_pages,
+                               const int32_t* block_table, int32_t bt_stride,
+                               const int32_t* seq_lens, int32_t batch, int32_t max_q_len,
+                               float softmax_scale, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int32_t* status, cudaStream_t stream,
+                               int32_t max_ctas, const pa_score_opts& score);
 size_t prefill_workspace_bytes(int batch);
 size_t prefill_score_workspace_bytes(int batch, int total_q);
 
@@ -41,10 +49,15 @@ pa_status prefill_call(pa_dims dims, const void* q, const int32_t* cu_q_lens, in
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pool) |
        reinterpret_cast<uintptr_t>(v_pool) | reinterpret_cast<uintptr_t>(out)) & 15u)
     return PA_ERR_INVALID_ARG;
+  if (score != nullptr)
+    return launch_prefill_score(dims.num_kv_heads, q, total_q, cu_q_lens, k_pool, v_pool, num_pages,
+                                block_table, bt_stride, seq_lens, batch, max_q_len, softmax_scale, out,
+                                lse, workspace, workspace_bytes, status,
+                                reinterpret_cast<cudaStream_t>(stream), max_ctas, *score);
   return launch_prefill_tc(dims.num_kv_heads, q, total_q, cu_q_lens, k_pool, v_pool, num_pages,
                            block_table, bt_stride, seq_lens, batch, max_q_len, softmax_scale, out,
                            lse, workspace, workspace_bytes, status,
-                           reinterpret_cast<cudaStream_t>(stream), max_ctas, score);
+                           reinterpret_cast<cudaStream_t>(stream), max_ctas);
 }
 }  // namespace
 }  // namespace pa

@@ -46,7 +46,6 @@
 #include <stdint.h>
 
 #include "pa_common.cuh"
-#include "score_common.cuh"
 #include "tc_common.cuh"
 
 namespace pa {
@@ -92,11 +91,8 @@ constexpr int kMergeRows = 128;  // threads of a merge CTA: one per row of a que
 // One piece of the walk as the roles use it: key tiles [jb, je) of job (b, g, qt), with the
 // chunk's first packed row q0, its length n, the sequence's keys L and the chunk's offset off;
 // J = the job's key tiles; valid = 0 ends the walk.
-// With score options, the job's key tiles are a list: tiles [0, n1) of the prefix, then tile
-// i + shift for i >= n1; prefix is the sequence's, [lo, hi) what the job's rows see besides it.
 struct PieceDesc {
   int32_t b, g, qt, q0, n, L, off, J, jb, je, valid;
-  int32_t prefix, n1, shift, lo, hi;
 };
 
 struct PrefillTcSmem {  // placed at a 1024-byte aligned address (swizzle atoms)
@@ -128,7 +124,6 @@ struct PrefillTcSmem {  // placed at a 1024-byte aligned address (swizzle atoms)
 static_assert(sizeof(PrefillTcSmem) <= 232448, "prefill shared memory over the 227 KB limit");
 
 struct PrefillTcParams {
-  static constexpr bool kScore = false, kCap = false, kBias = false;
   int32_t hkv, hq;        // KV heads and query heads of the call (hq = 2 hkv)
   const int32_t* cu_q_lens;
   const int32_t* seq_lens;
@@ -183,321 +178,6 @@ __device__ __forceinline__ long long tiles_of(const SeqGeom& s, int qt) {
 // Units of the jobs before q tile qt of one head: their key tiles and their cost units.
 __device__ __forceinline__ long long units_before(const SeqGeom& s, int qt) {
   return static_cast<long long>(qt) * (s.a + kJobCost) + static_cast<long long>(qt) * (qt - 1) / 2;
-}
-
-// ---------------------------------------------------------------------------------------------
-// Score options (attn_prefill_chunk_score). The key range of a job then depends on its rows' masks,
-// so the jobs' geometry and the work split come from a plan kernel instead of closed forms: one
-// TileDesc per query tile (all KV heads share it), the running count of units before each, and
-// the CTAs' shares. Jobs are ordered KV head, then query tile over all chunks; job g * tiles + i
-// starts at unit g * units + ws_units[i].
-// ---------------------------------------------------------------------------------------------
-struct TileDesc {
-  int32_t b, qt, q0, n, L, off;
-  int32_t J;                 // key tiles of the job (at least 1: rows that see nothing are written too)
-  int32_t prefix, n1, shift, lo, hi;
-};
-struct PlanHeader {
-  int32_t tiles, rounds, grid, pad;
-  long long units;  // units of one KV head's jobs
-};
-
-// kCapT: tanh cap, kBiasT: distance bias (the masks are there in any case). scale_log2 is the
-// factor of the raw products: softmax_scale * log2 e, or softmax_scale / cap with a cap.
-template <bool kCapT, bool kBiasT>
-struct PrefillScoreParams : PrefillTcParams {
-  static constexpr bool kScore = true, kCap = kCapT, kBias = kBiasT;
-  ScoreParams score;
-  int32_t total_q, max_tiles;
-  const uint16_t* q_rows;    // the operands, for repair_row
-  const uint16_t* k_rows;
-  const uint16_t* v_rows;
-  PlanHeader* ws_plan;
-  TileDesc* ws_tiles;        // [max_tiles]
-  long long* ws_units;       // [max_tiles + 1] units of the tiles before, in one head
-  int32_t* ws_first_tile;    // [batch + 1]
-};
-
-constexpr int kPlanThreads = 1024;
-
-__device__ __forceinline__ long long block_scan_incl(long long v, long long* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += n;
-  }
-  __syncthreads();  // (the sums of an earlier scan have been read)
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  long long before = 0;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
-  return v + before;
-}
-
-// One CTA: the chunks' query tiles, each tile's key tiles (a warp per tile; its 128 rows' masks
-// reduced by the lanes), a scan of their units, and the balanced split of plan_split.
-template <class P>
-__global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p, int G) {
-  asm volatile("griddepcontrol.launch_dependents;");  // its CTAs wait for this grid's completion
-  __shared__ long long warp_sums[kPlanThreads / 32];
-  __shared__ int32_t first_tile[kMaxBatch + 1];
-  __shared__ int32_t seq[kMaxBatch][5];  // q0, n, L, off, prefix
-  __shared__ long long carry;
-  __shared__ int32_t rounds;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  // ---- chunks: a chunk that does not fit its sequence, its table row or the packing is flagged
-  //      and gets no tile
-  int nqt = 0;
-  if (tid < p.batch) {
-    const int q0 = p.cu_q_lens[tid], n = p.cu_q_lens[tid + 1] - q0, L = p.seq_lens[tid];
-    if (n > 0) {
-      if (n > L || L > p.bt_stride * kPage || q0 < 0 || n > p.total_q - q0) flag_error(p.status, PA_DEV_ERR_LENGTH);
-      else nqt = (n + kTileM - 1) / kTileM;
-    }
-    seq[tid][0] = q0;
-    seq[tid][1] = n;
-    seq[tid][2] = L;
-    seq[tid][3] = L - n;
-    seq[tid][4] = nqt > 0 ? min(score_prefix(p.score, tid, p.status, true), L) : 0;
-  }
-  const long long tiles_incl = block_scan_incl(nqt, warp_sums);
-  if (tid < p.batch) first_tile[tid] = static_cast<int32_t>(min(tiles_incl - nqt, static_cast<long long>(p.max_tiles)));
-  if (tid == p.batch - 1) {
-    // (chunks that overlap in the packing could need more tiles than it has rows for: the rest is
-    // dropped and flagged)
-    if (tiles_incl > p.max_tiles) flag_error(p.status, PA_DEV_ERR_LENGTH);
-    first_tile[p.batch] = static_cast<int32_t>(min(tiles_incl, static_cast<long long>(p.max_tiles)));
-  }
-  __syncthreads();
-  const int tiles = first_tile[p.batch];
-
-  // ---- tiles
-  for (int i = warp; i < tiles; i += kPlanThreads / 32) {
-    int b = 0, hi_b = p.batch;  // the last b with first_tile[b] <= i has tiles
-    while (hi_b - b > 1) {
-      const int mid = (b + hi_b) >> 1;
-      if (first_tile[mid] <= i) b = mid; else hi_b = mid;
-    }
-    TileDesc d;
-    d.b = b;
-    d.qt = i - first_tile[b];
-    d.q0 = seq[b][0];
-    d.n = seq[b][1];
-    d.L = seq[b][2];
-    d.off = seq[b][3];
-    d.prefix = seq[b][4];
-    int lo = 0x7fffffff, hi = 0;
-    if (p.score.row_start == nullptr) {  // a row sees at least itself: the ends decide
-      lo = score_first_key(p.score, 0, d.off + d.qt * kTileM);
-      hi = d.off + min(d.n, (d.qt + 1) * kTileM);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kTileM / 32; ++k) {
-        const int row = d.qt * kTileM + 32 * k + lane;
-        if (row < d.n) {
-          const int first = score_first_key(p.score, d.q0 + row, d.off + row);
-          if (first <= d.off + row) {
-            lo = min(lo, first);
-            hi = max(hi, d.off + row + 1);
-          }
-        }
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-    }
-    d.lo = lo;
-    d.hi = hi;
-    d.n1 = (d.prefix + kTileN - 1) / kTileN;
-    const int end = (hi + kTileN - 1) / kTileN;
-    const int t0 = max(min(lo, hi) / kTileN, d.n1);
-    d.shift = t0 - d.n1;
-    d.J = max(1, d.n1 + max(0, end - t0));
-    if (lane == 0) p.ws_tiles[i] = d;
-  }
-  for (int b = tid; b <= p.batch; b += kPlanThreads) p.ws_first_tile[b] = first_tile[b];
-  if (tid == 0) carry = 0;
-  __syncthreads();
-
-  // ---- units before each tile
-  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    const long long u = i < tiles ? p.ws_tiles[i].J + kJobCost : 0;
-    const long long incl = block_scan_incl(u, warp_sums) + carry;
-    if (i < tiles) p.ws_units[i] = incl - u;
-    __syncthreads();
-    if (tid == kPlanThreads - 1) carry = incl;
-    __syncthreads();
-  }
-  const long long T = carry;
-  if (tid == 0) {
-    p.ws_units[tiles] = T;
-    rounds = 0;
-  }
-  __syncthreads();
-
-  // ---- the split (as plan_split): whole jobs round-robin while they stay within the equal share,
-  //      then the remaining units in consecutive ranges that level the CTAs
-  const long long total = T * p.hkv, target = (total + G - 1) / G;
-  const int jobs = tiles * p.hkv;
-  auto job_cost = [&](int jo) { return static_cast<long long>(p.ws_tiles[jo % tiles].J + kJobCost); };
-  const int rmax = jobs / G;
-  if (tid == 0) rounds = rmax;
-  __syncthreads();
-  if (tid < G) {
-    long long acc = 0;
-    int r = 0;
-    for (; r < rmax; ++r) {
-      acc += job_cost(tid + r * G);
-      if (acc > target) break;
-    }
-    if (r < rmax) atomicMin(&rounds, r);
-  }
-  __syncthreads();
-  const int n_rounds = rounds;
-  long long tail = 0;
-  if (tid < G) {
-    long long whole = 0;
-    for (int r = 0; r < n_rounds; ++r) whole += job_cost(tid + r * G);
-    tail = target - whole;
-  }
-  const long long excl = block_scan_incl(tail, warp_sums) - tail;
-  const int n_dp = n_rounds * G;
-  const long long T0 = n_dp < jobs ? (n_dp / tiles) * T + p.ws_units[n_dp % tiles] : total;
-  if (tid < G) p.ws_tail[tid] = min(total, T0 + excl);
-  if (tid == 0) {
-    p.ws_tail[G] = total;
-    *p.ws_plan = PlanHeader{tiles, n_rounds, G, 0, T};
-    p.ws_header[3] = n_dp;
-  }
-}
-
-// The pieces one CTA owns under a plan, in the order of JobWalker: whole jobs, then its range.
-template <class P>
-struct ScoreWalker {
-  const P* p;
-  long long U0, U1, T, u0;  // u0: first unit of the current job
-  int tiles, rounds, round, G, job;
-  PieceDesc cur;
-
-  __device__ void set(int jo, bool whole) {
-    job = jo;
-    cur.valid = 0;
-    if (jo >= tiles * p->hkv) return;
-    const int g = jo / tiles, i = jo - g * tiles;
-    const TileDesc d = p->ws_tiles[i];
-    u0 = g * T + p->ws_units[i];
-    cur.b = d.b;
-    cur.g = g;
-    cur.qt = d.qt;
-    cur.q0 = d.q0;
-    cur.n = d.n;
-    cur.L = d.L;
-    cur.off = d.off;
-    cur.J = d.J;
-    cur.prefix = d.prefix;
-    cur.n1 = d.n1;
-    cur.shift = d.shift;
-    cur.lo = d.lo;
-    cur.hi = d.hi;
-    cur.jb = whole ? 0 : static_cast<int>(max(U0, u0) - u0);
-    cur.je = whole ? d.J : static_cast<int>(min(U1, u0 + d.J) - u0);
-    cur.valid = whole || (u0 < U1 && cur.jb < cur.je);
-  }
-
-  __device__ void start_tail() {
-    cur.valid = 0;
-    if (U0 >= U1) return;
-    const int g = static_cast<int>(U0 / T);
-    const long long rem = U0 - g * T;
-    int lo = 0, hi = tiles;  // last tile with units before it <= rem
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p->ws_units[mid] <= rem) lo = mid; else hi = mid;
-    }
-    set(g * tiles + lo, false);
-    // a range that starts in the cost units after a job's last key tile holds none of its tiles
-    if (!cur.valid && u0 + cur.J + kJobCost < U1) set(job + 1, false);
-  }
-
-  __device__ void start(const P& pp) {
-    p = &pp;
-    const PlanHeader h = *pp.ws_plan;
-    tiles = h.tiles;
-    rounds = h.rounds;
-    G = h.grid;
-    T = h.units;
-    U0 = pp.ws_tail[blockIdx.x];
-    U1 = pp.ws_tail[blockIdx.x + 1];
-    round = 0;
-    if (rounds > 0) set(static_cast<int>(blockIdx.x), true);
-    else start_tail();
-  }
-
-  __device__ void next() {
-    if (round < rounds) {
-      if (++round < rounds) set(static_cast<int>(blockIdx.x) + round * G, true);
-      else start_tail();
-      return;
-    }
-    set(job + 1, false);
-  }
-};
-
-// What the softmax warps need of a row: the keys it sees (prefix, or [lo, qpos]) and the nearest
-// one's distance (0 when it sees its own position).
-struct RowMask {
-  int prefix, lo, qpos, nearest;
-};
-
-// Visible keys among the 32 from `base` on, bit c = key base + c.
-__device__ __forceinline__ uint32_t row_mask_word(const RowMask& m, int base) {
-  auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
-  return below(m.prefix - base) | (below(m.qpos + 1 - base) & ~below(m.lo - base));
-}
-
-// A masked key's P is 0, and 0 times a non-finite V is NaN: a V row that one row of a tile sees and
-// another does not (a later token, another document) would reach both through the MMA. Rows that
-// come out non-finite are therefore recomputed here from their visible keys alone, one after the
-// other by their whole warp, and stored over what was stored. This costs time only on inputs that
-// hold non-finite values (a row's keys at ~50 cycles each, 0.1 s for a warp's 32 rows of 131,072
-// keys, well inside the other warps' 2 s waits).
-template <class P>
-__device__ __forceinline__ void repair_row(const P& p, const PieceDesc& d, int row_in_chunk, int head,
-                                           const RowMask& m, float slope2, float m_eff, float scale_o,
-                                           float (&acc)[4]) {
-  const int lane = threadIdx.x & 31;
-  const uint2 qw = *(reinterpret_cast<const uint2*>(
-                         p.q_rows + (static_cast<int64_t>(d.q0 + row_in_chunk) * p.hq + head) * kHeadDim) + lane);
-  const float q[4] = {bf16lo(qw.x), bf16hi(qw.x), bf16lo(qw.y), bf16hi(qw.y)};
-  acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-  const int32_t* bt_row = p.block_table + static_cast<int64_t>(d.b) * p.bt_stride;
-  for (int j = d.jb; j < d.je; ++j) {
-    const int k0 = (j < d.n1 ? j : j + d.shift) * kTileN;
-    for (int w = 0; w < kTileN / 32; ++w) {
-      uint32_t seen = row_mask_word(m, k0 + 32 * w);
-      for (; seen != 0; seen &= seen - 1) {
-        const int key = k0 + 32 * w + __ffs(seen) - 1;
-        int page = bt_row[key / kPage];
-        if (page < 0 || page >= p.num_pages) page = 0;  // (flagged by the producers)
-        const int64_t at = ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + d.g) * kHeadDim;
-        const uint2 kw = *(reinterpret_cast<const uint2*>(p.k_rows + at) + lane);
-        float s = q[0] * bf16lo(kw.x) + q[1] * bf16hi(kw.x) + q[2] * bf16lo(kw.y) + q[3] * bf16hi(kw.y);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float x = score_of(p.score, s * p.scale_log2, slope2, abs(m.qpos - key) - m.nearest);
-        const float pr = fast_exp2(x - m_eff);
-        const uint2 vw = *(reinterpret_cast<const uint2*>(p.v_rows + at) + lane);
-        acc[0] += pr * bf16lo(vw.x);
-        acc[1] += pr * bf16hi(vw.x);
-        acc[2] += pr * bf16lo(vw.y);
-        acc[3] += pr * bf16hi(vw.y);
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] *= scale_o;
 }
 
 // One job piece this CTA owns: key tiles [jb, je) of job (b, g, qt).
@@ -785,76 +465,12 @@ __device__ void plan_split(const PrefillTcParams& p, PrefillTcSmem& s, int G, in
   U1 = s.plan_u1;
 }
 
-// cap * tanh of 128 raw products as s P(s^2) with N terms, in place.
-template <int N>
-__device__ __forceinline__ void cap_poly(const float (&a)[N], uint32_t (&sb)[128]) {
-#pragma unroll
-  for (int c = 0; c < 128; c += 2) {
-    const float2 s = make_float2(__uint_as_float(sb[c]), __uint_as_float(sb[c + 1]));
-    const float2 t = mul2(s, s);
-    float2 y = make_float2(a[N - 1], a[N - 1]);
-#pragma unroll
-    for (int k = N - 2; k >= 0; --k) y = fma2(y, t, make_float2(a[k], a[k]));
-    y = mul2(y, s);
-    sb[c] = __float_as_uint(y.x);
-    sb[c + 1] = __float_as_uint(y.y);
-  }
-}
-
-// Cap and bias of a row's 128 raw products, in place. mx: the largest magnitude of the products on
-// entry with a cap, their max without one; on return a max of the scores before the bias, or an
-// upper bound of it (a bias moves the maximum: the caller takes it afterwards). Capped scores come
-// out in log2 units; uncapped ones stay raw products, with the bias in their units (`slope` = the
-// head's slope over the softmax scale).
-// The tanh: an exponential and a quotient per score would take three trips through the MUFU unit
-// instead of one, which then bounds the kernel (3.15 ms for 4,096 queries at 61,440); while a
-// warp's products are small against the cap, FMA-pipe polynomials serve (two ranges).
-template <class P>
-__device__ __forceinline__ void score_tile(const P& p, uint32_t (&sb)[128], const RowMask& rm, int k0,
-                                           float slope, float& mx) {
-  if constexpr (P::kCap) {
-    const float cap = p.score.cap_log2;
-    if (__all_sync(0xffffffffu, mx <= p.score.poly_max[0])) {
-      cap_poly<4>(p.score.poly4, sb);
-    } else if (__all_sync(0xffffffffu, mx <= p.score.poly_max[1])) {
-      cap_poly<6>(p.score.poly6, sb);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 128; ++c)
-        sb[c] = __float_as_uint(cap * tanh_exp(__uint_as_float(sb[c]) * p.scale_log2));
-    }
-    mx = cap * tanh_exp(mx * p.scale_log2);  // tanh is odd and monotone
-  }
-  if constexpr (P::kBias) {
-    // - slope * distance, the distance (an exact small integer) counted from the nearest visible key
-    const float at = static_cast<float>(rm.qpos - k0);  // the column of the row's own position
-    const float near = static_cast<float>(rm.nearest);
-    if (k0 + kTileN - 1 <= rm.qpos) {
-      const float2 s2 = make_float2(slope, slope), a2 = make_float2(near - at, near - at);
-#pragma unroll
-      for (int c = 0; c < 128; c += 2) {
-        const float2 d = add2(make_float2(static_cast<float>(c), static_cast<float>(c + 1)), a2);
-        const float2 x = fma2(d, s2, make_float2(__uint_as_float(sb[c]), __uint_as_float(sb[c + 1])));
-        sb[c] = __float_as_uint(x.x);
-        sb[c + 1] = __float_as_uint(x.y);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 128; ++c)
-        sb[c] = __float_as_uint(fmaf(near - fabsf(at - static_cast<float>(c)), slope, __uint_as_float(sb[c])));
-    }
-  }
-}
-
-template <class P>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ CUtensorMap k_map,
-                  const __grid_constant__ CUtensorMap v_map, const P p) {
+                  const __grid_constant__ CUtensorMap v_map, const PrefillTcParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // a programmatic dependent of its plan kernel
-  if constexpr (P::kScore) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel waits for completion
   if ((smem_addr(smem_raw) & 1023u) != 0) {
     // not the layout this kernel was built for: do nothing, and make the merge do nothing
@@ -866,29 +482,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     return;
   }
   PrefillTcSmem& s = *reinterpret_cast<PrefillTcSmem*>(smem_raw);
+  build_unit_prefix(p, s);
+  const long long total = s.total_units;
   const int G = gridDim.x;
   int rounds;
-  long long U0, U1;
-  if constexpr (P::kScore) {
-    rounds = p.ws_plan->rounds;
-    U0 = p.ws_tail[blockIdx.x];
-    U1 = p.ws_tail[blockIdx.x + 1];
-  } else {
-    build_unit_prefix(p, s);
-    const long long total = s.total_units;
-    long long T0;
-    plan_split(p, s, G, rounds, T0, U0, U1);
-    if (blockIdx.x == 0) {
-      if (threadIdx.x == 0) {
-        p.ws_header[0] = G;
-        p.ws_header[1] = total;
-        p.ws_header[2] = T0;
-        p.ws_header[3] = static_cast<long long>(rounds) * G;
-      }
-      for (int b = threadIdx.x; b <= p.batch; b += kThreads) {
-        p.ws_prefix[b] = s.unit_prefix[b];
-        p.ws_job_prefix[b] = s.job_prefix[b];
-      }
+  long long T0, U0, U1;
+  plan_split(p, s, G, rounds, T0, U0, U1);
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) {
+      p.ws_header[0] = G;
+      p.ws_header[1] = total;
+      p.ws_header[2] = T0;
+      p.ws_header[3] = static_cast<long long>(rounds) * G;
+    }
+    for (int b = threadIdx.x; b <= p.batch; b += kThreads) {
+      p.ws_prefix[b] = s.unit_prefix[b];
+      p.ws_job_prefix[b] = s.job_prefix[b];
     }
   }
   if (rounds == 0 && U0 >= U1) return;  // uniform across the CTA: nothing allocated yet
@@ -942,14 +551,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const int32_t* bt_row = p.block_table + static_cast<int64_t>(pc.b) * p.bt_stride;
       auto page_token = [&](int j) {
         int tok = oob_token;
-        int key0 = j * kTileN + kPage * lane;
-        bool used = key0 < pc.L;
-        if constexpr (P::kScore) {
-          // a page no row of the job sees is not looked up: it arrives as zeros
-          if (j >= pc.n1) key0 += pc.shift * kTileN;
-          used = key0 < pc.prefix || (key0 + kPage > pc.lo && key0 < pc.hi);
-        }
-        if (lane < kTileN / kPage && used) {
+        const int key0 = j * kTileN + kPage * lane;
+        if (lane < kTileN / kPage && key0 < pc.L) {
           const int e = bt_row[key0 / kPage];
           if (e < 0 || e >= p.num_pages) {
             flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
@@ -1051,10 +654,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         if (!wait_or_flag(&s.piece_full[pslot], (pk / kPieceRing) & 1, p.status)) break;
         const volatile PieceDesc& pv = s.piece[pslot];
         const int pvalid = pv.valid, pjb = pv.jb, pje = pv.je, pL = pv.L;
-        int last = pje - 1;  // the piece's last key tile
-        if constexpr (P::kScore) {
-          if (last >= pv.n1) last += pv.shift;
-        }
         mbar_arrive(&s.piece_empty[pslot]);
         ++pk;
         if (!pvalid || !ok) break;
@@ -1063,7 +662,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         // holds key L - 1 was loaded whole, so the V rows of the pool slots after the last key
         // ([zl, next multiple of 16)) are zeroed, that P = 0 there cannot meet an unwritten
         // (possibly NaN) slot; the pages after it were never loaded (zero fill).
-        const int zl = pL - last * kTileN;
+        const int zl = pL - (pje - 1) * kTileN;
         const int zero_i = (zl > 0 && zl < kTileN && (zl & 15) != 0) ? nt - 1 : -1;
         const uint32_t qph = jc & 1, oph = (jc - 1) & 1;
         ok = wait_or_flag(&s.q_full, qph, p.status) && wait_or_flag(&s.k_full[kst], kph, p.status);
@@ -1134,20 +733,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     __syncwarp();
   } else if (warp == kSchedWarp) {
     // ------------------------------------------------------------------ scheduler
-    if (P::kScore && lane == 0) {
-      if constexpr (P::kScore) {
-        ScoreWalker<P> sw;
-        sw.start(p);
-        for (uint32_t k = 0;; ++k) {
-          const uint32_t slot = k % kPieceRing, ph = (k / kPieceRing) & 1;
-          if (!wait_or_flag(&s.piece_empty[slot], ph ^ 1u, p.status)) break;
-          s.piece[slot] = sw.cur;
-          mbar_arrive(&s.piece_full[slot]);
-          if (!sw.cur.valid) break;
-          sw.next();
-        }
-      }
-    } else if (lane == 0) {
+    if (lane == 0) {
       JobWalker jw;
       jw.start(p, s.unit_prefix, s.job_prefix, rounds, G, U0, U1);
       for (uint32_t k = 0;; ++k) {
@@ -1203,18 +789,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const int nt = pv.je - pjb;
       const int qrow = pv.qt * kTileM + r;
       const int qpos = pv.off + qrow;              // absolute position of this query
-      [[maybe_unused]] RowMask rm;
-      [[maybe_unused]] float slope = 0.f;  // in the units of score_tile
-      [[maybe_unused]] int n1 = 0, shift = 0;
-      if constexpr (P::kScore) {
-        n1 = pv.n1;
-        shift = pv.shift;
-        rm.prefix = pv.prefix;
-        rm.qpos = qpos;
-        rm.lo = qrow < pv.n ? score_first_key(p.score, pv.q0 + qrow, qpos) : 0;
-        rm.nearest = rm.lo <= qpos ? 0 : max(0, qpos + 1 - rm.prefix);
-        if constexpr (P::kBias) slope = slope_over(p.score, 2 * pv.g + t, P::kCap ? 1.0f : p.scale_log2);
-      }
       float m_used = -CUDART_INF_F, l = 0.f;
       for (int i = 0; i < nt; ++i) {
         const uint32_t cur = it + i;
@@ -1232,43 +806,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         uint32_t sb[128];  // raw scores (fp32 bits) of this row
         float cm[4];       // the maximum of each 32-column piece, from the TMEM load itself
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if constexpr (P::kCap) tc::tmem_ld32_absmax(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
-          else tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
-        }
+        for (int c = 0; c < 4; ++c)
+          tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
         tc::tmem_wait_ld();
-        int k0 = (pjb + i) * kTileN;
+        const int k0 = (pjb + i) * kTileN;
         float mx = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
-        bool partial;  // the tile holds keys this row does not see
-        if constexpr (P::kScore) {
-          if (pjb + i >= n1) k0 += shift * kTileN;
-          partial = k0 + kTileN > rm.prefix && (k0 < rm.lo || k0 + kTileN - 1 > qpos);
-          score_tile<P>(p, sb, rm, k0, slope, mx);
-        } else {
-          partial = k0 + kTileN - 1 > qpos;
-        }
-        // With a cap, mx is the capped largest magnitude: it bounds the max from above, and as the
-        // exponents' reference it leaves every weight that matters in fp32's range while the max,
-        // at least -mx, is within 2^-100 of it; beyond that the max itself is taken.
-        const bool need_max = P::kBias || (P::kCap && mx > 50.f);
-        if (partial || need_max) {
-          // mask the keys this row does not see, then take the row max over what is left (8
-          // independent partial maxima, two new elements per three-input max)
-          if constexpr (P::kScore) {
-            if (partial) {
+        if (k0 + kTileN - 1 > qpos) {
+          // the tile crosses this row's position: mask the keys after the query, then take the
+          // row max over what is left (8 independent partial maxima, two new elements per
+          // three-input max)
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const uint32_t seen = row_mask_word(rm, k0 + 32 * w);
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!(seen >> c & 1u)) sb[32 * w + c] = 0xff800000u;  // -inf
-              }
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (k0 + c > qpos) sb[c] = 0xff800000u;  // -inf: key after this query
-          }
+          for (int c = 0; c < 128; ++c)
+            if (k0 + c > qpos) sb[c] = 0xff800000u;  // -inf: key after this query
           float pm[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -1283,8 +832,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sb[120 + k]));
           mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
         }
-        constexpr bool kScaled = P::kCap;  // capped scores are in log2 units already
-        const float mx2 = kScaled ? mx : mx * p.scale_log2;
+        const float mx2 = mx * p.scale_log2;
         const bool grow = mx2 > m_used + kRescaleThreshold;
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? mx2 : m_used;
@@ -1319,9 +867,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           uint32_t pk[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float2 sv = make_float2(__uint_as_float(sb[c * 64 + 2 * k]),
-                                          __uint_as_float(sb[c * 64 + 2 * k + 1]));
-            const float2 x = kScaled ? add2(sv, nm2) : fma2(sv, sc2, nm2);
+            const float2 x = fma2(make_float2(__uint_as_float(sb[c * 64 + 2 * k]),
+                                              __uint_as_float(sb[c * 64 + 2 * k + 1])), sc2, nm2);
             // exp2 on the MUFU unit (moving a share of them to an FMA-pipe polynomial, or
             // fusing the row max into this pass, measured slower on GB300)
             const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
@@ -1346,15 +893,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       tc::fence_after_sync();
       if (leader) mbar_arrive(&s.v_empty[(it + nt - 1) % kVStages]);
       const int pn = pv.n, pq0 = pv.q0, pJ = pv.J, pg = pv.g;
-      [[maybe_unused]] PieceDesc desc;
-      if constexpr (P::kScore) desc = s.piece[pslot];
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.piece_empty[pslot]);
       ++pk;
       const bool live = qrow < pn;
-      // with score options a row may see nothing, or nothing that carries weight: l = 0, o = 0
-      const bool none = P::kScore && l == 0.f;
-      const float inv = none ? 0.f : 1.0f / l;
+      const float inv = 1.0f / l;
       const bool whole = pjb == 0 && pjb + nt == pJ;
       const int head = 2 * pg + t;
       // all of O's 128 columns loaded at once (the scores' registers are free here), one wait;
@@ -1383,18 +926,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             }
           }
         }
-        if (live && p.lse != nullptr) {
-          float v = none ? -CUDART_INF_F : (m_used + log2f(l)) * kLn2;
-          if constexpr (P::kBias) {
-            if (rm.nearest > 0) v -= p.score.slopes[head] * static_cast<float>(rm.nearest);
-          }
-          p.lse[static_cast<int64_t>(pq0 + qrow) * p.hq + head] = v;
-        }
+        if (live && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(pq0 + qrow) * p.hq + head] = (m_used + log2f(l)) * kLn2;
       } else {
         // a piece of a job shared with neighbouring CTAs: slot 1 if it starts the job, else 0.
         // A row that saw no key in this piece contributes nothing: o = 0, lse = -inf.
         const int slot = pjb == 0 ? 1 : 0;
-        const bool empty = P::kScore ? none : m_used == -CUDART_INF_F;
+        const bool empty = m_used == -CUDART_INF_F;
         const float sc_o = empty ? 0.f : inv;
         uint8_t* rec = p.ws_records + (2 * static_cast<size_t>(blockIdx.x) + slot) * kRecordBytes;
         float4* dst = reinterpret_cast<float4*>(rec) + t * 32 * 128 + r;
@@ -1409,38 +947,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         reinterpret_cast<float*>(rec + kRecordO)[t * 128 + r] =
             empty ? -CUDART_INF_F : (m_used + log2f(l)) * kLn2;
-      }
-      if constexpr (P::kScore) {
-        float z = 0.f;  // NaN if any of the row's values is not finite
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) z = fmaf(__uint_as_float(oall[c][k]), 0.f, z);
-        }
-        uint32_t bad = __ballot_sync(0xffffffffu, live && z != 0.f);
-        for (; bad != 0; bad &= bad - 1) {
-          const int who = __ffs(bad) - 1;
-          RowMask wm;
-          wm.prefix = rm.prefix;
-          wm.lo = __shfl_sync(0xffffffffu, rm.lo, who);
-          wm.qpos = __shfl_sync(0xffffffffu, rm.qpos, who);
-          wm.nearest = __shfl_sync(0xffffffffu, rm.nearest, who);
-          const float wmu = __shfl_sync(0xffffffffu, m_used, who);
-          const float winv = __shfl_sync(0xffffffffu, inv, who);
-          const int wrow = desc.qt * kTileM + quarter * 32 + who;
-          float a[4];
-          repair_row(p, desc, wrow, head, wm, P::kBias ? slope_over(p.score, head, 1.0f) : 0.f, wmu == -CUDART_INF_F ? 0.f : wmu, winv, a);
-          __syncwarp();  // after the row's own lane has stored it
-          if (whole) {
-            uint2* dst = reinterpret_cast<uint2*>(
-                p.out + (static_cast<int64_t>(pq0 + wrow) * p.hq + head) * kHeadDim);
-            dst[lane] = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-          } else {
-            uint8_t* rec = p.ws_records + (2 * static_cast<size_t>(blockIdx.x) + (pjb == 0 ? 1 : 0)) * kRecordBytes;
-            reinterpret_cast<float4*>(rec)[(t * 32 + lane) * 128 + quarter * 32 + who] =
-                make_float4(a[0], a[1], a[2], a[3]);
-          }
-        }
       }
       it += nt;
     }
@@ -1457,8 +963,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 // Combine the pieces of jobs that were cut by CTA range boundaries. Eight CTAs per job (two
 // heads x four 32-dim quarters), one thread per row. The pieces are slot 1 of the first CTA and
 // slot 0 of each later CTA.
-template <class P>
-__global__ void __launch_bounds__(kMergeRows) prefill_merge_kernel(const P p) {
+__global__ void __launch_bounds__(kMergeRows) prefill_merge_kernel(const PrefillTcParams p) {
   // programmatic dependent of prefill_tc_kernel: wait until that grid is complete and visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // CTA (qt, g * 8 + t * 4 + quarter, b), counted from the end of the grid: rows of query tile
@@ -1470,30 +975,13 @@ __global__ void __launch_bounds__(kMergeRows) prefill_merge_kernel(const P p) {
   const int y = gridDim.y - 1 - blockIdx.y;
   const int g = y >> 3, t = (y >> 2) & 1, quarter = y & 3;
   const int qt = gridDim.x - 1 - blockIdx.x;
-  long long u0, J;
-  int G, jo, q0, n;  // G: the prefill grid, <= kThreads; the chunk's first packed row and length
-  if constexpr (P::kScore) {
-    const PlanHeader h = *p.ws_plan;
-    const int tile = p.ws_first_tile[b] + qt;
-    if (tile >= p.ws_first_tile[b + 1]) return;
-    const TileDesc d = p.ws_tiles[tile];
-    G = min(h.grid, kThreads);
-    jo = g * h.tiles + tile;
-    u0 = g * h.units + p.ws_units[tile];
-    J = d.J;
-    q0 = d.q0;
-    n = d.n;
-  } else {
-    const SeqGeom s = seq_geom(p, b, false);
-    if (qt >= s.nqt) return;
-    G = min(static_cast<int>(p.ws_header[0]), kThreads);
-    jo = p.ws_job_prefix[b] + g * s.nqt + qt;
-    u0 = p.ws_prefix[b] + g * s.T + units_before(s, qt);
-    J = tiles_of(s, qt);
-    q0 = s.q0;
-    n = s.n;
-  }
+  const SeqGeom s = seq_geom(p, b, false);
+  if (qt >= s.nqt) return;
+  const int jo = p.ws_job_prefix[b] + g * s.nqt + qt;
   if (jo < p.ws_header[3]) return;  // done whole in the round-robin phase
+  const int G = min(static_cast<int>(p.ws_header[0]), kThreads);  // the prefill grid, <= kThreads
+  const long long u0 = p.ws_prefix[b] + g * s.T + units_before(s, qt);
+  const long long J = tiles_of(s, qt);
   // the split's range starts, staged in shared memory: one round of loads instead of a chain of
   // dependent ones per binary search
   __shared__ long long tail[kThreads + 1];
@@ -1513,7 +1001,7 @@ __global__ void __launch_bounds__(kMergeRows) prefill_merge_kernel(const P p) {
   if (c0 == c1) return;
   const int r = threadIdx.x;
   const int qrow = qt * kTileM + r;
-  if (qrow >= n) return;
+  if (qrow >= s.n) return;
   // the piece in CTA c0 starts the job (slot 1); later CTAs hold continuations (slot 0); CTAs with
   // an empty range in between hold nothing
   auto rec_of = [&](int c) {
@@ -1547,9 +1035,9 @@ __global__ void __launch_bounds__(kMergeRows) prefill_merge_kernel(const P p) {
       acc[4 * d + 3] += w * v[d].w;
     }
   }
-  const float inv = P::kScore && sum == 0.f ? 0.f : 1.0f / sum;
+  const float inv = 1.0f / sum;
   const int head = 2 * g + t;
-  uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(q0 + qrow) * p.hq + head) * kHeadDim +
+  uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(s.q0 + qrow) * p.hq + head) * kHeadDim +
                                         32 * quarter);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -1560,16 +1048,8 @@ __global__ void __launch_bounds__(kMergeRows) prefill_merge_kernel(const P p) {
     w.w = pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv);
     dst[k] = w;
   }
-  if (quarter == 0 && p.lse != nullptr) {
-    float v = m + logf(sum);
-    if constexpr (P::kBias) {  // distances were counted from the nearest visible key
-      const TileDesc d = p.ws_tiles[p.ws_first_tile[b] + qt];
-      const int pos = d.off + qrow;
-      if (score_first_key(p.score, q0 + qrow, pos) > pos)
-        v -= p.score.slopes[head] * static_cast<float>(max(0, pos + 1 - d.prefix));
-    }
-    p.lse[static_cast<int64_t>(q0 + qrow) * p.hq + head] = v;
-  }
+  if (quarter == 0 && p.lse != nullptr)
+    p.lse[static_cast<int64_t>(s.q0 + qrow) * p.hq + head] = m + logf(sum);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1578,11 +1058,10 @@ __global__ void __launch_bounds__(kMergeRows) prefill_merge_kernel(const P p) {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct PrefillWs {
-  size_t header, prefix, job_prefix, tail, records, plan, tiles, units, first_tile, total;
+  size_t header, prefix, job_prefix, tail, records, total;
 };
 
-// max_tiles: query tiles of a call with score options (its plan comes after the records), else 0.
-PrefillWs prefill_ws(int batch, int grid, int max_tiles = 0) {
+PrefillWs prefill_ws(int batch, int grid) {
   PrefillWs w;
   w.header = 0;
   w.prefix = 256;
@@ -1590,18 +1069,8 @@ PrefillWs prefill_ws(int batch, int grid, int max_tiles = 0) {
   w.tail = align256(w.job_prefix + sizeof(int32_t) * (batch + 1));
   w.records = align256(w.tail + sizeof(long long) * (grid + 1));
   w.total = align256(w.records + 2 * static_cast<size_t>(grid) * kRecordBytes);
-  if (max_tiles > 0) {
-    w.plan = w.total;
-    w.tiles = align256(w.plan + sizeof(PlanHeader));
-    w.units = align256(w.tiles + sizeof(TileDesc) * max_tiles);
-    w.first_tile = align256(w.units + sizeof(long long) * (max_tiles + 1));
-    w.total = align256(w.first_tile + sizeof(int32_t) * (batch + 1));
-  }
   return w;
 }
-
-// Query tiles of a call: each chunk may end in one that is not full.
-int score_tiles(int64_t total_q, int batch) { return static_cast<int>(total_q / kTileM + batch); }
 
 // One persistent CTA per SM; plan_split gives each CTA one thread of its CTA, so at most kThreads.
 int prefill_grid() { return std::min(sm_count_current_device(), kThreads); }
@@ -1614,96 +1083,13 @@ size_t prefill_workspace_bytes(int batch) {
   return prefill_ws(batch, grid).total;
 }
 
-size_t prefill_score_workspace_bytes(int batch, int total_q) {
-  const int grid = prefill_grid();
-  if (grid <= 0 || batch <= 0 || total_q < 0) return 0;
-  return prefill_ws(batch, grid, score_tiles(total_q, batch)).total;
-}
-
-namespace {
-
-// Attributes of one instance and its merge, once per device and thread.
-template <class P>
-pa_status configure_prefill(int smem) {
-  static thread_local int configured_device = -1;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (configured_device == dev) return PA_OK;
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(prefill_tc)");
-  // same carveout for the shared-memory-free merge kernel: no reconfiguration between them
-  e = cudaFuncSetAttribute(prefill_merge_kernel<P>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(prefill merge)");
-  // The in-kernel register split needs the full launch budget; a build that launched with
-  // fewer registers per thread would make setmaxnreg.inc wait forever, so refuse to launch.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prefill_tc_kernel<P>);
-  if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncGetAttributes(prefill_tc)");
-  if (fa.numRegs < kLaunchRegs) {
-    snprintf_error("prefill_tc_kernel built with %d registers/thread, needs %d for its split",
-                   fa.numRegs, kLaunchRegs);
-    return PA_ERR_UNSUPPORTED;
-  }
-  configured_device = dev;
-  return PA_OK;
-}
-
-template <class P>
-cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, const P& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-template <class P>
-pa_status launch_merge(const P& p, int max_q_len, cudaStream_t stream) {
-  const cudaError_t e = launch_dependent(prefill_merge_kernel<P>,
-                                         dim3((max_q_len + kTileM - 1) / kTileM, p.hkv * 8, p.batch),
-                                         kMergeRows, p, stream);
-  return e == cudaSuccess ? PA_OK : record_cuda_error(e, "prefill_merge_kernel");
-}
-
-// Plan, attention and merge of one call with score options.
-template <class P>
-pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const P& p,
-                       int grid, int max_q_len, cudaStream_t stream) {
-  const int smem = static_cast<int>(sizeof(PrefillTcSmem));
-  const pa_status st = configure_prefill<P>(smem);
-  if (st != PA_OK) return st;
-  prefill_plan_kernel<P><<<1, kPlanThreads, 0, stream>>>(p, grid);
-  PA_CHECK_LAUNCH("prefill_plan_kernel");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<P>, qm, km, vm, p);
-  if (e != cudaSuccess) return record_cuda_error(e, "prefill_tc_kernel");
-  return launch_merge(p, max_q_len, stream);
-}
-
-}  // namespace
-
 pa_status launch_prefill_tc(int32_t hkv, const void* q, int32_t total_q, const int32_t* cu_q_lens,
                             const void* k_pool, const void* v_pool, int64_t num_pages,
                             const int32_t* block_table, int32_t bt_stride,
                             const int32_t* seq_lens, int32_t batch, int32_t max_q_len,
                             float softmax_scale, void* out, float* lse, void* workspace,
                             size_t workspace_bytes, int32_t* status, cudaStream_t stream,
-                            int32_t max_ctas, const pa_score_opts* score) {
+                            int32_t max_ctas) {
   if (batch > kMaxBatch) {
     snprintf_error("attn_prefill_chunk: at most %d chunks per call", kMaxBatch);
     return PA_ERR_UNSUPPORTED;
@@ -1713,8 +1099,7 @@ pa_status launch_prefill_tc(int32_t hkv, const void* q, int32_t total_q, const i
   if (full_grid <= 0) return PA_ERR_CUDA;
   // one persistent CTA per SM, or fewer when the caller caps the grid (the plan adapts to it)
   const int grid = max_ctas > 0 ? std::min(full_grid, static_cast<int>(max_ctas)) : full_grid;
-  const int max_tiles = score != nullptr ? score_tiles(total_q, batch) : 0;
-  const PrefillWs w = prefill_ws(batch, grid, max_tiles);
+  const PrefillWs w = prefill_ws(batch, grid);
   if (workspace == nullptr || workspace_bytes < w.total) return PA_ERR_WORKSPACE_TOO_SMALL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
   CUtensorMap qm, km, vm;
@@ -1724,6 +1109,30 @@ pa_status launch_prefill_tc(int32_t hkv, const void* q, int32_t total_q, const i
       !make_map_3d(&vm, v_pool, static_cast<uint64_t>(num_pages) * kPage, hkv, kPage)) {
     snprintf_error("cuTensorMapEncodeTiled failed for the prefill operands");
     return PA_ERR_CUDA;
+  }
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int smem = static_cast<int>(sizeof(PrefillTcSmem));
+  if (configured_device != dev) {
+    cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(prefill_tc)");
+    // same carveout for the shared-memory-free merge kernel: no reconfiguration between them
+    e = cudaFuncSetAttribute(prefill_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(prefill merge)");
+    // The in-kernel register split needs the full launch budget; a build that launched with
+    // fewer registers per thread would make setmaxnreg.inc wait forever, so refuse to launch.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, prefill_tc_kernel);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncGetAttributes(prefill_tc)");
+    if (fa.numRegs < kLaunchRegs) {
+      snprintf_error("prefill_tc_kernel built with %d registers/thread, needs %d for its split",
+                     fa.numRegs, kLaunchRegs);
+      return PA_ERR_UNSUPPORTED;
+    }
+    configured_device = dev;
   }
   PrefillTcParams p;
   p.hkv = hkv;
@@ -1744,31 +1153,20 @@ pa_status launch_prefill_tc(int32_t hkv, const void* q, int32_t total_q, const i
   p.ws_job_prefix = reinterpret_cast<int32_t*>(ws + w.job_prefix);
   p.ws_tail = reinterpret_cast<long long*>(ws + w.tail);
   p.ws_records = ws + w.records;
-  if (score == nullptr) {
-    const int smem = static_cast<int>(sizeof(PrefillTcSmem));
-    const pa_status st = configure_prefill<PrefillTcParams>(smem);
-    if (st != PA_OK) return st;
-    prefill_tc_kernel<PrefillTcParams><<<grid, kThreads, smem, stream>>>(qm, km, vm, p);
-    PA_CHECK_LAUNCH("prefill_tc_kernel");
-    return launch_merge(p, max_q_len, stream);
-  }
-  auto scored = [&](auto sp) {
-    static_cast<PrefillTcParams&>(sp) = p;
-    sp.score = score_params(*score, softmax_scale, &sp.scale_log2);
-    sp.total_q = total_q;
-    sp.max_tiles = max_tiles;
-    sp.q_rows = static_cast<const uint16_t*>(q);
-    sp.k_rows = static_cast<const uint16_t*>(k_pool);
-    sp.v_rows = static_cast<const uint16_t*>(v_pool);
-    sp.ws_plan = reinterpret_cast<PlanHeader*>(ws + w.plan);
-    sp.ws_tiles = reinterpret_cast<TileDesc*>(ws + w.tiles);
-    sp.ws_units = reinterpret_cast<long long*>(ws + w.units);
-    sp.ws_first_tile = reinterpret_cast<int32_t*>(ws + w.first_tile);
-    return launch_score(qm, km, vm, sp, grid, max_q_len, stream);
-  };
-  const bool cap = score->softcap > 0.f, bias = score->alibi_slopes != nullptr;
-  return cap ? (bias ? scored(PrefillScoreParams<true, true>()) : scored(PrefillScoreParams<true, false>()))
-             : (bias ? scored(PrefillScoreParams<false, true>()) : scored(PrefillScoreParams<false, false>()));
+  prefill_tc_kernel<<<grid, kThreads, smem, stream>>>(qm, km, vm, p);
+  PA_CHECK_LAUNCH("prefill_tc_kernel");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((max_q_len + kTileM - 1) / kTileM, hkv * 8, batch);
+  cfg.blockDim = dim3(kMergeRows);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_merge_kernel, p);
+  if (e != cudaSuccess) return record_cuda_error(e, "prefill_merge_kernel");
+  return PA_OK;
 }
 
 }  // namespace pa

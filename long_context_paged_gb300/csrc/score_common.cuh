@@ -27,16 +27,16 @@ struct ScoreParams {
   int32_t max_prefix;
   const int32_t* row_start;  // [rows] or null
   // softcap * log2 e * tanh(q_scale * s) of a raw product s as an odd polynomial s P(s^2), for
-  // |s| <= poly_max[k] (4 terms up to |q_scale s| = 1/2, 6 terms up to 1; 0: not usable)
-  float poly4[4], poly6[6], poly_max[2];
+  // |s| <= poly_max (|q_scale s| <= 1; 0: not usable)
+  float poly[6], poly_max;
 };
 
-// Coefficients of x P(x^2) nearest to tanh x on |x| <= 1/2 (error 1.3e-7) and |x| <= 1 (2.5e-7):
-// least maximum error over a dense grid by iteratively reweighted least squares (Lawson), rounded to
-// fp32. With a cap of 50 the errors are 2^-17 and 2^-16 of a score.
-constexpr double kTanh4[4] = {9.999976754e-01, -3.332065642e-01, 1.314514577e-01, -4.337248206e-02};
-constexpr double kTanh6[6] = {9.999968410e-01, -3.332400322e-01, 1.325352490e-01,
-                              -5.097286403e-02, 1.611418277e-02, -2.839466557e-03};
+// Coefficients of x P(x^2) nearest to tanh x on |x| <= 1: least maximum error over a dense grid by
+// iteratively reweighted least squares (Lawson), rounded to fp32. The error, 2.5e-7, times a cap of 50
+// is 2^-16 of a score.
+constexpr int kTanhTerms = 6;
+constexpr double kTanh[kTanhTerms] = {9.999968410e-01, -3.332400322e-01, 1.325352490e-01,
+                                      -5.097286403e-02, 1.611418277e-02, -2.839466557e-03};
 
 inline bool score_opts_valid(const pa_score_opts& o) {
   return (o.softcap == 0.f || (o.softcap >= 1e-6f && o.softcap < 1e30f)) && o.window >= 0 && o.max_prefix_len >= 0 &&
@@ -62,16 +62,12 @@ inline ScoreParams score_params(const pa_score_opts& o, float softmax_scale, flo
   s.max_prefix = o.max_prefix_len;
   s.row_start = o.row_start;
   *q_scale = o.softcap > 0.f ? softmax_scale / o.softcap : softmax_scale * kLog2e;
-  s.poly_max[0] = s.poly_max[1] = 0.f;
+  s.poly_max = 0.f;
   const double x = *q_scale;
   if (o.softcap > 0.f && x >= 0x1p-10 && x <= 0x1p10) {  // the folded coefficients stay in range
     double a = static_cast<double>(s.cap_log2) * x;
-    for (int k = 0; k < 6; ++k, a *= x * x) {
-      if (k < 4) s.poly4[k] = static_cast<float>(kTanh4[k] * a);
-      s.poly6[k] = static_cast<float>(kTanh6[k] * a);
-    }
-    s.poly_max[0] = static_cast<float>(0.5 / x);
-    s.poly_max[1] = static_cast<float>(1.0 / x);
+    for (int k = 0; k < kTanhTerms; ++k, a *= x * x) s.poly[k] = static_cast<float>(kTanh[k] * a);
+    s.poly_max = static_cast<float>(1.0 / x);
   }
   return s;
 }
