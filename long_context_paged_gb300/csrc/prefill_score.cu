@@ -442,28 +442,66 @@ struct CapPoly {
   }
 };
 
-// Whether a warp's tile can be scored in the weights' own pass: no key masked, the products within
-// the tanh polynomial's range, the bias linear over the tile, and a bound `top` of each row's largest
-// score near enough to it. mx: the largest raw product (magnitude with a cap). With a cap,
-// cap tanh(max |s|) bounds the scores and their max is at least its negative; with a bias, the
-// bias of the nearest column bounds the bias, and falls by 127 slopes over the tile. The exponents'
-// reference may be above the max by up to kMaxSlack: the weights that matter then stay 2^-26 above
-// fp32's smallest normal number. d0: bias distance of column 0.
+// -inf for the keys that the row does not see.
+__device__ __forceinline__ void mask_tile(uint32_t (&sb)[kTileN], const RowMask& rm, int k0) {
+#pragma unroll
+  for (int w = 0; w < kTileN / 32; ++w) {
+    const uint32_t seen = row_mask_word(rm, k0 + 32 * w);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!(seen >> c & 1u)) sb[32 * w + c] = 0xff800000u;
+  }
+}
+
+// The maximum of each 32-column piece (four independent partial maxima of two elements a step).
+__device__ __forceinline__ void piece_max(const uint32_t (&sb)[kTileN], float (&cm)[4]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t* v = sb + 32 * w;
+    float pm[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) pm[k] = fmax3(__uint_as_float(v[k]), __uint_as_float(v[k + 4]), __uint_as_float(v[k + 8]));
+#pragma unroll
+    for (int c = 12; c < 28; c += 8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pm[k] = fmax3(pm[k], __uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k]));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(v[28 + k]));
+    cm[w] = fmax3(pm[0], pm[1], fmaxf(pm[2], pm[3]));
+  }
+}
+
+// Whether a warp's tile can be scored in the weights' own pass: the products within the tanh
+// polynomial's range and no key masked (with a cap), the bias linear over the tile's visible keys,
+// and a bound `top` of each row's largest score near enough to it. cm: the largest visible product of
+// each 32-column piece (magnitude with a cap). cap tanh(max |s|) bounds capped scores, and their max
+// is at least its negative; the distance of a piece's nearest column bounds its bias, which falls by
+// 31 slopes over the piece. The exponents' reference may be above the max by up to kMaxSlack: the
+// weights that matter then stay 2^-26 above fp32's smallest normal number. d0: bias distance of
+// column 0.
 template <class P>
-__device__ __forceinline__ bool score_bound(const P& p, const RowMask& rm, int k0, float slope2, float mx,
+__device__ __forceinline__ bool score_bound(const P& p, const RowMask& rm, int k0, float slope2, const float (&cm)[4],
                                             bool partial, float& top, float& d0) {
-  bool good = !partial;
+  bool good = true;
   float slack = 0.f;
   if constexpr (P::kCap) {
-    top = p.score.cap_log2 * tanh_exp(mx * p.scale_log2);
+    const float hi = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
+    good = !partial && hi <= p.score.poly_max;
+    top = p.score.cap_log2 * tanh_exp(hi * p.scale_log2);
     slack = 2.f * top;
-    good = good && mx <= p.score.poly_max;
   }
   if constexpr (P::kBias) {
     d0 = static_cast<float>(rm.qpos - k0 - rm.nearest);
-    top -= slope2 * (slope2 >= 0.f ? d0 - (kTileN - 1) : d0);
-    slack += fabsf(slope2) * (kTileN - 1);
-    good = good && k0 + kTileN - 1 <= rm.qpos;
+    top = -CUDART_INF_F;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float d = fmaxf(d0 - (slope2 >= 0.f ? 32.f * c + 31.f : 32.f * c), 0.f);
+      const float hi = P::kCap ? p.score.cap_log2 * tanh_exp(cm[c] * p.scale_log2) : cm[c] * p.scale_log2;
+      top = fmaxf(top, fmaf(-slope2, d, hi));
+    }
+    slack += fabsf(slope2) * 31.f;
+    good = good && (k0 + kTileN - 1 <= rm.qpos || k0 >= rm.prefix);  // keys after the row: in the prefix
   }
   return __all_sync(0xffffffffu, good && slack <= kMaxSlack);
 }
@@ -471,15 +509,29 @@ __device__ __forceinline__ bool score_bound(const P& p, const RowMask& rm, int k
 // Any other tile: scores in log2 units, in place.
 template <class P>
 __device__ __forceinline__ void score_tile(const P& p, uint32_t (&sb)[kTileN], const RowMask& rm, int k0,
-                                           float slope2) {
+                                           float slope2, float mx) {
   const float at = static_cast<float>(rm.qpos - k0);  // the column of the row's own position
   const float near = static_cast<float>(rm.nearest);
+  if constexpr (P::kCap) {
+    if (__all_sync(0xffffffffu, mx <= p.score.poly_max)) {
+      const CapPoly poly(p.score.poly);
 #pragma unroll
-  for (int c = 0; c < kTileN; ++c) {
-    float x = __uint_as_float(sb[c]) * p.scale_log2;
-    if constexpr (P::kCap) x = p.score.cap_log2 * tanh_exp(x);
-    if constexpr (P::kBias) x = fmaf(near - fabsf(at - static_cast<float>(c)), slope2, x);
-    sb[c] = __float_as_uint(x);
+      for (int c = 0; c < kTileN; c += 2) {
+        const float2 y = poly(make_float2(__uint_as_float(sb[c]), __uint_as_float(sb[c + 1])), make_float2(0.f, 0.f));
+        sb[c] = __float_as_uint(y.x);
+        sb[c + 1] = __float_as_uint(y.y);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kTileN; ++c)
+        sb[c] = __float_as_uint(p.score.cap_log2 * tanh_exp(__uint_as_float(sb[c]) * p.scale_log2));
+    }
+  }
+  if constexpr (P::kBias) {
+    const float scale = P::kCap ? 1.0f : p.scale_log2;
+#pragma unroll
+    for (int c = 0; c < kTileN; ++c)
+      sb[c] = __float_as_uint(fmaf(near - fabsf(at - static_cast<float>(c)), slope2, __uint_as_float(sb[c]) * scale));
   }
 }
 
@@ -796,43 +848,27 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
           else tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
         }
         tc::tmem_wait_ld();
-        const float mx = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
         const int j = pjb + i;
         const int k0 = (j < n1 ? j : j + shift) * kTileN;
         const bool partial = k0 + kTileN > rm.prefix && (k0 < rm.lo || k0 + kTileN - 1 > rm.qpos);
-        float top = mx * p.scale_log2;  // the scores' maximum, or a bound of it (log2 units)
-        bool one_pass = !partial;
+        bool one_pass = true;             // (scores without options always are)
         [[maybe_unused]] float d0 = 0.f;  // bias distance of column 0, from the nearest visible key
-        if constexpr (kLog2Units) {
-          one_pass = score_bound<P>(p, rm, k0, slope2, mx, partial, top, d0);
-          if (!one_pass) score_tile<P>(p, sb, rm, k0, slope2);
+        float top = 0.f;                  // the scores' maximum, or a bound of it (log2 units)
+        // without a cap the raw products are masked: a bias leaves -inf what it is
+        if (!P::kCap && partial) {
+          mask_tile(sb, rm, k0);
+          piece_max(sb, cm);
         }
-        if (!one_pass) {
-          if (partial) {
-#pragma unroll
-            for (int w = 0; w < kTileN / 32; ++w) {
-              const uint32_t seen = row_mask_word(rm, k0 + 32 * w);
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(seen >> c & 1u)) sb[32 * w + c] = 0xff800000u;  // -inf
-            }
+        if constexpr (kLog2Units) {
+          one_pass = score_bound<P>(p, rm, k0, slope2, cm, partial, top, d0);
+          if (!one_pass) {
+            score_tile<P>(p, sb, rm, k0, slope2, fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3])));
+            if (P::kCap && partial) mask_tile(sb, rm, k0);
+            piece_max(sb, cm);
+            top = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
           }
-          // the row max over what is left (8 independent partial maxima, two new elements per
-          // three-input max)
-          float pm[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            pm[k] = fmax3(__uint_as_float(sb[k]), __uint_as_float(sb[k + 8]), __uint_as_float(sb[k + 16]));
-#pragma unroll
-          for (int c = 24; c < 120; c += 16) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              pm[k] = fmax3(pm[k], __uint_as_float(sb[c + k]), __uint_as_float(sb[c + 8 + k]));
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], __uint_as_float(sb[120 + k]));
-          top = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-          if constexpr (!kLog2Units) top *= p.scale_log2;
+        } else {
+          top = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3])) * p.scale_log2;
         }
         const bool grow = top > m_used + kRescaleThreshold;
         if (__any_sync(0xffffffffu, grow)) {
