@@ -162,18 +162,45 @@ def load():
 # ----------------------------------------------------------------------------------------------
 # marshalling helpers
 # ----------------------------------------------------------------------------------------------
+_dims_cache = {}
+
+
 def _dims(dims):
-    return Dims(*(dims or DEFAULT_DIMS))
+    """The Dims of a (num_q_heads, num_kv_heads, head_dim, page_size) tuple, made once per tuple."""
+    dims = DEFAULT_DIMS if dims is None else dims
+    try:
+        return _dims_cache[dims]
+    except (KeyError, TypeError):
+        d = Dims(*(dims or DEFAULT_DIMS))
+        if isinstance(dims, tuple):
+            _dims_cache[dims] = d
+        return d
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
+    """The stream's handle; the current stream of the current device for None (read directly: making
+    a torch.cuda.Stream object for it takes longer than a kernel launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on `stream` (None: the current one): allocated from that stream's memory,
+    so that the block is neither still read by other work nor handed out again before this work ran."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _need(t, name, dtype, ndim=None):
@@ -216,14 +243,54 @@ def _rows_at_least(name, t, n):
         raise ValueError(f"{name} must have at least {n} rows, got {t.shape[0]}")
 
 
+_heads_cache = {}
+
+
 def _heads(dims):
     """(query heads, KV heads) of a shape the library supports, else None: the library itself
     then rejects the call (PA_ERR_UNSUPPORTED) and the shape checks below are skipped."""
+    dims = DEFAULT_DIMS if dims is None else dims
+    try:
+        return _heads_cache[dims]
+    except (KeyError, TypeError):
+        pass
     d = _dims(dims)
+    r = None
     if (d.head_dim == 128 and d.page_size == 16 and d.num_kv_heads in (1, 2, 4, 8)
             and d.num_q_heads == 2 * d.num_kv_heads):
-        return d.num_q_heads, d.num_kv_heads
-    return None
+        r = d.num_q_heads, d.num_kv_heads
+    if isinstance(dims, tuple):
+        _heads_cache[dims] = r
+    return r
+
+
+def _tensor(call, t, name, dtype, dev):
+    """data_ptr of a contiguous tensor of this type on device `dev`: the checks of _need and
+    _on_device in the fewest attribute reads, since a small call's time is its checks'."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a tensor") from None
+    _need(t, name, dtype)
+    _on_device(call, t)
+    raise ValueError(f"{call}: tensors must be on one device (cuda:{dev}), got {t.device}")
+
+
+def _device(call, t, name, dtype):
+    """The CUDA device index of a call's first tensor, which has to be the current device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _need(t, name, dtype)
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        _on_device(call, t)
+    return dev
+
+
+def _sized(name, t, shape):
+    """t must have exactly this shape."""
+    if t.shape != shape:
+        _shape(name, t, shape)
 
 
 def _pools(k_pool, v_pool, hkv):
@@ -288,34 +355,49 @@ def prefill_score_workspace_size(batch: int, total_q: int, dims=None) -> int:
     return int(load().pa_prefill_score_workspace_size(_dims(dims), batch, total_q))
 
 
-def _workspace(nbytes, device, workspace):
+_ws_sizes = {}
+
+
+def _workspace_size(fn, *key):
+    """fn(*key), a size that depends on the arguments and the device alone, looked up once."""
+    if isinstance(key[-1], list):  # dims given as a list
+        key = key[:-1] + (tuple(key[-1]),)
+    key = (fn, torch.cuda.current_device()) + key
+    n = _ws_sizes.get(key)
+    if n is None:
+        if len(_ws_sizes) > 4096:  # (a server's shapes are few; this bounds a caller that varies them)
+            _ws_sizes.clear()
+        n = _ws_sizes[key] = fn(*key[2:])
+    return n
+
+
+def _workspace(nbytes, device, workspace, stream=None):
     if workspace is not None:
         return workspace
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return _empty(max(nbytes, 256), torch.uint8, device, stream)
 
 
-def _score(call, hq, batch, rows, max_seq_len, softcap, alibi_slopes, window, prefix_lens,
+def _score(call, dev, hq, batch, rows, max_seq_len, softcap, alibi_slopes, window, prefix_lens,
            max_prefix_len, row_start):
     """The score options as a ScoreOpts, or None when none is set. Tensors are checked here; the
     caller keeps them alive until the call has been made."""
-    if (not softcap and alibi_slopes is None and not window and prefix_lens is None
-            and row_start is None):
+    slopes = prefix = start = 0
+    if alibi_slopes is not None:
+        slopes = _tensor(call, alibi_slopes, "alibi_slopes", torch.float32, dev)
+        _sized("alibi_slopes", alibi_slopes, (hq,))
+    if prefix_lens is not None:
+        prefix = _tensor(call, prefix_lens, "prefix_lens", torch.int32, dev)
+        _rows_at_least("prefix_lens", prefix_lens, batch)
+        if max_prefix_len is None:
+            max_prefix_len = max_seq_len
+    else:
+        max_prefix_len = 0
+    if row_start is not None:
+        start = _tensor(call, row_start, "row_start", torch.int32, dev)
+        _rows_at_least("row_start", row_start, rows)
+    elif not softcap and not window and not slopes and prefix_lens is None:
         return None
-    for t, n, d, shape in ((alibi_slopes, "alibi_slopes", torch.float32, hq),
-                           (prefix_lens, "prefix_lens", torch.int32, batch),
-                           (row_start, "row_start", torch.int32, rows)):
-        if t is not None:
-            _need(t, n, d, 1)
-            if n == "alibi_slopes":
-                _shape(n, t, (shape,))
-            else:
-                _rows_at_least(n, t, shape)
-    _on_device(call, alibi_slopes, prefix_lens, row_start)
-    if max_prefix_len is None:
-        max_prefix_len = max_seq_len if prefix_lens is not None else 0
-    return ScoreOpts(float(softcap), 0 if alibi_slopes is None else alibi_slopes.data_ptr(),
-                     int(window), 0 if prefix_lens is None else prefix_lens.data_ptr(),
-                     int(max_prefix_len), 0 if row_start is None else row_start.data_ptr())
+    return ScoreOpts(float(softcap), slopes, int(window), prefix, int(max_prefix_len), start)
 
 
 def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int,
@@ -331,43 +413,60 @@ def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int
     Score options (attn_decode_paged_score). Key j is seen from position i when j < prefix_lens[b]
     or max(row_start[b], i - window + 1) <= j <= i; its score is softcap * tanh(s / softcap) minus
     alibi_slopes[h] * |i - j|. max_prefix_len: host bound of prefix_lens (default max_seq_len)."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(k_pool, "k_pool", torch.bfloat16, 4)
-    _need(v_pool, "v_pool", torch.bfloat16, 4)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    B = q.shape[0]
-    _rows_at_least("block_table", block_table, B)
+    call = "attn_decode_paged"
+    dev = _device(call, q, "q", torch.bfloat16)
+    pq = _tensor(call, q, "q", torch.bfloat16, dev)
+    pk = _tensor(call, k_pool, "k_pool", torch.bfloat16, dev)
+    pv = _tensor(call, v_pool, "v_pool", torch.bfloat16, dev)
+    pbt = _tensor(call, block_table, "block_table", torch.int32, dev)
+    psl = _tensor(call, seq_lens, "seq_lens", torch.int32, dev)
+    for t, n, d in ((q, "q", 3), (k_pool, "k_pool", 4), (v_pool, "v_pool", 4),
+                    (block_table, "block_table", 2), (seq_lens, "seq_lens", 1)):
+        if t.dim() != d:
+            raise ValueError(f"{n} must have {d} dims, got {t.dim()}")
+    B, hq = q.shape[0], q.shape[1]
+    rows, bt_stride = block_table.shape
+    if rows < B:
+        _rows_at_least("block_table", block_table, B)
     _rows_at_least("seq_lens", seq_lens, B)
+    num_pages = k_pool.shape[0]
     heads = _heads(dims)
     if heads is not None:
-        _shape("q", q, (B, heads[0], 128))
-        _pools(k_pool, v_pool, heads[1])
-        _given(out, "out", torch.bfloat16, (B, heads[0], 128))
-        _given(lse, "lse", torch.float32, (B, heads[0]))
+        _sized("q", q, (B, heads[0], 128))
+        _sized("k_pool", k_pool, (num_pages, 16, heads[1], 128))
+        _sized("v_pool", v_pool, (num_pages, 16, heads[1], 128))
     if out is None:
-        out = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = torch.empty(B, q.shape[1], dtype=torch.float32, device=q.device)
-    ws_bytes = decode_workspace_size(B, max_seq_len, split_tokens, dims)
-    workspace = _workspace(ws_bytes, q.device, workspace)
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _on_device("attn_decode_paged", q, k_pool, v_pool, block_table, seq_lens, out, lse,
-               workspace, status)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+        po = out.data_ptr()
+    else:
+        po = _tensor(call, out, "out", torch.bfloat16, dev)
+        _sized("out", out, q.shape)
+    if lse is None:
+        if want_lse:
+            lse = _empty((B, hq), torch.float32, q.device, stream)
+        pl = None if lse is None else lse.data_ptr()
+    else:
+        pl = _tensor(call, lse, "lse", torch.float32, dev)
+        _sized("lse", lse, (B, hq))
+    max_seq_len, split_tokens = int(max_seq_len), int(split_tokens)
+    score = _score(call, dev, hq, B, B, max_seq_len, softcap, alibi_slopes, window, prefix_lens,
+                   max_prefix_len, row_start)
+    if workspace is None:
+        workspace = _workspace(_workspace_size(decode_workspace_size, B, max_seq_len, split_tokens, dims),
+                               q.device, None, stream)
+    else:
+        _on_device(call, workspace)
+    ps = None if status is None else _tensor(call, status, "status", torch.int32, dev)
     lib = load()
-    args = (_dims(dims), _ptr(q), _ptr(k_pool), _ptr(v_pool), k_pool.shape[0], _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), B, int(max_seq_len), float(softmax_scale),
-            int(split_tokens), _ptr(out), _ptr(lse), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    args = (_dims(dims), pq, pk, pv, num_pages, pbt, bt_stride, psl, B, max_seq_len, float(softmax_scale),
+            split_tokens, po, pl, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            ps, _stream(stream))
     keep, ref = _opts(max_ctas)
-    score = _score("attn_decode_paged", q.shape[1], B, B, int(max_seq_len), softcap, alibi_slopes,
-                   window, prefix_lens, max_prefix_len, row_start)
     if score is not None:
-        _check("attn_decode_paged_score", lib.attn_decode_paged_score(*args, ref,
-                                                                      ctypes.byref(score)))
+        _check("attn_decode_paged_score",
+               lib.attn_decode_paged_score(*args, ref, ctypes.byref(score)))
     elif ref is None:
-        _check("attn_decode_paged", lib.attn_decode_paged(*args))
+        _check(call, lib.attn_decode_paged(*args))
     else:
         _check("attn_decode_paged_ex", lib.attn_decode_paged_ex(*args, ref))
     del keep
@@ -420,49 +519,63 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
     Score options as in attn_decode_paged, row_start per query row [Tq]
     (attn_prefill_chunk_score; a workspace passed in then has prefill_score_workspace_size
     bytes)."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
-    _need(k_pool, "k_pool", torch.bfloat16, 4)
-    _need(v_pool, "v_pool", torch.bfloat16, 4)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
+    call = "attn_prefill_chunk"
+    dev = _device(call, q, "q", torch.bfloat16)
+    pq = _tensor(call, q, "q", torch.bfloat16, dev)
+    pcu = _tensor(call, cu_q_lens, "cu_q_lens", torch.int32, dev)
+    pk = _tensor(call, k_pool, "k_pool", torch.bfloat16, dev)
+    pv = _tensor(call, v_pool, "v_pool", torch.bfloat16, dev)
+    pbt = _tensor(call, block_table, "block_table", torch.int32, dev)
+    psl = _tensor(call, seq_lens, "seq_lens", torch.int32, dev)
+    for t, n, d in ((q, "q", 3), (cu_q_lens, "cu_q_lens", 1), (k_pool, "k_pool", 4),
+                    (v_pool, "v_pool", 4), (block_table, "block_table", 2), (seq_lens, "seq_lens", 1)):
+        if t.dim() != d:
+            raise ValueError(f"{n} must have {d} dims, got {t.dim()}")
     B = seq_lens.shape[0]
-    Tq = q.shape[0]
+    Tq, hq = q.shape[0], q.shape[1]
+    rows, bt_stride = block_table.shape
     _rows_at_least("cu_q_lens", cu_q_lens, B + 1)
-    _rows_at_least("block_table", block_table, B)
+    if rows < B:
+        _rows_at_least("block_table", block_table, B)
+    num_pages = k_pool.shape[0]
     heads = _heads(dims)
     if heads is not None:
-        _shape("q", q, (Tq, heads[0], 128))
-        _pools(k_pool, v_pool, heads[1])
-        _given(out, "out", torch.bfloat16, (Tq, heads[0], 128))
-        _given(lse, "lse", torch.float32, (Tq, heads[0]))
+        _sized("q", q, (Tq, heads[0], 128))
+        _sized("k_pool", k_pool, (num_pages, 16, heads[1], 128))
+        _sized("v_pool", v_pool, (num_pages, 16, heads[1], 128))
     if out is None:
-        out = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
-    score = _score("attn_prefill_chunk", q.shape[1], B, Tq, int(max_seq_len), softcap, alibi_slopes,
-                   window, prefix_lens, max_prefix_len, row_start)
-    ws_bytes = (prefill_workspace_size(B, max_q_len, max_seq_len, dims) if score is None
-                else prefill_score_workspace_size(B, Tq, dims))
-    if ws_bytes > 0:
-        workspace = _workspace(ws_bytes, q.device, workspace)
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _on_device("attn_prefill_chunk", q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, out,
-               lse, workspace, status)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+        po = out.data_ptr()
+    else:
+        po = _tensor(call, out, "out", torch.bfloat16, dev)
+        _sized("out", out, q.shape)
+    if lse is None:
+        if want_lse:
+            lse = _empty((Tq, hq), torch.float32, q.device, stream)
+        pl = None if lse is None else lse.data_ptr()
+    else:
+        pl = _tensor(call, lse, "lse", torch.float32, dev)
+        _sized("lse", lse, (Tq, hq))
+    max_q_len, max_seq_len = int(max_q_len), int(max_seq_len)
+    score = _score(call, dev, hq, B, Tq, max_seq_len, softcap, alibi_slopes, window, prefix_lens,
+                   max_prefix_len, row_start)
+    if workspace is None:
+        nbytes = (_workspace_size(prefill_workspace_size, B, max_q_len, max_seq_len, dims) if score is None
+                  else _workspace_size(prefill_score_workspace_size, B, Tq, dims))
+        workspace = _workspace(nbytes, q.device, None, stream)
+    else:
+        _on_device(call, workspace)
+    ps = None if status is None else _tensor(call, status, "status", torch.int32, dev)
     lib = load()
-    args = (_dims(dims), _ptr(q), _ptr(cu_q_lens), q.shape[0], _ptr(k_pool), _ptr(v_pool),
-            k_pool.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
-            int(max_q_len), int(max_seq_len), float(softmax_scale), _ptr(out), _ptr(lse),
-            _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _ptr(status), _stream(stream))
+    args = (_dims(dims), pq, pcu, Tq, pk, pv, num_pages, pbt, bt_stride, psl, B, max_q_len, max_seq_len,
+            float(softmax_scale), po, pl, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            ps, _stream(stream))
     keep, ref = _opts(max_ctas)
     if score is not None:
-        _check("attn_prefill_chunk_score", lib.attn_prefill_chunk_score(*args, ref,
-                                                                        ctypes.byref(score)))
+        _check("attn_prefill_chunk_score",
+               lib.attn_prefill_chunk_score(*args, ref, ctypes.byref(score)))
     elif ref is None:
-        _check("attn_prefill_chunk", lib.attn_prefill_chunk(*args))
+        _check(call, lib.attn_prefill_chunk(*args))
     else:
         _check("attn_prefill_chunk_ex", lib.attn_prefill_chunk_ex(*args, ref))
     del keep
@@ -495,11 +608,14 @@ StepPlan = collections.namedtuple("StepPlan",
                                   "cu_new_lens seq_lens positions slot_map free_count")
 
 
-def _new_or_given(t, name, dtype, shape, device):
+def _new_or_given(call, t, name, dtype, shape, dev, stream):
+    """(tensor, data_ptr) of an output: the caller's, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _given(t, name, dtype, shape)
-    return t
+        t = _empty(shape, dtype, dev, stream)
+        return t, t.data_ptr()
+    p = _tensor(call, t, name, dtype, dev)
+    _sized(name, t, shape)
+    return t, p
 
 
 def paged_step_plan(cached_lens, new_lens, block_table, free_pages, free_count, num_pages: int, *,
@@ -512,32 +628,32 @@ def paged_step_plan(cached_lens, new_lens, block_table, free_pages, free_count, 
     free_pages[:free_count] are free; pages are taken from its end, in request order. Requests
     that the free pages do not cover are left as they are (their rows get slot -1,
     DEV_ERR_NO_PAGES). free_count_out may be free_count, seq_lens may be cached_lens."""
-    for t, n, d in ((cached_lens, "cached_lens", 1), (new_lens, "new_lens", 1),
-                    (block_table, "block_table", 2), (free_pages, "free_pages", 1),
-                    (free_count, "free_count", 1)):
-        _need(t, n, torch.int32, d)
+    call, i32 = "paged_step_plan", torch.int32
+    dev = _device(call, cached_lens, "cached_lens", i32)
+    pc = _tensor(call, cached_lens, "cached_lens", i32, dev)
+    pn = _tensor(call, new_lens, "new_lens", i32, dev)
+    pbt = _tensor(call, block_table, "block_table", i32, dev)
+    pf = _tensor(call, free_pages, "free_pages", i32, dev)
+    pfc = _tensor(call, free_count, "free_count", i32, dev)
+    if cached_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1 or free_count.dim() != 1:
+        raise ValueError("cached_lens, free_pages and free_count must have 1 dim, block_table 2")
     B = cached_lens.shape[0]
-    _shape("new_lens", new_lens, (B,))
-    _rows_at_least("block_table", block_table, B)
+    _sized("new_lens", new_lens, (B,))
+    rows, bt_stride = block_table.shape
+    if rows < B:
+        _rows_at_least("block_table", block_table, B)
     _rows_at_least("free_count", free_count, 1)
-    dev = cached_lens.device
     total_rows = int(total_rows)
     if total_rows < 0:
         raise ValueError("total_rows must be >= 0")
-    free_count_out = _new_or_given(free_count_out, "free_count_out", torch.int32, (1,), dev)
-    cu_new_lens = _new_or_given(cu_new_lens, "cu_new_lens", torch.int32, (B + 1,), dev)
-    seq_lens = _new_or_given(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    positions = _new_or_given(positions, "positions", torch.int32, (total_rows,), dev)
-    slot_map = _new_or_given(slot_map, "slot_map", torch.int64, (total_rows,), dev)
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _on_device("paged_step_plan", cached_lens, new_lens, block_table, free_pages, free_count,
-               free_count_out, cu_new_lens, seq_lens, positions, slot_map, status)
-    _check("paged_step_plan", load().paged_step_plan(
-        _ptr(cached_lens), _ptr(new_lens), B, _ptr(block_table), block_table.shape[1],
-        _ptr(free_pages), free_pages.shape[0], _ptr(free_count), int(num_pages), total_rows,
-        _ptr(free_count_out), _ptr(cu_new_lens), _ptr(seq_lens), _ptr(positions), _ptr(slot_map),
-        _ptr(status), _stream(stream)))
+    free_count_out, pfo = _new_or_given(call, free_count_out, "free_count_out", i32, (1,), dev, stream)
+    cu_new_lens, pcu = _new_or_given(call, cu_new_lens, "cu_new_lens", i32, (B + 1,), dev, stream)
+    seq_lens, psl = _new_or_given(call, seq_lens, "seq_lens", i32, (B,), dev, stream)
+    positions, pp = _new_or_given(call, positions, "positions", i32, (total_rows,), dev, stream)
+    slot_map, psm = _new_or_given(call, slot_map, "slot_map", torch.int64, (total_rows,), dev, stream)
+    ps = None if status is None else _tensor(call, status, "status", i32, dev)
+    _check(call, load().paged_step_plan(pc, pn, B, pbt, bt_stride, pf, free_pages.shape[0], pfc, int(num_pages),
+                                        total_rows, pfo, pcu, psl, pp, psm, ps, _stream(stream)))
     return StepPlan(cu_new_lens, seq_lens, positions, slot_map, free_count_out)
 
 
@@ -546,24 +662,25 @@ def paged_release(begin_pages, end_pages, block_table, free_pages, free_count, n
     """Append the pages of each request's logical range [begin_pages[b], end_pages[b]) to
     free_pages and set their block_table entries to -1 (entries that are -1 are skipped).
     Returns the new free count [1] (free_count_out, which may be free_count)."""
-    for t, n, d in ((begin_pages, "begin_pages", 1), (end_pages, "end_pages", 1),
-                    (block_table, "block_table", 2), (free_pages, "free_pages", 1),
-                    (free_count, "free_count", 1)):
-        _need(t, n, torch.int32, d)
+    call, i32 = "paged_release", torch.int32
+    dev = _device(call, begin_pages, "begin_pages", i32)
+    pb = _tensor(call, begin_pages, "begin_pages", i32, dev)
+    pe = _tensor(call, end_pages, "end_pages", i32, dev)
+    pbt = _tensor(call, block_table, "block_table", i32, dev)
+    pf = _tensor(call, free_pages, "free_pages", i32, dev)
+    pfc = _tensor(call, free_count, "free_count", i32, dev)
+    if begin_pages.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1 or free_count.dim() != 1:
+        raise ValueError("begin_pages, free_pages and free_count must have 1 dim, block_table 2")
     B = begin_pages.shape[0]
-    _shape("end_pages", end_pages, (B,))
-    _rows_at_least("block_table", block_table, B)
+    _sized("end_pages", end_pages, (B,))
+    rows, bt_stride = block_table.shape
+    if rows < B:
+        _rows_at_least("block_table", block_table, B)
     _rows_at_least("free_count", free_count, 1)
-    free_count_out = _new_or_given(free_count_out, "free_count_out", torch.int32, (1,),
-                                   begin_pages.device)
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _on_device("paged_release", begin_pages, end_pages, block_table, free_pages, free_count,
-               free_count_out, status)
-    _check("paged_release", load().paged_release(
-        _ptr(begin_pages), _ptr(end_pages), B, _ptr(block_table), block_table.shape[1],
-        _ptr(free_pages), free_pages.shape[0], _ptr(free_count), int(num_pages),
-        _ptr(free_count_out), _ptr(status), _stream(stream)))
+    free_count_out, pfo = _new_or_given(call, free_count_out, "free_count_out", i32, (1,), dev, stream)
+    ps = None if status is None else _tensor(call, status, "status", i32, dev)
+    _check(call, load().paged_release(pb, pe, B, pbt, bt_stride, pf, free_pages.shape[0], pfc, int(num_pages), pfo,
+                                      ps, _stream(stream)))
     return free_count_out
 
 
@@ -593,23 +710,20 @@ def rope_inv_freq(rot_dim: int = 128, theta: float = 1e6, *, scaling: str = "non
     return freq, float(a.value)
 
 
-def _rows_strided(t, name, heads):
-    """A [T, heads, 128] bf16 tensor whose rows may lie apart; returns their stride."""
+def _rows_strided(call, t, name, dev, T, heads):
+    """(data_ptr, row stride) of a [T, heads, 128] bf16 tensor whose rows may lie apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
-    T, h, d = t.shape
-    if heads is not None and (h, d) != (heads, 128):
-        raise ValueError(f"{name} must have shape ('*', {heads}, 128), got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        _on_device(call, t)
+    if t.shape != (T, heads, 128):
+        raise ValueError(f"{name} must have shape {(T, heads, 128)}, got {tuple(t.shape)}")
     row, head, dim = t.stride()
-    if (dim != 1 and d > 1) or (head != d and h > 1):
+    if dim != 1 or (head != 128 and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return row if T > 1 else h * d
+    return t.data_ptr(), row if T > 1 else heads * 128
 
 
 def rope_append_paged(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq, *,
@@ -620,39 +734,39 @@ def rope_append_paged(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_
     their positions, write k and v into the pools at slot_map (negative: padding row, left
     alone). Returns q_out [T, Hq, 128]. rot_dim is 2 * len(inv_freq); rows of q, k_new and v_new
     may be strided (slices of one projection)."""
-    heads = _heads(dims)
-    qs = _rows_strided(q, "q", None if heads is None else heads[0])
-    ks = _rows_strided(k_new, "k_new", None if heads is None else heads[1])
-    vs = _rows_strided(v_new, "v_new", None if heads is None else heads[1])
-    T = q.shape[0]
-    _need(positions, "positions", torch.int32, 1)
-    _need(slot_map, "slot_map", torch.int64, 1)
-    _need(inv_freq, "inv_freq", torch.float64, 1)
-    for t, n in ((k_new, "k_new"), (v_new, "v_new"), (positions, "positions"),
-                 (slot_map, "slot_map")):
-        if t.shape[0] != T:
-            raise ValueError(f"{n} must have {T} rows, got {t.shape[0]}")
-    _need(k_pool, "k_pool", torch.bfloat16, 4)
-    _need(v_pool, "v_pool", torch.bfloat16, 4)
-    if heads is not None:
-        _pools(k_pool, v_pool, heads[1])
-    for t, n in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
-        if t is not None:
-            _need(t, n, torch.float32, 1)
-            _shape(n, t, (128,))
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _given(q_out, "q_out", torch.bfloat16, tuple(q.shape))
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _on_device("rope_append_paged", q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq,
-               q_gamma, k_gamma, q_out, status)
-    _check("rope_append_paged", load().rope_append_paged(
-        _dims(dims), 2 * inv_freq.shape[0], 1 if interleaved else 0, _ptr(inv_freq),
-        float(attn_factor), _ptr(q), qs, _ptr(k_new), ks, _ptr(v_new), vs, T, _ptr(positions),
-        _ptr(slot_map), _ptr(q_gamma), _ptr(k_gamma), float(eps), _ptr(q_out), _ptr(k_pool),
-        _ptr(v_pool), k_pool.shape[0], _ptr(status), _stream(stream)))
+    call = "rope_append_paged"
+    dev = _device(call, q, "q", torch.bfloat16)
+    hq, hkv = _heads(dims) or tuple(dims[:2])  # (other shapes: the library rejects them)
+    T = q.shape[0] if q.dim() else 0
+    pq, qs = _rows_strided(call, q, "q", dev, T, hq)
+    pk, ks = _rows_strided(call, k_new, "k_new", dev, T, hkv)
+    pv, vs = _rows_strided(call, v_new, "v_new", dev, T, hkv)
+    pp = _tensor(call, positions, "positions", torch.int32, dev)
+    psm = _tensor(call, slot_map, "slot_map", torch.int64, dev)
+    pif = _tensor(call, inv_freq, "inv_freq", torch.float64, dev)
+    _sized("positions", positions, (T,))
+    _sized("slot_map", slot_map, (T,))
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq must have 1 dim, got {inv_freq.dim()}")
+    pkp = _tensor(call, k_pool, "k_pool", torch.bfloat16, dev)
+    pvp = _tensor(call, v_pool, "v_pool", torch.bfloat16, dev)
+    if k_pool.dim() != 4:
+        raise ValueError(f"k_pool must have 4 dims, got {k_pool.dim()}")
+    num_pages = k_pool.shape[0]
+    _sized("k_pool", k_pool, (num_pages, 16, hkv, 128))
+    _sized("v_pool", v_pool, (num_pages, 16, hkv, 128))
+    pqg = pkg = None
+    if q_gamma is not None:
+        pqg = _tensor(call, q_gamma, "q_gamma", torch.float32, dev)
+        _sized("q_gamma", q_gamma, (128,))
+    if k_gamma is not None:
+        pkg = _tensor(call, k_gamma, "k_gamma", torch.float32, dev)
+        _sized("k_gamma", k_gamma, (128,))
+    q_out, pqo = _new_or_given(call, q_out, "q_out", torch.bfloat16, (T, hq, 128), dev, stream)
+    ps = None if status is None else _tensor(call, status, "status", torch.int32, dev)
+    _check(call, load().rope_append_paged(
+        _dims(dims), 2 * inv_freq.shape[0], 1 if interleaved else 0, pif, float(attn_factor), pq, qs, pk, ks, pv,
+        vs, T, pp, psm, pqg, pkg, float(eps), pqo, pkp, pvp, num_pages, ps, _stream(stream)))
     return q_out
 
 
