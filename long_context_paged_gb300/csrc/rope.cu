@@ -6,7 +6,8 @@
 // the pair being dims (i, i + rot / 2) or, interleaved, (2i, 2i + 1); before it, q and k rows may
 // be RMS-normalised per head: x / sqrt(mean x^2 + eps) * gamma. One pass in fp32, one rounding
 // to bf16 at the end. The bound is memory: every q, k and v row is read once and written once
-// (16 KB per token of the 16/8-head decoder), against ~70 operations per 16 bytes.
+// (16 KB per token of the 16/8-head decoder). Measured: 4,127 rows with norms 18.3 us (3.7 TB/s; a
+// copy of the same 67.6 MB takes 14.6 us at that size).
 //
 // The angle. At position 100,000 an fp32 product position * inv_freq is off by up to 0.004 rad,
 // more than a bf16 rounding. Here a frequency is held in turns as a 64-bit binary fraction
@@ -14,13 +15,14 @@
 // fraction of a turn of that frequency for every int32 position, one integer multiply; its upper
 // half, as fp32, goes to sincospif.
 //
-// Layout. A unit is one token's KV head: its two q rows, its k row and its v row, 256 bytes each.
-// Half a warp takes a unit, 16 bytes (8 dims) of each row per lane, all four loads in flight
-// before anything else; 16 units per CTA pass. The cosines and sines of the pass's tokens are
-// computed once by the CTA and shared through shared memory (with one sincospif per lane and pair
-// the 8 heads of a token would compute them 8 times), while the row loads are in flight. The
-// partner of a dim in the half layout is rot / 16 lanes away: the raw words are exchanged by four
-// shuffles per row, before the norm, whose factor is common to the row.
+// Layout. A unit is one token's KV head: its two q rows, its k row and its v row, 256 bytes each. A
+// warp takes two units a pass (two heads of one token, unless the call has one KV head), 8 bytes
+// (4 dims) of each row per lane, all eight loads in flight before anything else; 16 units per CTA
+// pass. The cosines and sines of the pass's tokens are computed once by the CTA and shared through
+// shared memory (with one sincospif per lane and pair the 8 heads of a token would compute them 8
+// times), while the row loads are in flight; a lane multiplies them by gamma once for the rows that
+// share both. The partner of a dim in the half layout is rot / 8 lanes away: the raw words are
+// exchanged by two shuffles per row, before the norm, whose factor is common to the row.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -33,10 +35,12 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = kThreads / 16;       // units of a CTA pass
+constexpr int kUnits = kThreads / 16;       // units of a CTA pass: two a warp
 constexpr int kMaxPairs = kHeadDim / 2;
-// CTAs per SM of a long call: enough row loads in flight to cover the latency (8 x 16 KB per SM)
-constexpr int kCtasPerSm = 8;
+constexpr int kTableTokens = 32;            // tokens whose cosines and sines are held at a time
+// Two CTAs per SM at 110 registers: a pass in flight and one ahead of it for every warp. Three or four
+// CTAs of 80 or 64 registers spill and measured slower (20.5 and 24.4 against 18.3 us for 4,127 rows).
+constexpr int kCtasPerSm = 2;
 
 struct RopeParams {
   int32_t hkv_shift;  // log2 of the KV heads
@@ -60,159 +64,221 @@ struct RopeParams {
   int32_t* status;
 };
 
-__device__ __forceinline__ uint4 load_row16(const uint16_t* p) {
-  return __ldcs(reinterpret_cast<const uint4*>(p));  // read once: do not keep it in L1
+__device__ __forceinline__ uint2 load_row8(const uint16_t* p) {
+  return __ldcs(reinterpret_cast<const uint2*>(p));  // read once: do not keep it in L1
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
-  x[4] = bf16lo(w.z); x[5] = bf16hi(w.z); x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
+// The fraction of a turn in f radians, as a 64-bit binary fraction: f = m 2^e with an integer m, so
+// frac(f / 2 pi) 2^64 is the low 64 bits of m C 2^e with C = 2^64 / (2 pi). Integer arithmetic: fp64
+// instructions run at 1/64 of the fp32 rate here, and a CTA's 64 conversions in fp64 took longer
+// than its rows (24 us for 4,127 rows).
+__device__ __forceinline__ unsigned long long turn_fraction(double f) {
+  constexpr unsigned long long kTurns = 0x28be60db9391054aull;  // 2^64 / (2 pi)
+  const long long bits = __double_as_longlong(f);
+  const int field = static_cast<int>(bits >> 52) & 0x7ff;
+  if (field == 0) return 0;  // zero (or subnormal: no turn at any int32 position)
+  const unsigned long long m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+  const int e = field - 1075;
+  const unsigned long long lo = m * kTurns, hi = __umul64hi(m, kTurns);
+  unsigned long long r = 0;
+  if (e >= 0) r = e < 64 ? lo << e : 0;
+  else if (e > -64) r = (hi << (64 + e)) | (lo >> -e);
+  else if (e > -128) r = hi >> (-e - 64);
+  return bits < 0 ? 0 - r : r;
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+// The factors of a lane's 4 dims: a row x with partner values y turns into
+//     inv * (x own + y other),   own = gamma cos, other = -+ gamma(partner) sin,
+// inv being the row's norm (1 without one). Lanes past rot: own = gamma, other = 0.
+struct Factors {
+  float2 own[2], other[2];
+};
 
-// Norm (gamma != null) and rotation of one 128-dim row held 8 dims a lane by half a warp.
-// kInterleaved: the pairs are inside a lane; else the partner dims are in lane `partner`, and
-// sign is -1 for the first dims of the pairs, +1 for the second, 0 for lanes past rot.
 template <bool kInterleaved>
-__device__ __forceinline__ uint4 turn_row(uint4 raw, const float* gamma, float eps, int c, int partner,
-                                          float sign, const float (&cs)[8], const float (&sn)[8]) {
-  float x[8];
-  unpack8(raw, x);
-  float inv = 1.f;
+__device__ __forceinline__ Factors factors(const float* gamma, int lane, int partner, float sign,
+                                           const float2 (&cs)[2], const float2 (&sn)[2]) {
+  Factors f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f.own[i] = cs[i];
+    f.other[i] = kInterleaved ? make_float2(-sn[i].x, sn[i].y) : mul2(sn[i], make_float2(sign, sign));
+  }
   if (gamma != nullptr) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    inv = 1.0f / sqrtf(sum * (1.0f / kHeadDim) + eps);
-    float g[8];
-    load8(gamma + 8 * c, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= inv * g[i];
-  }
-  float r[8];
-  if (kInterleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {  // sign = 0: dims past rot keep their value
-      r[i] = sign != 0.f ? x[i] * cs[i / 2] - x[i + 1] * sn[i / 2] : x[i];
-      r[i + 1] = sign != 0.f ? x[i + 1] * cs[i / 2] + x[i] * sn[i / 2] : x[i + 1];
+    const float4 g = *reinterpret_cast<const float4*>(gamma + 4 * lane);
+    f.own[0] = mul2(f.own[0], make_float2(g.x, g.y));
+    f.own[1] = mul2(f.own[1], make_float2(g.z, g.w));
+    if (kInterleaved) {
+      f.other[0] = mul2(f.other[0], make_float2(g.y, g.x));
+      f.other[1] = mul2(f.other[1], make_float2(g.w, g.z));
+    } else {
+      const float4 h = *reinterpret_cast<const float4*>(gamma + 4 * partner);
+      f.other[0] = mul2(f.other[0], make_float2(h.x, h.y));
+      f.other[1] = mul2(f.other[1], make_float2(h.z, h.w));
     }
-  } else {
-    uint4 other;
-    other.x = __shfl_sync(0xffffffffu, raw.x, partner);
-    other.y = __shfl_sync(0xffffffffu, raw.y, partner);
-    other.z = __shfl_sync(0xffffffffu, raw.z, partner);
-    other.w = __shfl_sync(0xffffffffu, raw.w, partner);
-    float y[8];
-    unpack8(other, y);
-    if (gamma != nullptr) {
-      float g[8];
-      load8(gamma + 8 * (partner & 15), g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= inv * g[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = sign != 0.f ? x[i] * cs[i] + sign * y[i] * sn[i] : x[i];
   }
-  return make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]),
-                    pack_bf16x2(r[6], r[7]));
+  return f;
 }
 
+// Sum of a lane's 4 squares.
+__device__ __forceinline__ float squares(uint2 raw) {
+  const float2 x0 = make_float2(bf16lo(raw.x), bf16hi(raw.x)), x1 = make_float2(bf16lo(raw.y), bf16hi(raw.y));
+  const float2 sq = fma2(x1, x1, mul2(x0, x0));
+  return sq.x + sq.y;
+}
+
+// Rotation of one 128-dim row held 4 dims a lane by a warp; inv: its norm's factor.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p) {
-  __shared__ unsigned long long turn[kMaxPairs];
-  // cosines and sines (times attn_factor) of a pass's tokens (at most one per unit), two buffers:
-  // one barrier per pass
-  __shared__ __align__(16) float cos_s[2][kUnits][kMaxPairs], sin_s[2][kUnits][kMaxPairs];
-  const int tid = threadIdx.x, lane = tid & 31, c = lane & 15, u = tid >> 4;
-  const int pairs = p.rot >> 1;
-  if (tid < pairs) {
-    double t = p.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
-    t -= floor(t);
-    turn[tid] = static_cast<unsigned long long>(t * 18446744073709551616.0);  // 2^64
+__device__ __forceinline__ uint2 turn_row(uint2 raw, float inv, int partner, float sign, const Factors& f) {
+  const float2 x0 = make_float2(bf16lo(raw.x), bf16hi(raw.x)), x1 = make_float2(bf16lo(raw.y), bf16hi(raw.y));
+  float2 y0, y1;
+  if (kInterleaved) {  // the partner is the pair's other dim
+    y0 = make_float2(x0.y, x0.x);
+    y1 = make_float2(x1.y, x1.x);
+  } else {             // the partner is rot / 8 lanes away: exchange the raw words
+    const uint32_t a = __shfl_sync(0xffffffffu, raw.x, partner), b = __shfl_sync(0xffffffffu, raw.y, partner);
+    y0 = make_float2(bf16lo(a), bf16hi(a));
+    y1 = make_float2(bf16lo(b), bf16hi(b));
   }
-  // half layout: lanes [0, rot/16) hold the pairs' first dims, the next rot/16 the second
-  const int span = p.rot >> 4;
+  if (sign == 0.f) y0 = y1 = make_float2(0.f, 0.f);  // past rot: not even 0 times an infinite partner
+  const float2 inv2 = make_float2(inv, inv);
+  const float2 r0 = mul2(fma2(y0, f.other[0], mul2(x0, f.own[0])), inv2);
+  const float2 r1 = mul2(fma2(y1, f.other[1], mul2(x1, f.own[1])), inv2);
+  return make_uint2(pack_bf16x2(r0.x, r0.y), pack_bf16x2(r1.x, r1.y));
+}
+
+// The rows of one warp's two units of a pass, as loaded.
+struct UnitRows {
+  uint2 q0[2], q1[2], k[2], v[2];
+  int64_t slot[2];
+};
+
+__device__ __forceinline__ void load_units(const RopeParams& p, int64_t unit0, int lane, UnitRows& r) {
+  const int hkv = 1 << p.hkv_shift;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t unit = unit0 + i, t = unit >> p.hkv_shift;
+    const int g = static_cast<int>(unit) & (hkv - 1);
+    r.q0[i] = r.q1[i] = r.k[i] = r.v[i] = make_uint2(0u, 0u);
+    r.slot[i] = -1;
+    if (unit < p.units) {
+      const uint16_t* qr = p.q + t * p.q_stride + 2 * g * kHeadDim + 4 * lane;
+      r.q0[i] = load_row8(qr);
+      r.q1[i] = load_row8(qr + kHeadDim);
+      r.k[i] = load_row8(p.k + t * p.k_stride + g * kHeadDim + 4 * lane);
+      r.v[i] = load_row8(p.v + t * p.v_stride + g * kHeadDim + 4 * lane);
+      r.slot[i] = p.slots[t];
+    }
+  }
+}
+
+// CTA b takes passes b * passes_per_cta .. of kUnits units each: consecutive tokens. Their cosines
+// and sines are computed kTableTokens tokens at a time; between two such chunks no barrier holds a
+// warp up, and each warp loads the rows of its next pass before it works on this one's.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_append_kernel(const RopeParams p, int passes_per_cta) {
+  __shared__ __align__(16) float cos_s[kTableTokens][kMaxPairs], sin_s[kTableTokens][kMaxPairs];
+  const int tid = threadIdx.x, lane = tid & 31, u = (tid >> 5) * 2;
+  const int pairs = p.rot >> 1;
+  // half layout: lanes [0, rot / 8) hold the pairs' first dims, the next rot / 8 the second
+  const int span = p.rot >> 3;
   float sign = 0.f;
   int partner = lane;
   if (kInterleaved) {
-    sign = 8 * c < p.rot ? 1.f : 0.f;
-  } else if (c < span) {
+    sign = 4 * lane < p.rot ? 1.f : 0.f;
+  } else if (lane < span) {
     sign = -1.f;
     partner = lane + span;
-  } else if (c < 2 * span) {
+  } else if (lane < 2 * span) {
     sign = 1.f;
     partner = lane - span;
   }
   const int hkv = 1 << p.hkv_shift;
-  const int tokens = max(1, kUnits >> p.hkv_shift);  // tokens of a pass (16 / hkv: hkv <= 8)
-  __syncthreads();
-  int buf = 0;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kUnits; first < p.units;
-       first += static_cast<int64_t>(gridDim.x) * kUnits, buf ^= 1) {
-    const int64_t unit = first + u;
-    const bool live = unit < p.units;
-    const int64_t t = unit >> p.hkv_shift;
-    const int g = static_cast<int>(unit) & (hkv - 1);
-    uint4 q0 = {}, q1 = {}, k0 = {}, v0 = {};
-    int64_t slot = -1;
-    if (live) {
-      const uint16_t* qr = p.q + t * p.q_stride + 2 * g * kHeadDim + 8 * c;
-      q0 = load_row16(qr);
-      q1 = load_row16(qr + kHeadDim);
-      k0 = load_row16(p.k + t * p.k_stride + g * kHeadDim + 8 * c);
-      v0 = load_row16(p.v + t * p.v_stride + g * kHeadDim + 8 * c);
-      slot = p.slots[t];
-    }
-    // the pass's first token is a whole one: kUnits is a multiple of the KV heads
-    for (int i = tid; i < tokens * kMaxPairs; i += kThreads) {
-      const int64_t tt = (first >> p.hkv_shift) + (i >> 6);
-      const int j = i & (kMaxPairs - 1);
-      if (j < pairs && (tt << p.hkv_shift) < p.units) {
-        const long long pos = p.positions[tt];
-        const unsigned long long phase = static_cast<unsigned long long>(pos) * turn[j];
-        // the signed upper half: [-1/2, 1/2) turns, in half turns for sincospif
-        const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * (1.0f / 2147483648.0f);
-        float sn, cs;
-        sincospif(half_turns, &sn, &cs);
-        cos_s[buf][i >> 6][j] = cs * p.attn_factor;
-        sin_s[buf][i >> 6][j] = sn * p.attn_factor;
+  const int tokens = kUnits >> p.hkv_shift;           // tokens of a pass: whole ones (hkv <= 8)
+  const int chunk = kTableTokens / tokens;            // passes of a table
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * passes_per_cta * kUnits;
+  UnitRows rows;
+  load_units(p, first + u, lane, rows);
+  for (int pass = 0; pass < passes_per_cta; ++pass) {
+    const int64_t unit0 = first + static_cast<int64_t>(pass) * kUnits;
+    if (unit0 >= p.units) break;
+    if (pass % chunk == 0) {
+      if (pass > 0) __syncthreads();  // the table before has been read
+      const int n = min(chunk, passes_per_cta - pass) * tokens;
+      for (int i = tid; i < n * kMaxPairs; i += kThreads) {
+        const int64_t t = (unit0 >> p.hkv_shift) + (i >> 6);
+        const int j = i & (kMaxPairs - 1);
+        if (j < pairs && (t << p.hkv_shift) < p.units) {
+          const long long pos = p.positions[t];
+          const unsigned long long phase = static_cast<unsigned long long>(pos) * turn_fraction(p.inv_freq[j]);
+          // the signed upper half: [-1/2, 1/2) turns, in half turns for sincospif
+          const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * (1.0f / 2147483648.0f);
+          float sn, cs;
+          sincospif(half_turns, &sn, &cs);
+          cos_s[i >> 6][j] = cs * p.attn_factor;
+          sin_s[i >> 6][j] = sn * p.attn_factor;
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
-    // (the other buffer is rewritten only after every thread has passed this barrier)
-    float cs[8], sn[8];
-    const int row = u >> p.hkv_shift;
-    if (kInterleaved) {
-      const int at = 8 * c < p.rot ? 4 * c : 0;
-      const float4 a = *reinterpret_cast<const float4*>(&cos_s[buf][row][at]);
-      const float4 b = *reinterpret_cast<const float4*>(&sin_s[buf][row][at]);
-      cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
-      sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
-    } else {
-      const int at = c < span ? 8 * c : (c < 2 * span ? 8 * (c - span) : 0);
-      load8(&cos_s[buf][row][at], cs);
-      load8(&sin_s[buf][row][at], sn);
+    const UnitRows cur = rows;
+    if (pass + 1 < passes_per_cta) load_units(p, unit0 + kUnits + u, lane, rows);
+    // the norms of the warp's six rows together: six independent sums a reduction step
+    float inv[6] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (p.q_gamma != nullptr || p.k_gamma != nullptr) {
+      float sum[6] = {squares(cur.q0[0]), squares(cur.q1[0]), squares(cur.k[0]),
+                      squares(cur.q0[1]), squares(cur.q1[1]), squares(cur.k[1])};
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+      }
+#pragma unroll
+      for (int i = 0; i < 6; ++i)
+        if ((i % 3 < 2 ? p.q_gamma : p.k_gamma) != nullptr) inv[i] = rsqrtf(sum[i] * (1.0f / kHeadDim) + p.eps);
     }
-    const uint4 q0r = turn_row<kInterleaved>(q0, p.q_gamma, p.eps, c, partner, sign, cs, sn);
-    const uint4 q1r = turn_row<kInterleaved>(q1, p.q_gamma, p.eps, c, partner, sign, cs, sn);
-    const uint4 k0r = turn_row<kInterleaved>(k0, p.k_gamma, p.eps, c, partner, sign, cs, sn);
-    if (slot >= p.num_slots) {
-      if (c == 0) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
-      slot = -1;
-    }
-    if (slot >= 0) {  // a negative slot: a padding row, nothing is written
-      uint16_t* qo = p.q_out + (t * (2 * hkv) + 2 * g) * kHeadDim + 8 * c;
-      *reinterpret_cast<uint4*>(qo) = q0r;
-      *reinterpret_cast<uint4*>(qo + kHeadDim) = q1r;
-      const int64_t at = (slot * hkv + g) * kHeadDim + 8 * c;
-      *reinterpret_cast<uint4*>(p.k_pool + at) = k0r;
-      *reinterpret_cast<uint4*>(p.v_pool + at) = v0;
+    Factors fq, fk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i == 0 || hkv == 1) {  // the second unit is another head of the same token
+        float2 cs[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+        float2 sn[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const int row = (pass % chunk) * tokens + ((u + i) >> p.hkv_shift);
+        if (sign != 0.f) {
+          if (kInterleaved) {  // one angle a pair
+            const float2 a = *reinterpret_cast<const float2*>(&cos_s[row][2 * lane]);
+            const float2 b = *reinterpret_cast<const float2*>(&sin_s[row][2 * lane]);
+            cs[0] = make_float2(a.x, a.x);
+            cs[1] = make_float2(a.y, a.y);
+            sn[0] = make_float2(b.x, b.x);
+            sn[1] = make_float2(b.y, b.y);
+          } else {
+            const int at = 4 * (lane < span ? lane : lane - span);
+            const float4 a = *reinterpret_cast<const float4*>(&cos_s[row][at]);
+            const float4 b = *reinterpret_cast<const float4*>(&sin_s[row][at]);
+            cs[0] = make_float2(a.x, a.y);
+            cs[1] = make_float2(a.z, a.w);
+            sn[0] = make_float2(b.x, b.y);
+            sn[1] = make_float2(b.z, b.w);
+          }
+        }
+        fq = factors<kInterleaved>(p.q_gamma, lane, partner, sign, cs, sn);
+        fk = factors<kInterleaved>(p.k_gamma, lane, partner, sign, cs, sn);
+      }
+      const uint2 q0r = turn_row<kInterleaved>(cur.q0[i], inv[3 * i], partner, sign, fq);
+      const uint2 q1r = turn_row<kInterleaved>(cur.q1[i], inv[3 * i + 1], partner, sign, fq);
+      const uint2 k0r = turn_row<kInterleaved>(cur.k[i], inv[3 * i + 2], partner, sign, fk);
+      const int64_t slot = cur.slot[i];  // negative: a padding row, nothing is written
+      if (slot >= p.num_slots && lane == 0) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
+      if (slot >= 0 && slot < p.num_slots) {
+        const int64_t unit = unit0 + u + i, t = unit >> p.hkv_shift;
+        const int g = static_cast<int>(unit) & (hkv - 1);
+        uint16_t* qo = p.q_out + (t * (2 * hkv) + 2 * g) * kHeadDim + 4 * lane;
+        *reinterpret_cast<uint2*>(qo) = q0r;
+        *reinterpret_cast<uint2*>(qo + kHeadDim) = q1r;
+        const int64_t at = (slot * hkv + g) * kHeadDim + 4 * lane;
+        *reinterpret_cast<uint2*>(p.k_pool + at) = k0r;
+        *reinterpret_cast<uint2*>(p.v_pool + at) = cur.v[i];
+      }
     }
   }
 }
@@ -276,10 +342,13 @@ extern "C" pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t in
   p.num_slots = num_pages * kPage;
   p.status = status;
   const int64_t passes = (p.units + kUnits - 1) / kUnits;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(passes, static_cast<int64_t>(sms) * kCtasPerSm));
+  // as many CTAs as are resident, each with the same number of passes
+  const int64_t most = static_cast<int64_t>(sms) * kCtasPerSm;
+  const int per_cta = static_cast<int>((passes + most - 1) / most);
+  const unsigned grid = static_cast<unsigned>((passes + per_cta - 1) / per_cta);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (interleaved) rope_append_kernel<true><<<grid, kThreads, 0, st>>>(p);
-  else rope_append_kernel<false><<<grid, kThreads, 0, st>>>(p);
+  if (interleaved) rope_append_kernel<true><<<grid, kThreads, 0, st>>>(p, per_cta);
+  else rope_append_kernel<false><<<grid, kThreads, 0, st>>>(p, per_cta);
   PA_CHECK_LAUNCH("rope_append_kernel");
   return PA_OK;
 }

@@ -50,6 +50,7 @@ struct PlanParams {
   int32_t* positions;
   int64_t* slots;
   int32_t* status;
+  bool vector_rows;  // positions and slots are 16-byte aligned
 };
 
 struct PlanSmem {
@@ -187,23 +188,52 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
   }
   // ---- per row: position and slot; rows of requests that wait, and rows past the last request,
   //      are (0, -1)
-  for (int t = id; t < p.total_rows; t += all) {
-    int pos = 0;
-    int64_t slot = -1;
-    if (t < total) {
-      const int b = last_at_most(s.cu, p.batch, t);
-      const int cb = s.cached[b];
-      if (cb >= 0) {
-        pos = cb + t - s.cu[b];
-        const int lp = pos / kPage, held = pages_of(cb);
-        const int page = lp < held ? p.block_table[static_cast<int64_t>(b) * p.bt_stride + lp]
-                                   : p.free_pages[free_count - 1 - (s.need[b] + lp - held)];
-        if (page < 0 || page >= p.num_pages) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
-        else slot = static_cast<int64_t>(page) * kPage + pos % kPage;
+  //      are (0, -1). Four consecutive rows a thread: one search (the next rows are mostly the same
+  //      request's or the next one's), four page loads in flight, 16-byte stores.
+  for (int64_t t0 = 4ll * id; t0 < p.total_rows; t0 += 4ll * all) {
+    int pos[4], page[4];
+    const int32_t* entry[4];
+    int b = t0 < total ? last_at_most(s.cu, p.batch, static_cast<int>(t0)) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t t = t0 + k;
+      pos[k] = 0;
+      entry[k] = nullptr;
+      if (t < total) {
+        if (t >= s.cu[b + 1]) {
+          ++b;
+          if (t >= s.cu[b + 1]) b = last_at_most(s.cu, p.batch, static_cast<int>(t));
+        }
+        const int cb = s.cached[b];
+        if (cb >= 0) {
+          pos[k] = cb + static_cast<int>(t) - s.cu[b];
+          const int lp = pos[k] / kPage, held = pages_of(cb);
+          entry[k] = lp < held ? p.block_table + static_cast<int64_t>(b) * p.bt_stride + lp
+                               : p.free_pages + (free_count - 1 - (s.need[b] + lp - held));
+        }
       }
     }
-    p.positions[t] = pos;
-    p.slots[t] = slot;
+    int64_t slot[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = entry[k] != nullptr ? *entry[k] : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      slot[k] = -1;
+      if (entry[k] != nullptr) {
+        if (page[k] < 0 || page[k] >= p.num_pages) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
+        else slot[k] = static_cast<int64_t>(page[k]) * kPage + pos[k] % kPage;
+      }
+    }
+    if (p.vector_rows && t0 + 4 <= p.total_rows) {
+      *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      reinterpret_cast<longlong2*>(p.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
+      reinterpret_cast<longlong2*>(p.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+      for (int k = 0; k < 4 && t0 + k < p.total_rows; ++k) {
+        p.positions[t0 + k] = pos[k];
+        p.slots[t0 + k] = slot[k];
+      }
+    }
   }
 }
 
@@ -383,7 +413,8 @@ extern "C" pa_status paged_step_plan(const int32_t* cached_lens, const int32_t* 
     configured_device = dev;
   }
   PlanParams p{cached_lens, new_lens, batch, block_table, bt_stride, free_pages, free_capacity, free_count,
-               num_pages, total_rows, free_count_out, cu_new_lens, seq_lens, positions, slot_map, status};
+               num_pages, total_rows, free_count_out, cu_new_lens, seq_lens, positions, slot_map, status,
+               ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slot_map)) & 15u) == 0};
   return launch_cluster(step_plan_kernel, p, cluster_of(std::max(total_rows, batch), kRowsPerCta),
                         sizeof(PlanSmem), reinterpret_cast<cudaStream_t>(stream), "step_plan_kernel");
 }
