@@ -23,7 +23,7 @@ pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, cons
                                const void* k_pool, const void* v_pool, int64_t num_pages,
                                const int32_t* block_table, int32_t bt_stride,
                                const int32_t* seq_lens, int32_t batch, int32_t max_q_len,
-                               float softmax_scale, void* out, float* lse, void* workspace,
+                               int32_t max_seq_len, float softmax_scale, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, int32_t* status, cudaStream_t stream,
                                int32_t max_ctas, const pa_score_opts& score);
 size_t prefill_workspace_bytes(int batch);
@@ -51,8 +51,8 @@ pa_status prefill_call(pa_dims dims, const void* q, const int32_t* cu_q_lens, in
     return PA_ERR_INVALID_ARG;
   if (score != nullptr)
     return launch_prefill_score(dims.num_kv_heads, q, total_q, cu_q_lens, k_pool, v_pool, num_pages,
-                                block_table, bt_stride, seq_lens, batch, max_q_len, softmax_scale, out,
-                                lse, workspace, workspace_bytes, status,
+                                block_table, bt_stride, seq_lens, batch, max_q_len, max_seq_len,
+                                softmax_scale, out, lse, workspace, workspace_bytes, status,
                                 reinterpret_cast<cudaStream_t>(stream), max_ctas, *score);
   return launch_prefill_tc(dims.num_kv_heads, q, total_q, cu_q_lens, k_pool, v_pool, num_pages,
                            block_table, bt_stride, seq_lens, batch, max_q_len, softmax_scale, out,

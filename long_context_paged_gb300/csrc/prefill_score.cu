@@ -61,6 +61,10 @@ constexpr int kMaxBatch = 128;
 constexpr int kVStages = 3;   // V is needed a whole P*V later than K: one more stage in flight
 // Fixed cost of a job beyond its key tiles, in tiles (its epilogue and the restart of its chain)
 constexpr int kJobCost = 3;
+// Up to this many keys a call whose jobs fit one to a CTA is not split. One CTA a job is faster while a
+// job has few tiles (375 queries at 0: 18.9 us, split and merged 27.4; 300 at 700: 26.3, split 29.9) and
+// slower beyond (300 at 1,700: 36.3, split 32.4).
+constexpr int kWholeKeys = 1024;
 // A partial result: o [2 heads][32 float4 columns][128 rows], then lse [2][128] fp32.
 constexpr size_t kRecordO = 2 * 128 * 128 * sizeof(float);
 constexpr size_t kRecordBytes = kRecordO + 2 * 128 * sizeof(float);
@@ -109,6 +113,7 @@ struct PrefillScoreParams {
   int32_t* status;
   ScoreParams score;
   int32_t total_q, max_tiles;
+  bool whole_only;           // a CTA per job: nothing is split (and no merge kernel follows)
   const uint16_t* q_rows;    // the operands, for repair_row
   const uint16_t* k_rows;
   const uint16_t* v_rows;
@@ -244,6 +249,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
   const long long total = T * p.hkv, target = (total + G - 1) / G;
   const int jobs = tiles * p.hkv;
   auto job_cost = [&](int jo) { return static_cast<long long>(p.ws_tiles[jo % tiles].J + kJobCost); };
+  if (p.whole_only) {  // jobs <= G (by the host's bound of the tiles): CTA c takes job c
+    for (int c = tid; c <= G; c += kPlanThreads) p.ws_tail[c] = total;
+    if (tid == 0) *p.ws_plan = PlanHeader{tiles, 1, G, 0, T, jobs};
+    return;
+  }
   const int rmax = jobs / G;
   if (tid == 0) rounds = rmax;
   __syncthreads();
@@ -554,7 +564,9 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
     return;
   }
   ScoreSmem& s = *reinterpret_cast<ScoreSmem*>(smem_raw);
-  if (p.ws_plan->rounds == 0 && p.ws_tail[blockIdx.x] >= p.ws_tail[blockIdx.x + 1]) return;  // no work
+  if (p.whole_only ? static_cast<int>(blockIdx.x) >= p.ws_plan->tiles * p.hkv
+                   : p.ws_plan->rounds == 0 && p.ws_tail[blockIdx.x] >= p.ws_tail[blockIdx.x + 1])
+    return;  // no work
 
   if (threadIdx.x == 0) {
     mbar_init(&s.q_full, 1);
@@ -1213,6 +1225,7 @@ pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUten
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_score_kernel<P>, qm, km, vm, p);
   if (e != cudaSuccess) return record_cuda_error(e, "prefill_score_kernel");
+  if (p.whole_only) return PA_OK;
   cfg.gridDim = dim3((max_q_len + kTileM - 1) / kTileM, p.hkv * 8, p.batch);
   cfg.blockDim = dim3(kMergeRows);
   cfg.dynamicSmemBytes = 0;
@@ -1232,7 +1245,7 @@ pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, cons
                                const void* k_pool, const void* v_pool, int64_t num_pages,
                                const int32_t* block_table, int32_t bt_stride,
                                const int32_t* seq_lens, int32_t batch, int32_t max_q_len,
-                               float softmax_scale, void* out, float* lse, void* workspace,
+                               int32_t max_seq_len, float softmax_scale, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, int32_t* status, cudaStream_t stream,
                                int32_t max_ctas, const pa_score_opts& score) {
   if (batch > kMaxBatch) {
@@ -1271,6 +1284,7 @@ pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, cons
     p.score = score_params(score, softmax_scale, &p.scale_log2);
     p.total_q = total_q;
     p.max_tiles = max_tiles;
+    p.whole_only = max_tiles * hkv <= grid && max_seq_len <= kWholeKeys;
     p.q_rows = static_cast<const uint16_t*>(q);
     p.k_rows = static_cast<const uint16_t*>(k_pool);
     p.v_rows = static_cast<const uint16_t*>(v_pool);
