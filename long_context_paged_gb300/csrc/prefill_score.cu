@@ -492,7 +492,7 @@ __device__ __forceinline__ void piece_max(const uint32_t (&sb)[kTileN], float (&
 // column 0.
 template <class P>
 __device__ __forceinline__ bool score_bound(const P& p, const RowMask& rm, int k0, float slope2, const float (&cm)[4],
-                                            bool partial, float& top, float& d0) {
+                                            bool hidden, bool partial, float& top, float& d0) {
   bool good = true;
   float slack = 0.f;
   if constexpr (P::kCap) {
@@ -513,7 +513,7 @@ __device__ __forceinline__ bool score_bound(const P& p, const RowMask& rm, int k
     slack += fabsf(slope2) * 31.f;
     good = good && (k0 + kTileN - 1 <= rm.qpos || k0 >= rm.prefix);  // keys after the row: in the prefix
   }
-  return __all_sync(0xffffffffu, good && slack <= kMaxSlack);
+  return __all_sync(0xffffffffu, hidden || (good && slack <= kMaxSlack));
 }
 
 // Any other tile: scores in log2 units, in place.
@@ -862,7 +862,10 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
         tc::tmem_wait_ld();
         const int j = pjb + i;
         const int k0 = (j < n1 ? j : j + shift) * kTileN;
-        const bool partial = k0 + kTileN > rm.prefix && (k0 < rm.lo || k0 + kTileN - 1 > rm.qpos);
+        // A row that sees no key of the tile (one that sees nothing at all makes every tile such a
+        // one for its warp) is not masked key by key: its exponents' offset is -inf.
+        const bool hidden = k0 >= rm.prefix && (k0 + kTileN <= rm.lo || k0 > rm.qpos || rm.lo > rm.qpos);
+        const bool partial = !hidden && k0 + kTileN > rm.prefix && (k0 < rm.lo || k0 + kTileN - 1 > rm.qpos);
         bool one_pass = true;             // (scores without options always are)
         [[maybe_unused]] float d0 = 0.f;  // bias distance of column 0, from the nearest visible key
         float top = 0.f;                  // the scores' maximum, or a bound of it (log2 units)
@@ -872,7 +875,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
           piece_max(sb, cm);
         }
         if constexpr (kLog2Units) {
-          one_pass = score_bound<P>(p, rm, k0, slope2, cm, partial, top, d0);
+          one_pass = score_bound<P>(p, rm, k0, slope2, cm, hidden, partial, top, d0);
           if (!one_pass) {
             score_tile<P>(p, sb, rm, k0, slope2, fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3])));
             if (P::kCap && partial) mask_tile(sb, rm, k0);
@@ -882,6 +885,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
         } else {
           top = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3])) * p.scale_log2;
         }
+        if (hidden) top = -CUDART_INF_F;
         const bool grow = top > m_used + kRescaleThreshold;
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? top : m_used;
@@ -905,7 +909,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         // weights (bf16) over S's first 64 columns. A row that has not met a visible key yet keeps
         // m_used = -inf; a finite offset then gives exp2(-inf) = 0 for its masked scores, not NaN.
-        const float m_eff = (m_used == -CUDART_INF_F) ? 0.f : m_used;
+        const float m_eff = hidden ? CUDART_INF_F : (m_used == -CUDART_INF_F) ? 0.f : m_used;
         const float2 nm2 = make_float2(-m_eff, -m_eff);
         float2 ls[4];  // 4 independent paired partial sums
 #pragma unroll
@@ -951,7 +955,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
           weights([&](float2 x, int) { return fma2(x, sc2, nm2); });
         }
         const float2 lsum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
-        l += lsum.x + lsum.y;
+        if (!hidden) l += lsum.x + lsum.y;  // (not even 0: a key the row does not see may be NaN)
         tc::tmem_wait_st();
         tc::fence_before_sync();
         // one elected arrive per warp: 128 arrivals on one barrier word serialise for hundreds

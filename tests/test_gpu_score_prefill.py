@@ -302,3 +302,30 @@ def test_large_capped_scores_of_one_sign(cuda_lib, cap, sign):
     inp.q[0] = q.to(torch.bfloat16)
     check(cuda_lib, inp, dict(softcap=cap))
     check(cuda_lib, inp, dict(softcap=cap, slopes=SLOPES, window=150), poison=False)
+
+
+@pytest.mark.parametrize("o", [dict(), dict(softcap=12.0), dict(slopes=SLOPES)])
+def test_rows_that_see_no_key_of_a_tile(cuda_lib, o):
+    """Rows that see nothing, or only tiles before or after the one at hand, beside rows that see it:
+    also where the keys they do not see are NaN (their own document's are not)."""
+    n, off = 256, 384
+    pos = np.arange(off, off + n)
+    start = np.where(pos % 7 == 3, pos + 1, np.where(pos % 2, off + 128 * ((pos - off) // 128), 0))
+    o = dict(o, row_start=start)
+    inp = W.make_paged(68, [off + n], [n], device="cuda", q_scale=2.0)
+    check(cuda_lib, inp, o, poison=False)
+    # NaN keys and values at positions 100 .. 105: rows of the documents that start later are unmoved
+    bt = inp.host_block_table
+    clean = call(cuda_lib, inp, o)
+    for p in range(100, 106):
+        inp.k_pools[0][int(bt[0, p // 16]), p % 16] = float("nan")
+        inp.v_pools[0][int(bt[0, p // 16]), p % 16] = float("nan")
+    later = [r for r in range(n) if start[r] > 105]
+    ref_o, ref_l = reference(inp, o, rows=set(later))
+    for cap in (None, 1, 5):
+        out, lse = call(cuda_lib, inp, o, max_ctas=cap)
+        torch.cuda.synchronize()
+        close(out, lse, ref_o, ref_l, rows=later, what=str(cap))
+        assert torch.equal(lse[later], clean[1][later]) or cap is not None
+        first = [r for r in range(n) if start[r] == 0]
+        assert bool(out[first].isnan().all())
