@@ -195,8 +195,9 @@ def _stream(stream):
 
 
 def _empty(shape, dtype, device, stream):
-    """A new tensor for work on `stream` (None: the current one): allocated from that stream's memory,
-    so that the block is neither still read by other work nor handed out again before this work ran."""
+    """A new tensor for work on `stream` (None: the current one): allocated from that stream's
+    memory, so that the block is neither still read by other work nor handed out again before this
+    work ran."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
@@ -287,6 +288,13 @@ def _device(call, t, name, dtype):
     return dev
 
 
+def _need_dims(*named):
+    """Every (name, tensor, dims) must have that many dims."""
+    for name, t, d in named:
+        if t.dim() != d:
+            raise ValueError(f"{name} must have {d} dims, got {t.dim()}")
+
+
 def _sized(name, t, shape):
     """t must have exactly this shape."""
     if t.shape != shape:
@@ -365,7 +373,7 @@ def _workspace_size(fn, *key):
     key = (fn, torch.cuda.current_device()) + key
     n = _ws_sizes.get(key)
     if n is None:
-        if len(_ws_sizes) > 4096:  # (a server's shapes are few; this bounds a caller that varies them)
+        if len(_ws_sizes) > 4096:  # a server's shapes are few; this bounds a caller that varies them
             _ws_sizes.clear()
         n = _ws_sizes[key] = fn(*key[2:])
     return n
@@ -420,11 +428,11 @@ def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int
     pv = _tensor(call, v_pool, "v_pool", torch.bfloat16, dev)
     pbt = _tensor(call, block_table, "block_table", torch.int32, dev)
     psl = _tensor(call, seq_lens, "seq_lens", torch.int32, dev)
-    for t, n, d in ((q, "q", 3), (k_pool, "k_pool", 4), (v_pool, "v_pool", 4),
-                    (block_table, "block_table", 2), (seq_lens, "seq_lens", 1)):
-        if t.dim() != d:
-            raise ValueError(f"{n} must have {d} dims, got {t.dim()}")
-    B, hq = q.shape[0], q.shape[1]
+    if not (q.dim() == 3 and k_pool.dim() == v_pool.dim() == 4 and block_table.dim() == 2
+            and seq_lens.dim() == 1):
+        _need_dims(("q", q, 3), ("k_pool", k_pool, 4), ("v_pool", v_pool, 4),
+                   ("block_table", block_table, 2), ("seq_lens", seq_lens, 1))
+    B, hq, _ = q.shape
     rows, bt_stride = block_table.shape
     if rows < B:
         _rows_at_least("block_table", block_table, B)
@@ -433,8 +441,9 @@ def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int
     heads = _heads(dims)
     if heads is not None:
         _sized("q", q, (B, heads[0], 128))
-        _sized("k_pool", k_pool, (num_pages, 16, heads[1], 128))
-        _sized("v_pool", v_pool, (num_pages, 16, heads[1], 128))
+        pool = (num_pages, 16, heads[1], 128)
+        _sized("k_pool", k_pool, pool)
+        _sized("v_pool", v_pool, pool)
     if out is None:
         out = _empty(q.shape, torch.bfloat16, q.device, stream)
         po = out.data_ptr()
@@ -452,15 +461,15 @@ def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int
     score = _score(call, dev, hq, B, B, max_seq_len, softcap, alibi_slopes, window, prefix_lens,
                    max_prefix_len, row_start)
     if workspace is None:
-        workspace = _workspace(_workspace_size(decode_workspace_size, B, max_seq_len, split_tokens, dims),
-                               q.device, None, stream)
+        nbytes = _workspace_size(decode_workspace_size, B, max_seq_len, split_tokens, dims)
+        workspace = _workspace(nbytes, q.device, None, stream)
     else:
         _on_device(call, workspace)
     ps = None if status is None else _tensor(call, status, "status", torch.int32, dev)
     lib = load()
-    args = (_dims(dims), pq, pk, pv, num_pages, pbt, bt_stride, psl, B, max_seq_len, float(softmax_scale),
-            split_tokens, po, pl, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            ps, _stream(stream))
+    args = (_dims(dims), pq, pk, pv, num_pages, pbt, bt_stride, psl, B, max_seq_len,
+            float(softmax_scale), split_tokens, po, pl, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), ps, _stream(stream))
     keep, ref = _opts(max_ctas)
     if score is not None:
         _check("attn_decode_paged_score",
@@ -527,12 +536,12 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
     pv = _tensor(call, v_pool, "v_pool", torch.bfloat16, dev)
     pbt = _tensor(call, block_table, "block_table", torch.int32, dev)
     psl = _tensor(call, seq_lens, "seq_lens", torch.int32, dev)
-    for t, n, d in ((q, "q", 3), (cu_q_lens, "cu_q_lens", 1), (k_pool, "k_pool", 4),
-                    (v_pool, "v_pool", 4), (block_table, "block_table", 2), (seq_lens, "seq_lens", 1)):
-        if t.dim() != d:
-            raise ValueError(f"{n} must have {d} dims, got {t.dim()}")
+    if not (q.dim() == 3 and k_pool.dim() == v_pool.dim() == 4 and block_table.dim() == 2
+            and cu_q_lens.dim() == seq_lens.dim() == 1):
+        _need_dims(("q", q, 3), ("cu_q_lens", cu_q_lens, 1), ("k_pool", k_pool, 4),
+                   ("v_pool", v_pool, 4), ("block_table", block_table, 2), ("seq_lens", seq_lens, 1))
     B = seq_lens.shape[0]
-    Tq, hq = q.shape[0], q.shape[1]
+    Tq, hq, _ = q.shape
     rows, bt_stride = block_table.shape
     _rows_at_least("cu_q_lens", cu_q_lens, B + 1)
     if rows < B:
@@ -541,8 +550,9 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
     heads = _heads(dims)
     if heads is not None:
         _sized("q", q, (Tq, heads[0], 128))
-        _sized("k_pool", k_pool, (num_pages, 16, heads[1], 128))
-        _sized("v_pool", v_pool, (num_pages, 16, heads[1], 128))
+        pool = (num_pages, 16, heads[1], 128)
+        _sized("k_pool", k_pool, pool)
+        _sized("v_pool", v_pool, pool)
     if out is None:
         out = _empty(q.shape, torch.bfloat16, q.device, stream)
         po = out.data_ptr()
@@ -560,16 +570,16 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
     score = _score(call, dev, hq, B, Tq, max_seq_len, softcap, alibi_slopes, window, prefix_lens,
                    max_prefix_len, row_start)
     if workspace is None:
-        nbytes = (_workspace_size(prefill_workspace_size, B, max_q_len, max_seq_len, dims) if score is None
-                  else _workspace_size(prefill_score_workspace_size, B, Tq, dims))
+        nbytes = (_workspace_size(prefill_score_workspace_size, B, Tq, dims) if score is not None
+                  else _workspace_size(prefill_workspace_size, B, max_q_len, max_seq_len, dims))
         workspace = _workspace(nbytes, q.device, None, stream)
     else:
         _on_device(call, workspace)
     ps = None if status is None else _tensor(call, status, "status", torch.int32, dev)
     lib = load()
-    args = (_dims(dims), pq, pcu, Tq, pk, pv, num_pages, pbt, bt_stride, psl, B, max_q_len, max_seq_len,
-            float(softmax_scale), po, pl, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            ps, _stream(stream))
+    args = (_dims(dims), pq, pcu, Tq, pk, pv, num_pages, pbt, bt_stride, psl, B, max_q_len,
+            max_seq_len, float(softmax_scale), po, pl, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), ps, _stream(stream))
     keep, ref = _opts(max_ctas)
     if score is not None:
         _check("attn_prefill_chunk_score",
@@ -635,8 +645,10 @@ def paged_step_plan(cached_lens, new_lens, block_table, free_pages, free_count, 
     pbt = _tensor(call, block_table, "block_table", i32, dev)
     pf = _tensor(call, free_pages, "free_pages", i32, dev)
     pfc = _tensor(call, free_count, "free_count", i32, dev)
-    if cached_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1 or free_count.dim() != 1:
-        raise ValueError("cached_lens, free_pages and free_count must have 1 dim, block_table 2")
+    if not (cached_lens.dim() == free_pages.dim() == free_count.dim() == 1
+            and block_table.dim() == 2):
+        _need_dims(("cached_lens", cached_lens, 1), ("block_table", block_table, 2),
+                   ("free_pages", free_pages, 1), ("free_count", free_count, 1))
     B = cached_lens.shape[0]
     _sized("new_lens", new_lens, (B,))
     rows, bt_stride = block_table.shape
@@ -646,14 +658,17 @@ def paged_step_plan(cached_lens, new_lens, block_table, free_pages, free_count, 
     total_rows = int(total_rows)
     if total_rows < 0:
         raise ValueError("total_rows must be >= 0")
-    free_count_out, pfo = _new_or_given(call, free_count_out, "free_count_out", i32, (1,), dev, stream)
+    free_count_out, pfo = _new_or_given(call, free_count_out, "free_count_out", i32, (1,), dev,
+                                        stream)
     cu_new_lens, pcu = _new_or_given(call, cu_new_lens, "cu_new_lens", i32, (B + 1,), dev, stream)
     seq_lens, psl = _new_or_given(call, seq_lens, "seq_lens", i32, (B,), dev, stream)
     positions, pp = _new_or_given(call, positions, "positions", i32, (total_rows,), dev, stream)
-    slot_map, psm = _new_or_given(call, slot_map, "slot_map", torch.int64, (total_rows,), dev, stream)
+    slot_map, psm = _new_or_given(call, slot_map, "slot_map", torch.int64, (total_rows,), dev,
+                                  stream)
     ps = None if status is None else _tensor(call, status, "status", i32, dev)
-    _check(call, load().paged_step_plan(pc, pn, B, pbt, bt_stride, pf, free_pages.shape[0], pfc, int(num_pages),
-                                        total_rows, pfo, pcu, psl, pp, psm, ps, _stream(stream)))
+    _check(call, load().paged_step_plan(
+        pc, pn, B, pbt, bt_stride, pf, free_pages.shape[0], pfc, int(num_pages), total_rows, pfo,
+        pcu, psl, pp, psm, ps, _stream(stream)))
     return StepPlan(cu_new_lens, seq_lens, positions, slot_map, free_count_out)
 
 
@@ -669,18 +684,21 @@ def paged_release(begin_pages, end_pages, block_table, free_pages, free_count, n
     pbt = _tensor(call, block_table, "block_table", i32, dev)
     pf = _tensor(call, free_pages, "free_pages", i32, dev)
     pfc = _tensor(call, free_count, "free_count", i32, dev)
-    if begin_pages.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1 or free_count.dim() != 1:
-        raise ValueError("begin_pages, free_pages and free_count must have 1 dim, block_table 2")
+    if not (begin_pages.dim() == free_pages.dim() == free_count.dim() == 1
+            and block_table.dim() == 2):
+        _need_dims(("begin_pages", begin_pages, 1), ("block_table", block_table, 2),
+                   ("free_pages", free_pages, 1), ("free_count", free_count, 1))
     B = begin_pages.shape[0]
     _sized("end_pages", end_pages, (B,))
     rows, bt_stride = block_table.shape
     if rows < B:
         _rows_at_least("block_table", block_table, B)
     _rows_at_least("free_count", free_count, 1)
-    free_count_out, pfo = _new_or_given(call, free_count_out, "free_count_out", i32, (1,), dev, stream)
+    free_count_out, pfo = _new_or_given(call, free_count_out, "free_count_out", i32, (1,), dev,
+                                        stream)
     ps = None if status is None else _tensor(call, status, "status", i32, dev)
-    _check(call, load().paged_release(pb, pe, B, pbt, bt_stride, pf, free_pages.shape[0], pfc, int(num_pages), pfo,
-                                      ps, _stream(stream)))
+    _check(call, load().paged_release(pb, pe, B, pbt, bt_stride, pf, free_pages.shape[0], pfc,
+                                      int(num_pages), pfo, ps, _stream(stream)))
     return free_count_out
 
 
@@ -765,8 +783,9 @@ def rope_append_paged(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_
     q_out, pqo = _new_or_given(call, q_out, "q_out", torch.bfloat16, (T, hq, 128), dev, stream)
     ps = None if status is None else _tensor(call, status, "status", torch.int32, dev)
     _check(call, load().rope_append_paged(
-        _dims(dims), 2 * inv_freq.shape[0], 1 if interleaved else 0, pif, float(attn_factor), pq, qs, pk, ks, pv,
-        vs, T, pp, psm, pqg, pkg, float(eps), pqo, pkp, pvp, num_pages, ps, _stream(stream)))
+        _dims(dims), 2 * inv_freq.shape[0], 1 if interleaved else 0, pif, float(attn_factor), pq, qs,
+        pk, ks, pv, vs, T, pp, psm, pqg, pkg, float(eps), pqo, pkp, pvp, num_pages, ps,
+        _stream(stream)))
     return q_out
 
 
