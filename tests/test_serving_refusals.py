@@ -102,3 +102,32 @@ def test_python_argument_checks(lib):
         pa.paged_step_plan(i, i, i, i, i, 4, total_rows=2)
     with pytest.raises(TypeError):
         pa.paged_release(i.float(), i, i, i, i, 4)
+
+
+def test_score_options(lib):
+    """Options are checked before any CUDA call, for both attention calls; NULL options and an empty
+    batch pass."""
+    import long_context_paged_gb300 as pa
+    good = pa.Dims(*pa.DEFAULT_DIMS)
+    nan = float("nan")
+
+    def both(softcap=0.0, window=0, max_prefix=0, prefix=0, batch=1):
+        o = ctypes.byref(pa.ScoreOpts(softcap, 0, window, prefix, max_prefix, 0))
+        # null q: refused too, so only an option error can be told apart by the empty batch's OK
+        d = lib.attn_decode_paged_score(good, None, None, None, 1, None, 1, None, batch, 16, 1.0, 0, None,
+                                        None, None, 0, None, None, None, o)
+        p = lib.attn_prefill_chunk_score(good, None, None, 1, None, None, 1, None, 1, None, batch, 1, 16,
+                                         1.0, None, None, None, 0, None, None, None, o)
+        assert d == p
+        return d
+
+    assert both(batch=0) == OK and both() == INVALID     # null pointers
+    assert both(softcap=30.0, window=5, max_prefix=131072, batch=0) == OK
+    for bad in (dict(softcap=-1.0), dict(softcap=nan), dict(softcap=float("inf")), dict(softcap=1e-9),
+                dict(window=-1), dict(max_prefix=-1), dict(max_prefix=131073)):
+        assert both(batch=0, **bad) == INVALID, bad
+    bad_cap = pa.LaunchOpts(-1)
+    assert lib.attn_decode_paged_score(good, None, None, None, 1, None, 1, None, 0, 16, 1.0, 0, None, None,
+                                       None, 0, None, None, ctypes.byref(bad_cap), None) == INVALID
+    assert lib.attn_prefill_chunk_score(pa.Dims(16, 4, 128, 16), None, None, 1, None, None, 1, None, 1, None,
+                                        1, 1, 16, 1.0, None, None, None, 0, None, None, None, None) == UNSUPPORTED
