@@ -534,7 +534,7 @@ __device__ __forceinline__ void score_tile(const P& p, uint32_t (&sb)[kTileN], c
     } else {
 #pragma unroll
       for (int c = 0; c < kTileN; ++c)
-        sb[c] = __float_as_uint(p.score.cap_log2 * tanh_exp(__uint_as_float(sb[c]) * p.scale_log2));
+        sb[c] = __float_as_uint(p.score.cap_log2 * tanh_score(__uint_as_float(sb[c]) * p.scale_log2));
     }
   }
   if constexpr (P::kBias) {

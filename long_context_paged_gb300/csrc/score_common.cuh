@@ -28,15 +28,18 @@ struct ScoreParams {
   const int32_t* row_start;  // [rows] or null
   // softcap * log2 e * tanh(q_scale * s) of a raw product s as an odd polynomial s P(s^2), for
   // |s| <= poly_max (|q_scale s| <= 1; 0: not usable)
-  float poly[6], poly_max;
+  float poly[7], poly_max;
 };
 
 // Coefficients of x P(x^2) nearest to tanh x on |x| <= 1: least maximum error over a dense grid by
-// iteratively reweighted least squares (Lawson), rounded to fp32. The error, 2.5e-7, times a cap of 50
-// is 2^-16 of a score.
-constexpr int kTanhTerms = 6;
-constexpr double kTanh[kTanhTerms] = {9.999968410e-01, -3.332400322e-01, 1.325352490e-01,
-                                      -5.097286403e-02, 1.611418277e-02, -2.839466557e-03};
+// iteratively reweighted least squares (Lawson), rounded to fp32. The error, 2.4e-8, times a cap of 50
+// is 2^-19 of a score; the fp32 evaluation adds roundings of up to 2^-23, of either sign.
+constexpr int kTanhTerms = 7;
+__host__ __device__ constexpr double tanh_coefficient(int k) {
+  constexpr double c[kTanhTerms] = {9.999997020e-01, -3.333213031e-01, 1.331958324e-01, -5.326583609e-02,
+                                    1.997328550e-02, -5.951282568e-03, 9.637727635e-04};
+  return c[k];
+}
 
 inline bool score_opts_valid(const pa_score_opts& o) {
   return (o.softcap == 0.f || (o.softcap >= 1e-6f && o.softcap < 1e30f)) && o.window >= 0 && o.max_prefix_len >= 0 &&
@@ -66,7 +69,7 @@ inline ScoreParams score_params(const pa_score_opts& o, float softmax_scale, flo
   const double x = *q_scale;
   if (o.softcap > 0.f && x >= 0x1p-10 && x <= 0x1p10) {  // the folded coefficients stay in range
     double a = static_cast<double>(s.cap_log2) * x;
-    for (int k = 0; k < kTanhTerms; ++k, a *= x * x) s.poly[k] = static_cast<float>(kTanh[k] * a);
+    for (int k = 0; k < kTanhTerms; ++k, a *= x * x) s.poly[k] = static_cast<float>(tanh_coefficient(k) * a);
     s.poly_max = static_cast<float>(1.0 / x);
   }
   return s;
@@ -95,17 +98,28 @@ __device__ __forceinline__ float slope_over(const ScoreParams& s, int head, floa
   return isinf(r) && !isinf(a) ? copysignf(3.402823466e38f, a) : r;
 }
 
-// tanh by one exponential: 1 - 2 / (e^{2x} + 1), within 2^-22 absolutely (the exponential and the
-// quotient err by 2^-22 of values below 2), which times a cap of 50 is 2^-16 of a score; exact at
-// the ends (e^{2x} = inf gives 1, 0 gives -1), NaN stays NaN.
+// tanh by one exponential: 1 - 2 / (e^{2x} + 1), within 2^-22 absolutely (near 0 the exponential's
+// error of 2^-22 counts half and the quotient is near 1); exact at the ends (e^{2x} = inf gives 1, 0
+// gives -1), NaN stays NaN.
 __device__ __forceinline__ float tanh_exp(float x) {
   return 1.0f - __fdividef(2.0f, fast_exp2(x * (2.0f * kLog2e)) + 1.0f);
+}
+
+// tanh of a score: the polynomial up to |x| = 1; beyond it the exponential form, whose errors shrink
+// there with 1 - tanh^2 and the quotient. A cap of 50 makes an absolute error of 2^-22 one of 10^-5 in
+// the log-sum-exp of a row with few keys, 2^-24 one that fp32 has anyway.
+__device__ __forceinline__ float tanh_score(float x) {
+  const float t = x * x;
+  float y = static_cast<float>(tanh_coefficient(kTanhTerms - 1));
+#pragma unroll
+  for (int k = kTanhTerms - 2; k >= 0; --k) y = fmaf(y, t, static_cast<float>(tanh_coefficient(k)));
+  return t <= 1.0f ? y * x : tanh_exp(x);
 }
 
 // The score in log2 units of q's scaled product x: capped, then the bias at `distance` (from the
 // nearest visible key) of a head of slope slope2 / log2 e.
 __device__ __forceinline__ float score_of(const ScoreParams& s, float x, float slope2, int distance) {
-  if (s.cap_log2 != 0.f) x = s.cap_log2 * tanh_exp(x);
+  if (s.cap_log2 != 0.f) x = s.cap_log2 * tanh_score(x);
   if (s.slopes != nullptr) x = fmaf(-slope2, static_cast<float>(distance), x);
   return x;
 }
