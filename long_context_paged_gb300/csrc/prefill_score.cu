@@ -126,6 +126,7 @@ struct PrefillScoreParams {
 };
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanTiles = 4096;  // tiles whose key-tile counts the plan keeps in shared memory
 
 __device__ __forceinline__ long long block_scan_incl(long long v, long long* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
   __shared__ int32_t seq[kMaxBatch][5];  // q0, n, L, off, prefix
   __shared__ long long carry;
   __shared__ int32_t rounds;
+  __shared__ int32_t count[kPlanTiles];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- chunks: a chunk that does not fit its sequence, its table row or the packing is flagged
@@ -221,8 +223,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
     const int t0 = max(min(lo, hi) / kTileN, d.n1);
     d.shift = t0 - d.n1;
     d.J = max(1, d.n1 + max(0, end - t0));
-    if (lane == 0) p.ws_tiles[i] = d;
+    if (lane == 0) {
+      p.ws_tiles[i] = d;
+      if (i < kPlanTiles) count[i] = d.J;
+    }
   }
+  auto key_tiles = [&](int i) { return i < kPlanTiles ? count[i] : p.ws_tiles[i].J; };
   for (int b = tid; b <= p.batch; b += kPlanThreads) p.ws_first_tile[b] = first_tile[b];
   if (tid == 0) carry = 0;
   __syncthreads();
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
   // ---- units before each tile
   for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    const long long u = i < tiles ? p.ws_tiles[i].J + kJobCost : 0;
+    const long long u = i < tiles ? key_tiles(i) + kJobCost : 0;
     const long long incl = block_scan_incl(u, warp_sums) + carry;
     if (i < tiles) p.ws_units[i] = incl - u;
     __syncthreads();
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
   //      then the remaining units in consecutive ranges that level the CTAs
   const long long total = T * p.hkv, target = (total + G - 1) / G;
   const int jobs = tiles * p.hkv;
-  auto job_cost = [&](int jo) { return static_cast<long long>(p.ws_tiles[jo % tiles].J + kJobCost); };
+  auto job_cost = [&](int jo) { return static_cast<long long>(key_tiles(jo % tiles) + kJobCost); };
   if (p.whole_only) {  // jobs <= G (by the host's bound of the tiles): CTA c takes job c
     for (int c = tid; c <= G; c += kPlanThreads) p.ws_tail[c] = total;
     if (tid == 0) *p.ws_plan = PlanHeader{tiles, 1, G, 0, T, jobs};
@@ -552,22 +558,14 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap v_map, const P p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // a programmatic dependent of its plan kernel; its merge kernel waits for its completion
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   if ((smem_addr(smem_raw) & 1023u) != 0) {
-    // not the layout this kernel was built for: do nothing, and make the merge do nothing
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.ws_plan->whole_jobs = 0x7fffffffffffffffll;
-      flag_error(p.status, PA_DEV_ERR_INTERNAL);
-    }
+    // not the layout this kernel was built for: do nothing (the merge then has nothing to read but
+    // what an earlier call left; the error flag says that the call failed)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.status, PA_DEV_ERR_INTERNAL);
     return;
   }
   ScoreSmem& s = *reinterpret_cast<ScoreSmem*>(smem_raw);
-  if (p.whole_only ? static_cast<int>(blockIdx.x) >= p.ws_plan->tiles * p.hkv
-                   : p.ws_plan->rounds == 0 && p.ws_tail[blockIdx.x] >= p.ws_tail[blockIdx.x + 1])
-    return;  // no work
-
   if (threadIdx.x == 0) {
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 2);       // released by each M tile's softmax
@@ -595,8 +593,16 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem_base;
+  // a programmatic dependent of its plan kernel, set up so far while that ran; its merge kernel
+  // waits for its completion
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const bool work = p.whole_only ? static_cast<int>(blockIdx.x) < p.ws_plan->tiles * p.hkv
+                                 : p.ws_plan->rounds > 0 || p.ws_tail[blockIdx.x] < p.ws_tail[blockIdx.x + 1];
 
-  if (warp >= kVWarp) {
+  if (!work) {
+    // nothing to do but to give the tensor memory back
+  } else if (warp >= kVWarp) {
     tc::regs_decrease<kControlRegs>();
   if (warp == kSchedWarp) {
     // ------------------------------------------------------------------ scheduler
@@ -1064,8 +1070,8 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
 // slot 0 of each later CTA.
 template <class P>
 __global__ void __launch_bounds__(kMergeRows) prefill_score_merge_kernel(const P p) {
-  // programmatic dependent of prefill_score_kernel: wait until that grid is complete and visible
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // A programmatic dependent of prefill_score_kernel, whose CTAs let it launch once they have seen
+  // the plan: the plan is read before the wait for that grid's results, further down.
   // CTA (qt, g * 8 + t * 4 + quarter, b), counted from the end of the grid: rows of query tile
   // qt, head 2g + t, dims 32 * quarter .. +31; one thread per row. A job cut into pieces is
   // merged by 8 CTAs, so the few split jobs of a call are spread over many SMs instead of one CTA
@@ -1077,13 +1083,16 @@ __global__ void __launch_bounds__(kMergeRows) prefill_score_merge_kernel(const P
   const int qt = gridDim.x - 1 - blockIdx.x;
   const PlanHeader h = *p.ws_plan;
   const int tile = p.ws_first_tile[b] + qt;
-  if (tile >= p.ws_first_tile[b + 1]) return;
+  if (tile >= p.ws_first_tile[b + 1] || g * h.tiles + tile < h.whole_jobs) {
+    // no such tile, or a job done whole. (Every CTA waits, that this grid does not end before the
+    // one whose results the stream's next work may read.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const TileDesc d = p.ws_tiles[tile];
   const int G = min(h.grid, kMaxGrid);
-  const int jo = g * h.tiles + tile;
   const long long u0 = g * h.units + p.ws_units[tile], J = d.J;
   const int q0 = d.q0, n = d.n;
-  if (jo < h.whole_jobs) return;  // done whole in the round-robin phase
   // the split's range starts, staged in shared memory: one round of loads instead of a chain of
   // dependent ones per binary search
   __shared__ long long tail[kMaxGrid + 1];
@@ -1100,6 +1109,7 @@ __global__ void __launch_bounds__(kMergeRows) prefill_score_merge_kernel(const P
     return lo;
   };
   const int c0 = cta_of(u0), c1 = cta_of(u0 + J - 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;
   const int r = threadIdx.x;
   const int qrow = qt * kTileM + r;
