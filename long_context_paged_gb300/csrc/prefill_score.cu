@@ -12,11 +12,15 @@
 //    row sees whole takes no masking; on the others a row's visible keys are two 32-bit mask words.
 //  * Scores. 8 softmax warps, one thread per row, as there: a row's 128 raw products come from TMEM with
 //    their maximum, and the weights go back as bf16 in one pass. The cap's tanh and the bias are taken in
-//    that same pass (the FMA pipe's work hides behind the MUFU unit's exponentials) wherever an upper
-//    bound of the scores' maximum follows from the products' maximum; see score_bound. Measured (4,096
-//    queries at 61,440): a pass of its own for the tanh, then the exponentials, 2,309 us; in one pass
-//    2,174 us. 16 softmax warps, two threads per row meeting at a barrier per tile, were slower (1,611
-//    against 1,340 us without options, 2,540 with a cap): 104 registers a thread spill.
+//    that same pass wherever a bound of the scores' maximum follows from the products' maximum (see
+//    score_bound), as a polynomial and a stepped distance on the FMA pipe, whose work then hides behind
+//    the MUFU unit's exponentials. Measured (4,096 queries at 61,440): masks alone 1,300 us (1,640
+//    TFLOP/s), as the plain kernel; cap 1,892 us (an exponential and a quotient per score took 3,146, a
+//    pass of its own for the polynomial 2,309, two polynomials by range 2,480: the code of the pass then
+//    no longer stays in the instruction cache); bias 1,746 us; both 2,590 us. What bounds it is a row's
+//    chain S -> weights -> P V: each paired FMA more per two scores costs 85 us. 16 softmax warps, two
+//    threads per row meeting at a barrier per tile, were slower (1,611 us with masks alone, 2,540 with a
+//    cap): at 96 to 104 registers a thread the pass spills.
 //  * Non-finite V rows are kept from the rows that do not see them (repair_row).
 #include <algorithm>
 
@@ -61,9 +65,10 @@ constexpr int kMaxBatch = 128;
 constexpr int kVStages = 3;   // V is needed a whole P*V later than K: one more stage in flight
 // Fixed cost of a job beyond its key tiles, in tiles (its epilogue and the restart of its chain)
 constexpr int kJobCost = 3;
-// Up to this many keys a call whose jobs fit one to a CTA is not split. One CTA a job is faster while a
-// job has few tiles (375 queries at 0: 18.9 us, split and merged 27.4; 300 at 700: 26.3, split 29.9) and
-// slower beyond (300 at 1,700: 36.3, split 32.4).
+// Up to this many keys a call whose jobs fit one to a CTA is not split. One CTA a job, without plan
+// and merge, is faster while a job has few tiles (300 queries at 700: 23.0 us, split 27.6; 375 at 0:
+// 15.7, split 27.4) and no longer at 2,000 keys (300 at 1,700: 33.1, split 30.1; 100 at 1,948: 31.9,
+// split 36.7).
 constexpr int kWholeKeys = 1024;
 // A partial result: o [2 heads][32 float4 columns][128 rows], then lse [2][128] fp32.
 constexpr size_t kRecordO = 2 * 128 * 128 * sizeof(float);
@@ -113,7 +118,7 @@ struct PrefillScoreParams {
   int32_t* status;
   ScoreParams score;
   int32_t total_q, max_tiles;
-  bool whole_only;           // a CTA per job: nothing is split (and no merge kernel follows)
+  bool whole_only;           // a CTA per job: nothing is split, and neither plan nor merge is needed
   const uint16_t* q_rows;    // the operands, for repair_row
   const uint16_t* k_rows;
   const uint16_t* v_rows;
@@ -143,6 +148,137 @@ __device__ __forceinline__ long long block_scan_incl(long long v, long long* war
   return v + before;
 }
 
+// A chunk's first packed row, rows, keys and prefix, and its query tiles: none for an empty chunk, and
+// none (flagged) for one that does not fit its sequence, its table row or the packing.
+struct Chunk {
+  int32_t q0, n, L, prefix, tiles;
+};
+template <class P>
+__device__ __forceinline__ Chunk chunk_of(const P& p, int b, bool report) {
+  Chunk c;
+  c.q0 = p.cu_q_lens[b];
+  c.n = p.cu_q_lens[b + 1] - c.q0;
+  c.L = p.seq_lens[b];
+  c.tiles = c.prefix = 0;
+  if (c.n <= 0) return c;
+  if (c.n > c.L || c.L > p.bt_stride * kPage || c.q0 < 0 || c.n > p.total_q - c.q0) {
+    if (report) flag_error(p.status, PA_DEV_ERR_LENGTH);
+    return c;
+  }
+  c.tiles = (c.n + kTileM - 1) / kTileM;
+  c.prefix = min(score_prefix(p.score, b, p.status, report), c.L);
+  return c;
+}
+
+// The key tiles of query tile qt of chunk c (sequence b), by a whole warp: the lanes reduce the masks
+// of its 128 rows.
+template <class P>
+__device__ __forceinline__ TileDesc tile_desc(const P& p, const Chunk& c, int b, int qt, int lane) {
+  TileDesc d;
+  d.b = b;
+  d.qt = qt;
+  d.q0 = c.q0;
+  d.n = c.n;
+  d.L = c.L;
+  d.off = c.L - c.n;
+  d.prefix = c.prefix;
+  int lo = 0x7fffffff, hi = 0;
+  if (p.score.row_start == nullptr) {  // a row sees at least itself: the ends decide
+    lo = score_first_key(p.score, 0, d.off + qt * kTileM);
+    hi = d.off + min(d.n, (qt + 1) * kTileM);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kTileM / 32; ++k) {
+      const int row = qt * kTileM + 32 * k + lane;
+      if (row < d.n) {
+        const int first = score_first_key(p.score, d.q0 + row, d.off + row);
+        if (first <= d.off + row) {
+          lo = min(lo, first);
+          hi = max(hi, d.off + row + 1);
+        }
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+  }
+  d.lo = lo;
+  d.hi = hi;
+  d.n1 = (d.prefix + kTileN - 1) / kTileN;
+  const int end = (hi + kTileN - 1) / kTileN;
+  const int t0 = max(min(lo, hi) / kTileN, d.n1);
+  d.shift = t0 - d.n1;
+  d.J = max(1, d.n1 + max(0, end - t0));
+  return d;
+}
+
+// Key tiles [jb, je) of job (g, d) as a piece.
+__device__ __forceinline__ PieceDesc piece_of(const TileDesc& d, int g, int jb, int je) {
+  PieceDesc c;
+  c.b = d.b;
+  c.g = g;
+  c.qt = d.qt;
+  c.q0 = d.q0;
+  c.n = d.n;
+  c.L = d.L;
+  c.off = d.off;
+  c.J = d.J;
+  c.prefix = d.prefix;
+  c.n1 = d.n1;
+  c.shift = d.shift;
+  c.lo = d.lo;
+  c.hi = d.hi;
+  c.jb = jb;
+  c.je = je;
+  c.valid = jb < je;
+  return c;
+}
+
+// The job of CTA blockIdx.x when a call is not split (whole_only: at most as many jobs as CTAs), by a
+// whole warp, without a plan: four chunks a lane (kMaxBatch = 128), their tiles scanned.
+template <class P>
+__device__ PieceDesc whole_job(const P& p, int lane) {
+  const bool report = blockIdx.x == 0;
+  int tiles[4], mine = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = 4 * lane + k;
+    tiles[k] = b < p.batch ? chunk_of(p, b, report).tiles : 0;
+    mine += tiles[k];
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  if (report && lane == 0 && total > p.max_tiles) flag_error(p.status, PA_DEV_ERR_LENGTH);
+  PieceDesc none;
+  none.valid = 0;
+  if (total == 0) return none;
+  const int g = static_cast<int>(blockIdx.x) / total, i = static_cast<int>(blockIdx.x) - g * total;
+  if (g >= p.hkv) return none;
+  // the lane whose chunks hold tile i names the chunk and the tile in it
+  int left = i - (incl - mine), b = -1, qt = 0;
+  const bool here = left >= 0 && left < mine;
+  if (here) {
+    b = 4 * lane;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (b == 4 * lane + k && left >= tiles[k]) {
+        left -= tiles[k];
+        ++b;
+      }
+    }
+    qt = left;
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  b = __shfl_sync(0xffffffffu, b, from);
+  qt = __shfl_sync(0xffffffffu, qt, from);
+  const TileDesc d = tile_desc(p, chunk_of(p, b, false), b, qt, lane);
+  return piece_of(d, g, 0, d.J);
+}
+
 // One CTA: the chunks' query tiles, each tile's key tiles (a warp per tile; its 128 rows' masks
 // reduced by the lanes), a scan of their units, and the balanced split of the work.
 template <class P>
@@ -150,26 +286,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
   asm volatile("griddepcontrol.launch_dependents;");  // its CTAs wait for this grid's completion
   __shared__ long long warp_sums[kPlanThreads / 32];
   __shared__ int32_t first_tile[kMaxBatch + 1];
-  __shared__ int32_t seq[kMaxBatch][5];  // q0, n, L, off, prefix
+  __shared__ Chunk chunks[kMaxBatch];
   __shared__ long long carry;
   __shared__ int32_t rounds;
   __shared__ int32_t count[kPlanTiles];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // ---- chunks: a chunk that does not fit its sequence, its table row or the packing is flagged
-  //      and gets no tile
+  // ---- chunks
   int nqt = 0;
   if (tid < p.batch) {
-    const int q0 = p.cu_q_lens[tid], n = p.cu_q_lens[tid + 1] - q0, L = p.seq_lens[tid];
-    if (n > 0) {
-      if (n > L || L > p.bt_stride * kPage || q0 < 0 || n > p.total_q - q0) flag_error(p.status, PA_DEV_ERR_LENGTH);
-      else nqt = (n + kTileM - 1) / kTileM;
-    }
-    seq[tid][0] = q0;
-    seq[tid][1] = n;
-    seq[tid][2] = L;
-    seq[tid][3] = L - n;
-    seq[tid][4] = nqt > 0 ? min(score_prefix(p.score, tid, p.status, true), L) : 0;
+    chunks[tid] = chunk_of(p, tid, true);
+    nqt = chunks[tid].tiles;
   }
   const long long tiles_incl = block_scan_incl(nqt, warp_sums);
   if (tid < p.batch) first_tile[tid] = static_cast<int32_t>(min(tiles_incl - nqt, static_cast<long long>(p.max_tiles)));
@@ -189,40 +316,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
       const int mid = (b + hi_b) >> 1;
       if (first_tile[mid] <= i) b = mid; else hi_b = mid;
     }
-    TileDesc d;
-    d.b = b;
-    d.qt = i - first_tile[b];
-    d.q0 = seq[b][0];
-    d.n = seq[b][1];
-    d.L = seq[b][2];
-    d.off = seq[b][3];
-    d.prefix = seq[b][4];
-    int lo = 0x7fffffff, hi = 0;
-    if (p.score.row_start == nullptr) {  // a row sees at least itself: the ends decide
-      lo = score_first_key(p.score, 0, d.off + d.qt * kTileM);
-      hi = d.off + min(d.n, (d.qt + 1) * kTileM);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kTileM / 32; ++k) {
-        const int row = d.qt * kTileM + 32 * k + lane;
-        if (row < d.n) {
-          const int first = score_first_key(p.score, d.q0 + row, d.off + row);
-          if (first <= d.off + row) {
-            lo = min(lo, first);
-            hi = max(hi, d.off + row + 1);
-          }
-        }
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-    }
-    d.lo = lo;
-    d.hi = hi;
-    d.n1 = (d.prefix + kTileN - 1) / kTileN;
-    const int end = (hi + kTileN - 1) / kTileN;
-    const int t0 = max(min(lo, hi) / kTileN, d.n1);
-    d.shift = t0 - d.n1;
-    d.J = max(1, d.n1 + max(0, end - t0));
+    const TileDesc d = tile_desc(p, chunks[b], b, i - first_tile[b], lane);
     if (lane == 0) {
       p.ws_tiles[i] = d;
       if (i < kPlanTiles) count[i] = d.J;
@@ -255,11 +349,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p
   const long long total = T * p.hkv, target = (total + G - 1) / G;
   const int jobs = tiles * p.hkv;
   auto job_cost = [&](int jo) { return static_cast<long long>(key_tiles(jo % tiles) + kJobCost); };
-  if (p.whole_only) {  // jobs <= G (by the host's bound of the tiles): CTA c takes job c
-    for (int c = tid; c <= G; c += kPlanThreads) p.ws_tail[c] = total;
-    if (tid == 0) *p.ws_plan = PlanHeader{tiles, 1, G, 0, T, jobs};
-    return;
-  }
   const int rmax = jobs / G;
   if (tid == 0) rounds = rmax;
   __syncthreads();
@@ -305,22 +394,9 @@ struct ScoreWalker {
     const int g = jo / tiles, i = jo - g * tiles;
     const TileDesc d = p->ws_tiles[i];
     u0 = g * T + p->ws_units[i];
-    cur.b = d.b;
-    cur.g = g;
-    cur.qt = d.qt;
-    cur.q0 = d.q0;
-    cur.n = d.n;
-    cur.L = d.L;
-    cur.off = d.off;
-    cur.J = d.J;
-    cur.prefix = d.prefix;
-    cur.n1 = d.n1;
-    cur.shift = d.shift;
-    cur.lo = d.lo;
-    cur.hi = d.hi;
-    cur.jb = whole ? 0 : static_cast<int>(max(U0, u0) - u0);
-    cur.je = whole ? d.J : static_cast<int>(min(U1, u0 + d.J) - u0);
-    cur.valid = whole || (u0 < U1 && cur.jb < cur.je);
+    cur = whole ? piece_of(d, g, 0, d.J)
+                : piece_of(d, g, static_cast<int>(max(U0, u0) - u0), static_cast<int>(min(U1, u0 + d.J) - u0));
+    if (!whole && u0 >= U1) cur.valid = 0;
   }
 
   __device__ void start_tail() {
@@ -597,8 +673,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
   // waits for its completion
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const bool work = p.whole_only ? static_cast<int>(blockIdx.x) < p.ws_plan->tiles * p.hkv
-                                 : p.ws_plan->rounds > 0 || p.ws_tail[blockIdx.x] < p.ws_tail[blockIdx.x + 1];
+  const bool work = p.whole_only || p.ws_plan->rounds > 0 || p.ws_tail[blockIdx.x] < p.ws_tail[blockIdx.x + 1];
 
   if (!work) {
     // nothing to do but to give the tensor memory back
@@ -606,7 +681,15 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
     tc::regs_decrease<kControlRegs>();
   if (warp == kSchedWarp) {
     // ------------------------------------------------------------------ scheduler
-    if (lane == 0) {
+    if (p.whole_only) {  // this CTA's one job, then the end (the ring has room for both)
+      const PieceDesc d = whole_job(p, lane);
+      if (lane == 0) {
+        s.piece[0] = d;
+        mbar_arrive(&s.piece_full[0]);
+        s.piece[1].valid = 0;
+        mbar_arrive(&s.piece_full[1]);
+      }
+    } else if (lane == 0) {
       ScoreWalker<P> sw;
       sw.start(p);
       for (uint32_t k = 0;; ++k) {
@@ -1225,6 +1308,11 @@ pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUten
     }
     configured_device = dev;
   }
+  if (p.whole_only) {
+    prefill_score_kernel<P><<<p.max_tiles * p.hkv, kThreads, smem, stream>>>(qm, km, vm, p);
+    PA_CHECK_LAUNCH("prefill_score_kernel");
+    return PA_OK;
+  }
   prefill_plan_kernel<P><<<1, kPlanThreads, 0, stream>>>(p, grid);
   PA_CHECK_LAUNCH("prefill_plan_kernel");
   cudaLaunchConfig_t cfg = {};
@@ -1239,7 +1327,6 @@ pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUten
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_score_kernel<P>, qm, km, vm, p);
   if (e != cudaSuccess) return record_cuda_error(e, "prefill_score_kernel");
-  if (p.whole_only) return PA_OK;
   cfg.gridDim = dim3((max_q_len + kTileM - 1) / kTileM, p.hkv * 8, p.batch);
   cfg.blockDim = dim3(kMergeRows);
   cfg.dynamicSmemBytes = 0;
