@@ -6,8 +6,9 @@
 // the pair being dims (i, i + rot / 2) or, interleaved, (2i, 2i + 1); before it, q and k rows may
 // be RMS-normalised per head: x / sqrt(mean x^2 + eps) * gamma. One pass in fp32, one rounding
 // to bf16 at the end. The bound is memory: every q, k and v row is read once and written once
-// (16 KB per token of the 16/8-head decoder). Measured: 4,127 rows with norms 18.3 us (3.7 TB/s; a
-// copy of the same 67.6 MB takes 14.6 us at that size).
+// (16 KB per token of the 16/8-head decoder). Measured inside a graph: 4,127 rows with norms 13.4 us
+// (5.0 TB/s), 31 rows 2.6 us. At 8 dims of a row per lane instead of 4, loads in the same pass and a
+// barrier per pass the first form took 21 us; now instruction issue (63 %) and memory are both near.
 //
 // The angle. At position 100,000 an fp32 product position * inv_freq is off by up to 0.004 rad,
 // more than a bf16 rounding. Here a frequency is held in turns as a 64-bit binary fraction
@@ -38,8 +39,8 @@ constexpr int kThreads = 256;
 constexpr int kUnits = kThreads / 16;       // units of a CTA pass: two a warp
 constexpr int kMaxPairs = kHeadDim / 2;
 constexpr int kTableTokens = 32;            // tokens whose cosines and sines are held at a time
-// Two CTAs per SM at 110 registers: a pass in flight and one ahead of it for every warp. Three or four
-// CTAs of 80 or 64 registers spill and measured slower (20.5 and 24.4 against 18.3 us for 4,127 rows).
+// Two CTAs per SM: a pass in flight and one ahead of it for every warp, at 122 registers. Three or four
+// CTAs of 80 or 64 registers spill and measured slower (16.8 and 24.1 against 13.4 us for 4,127 rows).
 constexpr int kCtasPerSm = 2;
 
 struct RopeParams {
@@ -128,7 +129,7 @@ __device__ __forceinline__ float squares(uint2 raw) {
 
 // Rotation of one 128-dim row held 4 dims a lane by a warp; inv: its norm's factor.
 template <bool kInterleaved>
-__device__ __forceinline__ uint2 turn_row(uint2 raw, float inv, int partner, float sign, const Factors& f) {
+__device__ __forceinline__ uint2 turn_row(uint2 raw, float inv, int partner, bool past, const Factors& f) {
   const float2 x0 = make_float2(bf16lo(raw.x), bf16hi(raw.x)), x1 = make_float2(bf16lo(raw.y), bf16hi(raw.y));
   float2 y0, y1;
   if (kInterleaved) {  // the partner is the pair's other dim
@@ -139,7 +140,7 @@ __device__ __forceinline__ uint2 turn_row(uint2 raw, float inv, int partner, flo
     y0 = make_float2(bf16lo(a), bf16hi(a));
     y1 = make_float2(bf16lo(b), bf16hi(b));
   }
-  if (sign == 0.f) y0 = y1 = make_float2(0.f, 0.f);  // past rot: not even 0 times an infinite partner
+  if (past) y0 = y1 = make_float2(0.f, 0.f);  // past rot: not even 0 times an infinite partner
   const float2 inv2 = make_float2(inv, inv);
   const float2 r0 = mul2(fma2(y0, f.other[0], mul2(x0, f.own[0])), inv2);
   const float2 r1 = mul2(fma2(y1, f.other[1], mul2(x1, f.own[1])), inv2);
@@ -152,21 +153,29 @@ struct UnitRows {
   int64_t slot[2];
 };
 
-__device__ __forceinline__ void load_units(const RopeParams& p, int64_t unit0, int lane, UnitRows& r) {
-  const int hkv = 1 << p.hkv_shift;
+// A lane's place in the rows of its warp's two units: unit i's rows start i * step further. Advanced by
+// constants from pass to pass, so that a pass computes no address but the slots'.
+struct UnitPlace {
+  const uint16_t *q, *k, *v;
+  const int64_t* slot;
+  uint16_t* out;
+  int64_t q_step, k_step, v_step, out_step;  // elements from unit 0's rows to unit 1's
+  int slot_step;                             // tokens from unit 0 to unit 1
+};
+
+// left: tokens of the call from unit 0's on.
+__device__ __forceinline__ void load_units(const UnitPlace& a, int64_t left, UnitRows& r) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t unit = unit0 + i, t = unit >> p.hkv_shift;
-    const int g = static_cast<int>(unit) & (hkv - 1);
     r.q0[i] = r.q1[i] = r.k[i] = r.v[i] = make_uint2(0u, 0u);
     r.slot[i] = -1;
-    if (unit < p.units) {
-      const uint16_t* qr = p.q + t * p.q_stride + 2 * g * kHeadDim + 4 * lane;
-      r.q0[i] = load_row8(qr);
-      r.q1[i] = load_row8(qr + kHeadDim);
-      r.k[i] = load_row8(p.k + t * p.k_stride + g * kHeadDim + 4 * lane);
-      r.v[i] = load_row8(p.v + t * p.v_stride + g * kHeadDim + 4 * lane);
-      r.slot[i] = p.slots[t];
+    if (i * a.slot_step < left) {
+      const uint16_t* q = a.q + (i ? a.q_step : 0);
+      r.q0[i] = load_row8(q);
+      r.q1[i] = load_row8(q + kHeadDim);
+      r.k[i] = load_row8(a.k + (i ? a.k_step : 0));
+      r.v[i] = load_row8(a.v + (i ? a.v_step : 0));
+      r.slot[i] = a.slot[i ? a.slot_step : 0];
     }
   }
 }
@@ -196,8 +205,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_append_kernel(const
   const int tokens = kUnits >> p.hkv_shift;           // tokens of a pass: whole ones (hkv <= 8)
   const int chunk = kTableTokens / tokens;            // passes of a table
   const int64_t first = static_cast<int64_t>(blockIdx.x) * passes_per_cta * kUnits;
+  const bool past = sign == 0.f;
+  UnitPlace at;
+  int64_t left;  // tokens from this warp's first one on
+  const int g = u & (hkv - 1);  // (one KV head: the second unit is the next token's)
+  {
+    const int64_t t = (first + u) >> p.hkv_shift;
+    left = (p.units >> p.hkv_shift) - t;
+    at.q = p.q + t * p.q_stride + 2 * g * kHeadDim + 4 * lane;
+    at.k = p.k + t * p.k_stride + g * kHeadDim + 4 * lane;
+    at.v = p.v + t * p.v_stride + g * kHeadDim + 4 * lane;
+    at.out = p.q_out + (t * (2 * hkv) + 2 * g) * kHeadDim + 4 * lane;
+    at.slot = p.slots + t;
+    at.q_step = hkv == 1 ? p.q_stride : 2 * kHeadDim;
+    at.k_step = hkv == 1 ? p.k_stride : kHeadDim;
+    at.v_step = hkv == 1 ? p.v_stride : kHeadDim;
+    at.out_step = 2 * kHeadDim;
+    at.slot_step = hkv == 1 ? 1 : 0;
+  }
+  const int64_t q_pass = tokens * p.q_stride, k_pass = tokens * p.k_stride, v_pass = tokens * p.v_stride;
+  uint16_t* const k_out = p.k_pool + g * kHeadDim + 4 * lane;
+  uint16_t* const v_out = p.v_pool + g * kHeadDim + 4 * lane;
+  const int unit_head = hkv == 1 ? 0 : kHeadDim;  // from unit 0's head in a slot to unit 1's
   UnitRows rows;
-  load_units(p, first + u, lane, rows);
+  load_units(at, left, rows);
+  const int j = tid & (kMaxPairs - 1);  // this thread's frequency in the tables (kThreads is a multiple)
+  const unsigned long long turn = j < pairs ? turn_fraction(p.inv_freq[j]) : 0;
   for (int pass = 0; pass < passes_per_cta; ++pass) {
     const int64_t unit0 = first + static_cast<int64_t>(pass) * kUnits;
     if (unit0 >= p.units) break;
@@ -206,10 +239,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_append_kernel(const
       const int n = min(chunk, passes_per_cta - pass) * tokens;
       for (int i = tid; i < n * kMaxPairs; i += kThreads) {
         const int64_t t = (unit0 >> p.hkv_shift) + (i >> 6);
-        const int j = i & (kMaxPairs - 1);
         if (j < pairs && (t << p.hkv_shift) < p.units) {
           const long long pos = p.positions[t];
-          const unsigned long long phase = static_cast<unsigned long long>(pos) * turn_fraction(p.inv_freq[j]);
+          const unsigned long long phase = static_cast<unsigned long long>(pos) * turn;
           // the signed upper half: [-1/2, 1/2) turns, in half turns for sincospif
           const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * (1.0f / 2147483648.0f);
           float sn, cs;
@@ -221,7 +253,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_append_kernel(const
       __syncthreads();
     }
     const UnitRows cur = rows;
-    if (pass + 1 < passes_per_cta) load_units(p, unit0 + kUnits + u, lane, rows);
+    uint16_t* const out = at.out;
+    if (pass + 1 < passes_per_cta) {
+      at.q += q_pass;
+      at.k += k_pass;
+      at.v += v_pass;
+      at.slot += tokens;
+      at.out += tokens * (2 * hkv * kHeadDim);
+      left -= tokens;
+      load_units(at, left, rows);
+    }
     // the norms of the warp's six rows together: six independent sums a reduction step
     float inv[6] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
     if (p.q_gamma != nullptr || p.k_gamma != nullptr) {
@@ -264,20 +305,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_append_kernel(const
         fq = factors<kInterleaved>(p.q_gamma, lane, partner, sign, cs, sn);
         fk = factors<kInterleaved>(p.k_gamma, lane, partner, sign, cs, sn);
       }
-      const uint2 q0r = turn_row<kInterleaved>(cur.q0[i], inv[3 * i], partner, sign, fq);
-      const uint2 q1r = turn_row<kInterleaved>(cur.q1[i], inv[3 * i + 1], partner, sign, fq);
-      const uint2 k0r = turn_row<kInterleaved>(cur.k[i], inv[3 * i + 2], partner, sign, fk);
+      const uint2 q0r = turn_row<kInterleaved>(cur.q0[i], inv[3 * i], partner, past, fq);
+      const uint2 q1r = turn_row<kInterleaved>(cur.q1[i], inv[3 * i + 1], partner, past, fq);
+      const uint2 k0r = turn_row<kInterleaved>(cur.k[i], inv[3 * i + 2], partner, past, fk);
       const int64_t slot = cur.slot[i];  // negative: a padding row, nothing is written
       if (slot >= p.num_slots && lane == 0) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
       if (slot >= 0 && slot < p.num_slots) {
-        const int64_t unit = unit0 + u + i, t = unit >> p.hkv_shift;
-        const int g = static_cast<int>(unit) & (hkv - 1);
-        uint16_t* qo = p.q_out + (t * (2 * hkv) + 2 * g) * kHeadDim + 4 * lane;
+        uint16_t* qo = out + i * at.out_step;
         *reinterpret_cast<uint2*>(qo) = q0r;
         *reinterpret_cast<uint2*>(qo + kHeadDim) = q1r;
-        const int64_t at = (slot * hkv + g) * kHeadDim + 4 * lane;
-        *reinterpret_cast<uint2*>(p.k_pool + at) = k0r;
-        *reinterpret_cast<uint2*>(p.v_pool + at) = cur.v[i];
+        const int64_t to = slot * (hkv * kHeadDim) + i * unit_head;
+        *reinterpret_cast<uint2*>(k_out + to) = k0r;
+        *reinterpret_cast<uint2*>(v_out + to) = cur.v[i];
       }
     }
   }
