@@ -518,6 +518,19 @@ __device__ __forceinline__ void repair_row(const P& p, const PieceDesc& d, int r
   for (int k = 0; k < 4; ++k) acc[k] *= scale_o;
 }
 
+// tc::tmem_ld32_max with the maximum of the magnitudes.
+__device__ __forceinline__ void tmem_ld32_absmax(uint32_t taddr, uint32_t (&r)[32], float& mx) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
+      "%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(mx)
+      : "r"(taddr));
+}
+
 // softcap * tanh of a pair of raw products as s P(s^2), plus `add` (log2 units).
 struct CapPoly {
   float2 k2[kTanhTerms];
@@ -945,7 +958,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
         float cm[4];          // the maximum of each 32-column piece (of magnitudes with a cap)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if constexpr (P::kCap) tc::tmem_ld32_absmax(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
+          if constexpr (P::kCap) tmem_ld32_absmax(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
           else tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
         }
         tc::tmem_wait_ld();
