@@ -60,7 +60,7 @@ constexpr int kMaxGrid = 512;
 constexpr uint32_t kBlockBytes = 128 * 128;  // 128 rows x 64 bf16 (one swizzled 64-dim block)
 constexpr uint32_t kTileBytes = 2 * kBlockBytes;
 constexpr float kRescaleThreshold = 8.0f;
-constexpr float kMaxSlack = 100.0f;  // log2 units: how far a bound taken for the max may be above it
+constexpr float kMaxSlack = 80.0f;  // log2 units: how far a bound taken for the max may be above it
 constexpr int kMaxBatch = 128;
 constexpr int kVStages = 3;   // V is needed a whole P*V later than K: one more stage in flight
 // Fixed cost of a job beyond its key tiles, in tiles (its epilogue and the restart of its chain)
@@ -583,7 +583,7 @@ __device__ __forceinline__ void piece_max(const uint32_t (&sb)[kTileN], float (&
 // each 32-column piece (magnitude with a cap). cap tanh(max |s|) bounds capped scores, and their max
 // is at least its negative; the distance of a piece's nearest column bounds its bias, which falls by
 // 31 slopes over the piece. The exponents' reference may be above the max by up to kMaxSlack: the
-// weights that matter then stay 2^-26 above fp32's smallest normal number. d0: bias distance of
+// weights that matter then stay 2^46 above fp32's smallest normal number. d0: bias distance of
 // column 0.
 template <class P>
 __device__ __forceinline__ bool score_bound(const P& p, const RowMask& rm, int k0, float slope2, const float (&cm)[4],

@@ -27,7 +27,7 @@ struct ScoreParams {
   int32_t max_prefix;
   const int32_t* row_start;  // [rows] or null
   // softcap * log2 e * tanh(q_scale * s) of a raw product s as an odd polynomial s P(s^2), for
-  // |s| <= poly_max (|q_scale s| <= 1; 0: not usable)
+  // |s| <= poly_max (|q_scale s| <= 1; 0: not usable: scores are then capped one by one)
   float poly[7], poly_max;
 };
 
@@ -67,7 +67,8 @@ inline ScoreParams score_params(const pa_score_opts& o, float softmax_scale, flo
   *q_scale = o.softcap > 0.f ? softmax_scale / o.softcap : softmax_scale * kLog2e;
   s.poly_max = 0.f;
   const double x = *q_scale;
-  if (o.softcap > 0.f && x >= 0x1p-10 && x <= 0x1p10) {  // the folded coefficients stay in range
+  // the folded coefficients, down to softcap x^13 and up to softcap x, stay in fp32's range
+  if (o.softcap > 0.f && o.softcap <= 1e6f && x >= 0x1p-10 && x <= 0x1p4) {
     double a = static_cast<double>(s.cap_log2) * x;
     for (int k = 0; k < kTanhTerms; ++k, a *= x * x) s.poly[k] = static_cast<float>(tanh_coefficient(k) * a);
     s.poly_max = static_cast<float>(1.0 / x);

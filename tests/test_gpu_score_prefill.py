@@ -329,3 +329,29 @@ def test_rows_that_see_no_key_of_a_tile(cuda_lib, o):
         assert torch.equal(lse[later], clean[1][later]) or cap is not None
         first = [r for r in range(n) if start[r] == 0]
         assert bool(out[first].isnan().all())
+
+
+@pytest.mark.parametrize("o,scale", [
+    (dict(softcap=1e4), None), (dict(softcap=1e20), None), (dict(softcap=1e-4), None),
+    (dict(softcap=200.0, slopes=SLOPES), None), (dict(softcap=30.0), 1e-4), (dict(softcap=30.0), 3.0),
+    (dict(slopes=-0.1 * SLOPES, window=100), None), (dict(slopes=-0.3 * SLOPES, softcap=20.0), None),
+    (dict(slopes=np.where(np.arange(16) % 2, 9.0, 0.0)), None),
+])
+def test_caps_scales_and_slopes_far_from_the_usual(cuda_lib, o, scale):
+    """A cap far above the scores is no cap (not a loss of their low bits), one far below makes all
+    weights equal; scores of every size, slopes of either sign and steep ones."""
+    q_lens, offs = np.array([140, 33]), np.array([200, 0])
+    inp = W.make_paged(69, offs + q_lens, q_lens, device="cuda", q_scale=2.0)
+    if scale is not None:
+        inp.scale = scale
+    check(cuda_lib, inp, o)
+    d = W.make_paged(70, [400, 33], [1, 1], device="cuda", q_scale=2.0)
+    if scale is not None:
+        d.scale = scale
+    for split in (0, 32):
+        out, lse = cuda_lib.attn_decode_paged(
+            d.q[0], d.k_pools[0], d.v_pools[0], d.block_table, d.seq_lens, 400, d.scale,
+            split_tokens=split, softcap=o.get("softcap", 0.0), window=o.get("window", 0),
+            alibi_slopes=None if o.get("slopes") is None else dev(o["slopes"], torch.float32))
+        close(out, lse, *S.decode_scored(bits(d.q[0]), bits(d.k_pools[0]), bits(d.v_pools[0]),
+                                         d.host_block_table, d.host_seq_lens, d.scale, **o))
