@@ -1,7 +1,8 @@
 """GB300-native paged GQA attention: Python binding of ``libpagedattn.so``.
 
-Thin ctypes marshalling over the C ABI in ``include/pagedattn.h``: every computation runs in
-the library's CUDA kernels. PyTorch only provides device memory and streams. There is no CPU
+Thin ctypes marshalling over the C ABI in ``include/pagedattn.h``, with a compiled fast path for the
+calls of a serving step (``csrc/fastcall.cpp``): every computation runs in the library's CUDA
+kernels. PyTorch only provides device memory and streams. There is no CPU
 or fallback path: if the shared library has not been built, ``load()`` raises.
 
 Calls (same names as the C ABI):
@@ -18,6 +19,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -43,6 +45,7 @@ DEV_ERR_NO_PAGES = 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
+_FAST = None  # the fast path's module (csrc/fastcall.cpp), once the library is loaded and if it is there
 
 
 def lib_path() -> str:
@@ -144,7 +147,7 @@ _SIGS = {
 
 def load():
     """Load the built library (raises if it is missing: there is no fallback)."""
-    global _LIB
+    global _LIB, _FAST
     if _LIB is None:
         path = lib_path()
         if not os.path.exists(path):
@@ -156,7 +159,22 @@ def load():
             fn.restype = res
             fn.argtypes = args
         _LIB = lib
+        _FAST = _load_fast()
     return _LIB
+
+
+def _load_fast():
+    """The fast path, if it was built for this PyTorch; None otherwise."""
+    path = os.path.join(_HERE, "_lib", "_pa_call.so")
+    if not os.path.exists(path):
+        return None
+    try:
+        spec = importlib.util.spec_from_file_location("_pa_call", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError:
+        return None
+    return mod if mod.torch_version.split("+")[0] == torch.__version__.split("+")[0] else None
 
 
 # ----------------------------------------------------------------------------------------------
@@ -215,6 +233,11 @@ def _need(t, name, dtype, ndim=None):
         raise ValueError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+
+
+def _handle(stream):
+    """A stream's handle for the fast path (None: the current stream)."""
+    return None if stream is None else stream.cuda_stream
 
 
 def _check(call, code):
@@ -422,6 +445,12 @@ def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int
     or max(row_start[b], i - window + 1) <= j <= i; its score is softcap * tanh(s / softcap) minus
     alibi_slopes[h] * |i - j|. max_prefix_len: host bound of prefix_lens (default max_seq_len)."""
     call = "attn_decode_paged"
+    if _FAST is not None and workspace is None and out is not None and (lse is not None
+                                                                        or not want_lse):
+        if _FAST.decode(q, k_pool, v_pool, block_table, seq_lens, max_seq_len, softmax_scale,
+                        split_tokens, out, lse, status, _handle(stream), dims, max_ctas, softcap,
+                        alibi_slopes, window, prefix_lens, max_prefix_len, row_start):
+            return out, lse
     dev = _device(call, q, "q", torch.bfloat16)
     pq = _tensor(call, q, "q", torch.bfloat16, dev)
     pk = _tensor(call, k_pool, "k_pool", torch.bfloat16, dev)
@@ -529,6 +558,12 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
     (attn_prefill_chunk_score; a workspace passed in then has prefill_score_workspace_size
     bytes)."""
     call = "attn_prefill_chunk"
+    if _FAST is not None and workspace is None and out is not None and (lse is not None
+                                                                        or not want_lse):
+        if _FAST.prefill(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_q_len, max_seq_len,
+                         softmax_scale, out, lse, status, _handle(stream), dims, max_ctas, softcap,
+                         alibi_slopes, window, prefix_lens, max_prefix_len, row_start):
+            return out, lse
     dev = _device(call, q, "q", torch.bfloat16)
     pq = _tensor(call, q, "q", torch.bfloat16, dev)
     pcu = _tensor(call, cu_q_lens, "cu_q_lens", torch.int32, dev)
@@ -639,6 +674,10 @@ def paged_step_plan(cached_lens, new_lens, block_table, free_pages, free_count, 
     that the free pages do not cover are left as they are (their rows get slot -1,
     DEV_ERR_NO_PAGES). free_count_out may be free_count, seq_lens may be cached_lens."""
     call, i32 = "paged_step_plan", torch.int32
+    if _FAST is not None and _FAST.step_plan(
+            cached_lens, new_lens, block_table, free_pages, free_count, num_pages, total_rows,
+            free_count_out, cu_new_lens, seq_lens, positions, slot_map, status, _handle(stream)):
+        return StepPlan(cu_new_lens, seq_lens, positions, slot_map, free_count_out)
     dev = _device(call, cached_lens, "cached_lens", i32)
     pc = _tensor(call, cached_lens, "cached_lens", i32, dev)
     pn = _tensor(call, new_lens, "new_lens", i32, dev)
@@ -678,6 +717,9 @@ def paged_release(begin_pages, end_pages, block_table, free_pages, free_count, n
     free_pages and set their block_table entries to -1 (entries that are -1 are skipped).
     Returns the new free count [1] (free_count_out, which may be free_count)."""
     call, i32 = "paged_release", torch.int32
+    if _FAST is not None and _FAST.release(begin_pages, end_pages, block_table, free_pages, free_count,
+                                           num_pages, free_count_out, status, _handle(stream)):
+        return free_count_out
     dev = _device(call, begin_pages, "begin_pages", i32)
     pb = _tensor(call, begin_pages, "begin_pages", i32, dev)
     pe = _tensor(call, end_pages, "end_pages", i32, dev)
@@ -753,6 +795,10 @@ def rope_append_paged(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_
     alone). Returns q_out [T, Hq, 128]. rot_dim is 2 * len(inv_freq); rows of q, k_new and v_new
     may be strided (slices of one projection)."""
     call = "rope_append_paged"
+    if _FAST is not None and _FAST.rope(
+            q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq, 1 if interleaved else 0,
+            attn_factor, q_gamma, k_gamma, eps, q_out, status, _handle(stream), dims):
+        return q_out
     dev = _device(call, q, "q", torch.bfloat16)
     hq, hkv = _heads(dims) or tuple(dims[:2])  # (other shapes: the library rejects them)
     T = q.shape[0] if q.dim() else 0

@@ -1,7 +1,9 @@
 """Build the CUDA library ``_lib/libpagedattn.so`` in-tree with nvcc (sm_103a only).
 
 Each ``csrc/*.cu`` translation unit is compiled to an object in parallel, then linked into
-one shared library that exports the C ABI declared in ``include/pagedattn.h``.
+one shared library that exports the C ABI declared in ``include/pagedattn.h``. Beside it,
+``_lib/_pa_call.so`` is the Python binding's fast path (``csrc/fastcall.cpp``, host C++ against the
+installed PyTorch's headers). The binding does without it where it cannot be built.
 """
 from __future__ import annotations
 
@@ -9,6 +11,8 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libpagedattn.so")
 INCLUDE = os.path.join(ROOT, "include")
+FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
+FAST = os.path.join(LIB_DIR, "_pa_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -44,6 +50,40 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_fast(verbose: bool, force: bool):
+    """Compile the binding's fast path; returns its error text, or None. Rebuilt when its source, the
+    C ABI or the installed PyTorch changed."""
+    import torch
+    stamp = os.path.join(BUILD, "_pa_call.torch")
+    known = open(stamp).read() if os.path.exists(stamp) else ""
+    if not force and known == torch.__version__ and not _stale(FAST, [FAST_SRC, __file__] + _headers()):
+        return None
+    if os.path.exists(FAST):
+        os.remove(FAST)
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = FAST + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-I", INCLUDE,
+           "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", FAST_SRC, "-o", tmp,
+           "-L", LIB_DIR, "-lpagedattn", "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return str(e)
+    if r.returncode != 0:
+        return r.stderr[-2000:]
+    os.replace(tmp, FAST)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return None
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
@@ -76,6 +116,10 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         tmp = LIB + ".tmp"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    error = _build_fast(verbose, force)
+    if error is not None:
+        print(f"the binding's fast path was not built, calls take its slower one: {error}",
+              file=sys.stderr)
     return LIB
 
 

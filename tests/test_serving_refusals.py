@@ -131,3 +131,18 @@ def test_score_options(lib):
                                        None, 0, None, None, ctypes.byref(bad_cap), None) == INVALID
     assert lib.attn_prefill_chunk_score(pa.Dims(16, 4, 128, 16), None, None, 1, None, None, 1, None, 1, None,
                                         1, 1, 16, 1.0, None, None, None, 0, None, None, None, None) == UNSUPPORTED
+
+
+def test_fast_path_takes_nothing_without_a_gpu(lib):
+    """Whatever it is given, the compiled path answers False, never an exception: the binding's own
+    checks name the error."""
+    import torch
+
+    import long_context_paged_gb300 as pa
+    fast = pa._FAST
+    assert fast is not None, "the fast path was not built"
+    t = torch.zeros(4, dtype=torch.int32)
+    for f in (fast.decode, fast.prefill, fast.rope, fast.step_plan, fast.release):
+        for n in range(24):
+            for x in (None, t, 1, -1, 1 << 70, 0.5, "x", (16, 8, 128, 16)):
+                assert f(*[x] * n) is False
