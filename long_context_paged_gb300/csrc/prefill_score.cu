@@ -283,6 +283,7 @@ __device__ PieceDesc whole_job(const P& p, int lane) {
 // reduced by the lanes), a scan of their units, and the balanced split of the work.
 template <class P>
 __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const P p, int G) {
+  await_previous();
   asm volatile("griddepcontrol.launch_dependents;");  // its CTAs wait for this grid's completion
   __shared__ long long warp_sums[kPlanThreads / 32];
   __shared__ int32_t first_tile[kMaxBatch + 1];
@@ -1322,12 +1323,12 @@ pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUten
     configured_device = dev;
   }
   if (p.whole_only) {
-    prefill_score_kernel<P><<<p.max_tiles * p.hkv, kThreads, smem, stream>>>(qm, km, vm, p);
-    PA_CHECK_LAUNCH("prefill_score_kernel");
-    return PA_OK;
+    const cudaError_t e = launch_dependent(prefill_score_kernel<P>, static_cast<unsigned>(p.max_tiles * p.hkv),
+                                           kThreads, smem, stream, 0, qm, km, vm, p);
+    return e == cudaSuccess ? PA_OK : record_cuda_error(e, "prefill_score_kernel");
   }
-  prefill_plan_kernel<P><<<1, kPlanThreads, 0, stream>>>(p, grid);
-  PA_CHECK_LAUNCH("prefill_plan_kernel");
+  cudaError_t e = launch_dependent(prefill_plan_kernel<P>, 1, kPlanThreads, 0, stream, 0, p, grid);
+  if (e != cudaSuccess) return record_cuda_error(e, "prefill_plan_kernel");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
@@ -1338,7 +1339,7 @@ pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_score_kernel<P>, qm, km, vm, p);
+  e = cudaLaunchKernelEx(&cfg, prefill_score_kernel<P>, qm, km, vm, p);
   if (e != cudaSuccess) return record_cuda_error(e, "prefill_score_kernel");
   cfg.gridDim = dim3((max_q_len + kTileM - 1) / kTileM, p.hkv * 8, p.batch);
   cfg.blockDim = dim3(kMergeRows);

@@ -6,8 +6,8 @@
 // the pair being dims (i, i + rot / 2) or, interleaved, (2i, 2i + 1); before it, q and k rows may
 // be RMS-normalised per head: x / sqrt(mean x^2 + eps) * gamma. One pass in fp32, one rounding
 // to bf16 at the end. The bound is memory: every q, k and v row is read once and written once
-// (16 KB per token of the 16/8-head decoder). Measured inside a graph: 4,127 rows with norms 13.4 us
-// (5.0 TB/s), 31 rows 2.6 us. At 8 dims of a row per lane instead of 4, loads in the same pass and a
+// (16 KB per token of the 16/8-head decoder). Measured inside a graph: 4,127 rows with norms 13.2 us
+// (5.1 TB/s), 31 rows 2.6 us. At 8 dims of a row per lane instead of 4, loads in the same pass and a
 // barrier per pass the first form took 21 us; now instruction issue (63 %) and memory are both near.
 //
 // The angle. At position 100,000 an fp32 product position * inv_freq is off by up to 0.004 rad,
@@ -40,7 +40,7 @@ constexpr int kUnits = kThreads / 16;       // units of a CTA pass: two a warp
 constexpr int kMaxPairs = kHeadDim / 2;
 constexpr int kTableTokens = 32;            // tokens whose cosines and sines are held at a time
 // Two CTAs per SM: a pass in flight and one ahead of it for every warp, at 122 registers. Three or four
-// CTAs of 80 or 64 registers spill and measured slower (16.8 and 24.1 against 13.4 us for 4,127 rows).
+// CTAs of 80 or 64 registers spill and measured slower (16.8 and 24.1 against 13.2 us for 4,127 rows).
 constexpr int kCtasPerSm = 2;
 
 struct RopeParams {
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_append_kernel(const
   uint16_t* const v_out = p.v_pool + g * kHeadDim + 4 * lane;
   const int unit_head = hkv == 1 ? 0 : kHeadDim;  // from unit 0's head in a slot to unit 1's
   UnitRows rows;
+  await_previous();
   load_units(at, left, rows);
   const int j = tid & (kMaxPairs - 1);  // this thread's frequency in the tables (kThreads is a multiple)
   const unsigned long long turn = j < pairs ? turn_fraction(p.inv_freq[j]) : 0;
@@ -386,10 +387,9 @@ extern "C" pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t in
   const int per_cta = static_cast<int>((passes + most - 1) / most);
   const unsigned grid = static_cast<unsigned>((passes + per_cta - 1) / per_cta);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (interleaved) rope_append_kernel<true><<<grid, kThreads, 0, st>>>(p, per_cta);
-  else rope_append_kernel<false><<<grid, kThreads, 0, st>>>(p, per_cta);
-  PA_CHECK_LAUNCH("rope_append_kernel");
-  return PA_OK;
+  const cudaError_t e = launch_dependent(interleaved ? rope_append_kernel<true> : rope_append_kernel<false>,
+                                         grid, kThreads, 0, st, 0, p, per_cta);
+  return e == cudaSuccess ? PA_OK : record_cuda_error(e, "rope_append_kernel");
 }
 
 extern "C" pa_status pa_rope_inv_freq(int32_t rot_dim, double theta, const pa_rope_scaling* scaling,

@@ -15,7 +15,7 @@
 // thread at most) and then writes its share of the rows, so that nothing is exchanged between
 // CTAs. Where an output is an input's buffer (lengths or free count updated in place), the grid is one
 // cluster of at most 8 CTAs, whose barrier orders the reads before the writes; else any grid does
-// (57,000 rows: 8.7 us, in place 11.6 us).
+// (57,000 rows: 8.4 us, in place 11.6 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -32,7 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxCluster = 8;
 // Rows (or requests) one CTA takes before a second one is launched. 512 to 4,096 measure alike (4,096
-// requests with 57,000 rows 8.7 us, 32 requests with 4,127 rows 5.3 us): the chain of loads, scan and
+// requests with 57,000 rows 8.4 us, 32 requests with 4,127 rows 5.0 us): the chain of loads, scan and
 // stores is what takes the time.
 constexpr int kRowsPerCta = 2048;
 
@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
   const bool report = rank == 0;
   const int capacity = p.bt_stride * kPage;  // < 2^31: checked on the host
 
+  await_previous();
   const int free_count = read_free_count(p.free_count, p.free_capacity, p.status, report && tid == 0);
   const int per = (p.batch + kThreads - 1) / kThreads;  // <= 4
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParam
   __shared__ int32_t cta_count[kMaxCluster];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  await_previous();
   const int free_count = read_free_count(p.free_count, p.free_capacity, p.status, rank == 0 && tid == 0);
   // this warp's requests: a contiguous share, so that the pushes of all warps are in order
   const int w = rank * kWarps + warp, all = ctas * kWarps;
@@ -367,19 +369,7 @@ int cluster_of(int64_t work, int64_t per_cta) {
 template <class Params>
 pa_status launch_cluster(void (*kernel)(Params), const Params& p, int ctas, size_t smem,
                          cudaStream_t stream, const char* name) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = launch_dependent(kernel, static_cast<unsigned>(ctas), kThreads, smem, stream, ctas, p);
   return e == cudaSuccess ? PA_OK : record_cuda_error(e, name);
 }
 
@@ -427,9 +417,8 @@ extern "C" pa_status paged_step_plan(const int32_t* cached_lens, const int32_t* 
   const int sms = sm_count_current_device();
   if (sms <= 0) return PA_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(sms, std::max<int64_t>(1, (work + kRowsPerCta - 1) / kRowsPerCta)));
-  step_plan_kernel<<<grid, kThreads, sizeof(PlanSmem), st>>>(p);
-  PA_CHECK_LAUNCH("step_plan_kernel");
-  return PA_OK;
+  const cudaError_t e = launch_dependent(step_plan_kernel, grid, kThreads, sizeof(PlanSmem), st, 0, p);
+  return e == cudaSuccess ? PA_OK : record_cuda_error(e, "step_plan_kernel");
 }
 
 extern "C" pa_status paged_release(const int32_t* begin_pages, const int32_t* end_pages, int32_t batch,
