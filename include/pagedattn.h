@@ -281,6 +281,7 @@ pa_status attn_prefill_chunk_ex(pa_dims dims, const void* q, const int32_t* cu_q
  *                   are cut and flagged PA_DEV_ERR_LENGTH; 0: no prefix
  *   row_start       int32 on the device, per query row ([batch] / [total_q]), or NULL: first key
  *                   of the row's document; past i: the row sees the prefix only
+ * A chunk longer than max_q_len is flagged PA_DEV_ERR_LENGTH and produces nothing.
  * attn_prefill_chunk_score takes its workspace size from pa_prefill_score_workspace_size; the
  * decode's is pa_decode_workspace_size. Scores without options give what the plain call gives
  * up to rounding.
@@ -365,7 +366,8 @@ pa_status attn_merge_lse(int32_t num_parts, int32_t rows, int32_t heads, int32_t
  * appended to the free list in (request, page) order and become -1 in the table; entries that are
  * -1 already are skipped. (0, ceil(seq_len / 16)) gives back a finished request, a range in the
  * middle what a sliding window has left behind. If the list has no room for all of them nothing is
- * released (PA_DEV_ERR_LENGTH). Each page must be held by one request only.
+ * released (PA_DEV_ERR_LENGTH). Each page must be held by one request only. A table of 2^31 entries
+ * or more is PA_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------------------------ */
 pa_status paged_step_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
                           int32_t* block_table, int32_t bt_stride, const int32_t* free_pages,

@@ -179,8 +179,10 @@ __device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.f ? 0.
 template <class P>
 __device__ __forceinline__ float lse_shift(const P& p, int b, int h) {
   if constexpr (P::kScore) {
-    if (p.score.slopes != nullptr && p.score.row_start != nullptr)
-      return -p.score.slopes[h] * static_cast<float>(seq_view(p, b, false).nearest());
+    if (p.score.slopes != nullptr && p.score.row_start != nullptr) {
+      const auto v = seq_view(p, b, false);  // (an empty row's -inf stays that, whatever the slope)
+      if (v.pages > 0) return -p.score.slopes[h] * static_cast<float>(v.nearest());
+    }
   }
   return 0.f;
 }

@@ -117,7 +117,7 @@ struct PrefillScoreParams {
   float* lse;
   int32_t* status;
   ScoreParams score;
-  int32_t total_q, max_tiles;
+  int32_t total_q, max_tiles, max_q_len;
   bool whole_only;           // a CTA per job: nothing is split, and neither plan nor merge is needed
   const uint16_t* q_rows;    // the operands, for repair_row
   const uint16_t* k_rows;
@@ -149,7 +149,8 @@ __device__ __forceinline__ long long block_scan_incl(long long v, long long* war
 }
 
 // A chunk's first packed row, rows, keys and prefix, and its query tiles: none for an empty chunk, and
-// none (flagged) for one that does not fit its sequence, its table row or the packing.
+// none (flagged) for one that does not fit its sequence, its table row, the packing or the host's bound
+// (which the merge's grid is sized by).
 struct Chunk {
   int32_t q0, n, L, prefix, tiles;
 };
@@ -161,7 +162,7 @@ __device__ __forceinline__ Chunk chunk_of(const P& p, int b, bool report) {
   c.L = p.seq_lens[b];
   c.tiles = c.prefix = 0;
   if (c.n <= 0) return c;
-  if (c.n > c.L || c.L > p.bt_stride * kPage || c.q0 < 0 || c.n > p.total_q - c.q0) {
+  if (c.n > c.L || c.n > p.max_q_len || c.L > p.bt_stride * kPage || c.q0 < 0 || c.n > p.total_q - c.q0) {
     if (report) flag_error(p.status, PA_DEV_ERR_LENGTH);
     return c;
   }
@@ -1112,7 +1113,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
           if (p.lse != nullptr) {
             float v = none ? -CUDART_INF_F : (m_used + log2f(l)) * kLn2;
             if constexpr (P::kBias) {
-              if (rm.nearest > 0) v -= p.score.slopes[head] * static_cast<float>(rm.nearest);
+              if (!none && rm.nearest > 0) v -= p.score.slopes[head] * static_cast<float>(rm.nearest);
             }
             p.lse[static_cast<int64_t>(desc.q0 + qrow) * p.hq + head] = v;
           }
@@ -1261,7 +1262,7 @@ __global__ void __launch_bounds__(kMergeRows) prefill_score_merge_kernel(const P
     float v = m + logf(sum);
     if constexpr (P::kBias) {  // distances were counted from the nearest visible key
       const int pos = d.off + qrow;
-      if (score_first_key(p.score, q0 + qrow, pos) > pos)
+      if (sum != 0.f && score_first_key(p.score, q0 + qrow, pos) > pos)
         v -= p.score.slopes[head] * static_cast<float>(max(0, pos + 1 - d.prefix));
     }
     p.lse[static_cast<int64_t>(q0 + qrow) * p.hq + head] = v;
@@ -1298,7 +1299,7 @@ int score_grid() { return std::min(sm_count_current_device(), kMaxGrid); }
 // Plan, attention and merge of one call; each is a programmatic dependent of the one before.
 template <class P>
 pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const P& p,
-                       int grid, int max_q_len, cudaStream_t stream) {
+                       int grid, cudaStream_t stream) {
   const int smem = static_cast<int>(sizeof(ScoreSmem));
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -1341,7 +1342,7 @@ pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUten
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, prefill_score_kernel<P>, qm, km, vm, p);
   if (e != cudaSuccess) return record_cuda_error(e, "prefill_score_kernel");
-  cfg.gridDim = dim3((max_q_len + kTileM - 1) / kTileM, p.hkv * 8, p.batch);
+  cfg.gridDim = dim3((p.max_q_len + kTileM - 1) / kTileM, p.hkv * 8, p.batch);
   cfg.blockDim = dim3(kMergeRows);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, prefill_score_merge_kernel<P>, p);
@@ -1399,6 +1400,7 @@ pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, cons
     p.score = score_params(score, softmax_scale, &p.scale_log2);
     p.total_q = total_q;
     p.max_tiles = max_tiles;
+    p.max_q_len = max_q_len;
     p.whole_only = max_tiles * hkv <= grid && max_seq_len <= kWholeKeys;
     p.q_rows = static_cast<const uint16_t*>(q);
     p.k_rows = static_cast<const uint16_t*>(k_pool);
@@ -1409,7 +1411,7 @@ pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, cons
     p.ws_first_tile = reinterpret_cast<int32_t*>(ws + w.first_tile);
     p.ws_tail = reinterpret_cast<long long*>(ws + w.tail);
     p.ws_records = ws + w.records;
-    return launch_score(qm, km, vm, p, grid, max_q_len, stream);
+    return launch_score(qm, km, vm, p, grid, stream);
   };
   const bool cap = score.softcap > 0.f, bias = score.alibi_slopes != nullptr;
   return cap ? (bias ? run(PrefillScoreParams<true, true>()) : run(PrefillScoreParams<true, false>()))

@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
     const int b = last_at_most(s.need, p.batch + 1, free_count);
     used = s.need[b];
   }
-  for (int i = id; i < used; i += all) {
+  for (int64_t i0 = id; i0 < used; i0 += all) {
+    const int i = static_cast<int>(i0);
     const int b = last_at_most(s.need, p.batch, i);
     const int lp = pages_of(s.cached[b]) + (i - s.need[b]);
     p.block_table[static_cast<int64_t>(b) * p.bt_stride + lp] = p.free_pages[free_count - 1 - i];
@@ -192,7 +193,6 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
     if (total > p.total_rows) flag_error(p.status, PA_DEV_ERR_LENGTH);
   }
   // ---- per row: position and slot; rows of requests that wait, and rows past the last request,
-  //      are (0, -1)
   //      are (0, -1). Four consecutive rows a thread: one search (the next rows are mostly the same
   //      request's or the next one's), four page loads in flight, 16-byte stores.
   for (int64_t t0 = 4ll * id; t0 < p.total_rows; t0 += 4ll * all) {
@@ -431,6 +431,10 @@ extern "C" pa_status paged_release(const int32_t* begin_pages, const int32_t* en
     return PA_ERR_INVALID_ARG;
   if (batch > kMaxBatch) {
     snprintf_error("paged_release: at most %d requests per call", kMaxBatch);
+    return PA_ERR_UNSUPPORTED;
+  }
+  if (static_cast<int64_t>(batch) * bt_stride > 0x7fffffff) {  // the pages are counted in 32 bits
+    snprintf_error("paged_release: a table of %d x %d entries (2^31 and more are not supported)", batch, bt_stride);
     return PA_ERR_UNSUPPORTED;
   }
   if (!free_count || !free_count_out || (batch > 0 && (!begin_pages || !end_pages || !block_table)) ||

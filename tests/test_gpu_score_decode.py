@@ -228,3 +228,17 @@ def test_replayed_from_a_graph_with_new_lengths(cuda_lib):
                               inp.host_block_table, lens, inp.scale, softcap=10.0, window=512,
                               prefix=[40, 0])
         close(out, lse, *ref, what=str(lens))
+
+
+@pytest.mark.parametrize("lens", [[40, 900], [40, 50000]])
+@pytest.mark.parametrize("slope", [float("inf"), float("-inf"), float("nan")])
+def test_rows_without_keys_under_any_slope(cuda_lib, lens, slope):
+    inp = W.make_paged(71, lens, [1, 1], device="cuda")
+    slopes = torch.full((16,), 0.25, device="cuda")
+    slopes[5] = slope
+    out, lse = cuda_lib.attn_decode_paged(inp.q[0], inp.k_pools[0], inp.v_pools[0], inp.block_table,
+                                          inp.seq_lens, max(lens), inp.scale, alibi_slopes=slopes,
+                                          row_start=dev([0, lens[1]]))
+    assert bool((lse[1] == float("-inf")).all()) and not bool(out[1].any())
+    keep = [h for h in range(16) if h != 5]
+    assert bool(lse[0, keep].isfinite().all()) and bool(out[0, keep].isfinite().all())

@@ -355,3 +355,38 @@ def test_caps_scales_and_slopes_far_from_the_usual(cuda_lib, o, scale):
             alibi_slopes=None if o.get("slopes") is None else dev(o["slopes"], torch.float32))
         close(out, lse, *S.decode_scored(bits(d.q[0]), bits(d.k_pools[0]), bits(d.v_pools[0]),
                                          d.host_block_table, d.host_seq_lens, d.scale, **o))
+
+
+@pytest.mark.parametrize("off", [0, 3000])
+def test_chunks_longer_than_the_bound_are_flagged_and_left_alone(cuda_lib, off):
+    q_lens, lens = np.array([40, 300, 20]), np.array([40, 300, 20]) + off
+    inp = W.make_paged(69, lens, q_lens, device="cuda")
+    want = call(cuda_lib, inp, dict(window=500))
+    out = torch.full((360, 16, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cuda_lib.attn_prefill_chunk(inp.q[0], inp.cu_q_lens, inp.k_pools[0], inp.v_pools[0], inp.block_table,
+                                inp.seq_lens, 299, int(lens.max()), inp.scale, out=out, status=status,
+                                window=500)
+    assert cuda_lib.read_device_status(status) == cuda_lib.DEV_ERR_LENGTH
+    assert bool((out[40:340] == 9.0).all())
+    # (the split of the work differs, and with it the order of a row's sums: 2^-8 of a value in bf16,
+    # and the weights' roundings, as above)
+    for r in (slice(0, 40), slice(340, 360)):
+        a, b = out[r].double(), want[0][r].double()
+        assert bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + 6 * (2.0 ** -7 + 2.0 ** -12)).all())
+
+
+@pytest.mark.parametrize("off", [0, 3000])
+@pytest.mark.parametrize("slope", [float("inf"), float("-inf"), float("nan")])
+def test_rows_without_keys_under_any_slope(cuda_lib, off, slope):
+    n = 150
+    inp = W.make_paged(70, [off + n], [n], device="cuda")
+    start = np.zeros(n, int)
+    start[::3] = off + n                                          # rows that see nothing
+    slopes = SLOPES.copy()
+    slopes[5] = slope
+    for cap in (0.0, 20.0):
+        out, lse = call(cuda_lib, inp, dict(slopes=slopes, row_start=start, softcap=cap), max_ctas=7)
+        assert bool((lse[::3] == float("-inf")).all()) and not bool(out[::3].any())
+        keep = [h for h in range(16) if h != 5]
+        assert bool(lse[1::3][:, keep].isfinite().all()) and bool(out[1::3][:, keep].isfinite().all())

@@ -146,3 +146,8 @@ def test_fast_path_takes_nothing_without_a_gpu(lib):
         for n in range(24):
             for x in (None, t, 1, -1, 1 << 70, 0.5, "x", (16, 8, 128, 16)):
                 assert f(*[x] * n) is False
+
+
+def test_release_of_a_table_past_32_bit_counts(lib):
+    for batch, stride, want in ((64, 1 << 25, UNSUPPORTED), (4096, 1 << 19, UNSUPPORTED)):
+        assert lib.paged_release(A, A, batch, A, stride, A, 8, A, 64, A, None, None) == want
