@@ -40,32 +40,6 @@ int sm_count_current_device();
     if (e_ != cudaSuccess) return ::pa::record_cuda_error(e_, where); \
   } while (0)
 
-// A launch as a programmatic dependent of the work before it on the stream: it may be set up during
-// that work's tail, and its kernel starts with await_previous(), before any access to memory. Measured
-// against plain launches, calls in a row: 31 rotary rows 4.6 -> 3.8 us, 4,127 16.7 -> 14.4, a plan of
-// 32 requests 7.8 -> 5.8. (A kernel that in turn lets the next one start early gained nothing more.)
-template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
-                             cudaStream_t stream, int cluster, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ---------------------------------------------------------------------------------------------
 // Device status word.
 // ---------------------------------------------------------------------------------------------

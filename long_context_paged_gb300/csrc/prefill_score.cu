@@ -30,6 +30,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include "dependent_launch.cuh"
 #include "pa_common.cuh"
 #include "score_common.cuh"
 #include "tc_common.cuh"

@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "dependent_launch.cuh"
 #include "pa_common.cuh"
 
 namespace pa {

@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "cluster_common.cuh"
+#include "dependent_launch.cuh"
 #include "pa_common.cuh"
 
 namespace pa {
