@@ -240,6 +240,16 @@ def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
 
+def _attn_outputs(q, out, lse, want_lse, stream):
+    """out and lse of an attention call, new ones where they were not given (and q has a shape)."""
+    if isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3:
+        if out is None:
+            out = _empty(q.shape, torch.bfloat16, q.device, stream)
+        if lse is None and want_lse:
+            lse = _empty(q.shape[:2], torch.float32, q.device, stream)
+    return out, lse
+
+
 def _check(call, code):
     if code != 0:
         raise PagedAttnError(call, code)
@@ -445,12 +455,12 @@ def attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, max_seq_len: int
     or max(row_start[b], i - window + 1) <= j <= i; its score is softcap * tanh(s / softcap) minus
     alibi_slopes[h] * |i - j|. max_prefix_len: host bound of prefix_lens (default max_seq_len)."""
     call = "attn_decode_paged"
-    if _FAST is not None and workspace is None and out is not None and (lse is not None
-                                                                        or not want_lse):
+    if _FAST is not None:
+        o, l = _attn_outputs(q, out, lse, want_lse, stream)
         if _FAST.decode(q, k_pool, v_pool, block_table, seq_lens, max_seq_len, softmax_scale,
-                        split_tokens, out, lse, status, _handle(stream), dims, max_ctas, softcap,
+                        split_tokens, o, l, workspace, status, _handle(stream), dims, max_ctas, softcap,
                         alibi_slopes, window, prefix_lens, max_prefix_len, row_start):
-            return out, lse
+            return o, l
     dev = _device(call, q, "q", torch.bfloat16)
     pq = _tensor(call, q, "q", torch.bfloat16, dev)
     pk = _tensor(call, k_pool, "k_pool", torch.bfloat16, dev)
@@ -558,12 +568,12 @@ def attn_prefill_chunk(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_
     (attn_prefill_chunk_score; a workspace passed in then has prefill_score_workspace_size
     bytes)."""
     call = "attn_prefill_chunk"
-    if _FAST is not None and workspace is None and out is not None and (lse is not None
-                                                                        or not want_lse):
+    if _FAST is not None:
+        o, l = _attn_outputs(q, out, lse, want_lse, stream)
         if _FAST.prefill(q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_q_len, max_seq_len,
-                         softmax_scale, out, lse, status, _handle(stream), dims, max_ctas, softcap,
+                         softmax_scale, o, l, workspace, status, _handle(stream), dims, max_ctas, softcap,
                          alibi_slopes, window, prefix_lens, max_prefix_len, row_start):
-            return out, lse
+            return o, l
     dev = _device(call, q, "q", torch.bfloat16)
     pq = _tensor(call, q, "q", torch.bfloat16, dev)
     pcu = _tensor(call, cu_q_lens, "cu_q_lens", torch.int32, dev)
@@ -795,10 +805,12 @@ def rope_append_paged(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_
     alone). Returns q_out [T, Hq, 128]. rot_dim is 2 * len(inv_freq); rows of q, k_new and v_new
     may be strided (slices of one projection)."""
     call = "rope_append_paged"
-    if _FAST is not None and _FAST.rope(
-            q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq, 1 if interleaved else 0,
-            attn_factor, q_gamma, k_gamma, eps, q_out, status, _handle(stream), dims):
-        return q_out
+    if _FAST is not None:
+        o, _ = _attn_outputs(q, q_out, None, False, stream)
+        if _FAST.rope(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq,
+                      1 if interleaved else 0, attn_factor, q_gamma, k_gamma, eps, o, status,
+                      _handle(stream), dims):
+            return o
     dev = _device(call, q, "q", torch.bfloat16)
     hq, hkv = _heads(dims) or tuple(dims[:2])  # (other shapes: the library rejects them)
     T = q.shape[0] if q.dim() else 0

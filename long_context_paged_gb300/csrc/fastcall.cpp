@@ -70,6 +70,14 @@ struct Reader {
     if (good && !t->is_contiguous()) good = false;
     return good ? t->data_ptr() : nullptr;
   }
+  // A workspace: bytes on the device, or None.
+  const at::Tensor* bytes_or_none() {
+    if (i < n && a[i] == Py_None) {
+      ++i;
+      return nullptr;
+    }
+    return tensor(ScalarType::Byte, 1);
+  }
   long long integer() {
     PyObject* o = next();
     if (!PyLong_Check(o)) {
@@ -162,14 +170,23 @@ struct Unlocked {
   Unlocked& operator=(const Unlocked&) = delete;
 };
 
-// A workspace of the stream's own memory for the length of one call: given back as soon as the call is
-// launched, to be handed out again only to later work of the same stream.
+// A call's workspace: the caller's, or memory of the stream for the length of the call, given back as
+// soon as the call is launched, to be handed out again only to later work of the same stream.
 struct Scratch {
   void* p = nullptr;
-  Scratch(size_t bytes, cudaStream_t st) {
-    p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes < 256 ? 256 : bytes, st);
+  size_t bytes = 0;
+  bool own = false;
+  Scratch(const at::Tensor* given, size_t need, cudaStream_t st) {
+    if (given != nullptr) {
+      p = given->data_ptr();
+      bytes = given->nbytes();
+      return;
+    }
+    bytes = need < 256 ? 256 : need;
+    p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, st);
+    own = true;
   }
-  ~Scratch() { if (p != nullptr) c10::cuda::CUDACachingAllocator::raw_delete(p); }
+  ~Scratch() { if (own) c10::cuda::CUDACachingAllocator::raw_delete(p); }
   Scratch(const Scratch&) = delete;
   Scratch& operator=(const Scratch&) = delete;
 };
@@ -221,8 +238,8 @@ PyObject* guarded(F f) {
   return PyBool_FromLong(made);
 }
 
-// (q, k_pool, v_pool, block_table, seq_lens, max_seq_len, scale, split_tokens, out, lse, status,
-//  stream, dims, max_ctas, options)
+// (q, k_pool, v_pool, block_table, seq_lens, max_seq_len, scale, split_tokens, out, lse,
+//  workspace, status, stream, dims, max_ctas, options)
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> bool {
     Reader r(a, n);
@@ -236,6 +253,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t split = r.int32();
     const at::Tensor* out = r.tensor(ScalarType::BFloat16, 3);
     const at::Tensor* lse = r.tensor_or_none(ScalarType::Float, 2);
+    const at::Tensor* workspace = r.bytes_or_none();
     void* status = r.status();
     cudaStream_t st = r.stream();
     const pa_dims d = r.dims();
@@ -254,25 +272,25 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.shape(lse, B, hq);
     if (!r.done() || B > INT32_MAX || table->size(1) > INT32_MAX) return false;
     const int32_t batch = static_cast<int32_t>(B), stride = static_cast<int32_t>(table->size(1));
-    const size_t bytes = pa_decode_workspace_size(d, batch, max_len, split);
+    const size_t need = workspace ? 0 : pa_decode_workspace_size(d, batch, max_len, split);
     Unlocked unlocked;
-    Scratch scratch(bytes, st);
+    Scratch scratch(workspace, need, st);
     pa_stream_t s = reinterpret_cast<pa_stream_t>(st);
-    const size_t have = bytes < 256 ? 256 : bytes;
     if (scored)
       return attn_decode_paged_score(d, q->data_ptr(), k->data_ptr(), v->data_ptr(), k->size(0),
                                           ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch, max_len,
-                                          scale, split, out->data_ptr(), ptr<float>(lse), scratch.p, have,
+                                          scale, split, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
                                           static_cast<int32_t*>(status), s, opts, &so) == PA_OK;
     return attn_decode_paged_ex(d, q->data_ptr(), k->data_ptr(), v->data_ptr(), k->size(0),
-                                     ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch, max_len, scale,
-                                     split, out->data_ptr(), ptr<float>(lse), scratch.p, have,
+                                     ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch,
+                                     max_len, scale,
+                                     split, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
                                      static_cast<int32_t*>(status), s, opts) == PA_OK;
   });
 }
 
 // (q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_q_len, max_seq_len, scale, out, lse,
-//  status, stream, dims, max_ctas, options)
+//  workspace, status, stream, dims, max_ctas, options)
 PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> bool {
     Reader r(a, n);
@@ -286,6 +304,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = static_cast<float>(r.number());
     const at::Tensor* out = r.tensor(ScalarType::BFloat16, 3);
     const at::Tensor* lse = r.tensor_or_none(ScalarType::Float, 2);
+    const at::Tensor* workspace = r.bytes_or_none();
     void* status = r.status();
     cudaStream_t st = r.stream();
     const pa_dims d = r.dims();
@@ -305,20 +324,21 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!r.done() || B > INT32_MAX || T > INT32_MAX || table->size(1) > INT32_MAX) return false;
     const int32_t batch = static_cast<int32_t>(B), rows = static_cast<int32_t>(T);
     const int32_t stride = static_cast<int32_t>(table->size(1));
-    const size_t bytes = scored ? pa_prefill_score_workspace_size(d, batch, rows)
-                                : pa_prefill_workspace_size(d, batch, max_q, max_len);
+    const size_t need = workspace ? 0
+                        : scored  ? pa_prefill_score_workspace_size(d, batch, rows)
+                                  : pa_prefill_workspace_size(d, batch, max_q, max_len);
     Unlocked unlocked;
-    Scratch scratch(bytes, st);
-    const size_t have = bytes < 256 ? 256 : bytes;
+    Scratch scratch(workspace, need, st);
     pa_stream_t s = reinterpret_cast<pa_stream_t>(st);
     if (scored)
       return attn_prefill_chunk_score(d, q->data_ptr(), ptr<const int32_t>(cu), rows, k->data_ptr(), v->data_ptr(),
                                            k->size(0), ptr<const int32_t>(table), stride, ptr<const int32_t>(lens),
                                            batch, max_q, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p,
-                                           have, static_cast<int32_t*>(status), s, opts, &so) == PA_OK;
+                                           scratch.bytes, static_cast<int32_t*>(status), s, opts, &so) == PA_OK;
     return attn_prefill_chunk_ex(d, q->data_ptr(), ptr<const int32_t>(cu), rows, k->data_ptr(), v->data_ptr(),
                                       k->size(0), ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch,
-                                      max_q, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p, have,
+                                      max_q, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p,
+                                      scratch.bytes,
                                       static_cast<int32_t*>(status), s, opts) == PA_OK;
   });
 }

@@ -196,3 +196,27 @@ def test_a_code_of_the_library_is_raised_by_its_name(cuda_lib, fast):
     with pytest.raises(cuda_lib.PagedAttnError, match="rope_append_paged"):
         c.rope(eps=-1.0)
     assert [ok for _, ok in fast.seen] == [False] * 3
+
+
+@pytest.mark.parametrize("name", ["decode", "decode_score", "prefill", "prefill_score", "rope"])
+def test_outputs_and_workspaces_of_the_caller_or_not(cuda_lib, fast, monkeypatch, name):
+    c = Calls(cuda_lib)
+    fn, out = getattr(c, name), "q_out" if name == "rope" else "out"
+    want = slow(cuda_lib, monkeypatch, fn)
+    same(fn(**{out: None}), want)
+    if name != "rope":
+        same(fn(out=None, lse=None), want)
+        assert fn(lse=None, want_lse=False)[1] is None
+        size = {"decode": lambda: cuda_lib.decode_workspace_size(len(LENS), max(LENS), 0, DIMS),
+                "prefill": lambda: cuda_lib.prefill_workspace_size(len(LENS), max(NEW), max(LENS), DIMS),
+                "prefill_score": lambda: cuda_lib.prefill_score_workspace_size(len(LENS), c.T, DIMS)}
+        n = size[CALLS[name] if name != "prefill_score" else name]()
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
+        same(fn(workspace=ws), want)
+        assert [ok for _, ok in fast.seen] == [True] * 4
+        with pytest.raises(cuda_lib.PagedAttnError):
+            fn(workspace=ws[:0])
+        same(fn(workspace=torch.empty(n // 4 + 64, dtype=torch.int32, device="cuda")), want)
+        assert [ok for _, ok in fast.seen[4:]] == [False] * 2  # (any tensor will do, by the slower path)
+    else:
+        assert [ok for _, ok in fast.seen] == [True]
