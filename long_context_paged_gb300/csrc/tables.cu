@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParam
   __shared__ int32_t cta_count[kMaxCluster];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  if (ctas > 1) cluster_sync_all();  // every CTA has started before any writes to another's shared memory
   await_previous();
   const int free_count = read_free_count(p.free_count, p.free_capacity, p.status, rank == 0 && tid == 0);
   // this warp's requests: a contiguous share, so that the pushes of all warps are in order

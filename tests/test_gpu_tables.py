@@ -187,3 +187,22 @@ def test_plan_and_release_on_another_stream(cuda_lib):
     # every page is free again, once
     assert n.item() == a[4] + int((-(-a[0] // 16)).sum())
     assert len(set(room[:n.item()].tolist())) == n.item()
+
+
+@pytest.mark.parametrize("B", [33, 129, 257, 4096])
+def test_release_with_ctas_that_have_nothing_to_count(cuda_lib, B):
+    """Only the last request gives pages back: the other CTAs of the cluster are at the exchange of
+    their counts at once. Calls in a row, each launched during the tail of the one before."""
+    table = np.full((B, 40), -1)
+    table[-1] = np.arange(40)
+    begin, end = np.zeros(B), np.zeros(B)
+    end[-1] = 40
+    b, e, t = dev(begin), dev(end), dev(table)
+    runs = [(t.clone(), dev(np.full(50, 7)), dev([3])) for _ in range(50)]
+    torch.cuda.synchronize()
+    for ti, f, n in runs:
+        cuda_lib.paged_release(b, e, ti, f, n, 64, free_count_out=n)
+    want_t, want_f, want_n, _ = S.release(begin, end, table, np.full(50, 7), 3, 64)
+    for ti, f, n in runs:
+        assert n.item() == want_n and np.array_equal(f.cpu().numpy(), want_f)
+        assert np.array_equal(ti.cpu().numpy(), want_t)
