@@ -264,7 +264,8 @@ struct ReleaseParams {
   int32_t* status;
 };
 
-// The page range of request b, cut to its table row (flagged if it had to be).
+// The page range of request b, cut to its table row, flagged if pages outside the row were named. (Any
+// begin past the row, up to INT32_MAX, is cut too, so that stepping on from it stays within 32 bits.)
 __device__ __forceinline__ void release_range(const ReleaseParams& p, int b, bool report, int& lo, int& hi) {
   lo = p.begin[b];
   hi = p.end[b];
@@ -273,6 +274,7 @@ __device__ __forceinline__ void release_range(const ReleaseParams& p, int b, boo
     lo = max(lo, 0);
     hi = min(hi, p.bt_stride);
   }
+  lo = min(lo, p.bt_stride);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) release_kernel(const ReleaseParams p) {

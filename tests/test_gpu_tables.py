@@ -206,3 +206,20 @@ def test_release_with_ctas_that_have_nothing_to_count(cuda_lib, B):
     for ti, f, n in runs:
         assert n.item() == want_n and np.array_equal(f.cpu().numpy(), want_f)
         assert np.array_equal(ti.cpu().numpy(), want_t)
+
+
+@pytest.mark.parametrize("B", [1, 8, 200])
+def test_release_of_ranges_that_begin_past_their_row(cuda_lib, B):
+    """A begin past the row, up to the largest int32, is an empty range, whatever its end."""
+    top = 2**31 - 1
+    begin = np.resize([top, top - 30, top - 31, top - 127, 40, 41, 0, top], B)
+    end = np.resize([0, top, 40, -5, 40, 40, 40, -2**31], B)
+    table = np.arange(B * 40).reshape(B, 40)
+    free = np.full(B * 40 + 5, 77)
+    want_t, want_f, want_n, flags = S.release(begin, end, table, free, 2, B * 40)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    t, f = dev(table), dev(free)
+    n = cuda_lib.paged_release(dev(begin), dev(end), t, f, dev([2]), B * 40, status=status)
+    assert n.item() == want_n and np.array_equal(f.cpu().numpy(), want_f)
+    assert np.array_equal(t.cpu().numpy(), want_t)
+    assert cuda_lib.read_device_status(status) == sum(BITS[x] for x in flags)
