@@ -27,7 +27,8 @@ struct ScoreParams {
   int32_t max_prefix;
   const int32_t* row_start;  // [rows] or null
   // softcap * log2 e * tanh(q_scale * s) of a raw product s as an odd polynomial s P(s^2), for
-  // |s| <= poly_max (|q_scale s| <= 1; 0: not usable: scores are then capped one by one)
+  // |s| <= poly_max (|q_scale s| <= 1; negative: not usable, not even for products of 0: scores are
+  // then capped one by one)
   float poly[7], poly_max;
 };
 
@@ -57,7 +58,7 @@ inline int score_max_visible(const pa_score_opts& o, int max_seq_len) {
 
 // q's factor (*q_scale): the softmax scale in log2 units or, with a cap, over the cap.
 inline ScoreParams score_params(const pa_score_opts& o, float softmax_scale, float* q_scale) {
-  ScoreParams s;
+  ScoreParams s{};
   s.cap_log2 = o.softcap * kLog2e;
   s.slopes = o.alibi_slopes;
   s.window = o.window;
@@ -65,7 +66,7 @@ inline ScoreParams score_params(const pa_score_opts& o, float softmax_scale, flo
   s.max_prefix = o.max_prefix_len;
   s.row_start = o.row_start;
   *q_scale = o.softcap > 0.f ? softmax_scale / o.softcap : softmax_scale * kLog2e;
-  s.poly_max = 0.f;
+  s.poly_max = -1.f;
   const double x = *q_scale;
   // the folded coefficients, down to softcap x^13 and up to softcap x, stay in fp32's range
   if (o.softcap > 0.f && o.softcap <= 1e6f && x >= 0x1p-10 && x <= 0x1p4) {

@@ -390,3 +390,18 @@ def test_rows_without_keys_under_any_slope(cuda_lib, off, slope):
         assert bool((lse[::3] == float("-inf")).all()) and not bool(out[::3].any())
         keep = [h for h in range(16) if h != 5]
         assert bool(lse[1::3][:, keep].isfinite().all()) and bool(out[1::3][:, keep].isfinite().all())
+
+
+@pytest.mark.parametrize("cap", [1e-4, 30.0, 200.0, 1e5])
+@pytest.mark.parametrize("bias", [False, True])
+def test_products_that_are_all_zero(cuda_lib, cap, bias):
+    """Zero q rows and zeroed keys, a warp's worth and a tile's and more of each: every score of such a
+    row is 0 before the bias, also under caps that the folded polynomial does not serve."""
+    o = dict(softcap=cap, **(dict(slopes=SLOPES) if bias else {}))
+    for seed in range(3):
+        inp = W.make_paged(520 + seed, [530], [260], device="cuda", q_scale=3.0)
+        inp.q[0][32:96] = 0
+        inp.q[0][200:260, 5:] = 0
+        for p in range(0, 272):
+            inp.k_pools[0][int(inp.host_block_table[0, p // 16]), p % 16] = 0
+        check(cuda_lib, inp, o)
