@@ -21,7 +21,8 @@
 //    chain S -> weights -> P V: each paired FMA more per two scores costs 85 us. 16 softmax warps, two
 //    threads per row meeting at a barrier per tile, were slower (1,611 us with masks alone, 2,540 with a
 //    cap): at 96 to 104 registers a thread the pass spills.
-//  * Non-finite V rows are kept from the rows that do not see them (repair_row).
+//  * Non-finite K and V rows are kept from the rows that do not see them: the slots behind a sequence's
+//    end are cleared by the producers, and rows that a non-finite value reached are repaired (repair_rows).
 #include <algorithm>
 
 #include <cuda.h>
@@ -94,9 +95,11 @@ struct TileDesc {
   int32_t b, qt, q0, n, L, off;
   int32_t J;                 // key tiles of the job (at least 1: rows that see nothing are written too)
   int32_t prefix, n1, shift, lo, hi;
+  uint32_t repair;           // bit h: query head h has rows for repair_rows
 };
 struct PlanHeader {
-  int32_t tiles, rounds, grid, pad;
+  int32_t tiles, rounds, grid;
+  int32_t repair;        // a tile has rows for repair_rows
   long long units;       // units of one KV head's jobs
   long long whole_jobs;  // jobs below this one were done whole, in the round-robin phase
 };
@@ -119,8 +122,7 @@ struct PrefillScoreParams {
   int32_t* status;
   ScoreParams score;
   int32_t total_q, max_tiles, max_q_len;
-  bool whole_only;           // a CTA per job: nothing is split, and neither plan nor merge is needed
-  const uint16_t* q_rows;    // the operands, for repair_row
+  const uint16_t* q_rows;    // the operands, for repair_rows
   const uint16_t* k_rows;
   const uint16_t* v_rows;
   PlanHeader* ws_plan;
@@ -210,6 +212,7 @@ __device__ __forceinline__ TileDesc tile_desc(const P& p, const Chunk& c, int b,
   const int t0 = max(min(lo, hi) / kTileN, d.n1);
   d.shift = t0 - d.n1;
   d.J = max(1, d.n1 + max(0, end - t0));
+  d.repair = 0;
   return d;
 }
 
@@ -235,7 +238,7 @@ __device__ __forceinline__ PieceDesc piece_of(const TileDesc& d, int g, int jb, 
   return c;
 }
 
-// The job of CTA blockIdx.x when a call is not split (whole_only: at most as many jobs as CTAs), by a
+// The job of CTA blockIdx.x when a call is not split (kWhole: at most as many jobs as CTAs), by a
 // whole warp, without a plan: four chunks a lane (kMaxBatch = 128), their tiles scanned.
 template <class P>
 __device__ PieceDesc whole_job(const P& p, int lane) {
@@ -457,6 +460,7 @@ struct ScoreSmem {  // placed at a 1024-byte aligned address (swizzle atoms)
   uint64_t s_full[2], p1_full, o_ready[2], o_free[2];
   uint64_t mma_done;
   uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
+  uint64_t tail_full[2];          // copies of a tile that its producer clears the tail of: K, V
   uint32_t tmem_base;
 };
 static_assert(sizeof(ScoreSmem) <= 232448, "prefill shared memory over the 227 KB limit");
@@ -479,46 +483,237 @@ __device__ __forceinline__ uint32_t row_mask_word(const RowMask& m, int base) {
   return below(m.prefix - base) | (below(m.qpos + 1 - base) & ~below(m.lo - base));
 }
 
-// A masked key's P is 0, and 0 times a non-finite V is NaN: a V row that one row of a tile sees and
-// another does not (a later token, another document) would reach both through the MMA. Rows that
-// come out non-finite are therefore recomputed here from their visible keys alone, one after the
-// other by their warp, and stored over what was stored. This costs time only on inputs that hold
-// non-finite values: a row's keys at ~50 cycles each, 0.1 s for a warp's 32 rows of 131,072 keys, well
-// inside the other warps' 2 s waits. acc: dims 4 lane .. + 3.
+// Whether one of a word's two bf16 is not finite (its exponent is all ones).
+__device__ __forceinline__ bool word_not_finite(uint32_t w) {
+  return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+}
+
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+// Two pages' first slots: the 32 keys from `base` on. Entries of keys outside `used` are not looked up.
 template <class P>
-__device__ __forceinline__ void repair_row(const P& p, const PieceDesc& d, int row_in_chunk, int head,
-                                           const RowMask& m, float slope2, float m_eff, float scale_o,
-                                           float (&acc)[4]) {
-  const int lane = threadIdx.x & 31;
-  const uint2 qw = *(reinterpret_cast<const uint2*>(
-                         p.q_rows + (static_cast<int64_t>(d.q0 + row_in_chunk) * p.hq + head) * kHeadDim) + lane);
-  const float q[4] = {bf16lo(qw.x), bf16hi(qw.x), bf16lo(qw.y), bf16hi(qw.y)};
-  acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-  const int32_t* bt_row = p.block_table + static_cast<int64_t>(d.b) * p.bt_stride;
-  for (int j = d.jb; j < d.je; ++j) {
-    const int k0 = (j < d.n1 ? j : j + d.shift) * kTileN;
-    for (int w = 0; w < kTileN / 32; ++w) {
-      for (uint32_t seen = row_mask_word(m, k0 + 32 * w); seen != 0; seen &= seen - 1) {
-        const int key = k0 + 32 * w + __ffs(seen) - 1;
-        int page = bt_row[key / kPage];
-        if (page < 0 || page >= p.num_pages) page = 0;  // (flagged by the producers)
-        const int64_t at = ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + d.g) * kHeadDim;
-        const uint2 kw = *(reinterpret_cast<const uint2*>(p.k_rows + at) + lane);
-        float s = q[0] * bf16lo(kw.x) + q[1] * bf16hi(kw.x) + q[2] * bf16lo(kw.y) + q[3] * bf16hi(kw.y);
+__device__ __forceinline__ void word_slots(const P& p, const int32_t* bt_row, int base, uint32_t used, int64_t (&slot)[2]) {
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float x = score_of(p.score, s * p.scale_log2, slope2, abs(m.qpos - key) - m.nearest);
-        const float pr = fast_exp2(x - m_eff);
-        const uint2 vw = *(reinterpret_cast<const uint2*>(p.v_rows + at) + lane);
-        acc[0] += pr * bf16lo(vw.x);
-        acc[1] += pr * bf16hi(vw.x);
-        acc[2] += pr * bf16lo(vw.y);
-        acc[3] += pr * bf16hi(vw.y);
+  for (int h = 0; h < 2; ++h) {
+    const int e = (used >> (16 * h) & 0xffffu) != 0 ? bt_row[base / kPage + h] : 0;
+    slot[h] = static_cast<int64_t>(e < 0 || e >= p.num_pages ? 0 : e) * kPage;  // (flagged by the producers)
+  }
+}
+
+// The non-finite values of V that rows of a warp see: bit r of word k, row r of the warp in dim 4 lane + k.
+struct NonFinite {
+  uint32_t nan[4], up[4], down[4];
+  // What row r's weighted mean is in dim 4 lane + k: x where it sees finite values alone
+  __device__ __forceinline__ bool over(int r, int k, float& x) const {
+    const bool u = up[k] >> r & 1u, d = down[k] >> r & 1u;
+    if ((nan[k] >> r & 1u) || (u && d)) x = CUDART_NAN_F;
+    else if (u || d) x = u ? CUDART_INF_F : -CUDART_INF_F;
+    else return false;
+    return true;
+  }
+};
+
+// A masked key's P is 0, and 0 times a non-finite V is NaN: a V row that one row of a tile sees and
+// another does not (a later token, another document, the rest of a prompt's page) reaches both through
+// the MMA. A job's rows that came out non-finite are put right here, 32 rows of one head by a warp:
+//   1. One walk over the V rows that any of them sees notes who sees which non-finite values: where a row
+//      sees some, they are its result (weights are positive), and the rest of it may be right already.
+//   2. Rows that are non-finite where what they see is finite are computed again from their visible keys,
+//      kRows at a time: a key per lane for the scores, four dims per lane for the sum.
+// Only inputs that hold non-finite values come here, and once their job's rows are stored: no wait of
+// another warp runs meanwhile. Measured with all rows of a job non-finite, per key of the job: 0.06 us for
+// the walk, 1.3 us where every row is computed again (4,093 keys: 0.23 and 5.3 ms beside 58 us).
+template <class P>
+__device__ __forceinline__ void repair_rows(const P& p, const TileDesc& d, int g, int t, int quarter) {
+  constexpr int kRows = 8;
+  const int lane = threadIdx.x & 31, head = 2 * g + t;
+  const int row0 = d.qt * kTileM + quarter * 32;  // the warp's first row, in the chunk
+  const int32_t* bt_row = p.block_table + static_cast<int64_t>(d.b) * p.bt_stride;
+  const int64_t slot_row = static_cast<int64_t>(p.hkv) * kHeadDim;
+  const uint16_t* const v_lane = p.v_rows + g * kHeadDim + 4 * lane;
+
+  // this lane's 4 dims of a row, as stored
+  auto out_at = [&](int r) {
+    return reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(d.q0 + row0 + r) * p.hq + head) * kHeadDim) + lane;
+  };
+  auto load = [&](int r, float (&x)[4]) {
+    const uint2 w = *out_at(r);
+    x[0] = bf16lo(w.x);
+    x[1] = bf16hi(w.x);
+    x[2] = bf16lo(w.y);
+    x[3] = bf16hi(w.y);
+  };
+  auto store = [&](int r, const float (&x)[4]) {
+    *out_at(r) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  };
+  auto mask_of = [&](int r) {
+    RowMask m;
+    m.prefix = d.prefix;
+    m.qpos = d.off + row0 + r;
+    m.lo = score_first_key(p.score, d.q0 + row0 + r, m.qpos);
+    m.nearest = m.lo <= m.qpos ? 0 : max(0, m.qpos + 1 - m.prefix);
+    return m;
+  };
+
+  // the rows to look at: not finite, and not for a score that is NaN (then all of the row is)
+  uint32_t bad = 0;
+  for (int r = 0; r < min(32, d.n - row0); ++r) {
+    float x[4];
+    load(r, x);
+    const bool odd = not_finite(x[0]) || not_finite(x[1]) || not_finite(x[2]) || not_finite(x[3]);
+    if (!__any_sync(0xffffffffu, odd)) continue;
+    if (p.lse != nullptr && isnan(p.lse[static_cast<int64_t>(d.q0 + row0 + r) * p.hq + head])) continue;
+    bad |= 1u << r;
+  }
+  if (bad == 0) return;
+
+  const bool mine = bad >> lane & 1u;
+  RowMask rm{};
+  if (mine) rm = mask_of(lane);
+  NonFinite nf;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) nf.nan[k] = nf.up[k] = nf.down[k] = 0;
+  for (int w = 0; w < 4 * d.J; ++w) {
+    const int base = ((w >> 2) < d.n1 ? w >> 2 : (w >> 2) + d.shift) * kTileN + 32 * (w & 3);
+    const uint32_t seen = mine ? row_mask_word(rm, base) : 0u;
+    const uint32_t any = __reduce_or_sync(0xffffffffu, seen);
+    if (any == 0) continue;
+    int64_t slot[2];
+    word_slots(p, bt_row, base, any, slot);
+#pragma unroll 1
+    for (int c0 = 0; c0 < 32; c0 += 16) {
+      uint2 vw[16];
+      const int64_t first = c0 == 0 ? slot[0] : slot[1];
+      bool found = false;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        vw[c] = make_uint2(0u, 0u);
+        if (any >> (c0 + c) & 1u) vw[c] = *reinterpret_cast<const uint2*>(v_lane + (first + c) * slot_row);
+        found = found || word_not_finite(vw[c].x) || word_not_finite(vw[c].y);
+      }
+      if (!__any_sync(0xffffffffu, found)) continue;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint32_t rows = __ballot_sync(0xffffffffu, seen >> (c0 + c) & 1u);
+        const float v[4] = {bf16lo(vw[c].x), bf16hi(vw[c].x), bf16lo(vw[c].y), bf16hi(vw[c].y)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (isnan(v[k])) nf.nan[k] |= rows;
+          else if (not_finite(v[k])) (v[k] > 0.f ? nf.up[k] : nf.down[k]) |= rows;
+        }
       }
     }
   }
+
+  uint32_t again = 0;
+  for (uint32_t left = bad; left != 0; left &= left - 1) {
+    const int r = __ffs(left) - 1;
+    float x[4];
+    load(r, x);
+    bool wrong = false;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] *= scale_o;
+    for (int k = 0; k < 4; ++k)
+      if (!nf.over(r, k, x[k])) wrong = wrong || not_finite(x[k]);
+    if (__any_sync(0xffffffffu, wrong)) again |= 1u << r;
+    else store(r, x);
+  }
+
+  float slope2 = 0.f;
+  if constexpr (P::kBias) slope2 = slope_over(p.score, head, 1.0f);
+#pragma unroll 1
+  while (again != 0) {
+    int row[kRows];
+    RowMask m[kRows];
+    float top[kRows], sum[kRows], acc[kRows][4];  // running maximum, the lane's share of the sum, the lane's dims
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      row[i] = again != 0 ? __ffs(again) - 1 : row[0];  // (fewer left: the first one again)
+      again &= again - 1;
+      m[i] = mask_of(row[i]);
+      top[i] = -CUDART_INF_F;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+    }
+    for (int w = 0; w < 4 * d.J; ++w) {
+      const int base = ((w >> 2) < d.n1 ? w >> 2 : (w >> 2) + d.shift) * kTileN + 32 * (w & 3);
+      uint32_t seen[kRows], any = 0;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) any |= seen[i] = row_mask_word(m[i], base);
+      if (any == 0) continue;
+      int64_t slot[2];
+      word_slots(p, bt_row, base, any, slot);
+      float s[kRows] = {};
+      if (any >> lane & 1u) {  // scores: key base + lane
+        const uint4* k_row = reinterpret_cast<const uint4*>(
+            p.k_rows + ((lane < 16 ? slot[0] : slot[1]) + (lane & 15)) * slot_row + g * kHeadDim);
+#pragma unroll 4
+        for (int c = 0; c < kHeadDim / 8; ++c) {
+          const uint4 kw = k_row[c];
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const uint4 qw = reinterpret_cast<const uint4*>(
+                p.q_rows + (static_cast<int64_t>(d.q0 + row0 + row[i]) * p.hq + head) * kHeadDim)[c];
+            s[i] += bf16lo(qw.x) * bf16lo(kw.x) + bf16hi(qw.x) * bf16hi(kw.x) + bf16lo(qw.y) * bf16lo(kw.y) +
+                    bf16hi(qw.y) * bf16hi(kw.y) + bf16lo(qw.z) * bf16lo(kw.z) + bf16hi(qw.z) * bf16hi(kw.z) +
+                    bf16lo(qw.w) * bf16lo(kw.w) + bf16hi(qw.w) * bf16hi(kw.w);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const bool sees = seen[i] >> lane & 1u;
+        const float x = score_of(p.score, s[i] * p.scale_log2, slope2, abs(m[i].qpos - base - lane) - m[i].nearest);
+        float mx = sees ? x : -CUDART_INF_F;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (mx > top[i]) {
+          const float alpha = fast_exp2(top[i] - mx);
+          top[i] = mx;
+          sum[i] *= alpha;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][k] *= alpha;
+        }
+        s[i] = sees && !(x == -CUDART_INF_F) ? fast_exp2(x - top[i]) : 0.f;
+        sum[i] += s[i];
+      }
+#pragma unroll 1
+      for (int c0 = 0; c0 < 32; c0 += 8) {
+        uint2 vw[8];
+        const int64_t first = c0 < 16 ? slot[0] : slot[1];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          vw[c] = make_uint2(0u, 0u);
+          if (any >> (c0 + c) & 1u)
+            vw[c] = *reinterpret_cast<const uint2*>(v_lane + (first + (c0 & 15) + c) * slot_row);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float v[4] = {bf16lo(vw[c].x), bf16hi(vw[c].x), bf16lo(vw[c].y), bf16hi(vw[c].y)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = not_finite(v[k]) ? 0.f : v[k];  // (who sees it gets it below)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const float pr = __shfl_sync(0xffffffffu, s[i], c0 + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i][k] = fmaf(pr, v[k], acc[i][k]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+      const float f = sum[i] == 0.f ? 0.f : 1.0f / sum[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[i][k] *= f;
+        if (sum[i] != 0.f) nf.over(row[i], k, acc[i][k]);
+      }
+      store(row[i], acc[i]);
+    }
+  }
 }
 
 // tc::tmem_ld32_max with the maximum of the magnitudes.
@@ -643,7 +838,25 @@ __device__ __forceinline__ void score_tile(const P& p, uint32_t (&sb)[kTileN], c
   }
 }
 
+// repair_rows of a CTA's one job. (Not inlined: kept out of the tile loop's registers.)
 template <class P>
+__device__ __noinline__ void repair_job(const P& p, const PieceDesc& c, int t, int quarter) {
+  TileDesc d;
+  d.b = c.b;
+  d.qt = c.qt;
+  d.q0 = c.q0;
+  d.n = c.n;
+  d.off = c.off;
+  d.J = c.J;
+  d.prefix = c.prefix;
+  d.n1 = c.n1;
+  d.shift = c.shift;
+  __syncwarp();
+  repair_rows(p, d, c.g, t, quarter);
+}
+
+// kWhole: a CTA per job; nothing is split, and neither plan nor merge is needed.
+template <class P, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap k_map,
@@ -674,6 +887,8 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     mbar_init(&s.p1_full, 4);
     mbar_init(&s.mma_done, 1);
+    mbar_init(&s.tail_full[0], 1);
+    mbar_init(&s.tail_full[1], 1);
     for (int i = 0; i < kPieceRing; ++i) {
       mbar_init(&s.piece_full[i], 1);
       mbar_init(&s.piece_empty[i], kPieceReaders);
@@ -689,7 +904,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
   // waits for its completion
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const bool work = p.whole_only || p.ws_plan->rounds > 0 || p.ws_tail[blockIdx.x] < p.ws_tail[blockIdx.x + 1];
+  const bool work = kWhole || p.ws_plan->rounds > 0 || p.ws_tail[blockIdx.x] < p.ws_tail[blockIdx.x + 1];
 
   if (!work) {
     // nothing to do but to give the tensor memory back
@@ -697,7 +912,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
     tc::regs_decrease<kControlRegs>();
   if (warp == kSchedWarp) {
     // ------------------------------------------------------------------ scheduler
-    if (p.whole_only) {  // this CTA's one job, then the end (the ring has room for both)
+    if constexpr (kWhole) {  // this CTA's one job, then the end (the ring has room for both)
       const PieceDesc d = whole_job(p, lane);
       if (lane == 0) {
         s.piece[0] = d;
@@ -727,8 +942,9 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
     uint64_t* full = is_k ? s.k_full : s.pv_full;
     uint64_t* empty = is_k ? s.k_empty : s.v_empty;
     const int oob_token = static_cast<int>(p.num_pages * kPage);  // zero-filled coordinate
+    uint64_t* tail_full = &s.tail_full[is_k ? 0 : 1];
     bool ok = true;
-    uint32_t it = 0;
+    uint32_t it = 0, tails = 0;
     for (uint32_t jc = 0;; ++jc) {
       const uint32_t slot = jc % kPieceRing, ph = (jc / kPieceRing) & 1;
       ok = __all_sync(0xffffffffu, wait_or_flag(&s.piece_full[slot], ph, p.status));
@@ -776,13 +992,32 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
         if (lane == 0) ok = wait_or_flag(&empty[st], eph ^ 1u, p.status);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], kTileBytes);
+        // The page that holds the sequence's last key L - 1 is loaded whole. The pool slots after it may
+        // hold anything (unwritten ones a NaN): their rows are cleared before the tile is handed on, that
+        // neither a product, not even of a row that sees nothing of the tile, nor P = 0 meets them. (The
+        // pages after it are never loaded: zeros.) Only a piece's last tile can run past the end.
+        const int zl = pc.L - (j < pc.n1 ? j : j + pc.shift) * kTileN;
+        const bool tail = zl > 0 && zl < kTileN && (zl & (kPage - 1)) != 0;
+        uint64_t* landed = tail ? tail_full : &full[st];
+        if (lane == 0) mbar_arrive_expect_tx(landed, kTileBytes);
         __syncwarp();
         // 16 lanes issue the tile's 16 copies at once (page lane / 2, 64-dim block lane % 2)
         const int pg = (lane >> 1) & 7, kb = lane & 1;
         const int tk = __shfl_sync(0xffffffffu, tok, pg);
         if (lane < 2 * (kTileN / kPage))
-          tc::tma_load_3d(ring[st][kb] + pg * 2048, map, kb * 64, pc.g, tk, &full[st]);
+          tc::tma_load_3d(ring[st][kb] + pg * 2048, map, kb * 64, pc.g, tk, landed);
+        if (tail) {
+          ok = __all_sync(0xffffffffu, wait_or_flag(tail_full, tails & 1, p.status));
+          ++tails;
+          if (!ok) break;
+          for (int e = zl * 16 + lane; e < ((zl + 15) & ~15) * 16; e += 32) {
+            const int r = e >> 4, c = e & 15;   // row, 16-byte chunk (8 per 64-dim block)
+            *reinterpret_cast<uint4*>(ring[st][c >> 3] + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[st]);
+        }
         tok = tok_next;
         tok_next = tok_ahead;
       }
@@ -793,6 +1028,7 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
       for (uint32_t k = (it >= nst ? it - nst : 0); k < it; ++k)
         wait_or_flag(&full[k % nst], (k / nst) & 1, p.status);
     }
+    if (lane == 0 && tails > 0) wait_or_flag(tail_full, (tails - 1) & 1, p.status);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer (lane 0)
@@ -831,17 +1067,10 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
         const uint32_t pslot = jc % kPieceRing;
         if (!wait_or_flag(&s.piece_full[pslot], (jc / kPieceRing) & 1, p.status)) break;
         const volatile PieceDesc& pv = s.piece[pslot];
-        const int pvalid = pv.valid, pjb = pv.jb, pje = pv.je, pL = pv.L;
-        int last = pje - 1;  // the piece's last key tile
-        if (last >= pv.n1) last += pv.shift;
+        const int pvalid = pv.valid, pjb = pv.jb, pje = pv.je;
         mbar_arrive(&s.piece_empty[pslot]);
         if (!pvalid) break;
         const int nt = pje - pjb;
-        // Only a piece's last tile can run past the sequence end. The page that holds key L - 1 was
-        // loaded whole, so the V rows of the pool slots after it are zeroed, that P = 0 there cannot
-        // meet an unwritten (possibly NaN) slot; the pages after it were never loaded (zero fill).
-        const int zl = pL - last * kTileN;
-        const int zero_i = (zl > 0 && zl < kTileN && (zl & 15) != 0) ? nt - 1 : -1;
         const uint32_t qph = jc & 1, oph = (jc - 1) & 1;
         ok = wait_or_flag(&s.q_full, qph, p.status) && wait_or_flag(&s.k_full[kst], kph, p.status);
         if (!ok) break;
@@ -861,13 +1090,6 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
               (i == 0 && jc > 0 && !wait_or_flag(&s.o_free[0], oph, p.status))) {
             ok = false;
             break;
-          }
-          if (i == zero_i) {
-            for (int e = zl * 16; e < ((zl + 15) & ~15) * 16; ++e) {
-              const int r = e >> 4, c = e & 15;   // row, 16-byte chunk (8 per 64-dim block)
-              *reinterpret_cast<uint4*>(s.v[vst][c >> 3] + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_proxy_async_smem();
           }
           tc::fence_after_sync();
           issue_pv(tmem + 256, tmem, dv, acc);
@@ -1111,6 +1333,10 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
             w.w = pack_bf16x2(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv);
             *reinterpret_cast<uint4*>(out_row + 8 * k) = w;
           }
+          if (none && z != 0.f) {  // (0 times what no weight was on)
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(out_row + 8 * k) = make_uint4(0u, 0u, 0u, 0u);
+          }
           if (p.lse != nullptr) {
             float v = none ? -CUDART_INF_F : (m_used + log2f(l)) * kLn2;
             if constexpr (P::kBias) {
@@ -1130,26 +1356,13 @@ prefill_score_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         reinterpret_cast<float*>(rec + kRecordO)[t * 128 + r] = none ? -CUDART_INF_F : (m_used + log2f(l)) * kLn2;
       }
-      for (uint32_t bad = __ballot_sync(0xffffffffu, live && z != 0.f); bad != 0; bad &= bad - 1) {
-        const int who = __ffs(bad) - 1;
-        RowMask wm;
-        wm.prefix = rm.prefix;
-        wm.lo = __shfl_sync(0xffffffffu, rm.lo, who);
-        wm.qpos = __shfl_sync(0xffffffffu, rm.qpos, who);
-        wm.nearest = __shfl_sync(0xffffffffu, rm.nearest, who);
-        const float wmu = __shfl_sync(0xffffffffu, m_used, who);
-        const float winv = __shfl_sync(0xffffffffu, inv, who);
-        const int wrow = desc.qt * kTileM + quarter * 32 + who;
-        float a[4];
-        repair_row(p, desc, wrow, head, wm, slope2, wmu == -CUDART_INF_F ? 0.f : wmu, winv, a);
-        __syncwarp();  // after the row's own lane has stored it
-        if (whole) {
-          uint2* dst = reinterpret_cast<uint2*>(
-              p.out + (static_cast<int64_t>(desc.q0 + wrow) * p.hq + head) * kHeadDim);
-          dst[lane] = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-        } else {
-          reinterpret_cast<float4*>(rec)[(t * 32 + lane) * 128 + quarter * 32 + who] =
-              make_float4(a[0], a[1], a[2], a[3]);
+      // (a sum that is NaN: the row sees a score that is, and all of it is NaN)
+      if (__any_sync(0xffffffffu, live && z != 0.f && l > 0.f)) {
+        if constexpr (kWhole) {
+          repair_job(p, desc, t, quarter);
+        } else if (lane == 0) {  // for prefill_repair_kernel
+          atomicOr(&p.ws_tiles[p.ws_first_tile[desc.b] + desc.qt].repair, 1u << head);
+          p.ws_plan->repair = 1;
         }
       }
       it += nt;
@@ -1270,6 +1483,20 @@ __global__ void __launch_bounds__(kMergeRows) prefill_score_merge_kernel(const P
   }
 }
 
+// The jobs of a split call with rows for repair_rows, a warp per head and 32 rows; most calls have none.
+template <class P>
+__global__ void __launch_bounds__(256, 1) prefill_repair_kernel(const P p) {
+  await_previous();
+  const PlanHeader& h = *p.ws_plan;
+  if (h.repair == 0) return;
+  const int warp = threadIdx.x >> 5, t = warp >> 2;
+  for (int job = blockIdx.x; job < h.tiles * p.hkv; job += gridDim.x) {
+    const int g = job / h.tiles;
+    const TileDesc d = p.ws_tiles[job - g * h.tiles];
+    if (d.repair >> (2 * g + t) & 1u) repair_rows(p, d, g, t, warp & 3);
+  }
+}
+
 // ---------------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------------
@@ -1297,35 +1524,48 @@ int score_tiles(int64_t total_q, int batch) { return static_cast<int>(total_q / 
 // One persistent CTA per SM.
 int score_grid() { return std::min(sm_count_current_device(), kMaxGrid); }
 
-// Plan, attention and merge of one call; each is a programmatic dependent of the one before.
+// Allows an instance its shared memory and reads its registers.
+template <class P, bool kWhole>
+cudaError_t configure_score(int smem, int* regs) {
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncSetAttribute(prefill_score_kernel<P, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, prefill_score_kernel<P, kWhole>);
+  if (e == cudaSuccess) *regs = fa.numRegs;
+  return e;
+}
+
+// Plan, attention, merge and repair of one call, or its attention alone (whole: a CTA per job); each
+// is a programmatic dependent of the one before.
 template <class P>
 pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const P& p,
-                       int grid, cudaStream_t stream) {
+                       int grid, bool whole, cudaStream_t stream) {
   const int smem = static_cast<int>(sizeof(ScoreSmem));
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_score_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int regs = 0, regs_whole = 0;
+    cudaError_t e = configure_score<P, false>(smem, &regs);
+    if (e == cudaSuccess) e = configure_score<P, true>(smem, &regs_whole);
     if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(prefill_score)");
-    // same carveout for the merge kernel: no reconfiguration between them
-    e = cudaFuncSetAttribute(prefill_score_merge_kernel<P>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(prefill score merge)");
     // The in-kernel register split needs the full launch budget; a build that launched with
     // fewer registers per thread would make setmaxnreg.inc wait forever, so refuse to launch.
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, prefill_score_kernel<P>);
-    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncGetAttributes(prefill_score)");
-    if (fa.numRegs < kLaunchRegs) {
+    if (std::min(regs, regs_whole) < kLaunchRegs) {
       snprintf_error("prefill_score_kernel built with %d registers/thread, needs %d for its split",
-                     fa.numRegs, kLaunchRegs);
+                     std::min(regs, regs_whole), kLaunchRegs);
       return PA_ERR_UNSUPPORTED;
     }
+    // same carveout for the kernels after it: no reconfiguration between them
+    e = cudaFuncSetAttribute(prefill_score_merge_kernel<P>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(prefill_repair_kernel<P>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(prefill score merge)");
     configured_device = dev;
   }
-  if (p.whole_only) {
-    const cudaError_t e = launch_dependent(prefill_score_kernel<P>, static_cast<unsigned>(p.max_tiles * p.hkv),
+  if (whole) {
+    const cudaError_t e = launch_dependent(prefill_score_kernel<P, true>, static_cast<unsigned>(p.max_tiles * p.hkv),
                                            kThreads, smem, stream, 0, qm, km, vm, p);
     return e == cudaSuccess ? PA_OK : record_cuda_error(e, "prefill_score_kernel");
   }
@@ -1341,13 +1581,15 @@ pa_status launch_score(const CUtensorMap& qm, const CUtensorMap& km, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefill_score_kernel<P>, qm, km, vm, p);
+  e = cudaLaunchKernelEx(&cfg, prefill_score_kernel<P, false>, qm, km, vm, p);
   if (e != cudaSuccess) return record_cuda_error(e, "prefill_score_kernel");
   cfg.gridDim = dim3((p.max_q_len + kTileM - 1) / kTileM, p.hkv * 8, p.batch);
   cfg.blockDim = dim3(kMergeRows);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, prefill_score_merge_kernel<P>, p);
-  return e == cudaSuccess ? PA_OK : record_cuda_error(e, "prefill_score_merge_kernel");
+  if (e != cudaSuccess) return record_cuda_error(e, "prefill_score_merge_kernel");
+  e = launch_dependent(prefill_repair_kernel<P>, static_cast<unsigned>(grid), 256, 0, stream, 0, p);
+  return e == cudaSuccess ? PA_OK : record_cuda_error(e, "prefill_repair_kernel");
 }
 
 }  // namespace
@@ -1402,7 +1644,6 @@ pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, cons
     p.total_q = total_q;
     p.max_tiles = max_tiles;
     p.max_q_len = max_q_len;
-    p.whole_only = max_tiles * hkv <= grid && max_seq_len <= kWholeKeys;
     p.q_rows = static_cast<const uint16_t*>(q);
     p.k_rows = static_cast<const uint16_t*>(k_pool);
     p.v_rows = static_cast<const uint16_t*>(v_pool);
@@ -1412,7 +1653,7 @@ pa_status launch_prefill_score(int32_t hkv, const void* q, int32_t total_q, cons
     p.ws_first_tile = reinterpret_cast<int32_t*>(ws + w.first_tile);
     p.ws_tail = reinterpret_cast<long long*>(ws + w.tail);
     p.ws_records = ws + w.records;
-    return launch_score(qm, km, vm, p, grid, stream);
+    return launch_score(qm, km, vm, p, grid, max_tiles * hkv <= grid && max_seq_len <= kWholeKeys, stream);
   };
   const bool cap = score.softcap > 0.f, bias = score.alibi_slopes != nullptr;
   return cap ? (bias ? run(PrefillScoreParams<true, true>()) : run(PrefillScoreParams<true, false>()))
