@@ -360,7 +360,9 @@ pa_status attn_merge_lse(int32_t num_parts, int32_t rows, int32_t heads, int32_t
  *   cu_new_lens     int32 [batch+1]: packed row offsets (the cu_new_lens / cu_q_lens of the calls)
  *   seq_lens        int32 [batch]: tokens after the step (may be cached_lens itself)
  *   positions       int32 [total_rows];  slot_map  int64 [total_rows]: page * 16 + position % 16
- * A page outside [0, num_pages) is flagged PA_DEV_ERR_PAGE_OOB and its rows get slot -1.
+ * A page outside [0, num_pages), popped from the free list or held by a token that a row follows in
+ * its page, is flagged PA_DEV_ERR_PAGE_OOB and its rows get slot -1; the request counts as served all
+ * the same: the entry stays in the table and seq_lens advances.
  *
  * paged_release: the entries of logical pages [begin_pages[b], end_pages[b]) of each request are
  * appended to the free list in (request, page) order and become -1 in the table; entries that are

@@ -187,7 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
     const int i = static_cast<int>(i0);
     const int b = last_at_most(s.need, p.batch, i);
     const int lp = pages_of(s.cached[b]) + (i - s.need[b]);
-    p.block_table[static_cast<int64_t>(b) * p.bt_stride + lp] = p.free_pages[free_count - 1 - i];
+    const int page = p.free_pages[free_count - 1 - i];
+    if (page < 0 || page >= p.num_pages) flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
+    p.block_table[static_cast<int64_t>(b) * p.bt_stride + lp] = page;
   }
   if (id == 0) {
     *p.free_count_out = free_count - used;

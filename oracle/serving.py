@@ -44,6 +44,8 @@ def step_plan(cached, new, table, free, count, num_pages, total_rows, page_size=
             for k in range(need):
                 table[b, held + k] = free[count - 1 - used]
                 used += 1
+                if not 0 <= table[b, held + k] < num_pages:
+                    flags.add("page")
             for j in range(n):
                 t, p = cu[-1] + j, c + j
                 if t < total_rows:

@@ -223,3 +223,14 @@ def test_release_of_ranges_that_begin_past_their_row(cuda_lib, B):
     assert n.item() == want_n and np.array_equal(f.cpu().numpy(), want_f)
     assert np.array_equal(t.cpu().numpy(), want_t)
     assert cuda_lib.read_device_status(status) == sum(BITS[x] for x in flags)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 20, 300])
+@pytest.mark.parametrize("page", [99, 64, -4])
+def test_step_plan_flags_a_bad_page_that_no_row_reaches(cuda_lib, rows, page):
+    """A page of the free list outside the pool is flagged where it goes into a table, not only where a
+    row of the call lands on it; the entry and the lengths are as the definition says."""
+    a = ([5, 16, 0], [3, 250, 40], np.full((3, 20), 7), np.array(list(range(20, 30)) + [page] + list(range(30, 46))), 27, 64, rows)
+    want = S.step_plan(*a)
+    assert "page" in want["flags"]
+    check_plan(*run_plan(cuda_lib, *a), want)
