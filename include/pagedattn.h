@@ -357,7 +357,9 @@ pa_status attn_merge_lse(int32_t num_parts, int32_t rows, int32_t heads, int32_t
  *   total_rows      rows of positions and slot_map (>= the packed rows; fewer is flagged
  *                   PA_DEV_ERR_LENGTH and the rest is not written); rows past the last request's
  *                   are padding: position 0, slot -1
- *   cu_new_lens     int32 [batch+1]: packed row offsets (the cu_new_lens / cu_q_lens of the calls)
+ *   cu_new_lens     int32 [batch+1]: packed row offsets (the cu_new_lens / cu_q_lens of the calls), at
+ *                   most 2^31 - 1: lengths that sum to more are flagged with the rows that are not
+ *                   written
  *   seq_lens        int32 [batch]: tokens after the step (may be cached_lens itself)
  *   positions       int32 [total_rows];  slot_map  int64 [total_rows]: page * 16 + position % 16
  * A page outside [0, num_pages), popped from the free list or held by a token that a row follows in

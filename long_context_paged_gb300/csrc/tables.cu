@@ -109,12 +109,12 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
   const int free_count = read_free_count(p.free_count, p.free_capacity, p.status, report && tid == 0);
   const int per = (p.batch + kThreads - 1) / kThreads;  // <= 4
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
-  int c[4], n[4], need[4];
+  int c[4], n[4], need[4], len[4];  // len: tokens after the step
   bool valid[4];
   long long rows = 0, pages = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    c[k] = n[k] = need[k] = 0;
+    c[k] = n[k] = need[k] = len[k] = 0;
     valid[k] = false;
     if (b0 + k < b1) {
       c[k] = p.cached[b0 + k];
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
       s.need[b0 + k] = static_cast<int32_t>(min(q_run, kMax));
       c[k] = min(max(c[k], 0), capacity);
       s.cached[b0 + k] = served ? c[k] : ~c[k];
+      len[k] = served ? c[k] + n[k] : c[k];
       r_run += n[k];
       q_run += need[k];
       if (b0 + k == p.batch - 1) {
@@ -166,15 +167,15 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
   }
   if (p.in_place && ctas > 1) cluster_sync_all(); else __syncthreads();
 
-  // ---- per request: packed offset, length after the step, new table entries
-  const int all = ctas * kThreads, id = rank * kThreads + tid;
-  for (int b = id; b <= p.batch; b += all) {
-    p.cu[b] = s.cu[b];
-    if (b < p.batch) {
-      const int cb = s.cached[b];
-      p.seq_lens[b] = cb >= 0 ? cb + (s.cu[b + 1] - s.cu[b]) : ~cb;
-    }
+  // ---- per request: length after the step (from the lengths themselves: the packed offsets end at
+  //      2^31 - 1; by the last CTA, which has the fewest rows), packed offset, new table entries
+  if (rank == ctas - 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (b0 + k < b1) p.seq_lens[b0 + k] = len[k];
   }
+  const int all = ctas * kThreads, id = rank * kThreads + tid;
+  for (int b = id; b <= p.batch; b += all) p.cu[b] = s.cu[b];
   const int total = s.cu[p.batch];
   // the served needs are a prefix of all needs: everything up to the free count, cut back to
   // where the last served request ends

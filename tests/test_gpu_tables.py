@@ -234,3 +234,30 @@ def test_step_plan_flags_a_bad_page_that_no_row_reaches(cuda_lib, rows, page):
     want = S.step_plan(*a)
     assert "page" in want["flags"]
     check_plan(*run_plan(cuda_lib, *a), want)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("new", [[2**31 - 1, 3, 40, 0, 1], [5, 2**31 - 1, 2**31 - 1, 3, 40],
+                                 [2**30, 2**30, 1, 2**30, 17]])
+def test_step_plan_lengths_that_sum_past_32_bits(cuda_lib, new, in_place):
+    """Requests that do not fit keep their rows in the packing, whose offsets end at 2^31 - 1; the ones
+    that fit get their pages and lengths all the same."""
+    cached = [0, 5, 16, 7, 30]
+    table, free = np.arange(5 * 20).reshape(5, 20), np.arange(200, 260)
+    a = (cached, new, table, free, 60, 300, 64)
+    # (the sequential definition walks every row, so it is given the rows that do not fit as few)
+    few = [n if n < 1000 else 400 for n in new]
+    want = S.step_plan(cached, few, table, free, 60, 300, 64)
+    lens = dev(cached)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    t, count = dev(table), dev([60])
+    got = cuda_lib.paged_step_plan(lens, dev(new), t, dev(free), count, 300, total_rows=64, status=status,
+                                   **(dict(seq_lens=lens, free_count_out=count) if in_place else {}))
+    assert got.cu_new_lens.tolist() == [min(2**31 - 1, int(x)) for x in np.cumsum([0] + new)]
+    assert got.seq_lens.tolist() == want["seq_lens"].tolist()
+    assert got.free_count.item() == want["count"] and np.array_equal(t.cpu().numpy(), want["table"])
+    first = next(i for i, n in enumerate(new) if n >= 1000)
+    rows = min(64, sum(new[:first]))
+    assert np.array_equal(got.slot_map.cpu().numpy()[:rows], want["slots"][:rows])
+    assert (got.slot_map[rows:] == -1).all() and (got.positions[rows:] == 0).all()
+    assert cuda_lib.read_device_status(status) == BITS["length"] and want["flags"] == {"length"}
