@@ -174,7 +174,10 @@ def _load_fast():
         spec.loader.exec_module(mod)
     except ImportError:
         return None
-    return mod if mod.torch_version.split("+")[0] == torch.__version__.split("+")[0] else None
+    if mod.torch_version.split("+")[0] != torch.__version__.split("+")[0]:
+        return None
+    mod.set_error(PagedAttnError)
+    return mod
 
 
 # ----------------------------------------------------------------------------------------------

@@ -8,10 +8,10 @@
 //
 // These functions take the same arguments as the Python wrappers, make the same checks on the tensors
 // themselves, and call the C ABI. They decide nothing else: whatever is not plainly right (a wrong
-// type, shape, device or layout, an argument of another kind, a status code of the C ABI) returns
-// False, and the wrapper's own path then makes the call or names the error; the C ABI refuses before
-// its first launch, so nothing runs twice. No computation happens here, and the binding works without
-// this module, only slower.
+// type, shape, device or layout, an argument of another kind, a refusal of the C ABI) returns False,
+// and the wrapper's own path then makes the call or names the error; the C ABI refuses before its first
+// launch, so nothing runs twice. A CUDA error may come from a later launch of the call: it is raised
+// from here. No computation happens here, and the binding works without this module, only slower.
 #include <Python.h>
 
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -225,23 +225,40 @@ const pa_launch_opts* launch_options(Reader& r, pa_launch_opts& o) {
   return &o;
 }
 
-// f(): whether the call was made. What it throws comes from before the call (a machine without a GPU, a
+// The binding's error class, called with a call's name and its status code (set_error).
+PyObject* error_class = nullptr;
+
+// What became of a call: not made, or made under this name with this status code.
+struct Made {
+  const char* name = nullptr;
+  pa_status code = PA_OK;
+};
+
+// f(): makes the call or not. What it throws comes from before the call (a machine without a GPU, a
 // tensor without strides or storage, the allocator): the wrapper meets it again and raises its error.
 template <class F>
 PyObject* guarded(F f) {
-  bool made = false;
+  Made made;
   try {
     made = f();
   } catch (const std::exception&) {
     PyErr_Clear();
   }
-  return PyBool_FromLong(made);
+  if (made.name != nullptr && made.code == PA_ERR_CUDA && error_class != nullptr) {
+    PyObject* e = PyObject_CallFunction(error_class, "si", made.name, static_cast<int>(made.code));
+    if (e != nullptr) {
+      PyErr_SetObject(error_class, e);
+      Py_DECREF(e);
+    }
+    return nullptr;
+  }
+  return PyBool_FromLong(made.name != nullptr && made.code == PA_OK);
 }
 
 // (q, k_pool, v_pool, block_table, seq_lens, max_seq_len, scale, split_tokens, out, lse,
 //  workspace, status, stream, dims, max_ctas, options)
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> bool {
+  return guarded([&]() -> Made {
     Reader r(a, n);
     const at::Tensor* q = r.tensor(ScalarType::BFloat16, 3);
     const at::Tensor* k = r.tensor(ScalarType::BFloat16, 4);
@@ -259,7 +276,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const pa_dims d = r.dims();
     pa_launch_opts lo{};
     const pa_launch_opts* opts = launch_options(r, lo);
-    if (!r.good) return false;
+    if (!r.good) return {};
     const int64_t B = q->size(0), hq = d.num_q_heads, hkv = d.num_kv_heads;
     pa_score_opts so{};
     const bool scored = score_options(r, so, static_cast<int>(hq), B, B, max_len);
@@ -270,29 +287,31 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.at_least(lens, B);
     r.shape(out, B, hq, 128);
     r.shape(lse, B, hq);
-    if (!r.done() || B > INT32_MAX || table->size(1) > INT32_MAX) return false;
+    if (!r.done() || B > INT32_MAX || table->size(1) > INT32_MAX) return {};
     const int32_t batch = static_cast<int32_t>(B), stride = static_cast<int32_t>(table->size(1));
     const size_t need = workspace ? 0 : pa_decode_workspace_size(d, batch, max_len, split);
     Unlocked unlocked;
     Scratch scratch(workspace, need, st);
     pa_stream_t s = reinterpret_cast<pa_stream_t>(st);
+    pa_status code;
     if (scored)
-      return attn_decode_paged_score(d, q->data_ptr(), k->data_ptr(), v->data_ptr(), k->size(0),
-                                          ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch, max_len,
-                                          scale, split, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
-                                          static_cast<int32_t*>(status), s, opts, &so) == PA_OK;
-    return attn_decode_paged_ex(d, q->data_ptr(), k->data_ptr(), v->data_ptr(), k->size(0),
-                                     ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch,
-                                     max_len, scale,
-                                     split, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
-                                     static_cast<int32_t*>(status), s, opts) == PA_OK;
+      code = attn_decode_paged_score(d, q->data_ptr(), k->data_ptr(), v->data_ptr(), k->size(0),
+                                     ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch, max_len,
+                                     scale, split, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
+                                     static_cast<int32_t*>(status), s, opts, &so);
+    else
+      code = attn_decode_paged_ex(d, q->data_ptr(), k->data_ptr(), v->data_ptr(), k->size(0),
+                                  ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch, max_len, scale,
+                                  split, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
+                                  static_cast<int32_t*>(status), s, opts);
+    return {scored ? "attn_decode_paged_score" : "attn_decode_paged", code};
   });
 }
 
 // (q, cu_q_lens, k_pool, v_pool, block_table, seq_lens, max_q_len, max_seq_len, scale, out, lse,
 //  workspace, status, stream, dims, max_ctas, options)
 PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> bool {
+  return guarded([&]() -> Made {
     Reader r(a, n);
     const at::Tensor* q = r.tensor(ScalarType::BFloat16, 3);
     const at::Tensor* cu = r.tensor(ScalarType::Int, 1);
@@ -310,7 +329,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const pa_dims d = r.dims();
     pa_launch_opts lo{};
     const pa_launch_opts* opts = launch_options(r, lo);
-    if (!r.good) return false;
+    if (!r.good) return {};
     const int64_t B = lens->size(0), T = q->size(0), hq = d.num_q_heads, hkv = d.num_kv_heads;
     pa_score_opts so{};
     const bool scored = score_options(r, so, static_cast<int>(hq), B, T, max_len);
@@ -321,7 +340,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.at_least(table, B);
     r.shape(out, T, hq, 128);
     r.shape(lse, T, hq);
-    if (!r.done() || B > INT32_MAX || T > INT32_MAX || table->size(1) > INT32_MAX) return false;
+    if (!r.done() || B > INT32_MAX || T > INT32_MAX || table->size(1) > INT32_MAX) return {};
     const int32_t batch = static_cast<int32_t>(B), rows = static_cast<int32_t>(T);
     const int32_t stride = static_cast<int32_t>(table->size(1));
     const size_t need = workspace ? 0
@@ -330,16 +349,18 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Unlocked unlocked;
     Scratch scratch(workspace, need, st);
     pa_stream_t s = reinterpret_cast<pa_stream_t>(st);
+    pa_status code;
     if (scored)
-      return attn_prefill_chunk_score(d, q->data_ptr(), ptr<const int32_t>(cu), rows, k->data_ptr(), v->data_ptr(),
-                                           k->size(0), ptr<const int32_t>(table), stride, ptr<const int32_t>(lens),
-                                           batch, max_q, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p,
-                                           scratch.bytes, static_cast<int32_t*>(status), s, opts, &so) == PA_OK;
-    return attn_prefill_chunk_ex(d, q->data_ptr(), ptr<const int32_t>(cu), rows, k->data_ptr(), v->data_ptr(),
+      code = attn_prefill_chunk_score(d, q->data_ptr(), ptr<const int32_t>(cu), rows, k->data_ptr(), v->data_ptr(),
                                       k->size(0), ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch,
                                       max_q, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p,
-                                      scratch.bytes,
-                                      static_cast<int32_t*>(status), s, opts) == PA_OK;
+                                      scratch.bytes, static_cast<int32_t*>(status), s, opts, &so);
+    else
+      code = attn_prefill_chunk_ex(d, q->data_ptr(), ptr<const int32_t>(cu), rows, k->data_ptr(), v->data_ptr(),
+                                   k->size(0), ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch,
+                                   max_q, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
+                                   static_cast<int32_t*>(status), s, opts);
+    return {scored ? "attn_prefill_chunk_score" : "attn_prefill_chunk", code};
   });
 }
 
@@ -355,7 +376,7 @@ int64_t row_stride(Reader& r, const at::Tensor* t, int64_t T, int64_t heads) {
 // (q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_freq, interleaved, attn_factor, q_gamma,
 //  k_gamma, eps, q_out, status, stream, dims)
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> bool {
+  return guarded([&]() -> Made {
     Reader r(a, n);
     const at::Tensor* q = r.tensor_of(r.next(), ScalarType::BFloat16);
     const at::Tensor* k = r.tensor_of(r.next(), ScalarType::BFloat16);
@@ -374,7 +395,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* status = r.status();
     cudaStream_t st = r.stream();
     const pa_dims d = r.dims();
-    if (!r.done() || q->dim() != 3) return false;
+    if (!r.done() || q->dim() != 3) return {};
     const int64_t T = q->size(0), hq = d.num_q_heads, hkv = d.num_kv_heads;
     const int64_t qs = row_stride(r, q, T, hq), ks = row_stride(r, k, T, hkv), vs = row_stride(r, v, T, hkv);
     r.shape(pos, T);
@@ -384,21 +405,22 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.shape(qg, 128);
     r.shape(kg, 128);
     r.shape(out, T, hq, 128);
-    if (!r.good || T > INT32_MAX || freq->size(0) > 128) return false;
+    if (!r.good || T > INT32_MAX || freq->size(0) > 128) return {};
     Unlocked unlocked;
-    return rope_append_paged(d, 2 * static_cast<int32_t>(freq->size(0)), interleaved, ptr<const double>(freq),
-                                  factor, q->data_ptr(), qs, k->data_ptr(), ks, v->data_ptr(), vs,
-                                  static_cast<int32_t>(T), ptr<const int32_t>(pos), ptr<const int64_t>(slots),
-                                  ptr<const float>(qg), ptr<const float>(kg), eps, out->data_ptr(), kp->data_ptr(),
-                                  vp->data_ptr(), kp->size(0), static_cast<int32_t*>(status),
-                                  reinterpret_cast<pa_stream_t>(st)) == PA_OK;
+    const pa_status code = rope_append_paged(d, 2 * static_cast<int32_t>(freq->size(0)), interleaved,
+                                             ptr<const double>(freq), factor, q->data_ptr(), qs, k->data_ptr(), ks,
+                                             v->data_ptr(), vs, static_cast<int32_t>(T), ptr<const int32_t>(pos),
+                                             ptr<const int64_t>(slots), ptr<const float>(qg), ptr<const float>(kg),
+                                             eps, out->data_ptr(), kp->data_ptr(), vp->data_ptr(), kp->size(0),
+                                             static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
+    return {"rope_append_paged", code};
   });
 }
 
 // (cached_lens, new_lens, block_table, free_pages, free_count, num_pages, total_rows, free_count_out,
 //  cu_new_lens, seq_lens, positions, slot_map, status, stream)
 PyObject* step_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> bool {
+  return guarded([&]() -> Made {
     Reader r(a, n);
     const at::Tensor* cached = r.tensor(ScalarType::Int, 1);
     const at::Tensor* fresh = r.tensor(ScalarType::Int, 1);
@@ -414,7 +436,7 @@ PyObject* step_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* slots = r.tensor(ScalarType::Long, 1);
     void* status = r.status();
     cudaStream_t st = r.stream();
-    if (!r.done()) return false;
+    if (!r.done()) return {};
     const int64_t B = cached->size(0);
     r.require(rows >= 0 && B <= INT32_MAX && table->size(1) <= INT32_MAX && free->size(0) <= INT32_MAX);
     r.shape(fresh, B);
@@ -425,21 +447,23 @@ PyObject* step_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.shape(lens, B);
     r.shape(pos, rows);
     r.shape(slots, rows);
-    if (!r.good) return false;
+    if (!r.good) return {};
     Unlocked unlocked;
-    return paged_step_plan(ptr<const int32_t>(cached), ptr<const int32_t>(fresh), static_cast<int32_t>(B),
-                                ptr<int32_t>(table), static_cast<int32_t>(table->size(1)), ptr<const int32_t>(free),
-                                static_cast<int32_t>(free->size(0)), ptr<const int32_t>(count), pages, rows,
-                                ptr<int32_t>(count_out), ptr<int32_t>(cu), ptr<int32_t>(lens), ptr<int32_t>(pos),
-                                ptr<int64_t>(slots), static_cast<int32_t*>(status),
-                                reinterpret_cast<pa_stream_t>(st)) == PA_OK;
+    const pa_status code = paged_step_plan(ptr<const int32_t>(cached), ptr<const int32_t>(fresh),
+                                           static_cast<int32_t>(B), ptr<int32_t>(table),
+                                           static_cast<int32_t>(table->size(1)), ptr<const int32_t>(free),
+                                           static_cast<int32_t>(free->size(0)), ptr<const int32_t>(count), pages,
+                                           rows, ptr<int32_t>(count_out), ptr<int32_t>(cu), ptr<int32_t>(lens),
+                                           ptr<int32_t>(pos), ptr<int64_t>(slots), static_cast<int32_t*>(status),
+                                           reinterpret_cast<pa_stream_t>(st));
+    return {"paged_step_plan", code};
   });
 }
 
 // (begin_pages, end_pages, block_table, free_pages, free_count, num_pages, free_count_out, status,
 //  stream)
 PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> bool {
+  return guarded([&]() -> Made {
     Reader r(a, n);
     const at::Tensor* begin = r.tensor(ScalarType::Int, 1);
     const at::Tensor* end = r.tensor(ScalarType::Int, 1);
@@ -450,21 +474,33 @@ PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* count_out = r.tensor(ScalarType::Int, 1);
     void* status = r.status();
     cudaStream_t st = r.stream();
-    if (!r.done()) return false;
+    if (!r.done()) return {};
     const int64_t B = begin->size(0);
     r.require(B <= INT32_MAX && table->size(1) <= INT32_MAX && free->size(0) <= INT32_MAX);
     r.shape(end, B);
     r.at_least(table, B);
     r.at_least(count, 1);
     r.shape(count_out, 1);
-    if (!r.good) return false;
+    if (!r.good) return {};
     Unlocked unlocked;
-    return paged_release(ptr<const int32_t>(begin), ptr<const int32_t>(end), static_cast<int32_t>(B),
-                              ptr<int32_t>(table), static_cast<int32_t>(table->size(1)), ptr<int32_t>(free),
-                              static_cast<int32_t>(free->size(0)), ptr<const int32_t>(count), pages,
-                              ptr<int32_t>(count_out), static_cast<int32_t*>(status),
-                              reinterpret_cast<pa_stream_t>(st)) == PA_OK;
+    const pa_status code = paged_release(ptr<const int32_t>(begin), ptr<const int32_t>(end), static_cast<int32_t>(B),
+                                         ptr<int32_t>(table), static_cast<int32_t>(table->size(1)),
+                                         ptr<int32_t>(free), static_cast<int32_t>(free->size(0)),
+                                         ptr<const int32_t>(count), pages, ptr<int32_t>(count_out),
+                                         static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
+    return {"paged_release", code};
   });
+}
+
+PyObject* set_error(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 1 || !PyType_Check(a[0])) {
+    PyErr_SetString(PyExc_TypeError, "set_error takes a class");
+    return nullptr;
+  }
+  Py_INCREF(a[0]);
+  Py_XDECREF(error_class);
+  error_class = a[0];
+  Py_RETURN_NONE;
 }
 
 #define PA_METHOD(name, doc) \
@@ -472,7 +508,8 @@ PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {
     PA_METHOD(decode, "attn_decode_paged"),      PA_METHOD(prefill, "attn_prefill_chunk"),
     PA_METHOD(rope, "rope_append_paged"),        PA_METHOD(step_plan, "paged_step_plan"),
-    PA_METHOD(release, "paged_release"),         {nullptr, nullptr, 0, nullptr},
+    PA_METHOD(release, "paged_release"),         PA_METHOD(set_error, "class of the errors raised"),
+    {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_call", "Fast path of the binding", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
