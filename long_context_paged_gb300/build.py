@@ -55,7 +55,10 @@ def _stale(target: str, deps) -> bool:
 def _build_fast(verbose: bool, force: bool):
     """Compile the binding's fast path; returns its error text, or None. Rebuilt when its source, the
     C ABI or the installed PyTorch changed."""
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        return f"PyTorch cannot be imported ({e})"
     stamp = os.path.join(BUILD, "_pa_call.torch")
     known = open(stamp).read() if os.path.exists(stamp) else ""
     if not force and known == torch.__version__ and not _stale(FAST, [FAST_SRC, __file__] + _headers()):
