@@ -15,7 +15,7 @@
 // thread at most) and then writes its share of the rows, so that nothing is exchanged between
 // CTAs. Where an output is an input's buffer (lengths or free count updated in place), the grid is one
 // cluster of at most 8 CTAs, whose barrier orders the reads before the writes; else any grid does
-// (57,000 rows: 8.4 us, in place 11.6 us).
+// (57,000 rows: 8.8 us, in place 11.9 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -32,10 +32,12 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxCluster = 8;
-// Rows (or requests) one CTA takes before a second one is launched. 512 to 4,096 measure alike (4,096
-// requests with 57,000 rows 8.4 us, 32 requests with 4,127 rows 5.0 us): the chain of loads, scan and
-// stores is what takes the time.
-constexpr int kRowsPerCta = 2048;
+// A call has a CTA for every so many rows (or requests), up to one per SM, in place up to kMaxCluster. A CTA
+// writes 4 consecutive rows a thread, 4,096 of them at a pass, so from 1,024 on the rows need no more CTAs
+// than 4,096 each would give: 57,000 rows take 8.9 us at 1,024 to 4,096 and 11.8 at 8,192, 4,127 rows 5.1
+// and 6.2. The requests' own work (a new page's search and table entry) is spread over all of them: 4,096
+// requests of a token each, all with a new page, 9.3 us at 512, 9.4 at 1,024, 10.8 at 2,048, 14.1 at 4,096.
+constexpr int kRowsPerCta = 1024;
 
 struct PlanParams {
   const int32_t* cached;
