@@ -12,7 +12,7 @@ import numpy as np
 from . import as_f64, gather_keys, kv_head_of
 
 __all__ = ["step_plan", "release", "rope_rows", "visible", "attend_scored", "decode_scored",
-           "prefill_scored"]
+           "prefill_scored", "rope_frequencies"]
 
 
 def step_plan(cached, new, table, free, count, num_pages, total_rows, page_size=16):
@@ -164,3 +164,36 @@ def decode_scored(q, k_pool, v_pool, table, seq_lens, scale, *, rows=None, **o):
     """One query row per sequence, at its last position."""
     B = len(seq_lens)
     return prefill_scored(q, np.arange(B + 1), k_pool, v_pool, table, seq_lens, scale, rows=rows, **o)
+
+
+def rope_frequencies(rot_dim, theta, kind="none", factor=1.0, original=32768, low_freq_factor=1.0,
+                     high_freq_factor=4.0, beta_fast=32.0, beta_slow=1.0, attn_factor=0.0):
+    """(frequencies [rot_dim / 2], factor of cos and sin), pair by pair from the definitions of the
+    stretchings: by wavelength (llama3), by rotations over the original context (yarn)."""
+    freqs, scale = [], 1.0
+    if kind == "yarn":
+        # the pair index (a real number) whose wavelength fits `turns` times into the original context
+        pair = lambda turns: rot_dim / 2 * math.log(original / (2 * math.pi * turns)) / math.log(theta)
+        first, last = max(0, math.floor(pair(beta_fast))), min(rot_dim - 1, math.ceil(pair(beta_slow)))
+        scale = attn_factor if attn_factor > 0 else 1.0 + 0.1 * math.log(max(factor, 1.0))
+    for i in range(rot_dim // 2):
+        f = theta ** (-2.0 * i / rot_dim)
+        if kind == "linear":
+            f = f / factor
+        elif kind == "ntk":
+            f = (theta * factor ** (rot_dim / (rot_dim - 2))) ** (-2.0 * i / rot_dim)
+        elif kind == "llama3":
+            wavelength = 2 * math.pi / f
+            if wavelength > original / low_freq_factor:
+                f = f / factor
+            elif wavelength >= original / high_freq_factor:
+                kept = (original / wavelength - low_freq_factor) / (high_freq_factor - low_freq_factor)
+                f = (1 - kept) * f / factor + kept * f
+        elif kind == "yarn":
+            if i >= last:
+                f = f / factor
+            elif i > first:
+                divided = (i - first) / (last - first)
+                f = divided * f / factor + (1 - divided) * f
+        freqs.append(f)
+    return np.array(freqs), scale

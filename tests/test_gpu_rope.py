@@ -174,3 +174,35 @@ def test_non_finite_rows_stay_in_their_row(cuda_lib):
     kk = kp.view(-1, 8, 128)[:3]
     assert bool(kk[0].isfinite().all()) and bool(kk[2].isfinite().all())
     assert torch.equal(vp.view(-1, 8, 128)[:3].view(torch.int16), v.view(torch.int16))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hkv", [1, 2, 8])
+def test_rows_past_a_cta_s_first_table(cuda_lib, hkv, interleaved):
+    """21,001 rows: every CTA fills its table of angles at least three times on any GPU of up to 152 SMs
+    (two CTAs an SM, 32 tokens a table: 9,728 tokens are held at once)."""
+    T, hq = 21_001, 2 * hkv
+    qkv = bf(T, hq + 2 * hkv, 128, seed=1)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    pages = -(-T // 16)
+    kp = torch.zeros(pages, 16, hkv, 128, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    freq, fac = cuda_lib.rope_inv_freq(scaling="yarn", factor=4.0)
+    rng = np.random.default_rng(hkv)
+    pos = rng.integers(0, 131072, T)
+    slots = torch.tensor(rng.permutation(pages * 16)[:T], device="cuda")
+    gamma = 1 + 0.2 * torch.randn(128, device="cuda")
+    out = cuda_lib.rope_append_paged(q, k, v, torch.tensor(pos, dtype=torch.int32, device="cuda"), slots, kp, vp,
+                                     freq, interleaved=interleaved, attn_factor=fac, q_gamma=gamma, k_gamma=gamma,
+                                     dims=(hq, hkv, 128, 16))
+    torch.cuda.synchronize()
+    # rows of every table of a CTA, its first and last tokens among them
+    rows = np.unique(np.concatenate([rng.integers(0, T, 500), np.arange(9700, 9760), [0, 31, 32, T - 1]]))
+    gm = gamma.cpu().numpy()
+    at = torch.tensor(rows, device="cuda")
+    for x, got in ((q, out[at]), (k, kp.view(-1, hkv, 128)[slots[at]])):
+        y = as_f64(bits(x[at].contiguous()))
+        want = S.rope_rows(y, pos[rows], freq.cpu().numpy(), interleaved, fac, gm)
+        n = y / np.sqrt((y * y).mean(-1, keepdims=True) + 1e-6) * gm
+        assert_rounded(got.contiguous(), want, 2 * np.abs(n).max(-1, keepdims=True) * fac)
+    assert torch.equal(vp.view(-1, hkv, 128)[slots], v)

@@ -261,3 +261,18 @@ def test_step_plan_lengths_that_sum_past_32_bits(cuda_lib, new, in_place):
     assert np.array_equal(got.slot_map.cpu().numpy()[:rows], want["slots"][:rows])
     assert (got.slot_map[rows:] == -1).all() and (got.positions[rows:] == 0).all()
     assert cuda_lib.read_device_status(status) == BITS["length"] and want["flags"] == {"length"}
+
+
+@pytest.mark.parametrize("at", [(0, 1), (1, 0), (2, 0), (3, 3)])
+@pytest.mark.parametrize("B", [1, 37, 4000])
+def test_step_plan_into_part_of_a_larger_buffer(cuda_lib, B, at):
+    """positions and slot_map at offsets that 16-byte stores cannot take; what lies around them stays."""
+    a = make(B + 5, B, 60, 50, 1.0, 3)
+    want = S.step_plan(*a)
+    rows = a[6]
+    pos = torch.full((rows + 8,), 77, dtype=torch.int32, device="cuda")
+    slots = torch.full((rows + 8,), 77, dtype=torch.int64, device="cuda")
+    p, m = pos[at[0]:at[0] + rows], slots[at[1]:at[1] + rows]
+    check_plan(*run_plan(cuda_lib, *a, positions=p, slot_map=m), want)
+    assert bool((pos[:at[0]] == 77).all()) and bool((pos[at[0] + rows:] == 77).all())
+    assert bool((slots[:at[1]] == 77).all()) and bool((slots[at[1] + rows:] == 77).all())
