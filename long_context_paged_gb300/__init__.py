@@ -221,6 +221,8 @@ def _empty(shape, dtype, device, stream):
     work ran."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # (any object that has a stream's handle will do)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
