@@ -7,8 +7,8 @@ namespace pa {
 
 // A launch as a programmatic dependent of the work before it on the stream: it may be set up during
 // that work's tail, and its kernel starts with await_previous(), before any access to memory. Measured
-// against plain launches, calls in a row: 31 rotary rows 4.6 -> 3.8 us, 4,127 16.7 -> 14.4, a plan of
-// 32 requests 7.8 -> 5.8. (A kernel that in turn lets the next one start early gained nothing more.)
+// against plain launches, calls in a row: 31 rotary rows 4.1 -> 3.1 us, 4,127 17.3 -> 15.1, a plan of
+// 32 requests 8.2 -> 5.4, one of 4,096 10.3 -> 8.8. (A kernel that in turn lets the next one start early gained nothing more.)
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
                              cudaStream_t stream, int cluster, const Args&... args) {

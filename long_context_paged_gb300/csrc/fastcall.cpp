@@ -3,8 +3,9 @@
 // A small call's time is its host time: checking a dozen tensors through Python attributes and
 // converting two dozen arguments through ctypes takes up to 15 us, the launch 2-3 us, the kernel often
 // less. Measured, one call after another, through ctypes and through this file: decode of one sequence
-// of 1,000 keys 18.3 and 4.8 us, 375 prefill rows 24 and 18.4 (15.9 of it the kernel's), 31 rotary rows
-// 12.0 and 4.1, a plan for 32 requests 11.2 and 8.2 (5.7 of it the kernel's).
+// of 1,000 keys 18.9 and 4.7 us, 375 prefill rows 21.1 and 14.4 (14.3 of it the kernel's), 31 rotary rows
+// 12.7 and 3.0, a plan for 32 requests 10.8 and 5.4 (5.3 of it the kernel's), a release of 512 requests'
+// pages with a copy of the table 15.9 and 10.3.
 //
 // These functions take the same arguments as the Python wrappers, make the same checks on the tensors
 // themselves, and call the C ABI. They decide nothing else: whatever is not plainly right (a wrong

@@ -14,13 +14,18 @@
 //    their maximum, and the weights go back as bf16 in one pass. The cap's tanh and the bias are taken in
 //    that same pass wherever a bound of the scores' maximum follows from the products' maximum (see
 //    score_bound), as a polynomial and a stepped distance on the FMA pipe, whose work then hides behind
-//    the MUFU unit's exponentials. Measured (4,096 queries at 61,440): masks alone 1,300 us (1,640
-//    TFLOP/s), as the plain kernel; cap 1,892 us (an exponential and a quotient per score took 3,146, a
-//    pass of its own for the polynomial 2,309, two polynomials by range 2,480: the code of the pass then
-//    no longer stays in the instruction cache); bias 1,746 us; both 2,590 us. What bounds it is a row's
+//    the MUFU unit's exponentials. Measured (4,096 queries at 61,440): masks alone 1,270-1,330 us (1,600-
+//    1,680 TFLOP/s), as the plain kernel; cap 1,920 us (an exponential and a quotient per score took 3,146,
+//    a pass of its own for the polynomial 2,309, two polynomials by range 2,480: the code of the pass then
+//    no longer stays in the instruction cache); bias 1,740 us; both 2,560 us. What bounds it is a row's
 //    chain S -> weights -> P V: each paired FMA more per two scores costs 85 us. 16 softmax warps, two
 //    threads per row meeting at a barrier per tile, were slower (1,611 us with masks alone, 2,540 with a
 //    cap): at 96 to 104 registers a thread the pass spills.
+//  * Rounding. The weights are rounded to bf16 for P V: the tensor cores take P and V in one type, and V
+//    is bf16. Each is off by at most 2^-8 of itself, with either sign; their sum l takes them unrounded.
+//    Outputs are off by 0.0023 of their norm against 64 bits where the last rounding alone is off by
+//    0.0017. P in two bf16 parts would take P V, half of the tensor work, twice. The plain kernel does the
+//    same; the decode keeps its weights in fp32.
 //  * Non-finite K and V rows are kept from the rows that do not see them: the slots behind a sequence's
 //    end are cleared by the producers, and rows that a non-finite value reached are repaired (repair_rows).
 #include <algorithm>
@@ -68,9 +73,9 @@ constexpr int kVStages = 3;   // V is needed a whole P*V later than K: one more 
 // Fixed cost of a job beyond its key tiles, in tiles (its epilogue and the restart of its chain)
 constexpr int kJobCost = 3;
 // Up to this many keys a call whose jobs fit one to a CTA is not split. One CTA a job, without plan
-// and merge, is faster while a job has few tiles (300 queries at 700: 23.0 us, split 27.6; 375 at 0:
-// 15.7, split 27.4) and no longer at 2,000 keys (300 at 1,700: 33.1, split 30.1; 100 at 1,948: 31.9,
-// split 36.7).
+// and merge, is faster while a job has few tiles (300 queries at 700: 22.2 us, split 28.0; 375 at 0:
+// 14.3, split 25.2) and no longer at 2,000 keys (300 at 1,700: 34.0, split 32.2; 100 at 1,948: 32.7,
+// split 39.3). The host's bound of the lengths decides, since the grid does not wait for the lengths.
 constexpr int kWholeKeys = 1024;
 // A partial result: o [2 heads][32 float4 columns][128 rows], then lse [2][128] fp32.
 constexpr size_t kRecordO = 2 * 128 * 128 * sizeof(float);

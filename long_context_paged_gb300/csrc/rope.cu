@@ -40,7 +40,7 @@ constexpr int kThreads = 256;
 constexpr int kUnits = kThreads / 16;       // units of a CTA pass: two a warp
 constexpr int kMaxPairs = kHeadDim / 2;
 constexpr int kTableTokens = 32;            // tokens whose cosines and sines are held at a time
-// Two CTAs per SM: a pass in flight and one ahead of it for every warp, at 122 registers. Three or four
+// Two CTAs per SM: a pass in flight and one ahead of it for every warp, at 123 registers. Three or four
 // CTAs of 80 or 64 registers spill and measured slower (16.8 and 24.1 against 13.2 us for 4,127 rows).
 constexpr int kCtasPerSm = 2;
 
