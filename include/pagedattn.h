@@ -283,7 +283,7 @@ pa_status attn_prefill_chunk_ex(pa_dims dims, const void* q, const int32_t* cu_q
  *                   of the row's document; past i: the row sees the prefix only
  * Rows that see a NaN or an infinity in K or V get what the formula gives; rows that do not see it
  * are unmoved. (In the prefill, rows that share a key tile with such a value and do not see it are
- * computed a second time, at up to 1.3 us a key for the 128 rows of a query tile.)
+ * computed a second time, at up to 1.5 us a key for the 128 rows of a query tile.)
  * The decode weighs V in fp32; the prefill rounds the weights to bf16 before they meet V, as the
  * plain call does (outputs within 0.0023 of their norm, the last rounding alone 0.0017).
  * A chunk longer than max_q_len is flagged PA_DEV_ERR_LENGTH and produces nothing. max_seq_len also

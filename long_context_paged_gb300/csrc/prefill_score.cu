@@ -493,6 +493,8 @@ __device__ __forceinline__ bool word_not_finite(uint32_t w) {
   return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
 }
 
+// x, or fp32's smallest normal number where it is below (NaN stays NaN).
+__device__ __forceinline__ float above_zero(float x) { return x < 1.17549435e-38f ? 1.17549435e-38f : x; }
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
 
 // Two pages' first slots: the 32 keys from `base` on. Entries of keys outside `used` are not looked up.
@@ -508,26 +510,31 @@ __device__ __forceinline__ void word_slots(const P& p, const int32_t* bt_row, in
 // The non-finite values of V that rows of a warp see: bit r of word k, row r of the warp in dim 4 lane + k.
 struct NonFinite {
   uint32_t nan[4], up[4], down[4];
-  // What row r's weighted mean is in dim 4 lane + k: x where it sees finite values alone
-  __device__ __forceinline__ bool over(int r, int k, float& x) const {
+  // Whether x is known to be row r's weighted mean in dim 4 lane + k, or is so now: a finite value was not
+  // reached by another key's; NaN or infinities of both signs make it NaN, whatever their weights; an
+  // infinity makes it that infinity, unless its own weight is 0 (a score of -inf) and it is NaN.
+  __device__ __forceinline__ bool settled(int r, int k, float& x) const {
+    if (!not_finite(x)) return true;
     const bool u = up[k] >> r & 1u, d = down[k] >> r & 1u;
-    if ((nan[k] >> r & 1u) || (u && d)) x = CUDART_NAN_F;
-    else if (u || d) x = u ? CUDART_INF_F : -CUDART_INF_F;
-    else return false;
-    return true;
+    if ((nan[k] >> r & 1u) || (u && d)) {
+      x = CUDART_NAN_F;
+      return true;
+    }
+    return (u && x == CUDART_INF_F) || (d && x == -CUDART_INF_F);
   }
 };
 
 // A masked key's P is 0, and 0 times a non-finite V is NaN: a V row that one row of a tile sees and
 // another does not (a later token, another document, the rest of a prompt's page) reaches both through
 // the MMA. A job's rows that came out non-finite are put right here, 32 rows of one head by a warp:
-//   1. One walk over the V rows that any of them sees notes who sees which non-finite values: where a row
-//      sees some, they are its result (weights are positive), and the rest of it may be right already.
-//   2. Rows that are non-finite where what they see is finite are computed again from their visible keys,
-//      kRows at a time: a key per lane for the scores, four dims per lane for the sum.
+//   1. One walk over the V rows that any of them sees notes who sees which non-finite values; where that
+//      settles what a row is (NonFinite::settled), nothing more is done.
+//   2. The others are computed again from their visible keys, kRows at a time: a key per lane for the
+//      scores, four dims per lane for the sum. Weights and rescalings stay above 0 (fp32's smallest normal
+//      number) where the score is a number, that 0 times an infinity is not taken for NaN.
 // Only inputs that hold non-finite values come here, and once their job's rows are stored: no wait of
 // another warp runs meanwhile. Measured with all rows of a job non-finite, per key of the job: 0.06 us for
-// the walk, 1.3 us where every row is computed again (4,093 keys: 0.23 and 5.3 ms beside 58 us).
+// the walk, 1.5 us where every row is computed again (4,093 keys: 0.24 and 5.9 ms beside 58 us).
 template <class P>
 __device__ __forceinline__ void repair_rows(const P& p, const TileDesc& d, int g, int t, int quarter) {
   constexpr int kRows = 8;
@@ -618,7 +625,7 @@ __device__ __forceinline__ void repair_rows(const P& p, const TileDesc& d, int g
     bool wrong = false;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (!nf.over(r, k, x[k])) wrong = wrong || not_finite(x[k]);
+      if (!nf.settled(r, k, x[k])) wrong = true;
     if (__any_sync(0xffffffffu, wrong)) again |= 1u << r;
     else store(r, x);
   }
@@ -673,13 +680,13 @@ __device__ __forceinline__ void repair_rows(const P& p, const TileDesc& d, int g
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (mx > top[i]) {
-          const float alpha = fast_exp2(top[i] - mx);
+          const float alpha = top[i] == -CUDART_INF_F ? 0.f : above_zero(fast_exp2(top[i] - mx));
           top[i] = mx;
           sum[i] *= alpha;
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[i][k] *= alpha;
         }
-        s[i] = sees && !(x == -CUDART_INF_F) ? fast_exp2(x - top[i]) : 0.f;
+        s[i] = sees && !(x == -CUDART_INF_F) ? above_zero(fast_exp2(x - top[i])) : 0.f;
         sum[i] += s[i];
       }
 #pragma unroll 1
@@ -694,12 +701,11 @@ __device__ __forceinline__ void repair_rows(const P& p, const TileDesc& d, int g
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          float v[4] = {bf16lo(vw[c].x), bf16hi(vw[c].x), bf16lo(vw[c].y), bf16hi(vw[c].y)};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = not_finite(v[k]) ? 0.f : v[k];  // (who sees it gets it below)
+          const float v[4] = {bf16lo(vw[c].x), bf16hi(vw[c].x), bf16lo(vw[c].y), bf16hi(vw[c].y)};
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
             const float pr = __shfl_sync(0xffffffffu, s[i], c0 + c);
+            if (!(seen[i] >> (c0 + c) & 1u)) continue;
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][k] = fmaf(pr, v[k], acc[i][k]);
           }
@@ -710,12 +716,8 @@ __device__ __forceinline__ void repair_rows(const P& p, const TileDesc& d, int g
     for (int i = 0; i < kRows; ++i) {
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-      const float f = sum[i] == 0.f ? 0.f : 1.0f / sum[i];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[i][k] *= f;
-        if (sum[i] != 0.f) nf.over(row[i], k, acc[i][k]);
-      }
+      for (int k = 0; k < 4; ++k) acc[i][k] = sum[i] == 0.f ? 0.f : acc[i][k] / sum[i];
       store(row[i], acc[i]);
     }
   }

@@ -162,3 +162,42 @@ def test_what_non_finite_values_cost(cuda_lib):
     assert us(lambda inp: put(inp.v_pools[0], inp, 0, 1020, nan), wide) < 120 * clean
     assert us(lambda inp: [put(inp.v_pools[0], inp, 0, k, nan) for k in (5, 6, 7)], hide) < 120 * clean
     assert us(behind, wide) < 3 * clean
+
+
+@pytest.mark.parametrize("max_ctas", [None, 5])
+def test_infinities_under_weights_of_zero_and_far_below_one(cuda_lib, max_ctas):
+    """A key whose score is -inf has a weight of exactly 0: an infinity of its V makes the row NaN, as the
+    formula's 0 times infinity does, beside rows that do not see it; a weight of e^-100 is none that fp32
+    holds, and its infinity stays one; rows whose scores are all -inf are 0 whatever their V holds."""
+    n, off = 150, 90
+    for seed in range(4):
+        inp = W.make_paged(680 + seed, [off + n], [n], device="cuda")
+        K, V, inf = inp.k_pools[0], inp.v_pools[0], float("inf")
+        inp.q[0][:, :, 0] = inp.q[0][:, :, 0].abs() + 0.5      # the sign of dim 0 is known
+        put(K, inp, 0, 20, -inf, slice(0, 4), 0)               # score -inf in heads 0 .. 7
+        put(V, inp, 0, 20, inf, slice(0, 4), slice(0, 20))
+        put(V, inp, 0, 21, -inf, slice(0, 8), slice(10, 30))   # an ordinary weight
+        put(V, inp, 0, off + 70, inf, slice(0, 8), slice(25, 40))   # not seen by the rows before it
+        put(K, inp, 0, off + 40, -inf, slice(0, 2), 0)         # later rows: -inf again, finite V
+        for o in (dict(window=1000), dict(softcap=8.0, window=70), dict(window=60, slopes=FLAT),
+                  dict(row_start=np.full(n, 20), window=50), dict(row_start=np.maximum(off + np.arange(n) - 3, 0))):
+            run(cuda_lib, inp, o, max_ctas=max_ctas)
+        # one key far above the others: weights of e^-100 and less
+        put(K, inp, 0, 5, 0.0, slice(4, 8))
+        K[int(inp.host_block_table[0, 0]), 5, 4:8, 0] = 1280.0
+        put(V, inp, 0, 8, inf, slice(4, 8), slice(60, 70))
+        inp.q[0][:, :, 0] = 1.0
+        run(cuda_lib, inp, dict(window=1000), max_ctas=max_ctas)
+
+
+def test_rows_whose_scores_are_all_minus_infinity_are_zero(cuda_lib):
+    n, off = 40, 100
+    inp = W.make_paged(690, [off + n], [n], device="cuda")
+    inp.q[0][:, :, 0] = 1.0
+    for key in range(off + 10, off + 14):
+        put(inp.k_pools[0], inp, 0, key, float("-inf"), slice(None), 0)
+        put(inp.v_pools[0], inp, 0, key, float("nan"), slice(None), slice(0, 64))
+        put(inp.v_pools[0], inp, 0, key, float("inf"), slice(None), slice(64, 100))
+    for o in (dict(window=1), dict(window=3), dict(window=1, slopes=FLAT)):
+        for max_ctas in (None, 3):
+            run(cuda_lib, inp, o, max_ctas=max_ctas)
