@@ -174,6 +174,14 @@ __device__ __forceinline__ SeqView<DecodeScoreParams> seq_view(const DecodeScore
 // 1 / l of a softmax sum: 0 when nothing carried weight (no key visible, or every score -inf)
 __device__ __forceinline__ float inverse_or_zero(float l) { return l == 0.f ? 0.f : 1.0f / l; }
 
+// o of a row whose sum's inverse is inv: 0 when nothing carried weight, whatever the V of keys with a
+// score of -inf holds (0 times an infinity is NaN, and so is 0 times that). Rows that other keys carry
+// keep the NaN. Partial results keep it too: the other partials decide.
+template <class P>
+__device__ __forceinline__ float weighed(float o, float inv) {
+  return P::kScore && inv == 0.f ? 0.f : o * inv;
+}
+
 // The part of the log-sum-exp that the kernels leave out: they count a bias's distances from the
 // nearest visible key (see ScoreParams).
 template <class P>
@@ -631,10 +639,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_splitkv_kernel(const P p) 
       // (with several pages per stage a warp pair may have seen no page of this range: l = 0,
       // and its record is o = 0, lse = -inf, which the merge weighs by 0)
       const float inv = P::kScore ? inverse_or_zero(l_h) : (kSlots == 1 || l_h > 0.f) ? 1.0f / l_h : 0.f;
+      const bool complete = kSlots == 1 && lp0 == 0 && lp1 == n_pages;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] *= inv;
+      for (int i = 0; i < 8; ++i) o[i] = complete ? weighed<P>(o[i], inv) : o[i] * inv;
       const float lse_h = (m_h + log2f(l_h)) * kLn2;
-      if (kSlots == 1 && lp0 == 0 && lp1 == n_pages) {
+      if (complete) {
         uint4 w;
         w.x = pack_bf16x2(o[0], o[1]);
         w.y = pack_bf16x2(o[2], o[3]);
@@ -775,7 +784,8 @@ __global__ void __launch_bounds__(kWarps * 32) decode_merge_kernel(const P p) {
   }
   const float inv = P::kScore ? inverse_or_zero(wsum) : 1.0f / wsum;
   *reinterpret_cast<uint2*>(orow) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      make_uint2(pack_bf16x2(weighed<P>(acc.x, inv), weighed<P>(acc.y, inv)),
+                 pack_bf16x2(weighed<P>(acc.z, inv), weighed<P>(acc.w, inv)));
   if (lane == 0 && p.lse != nullptr) p.lse[b * hq + h] = (M + log2f(wsum)) * kLn2 + lse_shift(p, b, h);
 }
 
@@ -853,7 +863,7 @@ __global__ void __launch_bounds__(kMergeWarpsSmall * 32) decode_merge_dims_kerne
     a += sk * red_o[k][lane];
     wsum += sk * red_w[k];
   }
-  const float o_d = P::kScore ? a * inverse_or_zero(wsum) : a / wsum;
+  const float o_d = P::kScore ? weighed<P>(a, inverse_or_zero(wsum)) : a / wsum;
   orow[d] = static_cast<uint16_t>(pack_bf16x2(o_d, 0.f) & 0xffffu);
   if (blockIdx.z == 0 && lane == 0 && p.lse != nullptr)
     p.lse[b * hq + h] = (M + log2f(wsum)) * kLn2 + lse_shift(p, b, h);
@@ -1194,7 +1204,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) decode_cluster_kernel(const 
     const int head = 2 * g0 + qh;
     const float inv = P::kScore ? inverse_or_zero(l[k]) : l[k] > 0.f ? 1.0f / l[k] : 0.f;
     p.out[(static_cast<int64_t>(b) * kHqT + head) * kHeadDim + d] =
-        static_cast<uint16_t>(pack_bf16x2(o[k] * inv, 0.f) & 0xffffu);
+        static_cast<uint16_t>(pack_bf16x2(weighed<P>(o[k], inv), 0.f) & 0xffffu);
     if (d == 0 && p.lse != nullptr)
       p.lse[b * kHqT + head] = (M[k] + log2f(l[k])) * kLn2 + lse_shift(p, b, head);
   }

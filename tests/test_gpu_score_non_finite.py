@@ -201,3 +201,41 @@ def test_rows_whose_scores_are_all_minus_infinity_are_zero(cuda_lib):
     for o in (dict(window=1), dict(window=3), dict(window=1, slopes=FLAT)):
         for max_ctas in (None, 3):
             run(cuda_lib, inp, o, max_ctas=max_ctas)
+
+
+@pytest.mark.parametrize("split_tokens", [0, 16, 64])
+@pytest.mark.parametrize("hkv", [8, 2])
+def test_decode_rows_whose_scores_are_all_minus_infinity_are_zero(cuda_lib, hkv, split_tokens):
+    """One launch, and split with its merges: the keys seen have scores of -inf, their V holds NaN and
+    infinities; a row that also sees an ordinary key is NaN there, as the formula's 0 times infinity is."""
+    hq, dims = 2 * hkv, (2 * hkv, hkv, 128, 16)
+    lens = [3, 40, 700, 5000, 90, 1]
+    seen = [3, 40, 33, 300, 7, 1]                       # keys of the window
+    B = len(lens)
+    pages = [-(-n // 16) for n in lens]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    kp, vp = (torch.randn(sum(pages), 16, hkv, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(B, hq, 128, generator=g, device="cuda").to(torch.bfloat16)
+    q[:, :, 0] = 1.0
+    table = torch.zeros(B, max(pages), dtype=torch.int32, device="cuda")
+    at = np.concatenate([[0], np.cumsum(pages)])
+    for b in range(B):
+        table[b, :pages[b]] = torch.arange(at[b], at[b + 1], device="cuda")
+    for b, n in enumerate(lens):
+        for key in range(n - seen[b], n):
+            kp[int(at[b]) + key // 16, key % 16, :, 0] = float("-inf")
+            vp[int(at[b]) + key // 16, key % 16, :, 5:60] = float("inf") if key % 2 else float("nan")
+    start = torch.tensor([n - s for n, s in zip(lens, seen)], dtype=torch.int32, device="cuda")
+    call = lambda start: cuda_lib.attn_decode_paged(
+        q, kp, vp, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens), 0.09,
+        split_tokens=split_tokens, row_start=start, dims=dims)
+    out, lse = call(start)
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+    more = torch.clamp(start - 1, min=0)
+    out, lse = call(more)
+    for b in range(B):
+        if int(more[b]) < int(start[b]):               # the ordinary key carries the row
+            assert bool(out[b, :, 5:60].isnan().all()) and bool(out[b, :, 60:].isfinite().all())
+            assert bool(lse[b].isfinite().all())
+        else:
+            assert bool((out[b] == 0).all())
