@@ -282,8 +282,9 @@ pa_status attn_prefill_chunk_ex(pa_dims dims, const void* q, const int32_t* cu_q
  *   row_start       int32 on the device, per query row ([batch] / [total_q]), or NULL: first key
  *                   of the row's document; past i: the row sees the prefix only
  * Rows that see a NaN or an infinity in K or V get what the formula gives (a weight of 0 times an
- * infinity is NaN; the decode's weights are 0 from 2^-126 down); rows that do not see it are unmoved. (In the prefill, rows that share a key tile with such a value and do not see it are
- * computed a second time, at up to 1.5 us a key for the 128 rows of a query tile.)
+ * infinity is NaN; the decode's weights are 0 below 2^-126); rows that do not see it are unmoved.
+ * (In the prefill, rows that share a key tile with such a value and do not see it are computed a
+ * second time, at up to 1.5 us a key for the 128 rows of a query tile.)
  * The decode weighs V in fp32; the prefill rounds the weights to bf16 before they meet V, as the
  * plain call does (outputs within 0.0023 of their norm, the last rounding alone 0.0017).
  * A chunk longer than max_q_len is flagged PA_DEV_ERR_LENGTH and produces nothing. max_seq_len also

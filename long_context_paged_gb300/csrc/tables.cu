@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
   }
   const int all = ctas * kThreads, id = rank * kThreads + tid;
   for (int b = id; b <= p.batch; b += all) p.cu[b] = s.cu[b];
-  const int total = s.cu[p.batch];
+  const int total = s.cu[p.batch], rows_end = min(total, p.total_rows);
   // the served needs are a prefix of all needs: everything up to the free count, cut back to
   // where the last served request ends
   int used = s.need[p.batch];
@@ -204,13 +204,13 @@ __global__ void __launch_bounds__(kThreads, 1) step_plan_kernel(const PlanParams
   for (int64_t t0 = 4ll * id; t0 < p.total_rows; t0 += 4ll * all) {
     int pos[4], page[4];
     const int32_t* entry[4];
-    int b = t0 < total ? last_at_most(s.cu, p.batch, static_cast<int>(t0)) : 0;
+    int b = t0 < rows_end ? last_at_most(s.cu, p.batch, static_cast<int>(t0)) : 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t t = t0 + k;
       pos[k] = 0;
       entry[k] = nullptr;
-      if (t < total) {
+      if (t < rows_end) {
         if (t >= s.cu[b + 1]) {
           ++b;
           if (t >= s.cu[b + 1]) b = last_at_most(s.cu, p.batch, static_cast<int>(t));

@@ -276,3 +276,13 @@ def test_step_plan_into_part_of_a_larger_buffer(cuda_lib, B, at):
     check_plan(*run_plan(cuda_lib, *a, positions=p, slot_map=m), want)
     assert bool((pos[:at[0]] == 77).all()) and bool((pos[at[0] + rows:] == 77).all())
     assert bool((slots[:at[1]] == 77).all()) and bool((slots[at[1] + rows:] == 77).all())
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 6, 7])
+def test_step_plan_looks_at_no_page_of_rows_that_it_does_not_write(cuda_lib, rows):
+    """Rows past total_rows are not written, and the pages that they would land on are not flagged."""
+    table = np.array([[3, -1], [99, -1]])
+    a = ([0, 5], [rows, 2], table, np.array([7, 8]), 2, 64, rows)
+    want = S.step_plan(*a)
+    assert want["flags"] == {"length"}
+    check_plan(*run_plan(cuda_lib, *a), want)
