@@ -3,8 +3,8 @@ gets it, who does not is unmoved, over caches of every length and at a bounded c
 
 Tolerance of the finite values: that of test_gpu_score_prefill.close (2^-8 |o| + 6 (2^-8 + 2^-13), and
 2^-13 + 2^-23 |lse|). Rows that are computed again do not round their weights, which only takes an error
-away. Scores are small here (q_scale 1 or 2, a bias of at most 2 ln 2 per key seen), so that no weight
-of a key that holds an infinity underflows in fp32 and 0 times infinity does not arise.
+away. Scores are small here (q_scale 1, a bias of at most 2^-8 a key over at most 2,000 keys), so that no
+weight of a key that holds an infinity underflows in fp32, but where a test says so.
 """
 import numpy as np
 import pytest
@@ -17,7 +17,7 @@ from tests.test_gpu_score_prefill import call, reference
 
 pytestmark = pytest.mark.gpu
 
-FLAT = 2.0 ** (-8 - 0.25 * np.arange(16))     # slopes: 131,072 keys away 2^17 2^-8 at most, see below
+FLAT = 2.0 ** (-8 - 0.25 * np.arange(16))
 
 
 def same(out, lse, ref_o, ref_l, rows):
