@@ -457,6 +457,133 @@ pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t interleaved,
                             pa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
+ * attn_decode_paged_shared — one decode step of rows in groups that share leading pages: the shared
+ * keys are read once for the group instead of once a row.
+ *
+ * Source: the transcript is decoded with the whole audio prompt in the cache ("Optimizing ASR Models
+ * to Transcribe 90-Minute Multi-Speaker Audio", "ASR Model Primer"); hypotheses of one recording, or
+ * requests behind one instruction, have its pages in common. The pages describe no search over
+ * hypotheses.
+ *
+ * The result is attn_decode_paged's up to rounding: row b attends to its seq_lens[b] keys.
+ *   cu_group_rows  int32 [groups + 1]: group g is rows cu_group_rows[g] .. cu_group_rows[g+1]-1;
+ *                  rows in no group share nothing
+ *   shared_pages   int32 [groups]: leading pages that the group's rows have in common: the caller
+ *                  vouches that the first shared_pages[g] table entries are the same in every row of
+ *                  the group that has as many whole pages (shared_pages of paged_fork); they are read
+ *                  from the first such row's entries. A row with fewer than 16 * shared_pages[g] keys
+ *                  (an empty beam) reads its own entries alone. A value outside [0, bt_stride] is
+ *                  flagged PA_DEV_ERR_LENGTH and counts as 0.
+ *   max_group_rows host upper bound of a group's rows (sizes the workspace). A larger group, or
+ *                  cu_group_rows that are not ascending within [0, batch], are flagged
+ *                  PA_DEV_ERR_LENGTH and no row shares anything.
+ *   batch <= 4096, groups <= 4096; max_seq_len <= 131072, a longer sequence is flagged
+ *   PA_DEV_ERR_LENGTH (and cut to bt_stride * 16); softmax_scale as attn_prefill_chunk; q, pools and out 16-byte
+ *   aligned. Weights are rounded to bf16 before they meet V, as the prefill does.
+ *   workspace      at least pa_decode_shared_workspace_size(...) bytes, 256-byte aligned; calls that
+ *                  share one must not overlap on the GPU.
+ * A row without keys gets o = 0, lse = -inf; so does a row whose scores are all -inf. NaN and
+ * infinities in keys that a row sees give what the formula gives (a weight of 0 times an infinity is
+ * NaN); other rows are unmoved, those of the same group too unless the key is a shared one.
+ * ------------------------------------------------------------------------------------------ */
+size_t pa_decode_shared_workspace_size(pa_dims dims, int32_t batch, int32_t groups,
+                                       int32_t max_group_rows);
+
+pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const void* k_pool,
+                                   const void* v_pool, int64_t num_pages,
+                                   const int32_t* block_table, int32_t bt_stride,
+                                   const int32_t* seq_lens, int32_t batch,
+                                   const int32_t* cu_group_rows, const int32_t* shared_pages,
+                                   int32_t groups, int32_t max_group_rows, int32_t max_seq_len,
+                                   float softmax_scale, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t* status, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * beam_select — the k best continuations of each request's beams.
+ *
+ * Source: the decode loop emits the transcript token by token ("ASR Model Primer" of the same page);
+ * the pages describe no search.
+ *
+ * Candidate (b, v) of request n has the score  scores[n][b] + logits[n][b][v] - ln sum_u
+ * exp(logits[n][b][u]);  the k best are kept, best first, equal ones in the order of (b, v).
+ *   logits      PA_BF16 or PA_FP32 (logits_type) [requests * beams] rows of vocab, row_stride elements
+ *               apart (>= vocab); -inf: the token is not allowed
+ *   scores      fp32 [requests][beams]: sums of log-probabilities. A beam whose score is infinite or
+ *               NaN has no candidates (-inf: a beam that is not in use, the others of the first step)
+ *   live        int32 [requests][beams] or NULL (all live): a beam with 0 has ended; its one candidate
+ *               is itself, with its score and the token eos_token; its logits are not read
+ *   k           1 .. 64;  beams <= 64;  beams * vocab < 2^31;  requests * beams <= 2^20
+ *   eos_token   in [0, vocab), or -1: no token ends a beam
+ *   out_scores  fp32, parents (b), tokens (v), live_out int32: [requests][k]. live_out is 0 for a beam
+ *               that has ended, 1 else: the new_lens of paged_step_plan when k is beams. Places without a
+ *               candidate get -inf, -1, -1, 0. out_scores may be scores and live_out may be live where
+ *               k = beams.
+ * A beam with a NaN or +inf among its logits, or nothing but -inf, has no candidates. Scores of
+ * different beams are compared in 64 bits over fp32 sums of exponentials (3e-7 absolute).
+ *   workspace   at least pa_beam_workspace_size(...) bytes, 8-byte aligned
+ * ------------------------------------------------------------------------------------------ */
+#define PA_BF16 0
+#define PA_FP32 1
+
+size_t pa_beam_workspace_size(int32_t requests, int32_t beams, int32_t vocab, int32_t k);
+
+pa_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride,
+                      int32_t requests, int32_t beams, int32_t vocab, const float* scores,
+                      const int32_t* live, int32_t k, int32_t eos_token, float* out_scores,
+                      int32_t* parents, int32_t* tokens, int32_t* live_out, void* workspace,
+                      size_t workspace_bytes, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * paged_fork / paged_copy_pages — the paged cache follows the beams.
+ *
+ * Source: as beam_select; the pages give no page sharing.
+ *
+ * Rows g * beams .. g * beams + beams - 1 of the table are group g. Row b of a group continues the
+ * sequence of row parents[g][b] of it (-1: the row becomes empty), so it takes over that row's length
+ * and pages. Pages are shared by the rows of a group only, each at the same place in all rows that hold
+ * it; no reference counts are kept, the group's rows are looked at. In this order:
+ *   - row b's entries become its parent's for the pages of its length, -1 where it held more before;
+ *     other entries are not touched. seq_lens_out[row] = the parent's length, or 0.
+ *   - a child whose last page is partly filled gets a page of its own in its place if an earlier child
+ *     holds that page too, or any other child holds it filled: popped from the end of the free list in
+ *     row order, and copies[row] = (source page, destination page, tokens); other rows (-1, -1, 0).
+ *   - pages that the group held and holds no longer are appended to the free list after the pops, in
+ *     the order (group, logical page, row). (They do not serve the same call's copies.)
+ *   - shared_pages[g] = leading pages that all non-empty rows of the group hold and fill
+ *     (attn_decode_paged_shared); 0 without any.
+ * If a parent is outside [-1, beams), a length outside [0, bt_stride * 16] or the list would outgrow
+ * free_capacity (PA_DEV_ERR_LENGTH), or there are fewer free pages than copies (PA_DEV_ERR_NO_PAGES),
+ * nothing changes: lengths and free count go out as they came, no copies, shared_pages 0. Entries
+ * outside [0, num_pages) are not given back or copied (flagged PA_DEV_ERR_PAGE_OOB; -1 silently where
+ * given back).
+ *   parents       int32 [groups][beams], beams <= 64, groups * beams <= 4096
+ *   seq_lens      int32 [groups * beams];  seq_lens_out may be seq_lens
+ *   block_table   int32 [groups * beams][bt_stride], in place
+ *   free_pages, free_capacity, free_count, free_count_out   as paged_release
+ *   copies        int32 [groups * beams][3];  shared_pages int32 [groups]
+ *   workspace     at least pa_fork_workspace_size(...) bytes, 4-byte aligned
+ * parents = 0 in all rows of a group whose first row holds a prompt hands it to every beam; parents =
+ * -1 gives all the group's pages back (paged_release is for pages held by one row).
+ *
+ * paged_copy_pages copies the first tokens of a page, bit for bit, for every row of copies and every
+ * pool (the K and V pools of all layers; a host array of device pointers). A row with source -1 and 0
+ * tokens is none; pages outside the pool are flagged PA_DEV_ERR_PAGE_OOB, tokens outside [0, 16]
+ * PA_DEV_ERR_LENGTH, and skipped. No page may be the destination of two rows, or destination and source.
+ * ------------------------------------------------------------------------------------------ */
+size_t pa_fork_workspace_size(int32_t groups, int32_t beams, int32_t bt_stride);
+
+pa_status paged_fork(const int32_t* parents, const int32_t* seq_lens, int32_t groups,
+                     int32_t beams, int32_t* block_table, int32_t bt_stride, int32_t* free_pages,
+                     int32_t free_capacity, const int32_t* free_count, int64_t num_pages,
+                     int32_t* free_count_out, int32_t* seq_lens_out, int32_t* copies,
+                     int32_t* shared_pages, void* workspace, size_t workspace_bytes,
+                     int32_t* status, pa_stream_t stream);
+
+pa_status paged_copy_pages(pa_dims dims, const int32_t* copies, int32_t rows, void* const* pools,
+                           int32_t num_pools, int64_t num_pages, int32_t* status,
+                           pa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
  * adaptor_mlp_merge4 — the audio-text bridge that turns encoder frames into decoder embeddings.
  *
  * Source: 4x temporal merge (concatenate every 4 encoder frames, d_model 1024 -> 4096) and an

@@ -14,6 +14,10 @@ Calls (same names as the C ABI):
 * ``paged_step_plan``   block tables, positions and slot maps of a step from request lengths
 * ``paged_release``     give pages of finished or windowed requests back to the free list
 * ``rope_append_paged`` rotary positions of new q and k rows, K/V written into their slots
+* ``attn_decode_paged_shared`` a decode step of rows that share leading pages, read once a group
+* ``beam_select``       the best continuations of each request's beams, over beams and vocabulary
+* ``paged_fork``        block tables follow the beams: pages shared, copied, given back
+* ``paged_copy_pages``  the page copies that a fork orders, in all layers' pools
 """
 from __future__ import annotations
 
@@ -33,6 +37,8 @@ __all__ = [
     "read_device_status", "debug_decode_starve",
     "paged_step_plan", "StepPlan", "paged_release", "rope_append_paged", "rope_inv_freq",
     "RopeScaling", "ScoreOpts",
+    "attn_decode_paged_shared", "decode_shared_workspace_size", "beam_select", "BeamStep",
+    "beam_workspace_size", "paged_fork", "ForkPlan", "fork_workspace_size", "paged_copy_pages",
     "DEV_ERR_PAGE_OOB", "DEV_ERR_LENGTH", "DEV_ERR_TIMEOUT", "DEV_ERR_INTERNAL",
     "DEV_ERR_NO_PAGES", "lib_path",
 ]
@@ -138,6 +144,16 @@ _SIGS = {
                                 ctypes.POINTER(_F)]),
     "rope_append_paged": (_I32, [Dims, _I32, _I32, _P, _F, _P, _I64, _P, _I64, _P, _I64, _I32, _P,
                                  _P, _P, _P, _F, _P, _P, _P, _I64, _P, _P]),
+    "pa_decode_shared_workspace_size": (_SZ, [Dims, _I32, _I32, _I32]),
+    "attn_decode_paged_shared": (_I32, [Dims, _P, _P, _P, _I64, _P, _I32, _P, _I32, _P, _P, _I32, _I32,
+                                        _I32, _F, _P, _P, _P, _SZ, _P, _P]),
+    "pa_beam_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "beam_select": (_I32, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _I32, _I32, _P, _P, _P, _P, _P,
+                           _SZ, _P]),
+    "pa_fork_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "paged_fork": (_I32, [_P, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _I64, _P, _P, _P, _P, _P, _SZ, _P,
+                          _P]),
+    "paged_copy_pages": (_I32, [Dims, _P, _I32, ctypes.POINTER(_P), _I32, _I64, _P, _P]),
     "pa_read_device_status": (_I32, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
     "pa_status_string": (ctypes.c_char_p, [_I32]),
     "pa_last_error": (ctypes.c_char_p, []),
@@ -850,6 +866,198 @@ def rope_append_paged(q, k_new, v_new, positions, slot_map, k_pool, v_pool, inv_
         pk, ks, pv, vs, T, pp, psm, pqg, pkg, float(eps), pqo, pkp, pvp, num_pages, ps,
         _stream(stream)))
     return q_out
+
+
+# ----------------------------------------------------------------------------------------------
+# beam search over the paged cache
+# ----------------------------------------------------------------------------------------------
+def decode_shared_workspace_size(batch: int, groups: int, max_group_rows: int, dims=None) -> int:
+    """Workspace of attn_decode_paged_shared."""
+    return int(load().pa_decode_shared_workspace_size(_dims(dims), batch, groups, max_group_rows))
+
+
+def attn_decode_paged_shared(q, k_pool, v_pool, block_table, seq_lens, cu_group_rows, shared_pages,
+                             max_seq_len: int, softmax_scale: float, *, max_group_rows=None, out=None,
+                             lse=None, workspace=None, status=None, stream=None, want_lse=True,
+                             dims=None):
+    """attn_decode_paged for rows in groups that share leading pages: rows cu_group_rows[g] ..
+    cu_group_rows[g + 1] - 1 have their first shared_pages[g] block-table entries in common, and the
+    keys of those pages are read once for the group. q [B, Hq, D]; returns (out, lse).
+
+    max_group_rows: host bound of a group's rows (default: B). Rows in no group share nothing; a row
+    with fewer keys than the shared pages hold reads its own entries alone."""
+    call, i32 = "attn_decode_paged_shared", torch.int32
+    dev = _device(call, q, "q", torch.bfloat16)
+    pq = _tensor(call, q, "q", torch.bfloat16, dev)
+    pk = _tensor(call, k_pool, "k_pool", torch.bfloat16, dev)
+    pv = _tensor(call, v_pool, "v_pool", torch.bfloat16, dev)
+    pbt = _tensor(call, block_table, "block_table", i32, dev)
+    psl = _tensor(call, seq_lens, "seq_lens", i32, dev)
+    pcu = _tensor(call, cu_group_rows, "cu_group_rows", i32, dev)
+    psh = _tensor(call, shared_pages, "shared_pages", i32, dev)
+    _need_dims(("q", q, 3), ("k_pool", k_pool, 4), ("v_pool", v_pool, 4), ("block_table", block_table, 2),
+               ("seq_lens", seq_lens, 1), ("cu_group_rows", cu_group_rows, 1),
+               ("shared_pages", shared_pages, 1))
+    B, hq, _ = q.shape
+    G = shared_pages.shape[0]
+    _rows_at_least("block_table", block_table, B)
+    _rows_at_least("seq_lens", seq_lens, B)
+    if G:
+        _rows_at_least("cu_group_rows", cu_group_rows, G + 1)
+    num_pages = k_pool.shape[0]
+    heads = _heads(dims)
+    if heads is not None:
+        _sized("q", q, (B, heads[0], 128))
+        _sized("k_pool", k_pool, (num_pages, 16, heads[1], 128))
+        _sized("v_pool", v_pool, (num_pages, 16, heads[1], 128))
+    max_group_rows = B if max_group_rows is None else int(max_group_rows)
+    out, po = _new_or_given(call, out, "out", torch.bfloat16, q.shape, dev, stream)
+    pl = None
+    if lse is not None or want_lse:
+        lse, pl = _new_or_given(call, lse, "lse", torch.float32, (B, hq), dev, stream)
+    if workspace is None:
+        nbytes = _workspace_size(decode_shared_workspace_size, B, G, max_group_rows, dims)
+        workspace = _workspace(nbytes, q.device, None, stream)
+    else:
+        _on_device(call, workspace)
+    ps = None if status is None else _tensor(call, status, "status", i32, dev)
+    _check(call, load().attn_decode_paged_shared(
+        _dims(dims), pq, pk, pv, num_pages, pbt, block_table.shape[1], psl, B, pcu, psh, G, max_group_rows,
+        int(max_seq_len), float(softmax_scale), po, pl, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), ps, _stream(stream)))
+    return out, lse
+
+
+BeamStep = collections.namedtuple("BeamStep", "scores parents tokens live")
+_LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def beam_workspace_size(requests: int, beams: int, vocab: int, k: int) -> int:
+    """Workspace of beam_select."""
+    return int(load().pa_beam_workspace_size(requests, beams, vocab, k))
+
+
+def beam_select(logits, scores, k: int, *, live=None, eos_token: int = -1, out_scores=None, parents=None,
+                tokens=None, live_out=None, workspace=None, stream=None) -> BeamStep:
+    """The k best of each request's candidates scores[n, b] + log_softmax(logits[n, b])[v]: BeamStep(scores
+    fp32, parents (b), tokens (v), live int32), each [N, k], best first, equal scores in the order of
+    (b, v).
+
+    logits [N, W, V] bf16 or fp32 (rows may lie apart); scores fp32 [N, W], -inf for a beam that is not
+    in use; live int32 [N, W]: 0 for a beam that has ended (its one candidate is itself, with eos_token).
+    live of the result is 0 for beams that have ended, now or before: the new_lens of paged_step_plan.
+    Places without a candidate are (-inf, -1, -1, 0). out_scores may be scores and live_out may be live
+    where k is W."""
+    call, i32 = "beam_select", torch.int32
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a tensor")
+    if logits.dtype not in _LOGITS:
+        raise TypeError(f"logits must be {torch.bfloat16} or {torch.float32}, got {logits.dtype}")
+    dev = _device(call, logits, "logits", logits.dtype)
+    if logits.dim() != 3:
+        raise ValueError(f"logits must have 3 dims, got {logits.dim()}")
+    N, W, V = logits.shape
+    s0, s1, s2 = logits.stride()
+    if N and W > 1:
+        stride = s1
+    elif N > 1:
+        stride = s0
+    else:
+        stride = V
+    if N and ((V > 1 and s2 != 1) or (N > 1 and W > 1 and s0 != W * s1) or stride < V):
+        raise ValueError("logits: a row must be contiguous, and rows equally far apart")
+    psc = _tensor(call, scores, "scores", torch.float32, dev)
+    _sized("scores", scores, (N, W))
+    plv = None
+    if live is not None:
+        plv = _tensor(call, live, "live", i32, dev)
+        _sized("live", live, (N, W))
+    k = int(k)
+    shape = (N, max(k, 0))
+    out_scores, po = _new_or_given(call, out_scores, "out_scores", torch.float32, shape, dev, stream)
+    parents, pp = _new_or_given(call, parents, "parents", i32, shape, dev, stream)
+    tokens, pt = _new_or_given(call, tokens, "tokens", i32, shape, dev, stream)
+    live_out, pl = _new_or_given(call, live_out, "live_out", i32, shape, dev, stream)
+    if workspace is None:
+        nbytes = _workspace_size(beam_workspace_size, N, W, V, k)
+        workspace = _workspace(nbytes, logits.device, None, stream)
+    else:
+        _on_device(call, workspace)
+    _check(call, load().beam_select(
+        logits.data_ptr(), _LOGITS[logits.dtype], stride, N, W, V, psc, plv, k, int(eos_token), po, pp, pt,
+        pl, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return BeamStep(out_scores, parents, tokens, live_out)
+
+
+ForkPlan = collections.namedtuple("ForkPlan", "seq_lens copies shared_pages free_count")
+
+
+def fork_workspace_size(groups: int, beams: int, bt_stride: int) -> int:
+    """Workspace of paged_fork."""
+    return int(load().pa_fork_workspace_size(groups, beams, bt_stride))
+
+
+def paged_fork(parents, seq_lens, block_table, free_pages, free_count, num_pages: int, *,
+               free_count_out=None, seq_lens_out=None, copies=None, shared_pages=None, workspace=None,
+               status=None, stream=None) -> ForkPlan:
+    """Row g * W + b of block_table continues row g * W + parents[g, b] (parents int32 [G, W]; -1: the row
+    becomes empty): it gets that row's pages, shared between the rows of a group. block_table and
+    free_pages are updated in place; returns ForkPlan(seq_lens [G * W], copies [G * W, 3] for
+    paged_copy_pages, shared_pages [G] for attn_decode_paged_shared, free_count [1]).
+
+    A child that shares a partly filled last page with an earlier child gets a page of its own from the
+    free list, and its copy in copies; pages that no row of the group holds any more go to the list. If
+    the free pages do not cover the copies nothing changes (DEV_ERR_NO_PAGES). seq_lens_out may be
+    seq_lens, free_count_out may be free_count."""
+    call, i32 = "paged_fork", torch.int32
+    dev = _device(call, parents, "parents", i32)
+    ppa = _tensor(call, parents, "parents", i32, dev)
+    psl = _tensor(call, seq_lens, "seq_lens", i32, dev)
+    pbt = _tensor(call, block_table, "block_table", i32, dev)
+    pf = _tensor(call, free_pages, "free_pages", i32, dev)
+    pfc = _tensor(call, free_count, "free_count", i32, dev)
+    _need_dims(("parents", parents, 2), ("seq_lens", seq_lens, 1), ("block_table", block_table, 2),
+               ("free_pages", free_pages, 1), ("free_count", free_count, 1))
+    G, W = parents.shape
+    B, stride = G * W, block_table.shape[1]
+    _sized("seq_lens", seq_lens, (B,))
+    _rows_at_least("block_table", block_table, B)
+    _rows_at_least("free_count", free_count, 1)
+    free_count_out, pfo = _new_or_given(call, free_count_out, "free_count_out", i32, (1,), dev, stream)
+    seq_lens_out, pso = _new_or_given(call, seq_lens_out, "seq_lens_out", i32, (B,), dev, stream)
+    copies, pc = _new_or_given(call, copies, "copies", i32, (B, 3), dev, stream)
+    shared_pages, psh = _new_or_given(call, shared_pages, "shared_pages", i32, (G,), dev, stream)
+    if workspace is None:
+        workspace = _workspace(_workspace_size(fork_workspace_size, G, W, stride), parents.device, None, stream)
+    else:
+        _on_device(call, workspace)
+    ps = None if status is None else _tensor(call, status, "status", i32, dev)
+    _check(call, load().paged_fork(
+        ppa, psl, G, W, pbt, stride, pf, free_pages.shape[0], pfc, int(num_pages), pfo, pso, pc, psh,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), ps, _stream(stream)))
+    return ForkPlan(seq_lens_out, copies, shared_pages, free_count_out)
+
+
+def paged_copy_pages(copies, pools, *, status=None, stream=None, dims=None):
+    """Copy the first copies[i, 2] tokens of page copies[i, 0] to page copies[i, 1] in every pool of
+    `pools` (the K and V pools of all layers, bf16 [num_pages, 16, Hkv, 128] of one shape). copies int32
+    [rows, 3]; rows of (-1, -1, 0) copy nothing."""
+    call = "paged_copy_pages"
+    dev = _device(call, copies, "copies", torch.int32)
+    pc = _tensor(call, copies, "copies", torch.int32, dev)
+    _shape("copies", copies, (None, 3))
+    heads = _heads(dims)
+    ptrs = (ctypes.c_void_p * max(1, len(pools)))()
+    shape = pools[0].shape if len(pools) and isinstance(pools[0], torch.Tensor) else None
+    if heads is not None and shape is not None:
+        _shape("pools[0]", pools[0], (None, 16, heads[1], 128))
+    for i, t in enumerate(pools):
+        ptrs[i] = _tensor(call, t, f"pools[{i}]", torch.bfloat16, dev)
+        _sized(f"pools[{i}]", t, shape)
+    ps = None if status is None else _tensor(call, status, "status", torch.int32, dev)
+    _check(call, load().paged_copy_pages(
+        _dims(dims), pc, copies.shape[0], ptrs, len(pools), shape[0] if shape is not None else 1, ps,
+        _stream(stream)))
 
 
 def adaptor_workspace_size(num_frames: int) -> int:

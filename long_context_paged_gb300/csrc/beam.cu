@@ -1,0 +1,366 @@
+// beam_select: the best k continuations of each request's beams, over beams and vocabulary (sm_103a).
+//
+// Candidate (b, v) of a request has the score
+//     scores[b] + logits[b][v] - ln sum_u exp(logits[b][u])
+// and the k best are kept, equal scores in the order of (b, v). Within a beam the order is that of the
+// logits themselves, whatever the beam's score and normaliser: so one pass over a beam's logits finds
+// both its normaliser (running maximum and sum) and its k largest logits, and only those few meet the
+// other beams' in a second launch. Scores are formed in 64 bits there: what decides between beams is
+// the normalisers' precision (fp32 sums of at most 2^14 terms, added up in fp64), not the rounding of
+// a sum of large parts.
+//
+// The logits are read once from memory: bound by HBM for a full batch (64 x 8 rows of 151,936), by
+// latency for a single request. A row is cut into pieces so that a few rows still fill the GPU; a CTA
+// takes a piece, a thread 16-byte vectors kThreads apart.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "dependent_launch.cuh"
+#include "pa_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxBeams = 64;
+constexpr int kMaxK = 64;
+// Pieces of a row: as many as give kTargetCtas CTAs in all, none of them below kMinPiece tokens.
+constexpr int kTargetCtas = 1216;
+constexpr int kMinPiece = 4096;
+
+struct BeamParams {
+  const void* logits;
+  int64_t row_stride;
+  int32_t requests, beams, vocab, k, eos, pieces;
+  const float* scores;
+  const int32_t* live;
+  float* out_scores;
+  int32_t* parents;
+  int32_t* tokens;
+  int32_t* live_out;
+  // workspace: of each row and piece, the k largest logits in order, and (maximum, sum of exp)
+  float2* best;   // [rows][pieces][k]: value, token as bits (-1: none)
+  float2* stats;  // [rows][pieces]
+};
+
+// fp32 as an unsigned integer of the same order; -inf and NaN are 0, below everything else.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  if (!(x > -INFINITY)) return 0;
+  const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);  // (-0 and 0 are equal)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+
+__device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u;
+  return static_cast<uint64_t>(hi) << 32 | __reduce_max_sync(0xffffffffu, lo);
+}
+
+// A row's beam takes part with its tokens: it is live and has a score. (-inf: not in use.)
+__device__ __forceinline__ bool expands(const BeamParams& p, int row) {
+  const float s = p.scores[row];
+  return (p.live == nullptr || p.live[row] != 0) && s > -INFINITY && s < INFINITY;
+}
+
+// The row's logits as 16-byte vectors of kVec, after `head` and before `tail` single ones.
+template <class T>
+struct Row {
+  static constexpr int kVec = 16 / sizeof(T);
+  const T* base;
+  int head, vectors, tail;
+  __device__ Row(const T* b, int n) : base(b) {
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(b) & 15u) / sizeof(T));
+    head = min(n, off == 0 ? 0 : kVec - off);
+    vectors = (n - head) / kVec;
+    tail = n - head - vectors * kVec;
+  }
+};
+
+__device__ __forceinline__ void unpack(uint4 w, float (&x)[8]) {
+  x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
+  x[4] = bf16lo(w.z); x[5] = bf16hi(w.z); x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ void unpack(uint4 w, float (&x)[4]) {
+  x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
+  x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ float single(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ float single(float v) { return v; }
+
+// A logit's rank among a row's: by value, then the lower token.
+__device__ __forceinline__ uint64_t rank_of(float x, int token) {
+  const uint32_t o = order_of(x);
+  return o == 0 ? 0ull : static_cast<uint64_t>(o) << 32 | ~static_cast<uint32_t>(token);
+}
+
+// f(value, token) for every logit that this thread has in the piece [v0, v1) of the row's vectors;
+// the first piece has the single ones before the vectors too, the last those after.
+template <class T, class F>
+__device__ __forceinline__ void each(const Row<T>& r, int v0, int v1, bool first, bool last, F f) {
+  constexpr int kVec = Row<T>::kVec;
+  const int t = threadIdx.x;
+  if (first && t < r.head) f(single(r.base[t]), t);
+  const uint4* body = reinterpret_cast<const uint4*>(r.base + r.head);
+  for (int v = v0 + t; v < v1; v += kThreads) {
+    float x[kVec];
+    unpack(body[v], x);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f(x[i], r.head + v * kVec + i);
+  }
+  const int at = r.head + r.vectors * kVec + t;
+  if (last && t < r.tail) f(single(r.base[at]), at);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
+  __shared__ uint64_t warp_best[kWarps];
+  __shared__ float2 warp_stats[kWarps];
+  await_previous();
+  const int row = static_cast<int>(blockIdx.x) / p.pieces, piece = static_cast<int>(blockIdx.x) % p.pieces;
+  if (!expands(p, row)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Row<T> r(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab);
+  const int v0 = static_cast<int>(static_cast<int64_t>(r.vectors) * piece / p.pieces);
+  const int v1 = static_cast<int>(static_cast<int64_t>(r.vectors) * (piece + 1) / p.pieces);
+  const bool first = piece == 0, last = piece == p.pieces - 1;
+  // maximum, sum of exponentials and best candidate of this thread
+  float m = -INFINITY, s = 0.f;
+  uint64_t best = 0;
+  each(r, v0, v1, first, last, [&](float x, int token) {
+    if (x > m) {
+      s *= fast_exp2((m - x) * kLog2e);
+      m = x;
+    }
+    // (x - m, then the factor: one rounding each, so no error that all terms share)
+    if (x != -INFINITY) s += fast_exp2((x - m) * kLog2e);
+    best = max(best, rank_of(x, token));
+  });
+  // of the CTA
+  float wm = m, ws = s;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, wm, o), os = __shfl_xor_sync(0xffffffffu, ws, o);
+    const float nm = fmaxf(wm, om);
+    const float a = wm == nm ? ws : ws * fast_exp2((wm - nm) * kLog2e);
+    const float b = om == nm ? os : os * fast_exp2((om - nm) * kLog2e);
+    wm = nm;
+    ws = a + b;
+  }
+  if (lane == 0) warp_stats[warp] = make_float2(wm, ws);
+  __syncthreads();
+  const int64_t at = static_cast<int64_t>(row) * p.pieces + piece;
+  if (tid == 0) {
+    float cm = -INFINITY, cs = 0.f;
+    for (int w = 0; w < kWarps; ++w) cm = fmaxf(cm, warp_stats[w].x);
+    for (int w = 0; w < kWarps; ++w)
+      cs += warp_stats[w].x == cm ? warp_stats[w].y : warp_stats[w].y * fast_exp2((warp_stats[w].x - cm) * kLog2e);
+    p.stats[at] = make_float2(cm, cs);
+  }
+  // the k largest, one after the other; the thread that had it looks for its next
+  for (int k = 0; k < p.k; ++k) {
+    const uint64_t wb = warp_max64(best);
+    if (lane == 0) warp_best[warp] = wb;
+    __syncthreads();
+    uint64_t top = 0;
+    for (int w = 0; w < kWarps; ++w) top = max(top, warp_best[w]);
+    __syncthreads();
+    if (tid == 0)
+      p.best[at * p.k + k] = make_float2(value_of(static_cast<uint32_t>(top >> 32)),
+                                         __int_as_float(top == 0 ? -1 : static_cast<int>(~static_cast<uint32_t>(top))));
+    if (top != 0 && best == top) {
+      best = 0;
+      each(r, v0, v1, first, last, [&](float x, int token) {
+        const uint64_t c = rank_of(x, token);
+        if (c < top) best = max(best, c);
+      });
+    }
+  }
+}
+
+// A candidate of a request: score in 64 bits as an integer of the same order, and its place.
+struct Candidate {
+  uint64_t score;
+  uint32_t place;  // ~(beam * vocab + token): a lower place is a larger number
+};
+__device__ __forceinline__ uint64_t order_of(double x) {
+  if (!(x > -INFINITY)) return 0;
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x == 0.0 ? 0.0 : x));
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double double_of(uint64_t o) {
+  return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+__device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
+  return a.score > b.score || (a.score == b.score && a.place > b.place);
+}
+
+__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
+  __shared__ double shift[kMaxBeams];  // score minus normaliser of a beam
+  __shared__ uint8_t kind[kMaxBeams];  // 0: no candidates, 1: its tokens, 2: itself (finished)
+  __shared__ Candidate warp_best[kWarps];
+  extern __shared__ uint8_t used[];    // [beams][pieces] candidates taken
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = static_cast<int>(blockIdx.x), lists = p.beams * p.pieces;
+  await_previous();
+  for (int i = tid; i < lists; i += kThreads) used[i] = 0;
+  for (int b = warp; b < p.beams; b += kWarps) {
+    const int row = n * p.beams + b;
+    if (!expands(p, row)) {
+      if (lane == 0) {
+        const float s = p.scores[row];
+        kind[b] = p.live != nullptr && p.live[row] == 0 && s > -INFINITY && s < INFINITY ? 2 : 0;
+        shift[b] = s;
+      }
+      continue;
+    }
+    const float2* stats = p.stats + static_cast<int64_t>(row) * p.pieces;
+    float m = -INFINITY;
+    for (int i = lane; i < p.pieces; i += 32) m = fmaxf(m, stats[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    double sum = 0.0;
+    for (int i = lane; i < p.pieces; i += 32) {
+      const float2 v = stats[i];
+      sum += v.x == m ? static_cast<double>(v.y) : static_cast<double>(v.y) * fast_exp2((v.x - m) * kLog2e);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      const double norm = static_cast<double>(m) + log(sum);
+      // (a NaN or +inf among the logits, or nothing but -inf: no candidates)
+      kind[b] = norm > -INFINITY && norm < INFINITY ? 1 : 0;
+      shift[b] = static_cast<double>(p.scores[row]) - norm;
+    }
+  }
+  __syncthreads();
+  // this thread's best among the heads of its lists
+  auto head = [&](int list) {
+    const int b = list / p.pieces, at = used[list];
+    Candidate c{0, 0};
+    if (kind[b] == 1 && at < p.k) {
+      const float2 e = p.best[(static_cast<int64_t>(n) * lists + list) * p.k + at];
+      const int token = __float_as_int(e.y);
+      if (token >= 0) {
+        c.score = order_of(shift[b] + static_cast<double>(e.x));
+        c.place = ~static_cast<uint32_t>(b * p.vocab + token);
+      }
+    } else if (kind[b] == 2 && at == 0 && list == b * p.pieces) {
+      c.score = order_of(shift[b]);
+      c.place = ~static_cast<uint32_t>(b * p.vocab + max(p.eos, 0));
+    }
+    return c;
+  };
+  auto mine = [&](int& list) {
+    Candidate c{0, 0};
+    for (int i = tid; i < lists; i += kThreads) {
+      const Candidate h = head(i);
+      if (better(h, c)) {
+        c = h;
+        list = i;
+      }
+    }
+    return c;
+  };
+  int list = -1;
+  Candidate best = mine(list);
+  for (int k = 0; k < p.k; ++k) {
+    Candidate c = best;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Candidate other;
+      other.score = __shfl_xor_sync(0xffffffffu, c.score, o);
+      other.place = __shfl_xor_sync(0xffffffffu, c.place, o);
+      if (better(other, c)) c = other;
+    }
+    if (lane == 0) warp_best[warp] = c;
+    __syncthreads();
+    Candidate top = warp_best[0];
+    for (int w = 1; w < kWarps; ++w)
+      if (better(warp_best[w], top)) top = warp_best[w];
+    __syncthreads();
+    const int at = n * p.k + k;
+    if (top.score == 0) {
+      if (tid == 0) {
+        p.out_scores[at] = -INFINITY;
+        p.parents[at] = p.tokens[at] = -1;
+        p.live_out[at] = 0;
+      }
+    } else if (best.score == top.score && best.place == top.place) {
+      const int b = list / p.pieces;
+      const int token = kind[b] == 2 ? p.eos : static_cast<int>(~top.place) - b * p.vocab;
+      p.out_scores[at] = static_cast<float>(double_of(top.score));
+      p.parents[at] = b;
+      p.tokens[at] = token;
+      p.live_out[at] = kind[b] == 1 && token != p.eos ? 1 : 0;
+      ++used[list];
+      best = mine(list);
+    }
+  }
+}
+
+int pieces_of(int32_t requests, int32_t beams, int32_t vocab) {
+  const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(requests) * beams);
+  const int64_t most = std::max<int64_t>(1, vocab / kMinPiece);
+  return static_cast<int>(std::min(most, std::max<int64_t>(1, kTargetCtas / rows)));
+}
+
+bool beam_sizes_valid(int32_t requests, int32_t beams, int32_t vocab, int32_t k) {
+  return requests >= 0 && beams > 0 && vocab > 0 && k > 0;
+}
+
+bool beam_sizes_supported(int32_t requests, int32_t beams, int32_t vocab, int32_t k) {
+  return beams <= kMaxBeams && k <= kMaxK && static_cast<int64_t>(beams) * vocab < (1ll << 31) &&
+         static_cast<int64_t>(requests) * beams <= (1 << 20);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" size_t pa_beam_workspace_size(int32_t requests, int32_t beams, int32_t vocab, int32_t k) {
+  using namespace pa;
+  if (!beam_sizes_valid(requests, beams, vocab, k) || !beam_sizes_supported(requests, beams, vocab, k)) return 0;
+  const size_t lists = static_cast<size_t>(requests) * beams * pieces_of(requests, beams, vocab);
+  return (lists * (k + 1) * sizeof(float2) + 255) / 256 * 256;
+}
+
+extern "C" pa_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride, int32_t requests,
+                                 int32_t beams, int32_t vocab, const float* scores, const int32_t* live, int32_t k,
+                                 int32_t eos_token, float* out_scores, int32_t* parents, int32_t* tokens,
+                                 int32_t* live_out, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  using namespace pa;
+  if (!beam_sizes_valid(requests, beams, vocab, k) || row_stride < vocab || eos_token < -1 || eos_token >= vocab ||
+      (logits_type != PA_BF16 && logits_type != PA_FP32))
+    return PA_ERR_INVALID_ARG;
+  if (!beam_sizes_supported(requests, beams, vocab, k)) {
+    snprintf_error("beam_select: at most %d beams of a request, %d candidates, 2^31 tokens of all its beams and 2^20 rows",
+                   kMaxBeams, kMaxK);
+    return PA_ERR_UNSUPPORTED;
+  }
+  // in place: a request's results replace its own inputs only if there are as many
+  if (k != beams && ((out_scores && out_scores == scores) || (live && live_out == live))) return PA_ERR_INVALID_ARG;
+  if (requests == 0) return PA_OK;
+  if (!logits || !scores || !out_scores || !parents || !tokens || !live_out) return PA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) & (logits_type == PA_BF16 ? 1u : 3u)) return PA_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < pa_beam_workspace_size(requests, beams, vocab, k))
+    return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 7u) return PA_ERR_INVALID_ARG;
+  const int pieces = pieces_of(requests, beams, vocab);
+  const size_t lists = static_cast<size_t>(requests) * beams * pieces;
+  float2* best = static_cast<float2*>(workspace);
+  const BeamParams p{logits, row_stride, requests, beams, vocab, k, eos_token, pieces, scores, live, out_scores,
+                     parents, tokens, live_out, best, best + lists * k};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(lists);
+  cudaError_t e = logits_type == PA_BF16 ? launch_dependent(beam_rows_kernel<uint16_t>, grid, kThreads, 0, st, 0, p)
+                                         : launch_dependent(beam_rows_kernel<float>, grid, kThreads, 0, st, 0, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(beam_merge_kernel, static_cast<unsigned>(requests), kThreads,
+                         static_cast<size_t>(beams) * pieces, st, 0, p);
+  return e == cudaSuccess ? PA_OK : record_cuda_error(e, "beam_select");
+}

@@ -1,0 +1,866 @@
+// attn_decode_paged_shared: decode attention of rows that share leading pages (sm_103a).
+//
+// Row r's softmax over its L_r keys is a sum over two disjoint sets, the keys of the pages that its
+// group shares and the keys of its own pages after them:
+//     o_r = (e^{m1} O1_r + e^{m2} O2_r) / (e^{m1} l1_r + e^{m2} l2_r),
+// with running maximum m, sum l and unnormalised O of each set. The first set is the same for the whole
+// group, so its K and V are read once and meet all the group's query rows in one matrix product:
+// 64 rows x the 2 query heads of a KV head are the 128 rows of a tcgen05 tile. With R rows a shared key
+// costs 512 bytes of a KV head's cache and 4 * 128 * 2 R operations, so up to about 64 rows the call is
+// bound by HBM and reads the shared keys at its rate, R times fewer bytes than the plain decode.
+//
+// Work split. A segment is a run of keys with the rows that see all of it: (64 rows of a group, its
+// shared pages) or (one row, its own pages). Segments are cut into units of 128 keys, laid end to end
+// and divided into equal slices, one per CTA of a KV head; the Hkv CTAs of a slice read the heads of
+// the same pages at about the same time. A slice's part of a segment (a piece) leaves (m, l, O) in the
+// workspace; the merge joins a row's pieces of both sets. The segments are laid out by a plan kernel
+// of one CTA, from lengths that only the GPU knows.
+//
+// Per unit, in a CTA: S = Q K^T (A = Q, B = K in shared memory, fp32 in TMEM), P = 2^(scale S - m) by a
+// thread per row, written over S as bf16, O += P V (A = P in TMEM, B = V in shared memory). Units go to
+// two softmax warpgroups in turn, each with an S and an O of its own, so that one's exponentials run
+// beside the other's products. K and V come by tiled TMA, a page per copy.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "dependent_launch.cuh"
+#include "pa_common.cuh"
+#include "tc_common.cuh"
+
+namespace pa {
+
+bool make_map_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t heads, uint32_t box_rows);
+bool make_map_heads(CUtensorMap* map, const void* base, uint64_t outer, uint64_t heads, uint32_t box_heads,
+                    uint32_t box_rows);
+
+namespace {
+
+constexpr int kTileRows = 64;     // rows of a group per segment (x 2 query heads = 128)
+constexpr int kTileKeys = 128;    // keys of a unit
+constexpr int kTilePages = kTileKeys / kPage;
+constexpr int kStages = 5;        // K and V tiles in flight, in turn
+constexpr int kThreads = 384;     // 8 softmax warps; producer, MMA issuer and 2 spare
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kInfos = 8;         // published units in flight: more than the stages can hold
+constexpr int kQBoxRows = 8;      // query rows of a copy
+constexpr uint32_t kBlockBytes = 128 * 128;
+constexpr uint32_t kTileBytes = 2 * kBlockBytes;
+constexpr uint32_t kPageBytes = kPage * 128;  // a page's 16 keys x 64 dims of one head
+constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
+constexpr int kMaxBatch = 4096;
+constexpr int kMaxGroups = 4096;
+constexpr int kMaxSegments = kMaxBatch + kMaxGroups + kMaxBatch / kTileRows;
+constexpr int kMaxSlices = 256;   // CTAs per KV head
+// Registers of a softmax thread and of the others; 256 x 208 + 128 x 88 = 384 x 168, what the CTA is
+// launched with (checked on the host).
+constexpr int kSoftmaxRegs = 208;
+constexpr int kControlRegs = 88;
+constexpr int kLaunchRegs = (256 * kSoftmaxRegs + 128 * kControlRegs) / kThreads;
+constexpr int kRowFloats = kHeadDim + 2;      // O and (m, l) of a query row in the workspace
+
+struct Segment {
+  int32_t unit, units;       // first unit and number of units
+  int32_t row, rows;         // query rows
+  int32_t table_row;         // whose table entries are read
+  int32_t first_key, end_key;
+  int32_t pad;
+};
+
+struct RowPlan {
+  int32_t tile, in_tile;     // segment of the shared pages and the row's place in it (-1: none)
+  int32_t own;               // segment of the row's own pages (-1: none)
+  int32_t pad;
+};
+
+struct PlanHeader {
+  int32_t units, segments, tiles;  // tiles: segments of shared pages, which come first
+  int32_t pad;
+};
+
+struct SharedParams {
+  int32_t hkv, hq, batch, groups, max_group_rows, bt_stride, max_seq_len;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  const int32_t* cu_group_rows;
+  const int32_t* shared_pages;
+  int64_t num_pages;
+  float scale_log2;
+  int32_t slices;       // CTAs per KV head
+  int32_t tile_rows;    // capacity of a shared segment's partial results, in rows
+  uint16_t* out;
+  float* lse;
+  int32_t* status;
+  PlanHeader* header;
+  int32_t* slice_segment;  // [slices]
+  Segment* segments;
+  RowPlan* rows;           // [batch]
+  float* tile_parts;       // [slices + tiles][hkv][2 streams][2 tile_rows][128], then (m, l)
+  float* row_parts;        // [slices + batch][hkv][2 streams][2][128], then (m, l)
+};
+
+// ---------------------------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+struct PlanSmem {
+  long long warp_sums[kPlanThreads / 32], total;
+  int32_t bad;
+  int32_t cu[kMaxGroups + 1];
+  int32_t shared[kMaxGroups];     // shared pages
+  int32_t first[kMaxGroups];      // first row that uses them
+  int32_t tile0[kMaxGroups];      // first segment
+  int32_t unit[kMaxSegments + 1]; // first unit of each segment
+};
+
+// Exclusive prefix sum over the CTA of packed (count << 40 | units), and the total.
+__device__ __forceinline__ long long plan_scan(PlanSmem& s, long long v, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) s.warp_sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const long long w = s.warp_sums[lane];
+    long long x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long n = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += n;
+    }
+    s.warp_sums[lane] = x - w;
+    if (lane == 31) s.total = x;
+  }
+  __syncthreads();
+  total = s.total;
+  const long long before = s.warp_sums[warp] + incl - v;
+  __syncthreads();
+  return before;
+}
+
+__device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
+
+__global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PlanSmem& s = *reinterpret_cast<PlanSmem*>(smem_raw);
+  const int tid = threadIdx.x;
+  await_previous();
+  if (tid == 0) s.bad = 0;
+  const int G = p.groups;
+  for (int g = tid; g <= G && G > 0; g += kPlanThreads) s.cu[g] = p.cu_group_rows[g];
+  __syncthreads();
+  for (int g = tid; g < G; g += kPlanThreads) {
+    const int a = s.cu[g], b = s.cu[g + 1];
+    if (a < 0 || b < a || b > p.batch || b - a > p.max_group_rows) s.bad = 1;
+    int n = p.shared_pages[g];
+    if (n < 0 || n > p.bt_stride) {
+      flag_error(p.status, PA_DEV_ERR_LENGTH);
+      n = 0;
+    }
+    s.shared[g] = n;
+    s.first[g] = 0x7fffffff;
+  }
+  __syncthreads();
+  // groups that are not disjoint ranges of rows: no row shares anything
+  const bool grouped = G > 0 && !s.bad;
+  if (G > 0 && s.bad && tid == 0) flag_error(p.status, PA_DEV_ERR_LENGTH);
+  const int row_lo = grouped ? s.cu[0] : 0, row_hi = grouped ? s.cu[G] : 0;
+
+  // rows: four consecutive ones a thread at most
+  const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  int len[4], group[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) len[k] = b0 + k < b1 ? p.seq_lens[b0 + k] : 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = b0 + k;
+    group[k] = -1;
+    if (b >= b1) continue;
+    const int most = p.bt_stride * kPage;
+    if (len[k] < 0 || len[k] > most || len[k] > p.max_seq_len) flag_error(p.status, PA_DEV_ERR_LENGTH);
+    len[k] = min(max(len[k], 0), most);
+    if (b >= row_lo && b < row_hi) {
+      int lo = 0, hi = G;  // last g with cu[g] <= b (empty groups before it share its start)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.cu[mid] <= b) lo = mid; else hi = mid;
+      }
+      // a row shorter than the shared pages reads its own keys alone
+      if (s.shared[lo] > 0 && len[k] >= s.shared[lo] * kPage) {
+        group[k] = lo;
+        atomicMin(&s.first[lo], b);
+      }
+    }
+  }
+  __syncthreads();
+  // segments of shared pages
+  const int gper = (G + kPlanThreads - 1) / kPlanThreads;
+  const int g0 = min(G, tid * gper), g1 = min(G, g0 + gper);
+  long long mine = 0, total = 0;
+  for (int g = g0; g < g1; ++g)
+    if (grouped && s.first[g] != 0x7fffffff) {
+      const long long tiles = (s.cu[g + 1] - s.cu[g] + kTileRows - 1) / kTileRows;
+      mine += tiles << 40 | tiles * units_of(s.shared[g] * kPage);
+    }
+  long long at = plan_scan(s, mine, total);
+  const int tiles = static_cast<int>(total >> 40), tile_units = static_cast<int>(total & ((1ll << 40) - 1));
+  for (int g = g0; g < g1; ++g) {
+    if (!grouped || s.first[g] == 0x7fffffff) continue;
+    int seg = static_cast<int>(at >> 40), unit = static_cast<int>(at & ((1ll << 40) - 1));
+    const int units = units_of(s.shared[g] * kPage);
+    s.tile0[g] = seg;
+    for (int r = s.cu[g]; r < s.cu[g + 1]; r += kTileRows) {
+      p.segments[seg] = Segment{unit, units, r, min(kTileRows, s.cu[g + 1] - r), s.first[g], 0, s.shared[g] * kPage, 0};
+      s.unit[seg++] = unit;
+      unit += units;
+    }
+    at = static_cast<long long>(seg) << 40 | unit;
+  }
+  // segments of the rows' own pages
+  mine = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int first = group[k] >= 0 ? s.shared[group[k]] * kPage : 0;
+    const int units = units_of(len[k] - first);
+    if (units > 0) mine += 1ll << 40 | units;
+  }
+  at = plan_scan(s, mine, total);  // (its barriers also order s.tile0)
+  const int segments = tiles + static_cast<int>(total >> 40);
+  const int units_all = tile_units + static_cast<int>(total & ((1ll << 40) - 1));
+  int seg = tiles + static_cast<int>(at >> 40), unit = tile_units + static_cast<int>(at & ((1ll << 40) - 1));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = b0 + k, g = group[k];
+    if (b >= b1) continue;
+    const int first = g >= 0 ? s.shared[g] * kPage : 0;
+    const int units = units_of(len[k] - first);
+    RowPlan r{-1, 0, -1, 0};
+    if (g >= 0) {
+      const int in_group = b - s.cu[g];
+      r.tile = s.tile0[g] + in_group / kTileRows;
+      r.in_tile = in_group % kTileRows;
+    }
+    if (units > 0) {
+      r.own = seg;
+      p.segments[seg] = Segment{unit, units, b, 1, b, first, len[k], 0};
+      s.unit[seg++] = unit;
+      unit += units;
+    }
+    p.rows[b] = r;
+  }
+  if (tid == 0) {
+    s.unit[segments] = units_all;
+    *p.header = PlanHeader{units_all, segments, tiles, 0};
+  }
+  __syncthreads();
+  for (int i = tid; i < p.slices; i += kPlanThreads) {
+    const int u = static_cast<int>(static_cast<long long>(units_all) * i / p.slices);
+    int lo = 0, hi = max(segments, 1);  // last segment with a first unit <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.unit[mid] <= u) lo = mid; else hi = mid;
+    }
+    p.slice_segment[i] = lo;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// attention over the slices
+// ---------------------------------------------------------------------------------------------
+constexpr int kFirst = 1, kLast = 2;          // of this stream in the piece
+constexpr int kPieceStart = 4, kPieceEnd = 8; // of the piece
+constexpr int kQBuffer1 = 16;
+
+struct UnitInfo {
+  int64_t part;     // where the stream's partial result goes, in floats; row r's O at + 128 r
+  int32_t stats;    // (m, l) of row r at part + stats + 2 r
+  int32_t keys;
+  int32_t flags;
+  int32_t rows;     // query rows x heads
+  int32_t is_tile;
+  int32_t pad;
+};
+
+struct SharedSmem {
+  uint8_t ring[kStages][2][kBlockBytes];
+  uint8_t q[2][2][kBlockBytes];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t info_full[kInfos];
+  uint64_t s_full[2], p_full[2], o_ready[2], o_free[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  UnitInfo info[kInfos];
+};
+static_assert(sizeof(SharedSmem) <= 232448, "shared memory over the 227 KB limit");
+
+__device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (mbar_wait_bounded(bar, parity)) return true;
+  flag_error(status, PA_DEV_ERR_TIMEOUT);
+  return false;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map, const SharedParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  await_previous();
+  SharedSmem& s = *reinterpret_cast<SharedSmem*>(smem_raw);
+  const int head = static_cast<int>(blockIdx.x) % p.hkv, slice = static_cast<int>(blockIdx.x) / p.hkv;
+  const PlanHeader plan = *p.header;
+  const int u0 = static_cast<int>(static_cast<long long>(plan.units) * slice / p.slices);
+  const int u1 = static_cast<int>(static_cast<long long>(plan.units) * (slice + 1) / p.slices);
+  const int nt = u1 - u0;
+  if (nt <= 0) return;  // uniform across the CTA: nothing allocated yet
+  if ((smem_addr(smem_raw) & 1023u) != 0) {  // not the layout this kernel was built for
+    if (threadIdx.x == 0) flag_error(p.status, PA_DEV_ERR_INTERNAL);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.q_full[i], 1);
+      mbar_init(&s.q_empty[i], 1);
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.o_ready[i], 1);
+      mbar_init(&s.o_free[i], 4);
+    }
+    for (int i = 0; i < kInfos; ++i) mbar_init(&s.info_full[i], 1);
+    mbar_init(&s.mma_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc<512>(&s.tmem_base);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s.tmem_base;  // S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512)
+
+  if (warp >= 8) {
+    tc::regs_decrease<kControlRegs>();
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------ producer: units, Q, K and V
+    bool ok = true;
+    int it = 0, piece = 0, q_loads = 0;
+    uint32_t st = 0, ph = 0, loads = 0;  // next ring stage, its parity, tiles loaded
+    int seg = p.slice_segment[slice];
+    auto load_tile = [&](const CUtensorMap* map, int pages, int token) {
+      if (lane == 0) ok = wait_or_flag(&s.empty[st], ph ^ 1u, p.status);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) return;
+      if (lane == 0) mbar_arrive_expect_tx(&s.full[st], static_cast<uint32_t>(pages) * 2 * kPageBytes);
+      __syncwarp();
+      const int pg = (lane >> 1) & (kTilePages - 1), kb = lane & 1;
+      const int t = __shfl_sync(0xffffffffu, token, pg);
+      if (lane < 2 * pages) tc::tma_load_3d(s.ring[st][kb] + pg * kPageBytes, map, kb * 64, head, t, &s.full[st]);
+      ++loads;
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    };
+    while (it < nt && ok) {
+      const Segment g = p.segments[seg];
+      const int k0 = u0 + it - g.unit, k1 = min(u1 - g.unit, g.units);
+      const int32_t* entries = p.block_table + static_cast<int64_t>(g.table_row) * p.bt_stride;
+      // the first token of this lane's page of unit k
+      auto page_token = [&](int k) {
+        const int key = g.first_key + k * kTileKeys + lane * kPage;
+        if (lane >= kTilePages || k >= k1 || key >= g.end_key) return 0;
+        const int e = entries[key / kPage];
+        if (e < 0 || e >= p.num_pages) {
+          flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
+          return 0;
+        }
+        return e * kPage;
+      };
+      int token = page_token(k0), token_next = page_token(k0 + 1);
+      const int qb = piece & 1;
+      if (lane == 0) ok = wait_or_flag(&s.q_empty[qb], ((piece >> 1) & 1) ^ 1u, p.status);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      const int boxes = (g.rows + kQBoxRows - 1) / kQBoxRows;
+      if (lane == 0) mbar_arrive_expect_tx(&s.q_full[qb], boxes * 2 * (2 * kQBoxRows * 128));
+      __syncwarp();
+      ++q_loads;
+      if (lane < 2 * boxes)
+        tc::tma_load_3d(s.q[qb][lane & 1] + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
+                        g.row + (lane >> 1) * kQBoxRows, &s.q_full[qb]);
+      const bool is_tile = seg < plan.tiles;
+      for (int k = k0; k < k1; ++k, ++it) {
+        const int token_ahead = page_token(k + 2);
+        const int keys = min(kTileKeys, g.end_key - (g.first_key + k * kTileKeys));
+        const int pages = (keys + kPage - 1) / kPage;
+        load_tile(&k_map, pages, token);
+        if (!ok) break;
+        // (info slot: its last unit has been consumed, since the stage that this unit's K went to
+        //  was released by a later unit's products)
+        if (lane == 0) {
+          UnitInfo& f = s.info[it % kInfos];
+          const int stream = it & 1;
+          const int cap = is_tile ? 2 * p.tile_rows : 2;
+          const int64_t slot = ((static_cast<int64_t>(slice) + (is_tile ? seg : seg - plan.tiles)) * p.hkv + head) * 2 + stream;
+          f.part = slot * cap * kRowFloats;
+          f.stats = cap * kHeadDim;
+          f.keys = keys;
+          f.flags = (k - k0 < 2 ? kFirst : 0) | (k1 - 1 - k < 2 ? kLast : 0) | (k == k0 ? kPieceStart : 0) |
+                    (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0);
+          f.rows = 2 * g.rows;
+          f.is_tile = is_tile ? 1 : 0;
+          mbar_arrive(&s.info_full[it % kInfos]);
+        }
+        load_tile(&v_map, pages, token);
+        if (!ok) break;
+        token = token_next;
+        token_next = token_ahead;
+      }
+      ++piece;
+      ++seg;
+    }
+    // do not leave while copies into this CTA's shared memory may still be landing (only after a wait
+    // that gave up: else all of them have been consumed)
+    if (!ok && lane == 0) {
+      for (uint32_t k = loads > kStages ? loads - kStages : 0; k < loads; ++k)
+        wait_or_flag(&s.full[k % kStages], (k / kStages) & 1, p.status);
+      for (int k = max(0, q_loads - 2); k < q_loads; ++k) wait_or_flag(&s.q_full[k & 1], (k >> 1) & 1, p.status);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t dq = tc::smem_desc_sw128(smem_addr(s.q[0][0]), 16, 1024);
+      const uint64_t dk = tc::smem_desc_sw128(smem_addr(s.ring[0][0]), 16, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.ring[0][0]), kBlockBytes, 1024);
+      bool ok = true;
+      uint32_t kst = 0, kph = 0, vst = 1, vph = 0;  // stages of the next K and the next V tile
+      auto advance = [](uint32_t& stage, uint32_t& parity) {
+        stage += 2;
+        if (stage >= kStages) {
+          stage -= kStages;
+          parity ^= 1u;
+        }
+      };
+      uint32_t q_uses[2] = {0, 0}, pieces[2] = {0, 0};
+      int pages = 0, flags = 0;  // of the unit whose P V comes next
+      for (int it = 0; it <= nt && ok; ++it) {
+        int pages_now = 0, flags_now = 0;
+        if (it < nt) {
+          const int stream = it & 1;
+          ok = wait_or_flag(&s.info_full[it % kInfos], (it / kInfos) & 1, p.status);
+          if (!ok) break;
+          const volatile UnitInfo& f = s.info[it % kInfos];
+          pages_now = (f.keys + kPage - 1) / kPage;
+          flags_now = f.flags;
+          const int qb = flags_now & kQBuffer1 ? 1 : 0;
+          if (flags_now & kPieceStart) {
+            ok = wait_or_flag(&s.q_full[qb], q_uses[qb] & 1, p.status);
+            ++q_uses[qb];
+          }
+          ok = ok && wait_or_flag(&s.full[kst], kph, p.status);
+          if (!ok) break;
+          tc::fence_after_sync();
+          // N = the unit's keys in whole pages; the products run in the order of their issue, so S may
+          // take the columns of the P that the stream's last P V read
+          const uint32_t id = tc::idesc_bf16(128, 0, 0, 0) | static_cast<uint32_t>(pages_now * kPage >> 3) << 17;
+          const uint64_t a = dq + (qb * kTileBytes >> 4), b = dk + (kst * kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;
+            tc::mma_ss(tmem + stream * 128, a + off, b + off, id, kk > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&s.s_full[stream]);
+          tc::mma_commit(&s.empty[kst]);
+          if (flags_now & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
+          advance(kst, kph);
+        }
+        if (it > 0) {
+          const int t = it - 1, stream = t & 1;
+          ok = wait_or_flag(&s.p_full[stream], (t >> 1) & 1, p.status) && wait_or_flag(&s.full[vst], vph, p.status);
+          if (ok && (flags & kFirst)) {
+            if (pieces[stream] > 0) ok = wait_or_flag(&s.o_free[stream], (pieces[stream] - 1) & 1, p.status);
+            ++pieces[stream];
+          }
+          if (!ok) break;
+          tc::fence_after_sync();
+          constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
+          const uint64_t b = dv + (vst * kTileBytes >> 4);
+          for (int kk = 0; kk < pages; ++kk)
+            tc::mma_ts(tmem + 256 + stream * 128, tmem + stream * 128 + kk * 8, b + kk * (kPageBytes >> 4), id,
+                       kk > 0 || !(flags & kFirst) ? 1u : 0u);
+          tc::mma_commit(&s.empty[vst]);
+          if (flags & kLast) tc::mma_commit(&s.o_ready[stream]);
+          advance(vst, vph);
+        }
+        pages = pages_now;
+        flags = flags_now;
+      }
+      // every product must have finished before TMEM is released
+      tc::mma_commit(&s.mma_done);
+      wait_or_flag(&s.mma_done, 0, p.status);
+    }
+    __syncwarp();
+  }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    tc::regs_increase<kSoftmaxRegs>();
+    const int stream = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lane_bits + stream * 128, t_o = tmem + lane_bits + 256 + stream * 128;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    bool ok = true;
+    uint32_t n = 0, pieces = 0;
+    float m_used = -CUDART_INF_F, l = 0.f;
+    for (int it = stream; it < nt; it += 2, ++n) {
+      ok = __all_sync(0xffffffffu, wait_or_flag(&s.info_full[it % kInfos], (it / kInfos) & 1, p.status));
+      if (!ok) break;
+      const volatile UnitInfo& f = s.info[it % kInfos];
+      const int keys = f.keys, flags = f.flags, rows = f.rows, stats = f.stats;
+      float* part = (f.is_tile ? p.tile_parts : p.row_parts) + f.part;
+      const bool used = quarter * 32 < rows;  // some of this warp's rows are query rows
+      ok = __all_sync(0xffffffffu, wait_or_flag(&s.s_full[stream], n & 1, p.status));
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (flags & kFirst) {
+        m_used = -CUDART_INF_F;
+        l = 0.f;
+      }
+      if (used) {
+        uint32_t sb[128];
+        float cm[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
+        tc::tmem_wait_ld();
+        float mx = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
+        if (keys < kTileKeys) {  // keys past the segment's end (their scores are whatever TMEM held)
+          mx = -CUDART_INF_F;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            if (c >= keys) sb[c] = 0xff800000u;
+            mx = fmaxf(mx, __uint_as_float(sb[c]));
+          }
+        }
+        const float mx2 = mx * p.scale_log2;
+        const bool grow = mx2 > m_used + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = grow ? mx2 : m_used;
+          const float alpha = m_used == -CUDART_INF_F ? 0.f : fast_exp2(m_used - m_new);
+          if (!(flags & kFirst)) {
+            // O holds the stream's sum through its last unit: that product was issued before this
+            // unit's S, whose completion has been seen
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o32[32];
+              tc::tmem_ld32(t_o + c * 32, o32);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o32[k] = __float_as_uint(__uint_as_float(o32[k]) * alpha);
+              tc::tmem_st32(t_o + c * 32, o32);
+            }
+          }
+          l *= alpha;
+          m_used = m_new;
+        }
+        // the weights go to bf16 for the product (their sum is of the unrounded ones): off by 2^-8 of
+        // each at most, which averages out over the keys; V's own precision is no better
+        const float m_eff = m_used == -CUDART_INF_F ? 0.f : m_used;
+        const float2 nm2 = make_float2(-m_eff, -m_eff);
+        float2 ls[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float2 x = fma2(make_float2(__uint_as_float(sb[c * 64 + 2 * k]),
+                                              __uint_as_float(sb[c * 64 + 2 * k + 1])), sc2, nm2);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            ls[k & 3] = add2(ls[k & 3], e);
+            pk[k] = pack_bf16x2(e.x, e.y);
+          }
+          tc::tmem_st32(t_s + c * 32, pk);
+        }
+        const float2 sum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+        l += sum.x + sum.y;
+        tc::tmem_wait_st();
+      }
+      if (keys % kPage != 0) {
+        // slots of the last page after the last key may hold anything, NaN too: their V rows meet
+        // weights of 0 as zeros
+        const uint32_t v = 2 * static_cast<uint32_t>(it) + 1, vst = v % kStages;
+        ok = __all_sync(0xffffffffu, wait_or_flag(&s.full[vst], (v / kStages) & 1, p.status));
+        if (!ok) break;
+        const int end = (keys + kPage - 1) / kPage * kPage;
+        for (int e = keys * 16 + r; e < end * 16; e += 128)
+          *reinterpret_cast<uint4*>(s.ring[vst][(e >> 3) & 1] + (e >> 4) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.p_full[stream]);
+      if (flags & kLast) {
+        ok = __all_sync(0xffffffffu, wait_or_flag(&s.o_ready[stream], pieces & 1, p.status));
+        if (!ok) break;
+        ++pieces;
+        tc::fence_after_sync();
+        if (used) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tc::tmem_ld32(t_o + c * 32, o);
+            tc::tmem_wait_ld();
+            if (r < rows) {
+              float4* dst = reinterpret_cast<float4*>(part + r * kHeadDim + c * 32);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            }
+          }
+          // (a NaN among the scores: any finite maximum hands the NaN on)
+          if (r < rows) *reinterpret_cast<float2*>(part + stats + 2 * r) = make_float2(l == l ? m_used : 0.f, l);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o_free[stream]);
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc<512>(tmem);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// merge: a CTA per row, a warp per query head, four dims a lane
+// ---------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(512) shared_merge_kernel(const SharedParams p) {
+  await_previous();
+  const int b = static_cast<int>(blockIdx.x), hq = threadIdx.x >> 5, lane = threadIdx.x & 31, head = hq >> 1;
+  const PlanHeader plan = *p.header;
+  const RowPlan row = p.rows[b];
+  const long long U = plan.units, n = p.slices;
+  float m = -CUDART_INF_F, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int set = 0; set < 2; ++set) {
+    const int seg = set == 0 ? row.tile : row.own;
+    if (seg < 0) continue;
+    const int unit = p.segments[seg].unit, units = p.segments[seg].units;
+    const int cap = set == 0 ? 2 * p.tile_rows : 2;
+    const int r = set == 0 ? 2 * row.in_tile + (hq & 1) : hq & 1;
+    const int index = set == 0 ? seg : seg - plan.tiles;
+    const float* base = set == 0 ? p.tile_parts : p.row_parts;
+    // slices [i0, i1] hold it: slice i has units [U i / n, U (i + 1) / n)
+    const int i0 = static_cast<int>(((unit + 1ll) * n - 1) / U);
+    const int i1 = static_cast<int>((static_cast<long long>(unit + units) * n - 1) / U);
+    for (int at = 2 * i0; at <= 2 * i1 + 1; at += 32) {
+      // lane's partial result: (slice, stream)
+      const int i = (at + lane) >> 1, stream = (at + lane) & 1;
+      float2 ml = make_float2(-CUDART_INF_F, 0.f);
+      const float* part = base + (((static_cast<int64_t>(i) + index) * p.hkv + head) * 2 + stream) * cap * kRowFloats;
+      if (at + lane <= 2 * i1 + 1) {
+        const int a = static_cast<int>(U * i / n), e = static_cast<int>(U * (i + 1) / n);
+        const int first = max(a, unit), last = min(e, unit + units);
+        // units alternate between the streams, from the slice's first
+        if (last - first >= 2 || (last - first == 1 && ((first - a) & 1) == stream))
+          ml = *reinterpret_cast<const float2*>(part + cap * kHeadDim + 2 * r);
+      }
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float m_new = fmaxf(m, top);
+      if (m_new == -CUDART_INF_F) continue;
+      const float keep = m == -CUDART_INF_F ? 0.f : fast_exp2(m - m_new);
+      const float w = ml.x == -CUDART_INF_F ? 0.f : fast_exp2(ml.x - m_new);
+      m = m_new;
+      float sum = w * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = l * keep + sum;
+      acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+      const uint32_t some = __ballot_sync(0xffffffffu, ml.x != -CUDART_INF_F);
+      for (uint32_t left = some; left != 0; left &= left - 1) {
+        const int k = __ffs(left) - 1;
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float* pk = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), k));
+        const float4 v = reinterpret_cast<const float4*>(pk + r * kHeadDim)[lane];
+        acc.x += wk * v.x;
+        acc.y += wk * v.y;
+        acc.z += wk * v.z;
+        acc.w += wk * v.w;
+      }
+    }
+  }
+  const float inv = m == -CUDART_INF_F ? 0.f : 1.0f / l;
+  uint2 w = make_uint2(0u, 0u);
+  if (m != -CUDART_INF_F) {
+    w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  }
+  const int64_t at = static_cast<int64_t>(b) * p.hq + hq;
+  reinterpret_cast<uint2*>(p.out + at * kHeadDim)[lane] = w;
+  if (lane == 0 && p.lse != nullptr) p.lse[at] = m == -CUDART_INF_F ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------------
+struct SharedLayout {
+  int slices, tile_rows;
+  size_t header, slice_segment, segments, rows, tile_parts, row_parts, total;
+};
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+bool shared_layout(SharedLayout& l, int hkv, int batch, int groups, int max_group_rows) {
+  const int sms = sm_count_current_device();
+  if (sms <= 0) return false;
+  l.slices = std::min(kMaxSlices, std::max(1, sms / hkv));
+  l.tile_rows = std::max(1, std::min({kTileRows, max_group_rows, batch}));
+  // a group's segments: one, and one more for every kTileRows rows
+  const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kTileRows : 0;
+  l.header = 0;
+  l.slice_segment = 256;
+  l.segments = align256(l.slice_segment + sizeof(int32_t) * l.slices);
+  l.rows = align256(l.segments + sizeof(Segment) * (tiles + batch));
+  l.tile_parts = align256(l.rows + sizeof(RowPlan) * batch);
+  const size_t per_row = static_cast<size_t>(hkv) * 2 * 2 * kRowFloats * sizeof(float);
+  l.row_parts = align256(l.tile_parts + (groups > 0 ? (l.slices + tiles) * l.tile_rows * per_row : 0));
+  l.total = align256(l.row_parts + (static_cast<size_t>(l.slices) + batch) * per_row);
+  return true;
+}
+
+bool shared_sizes_valid(int batch, int groups, int max_group_rows) {
+  return batch >= 0 && groups >= 0 && max_group_rows >= 0;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" size_t pa_decode_shared_workspace_size(pa_dims dims, int32_t batch, int32_t groups,
+                                                  int32_t max_group_rows) {
+  using namespace pa;
+  SharedLayout l;
+  if (!gqa_dims_supported(dims) || !shared_sizes_valid(batch, groups, max_group_rows) || batch == 0 ||
+      batch > kMaxBatch || groups > kMaxGroups || !shared_layout(l, dims.num_kv_heads, batch, groups, max_group_rows))
+    return 0;
+  return l.total;
+}
+
+extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const void* k_pool, const void* v_pool,
+                                              int64_t num_pages, const int32_t* block_table, int32_t bt_stride,
+                                              const int32_t* seq_lens, int32_t batch, const int32_t* cu_group_rows,
+                                              const int32_t* shared_pages, int32_t groups, int32_t max_group_rows,
+                                              int32_t max_seq_len, float softmax_scale, void* out, float* lse,
+                                              void* workspace, size_t workspace_bytes, int32_t* status,
+                                              pa_stream_t stream) {
+  using namespace pa;
+  if (!gqa_dims_supported(dims)) return PA_ERR_UNSUPPORTED;
+  if (!shared_sizes_valid(batch, groups, max_group_rows) || num_pages <= 0 || bt_stride <= 0 ||
+      bt_stride > 0x7fffffff / kPage || max_seq_len < 0 || max_seq_len > 131072 ||
+      !(softmax_scale > 0.f && softmax_scale < 1e30f))
+    return PA_ERR_INVALID_ARG;
+  if (batch > kMaxBatch || groups > kMaxGroups) {
+    snprintf_error("attn_decode_paged_shared: at most %d rows and %d groups per call", kMaxBatch, kMaxGroups);
+    return PA_ERR_UNSUPPORTED;
+  }
+  if (num_pages * kPage >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  if (batch == 0) return PA_OK;
+  if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out || (groups > 0 && (!cu_group_rows || !shared_pages)))
+    return PA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pool) | reinterpret_cast<uintptr_t>(v_pool) |
+       reinterpret_cast<uintptr_t>(out)) & 15u)
+    return PA_ERR_INVALID_ARG;
+  SharedLayout l;
+  const int hkv = dims.num_kv_heads;
+  if (!shared_layout(l, hkv, batch, groups, max_group_rows)) return PA_ERR_CUDA;
+  if (workspace == nullptr || workspace_bytes < l.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
+  CUtensorMap qm, km, vm;
+  if (!make_map_heads(&qm, q, static_cast<uint64_t>(batch), dims.num_q_heads, kGroup, kQBoxRows) ||
+      !make_map_3d(&km, k_pool, static_cast<uint64_t>(num_pages) * kPage, hkv, kPage) ||
+      !make_map_3d(&vm, v_pool, static_cast<uint64_t>(num_pages) * kPage, hkv, kPage)) {
+    snprintf_error("cuTensorMapEncodeTiled failed for the decode's operands");
+    return PA_ERR_CUDA;
+  }
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_device != dev) {
+    cudaError_t e = cudaFuncSetAttribute(shared_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(sizeof(SharedSmem)));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(sizeof(PlanSmem)));
+    // same carveout for the merge: no reconfiguration between them
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(shared_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(decode_shared)");
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, shared_attention_kernel);
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncGetAttributes(decode_shared)");
+    if (fa.numRegs < kLaunchRegs) {  // (setmaxnreg.inc would wait forever)
+      snprintf_error("shared_attention_kernel built with %d registers/thread, needs %d for its split", fa.numRegs,
+                     kLaunchRegs);
+      return PA_ERR_UNSUPPORTED;
+    }
+    configured_device = dev;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SharedParams p;
+  p.hkv = hkv;
+  p.hq = dims.num_q_heads;
+  p.batch = batch;
+  p.groups = groups;
+  p.max_group_rows = max_group_rows;
+  p.bt_stride = bt_stride;
+  p.max_seq_len = max_seq_len;
+  p.seq_lens = seq_lens;
+  p.block_table = block_table;
+  p.cu_group_rows = cu_group_rows;
+  p.shared_pages = shared_pages;
+  p.num_pages = num_pages;
+  p.scale_log2 = softmax_scale * kLog2e;
+  p.slices = l.slices;
+  p.tile_rows = l.tile_rows;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.status = status;
+  p.header = reinterpret_cast<PlanHeader*>(ws + l.header);
+  p.slice_segment = reinterpret_cast<int32_t*>(ws + l.slice_segment);
+  p.segments = reinterpret_cast<Segment*>(ws + l.segments);
+  p.rows = reinterpret_cast<RowPlan*>(ws + l.rows);
+  p.tile_parts = reinterpret_cast<float*>(ws + l.tile_parts);
+  p.row_parts = reinterpret_cast<float*>(ws + l.row_parts);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_dependent(shared_plan_kernel, 1, kPlanThreads, sizeof(PlanSmem), st, 0, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(shared_attention_kernel, static_cast<unsigned>(l.slices * hkv), kThreads, sizeof(SharedSmem),
+                         st, 0, qm, km, vm, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(shared_merge_kernel, static_cast<unsigned>(batch), 32u * static_cast<unsigned>(p.hq), 0, st, 0, p);
+  return e == cudaSuccess ? PA_OK : record_cuda_error(e, "attn_decode_paged_shared");
+}

@@ -27,19 +27,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 }  // namespace
 
-// 3-D bf16 view [outer][heads][128 dims] (dims innermost); box = 64 dims x 1 head x box_rows;
+// 3-D bf16 view [outer][heads][128 dims] (dims innermost); box = 64 dims x box_heads x box_rows;
 // 128-byte swizzle; zero fill outside the tensor.
-bool make_map_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t heads,
-                 uint32_t box_rows) {
+bool make_map_heads(CUtensorMap* map, const void* base, uint64_t outer, uint64_t heads,
+                    uint32_t box_heads, uint32_t box_rows) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {128, heads, outer};
   cuuint64_t strides[2] = {256, heads * 256};
-  cuuint32_t box[3] = {64, 1, box_rows};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same with a box of one head.
+bool make_map_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t heads,
+                 uint32_t box_rows) {
+  return make_map_heads(map, base, outer, heads, 1, box_rows);
 }
 
 // 2-D bf16 matrix [rows][cols] with a row stride in bytes; box = 64 columns x box_rows rows;
