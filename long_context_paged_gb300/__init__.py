@@ -887,6 +887,11 @@ def attn_decode_paged_shared(q, k_pool, v_pool, block_table, seq_lens, cu_group_
     max_group_rows: host bound of a group's rows (default: B). Rows in no group share nothing; a row
     with fewer keys than the shared pages hold reads its own entries alone."""
     call, i32 = "attn_decode_paged_shared", torch.int32
+    if _FAST is not None:
+        o, l = _attn_outputs(q, out, lse, want_lse, stream)
+        if _FAST.decode_shared(q, k_pool, v_pool, block_table, seq_lens, cu_group_rows, shared_pages, max_seq_len,
+                               softmax_scale, max_group_rows, o, l, workspace, status, _handle(stream), dims):
+            return o, l
     dev = _device(call, q, "q", torch.bfloat16)
     pq = _tensor(call, q, "q", torch.bfloat16, dev)
     pk = _tensor(call, k_pool, "k_pool", torch.bfloat16, dev)
@@ -949,6 +954,11 @@ def beam_select(logits, scores, k: int, *, live=None, eos_token: int = -1, out_s
     Places without a candidate are (-inf, -1, -1, 0). out_scores may be scores and live_out may be live
     where k is W."""
     call, i32 = "beam_select", torch.int32
+    if _FAST is not None:
+        made = _FAST.beam(logits, scores, k, live, eos_token, out_scores, parents, tokens, live_out, workspace,
+                          _handle(stream))
+        if made:
+            return BeamStep._make(made)
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a tensor")
     if logits.dtype not in _LOGITS:
@@ -1010,6 +1020,11 @@ def paged_fork(parents, seq_lens, block_table, free_pages, free_count, num_pages
     the free pages do not cover the copies nothing changes (DEV_ERR_NO_PAGES). seq_lens_out may be
     seq_lens, free_count_out may be free_count."""
     call, i32 = "paged_fork", torch.int32
+    if _FAST is not None:
+        made = _FAST.fork(parents, seq_lens, block_table, free_pages, free_count, num_pages, seq_lens_out, copies,
+                          shared_pages, free_count_out, workspace, status, _handle(stream))
+        if made:
+            return ForkPlan._make(made)
     dev = _device(call, parents, "parents", i32)
     ppa = _tensor(call, parents, "parents", i32, dev)
     psl = _tensor(call, seq_lens, "seq_lens", i32, dev)
@@ -1043,6 +1058,8 @@ def paged_copy_pages(copies, pools, *, status=None, stream=None, dims=None):
     `pools` (the K and V pools of all layers, bf16 [num_pages, 16, Hkv, 128] of one shape). copies int32
     [rows, 3]; rows of (-1, -1, 0) copy nothing."""
     call = "paged_copy_pages"
+    if _FAST is not None and _FAST.copy_pages(copies, pools, status, _handle(stream), dims):
+        return
     dev = _device(call, copies, "copies", torch.int32)
     pc = _tensor(call, copies, "copies", torch.int32, dev)
     _shape("copies", copies, (None, 3))

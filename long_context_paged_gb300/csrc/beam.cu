@@ -27,6 +27,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxK = 64;
+constexpr int kList = 1024;  // candidates of a piece that the quick selection holds
 // Pieces of a row: as many as give kTargetCtas CTAs in all, none of them below kMinPiece tokens.
 constexpr int kTargetCtas = 1216;
 constexpr int kMinPiece = 4096;
@@ -99,87 +100,176 @@ __device__ __forceinline__ uint64_t rank_of(float x, int token) {
   return o == 0 ? 0ull : static_cast<uint64_t>(o) << 32 | ~static_cast<uint32_t>(token);
 }
 
-// f(value, token) for every logit that this thread has in the piece [v0, v1) of the row's vectors;
-// the first piece has the single ones before the vectors too, the last those after.
-template <class T, class F>
-__device__ __forceinline__ void each(const Row<T>& r, int v0, int v1, bool first, bool last, F f) {
-  constexpr int kVec = Row<T>::kVec;
-  const int t = threadIdx.x;
-  if (first && t < r.head) f(single(r.base[t]), t);
-  const uint4* body = reinterpret_cast<const uint4*>(r.base + r.head);
-  for (int v = v0 + t; v < v1; v += kThreads) {
-    float x[kVec];
-    unpack(body[v], x);
+// A vector of no logits: -inf in every place.
+template <class T>
+__device__ __forceinline__ uint4 no_logits() {
+  const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  return make_uint4(w, w, w, w);
+}
+
+// This thread's running maximum and sum of exponentials over n more logits, the first of them `token`;
+// `at` is the token of the first vector that held the maximum.
+template <int n>
+__device__ __forceinline__ void take(const float (&x)[n], int token, float& m, float& s, int& at) {
+  float top = x[0];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) f(x[i], r.head + v * kVec + i);
+  for (int i = 1; i < n; ++i) top = fmaxf(top, x[i]);
+  if (top > m) {
+    s *= fast_exp2((m - top) * kLog2e);
+    m = top;
+    at = token;
   }
-  const int at = r.head + r.vectors * kVec + t;
-  if (last && t < r.tail) f(single(r.base[at]), at);
+  // (x - m, then the factor: one rounding each, so no error that all terms share)
+  const float base = m == -INFINITY ? 0.f : m;
+  float sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < n; ++i) sum[i & 1] += fast_exp2((x[i] - base) * kLog2e);
+  s += sum[0] + sum[1];
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
-  __shared__ uint64_t warp_best[kWarps];
+  constexpr int kVec = Row<T>::kVec;
+  __shared__ uint64_t warp_best[kWarps], list[kList];
   __shared__ float2 warp_stats[kWarps];
-  await_previous();
+  __shared__ int found;
   const int row = static_cast<int>(blockIdx.x) / p.pieces, piece = static_cast<int>(blockIdx.x) % p.pieces;
-  if (!expands(p, row)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) found = 0;
+  await_previous();
+  if (!expands(p, row)) return;
   const Row<T> r(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab);
+  const uint4* body = reinterpret_cast<const uint4*>(r.base + r.head);
   const int v0 = static_cast<int>(static_cast<int64_t>(r.vectors) * piece / p.pieces);
   const int v1 = static_cast<int>(static_cast<int64_t>(r.vectors) * (piece + 1) / p.pieces);
-  const bool first = piece == 0, last = piece == p.pieces - 1;
-  // maximum, sum of exponentials and best candidate of this thread
+  // the first piece has the single logits before the vectors, the last those after
+  const int lead = piece == 0 ? r.head : 0, trail = piece == p.pieces - 1 ? r.tail : 0;
+  const int trail_at = r.head + r.vectors * kVec;
   float m = -INFINITY, s = 0.f;
-  uint64_t best = 0;
-  each(r, v0, v1, first, last, [&](float x, int token) {
-    if (x > m) {
-      s *= fast_exp2((m - x) * kLog2e);
-      m = x;
-    }
-    // (x - m, then the factor: one rounding each, so no error that all terms share)
-    if (x != -INFINITY) s += fast_exp2((x - m) * kLog2e);
-    best = max(best, rank_of(x, token));
-  });
-  // of the CTA
-  float wm = m, ws = s;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float om = __shfl_xor_sync(0xffffffffu, wm, o), os = __shfl_xor_sync(0xffffffffu, ws, o);
-    const float nm = fmaxf(wm, om);
-    const float a = wm == nm ? ws : ws * fast_exp2((wm - nm) * kLog2e);
-    const float b = om == nm ? os : os * fast_exp2((om - nm) * kLog2e);
-    wm = nm;
-    ws = a + b;
+  int at = 0;
+  if (tid < lead) {
+    const float x[1] = {single(r.base[tid])};
+    take(x, tid, m, s, at);
   }
-  if (lane == 0) warp_stats[warp] = make_float2(wm, ws);
+  for (int v = v0 + tid; v < v1; v += 4 * kThreads) {
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = v + j * kThreads < v1 ? body[v + j * kThreads] : no_logits<T>();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[kVec];
+      unpack(w[j], x);
+      take(x, r.head + (v + j * kThreads) * kVec, m, s, at);
+    }
+  }
+  if (tid < trail) {
+    const float x[1] = {single(r.base[trail_at + tid])};
+    take(x, trail_at + tid, m, s, at);
+  }
+  // A bound that k logits at least reach: the q-th best thread of each warp that has vectors (q of them
+  // make k), and of those the least. A thread's rank is its maximum and the first vector that has it:
+  // each thread above the bound has a logit above all of any thread below.
+  const uint64_t mine = m > -INFINITY ? static_cast<uint64_t>(order_of(m)) << 32 | ~static_cast<uint32_t>(at) : 0ull;
+  const int warps = min(kWarps, max(1, (v1 - v0 + 31) / 32));
+  uint64_t bound = 0;
+  if (warp < warps) {
+    uint64_t left = mine;
+    for (int q = (p.k + warps - 1) / warps; q > 0; --q) {
+      bound = warp_max64(left);
+      if (left == bound) left = 0;
+    }
+  }
+  // maximum and sum of the CTA
+  float wm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+  float ws = m == wm ? s : s * fast_exp2((m - wm) * kLog2e);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+  if (lane == 0) {
+    warp_stats[warp] = make_float2(wm, ws);
+    warp_best[warp] = bound;
+  }
   __syncthreads();
-  const int64_t at = static_cast<int64_t>(row) * p.pieces + piece;
+  const int64_t out = static_cast<int64_t>(row) * p.pieces + piece;
   if (tid == 0) {
     float cm = -INFINITY, cs = 0.f;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) cm = fmaxf(cm, warp_stats[w].x);
+#pragma unroll
     for (int w = 0; w < kWarps; ++w)
       cs += warp_stats[w].x == cm ? warp_stats[w].y : warp_stats[w].y * fast_exp2((warp_stats[w].x - cm) * kLog2e);
-    p.stats[at] = make_float2(cm, cs);
+    p.stats[out] = make_float2(cm, cs);
   }
-  // the k largest, one after the other; the thread that had it looks for its next
+  bound = warp_best[0];
+  for (int w = 1; w < warps; ++w) bound = min(bound, warp_best[w]);
+  // Logits that reach the bound, those of its own vector included, go to a list: the warp looks through
+  // the vectors of each of its threads that may have one, a lane a vector (the second read of a small
+  // part of the piece, from L2 mostly).
+  const uint64_t reach = bound > 0 ? bound - (kVec - 1) : 1;
+  auto keep = [&](float x, int token) {
+    const uint64_t c = rank_of(x, token);
+    if (c < reach) return;
+    const int i = atomicAdd(&found, 1);
+    if (i < kList) list[i] = c;
+  };
+  if (tid < lead) keep(single(r.base[tid]), tid);
+  if (tid < trail) keep(single(r.base[trail_at + tid]), trail_at + tid);
+  for (uint32_t some = __ballot_sync(0xffffffffu, mine >= reach); some != 0; some &= some - 1) {
+    const int first = v0 + warp * 32 + __ffs(some) - 1;
+    for (int v = first + lane * kThreads; v < v1; v += 32 * kThreads) {
+      float x[kVec];
+      unpack(body[v], x);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) keep(x[i], r.head + v * kVec + i);
+    }
+  }
+  __syncthreads();
+  const int n = found;
+  if (n <= kList) {
+    // an entry's place is the number of those above it
+    for (int i = tid; i < max(n, p.k); i += kThreads) {
+      if (i >= n) {
+        p.best[out * p.k + i] = make_float2(-INFINITY, __int_as_float(-1));
+        continue;
+      }
+      const uint64_t c = list[i];
+      int place = 0;
+      for (int j = 0; j < n; ++j) place += list[j] > c ? 1 : 0;
+      if (place < p.k)
+        p.best[out * p.k + place] = make_float2(value_of(static_cast<uint32_t>(c >> 32)),
+                                                __int_as_float(static_cast<int>(~static_cast<uint32_t>(c))));
+    }
+    return;
+  }
+  // More than the list holds (most of a row's logits alike or banned, in a pattern that leaves a warp
+  // without a high one): the k largest one after the other, each found below the last.
+  uint64_t top = ~0ull;
   for (int k = 0; k < p.k; ++k) {
-    const uint64_t wb = warp_max64(best);
-    if (lane == 0) warp_best[warp] = wb;
+    uint64_t best = 0;
+    auto look = [&](float x, int token) {
+      const uint64_t c = rank_of(x, token);
+      if (c < top) best = max(best, c);
+    };
+    if (mine >= reach || lead > 0 || trail > 0) {
+      if (tid < lead) look(single(r.base[tid]), tid);
+      if (tid < trail) look(single(r.base[trail_at + tid]), trail_at + tid);
+      for (int v = v0 + tid; v < v1; v += kThreads) {
+        float x[kVec];
+        unpack(body[v], x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) look(x[i], r.head + v * kVec + i);
+      }
+    }
+    best = warp_max64(best);
+    if (lane == 0) warp_best[warp] = best;
     __syncthreads();
-    uint64_t top = 0;
-    for (int w = 0; w < kWarps; ++w) top = max(top, warp_best[w]);
+    top = warp_best[0];
+    for (int w = 1; w < kWarps; ++w) top = max(top, warp_best[w]);
     __syncthreads();
     if (tid == 0)
-      p.best[at * p.k + k] = make_float2(value_of(static_cast<uint32_t>(top >> 32)),
-                                         __int_as_float(top == 0 ? -1 : static_cast<int>(~static_cast<uint32_t>(top))));
-    if (top != 0 && best == top) {
-      best = 0;
-      each(r, v0, v1, first, last, [&](float x, int token) {
-        const uint64_t c = rank_of(x, token);
-        if (c < top) best = max(best, c);
-      });
-    }
+      p.best[out * p.k + k] = make_float2(value_of(static_cast<uint32_t>(top >> 32)),
+                                          __int_as_float(top == 0 ? -1 : static_cast<int>(~static_cast<uint32_t>(top))));
   }
 }
 

@@ -15,10 +15,14 @@
 // from here. No computation happens here, and the binding works without this module, only slower.
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
+
+#include <utility>
+#include <vector>
 
 #include "pagedattn.h"
 
@@ -229,10 +233,12 @@ const pa_launch_opts* launch_options(Reader& r, pa_launch_opts& o) {
 // The binding's error class, called with a call's name and its status code (set_error).
 PyObject* error_class = nullptr;
 
-// What became of a call: not made, or made under this name with this status code.
+// What became of a call: not made, or made under this name with this status code; the outputs that
+// were made for it, if any.
 struct Made {
   const char* name = nullptr;
   pa_status code = PA_OK;
+  std::vector<at::Tensor> outputs;
 };
 
 // f(): makes the call or not. What it throws comes from before the call (a machine without a GPU, a
@@ -253,8 +259,44 @@ PyObject* guarded(F f) {
     }
     return nullptr;
   }
-  return PyBool_FromLong(made.name != nullptr && made.code == PA_OK);
+  const bool good = made.name != nullptr && made.code == PA_OK;
+  if (!good || made.outputs.empty()) return PyBool_FromLong(good);
+  PyObject* all = PyTuple_New(static_cast<Py_ssize_t>(made.outputs.size()));
+  for (size_t i = 0; all != nullptr && i < made.outputs.size(); ++i) {
+    PyObject* t = THPVariable_Wrap(std::move(made.outputs[i]));
+    if (t == nullptr) {
+      Py_DECREF(all);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(all, static_cast<Py_ssize_t>(i), t);
+  }
+  return all;
 }
+
+// An output of this type and shape: the caller's (checked), or a new one on the current stream. Both come
+// back as a tensor, in the order of a call's results.
+struct Outputs {
+  Reader& r;
+  bool current;  // the call is on the current stream (a given one: new outputs are left to the wrapper)
+  std::vector<at::Tensor> all;
+
+  void* take(ScalarType type, at::IntArrayRef shape) {
+    PyObject* o = r.next();
+    if (!r.good) return nullptr;
+    if (o == Py_None) {
+      r.require(current);
+      if (!r.good) return nullptr;
+      all.push_back(at::empty(shape, at::TensorOptions().dtype(type).device(
+                                         at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(r.dev)))));
+      return all.back().data_ptr();
+    }
+    const at::Tensor* t = r.tensor_of(o, type);
+    if (r.good && (!t->is_contiguous() || t->sizes() != shape)) r.good = false;
+    if (!r.good) return nullptr;
+    all.push_back(*t);
+    return t->data_ptr();
+  }
+};
 
 // (q, k_pool, v_pool, block_table, seq_lens, max_seq_len, scale, split_tokens, out, lse,
 //  workspace, status, stream, dims, max_ctas, options)
@@ -305,7 +347,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch, max_len, scale,
                                   split, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
                                   static_cast<int32_t*>(status), s, opts);
-    return {scored ? "attn_decode_paged_score" : "attn_decode_paged", code};
+    return {scored ? "attn_decode_paged_score" : "attn_decode_paged", code, {}};
   });
 }
 
@@ -361,7 +403,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    k->size(0), ptr<const int32_t>(table), stride, ptr<const int32_t>(lens), batch,
                                    max_q, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p, scratch.bytes,
                                    static_cast<int32_t*>(status), s, opts);
-    return {scored ? "attn_prefill_chunk_score" : "attn_prefill_chunk", code};
+    return {scored ? "attn_prefill_chunk_score" : "attn_prefill_chunk", code, {}};
   });
 }
 
@@ -414,7 +456,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                              ptr<const int64_t>(slots), ptr<const float>(qg), ptr<const float>(kg),
                                              eps, out->data_ptr(), kp->data_ptr(), vp->data_ptr(), kp->size(0),
                                              static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
-    return {"rope_append_paged", code};
+    return {"rope_append_paged", code, {}};
   });
 }
 
@@ -457,7 +499,7 @@ PyObject* step_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                            rows, ptr<int32_t>(count_out), ptr<int32_t>(cu), ptr<int32_t>(lens),
                                            ptr<int32_t>(pos), ptr<int64_t>(slots), static_cast<int32_t*>(status),
                                            reinterpret_cast<pa_stream_t>(st));
-    return {"paged_step_plan", code};
+    return {"paged_step_plan", code, {}};
   });
 }
 
@@ -489,7 +531,178 @@ PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                          ptr<int32_t>(free), static_cast<int32_t>(free->size(0)),
                                          ptr<const int32_t>(count), pages, ptr<int32_t>(count_out),
                                          static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
-    return {"paged_release", code};
+    return {"paged_release", code, {}};
+  });
+}
+
+// (q, k_pool, v_pool, block_table, seq_lens, cu_group_rows, shared_pages, max_seq_len, scale,
+//  max_group_rows, out, lse, workspace, status, stream, dims)
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> Made {
+    Reader r(a, n);
+    const at::Tensor* q = r.tensor(ScalarType::BFloat16, 3);
+    const at::Tensor* k = r.tensor(ScalarType::BFloat16, 4);
+    const at::Tensor* v = r.tensor(ScalarType::BFloat16, 4);
+    const at::Tensor* table = r.tensor(ScalarType::Int, 2);
+    const at::Tensor* lens = r.tensor(ScalarType::Int, 1);
+    const at::Tensor* cu = r.tensor(ScalarType::Int, 1);
+    const at::Tensor* shared = r.tensor(ScalarType::Int, 1);
+    const int32_t max_len = r.int32();
+    const float scale = static_cast<float>(r.number());
+    int32_t most = 0;
+    const bool bounded = !(r.i < r.n && r.a[r.i] == Py_None);
+    if (bounded) most = r.int32(); else ++r.i;
+    const at::Tensor* out = r.tensor(ScalarType::BFloat16, 3);
+    const at::Tensor* lse = r.tensor_or_none(ScalarType::Float, 2);
+    const at::Tensor* workspace = r.bytes_or_none();
+    void* status = r.status();
+    cudaStream_t st = r.stream();
+    const pa_dims d = r.dims();
+    if (!r.done()) return {};
+    const int64_t B = q->size(0), G = shared->size(0), hq = d.num_q_heads, hkv = d.num_kv_heads;
+    if (!bounded) most = static_cast<int32_t>(B);
+    r.shape(q, B, hq, 128);
+    r.shape(k, k->size(0), 16, hkv, 128);
+    r.shape(v, k->size(0), 16, hkv, 128);
+    r.at_least(table, B);
+    r.at_least(lens, B);
+    r.at_least(cu, G > 0 ? G + 1 : 0);
+    r.shape(out, B, hq, 128);
+    r.shape(lse, B, hq);
+    if (!r.good || B > INT32_MAX || G > INT32_MAX || table->size(1) > INT32_MAX) return {};
+    const int32_t batch = static_cast<int32_t>(B), groups = static_cast<int32_t>(G);
+    const size_t need = workspace ? 0 : pa_decode_shared_workspace_size(d, batch, groups, most);
+    Unlocked unlocked;
+    Scratch scratch(workspace, need, st);
+    const pa_status code = attn_decode_paged_shared(
+        d, q->data_ptr(), k->data_ptr(), v->data_ptr(), k->size(0), ptr<const int32_t>(table),
+        static_cast<int32_t>(table->size(1)), ptr<const int32_t>(lens), batch, ptr<const int32_t>(cu),
+        ptr<const int32_t>(shared), groups, most, max_len, scale, out->data_ptr(), ptr<float>(lse), scratch.p,
+        scratch.bytes, static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
+    return {"attn_decode_paged_shared", code, {}};
+  });
+}
+
+// (logits, scores, k, live, eos_token, out_scores, parents, tokens, live_out, workspace, stream); returns
+// the four outputs.
+PyObject* beam(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> Made {
+    Reader r(a, n);
+    PyObject* o = r.next();
+    if (!r.good || !THPVariable_Check(o)) return {};
+    const ScalarType type = THPVariable_Unpack(o).scalar_type();
+    if (type != ScalarType::BFloat16 && type != ScalarType::Float) return {};
+    const at::Tensor* x = r.tensor_of(o, type);
+    r.require(r.good && x->dim() == 3);
+    const at::Tensor* scores = r.tensor(ScalarType::Float, 2);
+    const int32_t k = r.int32();
+    const at::Tensor* live = r.tensor_or_none(ScalarType::Int, 2);
+    const int32_t eos = r.int32();
+    if (!r.good || k < 1 || k > 64 || n != 11) return {};
+    const int64_t N = x->size(0), W = x->size(1), V = x->size(2);
+    r.shape(scores, N, W);
+    r.shape(live, N, W);
+    r.require(N <= INT32_MAX && W > 0 && W <= INT32_MAX && V > 0 && V <= INT32_MAX);
+    const int64_t stride = W > 1 ? x->stride(1) : N > 1 ? x->stride(0) : V;
+    r.require((V == 1 || x->stride(2) == 1) && (N <= 1 || W <= 1 || x->stride(0) == W * x->stride(1)));
+    if (!r.good) return {};
+    Outputs out{r, a[10] == Py_None, {}};
+    const int64_t shape[2] = {N, k};
+    void* s = out.take(ScalarType::Float, shape);
+    void* parents = out.take(ScalarType::Int, shape);
+    void* tokens = out.take(ScalarType::Int, shape);
+    void* l = out.take(ScalarType::Int, shape);
+    const at::Tensor* workspace = r.bytes_or_none();
+    cudaStream_t st = r.stream();
+    if (!r.done()) return {};
+    const int32_t reqs = static_cast<int32_t>(N), beams = static_cast<int32_t>(W), vocab = static_cast<int32_t>(V);
+    const size_t need = workspace ? 0 : pa_beam_workspace_size(reqs, beams, vocab, k);
+    pa_status code;
+    {
+      Unlocked unlocked;
+      Scratch scratch(workspace, need, st);
+      code = beam_select(x->data_ptr(), type == ScalarType::BFloat16 ? PA_BF16 : PA_FP32, stride, reqs, beams, vocab,
+                         ptr<const float>(scores), ptr<const int32_t>(live), k, eos, static_cast<float*>(s),
+                         static_cast<int32_t*>(parents), static_cast<int32_t*>(tokens), static_cast<int32_t*>(l),
+                         scratch.p, scratch.bytes, reinterpret_cast<pa_stream_t>(st));
+    }
+    return {"beam_select", code, std::move(out.all)};
+  });
+}
+
+// (parents, seq_lens, block_table, free_pages, free_count, num_pages, seq_lens_out, copies, shared_pages,
+//  free_count_out, workspace, status, stream); returns the four outputs.
+PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> Made {
+    Reader r(a, n);
+    const at::Tensor* parents = r.tensor(ScalarType::Int, 2);
+    const at::Tensor* lens = r.tensor(ScalarType::Int, 1);
+    const at::Tensor* table = r.tensor(ScalarType::Int, 2);
+    const at::Tensor* free = r.tensor(ScalarType::Int, 1);
+    const at::Tensor* count = r.tensor(ScalarType::Int, 1);
+    const long long pages = r.integer();
+    if (!r.good || n != 13) return {};
+    const int64_t G = parents->size(0), W = parents->size(1), B = G * W;
+    r.require(G <= INT32_MAX && W <= INT32_MAX && B <= INT32_MAX && table->size(1) <= INT32_MAX &&
+              free->size(0) <= INT32_MAX);
+    r.shape(lens, B);
+    r.at_least(table, B);
+    r.at_least(count, 1);
+    if (!r.good) return {};
+    Outputs out{r, a[12] == Py_None, {}};
+    void* lens_out = out.take(ScalarType::Int, {B});
+    void* copies = out.take(ScalarType::Int, {B, 3});
+    void* shared = out.take(ScalarType::Int, {G});
+    void* count_out = out.take(ScalarType::Int, {1});
+    const at::Tensor* workspace = r.bytes_or_none();
+    void* status = r.status();
+    cudaStream_t st = r.stream();
+    if (!r.done()) return {};
+    const int32_t groups = static_cast<int32_t>(G), beams = static_cast<int32_t>(W);
+    const int32_t stride = static_cast<int32_t>(table->size(1));
+    const size_t need = workspace ? 0 : pa_fork_workspace_size(groups, beams, stride);
+    pa_status code;
+    {
+      Unlocked unlocked;
+      Scratch scratch(workspace, need, st);
+      code = paged_fork(ptr<const int32_t>(parents), ptr<const int32_t>(lens), groups, beams, ptr<int32_t>(table),
+                        stride, ptr<int32_t>(free), static_cast<int32_t>(free->size(0)), ptr<const int32_t>(count),
+                        pages, static_cast<int32_t*>(count_out), static_cast<int32_t*>(lens_out),
+                        static_cast<int32_t*>(copies), static_cast<int32_t*>(shared), scratch.p, scratch.bytes,
+                        static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
+    }
+    return {"paged_fork", code, std::move(out.all)};
+  });
+}
+
+// (copies, pools, status, stream, dims): pools a list or tuple.
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> Made {
+    Reader r(a, n);
+    const at::Tensor* copies = r.tensor(ScalarType::Int, 2);
+    PyObject* list = r.next();
+    void* status = r.status();
+    cudaStream_t st = r.stream();
+    const pa_dims d = r.dims();
+    if (!r.done() || copies->size(1) != 3 || copies->size(0) > INT32_MAX) return {};
+    if (!PyList_Check(list) && !PyTuple_Check(list)) return {};
+    const Py_ssize_t m = PySequence_Fast_GET_SIZE(list);
+    if (m < 1 || m > 4096) return {};
+    std::vector<void*> pools(static_cast<size_t>(m));
+    int64_t pages = 0;
+    for (Py_ssize_t i = 0; i < m; ++i) {
+      const at::Tensor* t = r.tensor_of(PySequence_Fast_GET_ITEM(list, i), ScalarType::BFloat16);
+      if (!r.good || t->dim() != 4 || !t->is_contiguous()) return {};
+      if (i == 0) pages = t->size(0);
+      r.shape(t, pages, 16, d.num_kv_heads, 128);
+      if (!r.good) return {};
+      pools[static_cast<size_t>(i)] = t->data_ptr();
+    }
+    Unlocked unlocked;
+    const pa_status code = paged_copy_pages(d, ptr<const int32_t>(copies), static_cast<int32_t>(copies->size(0)),
+                                            pools.data(), static_cast<int32_t>(m), pages,
+                                            static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
+    return {"paged_copy_pages", code, {}};
   });
 }
 
@@ -509,7 +722,9 @@ PyObject* set_error(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {
     PA_METHOD(decode, "attn_decode_paged"),      PA_METHOD(prefill, "attn_prefill_chunk"),
     PA_METHOD(rope, "rope_append_paged"),        PA_METHOD(step_plan, "paged_step_plan"),
-    PA_METHOD(release, "paged_release"),         PA_METHOD(set_error, "class of the errors raised"),
+    PA_METHOD(release, "paged_release"),         PA_METHOD(decode_shared, "attn_decode_paged_shared"),
+    PA_METHOD(beam, "beam_select"),              PA_METHOD(fork, "paged_fork"),
+    PA_METHOD(copy_pages, "paged_copy_pages"),   PA_METHOD(set_error, "class of the errors raised"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_call", "Fast path of the binding", -1, methods,
