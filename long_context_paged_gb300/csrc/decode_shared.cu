@@ -43,13 +43,15 @@ constexpr int kTileRows = 64;     // rows of a group per segment (x 2 query head
 constexpr int kTileKeys = 128;    // keys of a unit
 constexpr int kTilePages = kTileKeys / kPage;
 constexpr int kStages = 5;        // K and V tiles in flight, in turn
-constexpr int kThreads = 384;     // 8 softmax warps; producer, MMA issuer and 2 spare
+constexpr int kThreads = 384;     // 8 softmax warps; producer, two MMA issuers and a spare
 constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
+constexpr int kPvWarp = 9;        // issues O += P V
+constexpr int kScoreWarp = 10;    // issues S = Q K^T
 constexpr int kInfos = 8;         // published units in flight: more than the stages can hold
 constexpr int kQBoxRows = 8;      // query rows of a copy
-constexpr uint32_t kBlockBytes = 128 * 128;
+constexpr uint32_t kBlockBytes = kTileKeys * 128;  // a unit's keys x 64 dims
 constexpr uint32_t kTileBytes = 2 * kBlockBytes;
+constexpr uint32_t kQBlockBytes = 128 * 128;
 constexpr uint32_t kPageBytes = kPage * 128;  // a page's 16 keys x 64 dims of one head
 constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
 constexpr int kMaxBatch = 4096;
@@ -106,7 +108,7 @@ struct SharedParams {
 // ---------------------------------------------------------------------------------------------
 // plan
 // ---------------------------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;  // at most: four rows a thread
 
 struct PlanSmem {
   long long warp_sums[kPlanThreads / 32], total;
@@ -130,7 +132,7 @@ __device__ __forceinline__ long long plan_scan(PlanSmem& s, long long v, long lo
   if (lane == 31) s.warp_sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const long long w = s.warp_sums[lane];
+    const long long w = lane < static_cast<int>(blockDim.x >> 5) ? s.warp_sums[lane] : 0;
     long long x = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -152,13 +154,14 @@ __device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PlanSmem& s = *reinterpret_cast<PlanSmem*>(smem_raw);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x);
+  launch_next();
   await_previous();
   if (tid == 0) s.bad = 0;
   const int G = p.groups;
-  for (int g = tid; g <= G && G > 0; g += kPlanThreads) s.cu[g] = p.cu_group_rows[g];
+  for (int g = tid; g <= G && G > 0; g += threads) s.cu[g] = p.cu_group_rows[g];
   __syncthreads();
-  for (int g = tid; g < G; g += kPlanThreads) {
+  for (int g = tid; g < G; g += threads) {
     const int a = s.cu[g], b = s.cu[g + 1];
     if (a < 0 || b < a || b > p.batch || b - a > p.max_group_rows) s.bad = 1;
     int n = p.shared_pages[g];
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   const int row_lo = grouped ? s.cu[0] : 0, row_hi = grouped ? s.cu[G] : 0;
 
   // rows: four consecutive ones a thread at most
-  const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
+  const int per = (p.batch + threads - 1) / threads;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   int len[4], group[4];
 #pragma unroll
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   }
   __syncthreads();
   // segments of shared pages
-  const int gper = (G + kPlanThreads - 1) / kPlanThreads;
+  const int gper = (G + threads - 1) / threads;
   const int g0 = min(G, tid * gper), g1 = min(G, g0 + gper);
   long long mine = 0, total = 0;
   for (int g = g0; g < g1; ++g)
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     *p.header = PlanHeader{units_all, segments, tiles, 0};
   }
   __syncthreads();
-  for (int i = tid; i < p.slices; i += kPlanThreads) {
+  for (int i = tid; i < p.slices; i += threads) {
     const int u = static_cast<int>(static_cast<long long>(units_all) * i / p.slices);
     int lo = 0, hi = max(segments, 1);  // last segment with a first unit <= u
     while (hi - lo > 1) {
@@ -293,12 +296,12 @@ struct UnitInfo {
 
 struct SharedSmem {
   uint8_t ring[kStages][2][kBlockBytes];
-  uint8_t q[2][2][kBlockBytes];
+  uint8_t q[2][2][kQBlockBytes];
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t info_full[kInfos];
-  uint64_t s_full[2], p_full[2], o_ready[2], o_free[2];
-  uint64_t mma_done;
+  uint64_t s_full[2], p_full[2], p_free[2], o_ready[2], o_free[2];
+  uint64_t mma_done[2];
   uint32_t tmem_base;
   UnitInfo info[kInfos];
 };
@@ -310,11 +313,20 @@ __device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, int
   return false;
 }
 
+// The same for a whole warp, one lane of it polling: 32 lanes of eight warps at it slow every other
+// thread's barrier operations down.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, int32_t* status) {
+  bool ok = true;
+  if (lane == 0) ok = wait_or_flag(bar, parity, status);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_next();
   await_previous();
   SharedSmem& s = *reinterpret_cast<SharedSmem*>(smem_raw);
   const int head = static_cast<int>(blockIdx.x) % p.hkv, slice = static_cast<int>(blockIdx.x) / p.hkv;
@@ -337,14 +349,15 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       mbar_init(&s.q_empty[i], 1);
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.p_free[i], 1);
+      mbar_init(&s.mma_done[i], 1);
       mbar_init(&s.o_ready[i], 1);
       mbar_init(&s.o_free[i], 4);
     }
     for (int i = 0; i < kInfos; ++i) mbar_init(&s.info_full[i], 1);
-    mbar_init(&s.mma_done, 1);
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tc::tmem_alloc<512>(&s.tmem_base);
+  if (warp == kPvWarp) tc::tmem_alloc<512>(&s.tmem_base);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -357,38 +370,59 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     bool ok = true;
     int it = 0, piece = 0, q_loads = 0;
     uint32_t st = 0, ph = 0, loads = 0;  // next ring stage, its parity, tiles loaded
-    int seg = p.slice_segment[slice];
-    auto load_tile = [&](const CUtensorMap* map, int pages, int token) {
+    // the next free stage
+    auto acquire = [&] {
       if (lane == 0) ok = wait_or_flag(&s.empty[st], ph ^ 1u, p.status);
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) return;
+    };
+    // one 16-key page per lane and half of its dims: lane 2 i + h copies half h of the unit's page i
+    auto load = [&](const CUtensorMap* map, int pages, int token) {
       if (lane == 0) mbar_arrive_expect_tx(&s.full[st], static_cast<uint32_t>(pages) * 2 * kPageBytes);
       __syncwarp();
-      const int pg = (lane >> 1) & (kTilePages - 1), kb = lane & 1;
-      const int t = __shfl_sync(0xffffffffu, token, pg);
-      if (lane < 2 * pages) tc::tma_load_3d(s.ring[st][kb] + pg * kPageBytes, map, kb * 64, head, t, &s.full[st]);
+      if (lane < 2 * pages)
+        tc::tma_load_3d(s.ring[st][lane & 1] + (lane >> 1) * kPageBytes, map, (lane & 1) * 64, head, token, &s.full[st]);
       ++loads;
       if (++st == kStages) {
         st = 0;
         ph ^= 1u;
       }
     };
+    // Segments' records are read 32 at a time, a lane each; table entries 32 at a time (kBatch units), a
+    // batch ahead, and those of the next segment's first units while this one's are loaded: an entry
+    // read just before its copies would cost its latency in every unit.
+    constexpr int kBatch = 32 / kTilePages;
+    int seg = p.slice_segment[slice], records = seg;
+    Segment lane_record = p.segments[min(seg + lane, plan.segments - 1)];
+    auto record = [&](int i) {
+      if (i >= records + 32) {
+        records = i;
+        lane_record = p.segments[min(i + lane, plan.segments - 1)];
+      }
+      const int from = i - records;
+      Segment g;
+      g.unit = __shfl_sync(0xffffffffu, lane_record.unit, from);
+      g.units = __shfl_sync(0xffffffffu, lane_record.units, from);
+      g.row = __shfl_sync(0xffffffffu, lane_record.row, from);
+      g.rows = __shfl_sync(0xffffffffu, lane_record.rows, from);
+      g.table_row = __shfl_sync(0xffffffffu, lane_record.table_row, from);
+      g.first_key = __shfl_sync(0xffffffffu, lane_record.first_key, from);
+      g.end_key = __shfl_sync(0xffffffffu, lane_record.end_key, from);
+      return g;
+    };
+    auto entries = [&](const Segment& g, int k) {
+      const int key = g.first_key + k * kTileKeys + lane * kPage;
+      return key < g.end_key ? p.block_table[static_cast<int64_t>(g.table_row) * p.bt_stride + key / kPage] : 0;
+    };
+    Segment g = record(seg);
+    int batch = entries(g, u0 - g.unit);
     while (it < nt && ok) {
-      const Segment g = p.segments[seg];
       const int k0 = u0 + it - g.unit, k1 = min(u1 - g.unit, g.units);
-      const int32_t* entries = p.block_table + static_cast<int64_t>(g.table_row) * p.bt_stride;
-      // the first token of this lane's page of unit k
-      auto page_token = [&](int k) {
-        const int key = g.first_key + k * kTileKeys + lane * kPage;
-        if (lane >= kTilePages || k >= k1 || key >= g.end_key) return 0;
-        const int e = entries[key / kPage];
-        if (e < 0 || e >= p.num_pages) {
-          flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
-          return 0;
-        }
-        return e * kPage;
-      };
-      int token = page_token(k0), token_next = page_token(k0 + 1);
+      Segment next = g;
+      int next_batch = 0;
+      if (it + k1 - k0 < nt) {
+        next = record(seg + 1);
+        next_batch = entries(next, 0);
+      }
       const int qb = piece & 1;
       if (lane == 0) ok = wait_or_flag(&s.q_empty[qb], ((piece >> 1) & 1) ^ 1u, p.status);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -401,35 +435,46 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         tc::tma_load_3d(s.q[qb][lane & 1] + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
                         g.row + (lane >> 1) * kQBoxRows, &s.q_full[qb]);
       const bool is_tile = seg < plan.tiles;
-      for (int k = k0; k < k1; ++k, ++it) {
-        const int token_ahead = page_token(k + 2);
-        const int keys = min(kTileKeys, g.end_key - (g.first_key + k * kTileKeys));
-        const int pages = (keys + kPage - 1) / kPage;
-        load_tile(&k_map, pages, token);
-        if (!ok) break;
-        // (info slot: its last unit has been consumed, since the stage that this unit's K went to
-        //  was released by a later unit's products)
-        if (lane == 0) {
-          UnitInfo& f = s.info[it % kInfos];
-          const int stream = it & 1;
-          const int cap = is_tile ? 2 * p.tile_rows : 2;
-          const int64_t slot = ((static_cast<int64_t>(slice) + (is_tile ? seg : seg - plan.tiles)) * p.hkv + head) * 2 + stream;
-          f.part = slot * cap * kRowFloats;
-          f.stats = cap * kHeadDim;
-          f.keys = keys;
-          f.flags = (k - k0 < 2 ? kFirst : 0) | (k1 - 1 - k < 2 ? kLast : 0) | (k == k0 ? kPieceStart : 0) |
-                    (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0);
-          f.rows = 2 * g.rows;
-          f.is_tile = is_tile ? 1 : 0;
-          mbar_arrive(&s.info_full[it % kInfos]);
+      for (int kb = k0; kb < k1 && ok; kb += kBatch) {
+        const int ahead = kb + kBatch < k1 ? entries(g, kb + kBatch) : 0;
+        for (int k = kb; k < min(kb + kBatch, k1); ++k, ++it) {
+          const int keys = min(kTileKeys, g.end_key - (g.first_key + k * kTileKeys));
+          const int pages = (keys + kPage - 1) / kPage;
+          int e = __shfl_sync(0xffffffffu, batch, (k - kb) * kTilePages + ((lane >> 1) & (kTilePages - 1)));
+          if (lane < 2 * pages && (e < 0 || e >= p.num_pages)) {
+            flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
+            e = 0;
+          }
+          acquire();
+          if (!ok) break;
+          // The unit that this info slot held last has been consumed: the stage that K goes to was
+          // released by P V of the unit three before this one. K's barrier hands the info on too.
+          if (lane == 0) {
+            UnitInfo& f = s.info[it % kInfos];
+            const int stream = it & 1;
+            const int cap = is_tile ? 2 * p.tile_rows : 2;
+            const int64_t slot =
+                ((static_cast<int64_t>(slice) + (is_tile ? seg : seg - plan.tiles)) * p.hkv + head) * 2 + stream;
+            f.part = slot * cap * kRowFloats;
+            f.stats = cap * kHeadDim;
+            f.keys = keys;
+            f.flags = (k - k0 < 2 ? kFirst : 0) | (k1 - 1 - k < 2 ? kLast : 0) | (k == k0 ? kPieceStart : 0) |
+                      (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0);
+            f.rows = 2 * g.rows;
+            f.is_tile = is_tile ? 1 : 0;
+            mbar_arrive(&s.info_full[it % kInfos]);
+          }
+          load(&k_map, pages, e * kPage);
+          acquire();
+          if (!ok) break;
+          load(&v_map, pages, e * kPage);
         }
-        load_tile(&v_map, pages, token);
-        if (!ok) break;
-        token = token_next;
-        token_next = token_ahead;
+        batch = ahead;
       }
       ++piece;
       ++seg;
+      g = next;
+      batch = next_batch;
     }
     // do not leave while copies into this CTA's shared memory may still be landing (only after a wait
     // that gave up: else all of them have been consumed)
@@ -439,78 +484,97 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       for (int k = max(0, q_loads - 2); k < q_loads; ++k) wait_or_flag(&s.q_full[k & 1], (k >> 1) & 1, p.status);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMA issuer
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------------------ S = Q K^T
+    // Two warps issue the two products: every wait, group of instructions and commit takes an issuing
+    // thread some hundred cycles (measured: a wait on a phase long complete 170 to 300, 8 instructions
+    // 590, all of a 64-key unit 2,300 from one thread, 1.6 times what its bytes take to arrive).
     if (lane == 0) {
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(s.q[0][0]), 16, 1024);
       const uint64_t dk = tc::smem_desc_sw128(smem_addr(s.ring[0][0]), 16, 1024);
-      const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.ring[0][0]), kBlockBytes, 1024);
       bool ok = true;
-      uint32_t kst = 0, kph = 0, vst = 1, vph = 0;  // stages of the next K and the next V tile
-      auto advance = [](uint32_t& stage, uint32_t& parity) {
-        stage += 2;
-        if (stage >= kStages) {
-          stage -= kStages;
-          parity ^= 1u;
+      uint32_t st = 0, ph = 0, q_uses[2] = {0, 0};
+      for (int it = 0; it < nt; ++it) {
+        const int stream = it & 1;
+        // S takes the columns of the stream's last P
+        ok = (it < 2 || wait_or_flag(&s.p_free[stream], ((it >> 1) - 1) & 1, p.status)) &&
+             wait_or_flag(&s.full[st], ph, p.status);
+        if (!ok) break;
+        const volatile UnitInfo& f = s.info[it % kInfos];
+        const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
+        const int qb = flags & kQBuffer1 ? 1 : 0;
+        if (flags & kPieceStart) {
+          ok = wait_or_flag(&s.q_full[qb], q_uses[qb] & 1, p.status);
+          ++q_uses[qb];
+          if (!ok) break;
         }
-      };
-      uint32_t q_uses[2] = {0, 0}, pieces[2] = {0, 0};
-      int pages = 0, flags = 0;  // of the unit whose P V comes next
-      for (int it = 0; it <= nt && ok; ++it) {
-        int pages_now = 0, flags_now = 0;
-        if (it < nt) {
-          const int stream = it & 1;
-          ok = wait_or_flag(&s.info_full[it % kInfos], (it / kInfos) & 1, p.status);
-          if (!ok) break;
-          const volatile UnitInfo& f = s.info[it % kInfos];
-          pages_now = (f.keys + kPage - 1) / kPage;
-          flags_now = f.flags;
-          const int qb = flags_now & kQBuffer1 ? 1 : 0;
-          if (flags_now & kPieceStart) {
-            ok = wait_or_flag(&s.q_full[qb], q_uses[qb] & 1, p.status);
-            ++q_uses[qb];
-          }
-          ok = ok && wait_or_flag(&s.full[kst], kph, p.status);
-          if (!ok) break;
-          tc::fence_after_sync();
-          // N = the unit's keys in whole pages; the products run in the order of their issue, so S may
-          // take the columns of the P that the stream's last P V read
-          const uint32_t id = tc::idesc_bf16(128, 0, 0, 0) | static_cast<uint32_t>(pages_now * kPage >> 3) << 17;
-          const uint64_t a = dq + (qb * kTileBytes >> 4), b = dk + (kst * kTileBytes >> 4);
+        tc::fence_after_sync();
+        // N = the unit's keys in whole pages
+        const uint32_t id = tc::idesc_bf16(128, 0, 0, 0) | static_cast<uint32_t>(pages * kPage >> 3) << 17;
+        const uint64_t a = dq + (qb * 2 * kQBlockBytes >> 4), b = dk + (st * kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;
-            tc::mma_ss(tmem + stream * 128, a + off, b + off, id, kk > 0 ? 1u : 0u);
-          }
-          tc::mma_commit(&s.s_full[stream]);
-          tc::mma_commit(&s.empty[kst]);
-          if (flags_now & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
-          advance(kst, kph);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t step = (kk & 3) * 32;
+          const uint64_t ak = a + (((kk >> 2) * kQBlockBytes + step) >> 4);
+          const uint64_t bk = b + (((kk >> 2) * kBlockBytes + step) >> 4);
+          if (kk == 0) tc::mma_ss_c<false>(tmem + stream * kTileKeys, ak, bk, id);
+          else tc::mma_ss_c<true>(tmem + stream * kTileKeys, ak, bk, id);
         }
-        if (it > 0) {
-          const int t = it - 1, stream = t & 1;
-          ok = wait_or_flag(&s.p_full[stream], (t >> 1) & 1, p.status) && wait_or_flag(&s.full[vst], vph, p.status);
-          if (ok && (flags & kFirst)) {
-            if (pieces[stream] > 0) ok = wait_or_flag(&s.o_free[stream], (pieces[stream] - 1) & 1, p.status);
-            ++pieces[stream];
-          }
-          if (!ok) break;
-          tc::fence_after_sync();
-          constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
-          const uint64_t b = dv + (vst * kTileBytes >> 4);
-          for (int kk = 0; kk < pages; ++kk)
-            tc::mma_ts(tmem + 256 + stream * 128, tmem + stream * 128 + kk * 8, b + kk * (kPageBytes >> 4), id,
-                       kk > 0 || !(flags & kFirst) ? 1u : 0u);
-          tc::mma_commit(&s.empty[vst]);
-          if (flags & kLast) tc::mma_commit(&s.o_ready[stream]);
-          advance(vst, vph);
+        tc::mma_commit(&s.s_full[stream]);
+        tc::mma_commit(&s.empty[st]);
+        if (flags & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
+        st += 2;
+        if (st >= kStages) {
+          st -= kStages;
+          ph ^= 1u;
         }
-        pages = pages_now;
-        flags = flags_now;
       }
       // every product must have finished before TMEM is released
-      tc::mma_commit(&s.mma_done);
-      wait_or_flag(&s.mma_done, 0, p.status);
+      tc::mma_commit(&s.mma_done[0]);
+      wait_or_flag(&s.mma_done[0], 0, p.status);
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------------ O += P V
+    if (lane == 0) {
+      const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.ring[0][0]), kBlockBytes, 1024);
+      constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
+      bool ok = true;
+      uint32_t st = 1, ph = 0, pieces[2] = {0, 0};
+      for (int it = 0; it < nt; ++it) {
+        const int stream = it & 1;
+        // (P's barrier hands the info on too)
+        ok = wait_or_flag(&s.p_full[stream], (it >> 1) & 1, p.status) && wait_or_flag(&s.full[st], ph, p.status);
+        if (!ok) break;
+        const volatile UnitInfo& f = s.info[it % kInfos];
+        const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
+        if (flags & kFirst) {
+          if (pieces[stream] > 0) ok = wait_or_flag(&s.o_free[stream], (pieces[stream] - 1) & 1, p.status);
+          ++pieces[stream];
+          if (!ok) break;
+        }
+        tc::fence_after_sync();
+        const uint32_t o = tmem + 256 + stream * 128, a = tmem + stream * kTileKeys;
+        const uint64_t b = dv + (st * kTileBytes >> 4);
+        tc::mma_ts(o, a, b, id, flags & kFirst ? 0u : 1u);
+        if (pages == kTilePages) {
+#pragma unroll
+          for (int kk = 1; kk < kTilePages; ++kk)
+            tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
+        } else {
+          for (int kk = 1; kk < pages; ++kk) tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
+        }
+        tc::mma_commit(&s.p_free[stream]);
+        tc::mma_commit(&s.empty[st]);
+        if (flags & kLast) tc::mma_commit(&s.o_ready[stream]);
+        st += 2;
+        if (st >= kStages) {
+          st -= kStages;
+          ph ^= 1u;
+        }
+      }
+      tc::mma_commit(&s.mma_done[1]);
+      wait_or_flag(&s.mma_done[1], 0, p.status);
     }
     __syncwarp();
   }
@@ -520,19 +584,19 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     const int stream = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_bits + stream * 128, t_o = tmem + lane_bits + 256 + stream * 128;
+    const uint32_t t_s = tmem + lane_bits + stream * kTileKeys, t_o = tmem + lane_bits + 256 + stream * 128;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
     uint32_t n = 0, pieces = 0;
     float m_used = -CUDART_INF_F, l = 0.f;
     for (int it = stream; it < nt; it += 2, ++n) {
-      ok = __all_sync(0xffffffffu, wait_or_flag(&s.info_full[it % kInfos], (it / kInfos) & 1, p.status));
+      ok = warp_wait(&s.info_full[it % kInfos], (it / kInfos) & 1, lane, p.status);
       if (!ok) break;
       const volatile UnitInfo& f = s.info[it % kInfos];
       const int keys = f.keys, flags = f.flags, rows = f.rows, stats = f.stats;
       float* part = (f.is_tile ? p.tile_parts : p.row_parts) + f.part;
       const bool used = quarter * 32 < rows;  // some of this warp's rows are query rows
-      ok = __all_sync(0xffffffffu, wait_or_flag(&s.s_full[stream], n & 1, p.status));
+      ok = warp_wait(&s.s_full[stream], n & 1, lane, p.status);
       if (!ok) break;
       tc::fence_after_sync();
       if (flags & kFirst) {
@@ -540,7 +604,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         l = 0.f;
       }
       if (used) {
-        uint32_t sb[128];
+        uint32_t sb[kTileKeys];
         float cm[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -550,7 +614,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         if (keys < kTileKeys) {  // keys past the segment's end (their scores are whatever TMEM held)
           mx = -CUDART_INF_F;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
+          for (int c = 0; c < kTileKeys; ++c) {
             if (c >= keys) sb[c] = 0xff800000u;
             mx = fmaxf(mx, __uint_as_float(sb[c]));
           }
@@ -561,8 +625,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           const float m_new = grow ? mx2 : m_used;
           const float alpha = m_used == -CUDART_INF_F ? 0.f : fast_exp2(m_used - m_new);
           if (!(flags & kFirst)) {
-            // O holds the stream's sum through its last unit: that product was issued before this
-            // unit's S, whose completion has been seen
+            // O holds the stream's sum through its last unit: this unit's S was issued after that
+            // product had completed
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t o32[32];
@@ -604,7 +668,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         // slots of the last page after the last key may hold anything, NaN too: their V rows meet
         // weights of 0 as zeros
         const uint32_t v = 2 * static_cast<uint32_t>(it) + 1, vst = v % kStages;
-        ok = __all_sync(0xffffffffu, wait_or_flag(&s.full[vst], (v / kStages) & 1, p.status));
+        ok = warp_wait(&s.full[vst], (v / kStages) & 1, lane, p.status);
         if (!ok) break;
         const int end = (keys + kPage - 1) / kPage * kPage;
         for (int e = keys * 16 + r; e < end * 16; e += 128)
@@ -615,7 +679,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.p_full[stream]);
       if (flags & kLast) {
-        ok = __all_sync(0xffffffffu, wait_or_flag(&s.o_ready[stream], pieces & 1, p.status));
+        ok = warp_wait(&s.o_ready[stream], pieces & 1, lane, p.status);
         if (!ok) break;
         ++pieces;
         tc::fence_after_sync();
@@ -645,7 +709,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
 
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kPvWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc<512>(tmem);
   }
@@ -700,16 +764,28 @@ __global__ void __launch_bounds__(512) shared_merge_kernel(const SharedParams p)
       l = l * keep + sum;
       acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
       const uint32_t some = __ballot_sync(0xffffffffu, ml.x != -CUDART_INF_F);
-      for (uint32_t left = some; left != 0; left &= left - 1) {
-        const int k = __ffs(left) - 1;
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* pk = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), k));
-        const float4 v = reinterpret_cast<const float4*>(pk + r * kHeadDim)[lane];
-        acc.x += wk * v.x;
-        acc.y += wk * v.y;
-        acc.z += wk * v.z;
-        acc.w += wk * v.w;
+      // eight results' loads in flight
+      for (uint32_t left = some; left != 0;) {
+        float wk[8];
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int k = left != 0 ? __ffs(left) - 1 : 0;
+          wk[j] = __shfl_sync(0xffffffffu, w, k);
+          if (left == 0) wk[j] = 0.f;
+          const float* pk = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), k));
+          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (left != 0) v[j] = reinterpret_cast<const float4*>(pk + r * kHeadDim)[lane];
+          left &= left - 1;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc.x += wk[j] * v[j].x;
+          acc.y += wk[j] * v[j].y;
+          acc.z += wk[j] * v[j].z;
+          acc.w += wk[j] * v[j].w;
+        }
       }
     }
   }
@@ -856,7 +932,10 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   p.tile_parts = reinterpret_cast<float*>(ws + l.tile_parts);
   p.row_parts = reinterpret_cast<float*>(ws + l.row_parts);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_dependent(shared_plan_kernel, 1, kPlanThreads, sizeof(PlanSmem), st, 0, p);
+  // a thread per row, group and slice, in whole warps
+  const unsigned plan_threads = static_cast<unsigned>(
+      std::min(kPlanThreads, (std::max({static_cast<int>(batch), static_cast<int>(groups), l.slices}) + 31) / 32 * 32));
+  cudaError_t e = launch_dependent(shared_plan_kernel, 1, plan_threads, sizeof(PlanSmem), st, 0, p);
   if (e == cudaSuccess)
     e = launch_dependent(shared_attention_kernel, static_cast<unsigned>(l.slices * hkv), kThreads, sizeof(SharedSmem),
                          st, 0, qm, km, vm, p);

@@ -31,4 +31,8 @@ cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned 
 
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next dependent launch of the stream be set up while this kernel still runs (it waits in its
+// await_previous() all the same).
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace pa
