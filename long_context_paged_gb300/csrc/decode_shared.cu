@@ -33,7 +33,7 @@
 
 namespace pa {
 
-bool make_map_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t heads, uint32_t box_rows);
+bool make_map_pages(CUtensorMap* map, const void* base, uint64_t num_pages, uint64_t heads);
 bool make_map_heads(CUtensorMap* map, const void* base, uint64_t outer, uint64_t heads, uint32_t box_heads,
                     uint32_t box_rows);
 
@@ -42,17 +42,20 @@ namespace {
 constexpr int kTileRows = 64;     // rows of a group per segment (x 2 query heads = 128)
 constexpr int kTileKeys = 128;    // keys of a unit
 constexpr int kTilePages = kTileKeys / kPage;
-constexpr int kStages = 5;        // K and V tiles in flight, in turn
-constexpr int kThreads = 384;     // 8 softmax warps; producer, two MMA issuers and a spare
-constexpr int kProducerWarp = 8;
+constexpr int kKStages = 2;       // K tiles in flight, each released once its scores are there
+constexpr int kVStages = 3;       // V tiles in flight: needed a softmax later
+constexpr int kThreads = 384;     // 8 softmax warps, two producers, two MMA issuers
+constexpr int kKProducerWarp = 8;  // units, Q and K
+constexpr int kVProducerWarp = 11;
 constexpr int kPvWarp = 9;        // issues O += P V
 constexpr int kScoreWarp = 10;    // issues S = Q K^T
 constexpr int kInfos = 8;         // published units in flight: more than the stages can hold
 constexpr int kQBoxRows = 8;      // query rows of a copy
-constexpr uint32_t kBlockBytes = kTileKeys * 128;  // a unit's keys x 64 dims
-constexpr uint32_t kTileBytes = 2 * kBlockBytes;
+constexpr uint32_t kTileBytes = kTileKeys * 256;   // a unit's keys
 constexpr uint32_t kQBlockBytes = 128 * 128;
-constexpr uint32_t kPageBytes = kPage * 128;  // a page's 16 keys x 64 dims of one head
+constexpr uint32_t kPageBytes = kPage * 256;       // a page's 16 keys of one head: two groups of 8 keys, each
+constexpr uint32_t kGroupBytes = 8 * 256;          // of them 1 KB of the first 64 dims and 1 KB of the others
+constexpr uint32_t kHalfBytes = 8 * 128;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroups = 4096;
@@ -295,9 +298,10 @@ struct UnitInfo {
 };
 
 struct SharedSmem {
-  uint8_t ring[kStages][2][kBlockBytes];
+  uint8_t k[kKStages][kTileBytes];
+  uint8_t v[kVStages][kTileBytes];
   uint8_t q[2][2][kQBlockBytes];
-  uint64_t full[kStages], empty[kStages];
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t info_full[kInfos];
   uint64_t s_full[2], p_full[2], p_free[2], o_ready[2], o_free[2];
@@ -340,9 +344,13 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&s.v_full[i], 1);
+      mbar_init(&s.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.q_full[i], 1);
@@ -365,28 +373,20 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
 
   if (warp >= 8) {
     tc::regs_decrease<kControlRegs>();
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------------ producer: units, Q, K and V
+  if (warp == kKProducerWarp || warp == kVProducerWarp) {
+    // ------------------------------------------------------------------ producers
+    // Both walk the slice's units; one loads Q and K and publishes the units, the other loads V. A copy
+    // takes its issuing warp about 75 cycles, so a page is one copy, and K and V have a warp each (two
+    // copies a page from one warp: 3,700 cycles a unit, whose bytes take 2,800 to arrive).
+    const bool is_k = warp == kKProducerWarp;
+    const CUtensorMap* map = is_k ? &k_map : &v_map;
+    uint8_t(*ring)[kTileBytes] = is_k ? s.k : s.v;
+    uint64_t* full = is_k ? s.k_full : s.v_full;
+    uint64_t* empty = is_k ? s.k_empty : s.v_empty;
+    const uint32_t stages = is_k ? kKStages : kVStages;
     bool ok = true;
-    int it = 0, piece = 0, q_loads = 0;
+    int it = 0, piece = 0;
     uint32_t st = 0, ph = 0, loads = 0;  // next ring stage, its parity, tiles loaded
-    // the next free stage
-    auto acquire = [&] {
-      if (lane == 0) ok = wait_or_flag(&s.empty[st], ph ^ 1u, p.status);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    };
-    // one 16-key page per lane and half of its dims: lane 2 i + h copies half h of the unit's page i
-    auto load = [&](const CUtensorMap* map, int pages, int token) {
-      if (lane == 0) mbar_arrive_expect_tx(&s.full[st], static_cast<uint32_t>(pages) * 2 * kPageBytes);
-      __syncwarp();
-      if (lane < 2 * pages)
-        tc::tma_load_3d(s.ring[st][lane & 1] + (lane >> 1) * kPageBytes, map, (lane & 1) * 64, head, token, &s.full[st]);
-      ++loads;
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1u;
-      }
-    };
     // Segments' records are read 32 at a time, a lane each; table entries 32 at a time (kBatch units), a
     // batch ahead, and those of the next segment's first units while this one's are loaded: an entry
     // read just before its copies would cost its latency in every unit.
@@ -424,32 +424,37 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         next_batch = entries(next, 0);
       }
       const int qb = piece & 1;
-      if (lane == 0) ok = wait_or_flag(&s.q_empty[qb], ((piece >> 1) & 1) ^ 1u, p.status);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      const int boxes = (g.rows + kQBoxRows - 1) / kQBoxRows;
-      if (lane == 0) mbar_arrive_expect_tx(&s.q_full[qb], boxes * 2 * (2 * kQBoxRows * 128));
-      __syncwarp();
-      ++q_loads;
-      if (lane < 2 * boxes)
-        tc::tma_load_3d(s.q[qb][lane & 1] + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
-                        g.row + (lane >> 1) * kQBoxRows, &s.q_full[qb]);
+      if (is_k) {
+        if (lane == 0) ok = wait_or_flag(&s.q_empty[qb], ((piece >> 1) & 1) ^ 1u, p.status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const int boxes = (g.rows + kQBoxRows - 1) / kQBoxRows;
+        if (lane == 0) mbar_arrive_expect_tx(&s.q_full[qb], boxes * 2 * (2 * kQBoxRows * 128));
+        __syncwarp();
+        if (lane < 2 * boxes)
+          tc::tma_load_3d(s.q[qb][lane & 1] + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
+                          g.row + (lane >> 1) * kQBoxRows, &s.q_full[qb]);
+      }
+      ++piece;
       const bool is_tile = seg < plan.tiles;
       for (int kb = k0; kb < k1 && ok; kb += kBatch) {
         const int ahead = kb + kBatch < k1 ? entries(g, kb + kBatch) : 0;
         for (int k = kb; k < min(kb + kBatch, k1); ++k, ++it) {
           const int keys = min(kTileKeys, g.end_key - (g.first_key + k * kTileKeys));
           const int pages = (keys + kPage - 1) / kPage;
-          int e = __shfl_sync(0xffffffffu, batch, (k - kb) * kTilePages + ((lane >> 1) & (kTilePages - 1)));
-          if (lane < 2 * pages && (e < 0 || e >= p.num_pages)) {
+          // lane i copies the unit's page i
+          int e = __shfl_sync(0xffffffffu, batch, (k - kb) * kTilePages + (lane & (kTilePages - 1)));
+          if (lane < pages && (e < 0 || e >= p.num_pages)) {
             flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
             e = 0;
           }
-          acquire();
+          if (lane == 0) ok = wait_or_flag(&empty[st], ph ^ 1u, p.status);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          // The unit that this info slot held last has been consumed: the stage that K goes to was
-          // released by P V of the unit three before this one. K's barrier hands the info on too.
-          if (lane == 0) {
+          // K's barrier hands the info on. The unit that its slot held last has been consumed: K's stage
+          // was released by the scores of unit it - kKStages, which were issued after P V of the unit two
+          // before that one.
+          if (is_k && lane == 0) {
             UnitInfo& f = s.info[it % kInfos];
             const int stream = it & 1;
             const int cap = is_tile ? 2 * p.tile_rows : 2;
@@ -464,14 +469,17 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
             f.is_tile = is_tile ? 1 : 0;
             mbar_arrive(&s.info_full[it % kInfos]);
           }
-          load(&k_map, pages, e * kPage);
-          acquire();
-          if (!ok) break;
-          load(&v_map, pages, e * kPage);
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(pages) * kPageBytes);
+          __syncwarp();
+          if (lane < pages) tc::tma_load_5d(ring[st] + lane * kPageBytes, map, 0, 0, 0, 2 * e, head, &full[st]);
+          ++loads;
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
         batch = ahead;
       }
-      ++piece;
       ++seg;
       g = next;
       batch = next_batch;
@@ -479,9 +487,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // do not leave while copies into this CTA's shared memory may still be landing (only after a wait
     // that gave up: else all of them have been consumed)
     if (!ok && lane == 0) {
-      for (uint32_t k = loads > kStages ? loads - kStages : 0; k < loads; ++k)
-        wait_or_flag(&s.full[k % kStages], (k / kStages) & 1, p.status);
-      for (int k = max(0, q_loads - 2); k < q_loads; ++k) wait_or_flag(&s.q_full[k & 1], (k >> 1) & 1, p.status);
+      for (uint32_t k = loads > stages ? loads - stages : 0; k < loads; ++k)
+        wait_or_flag(&full[k % stages], (k / stages) & 1, p.status);
+      for (int k = max(0, piece - 2); is_k && k < piece; ++k) wait_or_flag(&s.q_full[k & 1], (k >> 1) & 1, p.status);
     }
     __syncwarp();
   } else if (warp == kScoreWarp) {
@@ -491,14 +499,14 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // 590, all of a 64-key unit 2,300 from one thread, 1.6 times what its bytes take to arrive).
     if (lane == 0) {
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(s.q[0][0]), 16, 1024);
-      const uint64_t dk = tc::smem_desc_sw128(smem_addr(s.ring[0][0]), 16, 1024);
+      const uint64_t dk = tc::smem_desc_sw128(smem_addr(s.k[0]), 16, kGroupBytes);
       bool ok = true;
       uint32_t st = 0, ph = 0, q_uses[2] = {0, 0};
       for (int it = 0; it < nt; ++it) {
         const int stream = it & 1;
         // S takes the columns of the stream's last P
         ok = (it < 2 || wait_or_flag(&s.p_free[stream], ((it >> 1) - 1) & 1, p.status)) &&
-             wait_or_flag(&s.full[st], ph, p.status);
+             wait_or_flag(&s.k_full[st], ph, p.status);
         if (!ok) break;
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
@@ -516,16 +524,15 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         for (int kk = 0; kk < 8; ++kk) {
           const uint32_t step = (kk & 3) * 32;
           const uint64_t ak = a + (((kk >> 2) * kQBlockBytes + step) >> 4);
-          const uint64_t bk = b + (((kk >> 2) * kBlockBytes + step) >> 4);
+          const uint64_t bk = b + (((kk >> 2) * kHalfBytes + step) >> 4);
           if (kk == 0) tc::mma_ss_c<false>(tmem + stream * kTileKeys, ak, bk, id);
           else tc::mma_ss_c<true>(tmem + stream * kTileKeys, ak, bk, id);
         }
         tc::mma_commit(&s.s_full[stream]);
-        tc::mma_commit(&s.empty[st]);
+        tc::mma_commit(&s.k_empty[st]);
         if (flags & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
-        st += 2;
-        if (st >= kStages) {
-          st -= kStages;
+        if (++st == kKStages) {
+          st = 0;
           ph ^= 1u;
         }
       }
@@ -537,14 +544,14 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------------ O += P V
     if (lane == 0) {
-      const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.ring[0][0]), kBlockBytes, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.v[0]), kHalfBytes, kGroupBytes);
       constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
       bool ok = true;
-      uint32_t st = 1, ph = 0, pieces[2] = {0, 0};
+      uint32_t st = 0, ph = 0, pieces[2] = {0, 0};
       for (int it = 0; it < nt; ++it) {
         const int stream = it & 1;
         // (P's barrier hands the info on too)
-        ok = wait_or_flag(&s.p_full[stream], (it >> 1) & 1, p.status) && wait_or_flag(&s.full[st], ph, p.status);
+        ok = wait_or_flag(&s.p_full[stream], (it >> 1) & 1, p.status) && wait_or_flag(&s.v_full[st], ph, p.status);
         if (!ok) break;
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
@@ -565,11 +572,10 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           for (int kk = 1; kk < pages; ++kk) tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
         }
         tc::mma_commit(&s.p_free[stream]);
-        tc::mma_commit(&s.empty[st]);
+        tc::mma_commit(&s.v_empty[st]);
         if (flags & kLast) tc::mma_commit(&s.o_ready[stream]);
-        st += 2;
-        if (st >= kStages) {
-          st -= kStages;
+        if (++st == kVStages) {
+          st = 0;
           ph ^= 1u;
         }
       }
@@ -667,12 +673,13 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       if (keys % kPage != 0) {
         // slots of the last page after the last key may hold anything, NaN too: their V rows meet
         // weights of 0 as zeros
-        const uint32_t v = 2 * static_cast<uint32_t>(it) + 1, vst = v % kStages;
-        ok = warp_wait(&s.full[vst], (v / kStages) & 1, lane, p.status);
+        const uint32_t vst = static_cast<uint32_t>(it) % kVStages;
+        ok = warp_wait(&s.v_full[vst], (static_cast<uint32_t>(it) / kVStages) & 1, lane, p.status);
         if (!ok) break;
         const int end = (keys + kPage - 1) / kPage * kPage;
-        for (int e = keys * 16 + r; e < end * 16; e += 128)
-          *reinterpret_cast<uint4*>(s.ring[vst][(e >> 3) & 1] + (e >> 4) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        for (int e = keys * 16 + r; e < end * 16; e += 128)  // 16 bytes of a key
+          *reinterpret_cast<uint4*>(s.v[vst] + (e >> 7) * kGroupBytes + ((e >> 3) & 1) * kHalfBytes + ((e >> 4) & 7) * 128 +
+                                    (e & 7) * 16) = make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async_smem();
       }
       tc::fence_before_sync();
@@ -876,8 +883,8 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
   CUtensorMap qm, km, vm;
   if (!make_map_heads(&qm, q, static_cast<uint64_t>(batch), dims.num_q_heads, kGroup, kQBoxRows) ||
-      !make_map_3d(&km, k_pool, static_cast<uint64_t>(num_pages) * kPage, hkv, kPage) ||
-      !make_map_3d(&vm, v_pool, static_cast<uint64_t>(num_pages) * kPage, hkv, kPage)) {
+      !make_map_pages(&km, k_pool, static_cast<uint64_t>(num_pages), hkv) ||
+      !make_map_pages(&vm, v_pool, static_cast<uint64_t>(num_pages), hkv)) {
     snprintf_error("cuTensorMapEncodeTiled failed for the decode's operands");
     return PA_ERR_CUDA;
   }

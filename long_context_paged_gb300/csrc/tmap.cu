@@ -48,6 +48,22 @@ bool make_map_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t he
   return make_map_heads(map, base, outer, heads, 1, box_rows);
 }
 
+// A page pool [num_pages][16 tokens][heads][128 dims] as 5-D [head][8 tokens' group][half of the dims][8
+// tokens][64 dims]; box = one head's page, which arrives as two groups of 8 tokens, each 1 KB of the first
+// 64 dims and 1 KB of the others: whole swizzle atoms at one stride however many pages stand behind each
+// other. 128-byte swizzle.
+bool make_map_pages(CUtensorMap* map, const void* base, uint64_t num_pages, uint64_t heads) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[5] = {64, 8, 2, num_pages * 2, heads};
+  cuuint64_t strides[4] = {heads * 256, 128, 8 * heads * 256, 256};
+  cuuint32_t box[5] = {64, 8, 2, 2, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2-D bf16 matrix [rows][cols] with a row stride in bytes; box = 64 columns x box_rows rows;
 // 128-byte swizzle; zero fill outside the matrix.
 bool make_map_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
