@@ -39,7 +39,8 @@ bool make_map_heads(CUtensorMap* map, const void* base, uint64_t outer, uint64_t
 
 namespace {
 
-constexpr int kTileRows = 64;     // rows of a group per segment (x 2 query heads = 128)
+constexpr int kTileRows = 64;     // rows of a matrix tile (x 2 query heads = 128)
+constexpr int kSegmentRows = 2 * kTileRows;  // rows of a group per segment
 constexpr int kTileKeys = 128;    // keys of a unit
 constexpr int kTilePages = kTileKeys / kPage;
 constexpr int kKStages = 2;       // K tiles in flight, each released once its scores are there
@@ -59,7 +60,7 @@ constexpr uint32_t kHalfBytes = 8 * 128;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroups = 4096;
-constexpr int kMaxSegments = kMaxBatch + kMaxGroups + kMaxBatch / kTileRows;
+constexpr int kMaxSegments = kMaxBatch + kMaxGroups + kMaxBatch / kSegmentRows;
 constexpr int kMaxSlices = 256;   // CTAs per KV head
 // Registers of a softmax thread and of the others; 256 x 208 + 128 x 88 = 384 x 168, what the CTA is
 // launched with (checked on the host).
@@ -76,11 +77,13 @@ struct Segment {
   int32_t pad;
 };
 
+// Where a row's partial results are: its segment of shared pages and its own, in units and as an index
+// into the results (units = 0: none).
 struct RowPlan {
-  int32_t tile, in_tile;     // segment of the shared pages and the row's place in it (-1: none)
-  int32_t own;               // segment of the row's own pages (-1: none)
-  int32_t pad;
+  int32_t tile_unit, tile_units, tile, in_tile;  // in_tile: the row's place; + kTwoTiles
+  int32_t own_unit, own_units, own, pad;
 };
+constexpr int kTwoTiles = 1 << 16;  // the segment has two matrix tiles, a stream each
 
 struct PlanHeader {
   int32_t units, segments, tiles;  // tiles: segments of shared pages, which come first
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   long long mine = 0, total = 0;
   for (int g = g0; g < g1; ++g)
     if (grouped && s.first[g] != 0x7fffffff) {
-      const long long tiles = (s.cu[g + 1] - s.cu[g] + kTileRows - 1) / kTileRows;
+      const long long tiles = (s.cu[g + 1] - s.cu[g] + kSegmentRows - 1) / kSegmentRows;
       mine += tiles << 40 | tiles * units_of(s.shared[g] * kPage);
     }
   long long at = plan_scan(s, mine, total);
@@ -225,8 +228,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     int seg = static_cast<int>(at >> 40), unit = static_cast<int>(at & ((1ll << 40) - 1));
     const int units = units_of(s.shared[g] * kPage);
     s.tile0[g] = seg;
-    for (int r = s.cu[g]; r < s.cu[g + 1]; r += kTileRows) {
-      p.segments[seg] = Segment{unit, units, r, min(kTileRows, s.cu[g + 1] - r), s.first[g], 0, s.shared[g] * kPage, 0};
+    for (int r = s.cu[g]; r < s.cu[g + 1]; r += kSegmentRows) {
+      p.segments[seg] = Segment{unit, units, r, min(kSegmentRows, s.cu[g + 1] - r), s.first[g], 0, s.shared[g] * kPage, 0};
       s.unit[seg++] = unit;
       unit += units;
     }
@@ -250,14 +253,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     if (b >= b1) continue;
     const int first = g >= 0 ? s.shared[g] * kPage : 0;
     const int units = units_of(len[k] - first);
-    RowPlan r{-1, 0, -1, 0};
+    RowPlan r{0, 0, 0, 0, 0, 0, 0, 0};
     if (g >= 0) {
       const int in_group = b - s.cu[g];
-      r.tile = s.tile0[g] + in_group / kTileRows;
-      r.in_tile = in_group % kTileRows;
+      r.tile = s.tile0[g] + in_group / kSegmentRows;
+      r.tile_units = units_of(first);
+      r.tile_unit = s.unit[r.tile];
+      const bool two = s.cu[g + 1] - s.cu[g] - in_group / kSegmentRows * kSegmentRows > kTileRows;
+      r.in_tile = in_group % kSegmentRows | (two ? kTwoTiles : 0);
     }
     if (units > 0) {
-      r.own = seg;
+      r.own = seg - tiles;
+      r.own_unit = unit;
+      r.own_units = units;
       p.segments[seg] = Segment{unit, units, b, 1, b, first, len[k], 0};
       s.unit[seg++] = unit;
       unit += units;
@@ -285,11 +293,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
 // ---------------------------------------------------------------------------------------------
 constexpr int kFirst = 1, kLast = 2;          // of this stream in the piece
 constexpr int kPieceStart = 4, kPieceEnd = 8; // of the piece
-constexpr int kQBuffer1 = 16;
+constexpr int kQBuffer1 = 16;                 // else buffer 0
+constexpr int kBoth = 32;                     // both streams take the unit, each a tile of its own
 
 struct UnitInfo {
-  int64_t part;     // where the stream's partial result goes, in floats; row r's O at + 128 r
-  int32_t stats;    // (m, l) of row r at part + stats + 2 r
+  int64_t part;     // where stream 0's partial result goes, in floats; row r's O at + 128 r
+  int32_t stats;    // (m, l) of row r at part + stats + 2 r; stream 1's result at part + stats / 128 * kRowFloats
   int32_t keys;
   int32_t flags;
   int32_t rows;     // query rows x heads
@@ -385,7 +394,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     uint64_t* empty = is_k ? s.k_empty : s.v_empty;
     const uint32_t stages = is_k ? kKStages : kVStages;
     bool ok = true;
-    int it = 0, piece = 0;
+    int it = 0, next_q = 0;
+    uint32_t q_par = 0, q_used = 0;  // bit b: parity of Q buffer b's next load; whether it had one
     uint32_t st = 0, ph = 0, loads = 0;  // next ring stage, its parity, tiles loaded
     // Segments' records are read 32 at a time, a lane each; table entries 32 at a time (kBatch units), a
     // batch ahead, and those of the next segment's first units while this one's are loaded: an entry
@@ -423,19 +433,27 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         next = record(seg + 1);
         next_batch = entries(next, 0);
       }
-      const int qb = piece & 1;
+      // a segment of two matrix tiles takes both Q buffers, another one the next
+      const bool two = g.rows > kTileRows;
+      const int qb = two ? 0 : next_q;
       if (is_k) {
-        if (lane == 0) ok = wait_or_flag(&s.q_empty[qb], ((piece >> 1) & 1) ^ 1u, p.status);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
+          const int buf = qb + t;
+          if (lane == 0) ok = wait_or_flag(&s.q_empty[buf], (q_par >> buf & 1) ^ 1u, p.status);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const int boxes = (min(kTileRows, g.rows - t * kTileRows) + kQBoxRows - 1) / kQBoxRows;
+          if (lane == 0) mbar_arrive_expect_tx(&s.q_full[buf], boxes * 2 * (2 * kQBoxRows * 128));
+          __syncwarp();
+          if (lane < 2 * boxes)
+            tc::tma_load_3d(s.q[buf][lane & 1] + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
+                            g.row + t * kTileRows + (lane >> 1) * kQBoxRows, &s.q_full[buf]);
+          q_par ^= 1u << buf;
+          q_used |= 1u << buf;
+        }
         if (!ok) break;
-        const int boxes = (g.rows + kQBoxRows - 1) / kQBoxRows;
-        if (lane == 0) mbar_arrive_expect_tx(&s.q_full[qb], boxes * 2 * (2 * kQBoxRows * 128));
-        __syncwarp();
-        if (lane < 2 * boxes)
-          tc::tma_load_3d(s.q[qb][lane & 1] + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
-                          g.row + (lane >> 1) * kQBoxRows, &s.q_full[qb]);
       }
-      ++piece;
+      next_q = qb ^ 1;
       const bool is_tile = seg < plan.tiles;
       for (int kb = k0; kb < k1 && ok; kb += kBatch) {
         const int ahead = kb + kBatch < k1 ? entries(g, kb + kBatch) : 0;
@@ -456,15 +474,16 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           // before that one.
           if (is_k && lane == 0) {
             UnitInfo& f = s.info[it % kInfos];
-            const int stream = it & 1;
             const int cap = is_tile ? 2 * p.tile_rows : 2;
             const int64_t slot =
-                ((static_cast<int64_t>(slice) + (is_tile ? seg : seg - plan.tiles)) * p.hkv + head) * 2 + stream;
+                ((static_cast<int64_t>(slice) + (is_tile ? seg : seg - plan.tiles)) * p.hkv + head) * 2;
             f.part = slot * cap * kRowFloats;
             f.stats = cap * kHeadDim;
             f.keys = keys;
-            f.flags = (k - k0 < 2 ? kFirst : 0) | (k1 - 1 - k < 2 ? kLast : 0) | (k == k0 ? kPieceStart : 0) |
-                      (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0);
+            const int streams = two ? 1 : 2;  // that take the piece's units in turn
+            f.flags = (k - k0 < streams ? kFirst : 0) | (k1 - 1 - k < streams ? kLast : 0) |
+                      (k == k0 ? kPieceStart : 0) | (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0) |
+                      (two ? kBoth : 0);
             f.rows = 2 * g.rows;
             f.is_tile = is_tile ? 1 : 0;
             mbar_arrive(&s.info_full[it % kInfos]);
@@ -489,7 +508,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     if (!ok && lane == 0) {
       for (uint32_t k = loads > stages ? loads - stages : 0; k < loads; ++k)
         wait_or_flag(&full[k % stages], (k / stages) & 1, p.status);
-      for (int k = max(0, piece - 2); is_k && k < piece; ++k) wait_or_flag(&s.q_full[k & 1], (k >> 1) & 1, p.status);
+      for (int b = 0; b < 2; ++b)
+        if (q_used >> b & 1) wait_or_flag(&s.q_full[b], (q_par >> b & 1) ^ 1u, p.status);
     }
     __syncwarp();
   } else if (warp == kScoreWarp) {
@@ -501,36 +521,45 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(s.q[0][0]), 16, 1024);
       const uint64_t dk = tc::smem_desc_sw128(smem_addr(s.k[0]), 16, kGroupBytes);
       bool ok = true;
-      uint32_t st = 0, ph = 0, q_uses[2] = {0, 0};
+      uint32_t st = 0, ph = 0;
+      // bits (an array indexed at run time would live in memory): of Q buffer b, the parity of its next
+      // load; of stream t, the parity of its next unit and whether it had one
+      uint32_t q_par = 0, par = 0, had = 0;
       for (int it = 0; it < nt; ++it) {
-        const int stream = it & 1;
-        // S takes the columns of the stream's last P
-        ok = (it < 2 || wait_or_flag(&s.p_free[stream], ((it >> 1) - 1) & 1, p.status)) &&
-             wait_or_flag(&s.k_full[st], ph, p.status);
+        ok = wait_or_flag(&s.k_full[st], ph, p.status);
         if (!ok) break;
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
-        const int qb = flags & kQBuffer1 ? 1 : 0;
-        if (flags & kPieceStart) {
-          ok = wait_or_flag(&s.q_full[qb], q_uses[qb] & 1, p.status);
-          ++q_uses[qb];
-          if (!ok) break;
-        }
-        tc::fence_after_sync();
+        const bool both = flags & kBoth;
         // N = the unit's keys in whole pages
         const uint32_t id = tc::idesc_bf16(128, 0, 0, 0) | static_cast<uint32_t>(pages * kPage >> 3) << 17;
-        const uint64_t a = dq + (qb * 2 * kQBlockBytes >> 4), b = dk + (st * kTileBytes >> 4);
+        const uint64_t b = dk + (st * kTileBytes >> 4);
+        for (int t = both ? 0 : it & 1, end = both ? 2 : t + 1; t < end && ok; ++t) {
+          const int qb = both ? t : (flags & kQBuffer1 ? 1 : 0);
+          // S takes the columns of the stream's last P
+          if (had >> t & 1) ok = wait_or_flag(&s.p_free[t], (par >> t & 1) ^ 1u, p.status);
+          had |= 1u << t;
+          par ^= 1u << t;
+          if (flags & kPieceStart) {
+            ok = ok && wait_or_flag(&s.q_full[qb], q_par >> qb & 1, p.status);
+            q_par ^= 1u << qb;
+          }
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t a = dq + (qb * 2 * kQBlockBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t step = (kk & 3) * 32;
-          const uint64_t ak = a + (((kk >> 2) * kQBlockBytes + step) >> 4);
-          const uint64_t bk = b + (((kk >> 2) * kHalfBytes + step) >> 4);
-          if (kk == 0) tc::mma_ss_c<false>(tmem + stream * kTileKeys, ak, bk, id);
-          else tc::mma_ss_c<true>(tmem + stream * kTileKeys, ak, bk, id);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t step = (kk & 3) * 32;
+            const uint64_t ak = a + (((kk >> 2) * kQBlockBytes + step) >> 4);
+            const uint64_t bk = b + (((kk >> 2) * kHalfBytes + step) >> 4);
+            if (kk == 0) tc::mma_ss_c<false>(tmem + t * kTileKeys, ak, bk, id);
+            else tc::mma_ss_c<true>(tmem + t * kTileKeys, ak, bk, id);
+          }
+          tc::mma_commit(&s.s_full[t]);
+          if (flags & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
         }
-        tc::mma_commit(&s.s_full[stream]);
+        if (!ok) break;
         tc::mma_commit(&s.k_empty[st]);
-        if (flags & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
         if (++st == kKStages) {
           st = 0;
           ph ^= 1u;
@@ -547,33 +576,41 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.v[0]), kHalfBytes, kGroupBytes);
       constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
       bool ok = true;
-      uint32_t st = 0, ph = 0, pieces[2] = {0, 0};
+      uint32_t st = 0, ph = 0;
+      // bits of stream t: the parity of its next unit; that of its next piece, and whether it had one
+      uint32_t par = 0, piece_par = 0, had = 0;
       for (int it = 0; it < nt; ++it) {
-        const int stream = it & 1;
-        // (P's barrier hands the info on too)
-        ok = wait_or_flag(&s.p_full[stream], (it >> 1) & 1, p.status) && wait_or_flag(&s.v_full[st], ph, p.status);
+        ok = wait_or_flag(&s.v_full[st], ph, p.status) &&
+             wait_or_flag(&s.info_full[it % kInfos], (it / kInfos) & 1, p.status);
         if (!ok) break;
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
-        if (flags & kFirst) {
-          if (pieces[stream] > 0) ok = wait_or_flag(&s.o_free[stream], (pieces[stream] - 1) & 1, p.status);
-          ++pieces[stream];
-          if (!ok) break;
-        }
-        tc::fence_after_sync();
-        const uint32_t o = tmem + 256 + stream * 128, a = tmem + stream * kTileKeys;
+        const bool both = flags & kBoth;
         const uint64_t b = dv + (st * kTileBytes >> 4);
-        tc::mma_ts(o, a, b, id, flags & kFirst ? 0u : 1u);
-        if (pages == kTilePages) {
+        for (int t = both ? 0 : it & 1, end = both ? 2 : t + 1; t < end && ok; ++t) {
+          ok = wait_or_flag(&s.p_full[t], par >> t & 1, p.status);
+          par ^= 1u << t;
+          if (flags & kFirst) {
+            if (had >> t & 1) ok = ok && wait_or_flag(&s.o_free[t], (piece_par >> t & 1) ^ 1u, p.status);
+            had |= 1u << t;
+            piece_par ^= 1u << t;
+          }
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t o = tmem + 256 + t * 128, a = tmem + t * kTileKeys;
+          tc::mma_ts(o, a, b, id, flags & kFirst ? 0u : 1u);
+          if (pages == kTilePages) {
 #pragma unroll
-          for (int kk = 1; kk < kTilePages; ++kk)
-            tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
-        } else {
-          for (int kk = 1; kk < pages; ++kk) tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
+            for (int kk = 1; kk < kTilePages; ++kk)
+              tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
+          } else {
+            for (int kk = 1; kk < pages; ++kk) tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
+          }
+          tc::mma_commit(&s.p_free[t]);
+          if (flags & kLast) tc::mma_commit(&s.o_ready[t]);
         }
-        tc::mma_commit(&s.p_free[stream]);
+        if (!ok) break;
         tc::mma_commit(&s.v_empty[st]);
-        if (flags & kLast) tc::mma_commit(&s.o_ready[stream]);
         if (++st == kVStages) {
           st = 0;
           ph ^= 1u;
@@ -595,15 +632,19 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     bool ok = true;
     uint32_t n = 0, pieces = 0;
     float m_used = -CUDART_INF_F, l = 0.f;
-    for (int it = stream; it < nt; it += 2, ++n) {
+    for (int it = 0; it < nt; ++it) {
       ok = warp_wait(&s.info_full[it % kInfos], (it / kInfos) & 1, lane, p.status);
       if (!ok) break;
       const volatile UnitInfo& f = s.info[it % kInfos];
-      const int keys = f.keys, flags = f.flags, rows = f.rows, stats = f.stats;
-      float* part = (f.is_tile ? p.tile_parts : p.row_parts) + f.part;
+      const int flags = f.flags;
+      if (!(flags & kBoth) && (it & 1) != stream) continue;
+      const int keys = f.keys, stats = f.stats;
+      const int rows = flags & kBoth ? min(f.rows - stream * 2 * kTileRows, 2 * kTileRows) : f.rows;
+      float* part = (f.is_tile ? p.tile_parts : p.row_parts) + f.part + stream * (stats / kHeadDim * kRowFloats);
       const bool used = quarter * 32 < rows;  // some of this warp's rows are query rows
       ok = warp_wait(&s.s_full[stream], n & 1, lane, p.status);
       if (!ok) break;
+      ++n;
       tc::fence_after_sync();
       if (flags & kFirst) {
         m_used = -CUDART_INF_F;
@@ -723,87 +764,139 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
 }
 
 // ---------------------------------------------------------------------------------------------
-// merge: a CTA per row, a warp per query head, four dims a lane
+// merge: a CTA per row and KV head. Its threads find the row's partial results and weigh them, then four
+// warps per query head add a quarter of them each, four dims a lane, eight results' loads in flight.
+// (A warp per query head alone, in a CTA per row, took 15 us for 8 rows of 38 results each.)
 // ---------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(512) shared_merge_kernel(const SharedParams p) {
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kMaxParts = 4 * kMaxSlices;  // two sets, two streams, every slice
+
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams p) {
+  __shared__ const float* where[kMaxParts];  // O of the row's first query head; the second's follows
+  __shared__ float weight[2][kMaxParts], part_l[2][kMaxParts];  // weight: m first
+  __shared__ float reduced[kMergeWarps][2];
+  __shared__ float4 sums[kMergeWarps][32];
+  const int b = static_cast<int>(blockIdx.x) / p.hkv, head = static_cast<int>(blockIdx.x) % p.hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   await_previous();
-  const int b = static_cast<int>(blockIdx.x), hq = threadIdx.x >> 5, lane = threadIdx.x & 31, head = hq >> 1;
-  const PlanHeader plan = *p.header;
+  const long long U = p.header->units, n = p.slices;
   const RowPlan row = p.rows[b];
-  const long long U = plan.units, n = p.slices;
-  float m = -CUDART_INF_F, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // slices [i0, i1] hold a set: slice i has units [U i / n, U (i + 1) / n)
+  int i0[2] = {0, 0}, count[2] = {0, 0};
 #pragma unroll
   for (int set = 0; set < 2; ++set) {
-    const int seg = set == 0 ? row.tile : row.own;
-    if (seg < 0) continue;
-    const int unit = p.segments[seg].unit, units = p.segments[seg].units;
+    const int unit = set == 0 ? row.tile_unit : row.own_unit, units = set == 0 ? row.tile_units : row.own_units;
+    if (units == 0) continue;
+    i0[set] = static_cast<int>(((unit + 1ll) * n - 1) / U);
+    count[set] = 2 * (static_cast<int>((static_cast<long long>(unit + units) * n - 1) / U) - i0[set] + 1);
+  }
+  const int total = count[0] + count[1];
+  float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+  for (int c = tid; c < total; c += kMergeThreads) {
+    const int set = c < count[0] ? 0 : 1, at = set == 0 ? c : c - count[0];
+    const int i = (set == 0 ? i0[0] : i0[1]) + (at >> 1), stream = at & 1;
+    const int unit = set == 0 ? row.tile_unit : row.own_unit, units = set == 0 ? row.tile_units : row.own_units;
     const int cap = set == 0 ? 2 * p.tile_rows : 2;
-    const int r = set == 0 ? 2 * row.in_tile + (hq & 1) : hq & 1;
-    const int index = set == 0 ? seg : seg - plan.tiles;
-    const float* base = set == 0 ? p.tile_parts : p.row_parts;
-    // slices [i0, i1] hold it: slice i has units [U i / n, U (i + 1) / n)
-    const int i0 = static_cast<int>(((unit + 1ll) * n - 1) / U);
-    const int i1 = static_cast<int>((static_cast<long long>(unit + units) * n - 1) / U);
-    for (int at = 2 * i0; at <= 2 * i1 + 1; at += 32) {
-      // lane's partial result: (slice, stream)
-      const int i = (at + lane) >> 1, stream = (at + lane) & 1;
-      float2 ml = make_float2(-CUDART_INF_F, 0.f);
-      const float* part = base + (((static_cast<int64_t>(i) + index) * p.hkv + head) * 2 + stream) * cap * kRowFloats;
-      if (at + lane <= 2 * i1 + 1) {
-        const int a = static_cast<int>(U * i / n), e = static_cast<int>(U * (i + 1) / n);
-        const int first = max(a, unit), last = min(e, unit + units);
-        // units alternate between the streams, from the slice's first
-        if (last - first >= 2 || (last - first == 1 && ((first - a) & 1) == stream))
-          ml = *reinterpret_cast<const float2*>(part + cap * kHeadDim + 2 * r);
-      }
-      float top = ml.x;
+    const int first = static_cast<int>(U * i / n), end = static_cast<int>(U * (i + 1) / n);
+    const int u0 = max(first, unit), u1 = min(end, unit + units);
+    int r = 0;
+    bool there;
+    if (set == 0 && (row.in_tile & kTwoTiles)) {  // a stream per tile
+      const int in_tile = row.in_tile & (kTwoTiles - 1);
+      there = u1 > u0 && stream == in_tile / kTileRows;
+      r = 2 * (in_tile % kTileRows);
+    } else {  // units alternate between the streams, from the slice's first
+      there = u1 - u0 >= 2 || (u1 - u0 == 1 && ((u0 - first) & 1) == stream);
+      if (set == 0) r = 2 * row.in_tile;
+    }
+    const float* part = (set == 0 ? p.tile_parts : p.row_parts) +
+                        (((static_cast<int64_t>(i) + (set == 0 ? row.tile : row.own)) * p.hkv + head) * 2 + stream) * cap * kRowFloats;
+    float4 ml = make_float4(-CUDART_INF_F, 0.f, -CUDART_INF_F, 0.f);  // (m, l) of both query heads
+    if (there) ml = *reinterpret_cast<const float4*>(part + cap * kHeadDim + 2 * r);
+    where[c] = there ? part + r * kHeadDim : nullptr;
+    weight[0][c] = ml.x;
+    weight[1][c] = ml.z;
+    part_l[0][c] = ml.y;
+    part_l[1][c] = ml.w;
+    top[0] = fmaxf(top[0], ml.x);
+    top[1] = fmaxf(top[1], ml.z);
+  }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float m_new = fmaxf(m, top);
-      if (m_new == -CUDART_INF_F) continue;
-      const float keep = m == -CUDART_INF_F ? 0.f : fast_exp2(m - m_new);
-      const float w = ml.x == -CUDART_INF_F ? 0.f : fast_exp2(ml.x - m_new);
-      m = m_new;
-      float sum = w * ml.y;
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l = l * keep + sum;
-      acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
-      const uint32_t some = __ballot_sync(0xffffffffu, ml.x != -CUDART_INF_F);
-      // eight results' loads in flight
-      for (uint32_t left = some; left != 0;) {
-        float wk[8];
-        float4 v[8];
+    for (int o = 16; o > 0; o >>= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+    if (lane == 0) reduced[warp][h] = top[h];
+  }
+  __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int k = left != 0 ? __ffs(left) - 1 : 0;
-          wk[j] = __shfl_sync(0xffffffffu, w, k);
-          if (left == 0) wk[j] = 0.f;
-          const float* pk = reinterpret_cast<const float*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), k));
-          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (left != 0) v[j] = reinterpret_cast<const float4*>(pk + r * kHeadDim)[lane];
-          left &= left - 1;
-        }
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          acc.x += wk[j] * v[j].x;
-          acc.y += wk[j] * v[j].y;
-          acc.z += wk[j] * v[j].z;
-          acc.w += wk[j] * v[j].w;
-        }
-      }
+    for (int w = 0; w < kMergeWarps; ++w) top[h] = fmaxf(top[h], reduced[w][h]);
+  __syncthreads();
+  float sum[2] = {0.f, 0.f};
+  for (int c = tid; c < total; c += kMergeThreads) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float m = weight[h][c], w = m == -CUDART_INF_F ? 0.f : fast_exp2(m - top[h]);
+      weight[h][c] = w;
+      sum[h] += w * part_l[h][c];
     }
   }
-  const float inv = m == -CUDART_INF_F ? 0.f : 1.0f / l;
-  uint2 w = make_uint2(0u, 0u);
-  if (m != -CUDART_INF_F) {
-    w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-    w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], o);
+    if (lane == 0) reduced[warp][h] = sum[h];
   }
-  const int64_t at = static_cast<int64_t>(b) * p.hq + hq;
-  reinterpret_cast<uint2*>(p.out + at * kHeadDim)[lane] = w;
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    sum[h] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) sum[h] += reduced[w][h];
+  }
+  const int h = warp & 1;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kStride = kMergeWarps / 2;
+  for (int c0 = warp >> 1; c0 < total; c0 += 8 * kStride) {
+    float w[8];
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + j * kStride;
+      w[j] = c < total ? weight[h][c] : 0.f;
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < total && where[c] != nullptr) v[j] = reinterpret_cast<const float4*>(where[c] + h * kHeadDim)[lane];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      acc.x += w[j] * v[j].x;
+      acc.y += w[j] * v[j].y;
+      acc.z += w[j] * v[j].z;
+      acc.w += w[j] * v[j].w;
+    }
+  }
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp >= 2) return;
+#pragma unroll
+  for (int w = 1; w < kStride; ++w) {
+    const float4 v = sums[2 * w + h][lane];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  const float m = h == 0 ? top[0] : top[1], l = h == 0 ? sum[0] : sum[1];
+  const float inv = 1.0f / l;
+  uint2 out = make_uint2(0u, 0u);
+  if (m != -CUDART_INF_F) {
+    out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  }
+  const int64_t at = static_cast<int64_t>(b) * p.hq + 2 * head + h;
+  reinterpret_cast<uint2*>(p.out + at * kHeadDim)[lane] = out;
   if (lane == 0 && p.lse != nullptr) p.lse[at] = m == -CUDART_INF_F ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
@@ -822,8 +915,8 @@ bool shared_layout(SharedLayout& l, int hkv, int batch, int groups, int max_grou
   if (sms <= 0) return false;
   l.slices = std::min(kMaxSlices, std::max(1, sms / hkv));
   l.tile_rows = std::max(1, std::min({kTileRows, max_group_rows, batch}));
-  // a group's segments: one, and one more for every kTileRows rows
-  const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kTileRows : 0;
+  // a group's segments: one, and one more for every kSegmentRows rows
+  const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kSegmentRows : 0;
   l.header = 0;
   l.slice_segment = 256;
   l.segments = align256(l.slice_segment + sizeof(int32_t) * l.slices);
@@ -947,6 +1040,6 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
     e = launch_dependent(shared_attention_kernel, static_cast<unsigned>(l.slices * hkv), kThreads, sizeof(SharedSmem),
                          st, 0, qm, km, vm, p);
   if (e == cudaSuccess)
-    e = launch_dependent(shared_merge_kernel, static_cast<unsigned>(batch), 32u * static_cast<unsigned>(p.hq), 0, st, 0, p);
+    e = launch_dependent(shared_merge_kernel, static_cast<unsigned>(batch * hkv), kMergeThreads, 0, st, 0, p);
   return e == cudaSuccess ? PA_OK : record_cuda_error(e, "attn_decode_paged_shared");
 }
