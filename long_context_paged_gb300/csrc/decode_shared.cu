@@ -41,6 +41,8 @@ namespace {
 
 constexpr int kTileRows = 64;     // rows of a matrix tile (x 2 query heads = 128)
 constexpr int kSegmentRows = 2 * kTileRows;  // rows of a group per segment
+constexpr int kFewRows = 8;       // a segment of so many rows is computed with its keys as the matrix's rows
+constexpr int kFew = 2 * kFewRows;
 constexpr int kTileKeys = 128;    // keys of a unit
 constexpr int kTilePages = kTileKeys / kPage;
 constexpr int kKStages = 2;       // K tiles in flight, each released once its scores are there
@@ -57,6 +59,10 @@ constexpr uint32_t kQBlockBytes = 128 * 128;
 constexpr uint32_t kPageBytes = kPage * 256;       // a page's 16 keys of one head: two groups of 8 keys, each
 constexpr uint32_t kGroupBytes = 8 * 256;          // of them 1 KB of the first 64 dims and 1 KB of the others
 constexpr uint32_t kHalfBytes = 8 * 128;
+// Weights of few rows (bf16 [2 halves of the keys][kFew rows][64 keys]): of stream t in Q buffer t, behind the
+// rows that such a segment has there. Segments of many rows fill the buffer, and come before.
+constexpr uint32_t kWeightsAt = 64 * 128;
+constexpr uint32_t kFewHalfBytes = kFew * 128;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroups = 4096;
@@ -122,7 +128,8 @@ struct PlanSmem {
   int32_t cu[kMaxGroups + 1];
   int32_t shared[kMaxGroups];     // shared pages
   int32_t first[kMaxGroups];      // first row that uses them
-  int32_t tile0[kMaxGroups];      // first segment
+  int32_t tile0[kMaxGroups];      // first segment of many rows
+  int32_t few0[kMaxGroups];       // the last segment, if it has few
   int32_t unit[kMaxSegments + 1]; // first unit of each segment
 };
 
@@ -215,25 +222,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   // segments of shared pages
   const int gper = (G + threads - 1) / threads;
   const int g0 = min(G, tid * gper), g1 = min(G, g0 + gper);
+  // (those of many rows come first: a CTA never goes back to them from those of few)
+  auto rows_of = [&](int g) { return grouped && s.first[g] != 0x7fffffff ? s.cu[g + 1] - s.cu[g] : 0; };
+  auto few_of = [&](int rows) { return rows % kSegmentRows <= kFewRows ? rows % kSegmentRows : 0; };
   long long mine = 0, total = 0;
-  for (int g = g0; g < g1; ++g)
-    if (grouped && s.first[g] != 0x7fffffff) {
-      const long long tiles = (s.cu[g + 1] - s.cu[g] + kSegmentRows - 1) / kSegmentRows;
-      mine += tiles << 40 | tiles * units_of(s.shared[g] * kPage);
+  int tiles = 0, tile_units = 0;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    mine = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int rows = rows_of(g), few = few_of(rows);
+      const long long n = pass == 0 ? (rows - few + kSegmentRows - 1) / kSegmentRows : few > 0;
+      mine += n << 40 | n * units_of(s.shared[g] * kPage);
     }
-  long long at = plan_scan(s, mine, total);
-  const int tiles = static_cast<int>(total >> 40), tile_units = static_cast<int>(total & ((1ll << 40) - 1));
-  for (int g = g0; g < g1; ++g) {
-    if (!grouped || s.first[g] == 0x7fffffff) continue;
-    int seg = static_cast<int>(at >> 40), unit = static_cast<int>(at & ((1ll << 40) - 1));
-    const int units = units_of(s.shared[g] * kPage);
-    s.tile0[g] = seg;
-    for (int r = s.cu[g]; r < s.cu[g + 1]; r += kSegmentRows) {
-      p.segments[seg] = Segment{unit, units, r, min(kSegmentRows, s.cu[g + 1] - r), s.first[g], 0, s.shared[g] * kPage, 0};
-      s.unit[seg++] = unit;
-      unit += units;
+    const long long at = plan_scan(s, mine, total);
+    int seg = tiles + static_cast<int>(at >> 40), unit = tile_units + static_cast<int>(at & ((1ll << 40) - 1));
+    for (int g = g0; g < g1; ++g) {
+      const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
+      const int begin = pass == 0 ? 0 : rows - few, end = pass == 0 ? rows - few : rows;
+      if (pass == 0) s.tile0[g] = seg; else s.few0[g] = seg;
+      for (int r = begin; r < end; r += kSegmentRows) {
+        p.segments[seg] = Segment{unit, units, s.cu[g] + r, min(kSegmentRows, end - r), s.first[g], 0, s.shared[g] * kPage, 0};
+        s.unit[seg++] = unit;
+        unit += units;
+      }
     }
-    at = static_cast<long long>(seg) << 40 | unit;
+    tiles += static_cast<int>(total >> 40);
+    tile_units += static_cast<int>(total & ((1ll << 40) - 1));
   }
   // segments of the rows' own pages
   mine = 0;
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     const int units = units_of(len[k] - first);
     if (units > 0) mine += 1ll << 40 | units;
   }
-  at = plan_scan(s, mine, total);  // (its barriers also order s.tile0)
+  const long long at = plan_scan(s, mine, total);  // (its barriers also order s.tile0)
   const int segments = tiles + static_cast<int>(total >> 40);
   const int units_all = tile_units + static_cast<int>(total & ((1ll << 40) - 1));
   int seg = tiles + static_cast<int>(at >> 40), unit = tile_units + static_cast<int>(at & ((1ll << 40) - 1));
@@ -255,12 +270,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     const int units = units_of(len[k] - first);
     RowPlan r{0, 0, 0, 0, 0, 0, 0, 0};
     if (g >= 0) {
-      const int in_group = b - s.cu[g];
-      r.tile = s.tile0[g] + in_group / kSegmentRows;
+      const int in_group = b - s.cu[g], rows = rows_of(g), few = few_of(rows), place = in_group / kSegmentRows;
+      r.tile = in_group < rows - few ? s.tile0[g] + place : s.few0[g];
       r.tile_units = units_of(first);
       r.tile_unit = s.unit[r.tile];
-      const bool two = s.cu[g + 1] - s.cu[g] - in_group / kSegmentRows * kSegmentRows > kTileRows;
-      r.in_tile = in_group % kSegmentRows | (two ? kTwoTiles : 0);
+      r.in_tile = in_group % kSegmentRows | (rows - place * kSegmentRows > kTileRows ? kTwoTiles : 0);
     }
     if (units > 0) {
       r.own = seg - tiles;
@@ -295,6 +309,7 @@ constexpr int kFirst = 1, kLast = 2;          // of this stream in the piece
 constexpr int kPieceStart = 4, kPieceEnd = 8; // of the piece
 constexpr int kQBuffer1 = 16;                 // else buffer 0
 constexpr int kBoth = 32;                     // both streams take the unit, each a tile of its own
+constexpr int kFewFlag = 64;                  // few rows: keys are the matrix's rows
 
 struct UnitInfo {
   int64_t part;     // where stream 0's partial result goes, in floats; row r's O at + 128 r
@@ -314,8 +329,9 @@ struct SharedSmem {
   uint64_t q_full[2], q_empty[2];
   uint64_t info_full[kInfos];
   uint64_t s_full[2], p_full[2], p_free[2], o_ready[2], o_free[2];
-  uint64_t mma_done[2];
+  uint64_t mma_done[2], met[2];
   uint32_t tmem_base;
+  float exchange[2][3][4][kFew];  // of each stream: maxima (two, in turn) and sums, per warp and row
   UnitInfo info[kInfos];
 };
 static_assert(sizeof(SharedSmem) <= 232448, "shared memory over the 227 KB limit");
@@ -331,7 +347,9 @@ __device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, int
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, int32_t* status) {
   bool ok = true;
   if (lane == 0) ok = wait_or_flag(bar, parity, status);
-  return __shfl_sync(0xffffffffu, ok, 0);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();  // (what the wait of one lane made visible is visible to the others)
+  return ok;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -368,6 +386,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       mbar_init(&s.p_full[i], 4);
       mbar_init(&s.p_free[i], 1);
       mbar_init(&s.mma_done[i], 1);
+      mbar_init(&s.met[i], 4);
       mbar_init(&s.o_ready[i], 1);
       mbar_init(&s.o_free[i], 4);
     }
@@ -483,7 +502,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
             const int streams = two ? 1 : 2;  // that take the piece's units in turn
             f.flags = (k - k0 < streams ? kFirst : 0) | (k1 - 1 - k < streams ? kLast : 0) |
                       (k == k0 ? kPieceStart : 0) | (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0) |
-                      (two ? kBoth : 0);
+                      (two ? kBoth : 0) | (g.rows <= kFewRows ? kFewFlag : 0);
             f.rows = 2 * g.rows;
             f.is_tile = is_tile ? 1 : 0;
             mbar_arrive(&s.info_full[it % kInfos]);
@@ -547,6 +566,17 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t a = dq + (qb * 2 * kQBlockBytes >> 4);
+          if (flags & kFewFlag) {  // S^T = K Q^T, of all the tile's rows: those past the unit's keys are not used
+            constexpr uint32_t few = tc::idesc_bf16(128, kFew, 0, 0);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t step = (kk & 3) * 32;
+              const uint64_t ak = a + (((kk >> 2) * kQBlockBytes + step) >> 4);
+              const uint64_t bk = b + (((kk >> 2) * kHalfBytes + step) >> 4);
+              if (kk == 0) tc::mma_ss_c<false>(tmem + t * kTileKeys, bk, ak, few);
+              else tc::mma_ss_c<true>(tmem + t * kTileKeys, bk, ak, few);
+            }
+          } else
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t step = (kk & 3) * 32;
@@ -574,6 +604,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // ------------------------------------------------------------------ O += P V
     if (lane == 0) {
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.v[0]), kHalfBytes, kGroupBytes);
+      const uint64_t dp = tc::smem_desc_sw128(smem_addr(s.q[0][0]) + kWeightsAt, 16, 1024);
       constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
       bool ok = true;
       uint32_t st = 0, ph = 0;
@@ -598,8 +629,13 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t o = tmem + 256 + t * 128, a = tmem + t * kTileKeys;
-          tc::mma_ts(o, a, b, id, flags & kFirst ? 0u : 1u);
-          if (pages == kTilePages) {
+          if (flags & kFewFlag) {  // O^T += V^T P^T
+            constexpr uint32_t few = tc::idesc_bf16(128, kFew, 1, 0);
+            const uint64_t w = dp + (t * 2 * kQBlockBytes >> 4);
+            for (int kk = 0; kk < pages; ++kk)
+              tc::mma_ss(o, b + kk * (kPageBytes >> 4), w + (((kk >> 2) * kFewHalfBytes + (kk & 3) * 32) >> 4), few,
+                         kk > 0 || !(flags & kFirst) ? 1u : 0u);
+          } else if (tc::mma_ts(o, a, b, id, flags & kFirst ? 0u : 1u); pages == kTilePages) {
 #pragma unroll
             for (int kk = 1; kk < kTilePages; ++kk)
               tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
@@ -622,135 +658,269 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     __syncwarp();
   }
   } else {
-    // ------------------------------------------------------------------ softmax
+    // ------------------------------------------------------------------ softmax warps
     tc::regs_increase<kSoftmaxRegs>();
     const int stream = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_bits + stream * kTileKeys, t_o = tmem + lane_bits + 256 + stream * 128;
-    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
-    uint32_t n = 0, pieces = 0;
-    float m_used = -CUDART_INF_F, l = 0.f;
-    for (int it = 0; it < nt; ++it) {
-      ok = warp_wait(&s.info_full[it % kInfos], (it / kInfos) & 1, lane, p.status);
-      if (!ok) break;
-      const volatile UnitInfo& f = s.info[it % kInfos];
-      const int flags = f.flags;
-      if (!(flags & kBoth) && (it & 1) != stream) continue;
-      const int keys = f.keys, stats = f.stats;
-      const int rows = flags & kBoth ? min(f.rows - stream * 2 * kTileRows, 2 * kTileRows) : f.rows;
-      float* part = (f.is_tile ? p.tile_parts : p.row_parts) + f.part + stream * (stats / kHeadDim * kRowFloats);
-      const bool used = quarter * 32 < rows;  // some of this warp's rows are query rows
-      ok = warp_wait(&s.s_full[stream], n & 1, lane, p.status);
-      if (!ok) break;
-      ++n;
-      tc::fence_after_sync();
-      if (flags & kFirst) {
-        m_used = -CUDART_INF_F;
-        l = 0.f;
+    int it = 0;
+    uint32_t n = 0, pieces = 0;  // units and pieces of this stream so far
+    // The next unit's flags; -1 after the last or a wait that gave up. Units of the other stream are passed
+    // over (their slots cannot have been used again: that takes this stream's own units done).
+    auto next_flags = [&](int& flags) {
+      for (; it < nt; ++it) {
+        ok = warp_wait(&s.info_full[it % kInfos], (it / kInfos) & 1, lane, p.status);
+        if (!ok) return false;
+        const volatile UnitInfo& f = s.info[it % kInfos];
+        flags = f.flags;
+        if ((flags & kBoth) || (it & 1) == stream) return true;
       }
-      if (used) {
-        uint32_t sb[kTileKeys];
-        float cm[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
-        tc::tmem_wait_ld();
-        float mx = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
-        if (keys < kTileKeys) {  // keys past the segment's end (their scores are whatever TMEM held)
-          mx = -CUDART_INF_F;
-#pragma unroll
-          for (int c = 0; c < kTileKeys; ++c) {
-            if (c >= keys) sb[c] = 0xff800000u;
-            mx = fmaxf(mx, __uint_as_float(sb[c]));
-          }
+      return false;
+    };
+    // Slots of the unit's last page after its last key may hold anything, NaN too: their V rows meet
+    // weights of 0 as zeros.
+    auto clear_tail = [&](int keys) {
+      const uint32_t vst = static_cast<uint32_t>(it) % kVStages;
+      ok = warp_wait(&s.v_full[vst], (static_cast<uint32_t>(it) / kVStages) & 1, lane, p.status);
+      if (!ok) return;
+      const int end = (keys + kPage - 1) / kPage * kPage;
+      for (int e = keys * 16 + r; e < end * 16; e += 128)  // 16 bytes of a key
+        *reinterpret_cast<uint4*>(s.v[vst] + (e >> 7) * kGroupBytes + ((e >> 3) & 1) * kHalfBytes + ((e >> 4) & 7) * 128 +
+                                  (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+      tc::fence_proxy_async_smem();
+    };
+    auto hand_over = [&](uint64_t* bar) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    int flags;
+    bool more = next_flags(flags);
+
+    // ------------------------------------------------------------------ softmax, a thread per row
+    {
+      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+      float m_used = -CUDART_INF_F, l = 0.f;
+      for (; more && !(flags & kFewFlag); ++it, more = next_flags(flags)) {
+        const volatile UnitInfo& f = s.info[it % kInfos];
+        const int keys = f.keys, stats = f.stats;
+        const int rows = flags & kBoth ? min(f.rows - stream * 2 * kTileRows, 2 * kTileRows) : f.rows;
+        float* part = p.tile_parts + f.part + stream * (stats / kHeadDim * kRowFloats);
+        const bool used = quarter * 32 < rows;  // some of this warp's rows are query rows
+        ok = warp_wait(&s.s_full[stream], n & 1, lane, p.status);
+        if (!ok) break;
+        ++n;
+        tc::fence_after_sync();
+        if (flags & kFirst) {
+          m_used = -CUDART_INF_F;
+          l = 0.f;
         }
-        const float mx2 = mx * p.scale_log2;
+        if (used) {
+          uint32_t sb[kTileKeys];
+          float cm[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            tc::tmem_ld32_max(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sb + c * 32), cm[c]);
+          tc::tmem_wait_ld();
+          float mx = fmax3(cm[0], cm[1], fmaxf(cm[2], cm[3]));
+          if (keys < kTileKeys) {  // keys past the segment's end (their scores are whatever TMEM held)
+            mx = -CUDART_INF_F;
+#pragma unroll
+            for (int c = 0; c < kTileKeys; ++c) {
+              if (c >= keys) sb[c] = 0xff800000u;
+              mx = fmaxf(mx, __uint_as_float(sb[c]));
+            }
+          }
+          const float mx2 = mx * p.scale_log2;
+          const bool grow = mx2 > m_used + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m_new = grow ? mx2 : m_used;
+            const float alpha = m_used == -CUDART_INF_F ? 0.f : fast_exp2(m_used - m_new);
+            if (!(flags & kFirst)) {
+              // O holds the stream's sum through its last unit: this unit's S was issued after that
+              // product had completed
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o32[32];
+                tc::tmem_ld32(t_o + c * 32, o32);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o32[k] = __float_as_uint(__uint_as_float(o32[k]) * alpha);
+                tc::tmem_st32(t_o + c * 32, o32);
+              }
+            }
+            l *= alpha;
+            m_used = m_new;
+          }
+          // the weights go to bf16 for the product (their sum is of the unrounded ones): off by 2^-8 of
+          // each at most, which averages out over the keys; V's own precision is no better
+          const float m_eff = m_used == -CUDART_INF_F ? 0.f : m_used;
+          const float2 nm2 = make_float2(-m_eff, -m_eff);
+          float2 ls[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float2 x = fma2(make_float2(__uint_as_float(sb[c * 64 + 2 * k]),
+                                                __uint_as_float(sb[c * 64 + 2 * k + 1])), sc2, nm2);
+              const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              ls[k & 3] = add2(ls[k & 3], e);
+              pk[k] = pack_bf16x2(e.x, e.y);
+            }
+            tc::tmem_st32(t_s + c * 32, pk);
+          }
+          const float2 sum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+          l += sum.x + sum.y;
+          tc::tmem_wait_st();
+        }
+        if (keys % kPage != 0) clear_tail(keys);
+        if (!ok) break;
+        hand_over(&s.p_full[stream]);
+        if (flags & kLast) {
+          ok = warp_wait(&s.o_ready[stream], pieces & 1, lane, p.status);
+          if (!ok) break;
+          ++pieces;
+          tc::fence_after_sync();
+          if (used) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tc::tmem_ld32(t_o + c * 32, o);
+              tc::tmem_wait_ld();
+              if (r < rows) {
+                float4* dst = reinterpret_cast<float4*>(part + r * kHeadDim + c * 32);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                       __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+              }
+            }
+            // (a NaN among the scores: any finite maximum hands the NaN on)
+            if (r < rows) *reinterpret_cast<float2*>(part + stats + 2 * r) = make_float2(l == l ? m_used : 0.f, l);
+          }
+          hand_over(&s.o_free[stream]);
+        }
+      }
+    }
+
+    // ------------------------------------------------------------------ softmax, a thread per key
+    // Lane c of every warp keeps row c's maximum; a row's maximum over the keys takes a reduction in each
+    // warp and a meeting of the four, its sum is left in the threads until the piece's end.
+    if (ok) {
+      float m_used = -CUDART_INF_F;
+      float l[kFew];  // this thread's keys' part of each row's sum
+      uint32_t meetings = 0;
+      // all[w][c]: value of lane c of warp w
+      auto meet = [&](float (*all)[kFew], float value) {
+        if (lane < kFew) all[quarter][lane] = value;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.met[stream]);
+        ok = warp_wait(&s.met[stream], meetings & 1, lane, p.status);
+        ++meetings;
+      };
+      for (; more && ok; ++it, more = ok && next_flags(flags)) {
+        const volatile UnitInfo& f = s.info[it % kInfos];
+        const int keys = f.keys, rows = f.rows, stats = f.stats;
+        float* part = (f.is_tile ? p.tile_parts : p.row_parts) + f.part + stream * (stats / kHeadDim * kRowFloats);
+        ok = warp_wait(&s.s_full[stream], n & 1, lane, p.status);
+        if (!ok) break;
+        ++n;
+        tc::fence_after_sync();
+        if (flags & kFirst) {
+          m_used = -CUDART_INF_F;
+#pragma unroll
+          for (int c = 0; c < kFew; ++c) l[c] = 0.f;
+        }
+        uint32_t sb[kFew];
+        tc::tmem_ld16(t_s, sb);
+        tc::tmem_wait_ld();
+        const bool seen = r < keys;
+        int best = 0;  // lane c: the warp's largest score of row c, as an integer of the same order
+#pragma unroll
+        for (int c = 0; c < kFew; ++c) {
+          if (c >= rows) break;
+          const float x = __uint_as_float(sb[c]);
+          int o = __float_as_int(seen && x == x ? x : -CUDART_INF_F);
+          o ^= (o >> 31) & 0x7fffffff;
+          o = __reduce_max_sync(0xffffffffu, o);
+          if (lane == c) best = o;
+        }
+        best ^= (best >> 31) & 0x7fffffff;
+        float (*all)[kFew] = s.exchange[stream][n & 1];
+        meet(all, __int_as_float(best));
+        if (!ok) break;
+        float mx2 = -CUDART_INF_F;
+        if (lane < rows)
+          mx2 = fmax3(all[0][lane], all[1][lane], fmaxf(all[2][lane], all[3][lane])) * p.scale_log2;
         const bool grow = mx2 > m_used + kRescaleThreshold;
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? mx2 : m_used;
           const float alpha = m_used == -CUDART_INF_F ? 0.f : fast_exp2(m_used - m_new);
-          if (!(flags & kFirst)) {
-            // O holds the stream's sum through its last unit: this unit's S was issued after that
-            // product had completed
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o32[32];
-              tc::tmem_ld32(t_o + c * 32, o32);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o32[k] = __float_as_uint(__uint_as_float(o32[k]) * alpha);
-              tc::tmem_st32(t_o + c * 32, o32);
-            }
-          }
-          l *= alpha;
           m_used = m_new;
-        }
-        // the weights go to bf16 for the product (their sum is of the unrounded ones): off by 2^-8 of
-        // each at most, which averages out over the keys; V's own precision is no better
-        const float m_eff = m_used == -CUDART_INF_F ? 0.f : m_used;
-        const float2 nm2 = make_float2(-m_eff, -m_eff);
-        float2 ls[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float2 x = fma2(make_float2(__uint_as_float(sb[c * 64 + 2 * k]),
-                                              __uint_as_float(sb[c * 64 + 2 * k + 1])), sc2, nm2);
-            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            ls[k & 3] = add2(ls[k & 3], e);
-            pk[k] = pack_bf16x2(e.x, e.y);
-          }
-          tc::tmem_st32(t_s + c * 32, pk);
-        }
-        const float2 sum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
-        l += sum.x + sum.y;
-        tc::tmem_wait_st();
-      }
-      if (keys % kPage != 0) {
-        // slots of the last page after the last key may hold anything, NaN too: their V rows meet
-        // weights of 0 as zeros
-        const uint32_t vst = static_cast<uint32_t>(it) % kVStages;
-        ok = warp_wait(&s.v_full[vst], (static_cast<uint32_t>(it) / kVStages) & 1, lane, p.status);
-        if (!ok) break;
-        const int end = (keys + kPage - 1) / kPage * kPage;
-        for (int e = keys * 16 + r; e < end * 16; e += 128)  // 16 bytes of a key
-          *reinterpret_cast<uint4*>(s.v[vst] + (e >> 7) * kGroupBytes + ((e >> 3) & 1) * kHalfBytes + ((e >> 4) & 7) * 128 +
-                                    (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-        tc::fence_proxy_async_smem();
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.p_full[stream]);
-      if (flags & kLast) {
-        ok = warp_wait(&s.o_ready[stream], pieces & 1, lane, p.status);
-        if (!ok) break;
-        ++pieces;
-        tc::fence_after_sync();
-        if (used) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tc::tmem_ld32(t_o + c * 32, o);
+          if (!(flags & kFirst)) {
+            uint32_t o[kFew];
+            tc::tmem_ld16(t_o, o);
             tc::tmem_wait_ld();
-            if (r < rows) {
-              float4* dst = reinterpret_cast<float4*>(part + r * kHeadDim + c * 32);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            for (int c = 0; c < kFew; ++c) {
+              const float a = __shfl_sync(0xffffffffu, alpha, c);
+              l[c] *= a;
+              o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
             }
+            tc::tmem_st16(t_o, o);
+            tc::tmem_wait_st();
           }
-          // (a NaN among the scores: any finite maximum hands the NaN on)
-          if (r < rows) *reinterpret_cast<float2*>(part + stats + 2 * r) = make_float2(l == l ? m_used : 0.f, l);
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.o_free[stream]);
+        const float m_eff = m_used == -CUDART_INF_F ? 0.f : m_used;
+        uint8_t* w = s.q[stream][0] + kWeightsAt + (r >> 6) * kFewHalfBytes + (r & 7) * 2;
+#pragma unroll
+        for (int c = 0; c < kFew; ++c) {
+          if (c >= rows) break;
+          const float m = __shfl_sync(0xffffffffu, m_eff, c);
+          const float e = seen ? fast_exp2(fmaf(__uint_as_float(sb[c]), p.scale_log2, -m)) : 0.f;
+          l[c] += e;
+          *reinterpret_cast<uint16_t*>(w + c * 128 + ((((r >> 3) & 7) ^ (c & 7)) << 4)) =
+              static_cast<uint16_t>(pack_bf16x2(e, 0.f));
+        }
+        tc::fence_proxy_async_smem();
+        if (keys % kPage != 0) clear_tail(keys);
+        if (!ok) break;
+        hand_over(&s.p_full[stream]);
+        if (flags & kLast) {
+          // lane c: the warp's sum of row c, then all four warps'
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < kFew; ++c) {
+            if (c >= rows) break;
+            float x = l[c];
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+            if (lane == c) sum = x;
+          }
+          all = s.exchange[stream][2];
+          meet(all, sum);
+          if (!ok) break;
+          ok = warp_wait(&s.o_ready[stream], pieces & 1, lane, p.status);
+          if (!ok) break;
+          ++pieces;
+          tc::fence_after_sync();
+          uint32_t o[kFew];
+          tc::tmem_ld16(t_o, o);
+          tc::tmem_wait_ld();
+          hand_over(&s.o_free[stream]);
+#pragma unroll
+          for (int c = 0; c < kFew; ++c)
+            if (c < rows) part[c * kHeadDim + r] = __uint_as_float(o[c]);
+          if (quarter == 0 && lane < rows) {
+            const float all_l = (all[0][lane] + all[1][lane]) + (all[2][lane] + all[3][lane]);
+            *reinterpret_cast<float2*>(part + stats + 2 * lane) = make_float2(all_l == all_l ? m_used : 0.f, all_l);
+          }
+        }
       }
     }
   }
