@@ -39,14 +39,12 @@ bool make_map_heads(CUtensorMap* map, const void* base, uint64_t outer, uint64_t
 
 namespace {
 
-constexpr int kTileRows = 64;     // rows of a matrix tile (x 2 query heads = 128)
-constexpr int kSegmentRows = 2 * kTileRows;  // rows of a group per segment
+constexpr int kTileRows = 64;     // rows of a group per segment (x 2 query heads = 128)
 constexpr int kFewRows = 8;       // a segment of so many rows is computed with its keys as the matrix's rows
 constexpr int kFew = 2 * kFewRows;
 constexpr int kTileKeys = 128;    // keys of a unit
 constexpr int kTilePages = kTileKeys / kPage;
-constexpr int kKStages = 2;       // K tiles in flight, each released once its scores are there
-constexpr int kVStages = 3;       // V tiles in flight: needed a softmax later
+constexpr int kStages = 3;        // K and V tiles in flight, of each
 constexpr int kThreads = 384;     // 8 softmax warps, two producers, two MMA issuers
 constexpr int kKProducerWarp = 8;  // units, Q and K
 constexpr int kVProducerWarp = 11;
@@ -59,14 +57,17 @@ constexpr uint32_t kQBlockBytes = 128 * 128;
 constexpr uint32_t kPageBytes = kPage * 256;       // a page's 16 keys of one head: two groups of 8 keys, each
 constexpr uint32_t kGroupBytes = 8 * 256;          // of them 1 KB of the first 64 dims and 1 KB of the others
 constexpr uint32_t kHalfBytes = 8 * 128;
-// Weights of few rows (bf16 [2 halves of the keys][kFew rows][64 keys]): of stream t in Q buffer t, behind the
-// rows that such a segment has there. Segments of many rows fill the buffer, and come before.
-constexpr uint32_t kWeightsAt = 64 * 128;
+// The Q buffer: a segment of many rows has all of it. Those of few rows, which come after all of those,
+// have two small Q buffers in turn and, for each stream, their weights in it (bf16 [2 halves of the keys]
+// [kFew rows][64 keys]).
 constexpr uint32_t kFewHalfBytes = kFew * 128;
+constexpr uint32_t kFewQBytes = 2 * kFewHalfBytes;
+constexpr uint32_t kWeightsAt = 2 * kFewQBytes;
+static_assert(kWeightsAt + 2 * kFewQBytes <= 2 * kQBlockBytes, "the small buffers fit in the large one");
 constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroups = 4096;
-constexpr int kMaxSegments = kMaxBatch + kMaxGroups + kMaxBatch / kSegmentRows;
+constexpr int kMaxSegments = kMaxBatch + kMaxGroups + kMaxBatch / kTileRows;
 constexpr int kMaxSlices = 256;   // CTAs per KV head
 // Registers of a softmax thread and of the others; 256 x 208 + 128 x 88 = 384 x 168, what the CTA is
 // launched with (checked on the host).
@@ -86,10 +87,9 @@ struct Segment {
 // Where a row's partial results are: its segment of shared pages and its own, in units and as an index
 // into the results (units = 0: none).
 struct RowPlan {
-  int32_t tile_unit, tile_units, tile, in_tile;  // in_tile: the row's place; + kTwoTiles
+  int32_t tile_unit, tile_units, tile, in_tile;  // in_tile: the row's place in it
   int32_t own_unit, own_units, own, pad;
 };
-constexpr int kTwoTiles = 1 << 16;  // the segment has two matrix tiles, a stream each
 
 struct PlanHeader {
   int32_t units, segments, tiles;  // tiles: segments of shared pages, which come first
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   const int g0 = min(G, tid * gper), g1 = min(G, g0 + gper);
   // (those of many rows come first: a CTA never goes back to them from those of few)
   auto rows_of = [&](int g) { return grouped && s.first[g] != 0x7fffffff ? s.cu[g + 1] - s.cu[g] : 0; };
-  auto few_of = [&](int rows) { return rows % kSegmentRows <= kFewRows ? rows % kSegmentRows : 0; };
+  auto few_of = [&](int rows) { return rows % kTileRows <= kFewRows ? rows % kTileRows : 0; };
   long long mine = 0, total = 0;
   int tiles = 0, tile_units = 0;
 #pragma unroll
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     mine = 0;
     for (int g = g0; g < g1; ++g) {
       const int rows = rows_of(g), few = few_of(rows);
-      const long long n = pass == 0 ? (rows - few + kSegmentRows - 1) / kSegmentRows : few > 0;
+      const long long n = pass == 0 ? (rows - few + kTileRows - 1) / kTileRows : few > 0;
       mine += n << 40 | n * units_of(s.shared[g] * kPage);
     }
     const long long at = plan_scan(s, mine, total);
@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
       const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
       const int begin = pass == 0 ? 0 : rows - few, end = pass == 0 ? rows - few : rows;
       if (pass == 0) s.tile0[g] = seg; else s.few0[g] = seg;
-      for (int r = begin; r < end; r += kSegmentRows) {
-        p.segments[seg] = Segment{unit, units, s.cu[g] + r, min(kSegmentRows, end - r), s.first[g], 0, s.shared[g] * kPage, 0};
+      for (int r = begin; r < end; r += kTileRows) {
+        p.segments[seg] = Segment{unit, units, s.cu[g] + r, min(kTileRows, end - r), s.first[g], 0, s.shared[g] * kPage, 0};
         s.unit[seg++] = unit;
         unit += units;
       }
@@ -270,11 +270,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     const int units = units_of(len[k] - first);
     RowPlan r{0, 0, 0, 0, 0, 0, 0, 0};
     if (g >= 0) {
-      const int in_group = b - s.cu[g], rows = rows_of(g), few = few_of(rows), place = in_group / kSegmentRows;
+      const int in_group = b - s.cu[g], rows = rows_of(g), few = few_of(rows), place = in_group / kTileRows;
       r.tile = in_group < rows - few ? s.tile0[g] + place : s.few0[g];
       r.tile_units = units_of(first);
       r.tile_unit = s.unit[r.tile];
-      r.in_tile = in_group % kSegmentRows | (rows - place * kSegmentRows > kTileRows ? kTwoTiles : 0);
+      r.in_tile = in_group % kTileRows;
     }
     if (units > 0) {
       r.own = seg - tiles;
@@ -308,8 +308,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
 constexpr int kFirst = 1, kLast = 2;          // of this stream in the piece
 constexpr int kPieceStart = 4, kPieceEnd = 8; // of the piece
 constexpr int kQBuffer1 = 16;                 // else buffer 0
-constexpr int kBoth = 32;                     // both streams take the unit, each a tile of its own
-constexpr int kFewFlag = 64;                  // few rows: keys are the matrix's rows
+constexpr int kFewFlag = 32;                  // few rows: keys are the matrix's rows
 
 struct UnitInfo {
   int64_t part;     // where stream 0's partial result goes, in floats; row r's O at + 128 r
@@ -322,10 +321,10 @@ struct UnitInfo {
 };
 
 struct SharedSmem {
-  uint8_t k[kKStages][kTileBytes];
-  uint8_t v[kVStages][kTileBytes];
-  uint8_t q[2][2][kQBlockBytes];
-  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint8_t k[kStages][kTileBytes];
+  uint8_t v[kStages][kTileBytes];
+  uint8_t q[2 * kQBlockBytes];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t info_full[kInfos];
   uint64_t s_full[2], p_full[2], p_free[2], o_ready[2], o_free[2];
@@ -371,11 +370,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kKStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.k_full[i], 1);
       mbar_init(&s.k_empty[i], 1);
-    }
-    for (int i = 0; i < kVStages; ++i) {
       mbar_init(&s.v_full[i], 1);
       mbar_init(&s.v_empty[i], 1);
     }
@@ -411,7 +408,6 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     uint8_t(*ring)[kTileBytes] = is_k ? s.k : s.v;
     uint64_t* full = is_k ? s.k_full : s.v_full;
     uint64_t* empty = is_k ? s.k_empty : s.v_empty;
-    const uint32_t stages = is_k ? kKStages : kVStages;
     bool ok = true;
     int it = 0, next_q = 0;
     uint32_t q_par = 0, q_used = 0;  // bit b: parity of Q buffer b's next load; whether it had one
@@ -452,27 +448,24 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         next = record(seg + 1);
         next_batch = entries(next, 0);
       }
-      // a segment of two matrix tiles takes both Q buffers, another one the next
-      const bool two = g.rows > kTileRows;
-      const int qb = two ? 0 : next_q;
+      const bool few = g.rows <= kFewRows;
+      const int qb = few ? next_q : 0;
       if (is_k) {
-        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
-          const int buf = qb + t;
-          if (lane == 0) ok = wait_or_flag(&s.q_empty[buf], (q_par >> buf & 1) ^ 1u, p.status);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          const int boxes = (min(kTileRows, g.rows - t * kTileRows) + kQBoxRows - 1) / kQBoxRows;
-          if (lane == 0) mbar_arrive_expect_tx(&s.q_full[buf], boxes * 2 * (2 * kQBoxRows * 128));
-          __syncwarp();
-          if (lane < 2 * boxes)
-            tc::tma_load_3d(s.q[buf][lane & 1] + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
-                            g.row + t * kTileRows + (lane >> 1) * kQBoxRows, &s.q_full[buf]);
-          q_par ^= 1u << buf;
-          q_used |= 1u << buf;
-        }
+        // (the first segment of few rows takes the barrier of those of many: none of them is left)
+        if (lane == 0) ok = wait_or_flag(&s.q_empty[qb], (q_par >> qb & 1) ^ 1u, p.status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        const int boxes = (g.rows + kQBoxRows - 1) / kQBoxRows;
+        uint8_t* to = s.q + (few ? qb * kFewQBytes : 0) + (lane & 1) * (few ? kFewHalfBytes : kQBlockBytes);
+        if (lane == 0) mbar_arrive_expect_tx(&s.q_full[qb], boxes * 2 * (2 * kQBoxRows * 128));
+        __syncwarp();
+        if (lane < 2 * boxes)
+          tc::tma_load_3d(to + (lane >> 1) * (2 * kQBoxRows * 128), &q_map, (lane & 1) * 64, 2 * head,
+                          g.row + (lane >> 1) * kQBoxRows, &s.q_full[qb]);
+        q_par ^= 1u << qb;
+        q_used |= 1u << qb;
       }
-      next_q = qb ^ 1;
+      if (few) next_q = qb ^ 1;
       const bool is_tile = seg < plan.tiles;
       for (int kb = k0; kb < k1 && ok; kb += kBatch) {
         const int ahead = kb + kBatch < k1 ? entries(g, kb + kBatch) : 0;
@@ -489,8 +482,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           // K's barrier hands the info on. The unit that its slot held last has been consumed: K's stage
-          // was released by the scores of unit it - kKStages, which were issued after P V of the unit two
-          // before that one.
+          // was released by the scores of unit it - kStages, which were issued after P V of the unit two
+          // before that one (it - 5; a slot serves every eighth).
           if (is_k && lane == 0) {
             UnitInfo& f = s.info[it % kInfos];
             const int cap = is_tile ? 2 * p.tile_rows : 2;
@@ -499,10 +492,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
             f.part = slot * cap * kRowFloats;
             f.stats = cap * kHeadDim;
             f.keys = keys;
-            const int streams = two ? 1 : 2;  // that take the piece's units in turn
-            f.flags = (k - k0 < streams ? kFirst : 0) | (k1 - 1 - k < streams ? kLast : 0) |
-                      (k == k0 ? kPieceStart : 0) | (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0) |
-                      (two ? kBoth : 0) | (g.rows <= kFewRows ? kFewFlag : 0);
+            f.flags = (k - k0 < 2 ? kFirst : 0) | (k1 - 1 - k < 2 ? kLast : 0) | (k == k0 ? kPieceStart : 0) |
+                      (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0) | (few ? kFewFlag : 0);
             f.rows = 2 * g.rows;
             f.is_tile = is_tile ? 1 : 0;
             mbar_arrive(&s.info_full[it % kInfos]);
@@ -511,7 +502,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           __syncwarp();
           if (lane < pages) tc::tma_load_5d(ring[st] + lane * kPageBytes, map, 0, 0, 0, 2 * e, head, &full[st]);
           ++loads;
-          if (++st == stages) {
+          if (++st == kStages) {
             st = 0;
             ph ^= 1u;
           }
@@ -525,8 +516,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // do not leave while copies into this CTA's shared memory may still be landing (only after a wait
     // that gave up: else all of them have been consumed)
     if (!ok && lane == 0) {
-      for (uint32_t k = loads > stages ? loads - stages : 0; k < loads; ++k)
-        wait_or_flag(&full[k % stages], (k / stages) & 1, p.status);
+      for (uint32_t k = loads > kStages ? loads - kStages : 0; k < loads; ++k)
+        wait_or_flag(&full[k % kStages], (k / kStages) & 1, p.status);
       for (int b = 0; b < 2; ++b)
         if (q_used >> b & 1) wait_or_flag(&s.q_full[b], (q_par >> b & 1) ^ 1u, p.status);
     }
@@ -537,7 +528,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // thread some hundred cycles (measured: a wait on a phase long complete 170 to 300, 8 instructions
     // 590, all of a 64-key unit 2,300 from one thread, 1.6 times what its bytes take to arrive).
     if (lane == 0) {
-      const uint64_t dq = tc::smem_desc_sw128(smem_addr(s.q[0][0]), 16, 1024);
+      const uint64_t dq = tc::smem_desc_sw128(smem_addr(s.q), 16, 1024);
       const uint64_t dk = tc::smem_desc_sw128(smem_addr(s.k[0]), 16, kGroupBytes);
       bool ok = true;
       uint32_t st = 0, ph = 0;
@@ -549,48 +540,45 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         if (!ok) break;
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
-        const bool both = flags & kBoth;
-        // N = the unit's keys in whole pages
-        const uint32_t id = tc::idesc_bf16(128, 0, 0, 0) | static_cast<uint32_t>(pages * kPage >> 3) << 17;
-        const uint64_t b = dk + (st * kTileBytes >> 4);
-        for (int t = both ? 0 : it & 1, end = both ? 2 : t + 1; t < end && ok; ++t) {
-          const int qb = both ? t : (flags & kQBuffer1 ? 1 : 0);
-          // S takes the columns of the stream's last P
-          if (had >> t & 1) ok = wait_or_flag(&s.p_free[t], (par >> t & 1) ^ 1u, p.status);
-          had |= 1u << t;
-          par ^= 1u << t;
-          if (flags & kPieceStart) {
-            ok = ok && wait_or_flag(&s.q_full[qb], q_par >> qb & 1, p.status);
-            q_par ^= 1u << qb;
-          }
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t a = dq + (qb * 2 * kQBlockBytes >> 4);
-          if (flags & kFewFlag) {  // S^T = K Q^T, of all the tile's rows: those past the unit's keys are not used
-            constexpr uint32_t few = tc::idesc_bf16(128, kFew, 0, 0);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t step = (kk & 3) * 32;
-              const uint64_t ak = a + (((kk >> 2) * kQBlockBytes + step) >> 4);
-              const uint64_t bk = b + (((kk >> 2) * kHalfBytes + step) >> 4);
-              if (kk == 0) tc::mma_ss_c<false>(tmem + t * kTileKeys, bk, ak, few);
-              else tc::mma_ss_c<true>(tmem + t * kTileKeys, bk, ak, few);
-            }
-          } else
+        const int t = it & 1, qb = flags & kQBuffer1 ? 1 : 0;
+        // S takes the columns of the stream's last P
+        if (had >> t & 1) ok = wait_or_flag(&s.p_free[t], (par >> t & 1) ^ 1u, p.status);
+        had |= 1u << t;
+        par ^= 1u << t;
+        if (flags & kPieceStart) {
+          ok = ok && wait_or_flag(&s.q_full[qb], q_par >> qb & 1, p.status);
+          q_par ^= 1u << qb;
+        }
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t k = dk + (st * kTileBytes >> 4);
+        const uint32_t to = tmem + t * kTileKeys;
+        if (flags & kFewFlag) {  // S^T = K Q^T, of all the tile's keys: those past the unit's are not used
+          constexpr uint32_t id = tc::idesc_bf16(128, kFew, 0, 0);
+          const uint64_t q = dq + (qb * kFewQBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t step = (kk & 3) * 32;
-            const uint64_t ak = a + (((kk >> 2) * kQBlockBytes + step) >> 4);
-            const uint64_t bk = b + (((kk >> 2) * kHalfBytes + step) >> 4);
-            if (kk == 0) tc::mma_ss_c<false>(tmem + t * kTileKeys, ak, bk, id);
-            else tc::mma_ss_c<true>(tmem + t * kTileKeys, ak, bk, id);
+            const uint64_t qk = q + (((kk >> 2) * kFewHalfBytes + step) >> 4);
+            const uint64_t kk_ = k + (((kk >> 2) * kHalfBytes + step) >> 4);
+            if (kk == 0) tc::mma_ss_c<false>(to, kk_, qk, id);
+            else tc::mma_ss_c<true>(to, kk_, qk, id);
           }
-          tc::mma_commit(&s.s_full[t]);
-          if (flags & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
+        } else {  // S = Q K^T; N = the unit's keys in whole pages
+          const uint32_t id = tc::idesc_bf16(128, 0, 0, 0) | static_cast<uint32_t>(pages * kPage >> 3) << 17;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t step = (kk & 3) * 32;
+            const uint64_t qk = dq + (((kk >> 2) * kQBlockBytes + step) >> 4);
+            const uint64_t kk_ = k + (((kk >> 2) * kHalfBytes + step) >> 4);
+            if (kk == 0) tc::mma_ss_c<false>(to, qk, kk_, id);
+            else tc::mma_ss_c<true>(to, qk, kk_, id);
+          }
         }
-        if (!ok) break;
+        tc::mma_commit(&s.s_full[t]);
         tc::mma_commit(&s.k_empty[st]);
-        if (++st == kKStages) {
+        if (flags & kPieceEnd) tc::mma_commit(&s.q_empty[qb]);
+        if (++st == kStages) {
           st = 0;
           ph ^= 1u;
         }
@@ -604,50 +592,53 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // ------------------------------------------------------------------ O += P V
     if (lane == 0) {
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(s.v[0]), kHalfBytes, kGroupBytes);
-      const uint64_t dp = tc::smem_desc_sw128(smem_addr(s.q[0][0]) + kWeightsAt, 16, 1024);
-      constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
+      const uint64_t dp = tc::smem_desc_sw128(smem_addr(s.q) + kWeightsAt, 16, 1024);
       bool ok = true;
       uint32_t st = 0, ph = 0;
-      // bits of stream t: the parity of its next unit; that of its next piece, and whether it had one
-      uint32_t par = 0, piece_par = 0, had = 0;
+      uint32_t piece_par = 0, had = 0;  // bits of stream t: the parity of its next piece, whether it had one
       for (int it = 0; it < nt; ++it) {
-        ok = wait_or_flag(&s.v_full[st], ph, p.status) &&
-             wait_or_flag(&s.info_full[it % kInfos], (it / kInfos) & 1, p.status);
+        const int t = it & 1;
+        // (P's barrier hands the info on too)
+        ok = wait_or_flag(&s.p_full[t], (it >> 1) & 1, p.status) && wait_or_flag(&s.v_full[st], ph, p.status);
         if (!ok) break;
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
-        const bool both = flags & kBoth;
-        const uint64_t b = dv + (st * kTileBytes >> 4);
-        for (int t = both ? 0 : it & 1, end = both ? 2 : t + 1; t < end && ok; ++t) {
-          ok = wait_or_flag(&s.p_full[t], par >> t & 1, p.status);
-          par ^= 1u << t;
-          if (flags & kFirst) {
-            if (had >> t & 1) ok = ok && wait_or_flag(&s.o_free[t], (piece_par >> t & 1) ^ 1u, p.status);
-            had |= 1u << t;
-            piece_par ^= 1u << t;
-          }
+        if (flags & kFirst) {
+          if (had >> t & 1) ok = wait_or_flag(&s.o_free[t], (piece_par >> t & 1) ^ 1u, p.status);
+          had |= 1u << t;
+          piece_par ^= 1u << t;
           if (!ok) break;
-          tc::fence_after_sync();
-          const uint32_t o = tmem + 256 + t * 128, a = tmem + t * kTileKeys;
-          if (flags & kFewFlag) {  // O^T += V^T P^T
-            constexpr uint32_t few = tc::idesc_bf16(128, kFew, 1, 0);
-            const uint64_t w = dp + (t * 2 * kQBlockBytes >> 4);
-            for (int kk = 0; kk < pages; ++kk)
-              tc::mma_ss(o, b + kk * (kPageBytes >> 4), w + (((kk >> 2) * kFewHalfBytes + (kk & 3) * 32) >> 4), few,
-                         kk > 0 || !(flags & kFirst) ? 1u : 0u);
-          } else if (tc::mma_ts(o, a, b, id, flags & kFirst ? 0u : 1u); pages == kTilePages) {
+        }
+        tc::fence_after_sync();
+        const uint32_t o = tmem + 256 + t * 128, first = flags & kFirst ? 0u : 1u;
+        const uint64_t v = dv + (st * kTileBytes >> 4);
+        if (flags & kFewFlag) {  // O^T += V^T P^T
+          constexpr uint32_t id = tc::idesc_bf16(128, kFew, 1, 0);
+          const uint64_t w = dp + (t * kFewQBytes >> 4);
+          tc::mma_ss(o, v, w, id, first);
+          if (pages == kTilePages) {
 #pragma unroll
             for (int kk = 1; kk < kTilePages; ++kk)
-              tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
+              tc::mma_ss_c<true>(o, v + kk * (kPageBytes >> 4), w + (((kk >> 2) * kFewHalfBytes + (kk & 3) * 32) >> 4), id);
           } else {
-            for (int kk = 1; kk < pages; ++kk) tc::mma_ts_c<true>(o, a + kk * 8, b + kk * (kPageBytes >> 4), id);
+            for (int kk = 1; kk < pages; ++kk)
+              tc::mma_ss_c<true>(o, v + kk * (kPageBytes >> 4), w + (((kk >> 2) * kFewHalfBytes + (kk & 3) * 32) >> 4), id);
           }
-          tc::mma_commit(&s.p_free[t]);
-          if (flags & kLast) tc::mma_commit(&s.o_ready[t]);
+        } else {  // O += P V
+          constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
+          const uint32_t w = tmem + t * kTileKeys;
+          tc::mma_ts(o, w, v, id, first);
+          if (pages == kTilePages) {
+#pragma unroll
+            for (int kk = 1; kk < kTilePages; ++kk) tc::mma_ts_c<true>(o, w + kk * 8, v + kk * (kPageBytes >> 4), id);
+          } else {
+            for (int kk = 1; kk < pages; ++kk) tc::mma_ts_c<true>(o, w + kk * 8, v + kk * (kPageBytes >> 4), id);
+          }
         }
-        if (!ok) break;
+        tc::mma_commit(&s.p_free[t]);
         tc::mma_commit(&s.v_empty[st]);
-        if (++st == kVStages) {
+        if (flags & kLast) tc::mma_commit(&s.o_ready[t]);
+        if (++st == kStages) {
           st = 0;
           ph ^= 1u;
         }
@@ -665,25 +656,22 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_bits + stream * kTileKeys, t_o = tmem + lane_bits + 256 + stream * 128;
     bool ok = true;
-    int it = 0;
+    int it = stream;
     uint32_t n = 0, pieces = 0;  // units and pieces of this stream so far
-    // The next unit's flags; -1 after the last or a wait that gave up. Units of the other stream are passed
-    // over (their slots cannot have been used again: that takes this stream's own units done).
+    // The next unit's flags; false after the last one or a wait that gave up.
     auto next_flags = [&](int& flags) {
-      for (; it < nt; ++it) {
-        ok = warp_wait(&s.info_full[it % kInfos], (it / kInfos) & 1, lane, p.status);
-        if (!ok) return false;
-        const volatile UnitInfo& f = s.info[it % kInfos];
-        flags = f.flags;
-        if ((flags & kBoth) || (it & 1) == stream) return true;
-      }
-      return false;
+      if (it >= nt) return false;
+      ok = warp_wait(&s.info_full[it % kInfos], (it / kInfos) & 1, lane, p.status);
+      if (!ok) return false;
+      const volatile UnitInfo& f = s.info[it % kInfos];
+      flags = f.flags;
+      return true;
     };
     // Slots of the unit's last page after its last key may hold anything, NaN too: their V rows meet
     // weights of 0 as zeros.
     auto clear_tail = [&](int keys) {
-      const uint32_t vst = static_cast<uint32_t>(it) % kVStages;
-      ok = warp_wait(&s.v_full[vst], (static_cast<uint32_t>(it) / kVStages) & 1, lane, p.status);
+      const uint32_t vst = static_cast<uint32_t>(it) % kStages;
+      ok = warp_wait(&s.v_full[vst], (static_cast<uint32_t>(it) / kStages) & 1, lane, p.status);
       if (!ok) return;
       const int end = (keys + kPage - 1) / kPage * kPage;
       for (int e = keys * 16 + r; e < end * 16; e += 128)  // 16 bytes of a key
@@ -703,10 +691,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     {
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       float m_used = -CUDART_INF_F, l = 0.f;
-      for (; more && !(flags & kFewFlag); ++it, more = next_flags(flags)) {
+      for (; more && !(flags & kFewFlag); it += 2, more = next_flags(flags)) {
         const volatile UnitInfo& f = s.info[it % kInfos];
-        const int keys = f.keys, stats = f.stats;
-        const int rows = flags & kBoth ? min(f.rows - stream * 2 * kTileRows, 2 * kTileRows) : f.rows;
+        const int keys = f.keys, rows = f.rows, stats = f.stats;
         float* part = p.tile_parts + f.part + stream * (stats / kHeadDim * kRowFloats);
         const bool used = quarter * 32 < rows;  // some of this warp's rows are query rows
         ok = warp_wait(&s.s_full[stream], n & 1, lane, p.status);
@@ -823,7 +810,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         ok = warp_wait(&s.met[stream], meetings & 1, lane, p.status);
         ++meetings;
       };
-      for (; more && ok; ++it, more = ok && next_flags(flags)) {
+      for (; more && ok; it += 2, more = ok && next_flags(flags)) {
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int keys = f.keys, rows = f.rows, stats = f.stats;
         float* part = (f.is_tile ? p.tile_parts : p.row_parts) + f.part + stream * (stats / kHeadDim * kRowFloats);
@@ -877,7 +864,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           }
         }
         const float m_eff = m_used == -CUDART_INF_F ? 0.f : m_used;
-        uint8_t* w = s.q[stream][0] + kWeightsAt + (r >> 6) * kFewHalfBytes + (r & 7) * 2;
+        uint8_t* w = s.q + kWeightsAt + stream * kFewQBytes + (r >> 6) * kFewHalfBytes + (r & 7) * 2;
 #pragma unroll
         for (int c = 0; c < kFew; ++c) {
           if (c >= rows) break;
@@ -970,16 +957,9 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     const int cap = set == 0 ? 2 * p.tile_rows : 2;
     const int first = static_cast<int>(U * i / n), end = static_cast<int>(U * (i + 1) / n);
     const int u0 = max(first, unit), u1 = min(end, unit + units);
-    int r = 0;
-    bool there;
-    if (set == 0 && (row.in_tile & kTwoTiles)) {  // a stream per tile
-      const int in_tile = row.in_tile & (kTwoTiles - 1);
-      there = u1 > u0 && stream == in_tile / kTileRows;
-      r = 2 * (in_tile % kTileRows);
-    } else {  // units alternate between the streams, from the slice's first
-      there = u1 - u0 >= 2 || (u1 - u0 == 1 && ((u0 - first) & 1) == stream);
-      if (set == 0) r = 2 * row.in_tile;
-    }
+    // units alternate between the streams, from the slice's first
+    const bool there = u1 - u0 >= 2 || (u1 - u0 == 1 && ((u0 - first) & 1) == stream);
+    const int r = set == 0 ? 2 * row.in_tile : 0;
     const float* part = (set == 0 ? p.tile_parts : p.row_parts) +
                         (((static_cast<int64_t>(i) + (set == 0 ? row.tile : row.own)) * p.hkv + head) * 2 + stream) * cap * kRowFloats;
     float4 ml = make_float4(-CUDART_INF_F, 0.f, -CUDART_INF_F, 0.f);  // (m, l) of both query heads
@@ -1085,8 +1065,8 @@ bool shared_layout(SharedLayout& l, int hkv, int batch, int groups, int max_grou
   if (sms <= 0) return false;
   l.slices = std::min(kMaxSlices, std::max(1, sms / hkv));
   l.tile_rows = std::max(1, std::min({kTileRows, max_group_rows, batch}));
-  // a group's segments: one, and one more for every kSegmentRows rows
-  const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kSegmentRows : 0;
+  // a group's segments: one, and one more for every kTileRows rows
+  const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kTileRows : 0;
   l.header = 0;
   l.slice_segment = 256;
   l.segments = align256(l.slice_segment + sizeof(int32_t) * l.slices);
