@@ -91,9 +91,12 @@ struct RowPlan {
   int32_t own_unit, own_units, own, pad;
 };
 
-struct PlanHeader {
-  int32_t units, segments, tiles;  // tiles: segments of shared pages, which come first
-  int32_t pad;
+// A slice: its units, the segment of the first one, and what all slices have alike.
+struct Slice {
+  int32_t u0, u1, segment;
+  int32_t segments, tiles;  // tiles: segments of shared pages, which come first
+  int32_t units;            // of all slices
+  int32_t pad[2];
 };
 
 struct SharedParams {
@@ -109,8 +112,7 @@ struct SharedParams {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  PlanHeader* header;
-  int32_t* slice_segment;  // [slices]
+  Slice* slice;            // [slices]
   Segment* segments;
   RowPlan* rows;           // [batch]
   float* tile_parts;       // [slices + tiles][hkv][2 streams][2 tile_rows][128], then (m, l)
@@ -123,7 +125,8 @@ struct SharedParams {
 constexpr int kPlanThreads = 1024;  // at most: four rows a thread
 
 struct PlanSmem {
-  long long warp_sums[kPlanThreads / 32], total;
+  long long warp_sums[3][kPlanThreads / 32];
+  long long totals[3];
   int32_t bad;
   int32_t cu[kMaxGroups + 1];
   int32_t shared[kMaxGroups];     // shared pages
@@ -133,50 +136,59 @@ struct PlanSmem {
   int32_t unit[kMaxSegments + 1]; // first unit of each segment
 };
 
-// Exclusive prefix sum over the CTA of packed (count << 40 | units), and the total.
-__device__ __forceinline__ long long plan_scan(PlanSmem& s, long long v, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = v;
+__device__ __forceinline__ long long warp_scan_sum(long long v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
+    const long long n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
   }
-  if (lane == 31) s.warp_sums[warp] = incl;
+  return v;
+}
+
+// Exclusive prefix sums over the CTA of three packed (count << 40 | units), and their totals.
+__device__ __forceinline__ void plan_scan(PlanSmem& s, long long (&v)[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    incl[k] = warp_scan_sum(v[k], lane);
+    if (lane == 31) s.warp_sums[k][warp] = incl[k];
+  }
   __syncthreads();
   if (warp == 0) {
-    const long long w = lane < static_cast<int>(blockDim.x >> 5) ? s.warp_sums[lane] : 0;
-    long long x = w;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long n = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += n;
+    for (int k = 0; k < 3; ++k) {
+      const long long w = lane < static_cast<int>(blockDim.x >> 5) ? s.warp_sums[k][lane] : 0;
+      const long long x = warp_scan_sum(w, lane);
+      s.warp_sums[k][lane] = x - w;
+      if (lane == 31) s.totals[k] = x;
     }
-    s.warp_sums[lane] = x - w;
-    if (lane == 31) s.total = x;
   }
   __syncthreads();
-  total = s.total;
-  const long long before = s.warp_sums[warp] + incl - v;
-  __syncthreads();
-  return before;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) v[k] = s.warp_sums[k][warp] + incl[k] - v[k];
 }
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
+__device__ __forceinline__ int count_of(long long packed) { return static_cast<int>(packed >> 40); }
+__device__ __forceinline__ int units_in(long long packed) { return static_cast<int>(packed & ((1ll << 40) - 1)); }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PlanSmem& s = *reinterpret_cast<PlanSmem*>(smem_raw);
-  const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x);
+  const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x), G = p.groups;
   launch_next();
-  await_previous();
   if (tid == 0) s.bad = 0;
-  const int G = p.groups;
-  for (int g = tid; g <= G && G > 0; g += threads) s.cu[g] = p.cu_group_rows[g];
-  __syncthreads();
-  for (int g = tid; g < G; g += threads) {
-    const int a = s.cu[g], b = s.cu[g + 1];
-    if (a < 0 || b < a || b > p.batch || b - a > p.max_group_rows) s.bad = 1;
+  await_previous();
+  // rows: four consecutive ones a thread at most
+  const int per = (p.batch + threads - 1) / threads;
+  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  int len[4], group[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) len[k] = b0 + k < b1 ? p.seq_lens[b0 + k] : 0;
+  for (int g = tid; g <= G && G > 0; g += threads) {
+    s.cu[g] = p.cu_group_rows[g];
+    if (g == G) break;
     int n = p.shared_pages[g];
     if (n < 0 || n > p.bt_stride) {
       flag_error(p.status, PA_DEV_ERR_LENGTH);
@@ -186,17 +198,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     s.first[g] = 0x7fffffff;
   }
   __syncthreads();
+  for (int g = tid; g < G; g += threads) {
+    const int a = s.cu[g], b = s.cu[g + 1];
+    if (a < 0 || b < a || b > p.batch || b - a > p.max_group_rows) s.bad = 1;
+  }
+  __syncthreads();
   // groups that are not disjoint ranges of rows: no row shares anything
   const bool grouped = G > 0 && !s.bad;
   if (G > 0 && s.bad && tid == 0) flag_error(p.status, PA_DEV_ERR_LENGTH);
   const int row_lo = grouped ? s.cu[0] : 0, row_hi = grouped ? s.cu[G] : 0;
-
-  // rows: four consecutive ones a thread at most
-  const int per = (p.batch + threads - 1) / threads;
-  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
-  int len[4], group[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) len[k] = b0 + k < b1 ? p.seq_lens[b0 + k] : 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int b = b0 + k;
@@ -219,24 +229,31 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     }
   }
   __syncthreads();
-  // segments of shared pages
+  // Segments: those of shared pages with many rows (a CTA never goes back to them from those with few),
+  // those with few, and the rows' own pages.
   const int gper = (G + threads - 1) / threads;
   const int g0 = min(G, tid * gper), g1 = min(G, g0 + gper);
-  // (those of many rows come first: a CTA never goes back to them from those of few)
   auto rows_of = [&](int g) { return grouped && s.first[g] != 0x7fffffff ? s.cu[g + 1] - s.cu[g] : 0; };
   auto few_of = [&](int rows) { return rows % kTileRows <= kFewRows ? rows % kTileRows : 0; };
-  long long mine = 0, total = 0;
-  int tiles = 0, tile_units = 0;
+  long long at[3] = {0, 0, 0};
+  for (int g = g0; g < g1; ++g) {
+    const int rows = rows_of(g), few = few_of(rows);
+    const long long units = units_of(s.shared[g] * kPage), many = (rows - few + kTileRows - 1) / kTileRows;
+    at[0] += many << 40 | many * units;
+    if (few > 0) at[1] += 1ll << 40 | units;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int units = units_of(len[k] - (group[k] >= 0 ? s.shared[group[k]] * kPage : 0));
+    if (units > 0) at[2] += 1ll << 40 | units;
+  }
+  plan_scan(s, at);
+  const int many_tiles = count_of(s.totals[0]), tiles = many_tiles + count_of(s.totals[1]);
+  const int many_units = units_in(s.totals[0]), tile_units = many_units + units_in(s.totals[1]);
+  const int segments = tiles + count_of(s.totals[2]), units_all = tile_units + units_in(s.totals[2]);
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
-    mine = 0;
-    for (int g = g0; g < g1; ++g) {
-      const int rows = rows_of(g), few = few_of(rows);
-      const long long n = pass == 0 ? (rows - few + kTileRows - 1) / kTileRows : few > 0;
-      mine += n << 40 | n * units_of(s.shared[g] * kPage);
-    }
-    const long long at = plan_scan(s, mine, total);
-    int seg = tiles + static_cast<int>(at >> 40), unit = tile_units + static_cast<int>(at & ((1ll << 40) - 1));
+    int seg = (pass == 0 ? 0 : many_tiles) + count_of(at[pass]), unit = (pass == 0 ? 0 : many_units) + units_in(at[pass]);
     for (int g = g0; g < g1; ++g) {
       const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
       const int begin = pass == 0 ? 0 : rows - few, end = pass == 0 ? rows - few : rows;
@@ -247,58 +264,51 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
         unit += units;
       }
     }
-    tiles += static_cast<int>(total >> 40);
-    tile_units += static_cast<int>(total & ((1ll << 40) - 1));
   }
-  // segments of the rows' own pages
-  mine = 0;
+  if (tid == 0) s.unit[segments] = units_all;
+  int seg = tiles + count_of(at[2]), unit = tile_units + units_in(at[2]);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int first = group[k] >= 0 ? s.shared[group[k]] * kPage : 0;
-    const int units = units_of(len[k] - first);
-    if (units > 0) mine += 1ll << 40 | units;
+    const int first = group[k] >= 0 ? s.shared[group[k]] * kPage : 0, units = units_of(len[k] - first);
+    if (b0 + k >= b1 || units <= 0) continue;
+    p.segments[seg] = Segment{unit, units, b0 + k, 1, b0 + k, first, len[k], 0};
+    s.unit[seg++] = unit;
+    unit += units;
   }
-  const long long at = plan_scan(s, mine, total);  // (its barriers also order s.tile0)
-  const int segments = tiles + static_cast<int>(total >> 40);
-  const int units_all = tile_units + static_cast<int>(total & ((1ll << 40) - 1));
-  int seg = tiles + static_cast<int>(at >> 40), unit = tile_units + static_cast<int>(at & ((1ll << 40) - 1));
+  __syncthreads();
+  seg = tiles + count_of(at[2]);
+  unit = tile_units + units_in(at[2]);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int b = b0 + k, g = group[k];
     if (b >= b1) continue;
     const int first = g >= 0 ? s.shared[g] * kPage : 0;
-    const int units = units_of(len[k] - first);
     RowPlan r{0, 0, 0, 0, 0, 0, 0, 0};
     if (g >= 0) {
-      const int in_group = b - s.cu[g], rows = rows_of(g), few = few_of(rows), place = in_group / kTileRows;
-      r.tile = in_group < rows - few ? s.tile0[g] + place : s.few0[g];
+      const int in_group = b - s.cu[g], rows = rows_of(g), few = few_of(rows);
+      r.tile = in_group < rows - few ? s.tile0[g] + in_group / kTileRows : s.few0[g];
       r.tile_units = units_of(first);
       r.tile_unit = s.unit[r.tile];
       r.in_tile = in_group % kTileRows;
     }
+    const int units = units_of(len[k] - first);
     if (units > 0) {
-      r.own = seg - tiles;
+      r.own = seg++ - tiles;
       r.own_unit = unit;
       r.own_units = units;
-      p.segments[seg] = Segment{unit, units, b, 1, b, first, len[k], 0};
-      s.unit[seg++] = unit;
       unit += units;
     }
     p.rows[b] = r;
   }
-  if (tid == 0) {
-    s.unit[segments] = units_all;
-    *p.header = PlanHeader{units_all, segments, tiles, 0};
-  }
-  __syncthreads();
   for (int i = tid; i < p.slices; i += threads) {
-    const int u = static_cast<int>(static_cast<long long>(units_all) * i / p.slices);
-    int lo = 0, hi = max(segments, 1);  // last segment with a first unit <= u
+    const int u0 = static_cast<int>(static_cast<long long>(units_all) * i / p.slices);
+    const int u1 = static_cast<int>(static_cast<long long>(units_all) * (i + 1) / p.slices);
+    int lo = 0, hi = max(segments, 1);  // last segment with a first unit <= u0
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s.unit[mid] <= u) lo = mid; else hi = mid;
+      if (s.unit[mid] <= u0) lo = mid; else hi = mid;
     }
-    p.slice_segment[i] = lo;
+    p.slice[i] = Slice{u0, u1, lo, segments, tiles, units_all, {0, 0}};
   }
 }
 
@@ -328,6 +338,7 @@ struct SharedSmem {
   uint64_t q_full[2], q_empty[2];
   uint64_t info_full[kInfos];
   uint64_t s_full[2], p_full[2], p_free[2], o_ready[2], o_free[2];
+  uint64_t few_ready[2][2], few_free[2][2];  // of a stream's two O with few rows
   uint64_t mma_done[2], met[2];
   uint32_t tmem_base;
   float exchange[2][3][4][kFew];  // of each stream: maxima (two, in turn) and sums, per warp and row
@@ -357,14 +368,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_next();
-  await_previous();
   SharedSmem& s = *reinterpret_cast<SharedSmem*>(smem_raw);
   const int head = static_cast<int>(blockIdx.x) % p.hkv, slice = static_cast<int>(blockIdx.x) / p.hkv;
-  const PlanHeader plan = *p.header;
-  const int u0 = static_cast<int>(static_cast<long long>(plan.units) * slice / p.slices);
-  const int u1 = static_cast<int>(static_cast<long long>(plan.units) * (slice + 1) / p.slices);
-  const int nt = u1 - u0;
-  if (nt <= 0) return;  // uniform across the CTA: nothing allocated yet
   if ((smem_addr(smem_raw) & 1023u) != 0) {  // not the layout this kernel was built for
     if (threadIdx.x == 0) flag_error(p.status, PA_DEV_ERR_INTERNAL);
     return;
@@ -386,6 +391,10 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       mbar_init(&s.met[i], 4);
       mbar_init(&s.o_ready[i], 1);
       mbar_init(&s.o_free[i], 4);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&s.few_ready[i][k], 1);
+        mbar_init(&s.few_free[i][k], 4);
+      }
     }
     for (int i = 0; i < kInfos; ++i) mbar_init(&s.info_full[i], 1);
     fence_mbar_init();
@@ -394,7 +403,11 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = s.tmem_base;  // S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512)
+  const uint32_t tmem = s.tmem_base;  // S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); few rows:
+                                      // S_t [0, 16) and two O_t at [64, 96) of the stream's S
+  await_previous();
+  const Slice plan = p.slice[slice];
+  const int u0 = plan.u0, u1 = plan.u1, nt = u1 - u0;
 
   if (warp >= 8) {
     tc::regs_decrease<kControlRegs>();
@@ -416,8 +429,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // batch ahead, and those of the next segment's first units while this one's are loaded: an entry
     // read just before its copies would cost its latency in every unit.
     constexpr int kBatch = 32 / kTilePages;
-    int seg = p.slice_segment[slice], records = seg;
-    Segment lane_record = p.segments[min(seg + lane, plan.segments - 1)];
+    int seg = plan.segment, records = seg;
+    Segment lane_record = p.segments[max(0, min(seg + lane, plan.segments - 1))];
     auto record = [&](int i) {
       if (i >= records + 32) {
         records = i;
@@ -439,7 +452,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       return key < g.end_key ? p.block_table[static_cast<int64_t>(g.table_row) * p.bt_stride + key / kPage] : 0;
     };
     Segment g = record(seg);
-    int batch = entries(g, u0 - g.unit);
+    int batch = nt > 0 ? entries(g, u0 - g.unit) : 0;
     while (it < nt && ok) {
       const int k0 = u0 + it - g.unit, k1 = min(u1 - g.unit, g.units);
       Segment next = g;
@@ -596,6 +609,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       bool ok = true;
       uint32_t st = 0, ph = 0;
       uint32_t piece_par = 0, had = 0;  // bits of stream t: the parity of its next piece, whether it had one
+      uint32_t few_pieces = 0;          // of stream t, 16 bits each
       for (int it = 0; it < nt; ++it) {
         const int t = it & 1;
         // (P's barrier hands the info on too)
@@ -603,18 +617,24 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         if (!ok) break;
         const volatile UnitInfo& f = s.info[it % kInfos];
         const int pages = (f.keys + kPage - 1) / kPage, flags = f.flags;
+        const uint32_t piece = few_pieces >> 16 * t & 0xffffu, buf = piece & 1;
         if (flags & kFirst) {
-          if (had >> t & 1) ok = wait_or_flag(&s.o_free[t], (piece_par >> t & 1) ^ 1u, p.status);
-          had |= 1u << t;
-          piece_par ^= 1u << t;
+          if (flags & kFewFlag) {
+            if (piece >= 2) ok = wait_or_flag(&s.few_free[t][buf], ((piece >> 1) & 1) ^ 1u, p.status);
+          } else {
+            if (had >> t & 1) ok = wait_or_flag(&s.o_free[t], (piece_par >> t & 1) ^ 1u, p.status);
+            had |= 1u << t;
+            piece_par ^= 1u << t;
+          }
           if (!ok) break;
         }
         tc::fence_after_sync();
-        const uint32_t o = tmem + 256 + t * 128, first = flags & kFirst ? 0u : 1u;
+        const uint32_t first = flags & kFirst ? 0u : 1u;
         const uint64_t v = dv + (st * kTileBytes >> 4);
         if (flags & kFewFlag) {  // O^T += V^T P^T
           constexpr uint32_t id = tc::idesc_bf16(128, kFew, 1, 0);
           const uint64_t w = dp + (t * kFewQBytes >> 4);
+          const uint32_t o = tmem + t * kTileKeys + 64 + buf * kFew;
           tc::mma_ss(o, v, w, id, first);
           if (pages == kTilePages) {
 #pragma unroll
@@ -626,7 +646,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           }
         } else {  // O += P V
           constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
-          const uint32_t w = tmem + t * kTileKeys;
+          const uint32_t w = tmem + t * kTileKeys, o = tmem + 256 + t * 128;
           tc::mma_ts(o, w, v, id, first);
           if (pages == kTilePages) {
 #pragma unroll
@@ -637,7 +657,10 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         }
         tc::mma_commit(&s.p_free[t]);
         tc::mma_commit(&s.v_empty[st]);
-        if (flags & kLast) tc::mma_commit(&s.o_ready[t]);
+        if (flags & kLast) {
+          tc::mma_commit(flags & kFewFlag ? &s.few_ready[t][buf] : &s.o_ready[t]);
+          if (flags & kFewFlag) few_pieces = (few_pieces & ~(0xffffu << 16 * t)) | ((piece + 1) & 0xffffu) << 16 * t;
+        }
         if (++st == kStages) {
           st = 0;
           ph ^= 1u;
@@ -802,6 +825,30 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       float m_used = -CUDART_INF_F;
       float l[kFew];  // this thread's keys' part of each row's sum
       uint32_t meetings = 0;
+      // A piece's O is stored after the next unit's weights have been handed over, while its products run;
+      // until then: where to, how many rows, and lane c's maximum and sum of row c.
+      uint32_t few_pieces = 0;
+      bool left = false;
+      float* left_part = nullptr;
+      int left_stats = 0, left_rows = 0;
+      float left_m = 0.f, left_l = 0.f;
+      auto store_left = [&] {
+        const uint32_t piece = few_pieces - 1, buf = piece & 1;
+        left = false;
+        ok = warp_wait(&s.few_ready[stream][buf], (piece >> 1) & 1, lane, p.status);
+        if (!ok) return;
+        tc::fence_after_sync();
+        uint32_t o[kFew];
+        tc::tmem_ld16(t_s + 64 + buf * kFew, o);
+        tc::tmem_wait_ld();
+        hand_over(&s.few_free[stream][buf]);
+#pragma unroll
+        for (int c = 0; c < kFew; ++c)
+          if (c < left_rows) left_part[c * kHeadDim + r] = __uint_as_float(o[c]);
+        // (a NaN among the scores: any finite maximum hands the NaN on)
+        if (quarter == 0 && lane < left_rows)
+          *reinterpret_cast<float2*>(left_part + left_stats + 2 * lane) = make_float2(left_l == left_l ? left_m : 0.f, left_l);
+      };
       // all[w][c]: value of lane c of warp w
       auto meet = [&](float (*all)[kFew], float value) {
         if (lane < kFew) all[quarter][lane] = value;
@@ -850,8 +897,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           const float alpha = m_used == -CUDART_INF_F ? 0.f : fast_exp2(m_used - m_new);
           m_used = m_new;
           if (!(flags & kFirst)) {
+            const uint32_t t_few = t_s + 64 + (few_pieces & 1) * kFew;
             uint32_t o[kFew];
-            tc::tmem_ld16(t_o, o);
+            tc::tmem_ld16(t_few, o);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < kFew; ++c) {
@@ -859,7 +907,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
               l[c] *= a;
               o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
             }
-            tc::tmem_st16(t_o, o);
+            tc::tmem_st16(t_few, o);
             tc::tmem_wait_st();
           }
         }
@@ -878,6 +926,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         if (keys % kPage != 0) clear_tail(keys);
         if (!ok) break;
         hand_over(&s.p_full[stream]);
+        if (left) store_left();
+        if (!ok) break;
         if (flags & kLast) {
           // lane c: the warp's sum of row c, then all four warps'
           float sum = 0.f;
@@ -892,23 +942,16 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           all = s.exchange[stream][2];
           meet(all, sum);
           if (!ok) break;
-          ok = warp_wait(&s.o_ready[stream], pieces & 1, lane, p.status);
-          if (!ok) break;
-          ++pieces;
-          tc::fence_after_sync();
-          uint32_t o[kFew];
-          tc::tmem_ld16(t_o, o);
-          tc::tmem_wait_ld();
-          hand_over(&s.o_free[stream]);
-#pragma unroll
-          for (int c = 0; c < kFew; ++c)
-            if (c < rows) part[c * kHeadDim + r] = __uint_as_float(o[c]);
-          if (quarter == 0 && lane < rows) {
-            const float all_l = (all[0][lane] + all[1][lane]) + (all[2][lane] + all[3][lane]);
-            *reinterpret_cast<float2*>(part + stats + 2 * lane) = make_float2(all_l == all_l ? m_used : 0.f, all_l);
-          }
+          left = true;
+          left_part = part;
+          left_stats = stats;
+          left_rows = rows;
+          left_m = m_used;
+          left_l = lane < kFew ? (all[0][lane] + all[1][lane]) + (all[2][lane] + all[3][lane]) : 0.f;
+          ++few_pieces;
         }
       }
+      if (ok && left) store_left();
     }
   }
 
@@ -937,7 +980,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   const int b = static_cast<int>(blockIdx.x) / p.hkv, head = static_cast<int>(blockIdx.x) % p.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   await_previous();
-  const long long U = p.header->units, n = p.slices;
+  const long long U = p.slice->units, n = p.slices;
   const RowPlan row = p.rows[b];
   // slices [i0, i1] hold a set: slice i has units [U i / n, U (i + 1) / n)
   int i0[2] = {0, 0}, count[2] = {0, 0};
@@ -1055,7 +1098,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 // ---------------------------------------------------------------------------------------------
 struct SharedLayout {
   int slices, tile_rows;
-  size_t header, slice_segment, segments, rows, tile_parts, row_parts, total;
+  size_t slice, segments, rows, tile_parts, row_parts, total;
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1067,9 +1110,8 @@ bool shared_layout(SharedLayout& l, int hkv, int batch, int groups, int max_grou
   l.tile_rows = std::max(1, std::min({kTileRows, max_group_rows, batch}));
   // a group's segments: one, and one more for every kTileRows rows
   const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kTileRows : 0;
-  l.header = 0;
-  l.slice_segment = 256;
-  l.segments = align256(l.slice_segment + sizeof(int32_t) * l.slices);
+  l.slice = 0;
+  l.segments = align256(sizeof(Slice) * l.slices);
   l.rows = align256(l.segments + sizeof(Segment) * (tiles + batch));
   l.tile_parts = align256(l.rows + sizeof(RowPlan) * batch);
   const size_t per_row = static_cast<size_t>(hkv) * 2 * 2 * kRowFloats * sizeof(float);
@@ -1175,8 +1217,7 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.status = status;
-  p.header = reinterpret_cast<PlanHeader*>(ws + l.header);
-  p.slice_segment = reinterpret_cast<int32_t*>(ws + l.slice_segment);
+  p.slice = reinterpret_cast<Slice*>(ws + l.slice);
   p.segments = reinterpret_cast<Segment*>(ws + l.segments);
   p.rows = reinterpret_cast<RowPlan*>(ws + l.rows);
   p.tile_parts = reinterpret_cast<float*>(ws + l.tile_parts);
