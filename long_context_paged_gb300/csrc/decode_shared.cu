@@ -81,7 +81,7 @@ struct Segment {
   int32_t row, rows;         // query rows
   int32_t table_row;         // whose table entries are read
   int32_t first_key, end_key;
-  int32_t pad;
+  int32_t index;             // among the segments of shared pages; ~index among the rows' own
 };
 
 // Where a row's partial results are: its segment of shared pages and its own, in units and as an index
@@ -94,9 +94,8 @@ struct RowPlan {
 // A slice: its units, the segment of the first one, and what all slices have alike.
 struct Slice {
   int32_t u0, u1, segment;
-  int32_t segments, tiles;  // tiles: segments of shared pages, which come first
-  int32_t units;            // of all slices
-  int32_t pad[2];
+  int32_t segments, units;  // of all slices
+  int32_t pad[3];
 };
 
 struct SharedParams {
@@ -128,13 +127,17 @@ struct PlanSmem {
   long long warp_sums[3][kPlanThreads / 32];
   long long totals[3];
   int32_t bad;
-  int32_t cu[kMaxGroups + 1];
-  int32_t shared[kMaxGroups];     // shared pages
-  int32_t first[kMaxGroups];      // first row that uses them
-  int32_t tile0[kMaxGroups];      // first segment of many rows
-  int32_t few0[kMaxGroups];       // the last segment, if it has few
-  int32_t unit[kMaxSegments + 1]; // first unit of each segment
+  // groups: first row, shared pages, first row that uses them; segments and units before the group's of
+  // many rows, and before its one of few
+  int32_t cu[kMaxGroups + 1], shared[kMaxGroups], first[kMaxGroups];
+  int32_t many_seg[kMaxGroups], many_unit[kMaxGroups], few_seg[kMaxGroups], few_unit[kMaxGroups];
+  // rows: keys, last group that starts at or before the row (-1: none), pages that it shares; segments
+  // and units of own pages before the row's
+  int32_t len[kMaxBatch], group[kMaxBatch], start[kMaxBatch];
+  int32_t own_seg[kMaxBatch + 1], own_unit[kMaxBatch + 1];
+  int32_t unit[kMaxSegments + 1];  // first unit of each segment
 };
+static_assert(sizeof(PlanSmem) <= 232448, "shared memory over the 227 KB limit");
 
 __device__ __forceinline__ long long warp_scan_sum(long long v, int lane) {
 #pragma unroll
@@ -173,22 +176,25 @@ __device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1
 __device__ __forceinline__ int count_of(long long packed) { return static_cast<int>(packed >> 40); }
 __device__ __forceinline__ int units_in(long long packed) { return static_cast<int>(packed & ((1ll << 40) - 1)); }
 
+// Loops are not unrolled: one CTA runs this code once, and its time is what fetching it takes.
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PlanSmem& s = *reinterpret_cast<PlanSmem*>(smem_raw);
-  const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x), G = p.groups;
+  const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x), G = p.groups, B = p.batch;
   launch_next();
   if (tid == 0) s.bad = 0;
   await_previous();
-  // rows: four consecutive ones a thread at most
-  const int per = (p.batch + threads - 1) / threads;
-  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
-  int len[4], group[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) len[k] = b0 + k < b1 ? p.seq_lens[b0 + k] : 0;
-  for (int g = tid; g <= G && G > 0; g += threads) {
+#pragma unroll 1
+  for (int b = tid; b < B; b += threads) {
+    int len = p.seq_lens[b];
+    const int most = p.bt_stride * kPage;
+    if (len < 0 || len > most || len > p.max_seq_len) flag_error(p.status, PA_DEV_ERR_LENGTH);
+    s.len[b] = min(max(len, 0), most);
+  }
+#pragma unroll 1
+  for (int g = tid; g < G; g += threads) {
     s.cu[g] = p.cu_group_rows[g];
-    if (g == G) break;
+    if (g == G - 1) s.cu[G] = p.cu_group_rows[G];
     int n = p.shared_pages[g];
     if (n < 0 || n > p.bt_stride) {
       flag_error(p.status, PA_DEV_ERR_LENGTH);
@@ -198,117 +204,155 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     s.first[g] = 0x7fffffff;
   }
   __syncthreads();
+#pragma unroll 1
   for (int g = tid; g < G; g += threads) {
     const int a = s.cu[g], b = s.cu[g + 1];
-    if (a < 0 || b < a || b > p.batch || b - a > p.max_group_rows) s.bad = 1;
+    if (a < 0 || b < a || b > B || b - a > p.max_group_rows) s.bad = 1;
   }
   __syncthreads();
   // groups that are not disjoint ranges of rows: no row shares anything
   const bool grouped = G > 0 && !s.bad;
   if (G > 0 && s.bad && tid == 0) flag_error(p.status, PA_DEV_ERR_LENGTH);
-  const int row_lo = grouped ? s.cu[0] : 0, row_hi = grouped ? s.cu[G] : 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int b = b0 + k;
-    group[k] = -1;
-    if (b >= b1) continue;
-    const int most = p.bt_stride * kPage;
-    if (len[k] < 0 || len[k] > most || len[k] > p.max_seq_len) flag_error(p.status, PA_DEV_ERR_LENGTH);
-    len[k] = min(max(len[k], 0), most);
-    if (b >= row_lo && b < row_hi) {
-      int lo = 0, hi = G;  // last g with cu[g] <= b (empty groups before it share its start)
+#pragma unroll 1
+  for (int b = tid; b < B; b += threads) {
+    int lo = -1, start = 0;
+    if (grouped && b >= s.cu[0]) {
+      int hi = G;
+      lo = 0;
+#pragma unroll 1
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s.cu[mid] <= b) lo = mid; else hi = mid;
       }
       // a row shorter than the shared pages reads its own keys alone
-      if (s.shared[lo] > 0 && len[k] >= s.shared[lo] * kPage) {
-        group[k] = lo;
+      if (b < s.cu[lo + 1] && s.shared[lo] > 0 && s.len[b] >= s.shared[lo] * kPage) {
+        start = s.shared[lo];
         atomicMin(&s.first[lo], b);
       }
     }
+    s.group[b] = lo;
+    s.start[b] = start;
   }
   __syncthreads();
-  // Segments: those of shared pages with many rows (a CTA never goes back to them from those with few),
-  // those with few, and the rows' own pages.
-  const int gper = (G + threads - 1) / threads;
-  const int g0 = min(G, tid * gper), g1 = min(G, g0 + gper);
+  // Segments, in this order: those of shared pages with many rows (a CTA never goes back to them from
+  // those with few); then by row the rows' own pages, a group's shared pages with few rows before its
+  // first row (short segments wait for memory more than they read, so they are spread over the slices).
+  const int gper = (G + threads - 1) / threads, g0 = min(G, tid * gper), g1 = min(G, g0 + gper);
+  const int per = (B + threads - 1) / threads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
   auto rows_of = [&](int g) { return grouped && s.first[g] != 0x7fffffff ? s.cu[g + 1] - s.cu[g] : 0; };
   auto few_of = [&](int rows) { return rows % kTileRows <= kFewRows ? rows % kTileRows : 0; };
-  long long at[3] = {0, 0, 0};
+  long long at[3] = {0, 0, 0};  // many, few, own
+#pragma unroll 1
   for (int g = g0; g < g1; ++g) {
     const int rows = rows_of(g), few = few_of(rows);
     const long long units = units_of(s.shared[g] * kPage), many = (rows - few + kTileRows - 1) / kTileRows;
     at[0] += many << 40 | many * units;
     if (few > 0) at[1] += 1ll << 40 | units;
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int units = units_of(len[k] - (group[k] >= 0 ? s.shared[group[k]] * kPage : 0));
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int units = units_of(s.len[b] - s.start[b] * kPage);
     if (units > 0) at[2] += 1ll << 40 | units;
   }
   plan_scan(s, at);
-  const int many_tiles = count_of(s.totals[0]), tiles = many_tiles + count_of(s.totals[1]);
-  const int many_units = units_in(s.totals[0]), tile_units = many_units + units_in(s.totals[1]);
-  const int segments = tiles + count_of(s.totals[2]), units_all = tile_units + units_in(s.totals[2]);
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    int seg = (pass == 0 ? 0 : many_tiles) + count_of(at[pass]), unit = (pass == 0 ? 0 : many_units) + units_in(at[pass]);
+  const int many_tiles = count_of(s.totals[0]), many_units = units_in(s.totals[0]);
+  const int segments = many_tiles + count_of(s.totals[1]) + count_of(s.totals[2]);
+  const int units_all = many_units + units_in(s.totals[1]) + units_in(s.totals[2]);
+  int few_seg = count_of(at[1]), few_unit = units_in(at[1]);
+  {
+    int seg = count_of(at[0]), unit = units_in(at[0]);
+#pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
-      const int begin = pass == 0 ? 0 : rows - few, end = pass == 0 ? rows - few : rows;
-      if (pass == 0) s.tile0[g] = seg; else s.few0[g] = seg;
-      for (int r = begin; r < end; r += kTileRows) {
-        p.segments[seg] = Segment{unit, units, s.cu[g] + r, min(kTileRows, end - r), s.first[g], 0, s.shared[g] * kPage, 0};
+      s.many_seg[g] = seg;
+      s.many_unit[g] = unit;
+#pragma unroll 1
+      for (int r = 0; r < rows - few; r += kTileRows) {
+        p.segments[seg] = Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
+                                  s.shared[g] * kPage, seg};
         s.unit[seg++] = unit;
         unit += units;
       }
+      s.few_seg[g] = few_seg;
+      s.few_unit[g] = few_unit;
+      if (few > 0) {
+        ++few_seg;
+        few_unit += units;
+      }
     }
   }
-  if (tid == 0) s.unit[segments] = units_all;
-  int seg = tiles + count_of(at[2]), unit = tile_units + units_in(at[2]);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int first = group[k] >= 0 ? s.shared[group[k]] * kPage : 0, units = units_of(len[k] - first);
-    if (b0 + k >= b1 || units <= 0) continue;
-    p.segments[seg] = Segment{unit, units, b0 + k, 1, b0 + k, first, len[k], 0};
-    s.unit[seg++] = unit;
-    unit += units;
+  {
+    int seg = count_of(at[2]), unit = units_in(at[2]);
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const int units = units_of(s.len[b] - s.start[b] * kPage);
+      s.own_seg[b] = seg;
+      s.own_unit[b] = unit;
+      if (units > 0) {
+        ++seg;
+        unit += units;
+      }
+    }
+    if (tid == 0) {
+      s.own_seg[B] = count_of(s.totals[2]);
+      s.own_unit[B] = units_in(s.totals[2]);
+      s.unit[segments] = units_all;
+    }
   }
   __syncthreads();
-  seg = tiles + count_of(at[2]);
-  unit = tile_units + units_in(at[2]);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int b = b0 + k, g = group[k];
-    if (b >= b1) continue;
-    const int first = g >= 0 ? s.shared[g] * kPage : 0;
+#pragma unroll 1
+  for (int g = tid; g < G; g += threads) {
+    const int rows = rows_of(g), few = few_of(rows);
+    if (few == 0) continue;
+    const int row = s.cu[g], seg = many_tiles + s.few_seg[g] + s.own_seg[row];
+    const int unit = many_units + s.few_unit[g] + s.own_unit[row];
+    p.segments[seg] = Segment{unit, units_of(s.shared[g] * kPage), row + rows - few, few, s.first[g], 0,
+                              s.shared[g] * kPage, many_tiles + s.few_seg[g]};
+    s.unit[seg] = unit;
+  }
+#pragma unroll 1
+  for (int b = tid; b < B; b += threads) {
+    const int g = s.group[b], start = s.start[b], units = units_of(s.len[b] - start * kPage);
     RowPlan r{0, 0, 0, 0, 0, 0, 0, 0};
+    int seg = many_tiles + s.own_seg[b], unit = many_units + s.own_unit[b];
     if (g >= 0) {
-      const int in_group = b - s.cu[g], rows = rows_of(g), few = few_of(rows);
-      r.tile = in_group < rows - few ? s.tile0[g] + in_group / kTileRows : s.few0[g];
-      r.tile_units = units_of(first);
-      r.tile_unit = s.unit[r.tile];
-      r.in_tile = in_group % kTileRows;
+      const int rows = rows_of(g), few = few_of(rows), in_group = b - s.cu[g];
+      seg += s.few_seg[g] + (few > 0 ? 1 : 0);
+      unit += s.few_unit[g] + (few > 0 ? units_of(s.shared[g] * kPage) : 0);
+      if (start > 0) {
+        const int place = in_group / kTileRows;
+        r.tile_units = units_of(start * kPage);
+        r.in_tile = in_group % kTileRows;
+        if (in_group < rows - few) {
+          r.tile = s.many_seg[g] + place;
+          r.tile_unit = s.many_unit[g] + place * r.tile_units;
+        } else {
+          r.tile = many_tiles + s.few_seg[g];
+          r.tile_unit = many_units + s.few_unit[g] + s.own_unit[s.cu[g]];
+        }
+      }
     }
-    const int units = units_of(len[k] - first);
     if (units > 0) {
-      r.own = seg++ - tiles;
+      r.own = s.own_seg[b];
       r.own_unit = unit;
       r.own_units = units;
-      unit += units;
+      p.segments[seg] = Segment{unit, units, b, 1, b, start * kPage, s.len[b], ~r.own};
+      s.unit[seg] = unit;
     }
     p.rows[b] = r;
   }
+  __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < p.slices; i += threads) {
     const int u0 = static_cast<int>(static_cast<long long>(units_all) * i / p.slices);
     const int u1 = static_cast<int>(static_cast<long long>(units_all) * (i + 1) / p.slices);
     int lo = 0, hi = max(segments, 1);  // last segment with a first unit <= u0
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s.unit[mid] <= u0) lo = mid; else hi = mid;
     }
-    p.slice[i] = Slice{u0, u1, lo, segments, tiles, units_all, {0, 0}};
+    p.slice[i] = Slice{u0, u1, lo, segments, units_all, {0, 0, 0}};
   }
 }
 
@@ -445,6 +489,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       g.table_row = __shfl_sync(0xffffffffu, lane_record.table_row, from);
       g.first_key = __shfl_sync(0xffffffffu, lane_record.first_key, from);
       g.end_key = __shfl_sync(0xffffffffu, lane_record.end_key, from);
+      g.index = __shfl_sync(0xffffffffu, lane_record.index, from);
       return g;
     };
     auto entries = [&](const Segment& g, int k) {
@@ -479,7 +524,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         q_used |= 1u << qb;
       }
       if (few) next_q = qb ^ 1;
-      const bool is_tile = seg < plan.tiles;
+      const bool is_tile = g.index >= 0;
       for (int kb = k0; kb < k1 && ok; kb += kBatch) {
         const int ahead = kb + kBatch < k1 ? entries(g, kb + kBatch) : 0;
         for (int k = kb; k < min(kb + kBatch, k1); ++k, ++it) {
@@ -501,7 +546,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
             UnitInfo& f = s.info[it % kInfos];
             const int cap = is_tile ? 2 * p.tile_rows : 2;
             const int64_t slot =
-                ((static_cast<int64_t>(slice) + (is_tile ? seg : seg - plan.tiles)) * p.hkv + head) * 2;
+                ((static_cast<int64_t>(slice) + (is_tile ? g.index : ~g.index)) * p.hkv + head) * 2;
             f.part = slot * cap * kRowFloats;
             f.stats = cap * kHeadDim;
             f.keys = keys;
