@@ -28,9 +28,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxK = 64;
 constexpr int kList = 1024;  // candidates of a piece that the quick selection holds
-// Pieces of a row: as many as give kTargetCtas CTAs in all, none of them below kMinPiece tokens.
-constexpr int kTargetCtas = 1216;
-constexpr int kMinPiece = 4096;
+constexpr int kFound = 512;  // candidates of a request that the quick ranking holds
+// Pieces of a row: as many as give kTargetCtas CTAs in all (three rounds of what the GPU holds, so that one
+// CTA's selection runs beside another's loads), none of them below four vectors a thread.
+constexpr int kTargetCtas = 2736;
+constexpr int kMinVectors = 4 * kThreads;
 
 struct BeamParams {
   const void* logits;
@@ -107,24 +109,53 @@ __device__ __forceinline__ uint4 no_logits() {
   return make_uint4(w, w, w, w);
 }
 
-// This thread's running maximum and sum of exponentials over n more logits, the first of them `token`;
-// `at` is the token of the first vector that held the maximum.
-template <int n>
-__device__ __forceinline__ void take(const float (&x)[n], int token, float& m, float& s, int& at) {
-  float top = x[0];
+// A thread's state over its logits: the largest, the token of the first vector that has it, and the sum of
+// exponentials against a reference that follows the largest at a distance (40 at most: sums stay below 2^77),
+// so that nothing is rescaled at every new maximum.
+struct Seen {
+  float top = -INFINITY, ref = -INFINITY, sum = 0.f;
+  int at = 0;
+
+  // n more logits x, the largest of them `most`, the first of them `token`.
+  template <int n>
+  __device__ __forceinline__ void take(const float (&x)[n], float most, int token) {
+    if (most > ref + 40.f) {
+      sum = ref == -INFINITY ? 0.f : sum * fast_exp2((ref - most) * kLog2e);
+      ref = most;
+    }
+    if (most > top) {
+      top = most;
+      at = token;
+    }
+    // (x - ref, then the factor: one rounding each, so no error that all terms share)
+    const float base = ref == -INFINITY ? 0.f : ref;
+    if (n == 1) {
+      sum += fast_exp2((x[0] - base) * kLog2e);
+      return;
+    }
+    const float2 minus = make_float2(-base, -base), log2e = make_float2(kLog2e, kLog2e);
+    float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 1; i < n; ++i) top = fmaxf(top, x[i]);
-  if (top > m) {
-    s *= fast_exp2((m - top) * kLog2e);
-    m = top;
-    at = token;
+    for (int i = 0; i + 1 < n; i += 2) {
+      const float2 e = mul2(add2(make_float2(x[i], x[i + 1]), minus), log2e);
+      part = add2(part, make_float2(fast_exp2(e.x), fast_exp2(e.y)));
+    }
+    sum += part.x + part.y;
   }
-  // (x - m, then the factor: one rounding each, so no error that all terms share)
-  const float base = m == -INFINITY ? 0.f : m;
-  float sum[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < n; ++i) sum[i & 1] += fast_exp2((x[i] - base) * kLog2e);
-  s += sum[0] + sum[1];
+};
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The largest logit of a vector (NaN where all are).
+__device__ __forceinline__ float most_of(uint4 w, const float (&)[8]) {
+  const uint32_t m = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
+  return fmaxf(bf16lo(m), bf16hi(m));
+}
+__device__ __forceinline__ float most_of(uint4, const float (&x)[4]) {
+  return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 }
 
 template <class T>
@@ -136,20 +167,20 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   const int row = static_cast<int>(blockIdx.x) / p.pieces, piece = static_cast<int>(blockIdx.x) % p.pieces;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) found = 0;
+  launch_next();
   await_previous();
   if (!expands(p, row)) return;
   const Row<T> r(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab);
   const uint4* body = reinterpret_cast<const uint4*>(r.base + r.head);
-  const int v0 = static_cast<int>(static_cast<int64_t>(r.vectors) * piece / p.pieces);
-  const int v1 = static_cast<int>(static_cast<int64_t>(r.vectors) * (piece + 1) / p.pieces);
+  const int per = (r.vectors + p.pieces - 1) / p.pieces;
+  const int v0 = min(r.vectors, piece * per), v1 = min(r.vectors, v0 + per);
   // the first piece has the single logits before the vectors, the last those after
   const int lead = piece == 0 ? r.head : 0, trail = piece == p.pieces - 1 ? r.tail : 0;
   const int trail_at = r.head + r.vectors * kVec;
-  float m = -INFINITY, s = 0.f;
-  int at = 0;
+  Seen seen;
   if (tid < lead) {
     const float x[1] = {single(r.base[tid])};
-    take(x, tid, m, s, at);
+    seen.take(x, x[0], tid);
   }
   for (int v = v0 + tid; v < v1; v += 4 * kThreads) {
     uint4 w[4];
@@ -159,17 +190,18 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
     for (int j = 0; j < 4; ++j) {
       float x[kVec];
       unpack(w[j], x);
-      take(x, r.head + (v + j * kThreads) * kVec, m, s, at);
+      seen.take(x, most_of(w[j], x), r.head + (v + j * kThreads) * kVec);
     }
   }
   if (tid < trail) {
     const float x[1] = {single(r.base[trail_at + tid])};
-    take(x, trail_at + tid, m, s, at);
+    seen.take(x, x[0], trail_at + tid);
   }
   // A bound that k logits at least reach: the q-th best thread of each warp that has vectors (q of them
   // make k), and of those the least. A thread's rank is its maximum and the first vector that has it:
   // each thread above the bound has a logit above all of any thread below.
-  const uint64_t mine = m > -INFINITY ? static_cast<uint64_t>(order_of(m)) << 32 | ~static_cast<uint32_t>(at) : 0ull;
+  const uint64_t mine =
+      seen.top > -INFINITY ? static_cast<uint64_t>(order_of(seen.top)) << 32 | ~static_cast<uint32_t>(seen.at) : 0ull;
   const int warps = min(kWarps, max(1, (v1 - v0 + 31) / 32));
   uint64_t bound = 0;
   if (warp < warps) {
@@ -180,10 +212,10 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
     }
   }
   // maximum and sum of the CTA
-  float wm = m;
+  float wm = seen.top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  float ws = m == wm ? s : s * fast_exp2((m - wm) * kLog2e);
+  float ws = seen.ref == wm ? seen.sum : seen.sum * fast_exp2((seen.ref - wm) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
   if (lane == 0) {
@@ -207,7 +239,9 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   // the vectors of each of its threads that may have one, a lane a vector (the second read of a small
   // part of the piece, from L2 mostly).
   const uint64_t reach = bound > 0 ? bound - (kVec - 1) : 1;
+  const float least = bound > 0 ? value_of(static_cast<uint32_t>(bound >> 32)) : -INFINITY;
   auto keep = [&](float x, int token) {
+    if (!(x >= least)) return;
     const uint64_t c = rank_of(x, token);
     if (c < reach) return;
     const int i = atomicAdd(&found, 1);
@@ -294,10 +328,13 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   __shared__ double shift[kMaxBeams];  // score minus normaliser of a beam
   __shared__ uint8_t kind[kMaxBeams];  // 0: no candidates, 1: its tokens, 2: itself (finished)
   __shared__ Candidate warp_best[kWarps];
+  __shared__ Candidate list[kFound];
+  __shared__ int found;
   extern __shared__ uint8_t used[];    // [beams][pieces] candidates taken
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = static_cast<int>(blockIdx.x), lists = p.beams * p.pieces;
   await_previous();
+  if (tid == 0) found = 0;
   for (int i = tid; i < lists; i += kThreads) used[i] = 0;
   for (int b = warp; b < p.beams; b += kWarps) {
     const int row = n * p.beams + b;
@@ -329,9 +366,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
   }
   __syncthreads();
-  // this thread's best among the heads of its lists
-  auto head = [&](int list) {
-    const int b = list / p.pieces, at = used[list];
+  auto entry = [&](int list, int at) {
+    const int b = list / p.pieces;
     Candidate c{0, 0};
     if (kind[b] == 1 && at < p.k) {
       const float2 e = p.best[(static_cast<int64_t>(n) * lists + list) * p.k + at];
@@ -346,19 +382,85 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
     return c;
   };
-  auto mine = [&](int& list) {
+  auto write = [&](int place, const Candidate& c) {
+    const int at = n * p.k + place;
+    if (c.score == 0) {
+      p.out_scores[at] = -INFINITY;
+      p.parents[at] = p.tokens[at] = -1;
+      p.live_out[at] = 0;
+      return;
+    }
+    const uint32_t index = ~c.place;
+    const int b = static_cast<int>(index / static_cast<uint32_t>(p.vocab));
+    const int token = kind[b] == 2 ? p.eos : static_cast<int>(index - static_cast<uint32_t>(b) * p.vocab);
+    p.out_scores[at] = static_cast<float>(double_of(c.score));
+    p.parents[at] = b;
+    p.tokens[at] = token;
+    p.live_out[at] = kind[b] == 1 && token != p.eos ? 1 : 0;
+  };
+  // A bound that k candidates at least reach, as in the first launch: from the best heads of each warp's
+  // lists (by score alone: equal ones all count). Candidates that reach it, in their lists' order, are ranked.
+  {
+    // (the lists go round the warps, so that every warp has some of each beam)
+    const int first = lane * kWarps + warp;
+    uint64_t best = 0;
+    for (int i = first; i < lists; i += kThreads) best = max(best, entry(i, 0).score);
+    const int warps = min(kWarps, lists);
+    uint64_t bound = 0;
+    if (warp < warps) {
+      uint64_t left = best;
+      for (int q = (p.k + warps - 1) / warps; q > 0; --q) {
+        bound = warp_max64(left);
+        // one thread of those that have it
+        const uint32_t same = __ballot_sync(0xffffffffu, left == bound);
+        if (lane == __ffs(same) - 1) left = 0;
+      }
+    }
+    if (lane == 0) warp_best[warp] = Candidate{bound, 0};
+    __syncthreads();
+    bound = warp_best[0].score;
+    for (int w = 1; w < warps; ++w) bound = min(bound, warp_best[w].score);
+    bound = max(bound, static_cast<uint64_t>(1));
+    if (best >= bound) {
+      for (int i = first; i < lists; i += kThreads) {
+        for (int at = 0; at < p.k; ++at) {
+          const Candidate c = entry(i, at);
+          if (c.score < bound) break;
+          const int to = atomicAdd(&found, 1);
+          if (to < kFound) list[to] = c;
+        }
+      }
+    }
+    __syncthreads();
+    const int m = found;
+    if (m <= kFound) {
+      for (int i = tid; i < max(m, p.k); i += kThreads) {
+        if (i >= m) {
+          write(i, Candidate{0, 0});
+          continue;
+        }
+        const Candidate c = list[i];
+        int place = 0;
+        for (int j = 0; j < m; ++j) place += better(list[j], c) ? 1 : 0;
+        if (place < p.k) write(place, c);
+      }
+      return;
+    }
+  }
+  // More than the list holds: one after the other, each thread with the heads of its lists.
+  auto mine = [&](int& from) {
     Candidate c{0, 0};
     for (int i = tid; i < lists; i += kThreads) {
-      const Candidate h = head(i);
+      const Candidate h = entry(i, used[i]);
       if (better(h, c)) {
         c = h;
-        list = i;
+        from = i;
       }
     }
     return c;
   };
-  int list = -1;
-  Candidate best = mine(list);
+  int from = -1;
+  Candidate best = mine(from);
   for (int k = 0; k < p.k; ++k) {
     Candidate c = best;
 #pragma unroll
@@ -374,29 +476,19 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     for (int w = 1; w < kWarps; ++w)
       if (better(warp_best[w], top)) top = warp_best[w];
     __syncthreads();
-    const int at = n * p.k + k;
     if (top.score == 0) {
-      if (tid == 0) {
-        p.out_scores[at] = -INFINITY;
-        p.parents[at] = p.tokens[at] = -1;
-        p.live_out[at] = 0;
-      }
+      if (tid == 0) write(k, top);
     } else if (best.score == top.score && best.place == top.place) {
-      const int b = list / p.pieces;
-      const int token = kind[b] == 2 ? p.eos : static_cast<int>(~top.place) - b * p.vocab;
-      p.out_scores[at] = static_cast<float>(double_of(top.score));
-      p.parents[at] = b;
-      p.tokens[at] = token;
-      p.live_out[at] = kind[b] == 1 && token != p.eos ? 1 : 0;
-      ++used[list];
-      best = mine(list);
+      write(k, top);
+      ++used[from];
+      best = mine(from);
     }
   }
 }
 
-int pieces_of(int32_t requests, int32_t beams, int32_t vocab) {
+int pieces_of(int32_t requests, int32_t beams, int32_t vocab, int32_t logits_type) {
   const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(requests) * beams);
-  const int64_t most = std::max<int64_t>(1, vocab / kMinPiece);
+  const int64_t most = std::max<int64_t>(1, vocab / (kMinVectors * (logits_type == PA_BF16 ? 8 : 4)));
   return static_cast<int>(std::min(most, std::max<int64_t>(1, kTargetCtas / rows)));
 }
 
@@ -415,7 +507,7 @@ bool beam_sizes_supported(int32_t requests, int32_t beams, int32_t vocab, int32_
 extern "C" size_t pa_beam_workspace_size(int32_t requests, int32_t beams, int32_t vocab, int32_t k) {
   using namespace pa;
   if (!beam_sizes_valid(requests, beams, vocab, k) || !beam_sizes_supported(requests, beams, vocab, k)) return 0;
-  const size_t lists = static_cast<size_t>(requests) * beams * pieces_of(requests, beams, vocab);
+  const size_t lists = static_cast<size_t>(requests) * beams * pieces_of(requests, beams, vocab, PA_FP32);  // (the most)
   return (lists * (k + 1) * sizeof(float2) + 255) / 256 * 256;
 }
 
@@ -440,7 +532,7 @@ extern "C" pa_status beam_select(const void* logits, int32_t logits_type, int64_
   if (workspace == nullptr || workspace_bytes < pa_beam_workspace_size(requests, beams, vocab, k))
     return PA_ERR_WORKSPACE_TOO_SMALL;
   if (reinterpret_cast<uintptr_t>(workspace) & 7u) return PA_ERR_INVALID_ARG;
-  const int pieces = pieces_of(requests, beams, vocab);
+  const int pieces = pieces_of(requests, beams, vocab, logits_type);
   const size_t lists = static_cast<size_t>(requests) * beams * pieces;
   float2* best = static_cast<float2*>(workspace);
   const BeamParams p{logits, row_stride, requests, beams, vocab, k, eos_token, pieces, scores, live, out_scores,
