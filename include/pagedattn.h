@@ -518,8 +518,9 @@ pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const void* k_po
  *               that has ended, 1 else: the new_lens of paged_step_plan when k is beams. Places without a
  *               candidate get -inf, -1, -1, 0. out_scores may be scores and live_out may be live where
  *               k = beams.
- * A beam with a NaN or +inf among its logits, or nothing but -inf, has no candidates. Scores of
- * different beams are compared in 64 bits over fp32 sums of exponentials (3e-7 absolute).
+ * A beam with a NaN or +inf among its logits, or nothing but -inf, has no candidates. Within a beam the
+ * order is that of its logits; scores of different beams are compared as pairs of floats (48 bits) over
+ * fp32 sums of exponentials (off by 3e-7).
  *   workspace   at least pa_beam_workspace_size(...) bytes, 8-byte aligned
  * ------------------------------------------------------------------------------------------ */
 #define PA_BF16 0

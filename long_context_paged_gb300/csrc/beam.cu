@@ -5,9 +5,9 @@
 // and the k best are kept, equal scores in the order of (b, v). Within a beam the order is that of the
 // logits themselves, whatever the beam's score and normaliser: so one pass over a beam's logits finds
 // both its normaliser (running maximum and sum) and its k largest logits, and only those few meet the
-// other beams' in a second launch. Scores are formed in 64 bits there: what decides between beams is
-// the normalisers' precision (fp32 sums of at most 2^14 terms, added up in fp64), not the rounding of
-// a sum of large parts.
+// other beams' in a second launch. Scores are formed as pairs of floats there (48 bits): what decides
+// between beams is the normalisers' precision (fp32 sums of exponentials), not the rounding of a sum
+// of large parts.
 //
 // The logits are read once from memory: bound by HBM for a full batch (64 x 8 rows of 151,936), by
 // latency for a single request. A row is cut into pieces so that a few rows still fill the GPU; a CTA
@@ -163,10 +163,11 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   constexpr int kVec = Row<T>::kVec;
   __shared__ uint64_t warp_best[kWarps], list[kList];
   __shared__ float2 warp_stats[kWarps];
-  __shared__ int found;
+  __shared__ int found, holding;
+  __shared__ uint8_t holders[kThreads];
   const int row = static_cast<int>(blockIdx.x) / p.pieces, piece = static_cast<int>(blockIdx.x) % p.pieces;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found = 0;
+  if (tid == 0) found = holding = 0;
   launch_next();
   await_previous();
   if (!expands(p, row)) return;
@@ -235,9 +236,9 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   }
   bound = warp_best[0];
   for (int w = 1; w < warps; ++w) bound = min(bound, warp_best[w]);
-  // Logits that reach the bound, those of its own vector included, go to a list: the warp looks through
-  // the vectors of each of its threads that may have one, a lane a vector (the second read of a small
-  // part of the piece, from L2 mostly).
+  // Logits that reach the bound, those of its own vector included, go to a list. Only threads whose own best
+  // reaches it can have one: they are listed, and all threads look through those threads' vectors (a second
+  // read of a small part of the piece, from L2 mostly).
   const uint64_t reach = bound > 0 ? bound - (kVec - 1) : 1;
   const float least = bound > 0 ? value_of(static_cast<uint32_t>(bound >> 32)) : -INFINITY;
   auto keep = [&](float x, int token) {
@@ -249,13 +250,16 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   };
   if (tid < lead) keep(single(r.base[tid]), tid);
   if (tid < trail) keep(single(r.base[trail_at + tid]), trail_at + tid);
-  for (uint32_t some = __ballot_sync(0xffffffffu, mine >= reach); some != 0; some &= some - 1) {
-    const int first = v0 + warp * 32 + __ffs(some) - 1;
-    for (int v = first + lane * kThreads; v < v1; v += 32 * kThreads) {
+  if (mine >= reach) holders[atomicAdd(&holding, 1)] = static_cast<uint8_t>(tid);
+  __syncthreads();
+  const int each = (v1 - v0 + kThreads - 1) / kThreads, looks = holding * each;
+  for (int i = tid; i < looks; i += kThreads) {
+    const int of = i / each, v = v0 + holders[of] + (i - of * each) * kThreads;
+    if (v < v1) {
       float x[kVec];
       unpack(body[v], x);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) keep(x[i], r.head + v * kVec + i);
+      for (int j = 0; j < kVec; ++j) keep(x[j], r.head + v * kVec + j);
     }
   }
   __syncthreads();
@@ -307,25 +311,44 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   }
 }
 
-// A candidate of a request: score in 64 bits as an integer of the same order, and its place.
+// Scores as a pair of floats whose sum they are, lo at most half a step of hi (48 bits: fp64 is 50 times
+// slower here, and took most of this launch).
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair exact_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return Pair{s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair add(Pair a, float b) {
+  const Pair s = exact_sum(a.hi, b);
+  return exact_sum(s.hi, s.lo + a.lo);
+}
+// ln x, of a normal x >= 2^-1 below 2^31: x = 2^e f with f in [3/4, 3/2), so that logf is off by half a step
+// of at most 0.41 (3e-8) and the rest is nearly exact; e times the high part of ln 2 (14 bits) is exact.
+__device__ __forceinline__ Pair natural_log(float x) {
+  const int e = (__float_as_int(x) - 0x3f400000) >> 23;
+  const float f = __int_as_float(__float_as_int(x) - (e << 23));
+  constexpr float kHigh = 11357.f / 16384.f, kLow = -2.9088971304691e-5f;  // ln 2
+  return exact_sum(e * kHigh, logf(f) + e * kLow);
+}
+// A pair as an integer of the same order; 0, below all, if it is -inf or NaN.
+__device__ __forceinline__ uint64_t order_of(Pair x) {
+  const uint32_t hi = order_of(x.hi);
+  return hi == 0 ? 0ull : static_cast<uint64_t>(hi) << 32 | order_of(x.lo);
+}
+
+// A candidate of a request: its score's order, and its place.
 struct Candidate {
   uint64_t score;
   uint32_t place;  // ~(beam * vocab + token): a lower place is a larger number
 };
-__device__ __forceinline__ uint64_t order_of(double x) {
-  if (!(x > -INFINITY)) return 0;
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x == 0.0 ? 0.0 : x));
-  return b >> 63 ? ~b : b | 1ull << 63;
-}
-__device__ __forceinline__ double double_of(uint64_t o) {
-  return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
-}
 __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
   return a.score > b.score || (a.score == b.score && a.place > b.place);
 }
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
-  __shared__ double shift[kMaxBeams];  // score minus normaliser of a beam
+  __shared__ Pair shift[kMaxBeams];    // score minus normaliser of a beam
   __shared__ uint8_t kind[kMaxBeams];  // 0: no candidates, 1: its tokens, 2: itself (finished)
   __shared__ Candidate warp_best[kWarps];
   __shared__ Candidate list[kFound];
@@ -342,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
       if (lane == 0) {
         const float s = p.scores[row];
         kind[b] = p.live != nullptr && p.live[row] == 0 && s > -INFINITY && s < INFINITY ? 2 : 0;
-        shift[b] = s;
+        shift[b] = Pair{s, 0.f};
       }
       continue;
     }
@@ -351,18 +374,27 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     for (int i = lane; i < p.pieces; i += 32) m = fmaxf(m, stats[i].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    double sum = 0.0;
+    Pair sum{0.f, 0.f};
     for (int i = lane; i < p.pieces; i += 32) {
       const float2 v = stats[i];
-      sum += v.x == m ? static_cast<double>(v.y) : static_cast<double>(v.y) * fast_exp2((v.x - m) * kLog2e);
+      sum = add(sum, v.x == m ? v.y : v.y * fast_exp2((v.x - m) * kLog2e));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, o), lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
+      // (lanes add the same two pairs in the same order)
+      sum = lane & o ? add(Pair{hi, lo + sum.lo}, sum.hi) : add(Pair{sum.hi, sum.lo + lo}, hi);
+    }
     if (lane == 0) {
-      const double norm = static_cast<double>(m) + log(sum);
       // (a NaN or +inf among the logits, or nothing but -inf: no candidates)
-      kind[b] = norm > -INFINITY && norm < INFINITY ? 1 : 0;
-      shift[b] = static_cast<double>(p.scores[row]) - norm;
+      const bool good = m > -INFINITY && m < INFINITY && sum.hi >= 0.5f && sum.hi < 2147483648.f;
+      kind[b] = good ? 1 : 0;
+      if (good) {
+        const Pair norm = natural_log(sum.hi);  // (sum.lo is below 2^-24 of it: ln moves by as much)
+        Pair s = exact_sum(p.scores[row], -m);
+        s = add(s, -norm.hi);
+        shift[b] = add(s, -(norm.lo + sum.lo / sum.hi));
+      }
     }
   }
   __syncthreads();
@@ -373,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
       const float2 e = p.best[(static_cast<int64_t>(n) * lists + list) * p.k + at];
       const int token = __float_as_int(e.y);
       if (token >= 0) {
-        c.score = order_of(shift[b] + static_cast<double>(e.x));
+        c.score = order_of(add(shift[b], e.x));
         c.place = ~static_cast<uint32_t>(b * p.vocab + token);
       }
     } else if (kind[b] == 2 && at == 0 && list == b * p.pieces) {
@@ -393,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     const uint32_t index = ~c.place;
     const int b = static_cast<int>(index / static_cast<uint32_t>(p.vocab));
     const int token = kind[b] == 2 ? p.eos : static_cast<int>(index - static_cast<uint32_t>(b) * p.vocab);
-    p.out_scores[at] = static_cast<float>(double_of(c.score));
+    p.out_scores[at] = value_of(static_cast<uint32_t>(c.score >> 32));
     p.parents[at] = b;
     p.tokens[at] = token;
     p.live_out[at] = kind[b] == 1 && token != p.eos ? 1 : 0;
