@@ -109,34 +109,29 @@ __device__ __forceinline__ uint4 no_logits() {
   return make_uint4(w, w, w, w);
 }
 
-// A thread's state over its logits: the largest, the token of the first vector that has it, and the sum of
-// exponentials against a reference that follows the largest at a distance (40 at most: sums stay below 2^77),
-// so that nothing is rescaled at every new maximum.
+// A thread's state over its logits: the largest, and the sum of exponentials against a reference that
+// follows the largest at a distance (40 at most: sums stay below 2^77), so that nothing is rescaled at
+// every new maximum.
 struct Seen {
   float top = -INFINITY, ref = -INFINITY, sum = 0.f;
-  int at = 0;
 
-  // n more logits x, the largest of them `most`, the first of them `token`.
-  template <int n>
-  __device__ __forceinline__ void take(const float (&x)[n], float most, int token) {
+  // The largest of the next logits.
+  __device__ __forceinline__ void reach(float most) {
     if (most > ref + 40.f) {
       sum = ref == -INFINITY ? 0.f : sum * fast_exp2((ref - most) * kLog2e);
       ref = most;
     }
-    if (most > top) {
-      top = most;
-      at = token;
-    }
-    // (x - ref, then the factor: one rounding each, so no error that all terms share)
-    const float base = ref == -INFINITY ? 0.f : ref;
-    if (n == 1) {
-      sum += fast_exp2((x[0] - base) * kLog2e);
-      return;
-    }
-    const float2 minus = make_float2(-base, -base), log2e = make_float2(kLog2e, kLog2e);
+    top = fmaxf(top, most);
+  }
+  // Those logits. (x - ref, then the factor: one rounding each, so no error that all terms share.)
+  __device__ __forceinline__ void take(float x) { sum += fast_exp2((x - (ref == -INFINITY ? 0.f : ref)) * kLog2e); }
+  template <int n>
+  __device__ __forceinline__ void take(const float (&x)[n]) {
+    const float base = ref == -INFINITY ? 0.f : -ref;
+    const float2 minus = make_float2(base, base), log2e = make_float2(kLog2e, kLog2e);
     float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i + 1 < n; i += 2) {
+    for (int i = 0; i < n; i += 2) {
       const float2 e = mul2(add2(make_float2(x[i], x[i + 1]), minus), log2e);
       part = add2(part, make_float2(fast_exp2(e.x), fast_exp2(e.y)));
     }
@@ -149,19 +144,29 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// The largest logit of a vector (NaN where all are).
-__device__ __forceinline__ float most_of(uint4 w, const float (&)[8]) {
-  const uint32_t m = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
-  return fmaxf(bf16lo(m), bf16hi(m));
+// The largest logit of four vectors.
+__device__ __forceinline__ float most_of(const uint4 (&w)[4], uint16_t) {
+  uint32_t m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = max_bf16x2(max_bf16x2(w[j].x, w[j].y), max_bf16x2(w[j].z, w[j].w));
+  const uint32_t all = max_bf16x2(max_bf16x2(m[0], m[1]), max_bf16x2(m[2], m[3]));
+  return fmaxf(bf16lo(all), bf16hi(all));
 }
-__device__ __forceinline__ float most_of(uint4, const float (&x)[4]) {
-  return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+__device__ __forceinline__ float most_of(const uint4 (&w)[4], float) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m = fmax3(m, __uint_as_float(w[j].x), __uint_as_float(w[j].y));
+    m = fmax3(m, __uint_as_float(w[j].z), __uint_as_float(w[j].w));
+  }
+  return m;
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
   constexpr int kVec = Row<T>::kVec;
   __shared__ uint64_t warp_best[kWarps], list[kList];
+  __shared__ uint32_t warp_bound[kWarps];
   __shared__ float2 warp_stats[kWarps];
   __shared__ int found, holding;
   __shared__ uint8_t holders[kThreads];
@@ -180,36 +185,37 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   const int trail_at = r.head + r.vectors * kVec;
   Seen seen;
   if (tid < lead) {
-    const float x[1] = {single(r.base[tid])};
-    seen.take(x, x[0], tid);
+    const float x = single(r.base[tid]);
+    seen.reach(x);
+    seen.take(x);
   }
   for (int v = v0 + tid; v < v1; v += 4 * kThreads) {
     uint4 w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = v + j * kThreads < v1 ? body[v + j * kThreads] : no_logits<T>();
+    seen.reach(most_of(w, T()));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float x[kVec];
       unpack(w[j], x);
-      seen.take(x, most_of(w[j], x), r.head + (v + j * kThreads) * kVec);
+      seen.take(x);
     }
   }
   if (tid < trail) {
-    const float x[1] = {single(r.base[trail_at + tid])};
-    seen.take(x, x[0], trail_at + tid);
+    const float x = single(r.base[trail_at + tid]);
+    seen.reach(x);
+    seen.take(x);
   }
   // A bound that k logits at least reach: the q-th best thread of each warp that has vectors (q of them
-  // make k), and of those the least. A thread's rank is its maximum and the first vector that has it:
-  // each thread above the bound has a logit above all of any thread below.
-  const uint64_t mine =
-      seen.top > -INFINITY ? static_cast<uint64_t>(order_of(seen.top)) << 32 | ~static_cast<uint32_t>(seen.at) : 0ull;
+  // make k; a thread counts by its largest logit), and of those the least.
+  const uint32_t mine = order_of(seen.top);
   const int warps = min(kWarps, max(1, (v1 - v0 + 31) / 32));
-  uint64_t bound = 0;
+  uint32_t bound = 0;
   if (warp < warps) {
-    uint64_t left = mine;
+    uint32_t left = mine;
     for (int q = (p.k + warps - 1) / warps; q > 0; --q) {
-      bound = warp_max64(left);
-      if (left == bound) left = 0;
+      bound = __reduce_max_sync(0xffffffffu, left);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
     }
   }
   // maximum and sum of the CTA
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
   if (lane == 0) {
     warp_stats[warp] = make_float2(wm, ws);
-    warp_best[warp] = bound;
+    warp_bound[warp] = bound;
   }
   __syncthreads();
   const int64_t out = static_cast<int64_t>(row) * p.pieces + piece;
@@ -234,23 +240,21 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
       cs += warp_stats[w].x == cm ? warp_stats[w].y : warp_stats[w].y * fast_exp2((warp_stats[w].x - cm) * kLog2e);
     p.stats[out] = make_float2(cm, cs);
   }
-  bound = warp_best[0];
-  for (int w = 1; w < warps; ++w) bound = min(bound, warp_best[w]);
-  // Logits that reach the bound, those of its own vector included, go to a list. Only threads whose own best
-  // reaches it can have one: they are listed, and all threads look through those threads' vectors (a second
-  // read of a small part of the piece, from L2 mostly).
-  const uint64_t reach = bound > 0 ? bound - (kVec - 1) : 1;
-  const float least = bound > 0 ? value_of(static_cast<uint32_t>(bound >> 32)) : -INFINITY;
+  bound = warp_bound[0];
+  for (int w = 1; w < warps; ++w) bound = min(bound, warp_bound[w]);
+  // Logits that reach the bound go to a list. Only threads whose own largest reaches it have one: they are
+  // listed, and all threads look through those threads' vectors (a second read of a small part of the
+  // piece, from L2 mostly).
+  const float least = bound > 0 ? value_of(bound) : -INFINITY;
+  const bool holds = mine > 0 && mine >= bound;
   auto keep = [&](float x, int token) {
-    if (!(x >= least)) return;
-    const uint64_t c = rank_of(x, token);
-    if (c < reach) return;
+    if (!(x >= least) || x == -INFINITY) return;
     const int i = atomicAdd(&found, 1);
-    if (i < kList) list[i] = c;
+    if (i < kList) list[i] = rank_of(x, token);
   };
   if (tid < lead) keep(single(r.base[tid]), tid);
   if (tid < trail) keep(single(r.base[trail_at + tid]), trail_at + tid);
-  if (mine >= reach) holders[atomicAdd(&holding, 1)] = static_cast<uint8_t>(tid);
+  if (holds) holders[atomicAdd(&holding, 1)] = static_cast<uint8_t>(tid);
   __syncthreads();
   const int each = (v1 - v0 + kThreads - 1) / kThreads, looks = holding * each;
   for (int i = tid; i < looks; i += kThreads) {
@@ -273,6 +277,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
       }
       const uint64_t c = list[i];
       int place = 0;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) place += list[j] > c ? 1 : 0;
       if (place < p.k)
         p.best[out * p.k + place] = make_float2(value_of(static_cast<uint32_t>(c >> 32)),
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
       const uint64_t c = rank_of(x, token);
       if (c < top) best = max(best, c);
     };
-    if (mine >= reach || lead > 0 || trail > 0) {
+    if (holds || lead > 0 || trail > 0) {
       if (tid < lead) look(single(r.base[tid]), tid);
       if (tid < trail) look(single(r.base[trail_at + tid]), trail_at + tid);
       for (int v = v0 + tid; v < v1; v += kThreads) {
@@ -473,6 +478,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
         }
         const Candidate c = list[i];
         int place = 0;
+#pragma unroll 8
         for (int j = 0; j < m; ++j) place += better(list[j], c) ? 1 : 0;
         if (place < p.k) write(place, c);
       }
