@@ -349,7 +349,7 @@ struct Candidate {
   uint32_t place;  // ~(beam * vocab + token): a lower place is a larger number
 };
 __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
-  return a.score > b.score || (a.score == b.score && a.place > b.place);
+  return (a.score > b.score) | ((a.score == b.score) & (a.place > b.place));  // (no branches)
 }
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
@@ -366,6 +366,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   for (int i = tid; i < lists; i += kThreads) used[i] = 0;
   for (int b = warp; b < p.beams; b += kWarps) {
     const int row = n * p.beams + b;
+    const float2* stats = p.stats + static_cast<int64_t>(row) * p.pieces;
+    // (read beside the score and the flag; of a row that is not expanded it is whatever was there)
+    const float2 mine = lane < p.pieces ? stats[lane] : make_float2(-INFINITY, 0.f);
     if (!expands(p, row)) {
       if (lane == 0) {
         const float s = p.scores[row];
@@ -374,13 +377,12 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
       }
       continue;
     }
-    const float2* stats = p.stats + static_cast<int64_t>(row) * p.pieces;
-    float m = -INFINITY;
-    for (int i = lane; i < p.pieces; i += 32) m = fmaxf(m, stats[i].x);
+    float m = mine.x;
+    for (int i = 32 + lane; i < p.pieces; i += 32) m = fmaxf(m, stats[i].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    Pair sum{0.f, 0.f};
-    for (int i = lane; i < p.pieces; i += 32) {
+    Pair sum{mine.x == m ? mine.y : mine.y * fast_exp2((mine.x - m) * kLog2e), 0.f};
+    for (int i = 32 + lane; i < p.pieces; i += 32) {
       const float2 v = stats[i];
       sum = add(sum, v.x == m ? v.y : v.y * fast_exp2((v.x - m) * kLog2e));
     }
@@ -403,16 +405,21 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
   }
   __syncthreads();
+  const float2* entries = p.best + static_cast<int64_t>(n) * lists * p.k;
+  auto candidate = [&](int b, float2 e) {
+    Candidate c{0, 0};
+    const int token = __float_as_int(e.y);
+    if (token >= 0) {
+      c.score = order_of(add(shift[b], e.x));
+      c.place = ~static_cast<uint32_t>(b * p.vocab + token);
+    }
+    return c;
+  };
   auto entry = [&](int list, int at) {
     const int b = list / p.pieces;
     Candidate c{0, 0};
     if (kind[b] == 1 && at < p.k) {
-      const float2 e = p.best[(static_cast<int64_t>(n) * lists + list) * p.k + at];
-      const int token = __float_as_int(e.y);
-      if (token >= 0) {
-        c.score = order_of(add(shift[b], e.x));
-        c.place = ~static_cast<uint32_t>(b * p.vocab + token);
-      }
+      c = candidate(b, entries[static_cast<int64_t>(list) * p.k + at]);
     } else if (kind[b] == 2 && at == 0 && list == b * p.pieces) {
       c.score = order_of(shift[b]);
       c.place = ~static_cast<uint32_t>(b * p.vocab + max(p.eos, 0));
@@ -460,11 +467,26 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     bound = max(bound, static_cast<uint64_t>(1));
     if (best >= bound) {
       for (int i = first; i < lists; i += kThreads) {
-        for (int at = 0; at < p.k; ++at) {
-          const Candidate c = entry(i, at);
-          if (c.score < bound) break;
+        const int b = i / p.pieces;
+        auto keep = [&](const Candidate& c) {
+          if (c.score < bound) return false;
           const int to = atomicAdd(&found, 1);
           if (to < kFound) list[to] = c;
+          return true;
+        };
+        if (kind[b] != 1) {
+          keep(entry(i, 0));
+          continue;
+        }
+        // four entries' loads at a time
+        const float2* e = entries + static_cast<int64_t>(i) * p.k;
+        bool more = true;
+        for (int at = 0; at < p.k && more; at += 4) {
+          float2 v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = at + j < p.k ? e[at + j] : make_float2(0.f, __int_as_float(-1));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) more = more && keep(candidate(b, v[j]));
         }
       }
     }
