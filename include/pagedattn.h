@@ -512,7 +512,7 @@ pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const void* k_po
  *               NaN has no candidates (-inf: a beam that is not in use, the others of the first step)
  *   live        int32 [requests][beams] or NULL (all live): a beam with 0 has ended; its one candidate
  *               is itself, with its score and the token eos_token; its logits are not read
- *   k           1 .. 64;  beams <= 64;  beams * vocab < 2^31;  requests * beams <= 2^20
+ *   k           1 .. 64;  beams <= 64;  beams * vocab < 2^31;  requests * beams <= 65,535
  *   eos_token   in [0, vocab), or -1: no token ends a beam
  *   out_scores  fp32, parents (b), tokens (v), live_out int32: [requests][k]. live_out is 0 for a beam
  *               that has ended, 1 else: the new_lens of paged_step_plan when k is beams. Places without a

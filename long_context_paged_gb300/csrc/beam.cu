@@ -27,6 +27,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxK = 64;
+constexpr int kMaxRows = 65535;
 constexpr int kList = 1024;  // candidates of a piece that the quick selection holds
 constexpr int kFound = 512;  // candidates of a request that the quick ranking holds
 // Pieces of a row: as many as give kTargetCtas CTAs in all (three rounds of what the GPU holds, so that one
@@ -144,7 +145,14 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// The largest logit of four vectors.
+// The largest logit of a vector, and of four.
+__device__ __forceinline__ float most_of(uint4 w, uint16_t) {
+  const uint32_t m = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
+  return fmaxf(bf16lo(m), bf16hi(m));
+}
+__device__ __forceinline__ float most_of(uint4 w, float) {
+  return fmax3(__uint_as_float(w.x), __uint_as_float(w.y), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
 __device__ __forceinline__ float most_of(const uint4 (&w)[4], uint16_t) {
   uint32_t m[4];
 #pragma unroll
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   __shared__ float2 warp_stats[kWarps];
   __shared__ int found, holding;
   __shared__ uint8_t holders[kThreads];
-  const int row = static_cast<int>(blockIdx.x) / p.pieces, piece = static_cast<int>(blockIdx.x) % p.pieces;
+  const int row = static_cast<int>(blockIdx.y), piece = static_cast<int>(blockIdx.x);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) found = holding = 0;
   launch_next();
@@ -259,12 +267,13 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   const int each = (v1 - v0 + kThreads - 1) / kThreads, looks = holding * each;
   for (int i = tid; i < looks; i += kThreads) {
     const int of = i / each, v = v0 + holders[of] + (i - of * each) * kThreads;
-    if (v < v1) {
-      float x[kVec];
-      unpack(body[v], x);
+    if (v >= v1) continue;
+    const uint4 w = body[v];
+    if (!(most_of(w, T()) >= least)) continue;  // most vectors
+    float x[kVec];
+    unpack(w, x);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) keep(x[j], r.head + v * kVec + j);
-    }
+    for (int j = 0; j < kVec; ++j) keep(x[j], r.head + v * kVec + j);
   }
   __syncthreads();
   const int n = found;
@@ -558,7 +567,7 @@ bool beam_sizes_valid(int32_t requests, int32_t beams, int32_t vocab, int32_t k)
 
 bool beam_sizes_supported(int32_t requests, int32_t beams, int32_t vocab, int32_t k) {
   return beams <= kMaxBeams && k <= kMaxK && static_cast<int64_t>(beams) * vocab < (1ll << 31) &&
-         static_cast<int64_t>(requests) * beams <= (1 << 20);
+         static_cast<int64_t>(requests) * beams <= kMaxRows;
 }
 
 }  // namespace
@@ -580,8 +589,8 @@ extern "C" pa_status beam_select(const void* logits, int32_t logits_type, int64_
       (logits_type != PA_BF16 && logits_type != PA_FP32))
     return PA_ERR_INVALID_ARG;
   if (!beam_sizes_supported(requests, beams, vocab, k)) {
-    snprintf_error("beam_select: at most %d beams of a request, %d candidates, 2^31 tokens of all its beams and 2^20 rows",
-                   kMaxBeams, kMaxK);
+    snprintf_error("beam_select: at most %d beams of a request, %d candidates, 2^31 tokens of all its beams and %d rows",
+                   kMaxBeams, kMaxK, kMaxRows);
     return PA_ERR_UNSUPPORTED;
   }
   // in place: a request's results replace its own inputs only if there are as many
@@ -598,7 +607,7 @@ extern "C" pa_status beam_select(const void* logits, int32_t logits_type, int64_
   const BeamParams p{logits, row_stride, requests, beams, vocab, k, eos_token, pieces, scores, live, out_scores,
                      parents, tokens, live_out, best, best + lists * k};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(lists);
+  const dim3 grid(static_cast<unsigned>(pieces), static_cast<unsigned>(requests * beams));
   cudaError_t e = logits_type == PA_BF16 ? launch_dependent(beam_rows_kernel<uint16_t>, grid, kThreads, 0, st, 0, p)
                                          : launch_dependent(beam_rows_kernel<float>, grid, kThreads, 0, st, 0, p);
   if (e == cudaSuccess)

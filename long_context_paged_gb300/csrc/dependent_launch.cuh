@@ -10,10 +10,10 @@ namespace pa {
 // against plain launches, calls in a row: 31 rotary rows 4.1 -> 3.1 us, 4,127 17.3 -> 15.1, a plan of
 // 32 requests 8.2 -> 5.4, one of 4,096 10.3 -> 8.8. (A kernel that in turn lets the next one start early gained nothing more.)
 template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
                              cudaStream_t stream, int cluster, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
