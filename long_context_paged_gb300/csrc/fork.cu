@@ -52,7 +52,7 @@ struct ForkParams {
   int32_t* status;
   int32_t blocks, span;  // page blocks per group, and pages in each (a multiple of kThreads)
   // workspace
-  int32_t* freed;    // [groups][blocks] pages that a block gives back
+  int32_t* freed;    // [groups][blocks] pages that a block gives back; -1: nothing in it changes
   int32_t* differ;   // [groups][blocks] its first page that the rows do not have in common
   int32_t* copied;   // [groups] copies; -1: the group's parents or lengths are not valid
   int32_t* copy_of;  // [rows] the page that the row's last page is copied from, or -1
@@ -65,38 +65,40 @@ struct ForkParams {
 struct Group {
   int32_t parent[kMaxBeams];  // -1: the row becomes empty
   int32_t old_len[kMaxBeams], len[kMaxBeams];
-  uint64_t has_child;         // rows that some child continues
-  uint64_t live;              // children that are not empty
-  int32_t max_pages;          // of the old rows
-  int32_t bad;
+  uint32_t has_child[2];      // rows that some child continues
+  uint32_t live[2];           // children that are not empty
+  int32_t max_pages[2];       // of the old rows, by half
 };
 
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
+__device__ __forceinline__ bool bit(const uint32_t (&m)[2], int i) { return m[i >> 5] >> (i & 31) & 1; }
 
-// One warp's worth of threads would do; every thread of the CTA takes part in the barriers.
-__device__ __forceinline__ void read_group(const ForkParams& p, const int32_t* lens, int g, Group& s) {
+// The group from this thread's row of it (rows are the first threads'); false if a parent or a length is
+// not valid. Every thread of the CTA takes part.
+__device__ __forceinline__ bool make_group(const ForkParams& p, int parent, int len, Group& s) {
   const int W = p.beams, t = threadIdx.x;
-  if (t == 0) {
-    s.has_child = s.live = 0;
-    s.max_pages = s.bad = 0;
-  }
-  __syncthreads();
-  if (t < W) {
-    const int parent = p.parents[g * W + t], len = lens[g * W + t];
-    if (parent < -1 || parent >= W || len < 0 || len > p.bt_stride * kPage) s.bad = 1;
+  const bool mine = t < W;
+  if (mine) {
     s.parent[t] = parent;
     s.old_len[t] = len;
-    if (len > 0) atomicMax(&s.max_pages, pages_of(min(len, p.bt_stride * kPage)));
+  }
+  const bool bad = mine && (parent < -1 || parent >= W || len < 0 || len > p.bt_stride * kPage);
+  if (__syncthreads_or(bad)) return false;
+  if (t < 64) {
+    bool child = false;
+    for (int b = 0; b < W; ++b) child |= mine && s.parent[b] == t;
+    const int now = mine && parent >= 0 ? s.old_len[parent] : 0;
+    if (mine) s.len[t] = now;
+    const uint32_t children = __ballot_sync(0xffffffffu, child), live = __ballot_sync(0xffffffffu, now > 0);
+    const int pages = __reduce_max_sync(0xffffffffu, mine ? pages_of(len) : 0);
+    if ((t & 31) == 0) {
+      s.has_child[t >> 5] = children;
+      s.live[t >> 5] = live;
+      s.max_pages[t >> 5] = pages;
+    }
   }
   __syncthreads();
-  if (t < W && !s.bad) {
-    const int parent = s.parent[t];
-    s.len[t] = parent < 0 ? 0 : s.old_len[parent];
-    if (parent >= 0)
-      atomicOr(reinterpret_cast<unsigned long long*>(&s.has_child), 1ull << parent);
-    if (s.len[t] > 0) atomicOr(reinterpret_cast<unsigned long long*>(&s.live), 1ull << t);
-  }
-  __syncthreads();
+  return true;
 }
 
 // Logical page j of the group's rows, read into this thread's column of `col`.
@@ -106,178 +108,208 @@ __device__ __forceinline__ void read_column(const ForkParams& p, const int32_t* 
     col[r * kThreads] = j < p.bt_stride ? rows[static_cast<int64_t>(r) * p.bt_stride + j] : -1;
 }
 
-// Whether row r, which has no child, gives back its page j: a page of the pool that no row with a
-// child holds, and no earlier row.
+// Whether row r, which has no child, gives back its page j: a page that no row with a child holds, and no
+// earlier row. (It may lie outside the pool: it is then flagged and goes nowhere.)
 __device__ __forceinline__ bool gives_back(const ForkParams& p, const Group& s, const int32_t* col, int j, int r) {
-  if (s.has_child >> r & 1 || j >= pages_of(s.old_len[r])) return false;
+  if (bit(s.has_child, r) || j >= pages_of(s.old_len[r])) return false;
   const int32_t e = col[r * kThreads];
-  if (e < 0 || e >= p.num_pages) return false;
+  if (e < 0) return false;
   for (int o = 0; o < p.beams; ++o)
-    if (o != r && (o < r || s.has_child >> o & 1) && col[o * kThreads] == e && j < pages_of(s.old_len[o])) return false;
+    if (o != r && (o < r || bit(s.has_child, o)) && col[o * kThreads] == e && j < pages_of(s.old_len[o])) return false;
   return true;
 }
 
-// Whether all rows in use have page j in common, filled.
-__device__ __forceinline__ bool common(const ForkParams& p, const Group& s, const int32_t* col, int j) {
+// What page j of the group's rows comes to: whether the rows in use have it in common, filled; whether some
+// entry changes (a partly filled last page may be copied).
+__device__ __forceinline__ void look(const ForkParams& p, const Group& s, const int32_t* col, int j, bool& common,
+                                     bool& changes) {
   int32_t one = -1;
-  for (uint64_t m = s.live; m != 0; m &= m - 1) {
-    const int b = __ffsll(static_cast<long long>(m)) - 1;
+  common = true;
+  changes = false;
+  for (int b = 0; b < p.beams; ++b) {
+    const int len = s.len[b], pages = pages_of(len), mine = col[b * kThreads];
+    const bool held = j < pages_of(s.old_len[b]);
+    if (len == 0) {
+      changes |= held;
+      continue;
+    }
     const int32_t e = col[s.parent[b] * kThreads];
     if (one < 0) one = e;
-    if (e < 0 || e != one || j >= s.len[b] / kPage) return false;
+    common &= e >= 0 && e == one && j < len / kPage;
+    changes |= j < pages ? e != mine || (len % kPage != 0 && j == len / kPage) : held;
   }
-  return one >= 0;
+  common &= one >= 0;
 }
 
-__device__ __forceinline__ int block_sum(int v, int32_t* scratch) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int sum = 0;
+// Sums of n values over the CTA.
+template <int n>
+__device__ __forceinline__ void block_sums(int (&v)[n], int32_t (*scratch)[kWarps]) {
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += scratch[w];
+  for (int k = 0; k < n; ++k) {
+    v[k] = __reduce_add_sync(0xffffffffu, v[k]);
+    if ((threadIdx.x & 31) == 0) scratch[k][threadIdx.x >> 5] = v[k];
+  }
   __syncthreads();
-  return sum;
+#pragma unroll
+  for (int k = 0; k < n; ++k) {
+    v[k] = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v[k] += scratch[k][w];
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) fork_count_kernel(const ForkParams p) {
   extern __shared__ int32_t columns[];  // [beams][kThreads]
   __shared__ Group s;
-  __shared__ int32_t scratch[kWarps], first;
+  __shared__ int32_t scratch[3][kWarps], first;
   const int tid = threadIdx.x, W = p.beams;
-  const int g = static_cast<int>(blockIdx.x) / p.blocks, block = static_cast<int>(blockIdx.x) % p.blocks;
+  const int g = static_cast<int>(blockIdx.y), block = static_cast<int>(blockIdx.x), at = g * p.blocks + block;
+  int32_t* col = columns + tid;
+  int32_t* rows = p.block_table + static_cast<int64_t>(g) * W * p.bt_stride;
+  const int j0 = block * p.span;
+  if (tid == 0) first = kNone;
+  launch_next();
   await_previous();
+  // everything that does not depend on anything is asked for first
+  const int i = g * W + tid;
+  const int parent = tid < W ? p.parents[i] : 0, len = tid < W ? p.seq_lens[i] : 0;
+  int count = block == 0 ? *p.free_count : 0;
+  read_column(p, rows, j0 + tid, col);
   // the end of the free list, from which copies take their pages, and the lengths: both may be
   // overwritten by the second launch
-  int count = *p.free_count;
-  if (count < 0 || count > p.free_capacity) {
-    if (blockIdx.x == 0 && tid == 0) flag_error(p.status, PA_DEV_ERR_LENGTH);
-    count = count < 0 ? 0 : p.free_capacity;
-  }
-  if (blockIdx.x == 0 && tid == 0) *p.count = count;
-  if (block == 0 && tid < W) {
-    const int i = g * W + tid;
-    p.old_lens[i] = p.seq_lens[i];
-    p.tail[i] = i < count ? p.free_pages[count - 1 - i] : -1;
-  }
-  if (tid == 0) first = kNone;
-  read_group(p, p.seq_lens, g, s);
-  int32_t* col = columns + tid;
-  const int32_t* rows = p.block_table + static_cast<int64_t>(g) * W * p.bt_stride;
-  int freed = 0;
-  const int j0 = block * p.span;
-  if (!s.bad) {
-    for (int j = j0 + tid; j < min(j0 + p.span, s.max_pages); j += kThreads) {
-      read_column(p, rows, j, col);
-      for (int r = 0; r < W; ++r) {
-        if (gives_back(p, s, col, j, r)) ++freed;
-        if (col[r * kThreads] >= p.num_pages && !(s.has_child >> r & 1) && j < pages_of(s.old_len[r]))
-          flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
-      }
-      if (!common(p, s, col, j)) atomicMin(&first, j);
+  if (block == 0) {
+    if (count < 0 || count > p.free_capacity) {
+      if (g == 0 && tid == 0) flag_error(p.status, PA_DEV_ERR_LENGTH);
+      count = count < 0 ? 0 : p.free_capacity;
+    }
+    if (g == 0 && tid == 0) *p.count = count;
+    if (tid < W) {
+      p.old_lens[i] = len;
+      p.tail[i] = i < count ? p.free_pages[count - 1 - i] : -1;
     }
   }
-  freed = block_sum(freed, scratch);
-  if (tid == 0) {
-    p.freed[blockIdx.x] = freed;
-    p.differ[blockIdx.x] = first;
-  }
-  if (block != 0) return;
-  // the children whose last page is copied: partly filled, and held by another child that comes
-  // first or has it filled
+  const bool good = make_group(p, parent, len, s);
+  int sums[3] = {0, 0, 0};  // pages given back, entries that change, copies
   int32_t from = -1;
-  if (tid < W) {
-    if (!s.bad && s.len[tid] % kPage != 0) {
+  if (good) {
+    const int end = min(j0 + p.span, max(s.max_pages[0], s.max_pages[1]));
+    for (int j = j0 + tid; j < end; j += kThreads) {
+      if (j >= j0 + kThreads) read_column(p, rows, j, col);
+      bool common, changes;
+      look(p, s, col, j, common, changes);
+      if (!common) atomicMin(&first, j);
+      if (!changes) continue;
+      sums[1] = 1;
+      for (int r = 0; r < W; ++r) {
+        if (!gives_back(p, s, col, j, r)) continue;
+        if (col[r * kThreads] < p.num_pages) ++sums[0];
+        else flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
+      }
+    }
+    // the children whose last page is copied: partly filled, and held by another child that comes
+    // first or has it filled
+    if (block == 0 && tid < W && s.len[tid] % kPage != 0) {
       const int last = s.len[tid] / kPage;
       const int32_t e = rows[static_cast<int64_t>(s.parent[tid]) * p.bt_stride + last];
       if (e < 0 || e >= p.num_pages) {
         flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
       } else {
+#pragma unroll 4
         for (int b = 0; b < W; ++b)
           if (b != tid && last < pages_of(s.len[b]) && (b < tid || s.len[b] >= (last + 1) * kPage) &&
               rows[static_cast<int64_t>(s.parent[b]) * p.bt_stride + last] == e)
             from = e;
       }
     }
-    p.copy_of[g * W + tid] = from;
   }
-  const int copied = block_sum(from >= 0 ? 1 : 0, scratch);
-  if (tid == 0) p.copied[g] = s.bad ? -1 : copied;
+  if (block == 0 && tid < W) p.copy_of[i] = from;
+  sums[2] = from >= 0 ? 1 : 0;
+  block_sums(sums, scratch);
+  if (tid == 0) {
+    p.freed[at] = sums[1] != 0 ? sums[0] : -1;
+    p.differ[at] = first;
+    if (block == 0) p.copied[g] = good ? sums[2] : -1;
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkParams p) {
   extern __shared__ int32_t columns[];
   __shared__ Group s;
-  __shared__ int32_t scratch[kWarps], fresh[kMaxBeams], warp_freed[kWarps];
+  __shared__ int32_t scratch[5][kWarps], fresh[kMaxBeams], warp_freed[kWarps], differs[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = p.beams;
-  const int g = static_cast<int>(blockIdx.x) / p.blocks, block = static_cast<int>(blockIdx.x) % p.blocks;
+  const int g = static_cast<int>(blockIdx.y), block = static_cast<int>(blockIdx.x), at = g * p.blocks + block;
+  int32_t* rows = p.block_table + static_cast<int64_t>(g) * W * p.bt_stride;
+  int32_t* col = columns + tid;
+  const int j0 = block * p.span, i = g * W + tid;
   await_previous();
+  const bool still = p.freed[at] < 0;  // nothing in this block changes
+  if (block != 0 && still) return;
+  const int parent = tid < W ? p.parents[i] : 0, len = tid < W ? p.old_lens[i] : 0;
+  const int from = tid < W ? p.copy_of[i] : -1, count = *p.count;
   // counts before this block, and of all
-  int before = 0, freed = 0, copies_before = 0, copies = 0, bad = 0;
-  for (int i = tid; i < p.groups * p.blocks; i += kThreads) {
-    const int n = p.freed[i];
-    freed += n;
-    if (i < static_cast<int>(blockIdx.x)) before += n;
+  int sums[5] = {0, 0, 0, 0, 0};  // given back: before, all; copies: before, all; groups that are not valid
+  for (int k = tid; k < p.groups * p.blocks; k += kThreads) {
+    const int n = max(p.freed[k], 0);
+    sums[1] += n;
+    if (k < at) sums[0] += n;
   }
-  for (int i = tid; i < p.groups; i += kThreads) {
-    const int n = p.copied[i];
-    if (n < 0) bad = 1;
-    copies += max(n, 0);
-    if (i < g) copies_before += max(n, 0);
+  for (int k = tid; k < p.groups; k += kThreads) {
+    const int n = p.copied[k];
+    if (n < 0) sums[4] = 1;
+    sums[3] += max(n, 0);
+    if (k < g) sums[2] += max(n, 0);
   }
-  before = block_sum(before, scratch);
-  freed = block_sum(freed, scratch);
-  copies_before = block_sum(copies_before, scratch);
-  copies = block_sum(copies, scratch);
-  bad = block_sum(bad, scratch);
-  const int count = *p.count;
-  const bool short_of = copies > count;
+  int differ = kNone;
+  if (block == 0)
+    for (int k = tid; k < p.blocks; k += kThreads) differ = min(differ, p.differ[g * p.blocks + k]);
+  block_sums(sums, scratch);
+  const int before = sums[0], freed = sums[1], copies_before = sums[2], copies = sums[3];
+  const bool bad = sums[4] != 0, short_of = copies > count;
   const bool full = static_cast<int64_t>(count) - copies + freed > p.free_capacity;
-  if (blockIdx.x == 0 && tid == 0) {
+  if (at == 0 && tid == 0) {
     if (bad || full) flag_error(p.status, PA_DEV_ERR_LENGTH);
     if (short_of) flag_error(p.status, PA_DEV_ERR_NO_PAGES);
     *p.free_count_out = bad || full || short_of ? count : count - copies + freed;
   }
   if (bad || full || short_of) {  // nothing changes
     if (block == 0 && tid < W) {
-      const int i = g * W + tid;
-      p.seq_lens_out[i] = p.old_lens[i];
+      p.seq_lens_out[i] = len;
       p.copies[3 * i] = p.copies[3 * i + 1] = -1;
       p.copies[3 * i + 2] = 0;
     }
     if (block == 0 && tid == 0) p.shared_pages[g] = 0;
     return;
   }
-  read_group(p, p.old_lens, g, s);
   // the pages that the group's copies get: the list's last ones, in row order
-  if (tid < W) {
-    int i = copies_before;
-    for (int b = 0; b < tid; ++b) i += p.copy_of[g * W + b] >= 0 ? 1 : 0;
-    fresh[tid] = p.copy_of[g * W + tid] >= 0 ? p.tail[i] : kNone;
+  if (tid < W) fresh[tid] = from;
+  make_group(p, parent, len, s);
+  int32_t page = kNone;
+  if (tid < W && from >= 0) {
+    int k = copies_before;
+    for (int b = 0; b < tid; ++b) k += fresh[b] >= 0 ? 1 : 0;
+    page = p.tail[k];
   }
   __syncthreads();
-  int32_t* rows = p.block_table + static_cast<int64_t>(g) * W * p.bt_stride;
-  int32_t* col = columns + tid;
+  if (tid < W) fresh[tid] = page;
   if (block == 0) {
-    int differ = kNone;
-    for (int i = tid; i < p.blocks; i += kThreads) differ = min(differ, p.differ[g * p.blocks + i]);
     if (tid < W && s.len[tid] > 0) differ = min(differ, s.len[tid] / kPage);
     differ = __reduce_min_sync(0xffffffffu, differ);
-    if (lane == 0) scratch[warp] = differ;
-    __syncthreads();
+    if (lane == 0) differs[warp] = differ;
+  }
+  __syncthreads();
+  if (block == 0) {
     if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) differ = min(differ, scratch[w]);
-      p.shared_pages[g] = s.live == 0 ? 0 : differ;
+      for (int w = 1; w < kWarps; ++w) differ = min(differ, differs[w]);
+      p.shared_pages[g] = (s.live[0] | s.live[1]) == 0 ? 0 : differ;
     }
     if (tid < W) {
-      const int i = g * W + tid, page = fresh[tid];
       p.seq_lens_out[i] = s.len[tid];
       int32_t src = -1, dst = -1, n = 0;
       if (page != kNone) {
         if (page < 0 || page >= p.num_pages) {
           flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
         } else {
-          src = p.copy_of[i];
+          src = from;
           dst = page;
           n = s.len[tid] % kPage;
         }
@@ -286,15 +318,19 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkParams p
       p.copies[3 * i + 1] = dst;
       p.copies[3 * i + 2] = n;
     }
+    if (still) return;
   }
-  int at = count - copies + before;
-  const int j0 = block * p.span, j1 = min(j0 + p.span, s.max_pages);
+  int to0 = count - copies + before;
+  const int j1 = min(j0 + p.span, max(s.max_pages[0], s.max_pages[1]));
   for (int jb = j0; jb < j1; jb += kThreads) {
     const int j = jb + tid;
     int n = 0;
+    bool common, changes = false;
     if (j < j1) {
       read_column(p, rows, j, col);
-      for (int r = 0; r < W; ++r) n += gives_back(p, s, col, j, r) ? 1 : 0;
+      look(p, s, col, j, common, changes);
+      if (changes)
+        for (int r = 0; r < W; ++r) n += col[r * kThreads] < p.num_pages && gives_back(p, s, col, j, r) ? 1 : 0;
     }
     // places of the pages given back: by page, then row
     int incl = n;
@@ -305,27 +341,27 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkParams p
     }
     if (lane == 31) warp_freed[warp] = incl;
     __syncthreads();
-    int to = at + incl - n;
+    int to = to0 + incl - n;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) to += warp_freed[w];
-      at += warp_freed[w];
+      to0 += warp_freed[w];
     }
     __syncthreads();
-    if (j < j1) {
-      for (int r = 0; n > 0 && r < W; ++r)
-        if (gives_back(p, s, col, j, r)) {
-          p.free_pages[to++] = col[r * kThreads];
-          --n;
-        }
-      for (int b = 0; b < W; ++b) {
-        const int32_t e = col[b * kThreads];
-        int32_t now = e;
-        if (j < pages_of(s.len[b]))
-          now = fresh[b] != kNone && j == s.len[b] / kPage ? fresh[b] : col[s.parent[b] * kThreads];
-        else if (j < pages_of(s.old_len[b]))
-          now = -1;
-        if (now != e) rows[static_cast<int64_t>(b) * p.bt_stride + j] = now;
+    if (!changes) continue;
+    for (int r = 0; n > 0 && r < W; ++r)
+      if (col[r * kThreads] < p.num_pages && gives_back(p, s, col, j, r)) {
+        p.free_pages[to++] = col[r * kThreads];
+        --n;
       }
+    for (int b = 0; b < W; ++b) {
+      const int32_t e = col[b * kThreads];
+      int32_t now = e;
+      if (j < pages_of(s.len[b]))
+        now = fresh[b] != kNone && j == s.len[b] / kPage ? fresh[b] : col[s.parent[b] * kThreads];
+      else if (j < pages_of(s.old_len[b]))
+        now = -1;
+      if (now != e) rows[static_cast<int64_t>(b) * p.bt_stride + j] = now;
     }
   }
 }
@@ -447,7 +483,7 @@ extern "C" pa_status paged_fork(const int32_t* parents, const int32_t* seq_lens,
   const ForkParams p{parents, seq_lens, groups, beams, block_table, bt_stride, free_pages, free_capacity, free_count,
                      num_pages, free_count_out, seq_lens_out, copies, shared_pages, status, l.blocks, l.span,
                      w + l.freed, w + l.differ, w + l.copied, w + l.copy_of, w + l.old_lens, w + l.tail, w + l.count};
-  const unsigned grid = static_cast<unsigned>(groups) * static_cast<unsigned>(l.blocks);
+  const dim3 grid(static_cast<unsigned>(l.blocks), static_cast<unsigned>(groups));  // (groups <= kMaxRows)
   const size_t smem = static_cast<size_t>(beams) * kThreads * sizeof(int32_t);
   cudaError_t e = launch_dependent(fork_count_kernel, grid, kThreads, smem, st, 0, p);
   if (e == cudaSuccess) e = launch_dependent(fork_apply_kernel, grid, kThreads, smem, st, 0, p);
