@@ -65,6 +65,7 @@ struct ForkParams {
 struct Group {
   int32_t parent[kMaxBeams];  // -1: the row becomes empty
   int32_t old_len[kMaxBeams], len[kMaxBeams];
+  int32_t old_pages[kMaxBeams], pages[kMaxBeams];
   uint32_t has_child[2];      // rows that some child continues
   uint32_t live[2];           // children that are not empty
   int32_t max_pages[2];       // of the old rows, by half
@@ -88,7 +89,11 @@ __device__ __forceinline__ bool make_group(const ForkParams& p, int parent, int 
     bool child = false;
     for (int b = 0; b < W; ++b) child |= mine && s.parent[b] == t;
     const int now = mine && parent >= 0 ? s.old_len[parent] : 0;
-    if (mine) s.len[t] = now;
+    if (mine) {
+      s.len[t] = now;
+      s.old_pages[t] = pages_of(len);
+      s.pages[t] = pages_of(now);
+    }
     const uint32_t children = __ballot_sync(0xffffffffu, child), live = __ballot_sync(0xffffffffu, now > 0);
     const int pages = __reduce_max_sync(0xffffffffu, mine ? pages_of(len) : 0);
     if ((t & 31) == 0) {
@@ -108,37 +113,82 @@ __device__ __forceinline__ void read_column(const ForkParams& p, const int32_t* 
     col[r * kThreads] = j < p.bt_stride ? rows[static_cast<int64_t>(r) * p.bt_stride + j] : -1;
 }
 
-// Whether row r, which has no child, gives back its page j: a page that no row with a child holds, and no
-// earlier row. (It may lie outside the pool: it is then flagged and goes nowhere.)
-__device__ __forceinline__ bool gives_back(const ForkParams& p, const Group& s, const int32_t* col, int j, int r) {
-  if (bit(s.has_child, r) || j >= pages_of(s.old_len[r])) return false;
-  const int32_t e = col[r * kThreads];
-  if (e < 0) return false;
-  for (int o = 0; o < p.beams; ++o)
-    if (o != r && (o < r || bit(s.has_child, o)) && col[o * kThreads] == e && j < pages_of(s.old_len[o])) return false;
-  return true;
+// What logical page j of the group's rows comes to.
+struct Verdict {
+  uint64_t gives;  // rows without children that give their page back: no row with a child holds it, and no
+                   // earlier row (it may lie outside the pool: it is then flagged and goes nowhere)
+  bool common;     // the rows in use have it in common, filled
+  bool changes;    // some entry may change (a partly filled last page may be copied)
+};
+
+// Up to 8 rows, unrolled: entries in registers, one round of shared-memory reads, pairs as bits. (The loops
+// below took 5 us for 8 rows, one read waiting for the other.)
+constexpr int kFewBeams = 8;
+
+__device__ __forceinline__ Verdict judge_few(const ForkParams& p, const Group& s, const int32_t* col, int j) {
+  int32_t e[kFewBeams], now[kFewBeams];
+  uint32_t held = 0, holds = 0, live = 0, same = 0;  // holds: after the fork; same: the entry stays
+  bool common = true;
+#pragma unroll
+  for (int b = 0; b < kFewBeams; ++b) {
+    const bool mine = b < p.beams;
+    e[b] = mine ? col[b * kThreads] : -1;
+    now[b] = mine ? col[max(s.parent[b], 0) * kThreads] : -1;
+    if (mine && j < s.old_pages[b]) held |= 1u << b;
+    if (mine && j < s.pages[b]) holds |= 1u << b;
+    if (mine && s.len[b] > 0) live |= 1u << b;
+    if (mine && j < s.len[b] / kPage && now[b] >= 0) same |= 1u << b;  // (filled, for now)
+  }
+  common = live != 0 && (same & live) == live;
+  const int32_t one = live != 0 ? __ffs(live) - 1 : 0;
+  int32_t first = -1;
+#pragma unroll
+  for (int b = 0; b < kFewBeams; ++b)
+    if (b == one) first = now[b];
+  uint32_t moved = held ^ holds, gives = 0;
+#pragma unroll
+  for (int b = 0; b < kFewBeams; ++b) {
+    common &= !(live >> b & 1) || now[b] == first;
+    // filled entries that stay do not change; a partly filled one may be copied
+    if ((holds >> b & 1) && (e[b] != now[b] || !(j < s.len[b] / kPage))) moved |= 1u << b;
+    uint32_t equal = 0;
+#pragma unroll
+    for (int o = 0; o < kFewBeams; ++o)
+      if (o != b && e[o] == e[b]) equal |= 1u << o;
+    if ((held >> b & 1) && e[b] >= 0 && (equal & held & (s.has_child[0] | ((1u << b) - 1u))) == 0) gives |= 1u << b;
+  }
+  return Verdict{gives & ~s.has_child[0], common, moved != 0};
 }
 
-// What page j of the group's rows comes to: whether the rows in use have it in common, filled; whether some
-// entry changes (a partly filled last page may be copied).
-__device__ __forceinline__ void look(const ForkParams& p, const Group& s, const int32_t* col, int j, bool& common,
-                                     bool& changes) {
+__device__ __forceinline__ Verdict judge_many(const ForkParams& p, const Group& s, const int32_t* col, int j) {
+  Verdict v{0, true, false};
   int32_t one = -1;
-  common = true;
-  changes = false;
   for (int b = 0; b < p.beams; ++b) {
-    const int len = s.len[b], pages = pages_of(len), mine = col[b * kThreads];
-    const bool held = j < pages_of(s.old_len[b]);
+    const int len = s.len[b];
+    const bool held = j < s.old_pages[b];
     if (len == 0) {
-      changes |= held;
+      v.changes |= held;
       continue;
     }
     const int32_t e = col[s.parent[b] * kThreads];
     if (one < 0) one = e;
-    common &= e >= 0 && e == one && j < len / kPage;
-    changes |= j < pages ? e != mine || (len % kPage != 0 && j == len / kPage) : held;
+    v.common &= e >= 0 && e == one && j < len / kPage;
+    v.changes |= j < s.pages[b] ? e != col[b * kThreads] || j >= len / kPage : held;
   }
-  common &= one >= 0;
+  v.common &= one >= 0;
+  for (int r = 0; v.changes && r < p.beams; ++r) {
+    const int32_t e = col[r * kThreads];
+    if (bit(s.has_child, r) || j >= s.old_pages[r] || e < 0) continue;
+    bool kept = false;
+    for (int o = 0; o < p.beams && !kept; ++o)
+      kept = o != r && (o < r || bit(s.has_child, o)) && col[o * kThreads] == e && j < s.old_pages[o];
+    if (!kept) v.gives |= 1ull << r;
+  }
+  return v;
+}
+
+__device__ __forceinline__ Verdict judge(const ForkParams& p, const Group& s, const int32_t* col, int j) {
+  return p.beams <= kFewBeams ? judge_few(p, s, col, j) : judge_many(p, s, col, j);
 }
 
 // Sums of n values over the CTA.
@@ -195,14 +245,12 @@ __global__ void __launch_bounds__(kThreads) fork_count_kernel(const ForkParams p
     const int end = min(j0 + p.span, max(s.max_pages[0], s.max_pages[1]));
     for (int j = j0 + tid; j < end; j += kThreads) {
       if (j >= j0 + kThreads) read_column(p, rows, j, col);
-      bool common, changes;
-      look(p, s, col, j, common, changes);
-      if (!common) atomicMin(&first, j);
-      if (!changes) continue;
+      const Verdict v = judge(p, s, col, j);
+      if (!v.common) atomicMin(&first, j);
+      if (!v.changes) continue;
       sums[1] = 1;
-      for (int r = 0; r < W; ++r) {
-        if (!gives_back(p, s, col, j, r)) continue;
-        if (col[r * kThreads] < p.num_pages) ++sums[0];
+      for (uint64_t m = v.gives; m != 0; m &= m - 1) {
+        if (col[(__ffsll(static_cast<long long>(m)) - 1) * kThreads] < p.num_pages) ++sums[0];
         else flag_error(p.status, PA_DEV_ERR_PAGE_OOB);
       }
     }
@@ -325,12 +373,16 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkParams p
   for (int jb = j0; jb < j1; jb += kThreads) {
     const int j = jb + tid;
     int n = 0;
-    bool common, changes = false;
+    Verdict v{0, true, false};
     if (j < j1) {
       read_column(p, rows, j, col);
-      look(p, s, col, j, common, changes);
-      if (changes)
-        for (int r = 0; r < W; ++r) n += col[r * kThreads] < p.num_pages && gives_back(p, s, col, j, r) ? 1 : 0;
+      v = judge(p, s, col, j);
+      if (!v.changes) v.gives = 0;
+      for (uint64_t m = v.gives; m != 0; m &= m - 1) {
+        const int r = __ffsll(static_cast<long long>(m)) - 1;
+        if (col[r * kThreads] < p.num_pages) ++n;
+        else v.gives &= ~(1ull << r);
+      }
     }
     // places of the pages given back: by page, then row
     int incl = n;
@@ -348,18 +400,16 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkParams p
       to0 += warp_freed[w];
     }
     __syncthreads();
-    if (!changes) continue;
-    for (int r = 0; n > 0 && r < W; ++r)
-      if (col[r * kThreads] < p.num_pages && gives_back(p, s, col, j, r)) {
-        p.free_pages[to++] = col[r * kThreads];
-        --n;
-      }
+    if (!v.changes) continue;
+    for (uint64_t m = v.gives; m != 0; m &= m - 1)
+      p.free_pages[to++] = col[(__ffsll(static_cast<long long>(m)) - 1) * kThreads];
+#pragma unroll 8
     for (int b = 0; b < W; ++b) {
       const int32_t e = col[b * kThreads];
       int32_t now = e;
-      if (j < pages_of(s.len[b]))
+      if (j < s.pages[b])
         now = fresh[b] != kNone && j == s.len[b] / kPage ? fresh[b] : col[s.parent[b] * kThreads];
-      else if (j < pages_of(s.old_len[b]))
+      else if (j < s.old_pages[b])
         now = -1;
       if (now != e) rows[static_cast<int64_t>(b) * p.bt_stride + j] = now;
     }
