@@ -478,8 +478,9 @@ pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t interleaved,
  *                  cu_group_rows that are not ascending within [0, batch], are flagged
  *                  PA_DEV_ERR_LENGTH and no row shares anything.
  *   batch <= 4096, groups <= 4096; max_seq_len <= 131072, a longer sequence is flagged
- *   PA_DEV_ERR_LENGTH (and cut to bt_stride * 16); softmax_scale as attn_prefill_chunk; q, pools and out 16-byte
- *   aligned. Weights are rounded to bf16 before they meet V, as the prefill does.
+ *   PA_DEV_ERR_LENGTH (and cut where it passes bt_stride * 16 or 131,072 keys); softmax_scale as
+ *   attn_prefill_chunk; q, pools and out 16-byte aligned. Weights are rounded to bf16 before they meet V,
+ *   as the prefill does.
  *   workspace      at least pa_decode_shared_workspace_size(...) bytes, 256-byte aligned; calls that
  *                  share one must not overlap on the GPU.
  * A row without keys gets o = 0, lse = -inf; so does a row whose scores are all -inf. NaN and
@@ -521,7 +522,8 @@ pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const void* k_po
  * A beam with a NaN or +inf among its logits, or nothing but -inf, has no candidates. Within a beam the
  * order is that of its logits; scores of different beams are compared as pairs of floats (48 bits) over
  * fp32 sums of exponentials (off by 3e-7).
- *   workspace   at least pa_beam_workspace_size(...) bytes, 8-byte aligned
+ *   workspace   at least pa_beam_workspace_size(...) bytes, 8-byte aligned; calls that share one must not
+ *               overlap on the GPU
  * ------------------------------------------------------------------------------------------ */
 #define PA_BF16 0
 #define PA_FP32 1
@@ -562,7 +564,8 @@ pa_status beam_select(const void* logits, int32_t logits_type, int64_t row_strid
  *   block_table   int32 [groups * beams][bt_stride], in place
  *   free_pages, free_capacity, free_count, free_count_out   as paged_release
  *   copies        int32 [groups * beams][3];  shared_pages int32 [groups]
- *   workspace     at least pa_fork_workspace_size(...) bytes, 4-byte aligned
+ *   workspace     at least pa_fork_workspace_size(...) bytes, 4-byte aligned; calls that share one must not
+ *                 overlap on the GPU
  * parents = 0 in all rows of a group whose first row holds a prompt hands it to every beam; parents =
  * -1 gives all the group's pages back (paged_release is for pages held by one row).
  *

@@ -67,6 +67,7 @@ static_assert(kWeightsAt + 2 * kFewQBytes <= 2 * kQBlockBytes, "the small buffer
 constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroups = 4096;
+constexpr int kMaxKeys = 131072;  // of a sequence: units are counted in 32 bits
 constexpr int kMaxSegments = kMaxBatch + kMaxGroups + kMaxBatch / kTileRows;
 constexpr int kMaxSlices = 256;   // CTAs per KV head
 // Registers of a softmax thread and of the others; 256 x 208 + 128 x 88 = 384 x 168, what the CTA is
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
     int len = p.seq_lens[b];
-    const int most = p.bt_stride * kPage;
+    const int most = min(p.bt_stride * kPage, kMaxKeys);
     if (len < 0 || len > most || len > p.max_seq_len) flag_error(p.status, PA_DEV_ERR_LENGTH);
     s.len[b] = min(max(len, 0), most);
   }
@@ -415,6 +416,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   SharedSmem& s = *reinterpret_cast<SharedSmem*>(smem_raw);
   const int head = static_cast<int>(blockIdx.x) % p.hkv, slice = static_cast<int>(blockIdx.x) / p.hkv;
   if ((smem_addr(smem_raw) & 1023u) != 0) {  // not the layout this kernel was built for
+    await_previous();
     if (threadIdx.x == 0) flag_error(p.status, PA_DEV_ERR_INTERNAL);
     return;
   }
@@ -1192,7 +1194,7 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   using namespace pa;
   if (!gqa_dims_supported(dims)) return PA_ERR_UNSUPPORTED;
   if (!shared_sizes_valid(batch, groups, max_group_rows) || num_pages <= 0 || bt_stride <= 0 ||
-      bt_stride > 0x7fffffff / kPage || max_seq_len < 0 || max_seq_len > 131072 ||
+      bt_stride > 0x7fffffff / kPage || max_seq_len < 0 || max_seq_len > kMaxKeys ||
       !(softmax_scale > 0.f && softmax_scale < 1e30f))
     return PA_ERR_INVALID_ARG;
   if (batch > kMaxBatch || groups > kMaxGroups) {

@@ -218,6 +218,60 @@ def test_streams_graphs_and_workspaces(cuda_lib):
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_rows_before_the_first_group_and_between(cuda_lib):
+    x = Inputs([(3, [50, 60, 48]), (12, [200] * 20)], [33, 150], seed=11)
+    x.table, x.lens = np.roll(x.table, 2, 0), x.lens[-2:] + x.lens[:-2]
+    x.q = x.q.roll(2, 0).contiguous()
+    x.cu = x.cu + 2
+    x.check(cuda_lib)
+    # a group that vouches for nothing, between two that do
+    y = Inputs([(3, [50, 60, 48]), (0, [20, 100]), (4, [64, 77])], seed=12)
+    y.check(cuda_lib)
+    y.cu, y.shared = [0, 3, 3, 5, 5, 7], [3, 2, 0, 9, 4]   # empty groups among them
+    y.check(cuda_lib)
+
+
+def test_calls_side_by_side(cuda_lib):
+    """Two streams at once, each call with scratch of its own."""
+    xs = [Inputs([(40, [700, 650, 777])], [100], seed=s) for s in (1, 2)]
+    want = [x.check(cuda_lib) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    args = [(x.q, x.k, x.v, dev(x.table), dev(x.lens), dev(x.cu), dev(x.shared), max(x.lens), SCALE) for x in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for st, a in zip(streams, args):
+            got.append(cuda_lib.attn_decode_paged_shared(*a, max_group_rows=3, stream=st))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_a_table_past_2_gib_of_entries_and_far_pages(cuda_lib):
+    """A row's entries and a page's keys at offsets past 32 bits."""
+    x = Inputs([(2, [40, 50])], [20], hkv=8, seed=13)
+    stride = 1 << 27
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    table = torch.zeros(3, stride, dtype=torch.int32, device="cuda")      # row 2 starts at 2^30 bytes
+    table[:, :x.table.shape[1]] = dev(x.table)
+    far = 70_000                                                          # 2.3 GB into the pool
+    k = torch.zeros(far + x.pages, 16, 8, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    k[far:], v[far:] = x.k, x.v
+    table[table > 0] += far
+    zero = [(r, j) for r in range(3) for j in range(x.table.shape[1]) if x.table[r, j] == 0]
+    for r, j in zero:
+        table[r, j] = far
+    table[table < 0] = -1
+    with pytest.raises(cuda_lib.PagedAttnError):                          # (a stride the lengths' type does not hold)
+        cuda_lib.attn_decode_paged_shared(x.q, k, v, table, dev(x.lens), dev(x.cu), dev(x.shared), 64, SCALE)
+    table = table[:, :stride - 64].contiguous()
+    out, lse = cuda_lib.attn_decode_paged_shared(x.q, k, v, table, dev(x.lens), dev(x.cu), dev(x.shared), 64, SCALE)
+    torch.cuda.synchronize()
+    x.close(out, lse)
+
+
 def test_the_same_bits_every_time(cuda_lib):
     x = Inputs([(40, [700 + 5 * i for i in range(9)]), (3, [60] * 4)], [300], seed=6)
     first = x.call(cuda_lib)
