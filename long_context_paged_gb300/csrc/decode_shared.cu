@@ -68,7 +68,6 @@ constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may 
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroups = 4096;
 constexpr int kMaxKeys = 131072;  // of a sequence: units are counted in 32 bits
-constexpr int kMaxSegments = kMaxBatch + kMaxGroups + kMaxBatch / kTileRows;
 constexpr int kMaxSlices = 256;   // CTAs per KV head
 // Registers of a softmax thread and of the others; 256 x 208 + 128 x 88 = 384 x 168, what the CTA is
 // launched with (checked on the host).
@@ -124,21 +123,29 @@ struct SharedParams {
 // ---------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;  // at most: four rows a thread
 
+template <int kGroups, int kRows>
 struct PlanSmem {
   long long warp_sums[3][kPlanThreads / 32];
   long long totals[3];
   int32_t bad;
+  Slice own;  // of the CTA (a plan made by every CTA)
   // groups: first row, shared pages, first row that uses them; segments and units before the group's of
   // many rows, and before its one of few
-  int32_t cu[kMaxGroups + 1], shared[kMaxGroups], first[kMaxGroups];
-  int32_t many_seg[kMaxGroups], many_unit[kMaxGroups], few_seg[kMaxGroups], few_unit[kMaxGroups];
+  int32_t cu[kGroups + 1], shared[kGroups], first[kGroups];
+  int32_t many_seg[kGroups], many_unit[kGroups], few_seg[kGroups], few_unit[kGroups];
   // rows: keys, last group that starts at or before the row (-1: none), pages that it shares; segments
   // and units of own pages before the row's
-  int32_t len[kMaxBatch], group[kMaxBatch], start[kMaxBatch];
-  int32_t own_seg[kMaxBatch + 1], own_unit[kMaxBatch + 1];
-  int32_t unit[kMaxSegments + 1];  // first unit of each segment
+  int32_t len[kRows], group[kRows], start[kRows];
+  int32_t own_seg[kRows + 1], own_unit[kRows + 1];
+  int32_t unit[kGroups + kRows + kRows / kTileRows + 1];  // first unit of each segment
 };
-static_assert(sizeof(PlanSmem) <= 232448, "shared memory over the 227 KB limit");
+using PlanOfAll = PlanSmem<kMaxGroups, kMaxBatch>;
+static_assert(sizeof(PlanOfAll) <= 232448, "shared memory over the 227 KB limit");
+
+// Calls of few rows per group and no more segments than this are planned by every CTA for itself, which takes
+// it 2 us of a launch's 4 (a plan kernel and the wait for it), and keeps the segments in shared memory.
+constexpr int kOwnPlanSegments = 512;
+using PlanOfFew = PlanSmem<kOwnPlanSegments, kOwnPlanSegments>;
 
 __device__ __forceinline__ long long warp_scan_sum(long long v, int lane) {
 #pragma unroll
@@ -150,7 +157,8 @@ __device__ __forceinline__ long long warp_scan_sum(long long v, int lane) {
 }
 
 // Exclusive prefix sums over the CTA of three packed (count << 40 | units), and their totals.
-__device__ __forceinline__ void plan_scan(PlanSmem& s, long long (&v)[3]) {
+template <class Smem>
+__device__ __forceinline__ void plan_scan(Smem& s, long long (&v)[3]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long incl[3];
 #pragma unroll
@@ -177,19 +185,17 @@ __device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1
 __device__ __forceinline__ int count_of(long long packed) { return static_cast<int>(packed >> 40); }
 __device__ __forceinline__ int units_in(long long packed) { return static_cast<int>(packed & ((1ll << 40) - 1)); }
 
-// Loops are not unrolled: one CTA runs this code once, and its time is what fetching it takes.
-__global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  PlanSmem& s = *reinterpret_cast<PlanSmem*>(smem_raw);
+// The segments into `segments`, and where `rows` is set the rows' places into p.rows. Returns the number of
+// segments and of units. Loops are not unrolled: this code runs once, and its time is what fetching it takes.
+template <class Smem>
+__device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segment* segments, bool rows) {
   const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x), G = p.groups, B = p.batch;
-  launch_next();
-  if (tid == 0) s.bad = 0;
-  await_previous();
+  int32_t* status = rows ? p.status : nullptr;  // (one CTA reports)
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
     int len = p.seq_lens[b];
     const int most = min(p.bt_stride * kPage, kMaxKeys);
-    if (len < 0 || len > most || len > p.max_seq_len) flag_error(p.status, PA_DEV_ERR_LENGTH);
+    if (len < 0 || len > most || len > p.max_seq_len) flag_error(status, PA_DEV_ERR_LENGTH);
     s.len[b] = min(max(len, 0), most);
   }
 #pragma unroll 1
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     if (g == G - 1) s.cu[G] = p.cu_group_rows[G];
     int n = p.shared_pages[g];
     if (n < 0 || n > p.bt_stride) {
-      flag_error(p.status, PA_DEV_ERR_LENGTH);
+      flag_error(status, PA_DEV_ERR_LENGTH);
       n = 0;
     }
     s.shared[g] = n;
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   __syncthreads();
   // groups that are not disjoint ranges of rows: no row shares anything
   const bool grouped = G > 0 && !s.bad;
-  if (G > 0 && s.bad && tid == 0) flag_error(p.status, PA_DEV_ERR_LENGTH);
+  if (G > 0 && s.bad && tid == 0) flag_error(status, PA_DEV_ERR_LENGTH);
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
     int lo = -1, start = 0;
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   }
   plan_scan(s, at);
   const int many_tiles = count_of(s.totals[0]), many_units = units_in(s.totals[0]);
-  const int segments = many_tiles + count_of(s.totals[1]) + count_of(s.totals[2]);
+  const int count = many_tiles + count_of(s.totals[1]) + count_of(s.totals[2]);
   const int units_all = many_units + units_in(s.totals[1]) + units_in(s.totals[2]);
   int few_seg = count_of(at[1]), few_unit = units_in(at[1]);
   {
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
       s.many_unit[g] = unit;
 #pragma unroll 1
       for (int r = 0; r < rows - few; r += kTileRows) {
-        p.segments[seg] = Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
+        segments[seg] = Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
                                   s.shared[g] * kPage, seg};
         s.unit[seg++] = unit;
         unit += units;
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     if (tid == 0) {
       s.own_seg[B] = count_of(s.totals[2]);
       s.own_unit[B] = units_in(s.totals[2]);
-      s.unit[segments] = units_all;
+      s.unit[count] = units_all;
     }
   }
   __syncthreads();
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
     if (few == 0) continue;
     const int row = s.cu[g], seg = many_tiles + s.few_seg[g] + s.own_seg[row];
     const int unit = many_units + s.few_unit[g] + s.own_unit[row];
-    p.segments[seg] = Segment{unit, units_of(s.shared[g] * kPage), row + rows - few, few, s.first[g], 0,
+    segments[seg] = Segment{unit, units_of(s.shared[g] * kPage), row + rows - few, few, s.first[g], 0,
                               s.shared[g] * kPage, many_tiles + s.few_seg[g]};
     s.unit[seg] = unit;
   }
@@ -337,24 +343,37 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
       r.own = s.own_seg[b];
       r.own_unit = unit;
       r.own_units = units;
-      p.segments[seg] = Segment{unit, units, b, 1, b, start * kPage, s.len[b], ~r.own};
+      segments[seg] = Segment{unit, units, b, 1, b, start * kPage, s.len[b], ~r.own};
       s.unit[seg] = unit;
     }
-    p.rows[b] = r;
+    if (rows) p.rows[b] = r;
   }
   __syncthreads();
+  return make_int2(count, units_all);
+}
+
+template <class Smem>
+__device__ __forceinline__ Slice slice_of(const SharedParams& p, const Smem& s, int2 plan, int i) {
+  const int u0 = static_cast<int>(static_cast<long long>(plan.y) * i / p.slices);
+  const int u1 = static_cast<int>(static_cast<long long>(plan.y) * (i + 1) / p.slices);
+  int lo = 0, hi = max(plan.x, 1);  // last segment with a first unit <= u0
 #pragma unroll 1
-  for (int i = tid; i < p.slices; i += threads) {
-    const int u0 = static_cast<int>(static_cast<long long>(units_all) * i / p.slices);
-    const int u1 = static_cast<int>(static_cast<long long>(units_all) * (i + 1) / p.slices);
-    int lo = 0, hi = max(segments, 1);  // last segment with a first unit <= u0
-#pragma unroll 1
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.unit[mid] <= u0) lo = mid; else hi = mid;
-    }
-    p.slice[i] = Slice{u0, u1, lo, segments, units_all, {0, 0, 0}};
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.unit[mid] <= u0) lo = mid; else hi = mid;
   }
+  return Slice{u0, u1, lo, plan.x, plan.y, {0, 0, 0}};
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PlanOfAll& s = *reinterpret_cast<PlanOfAll*>(smem_raw);
+  launch_next();
+  if (threadIdx.x == 0) s.bad = 0;
+  await_previous();
+  const int2 plan = make_plan(p, s, p.segments, true);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < p.slices; i += static_cast<int>(blockDim.x)) p.slice[i] = slice_of(p, s, plan, i);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -390,6 +409,9 @@ struct SharedSmem {
   UnitInfo info[kInfos];
 };
 static_assert(sizeof(SharedSmem) <= 232448, "shared memory over the 227 KB limit");
+static_assert(sizeof(PlanOfFew) <= 2 * kStages * kTileBytes, "an own plan fits in the ring");
+static_assert(kWeightsAt + 2 * kFewQBytes + kOwnPlanSegments * sizeof(Segment) <= 2 * kQBlockBytes,
+              "its segments fit behind the small buffers");
 
 __device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, int32_t* status) {
   if (mbar_wait_bounded(bar, parity)) return true;
@@ -407,6 +429,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int la
   return ok;
 }
 
+// kOwnPlan: the CTA makes its plan itself.
+template <bool kOwnPlan>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, const SharedParams p) {
@@ -452,7 +476,24 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   const uint32_t tmem = s.tmem_base;  // S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); few rows:
                                       // S_t [0, 16) and two O_t at [64, 96) of the stream's S
   await_previous();
-  const Slice plan = p.slice[slice];
+  Slice plan;
+  // segments of an own plan: in the Q buffer, behind what segments of few rows use of it
+  Segment* own_segments = reinterpret_cast<Segment*>(s.q + kWeightsAt + 2 * kFewQBytes);
+  if (kOwnPlan) {
+    PlanOfFew& ps = *reinterpret_cast<PlanOfFew*>(smem_raw);  // (in the ring, which is not in use yet)
+    if (threadIdx.x == 0) ps.bad = 0;
+    const int2 all = make_plan(p, ps, own_segments, blockIdx.x == 0);
+    if (threadIdx.x == 0) {
+      ps.own = slice_of(p, ps, all, slice);
+      if (blockIdx.x == 0) p.slice[0] = ps.own;  // (for the merge)
+    }
+    __syncthreads();
+    plan = ps.own;
+    tc::fence_proxy_async_smem();  // the ring's copies come after these accesses
+    __syncthreads();
+  } else {
+    plan = p.slice[slice];
+  }
   const int u0 = plan.u0, u1 = plan.u1, nt = u1 - u0;
 
   if (warp >= 8) {
@@ -476,8 +517,10 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     // read just before its copies would cost its latency in every unit.
     constexpr int kBatch = 32 / kTilePages;
     int seg = plan.segment, records = seg;
-    Segment lane_record = p.segments[max(0, min(seg + lane, plan.segments - 1))];
+    Segment lane_record{};
+    if (!kOwnPlan) lane_record = p.segments[max(0, min(seg + lane, plan.segments - 1))];
     auto record = [&](int i) {
+      if (kOwnPlan) return own_segments[i];
       if (i >= records + 32) {
         records = i;
         lane_record = p.segments[min(i + lane, plan.segments - 1)];
@@ -498,7 +541,8 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       const int key = g.first_key + k * kTileKeys + lane * kPage;
       return key < g.end_key ? p.block_table[static_cast<int64_t>(g.table_row) * p.bt_stride + key / kPage] : 0;
     };
-    Segment g = record(seg);
+    Segment g{};
+    if (nt > 0) g = record(seg);
     int batch = nt > 0 ? entries(g, u0 - g.unit) : 0;
     while (it < nt && ok) {
       const int k0 = u0 + it - g.unit, k1 = min(u1 - g.unit, g.units);
@@ -1021,100 +1065,79 @@ constexpr int kMaxParts = 4 * kMaxSlices;  // two sets, two streams, every slice
 
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams p) {
   __shared__ const float* where[kMaxParts];  // O of the row's first query head; the second's follows
-  __shared__ float weight[2][kMaxParts], part_l[2][kMaxParts];  // weight: m first
-  __shared__ float reduced[kMergeWarps][2];
+  __shared__ float4 stat[kMaxParts];         // (m, l) of both
   __shared__ float4 sums[kMergeWarps][32];
   const int b = static_cast<int>(blockIdx.x) / p.hkv, head = static_cast<int>(blockIdx.x) % p.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   await_previous();
-  const long long U = p.slice->units, n = p.slices;
+  const uint32_t n = static_cast<uint32_t>(p.slices), U = static_cast<uint32_t>(p.slice->units);
   const RowPlan row = p.rows[b];
+  // x / d, x < 2^32 n (a 64-bit division takes several times as long)
+  const bool small = U < 0xffffffffu / (n + 1);
+  auto over = [&](uint64_t x, uint32_t d) {
+    return small ? static_cast<int>(static_cast<uint32_t>(x) / d) : static_cast<int>(x / d);
+  };
   // slices [i0, i1] hold a set: slice i has units [U i / n, U (i + 1) / n)
   int i0[2] = {0, 0}, count[2] = {0, 0};
 #pragma unroll
   for (int set = 0; set < 2; ++set) {
     const int unit = set == 0 ? row.tile_unit : row.own_unit, units = set == 0 ? row.tile_units : row.own_units;
     if (units == 0) continue;
-    i0[set] = static_cast<int>(((unit + 1ll) * n - 1) / U);
-    count[set] = 2 * (static_cast<int>((static_cast<long long>(unit + units) * n - 1) / U) - i0[set] + 1);
+    i0[set] = over((static_cast<uint64_t>(unit) + 1) * n - 1, U);
+    count[set] = 2 * (over(static_cast<uint64_t>(unit + units) * n - 1, U) - i0[set] + 1);
   }
   const int total = count[0] + count[1];
-  float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
   for (int c = tid; c < total; c += kMergeThreads) {
     const int set = c < count[0] ? 0 : 1, at = set == 0 ? c : c - count[0];
     const int i = (set == 0 ? i0[0] : i0[1]) + (at >> 1), stream = at & 1;
     const int unit = set == 0 ? row.tile_unit : row.own_unit, units = set == 0 ? row.tile_units : row.own_units;
-    const int cap = set == 0 ? 2 * p.tile_rows : 2;
-    const int first = static_cast<int>(U * i / n), end = static_cast<int>(U * (i + 1) / n);
+    const int cap = set == 0 ? 2 * p.tile_rows : 2, r = set == 0 ? 2 * row.in_tile : 0;
+    const int first = over(static_cast<uint64_t>(U) * i, n), end = over(static_cast<uint64_t>(U) * (i + 1), n);
     const int u0 = max(first, unit), u1 = min(end, unit + units);
     // units alternate between the streams, from the slice's first
     const bool there = u1 - u0 >= 2 || (u1 - u0 == 1 && ((u0 - first) & 1) == stream);
-    const int r = set == 0 ? 2 * row.in_tile : 0;
     const float* part = (set == 0 ? p.tile_parts : p.row_parts) +
                         (((static_cast<int64_t>(i) + (set == 0 ? row.tile : row.own)) * p.hkv + head) * 2 + stream) * cap * kRowFloats;
-    float4 ml = make_float4(-CUDART_INF_F, 0.f, -CUDART_INF_F, 0.f);  // (m, l) of both query heads
-    if (there) ml = *reinterpret_cast<const float4*>(part + cap * kHeadDim + 2 * r);
     where[c] = there ? part + r * kHeadDim : nullptr;
-    weight[0][c] = ml.x;
-    weight[1][c] = ml.z;
-    part_l[0][c] = ml.y;
-    part_l[1][c] = ml.w;
-    top[0] = fmaxf(top[0], ml.x);
-    top[1] = fmaxf(top[1], ml.z);
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
-    if (lane == 0) reduced[warp][h] = top[h];
+    stat[c] = there ? *reinterpret_cast<const float4*>(part + cap * kHeadDim + 2 * r)
+                    : make_float4(-CUDART_INF_F, 0.f, -CUDART_INF_F, 0.f);
   }
   __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) top[h] = fmaxf(top[h], reduced[w][h]);
-  __syncthreads();
-  float sum[2] = {0.f, 0.f};
-  for (int c = tid; c < total; c += kMergeThreads) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float m = weight[h][c], w = m == -CUDART_INF_F ? 0.f : fast_exp2(m - top[h]);
-      weight[h][c] = w;
-      sum[h] += w * part_l[h][c];
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], o);
-    if (lane == 0) reduced[warp][h] = sum[h];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    sum[h] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) sum[h] += reduced[w][h];
-  }
+  // each warp on its own: its first results' loads go out, then the row's maximum and sum over all results
   const int h = warp & 1;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kStride = kMergeWarps / 2;
-  for (int c0 = warp >> 1; c0 < total; c0 += 8 * kStride) {
-    float w[8];
-    float4 v[8];
+  float4 v[8];
+  auto load = [&](int c0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = c0 + j * kStride;
-      w[j] = c < total ? weight[h][c] : 0.f;
       v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < total && where[c] != nullptr) v[j] = reinterpret_cast<const float4*>(where[c] + h * kHeadDim)[lane];
     }
+  };
+  load(warp >> 1);
+  float top = -CUDART_INF_F, l = 0.f;
+  for (int c = lane; c < total; c += 32) top = fmaxf(top, h == 0 ? stat[c].x : stat[c].z);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  auto weight = [&](int c) {
+    const float m = h == 0 ? stat[c].x : stat[c].z;
+    return m == -CUDART_INF_F ? 0.f : fast_exp2(m - top);
+  };
+  for (int c = lane; c < total; c += 32) l += weight(c) * (h == 0 ? stat[c].y : stat[c].w);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = warp >> 1; c0 < total; c0 += 8 * kStride) {
+    if (c0 >= 8 * kStride) load(c0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      acc.x += w[j] * v[j].x;
-      acc.y += w[j] * v[j].y;
-      acc.z += w[j] * v[j].z;
-      acc.w += w[j] * v[j].w;
+      const int c = c0 + j * kStride;
+      const float w = c < total ? weight(c) : 0.f;
+      acc.x += w * v[j].x;
+      acc.y += w * v[j].y;
+      acc.z += w * v[j].z;
+      acc.w += w * v[j].w;
     }
   }
   sums[warp][lane] = acc;
@@ -1122,22 +1145,21 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   if (warp >= 2) return;
 #pragma unroll
   for (int w = 1; w < kStride; ++w) {
-    const float4 v = sums[2 * w + h][lane];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+    const float4 o = sums[2 * w + h][lane];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
   }
-  const float m = h == 0 ? top[0] : top[1], l = h == 0 ? sum[0] : sum[1];
   const float inv = 1.0f / l;
   uint2 out = make_uint2(0u, 0u);
-  if (m != -CUDART_INF_F) {
+  if (top != -CUDART_INF_F) {
     out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
     out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   }
   const int64_t at = static_cast<int64_t>(b) * p.hq + 2 * head + h;
   reinterpret_cast<uint2*>(p.out + at * kHeadDim)[lane] = out;
-  if (lane == 0 && p.lse != nullptr) p.lse[at] = m == -CUDART_INF_F ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+  if (lane == 0 && p.lse != nullptr) p.lse[at] = top == -CUDART_INF_F ? -CUDART_INF_F : (top + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1224,24 +1246,24 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(shared_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(sizeof(SharedSmem)));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(sizeof(PlanSmem)));
+    cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(sizeof(PlanOfAll)));
     // same carveout for the merge: no reconfiguration between them
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(shared_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(decode_shared)");
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, shared_attention_kernel);
-    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncGetAttributes(decode_shared)");
-    if (fa.numRegs < kLaunchRegs) {  // (setmaxnreg.inc would wait forever)
-      snprintf_error("shared_attention_kernel built with %d registers/thread, needs %d for its split", fa.numRegs,
-                     kLaunchRegs);
-      return PA_ERR_UNSUPPORTED;
+    for (auto* kernel : {&shared_attention_kernel<false>, &shared_attention_kernel<true>}) {
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(SharedSmem)));
+      cudaFuncAttributes fa;
+      if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+      if (e == cudaSuccess && fa.numRegs < kLaunchRegs) {  // (setmaxnreg.inc would wait forever)
+        snprintf_error("shared_attention_kernel built with %d registers/thread, needs %d for its split", fa.numRegs,
+                       kLaunchRegs);
+        return PA_ERR_UNSUPPORTED;
+      }
     }
+    if (e != cudaSuccess) return record_cuda_error(e, "cudaFuncSetAttribute(decode_shared)");
     configured_device = dev;
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1270,13 +1292,18 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   p.tile_parts = reinterpret_cast<float*>(ws + l.tile_parts);
   p.row_parts = reinterpret_cast<float*>(ws + l.row_parts);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // a thread per row, group and slice, in whole warps
-  const unsigned plan_threads = static_cast<unsigned>(
-      std::min(kPlanThreads, (std::max({static_cast<int>(batch), static_cast<int>(groups), l.slices}) + 31) / 32 * 32));
-  cudaError_t e = launch_dependent(shared_plan_kernel, 1, plan_threads, sizeof(PlanSmem), st, 0, p);
-  if (e == cudaSuccess)
-    e = launch_dependent(shared_attention_kernel, static_cast<unsigned>(l.slices * hkv), kThreads, sizeof(SharedSmem),
-                         st, 0, qm, km, vm, p);
+  const unsigned grid = static_cast<unsigned>(l.slices * hkv);
+  cudaError_t e = cudaSuccess;
+  if (max_group_rows <= kFewRows && batch + groups <= kOwnPlanSegments) {
+    e = launch_dependent(shared_attention_kernel<true>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
+  } else {
+    // a thread per row, group and slice, in whole warps
+    const unsigned plan_threads = static_cast<unsigned>(
+        std::min(kPlanThreads, (std::max({static_cast<int>(batch), static_cast<int>(groups), l.slices}) + 31) / 32 * 32));
+    e = launch_dependent(shared_plan_kernel, 1, plan_threads, sizeof(PlanOfAll), st, 0, p);
+    if (e == cudaSuccess)
+      e = launch_dependent(shared_attention_kernel<false>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
+  }
   if (e == cudaSuccess)
     e = launch_dependent(shared_merge_kernel, static_cast<unsigned>(batch * hkv), kMergeThreads, 0, st, 0, p);
   return e == cudaSuccess ? PA_OK : record_cuda_error(e, "attn_decode_paged_shared");
