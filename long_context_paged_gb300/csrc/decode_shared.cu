@@ -127,7 +127,6 @@ template <int kGroups, int kRows>
 struct PlanSmem {
   long long warp_sums[3][kPlanThreads / 32];
   long long totals[3];
-  int32_t bad;
   Slice own;  // of the CTA (a plan made by every CTA)
   // groups: first row, shared pages, first row that uses them; segments and units before the group's of
   // many rows, and before its one of few
@@ -191,6 +190,7 @@ template <class Smem>
 __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segment* segments, bool rows) {
   const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x), G = p.groups, B = p.batch;
   int32_t* status = rows ? p.status : nullptr;  // (one CTA reports)
+  bool bad = false;
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
     int len = p.seq_lens[b];
@@ -200,9 +200,11 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
   }
 #pragma unroll 1
   for (int g = tid; g < G; g += threads) {
-    s.cu[g] = p.cu_group_rows[g];
-    if (g == G - 1) s.cu[G] = p.cu_group_rows[G];
+    const int a = p.cu_group_rows[g], b = p.cu_group_rows[g + 1];
     int n = p.shared_pages[g];
+    s.cu[g] = a;
+    if (g == G - 1) s.cu[G] = b;
+    bad |= a < 0 || b < a || b > B || b - a > p.max_group_rows;
     if (n < 0 || n > p.bt_stride) {
       flag_error(status, PA_DEV_ERR_LENGTH);
       n = 0;
@@ -210,16 +212,10 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
     s.shared[g] = n;
     s.first[g] = 0x7fffffff;
   }
-  __syncthreads();
-#pragma unroll 1
-  for (int g = tid; g < G; g += threads) {
-    const int a = s.cu[g], b = s.cu[g + 1];
-    if (a < 0 || b < a || b > B || b - a > p.max_group_rows) s.bad = 1;
-  }
-  __syncthreads();
   // groups that are not disjoint ranges of rows: no row shares anything
-  const bool grouped = G > 0 && !s.bad;
-  if (G > 0 && s.bad && tid == 0) flag_error(status, PA_DEV_ERR_LENGTH);
+  bad = __syncthreads_or(bad);
+  const bool grouped = G > 0 && !bad;
+  if (bad && tid == 0) flag_error(status, PA_DEV_ERR_LENGTH);
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
     int lo = -1, start = 0;
@@ -352,10 +348,20 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
   return make_int2(count, units_all);
 }
 
+// The slices' bounds U i / n and the slice of a unit by 32-bit divisions where they do (64-bit ones take
+// several times as long, and the calls' starts and ends wait for them).
+struct Divider {
+  bool small;
+  __device__ Divider(uint32_t U, uint32_t n) : small(U < 0xffffffffu / (n + 1)) {}
+  __device__ __forceinline__ int operator()(uint64_t x, uint32_t d) const {  // x < U (n + 1)
+    return small ? static_cast<int>(static_cast<uint32_t>(x) / d) : static_cast<int>(x / d);
+  }
+};
+
 template <class Smem>
 __device__ __forceinline__ Slice slice_of(const SharedParams& p, const Smem& s, int2 plan, int i) {
-  const int u0 = static_cast<int>(static_cast<long long>(plan.y) * i / p.slices);
-  const int u1 = static_cast<int>(static_cast<long long>(plan.y) * (i + 1) / p.slices);
+  const Divider over(plan.y, p.slices);
+  const int u0 = over(static_cast<uint64_t>(plan.y) * i, p.slices), u1 = over(static_cast<uint64_t>(plan.y) * (i + 1), p.slices);
   int lo = 0, hi = max(plan.x, 1);  // last segment with a first unit <= u0
 #pragma unroll 1
   while (hi - lo > 1) {
@@ -369,7 +375,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PlanOfAll& s = *reinterpret_cast<PlanOfAll*>(smem_raw);
   launch_next();
-  if (threadIdx.x == 0) s.bad = 0;
   await_previous();
   const int2 plan = make_plan(p, s, p.segments, true);
 #pragma unroll 1
@@ -481,7 +486,6 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   Segment* own_segments = reinterpret_cast<Segment*>(s.q + kWeightsAt + 2 * kFewQBytes);
   if (kOwnPlan) {
     PlanOfFew& ps = *reinterpret_cast<PlanOfFew*>(smem_raw);  // (in the ring, which is not in use yet)
-    if (threadIdx.x == 0) ps.bad = 0;
     const int2 all = make_plan(p, ps, own_segments, blockIdx.x == 0);
     if (threadIdx.x == 0) {
       ps.own = slice_of(p, ps, all, slice);
@@ -1072,11 +1076,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   await_previous();
   const uint32_t n = static_cast<uint32_t>(p.slices), U = static_cast<uint32_t>(p.slice->units);
   const RowPlan row = p.rows[b];
-  // x / d, x < 2^32 n (a 64-bit division takes several times as long)
-  const bool small = U < 0xffffffffu / (n + 1);
-  auto over = [&](uint64_t x, uint32_t d) {
-    return small ? static_cast<int>(static_cast<uint32_t>(x) / d) : static_cast<int>(x / d);
-  };
+  const Divider over(U, n);
   // slices [i0, i1] hold a set: slice i has units [U i / n, U (i + 1) / n)
   int i0[2] = {0, 0}, count[2] = {0, 0};
 #pragma unroll
