@@ -15,7 +15,6 @@
 // from here. No computation happens here, and the binding works without this module, only slower.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -273,29 +272,52 @@ PyObject* guarded(F f) {
   return all;
 }
 
-// An output of this type and shape: the caller's (checked), or a new one on the current stream. Both come
-// back as a tensor, in the order of a call's results.
+// The outputs of a call, in the order of its results: the caller's (checked), or new ones on the current stream.
+// New ones are parts of one block of memory: an allocation each takes longer than a launch.
 struct Outputs {
+  struct New {
+    size_t index, at;  // place among the outputs, first byte in the block
+    ScalarType type;
+    std::vector<int64_t> shape;
+  };
   Reader& r;
   bool current;  // the call is on the current stream (a given one: new outputs are left to the wrapper)
   std::vector<at::Tensor> all;
+  std::vector<New> made;
+  size_t bytes = 0;
 
-  void* take(ScalarType type, at::IntArrayRef shape) {
+  // The next output.
+  void take(ScalarType type, at::IntArrayRef shape) {
     PyObject* o = r.next();
-    if (!r.good) return nullptr;
-    if (o == Py_None) {
-      r.require(current);
-      if (!r.good) return nullptr;
-      all.push_back(at::empty(shape, at::TensorOptions().dtype(type).device(
-                                         at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(r.dev)))));
-      return all.back().data_ptr();
+    if (!r.good) return;
+    if (o != Py_None) {
+      const at::Tensor* t = r.tensor_of(o, type);
+      if (r.good && (!t->is_contiguous() || t->sizes() != shape)) r.good = false;
+      if (r.good) all.push_back(*t);
+      return;
     }
-    const at::Tensor* t = r.tensor_of(o, type);
-    if (r.good && (!t->is_contiguous() || t->sizes() != shape)) r.good = false;
-    if (!r.good) return nullptr;
-    all.push_back(*t);
-    return t->data_ptr();
+    r.require(current);
+    if (!r.good) return;
+    size_t n = c10::elementSize(type);
+    for (const int64_t d : shape) n *= static_cast<size_t>(d);
+    made.push_back(New{all.size(), bytes, type, shape.vec()});
+    bytes += (n + 255) / 256 * 256;
+    all.emplace_back();
   }
+  // Memory for the new ones, once all have been taken.
+  void allocate() {
+    if (!r.good || made.empty()) return;
+    c10::Allocator* a = c10::cuda::CUDACachingAllocator::get();
+    const c10::Storage block(c10::Storage::use_byte_size_t(), static_cast<int64_t>(bytes), a->allocate(bytes), a, false);
+    for (const New& m : made) {
+      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+          c10::Storage(block), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(m.type));
+      t.unsafeGetTensorImpl()->set_sizes_contiguous(m.shape);
+      t.unsafeGetTensorImpl()->set_storage_offset(static_cast<int64_t>(m.at / c10::elementSize(m.type)));
+      all[m.index] = std::move(t);
+    }
+  }
+  void* operator[](size_t i) { return all[i].data_ptr(); }
 };
 
 // (q, k_pool, v_pool, block_table, seq_lens, max_seq_len, scale, split_tokens, out, lse,
@@ -606,15 +628,14 @@ PyObject* beam(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t stride = W > 1 ? x->stride(1) : N > 1 ? x->stride(0) : V;
     r.require((V == 1 || x->stride(2) == 1) && (N <= 1 || W <= 1 || x->stride(0) == W * x->stride(1)));
     if (!r.good) return {};
-    Outputs out{r, a[10] == Py_None, {}};
+    Outputs out{r, a[10] == Py_None, {}, {}};
     const int64_t shape[2] = {N, k};
-    void* s = out.take(ScalarType::Float, shape);
-    void* parents = out.take(ScalarType::Int, shape);
-    void* tokens = out.take(ScalarType::Int, shape);
-    void* l = out.take(ScalarType::Int, shape);
+    out.take(ScalarType::Float, shape);
+    for (int i = 0; i < 3; ++i) out.take(ScalarType::Int, shape);
     const at::Tensor* workspace = r.bytes_or_none();
     cudaStream_t st = r.stream();
     if (!r.done()) return {};
+    out.allocate();
     const int32_t reqs = static_cast<int32_t>(N), beams = static_cast<int32_t>(W), vocab = static_cast<int32_t>(V);
     const size_t need = workspace ? 0 : pa_beam_workspace_size(reqs, beams, vocab, k);
     pa_status code;
@@ -622,8 +643,8 @@ PyObject* beam(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Unlocked unlocked;
       Scratch scratch(workspace, need, st);
       code = beam_select(x->data_ptr(), type == ScalarType::BFloat16 ? PA_BF16 : PA_FP32, stride, reqs, beams, vocab,
-                         ptr<const float>(scores), ptr<const int32_t>(live), k, eos, static_cast<float*>(s),
-                         static_cast<int32_t*>(parents), static_cast<int32_t*>(tokens), static_cast<int32_t*>(l),
+                         ptr<const float>(scores), ptr<const int32_t>(live), k, eos, static_cast<float*>(out[0]),
+                         static_cast<int32_t*>(out[1]), static_cast<int32_t*>(out[2]), static_cast<int32_t*>(out[3]),
                          scratch.p, scratch.bytes, reinterpret_cast<pa_stream_t>(st));
     }
     return {"beam_select", code, std::move(out.all)};
@@ -649,15 +670,16 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.at_least(table, B);
     r.at_least(count, 1);
     if (!r.good) return {};
-    Outputs out{r, a[12] == Py_None, {}};
-    void* lens_out = out.take(ScalarType::Int, {B});
-    void* copies = out.take(ScalarType::Int, {B, 3});
-    void* shared = out.take(ScalarType::Int, {G});
-    void* count_out = out.take(ScalarType::Int, {1});
+    Outputs out{r, a[12] == Py_None, {}, {}};
+    out.take(ScalarType::Int, {B});
+    out.take(ScalarType::Int, {B, 3});
+    out.take(ScalarType::Int, {G});
+    out.take(ScalarType::Int, {1});
     const at::Tensor* workspace = r.bytes_or_none();
     void* status = r.status();
     cudaStream_t st = r.stream();
     if (!r.done()) return {};
+    out.allocate();
     const int32_t groups = static_cast<int32_t>(G), beams = static_cast<int32_t>(W);
     const int32_t stride = static_cast<int32_t>(table->size(1));
     const size_t need = workspace ? 0 : pa_fork_workspace_size(groups, beams, stride);
@@ -667,8 +689,8 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Scratch scratch(workspace, need, st);
       code = paged_fork(ptr<const int32_t>(parents), ptr<const int32_t>(lens), groups, beams, ptr<int32_t>(table),
                         stride, ptr<int32_t>(free), static_cast<int32_t>(free->size(0)), ptr<const int32_t>(count),
-                        pages, static_cast<int32_t*>(count_out), static_cast<int32_t*>(lens_out),
-                        static_cast<int32_t*>(copies), static_cast<int32_t*>(shared), scratch.p, scratch.bytes,
+                        pages, static_cast<int32_t*>(out[3]), static_cast<int32_t*>(out[0]),
+                        static_cast<int32_t*>(out[1]), static_cast<int32_t*>(out[2]), scratch.p, scratch.bytes,
                         static_cast<int32_t*>(status), reinterpret_cast<pa_stream_t>(st));
     }
     return {"paged_fork", code, std::move(out.all)};
