@@ -9,6 +9,12 @@
 // costs 512 bytes of a KV head's cache and 4 * 128 * 2 R operations, so up to about 64 rows the call is
 // bound by HBM and reads the shared keys at its rate, R times fewer bytes than the plain decode.
 //
+// Measured on a GB300 (calls of a graph, 152 CTAs): 16 groups of 4 rows over 5,000 to 30,000 keys 157 us,
+// 6.2 TB/s of the bytes that have to be read (0.91 of a copy's rate; 64 rows read alone would be 3.7 GB);
+// 8 rows over 67,500 keys 61 us, of which the units take 41 (6.7 TB/s), the plan 3.5, the first copies 3.7,
+// the merge and its start 5.5 and the slowest CTA 2.5; 4 rows over 1,000 keys 13.8 us, a chain of latencies;
+// 307 rows in 4 groups 101 us (64 rows a pass: three passes over the keys of 131 rows).
+//
 // Work split. A segment is a run of keys with the rows that see all of it: (64 rows of a group, its
 // shared pages) or (one row, its own pages). Segments are cut into units of 128 keys, laid end to end
 // and divided into equal slices, one per CTA of a KV head; the Hkv CTAs of a slice read the heads of
@@ -17,9 +23,17 @@
 // of one CTA, from lengths that only the GPU knows.
 //
 // Per unit, in a CTA: S = Q K^T (A = Q, B = K in shared memory, fp32 in TMEM), P = 2^(scale S - m) by a
-// thread per row, written over S as bf16, O += P V (A = P in TMEM, B = V in shared memory). Units go to
-// two softmax warpgroups in turn, each with an S and an O of its own, so that one's exponentials run
-// beside the other's products. K and V come by tiled TMA, a page per copy.
+// thread per row, written over S as bf16, O += P V (A = P in TMEM, B = V in shared memory). With 8 rows or
+// fewer most of those 128 matrix rows would be padding and one warp would do all exponentials, so the
+// products are turned round: S^T = K Q^T (A = K, 16 columns), a thread per key, O^T += V^T P^T (A = V, B = P
+// in shared memory). (16 x 4 rows: 190 us with a thread per row, 169 with a thread per key.) Units go to
+// two softmax warpgroups in turn, each with an S and an O of its own, so that one's exponentials run beside
+// the other's products. K and V come by tiled TMA, a page per copy.
+//
+// Tried and left out: 64-key units (16 x 4 rows 216 -> 270 us: an issuing thread's waits and commits cost
+// more than its products); two row tiles on one K/V tile, a stream each, for 65 to 128 rows (4 groups of up to
+// 131 rows 112 -> 148 us: a stream's scores wait for its own weights and products, which two streams on
+// alternate units hide); a merge of 512 threads (8 rows 61.7 -> 60.8 us, 307 rows 101 -> 115).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>

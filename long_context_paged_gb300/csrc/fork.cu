@@ -16,6 +16,9 @@
 // the end of the free list); the second sums the counts before its own, and changes the tables, the
 // list and the lengths. If anything is wrong (a parent outside the group, a length past the table,
 // too few free pages) it changes nothing: that has to be known before the first store, hence two.
+// Measured on a GB300 (calls of a graph that also restore the table and the list by two copies): 4 rows of
+// 1,000 tokens 12 us, 512 rows of 2,000 to 67,500 tokens 22 us: each launch is a chain of loads (group and page
+// entries, counts, the end of the list).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -418,7 +421,8 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkParams p
 
 // ---------------------------------------------------------------------------------------------
 // paged_copy_pages: the first n tokens of a page, 16 bytes a thread and load, for every row of
-// copies[] and every pool: a CTA per pair. Bound by HBM (each byte read once and written once).
+// copies[] and every pool: a CTA per pair. Bound by HBM (each byte read once and written once): 512 rows,
+// half of them copied, in 56 pools, 503 MB in 76.4 us (6.6 TB/s, 0.97 of a copy's rate); 3 pages 2.9 us.
 // ---------------------------------------------------------------------------------------------
 constexpr int kPoolsPerLaunch = 128;
 
