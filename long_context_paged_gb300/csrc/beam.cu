@@ -107,13 +107,6 @@ __device__ __forceinline__ uint64_t rank_of(float x, int token) {
   return o == 0 ? 0ull : static_cast<uint64_t>(o) << 32 | ~static_cast<uint32_t>(token);
 }
 
-// A vector of no logits: -inf in every place.
-template <class T>
-__device__ __forceinline__ uint4 no_logits() {
-  const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-  return make_uint4(w, w, w, w);
-}
-
 // A thread's state over its logits: the largest, and the sum of exponentials against a reference that
 // follows the largest at a distance (40 at most: sums stay below 2^77), so that nothing is rescaled at
 // every new maximum.
@@ -190,7 +183,9 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   if (!expands(p, row)) return;
   const Row<T> r(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab);
   const uint4* body = reinterpret_cast<const uint4*>(r.base + r.head);
-  const int per = (r.vectors + p.pieces - 1) / p.pieces;
+  int per = (r.vectors + p.pieces - 1) / p.pieces;
+  // long pieces in whole rounds of four vectors a thread (the last one is shorter)
+  if (per > 3 * kMinVectors) per = (per + kMinVectors - 1) / kMinVectors * kMinVectors;
   const int v0 = min(r.vectors, piece * per), v1 = min(r.vectors, v0 + per);
   // the first piece has the single logits before the vectors, the last those after
   const int lead = piece == 0 ? r.head : 0, trail = piece == p.pieces - 1 ? r.tail : 0;
@@ -201,10 +196,11 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
     seen.reach(x);
     seen.take(x);
   }
-  for (int v = v0 + tid; v < v1; v += 4 * kThreads) {
+  int v = v0 + tid;
+  for (; v + 3 * kThreads < v1; v += 4 * kThreads) {
     uint4 w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = v + j * kThreads < v1 ? body[v + j * kThreads] : no_logits<T>();
+    for (int j = 0; j < 4; ++j) w[j] = body[v + j * kThreads];
     seen.reach(most_of(w, T()));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -212,6 +208,13 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
       unpack(w[j], x);
       seen.take(x);
     }
+  }
+  for (; v < v1; v += kThreads) {
+    const uint4 w = body[v];
+    float x[kVec];
+    unpack(w, x);
+    seen.reach(most_of(w, T()));
+    seen.take(x);
   }
   if (tid < trail) {
     const float x = single(r.base[trail_at + tid]);
