@@ -137,10 +137,14 @@ struct SharedParams {
 // ---------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;  // at most: four rows a thread
 
-template <int kGroups, int kRows>
+// Numbers of segments and their units travel as one word, segments above kShift bits of units.
+template <int kGroups, int kRows, class Word, int kShift, bool kFew>
 struct PlanSmem {
-  long long warp_sums[3][kPlanThreads / 32];
-  long long totals[3];
+  using Packed = Word;
+  static constexpr int kUnitBits = kShift;
+  static constexpr bool kFewOnly = kFew;  // no segments of many rows
+  Packed warp_sums[3][kPlanThreads / 32];
+  Packed totals[3];
   Slice own;  // of the CTA (a plan made by every CTA)
   // groups: first row, shared pages, first row that uses them; segments and units before the group's of
   // many rows, and before its one of few
@@ -152,59 +156,66 @@ struct PlanSmem {
   int32_t own_seg[kRows + 1], own_unit[kRows + 1];
   int32_t unit[kGroups + kRows + kRows / kTileRows + 1];  // first unit of each segment
 };
-using PlanOfAll = PlanSmem<kMaxGroups, kMaxBatch>;
+using PlanOfAll = PlanSmem<kMaxGroups, kMaxBatch, unsigned long long, 40, false>;
 static_assert(sizeof(PlanOfAll) <= 232448, "shared memory over the 227 KB limit");
 
 // Calls of few rows per group and no more segments than this are planned by every CTA for itself, which takes
 // it 2 us of a launch's 4 (a plan kernel and the wait for it), and keeps the segments in shared memory.
 constexpr int kOwnPlanSegments = 512;
-using PlanOfFew = PlanSmem<kOwnPlanSegments, kOwnPlanSegments>;
+using PlanOfFew = PlanSmem<kOwnPlanSegments, kOwnPlanSegments, uint32_t, 20, true>;
+static_assert(kOwnPlanSegments < 1 << 12 && kOwnPlanSegments * (kMaxKeys / kTileKeys) < 1 << 20, "fits in a word");
 
-__device__ __forceinline__ long long warp_scan_sum(long long v, int lane) {
+template <class T>
+__device__ __forceinline__ T warp_scan_sum(T v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, v, o);
+    const T n = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += n;
   }
   return v;
 }
 
-// Exclusive prefix sums over the CTA of three packed (count << 40 | units), and their totals.
+// Exclusive prefix sums over the CTA of packed numbers (from the first that can be other than 0), and their
+// totals.
 template <class Smem>
-__device__ __forceinline__ void plan_scan(Smem& s, long long (&v)[3]) {
+__device__ __forceinline__ void plan_scan(Smem& s, typename Smem::Packed (&v)[3]) {
+  using T = typename Smem::Packed;
+  constexpr int kFrom = Smem::kFewOnly ? 1 : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl[3];
+  T incl[3];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
+  for (int k = kFrom; k < 3; ++k) {
     incl[k] = warp_scan_sum(v[k], lane);
     if (lane == 31) s.warp_sums[k][warp] = incl[k];
   }
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const long long w = lane < static_cast<int>(blockDim.x >> 5) ? s.warp_sums[k][lane] : 0;
-      const long long x = warp_scan_sum(w, lane);
+    for (int k = kFrom; k < 3; ++k) {
+      const T w = lane < static_cast<int>(blockDim.x >> 5) ? s.warp_sums[k][lane] : 0;
+      const T x = warp_scan_sum(w, lane);
       s.warp_sums[k][lane] = x - w;
       if (lane == 31) s.totals[k] = x;
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 3; ++k) v[k] = s.warp_sums[k][warp] + incl[k] - v[k];
+  for (int k = kFrom; k < 3; ++k) v[k] = s.warp_sums[k][warp] + incl[k] - v[k];
 }
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
-__device__ __forceinline__ int count_of(long long packed) { return static_cast<int>(packed >> 40); }
-__device__ __forceinline__ int units_in(long long packed) { return static_cast<int>(packed & ((1ll << 40) - 1)); }
 
-// The segments into `segments`, and where `rows` is set the rows' places into p.rows. Returns the number of
+// The segments into `segments`, and where rows_out is set the rows' places into p.rows. Returns the number of
 // segments and of units. Loops are not unrolled: this code runs once, and its time is what fetching it takes.
 template <class Smem>
-__device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segment* segments, bool rows) {
+__device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segment* segments, bool rows_out) {
   const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x), G = p.groups, B = p.batch;
-  int32_t* status = rows ? p.status : nullptr;  // (one CTA reports)
+  int32_t* status = rows_out ? p.status : nullptr;  // (one CTA reports)
   bool bad = false;
+  using Packed = typename Smem::Packed;
+  constexpr Packed kOne = static_cast<Packed>(1) << Smem::kUnitBits;
+  auto count_of = [](Packed v) { return static_cast<int>(v >> Smem::kUnitBits); };
+  auto units_in = [](Packed v) { return static_cast<int>(v & (kOne - 1)); };
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
     int len = p.seq_lens[b];
@@ -258,21 +269,24 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
   const int per = (B + threads - 1) / threads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
   auto rows_of = [&](int g) { return grouped && s.first[g] != 0x7fffffff ? s.cu[g + 1] - s.cu[g] : 0; };
   auto few_of = [&](int rows) { return rows % kTileRows <= kFewRows ? rows % kTileRows : 0; };
-  long long at[3] = {0, 0, 0};  // many, few, own
+  Packed at[3] = {0, 0, 0};  // many, few, own
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
-    const int rows = rows_of(g), few = few_of(rows);
-    const long long units = units_of(s.shared[g] * kPage), many = (rows - few + kTileRows - 1) / kTileRows;
-    at[0] += many << 40 | many * units;
-    if (few > 0) at[1] += 1ll << 40 | units;
+    const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
+    if (!Smem::kFewOnly) {
+      const Packed many = (rows - few + kTileRows - 1) / kTileRows;
+      at[0] += many * kOne + many * units;
+    }
+    if (few > 0) at[1] += kOne + units;
   }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int units = units_of(s.len[b] - s.start[b] * kPage);
-    if (units > 0) at[2] += 1ll << 40 | units;
+    if (units > 0) at[2] += kOne + units;
   }
   plan_scan(s, at);
-  const int many_tiles = count_of(s.totals[0]), many_units = units_in(s.totals[0]);
+  const Packed many_total = Smem::kFewOnly ? 0 : s.totals[0];
+  const int many_tiles = count_of(many_total), many_units = units_in(many_total);
   const int count = many_tiles + count_of(s.totals[1]) + count_of(s.totals[2]);
   const int units_all = many_units + units_in(s.totals[1]) + units_in(s.totals[2]);
   int few_seg = count_of(at[1]), few_unit = units_in(at[1]);
@@ -281,10 +295,12 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
-      s.many_seg[g] = seg;
-      s.many_unit[g] = unit;
+      if (!Smem::kFewOnly) {
+        s.many_seg[g] = seg;
+        s.many_unit[g] = unit;
+      }
 #pragma unroll 1
-      for (int r = 0; r < rows - few; r += kTileRows) {
+      for (int r = 0; !Smem::kFewOnly && r < rows - few; r += kTileRows) {
         segments[seg] = Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
                                   s.shared[g] * kPage, seg};
         s.unit[seg++] = unit;
@@ -336,11 +352,11 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
       const int rows = rows_of(g), few = few_of(rows), in_group = b - s.cu[g];
       seg += s.few_seg[g] + (few > 0 ? 1 : 0);
       unit += s.few_unit[g] + (few > 0 ? units_of(s.shared[g] * kPage) : 0);
-      if (start > 0) {
+      if (rows_out && start > 0) {
         const int place = in_group / kTileRows;
         r.tile_units = units_of(start * kPage);
         r.in_tile = in_group % kTileRows;
-        if (in_group < rows - few) {
+        if (!Smem::kFewOnly && in_group < rows - few) {
           r.tile = s.many_seg[g] + place;
           r.tile_unit = s.many_unit[g] + place * r.tile_units;
         } else {
@@ -356,7 +372,7 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
       segments[seg] = Segment{unit, units, b, 1, b, start * kPage, s.len[b], ~r.own};
       s.unit[seg] = unit;
     }
-    if (rows) p.rows[b] = r;
+    if (rows_out) p.rows[b] = r;
   }
   __syncthreads();
   return make_int2(count, units_all);
@@ -372,17 +388,11 @@ struct Divider {
   }
 };
 
-template <class Smem>
-__device__ __forceinline__ Slice slice_of(const SharedParams& p, const Smem& s, int2 plan, int i) {
+// Slice i, but for the segment of its first unit.
+__device__ __forceinline__ Slice slice_of(const SharedParams& p, int2 plan, int i) {
   const Divider over(plan.y, p.slices);
   const int u0 = over(static_cast<uint64_t>(plan.y) * i, p.slices), u1 = over(static_cast<uint64_t>(plan.y) * (i + 1), p.slices);
-  int lo = 0, hi = max(plan.x, 1);  // last segment with a first unit <= u0
-#pragma unroll 1
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s.unit[mid] <= u0) lo = mid; else hi = mid;
-  }
-  return Slice{u0, u1, lo, plan.x, plan.y, {0, 0, 0}};
+  return Slice{u0, u1, 0, plan.x, plan.y, {0, 0, 0}};
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
@@ -392,7 +402,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const Shar
   await_previous();
   const int2 plan = make_plan(p, s, p.segments, true);
 #pragma unroll 1
-  for (int i = threadIdx.x; i < p.slices; i += static_cast<int>(blockDim.x)) p.slice[i] = slice_of(p, s, plan, i);
+  for (int i = threadIdx.x; i < p.slices; i += static_cast<int>(blockDim.x)) {
+    Slice own = slice_of(p, plan, i);
+    int lo = 0, hi = max(plan.x, 1);  // last segment with a first unit <= u0
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.unit[mid] <= own.u0) lo = mid; else hi = mid;
+    }
+    own.segment = lo;
+    p.slice[i] = own;
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -501,12 +521,12 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   if (kOwnPlan) {
     PlanOfFew& ps = *reinterpret_cast<PlanOfFew*>(smem_raw);  // (in the ring, which is not in use yet)
     const int2 all = make_plan(p, ps, own_segments, blockIdx.x == 0);
-    if (threadIdx.x == 0) {
-      ps.own = slice_of(p, ps, all, slice);
-      if (blockIdx.x == 0) p.slice[0] = ps.own;  // (for the merge)
-    }
+    plan = slice_of(p, all, slice);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.slice[0] = plan;  // (for the merge)
+    for (int i = threadIdx.x; i < all.x; i += kThreads)
+      if (ps.unit[i] <= plan.u0 && plan.u0 < ps.unit[i + 1]) ps.own.segment = i;
     __syncthreads();
-    plan = ps.own;
+    plan.segment = ps.own.segment;
     tc::fence_proxy_async_smem();  // the ring's copies come after these accesses
     __syncthreads();
   } else {
