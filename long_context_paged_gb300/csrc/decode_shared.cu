@@ -127,6 +127,7 @@ struct SharedParams {
   int32_t* status;
   Slice* slice;            // [slices]
   Segment* segments;
+  Segment* own_segments;   // [CTAs][kOwnPlanSegments]
   RowPlan* rows;           // [batch]
   float* tile_parts;       // [slices + tiles][hkv][2 streams][2 tile_rows][128], then (m, l)
   float* row_parts;        // [slices + batch][hkv][2 streams][2][128], then (m, l)
@@ -159,10 +160,13 @@ struct PlanSmem {
 using PlanOfAll = PlanSmem<kMaxGroups, kMaxBatch, unsigned long long, 40, false>;
 static_assert(sizeof(PlanOfAll) <= 232448, "shared memory over the 227 KB limit");
 
-// Calls of few rows per group and no more segments than this are planned by every CTA for itself, which takes
-// it 2 us of a launch's 4 (a plan kernel and the wait for it), and keeps the segments in shared memory.
+// How a call is planned. One of no more segments than this is planned by every CTA for itself, which spares it
+// the launch of a plan kernel and the wait for it (8 rows or fewer per group over 1,000 keys 15.0 -> 13.8 us).
+// With few rows per group the segments stay in shared memory, else they go to the CTA's part of the workspace.
 constexpr int kOwnPlanSegments = 512;
-using PlanOfFew = PlanSmem<kOwnPlanSegments, kOwnPlanSegments, uint32_t, 20, true>;
+enum Planned { kByKernel, kOwnFew, kOwnAny };
+template <bool kFew>
+using OwnPlan = PlanSmem<kOwnPlanSegments, kOwnPlanSegments, uint32_t, 20, kFew>;
 static_assert(kOwnPlanSegments < 1 << 12 && kOwnPlanSegments * (kMaxKeys / kTileKeys) < 1 << 20, "fits in a word");
 
 template <class T>
@@ -205,10 +209,27 @@ __device__ __forceinline__ void plan_scan(Smem& s, typename Smem::Packed (&v)[3]
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
 
-// The segments into `segments`, and where rows_out is set the rows' places into p.rows. Returns the number of
-// segments and of units. Loops are not unrolled: this code runs once, and its time is what fetching it takes.
-template <class Smem>
-__device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segment* segments, bool rows_out) {
+// The slices' bounds U i / n and the slice of a unit by 32-bit divisions where they do (64-bit ones take
+// several times as long, and the calls' starts and ends wait for them).
+struct Divider {
+  bool small;
+  __device__ Divider(uint32_t U, uint32_t n) : small(U < 0xffffffffu / (n + 1)) {}
+  __device__ __forceinline__ int operator()(uint64_t x, uint32_t d) const {  // x < U (n + 1)
+    return small ? static_cast<int>(static_cast<uint32_t>(x) / d) : static_cast<int>(x / d);
+  }
+};
+
+// Slice i, but for the segment of its first unit.
+__device__ __forceinline__ Slice slice_of(const SharedParams& p, int2 plan, int i) {
+  const Divider over(plan.y, p.slices);
+  const int u0 = over(static_cast<uint64_t>(plan.y) * i, p.slices), u1 = over(static_cast<uint64_t>(plan.y) * (i + 1), p.slices);
+  return Slice{u0, u1, 0, plan.x, plan.y, {0, 0, 0}};
+}
+
+// The segments (with kOwn those of slice `slice` alone) into `segments`, and where rows_out is set the rows' places
+// into p.rows. Returns the number of segments and of units. Loops are not unrolled: this code runs once, and its time is what fetching it takes.
+template <bool kOwn, class Smem>
+__device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segment* segments, int slice, bool rows_out) {
   const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x), G = p.groups, B = p.batch;
   int32_t* status = rows_out ? p.status : nullptr;  // (one CTA reports)
   bool bad = false;
@@ -289,6 +310,11 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
   const int many_tiles = count_of(many_total), many_units = units_in(many_total);
   const int count = many_tiles + count_of(s.totals[1]) + count_of(s.totals[2]);
   const int units_all = many_units + units_in(s.totals[1]) + units_in(s.totals[2]);
+  const Slice own = slice_of(p, make_int2(count, units_all), slice);
+  auto put = [&](int seg, const Segment& g) {
+    if (!kOwn || (g.unit < own.u1 && g.unit + g.units > own.u0)) segments[seg] = g;
+    s.unit[seg] = g.unit;
+  };
   int few_seg = count_of(at[1]), few_unit = units_in(at[1]);
   {
     int seg = count_of(at[0]), unit = units_in(at[0]);
@@ -301,9 +327,9 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
       }
 #pragma unroll 1
       for (int r = 0; !Smem::kFewOnly && r < rows - few; r += kTileRows) {
-        segments[seg] = Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
-                                  s.shared[g] * kPage, seg};
-        s.unit[seg++] = unit;
+        put(seg, Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
+                         s.shared[g] * kPage, seg});
+        ++seg;
         unit += units;
       }
       s.few_seg[g] = few_seg;
@@ -339,9 +365,8 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
     if (few == 0) continue;
     const int row = s.cu[g], seg = many_tiles + s.few_seg[g] + s.own_seg[row];
     const int unit = many_units + s.few_unit[g] + s.own_unit[row];
-    segments[seg] = Segment{unit, units_of(s.shared[g] * kPage), row + rows - few, few, s.first[g], 0,
-                              s.shared[g] * kPage, many_tiles + s.few_seg[g]};
-    s.unit[seg] = unit;
+    put(seg, Segment{unit, units_of(s.shared[g] * kPage), row + rows - few, few, s.first[g], 0,
+                     s.shared[g] * kPage, many_tiles + s.few_seg[g]});
   }
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
@@ -369,8 +394,7 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
       r.own = s.own_seg[b];
       r.own_unit = unit;
       r.own_units = units;
-      segments[seg] = Segment{unit, units, b, 1, b, start * kPage, s.len[b], ~r.own};
-      s.unit[seg] = unit;
+      put(seg, Segment{unit, units, b, 1, b, start * kPage, s.len[b], ~r.own});
     }
     if (rows_out) p.rows[b] = r;
   }
@@ -378,29 +402,12 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
   return make_int2(count, units_all);
 }
 
-// The slices' bounds U i / n and the slice of a unit by 32-bit divisions where they do (64-bit ones take
-// several times as long, and the calls' starts and ends wait for them).
-struct Divider {
-  bool small;
-  __device__ Divider(uint32_t U, uint32_t n) : small(U < 0xffffffffu / (n + 1)) {}
-  __device__ __forceinline__ int operator()(uint64_t x, uint32_t d) const {  // x < U (n + 1)
-    return small ? static_cast<int>(static_cast<uint32_t>(x) / d) : static_cast<int>(x / d);
-  }
-};
-
-// Slice i, but for the segment of its first unit.
-__device__ __forceinline__ Slice slice_of(const SharedParams& p, int2 plan, int i) {
-  const Divider over(plan.y, p.slices);
-  const int u0 = over(static_cast<uint64_t>(plan.y) * i, p.slices), u1 = over(static_cast<uint64_t>(plan.y) * (i + 1), p.slices);
-  return Slice{u0, u1, 0, plan.x, plan.y, {0, 0, 0}};
-}
-
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_kernel(const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PlanOfAll& s = *reinterpret_cast<PlanOfAll*>(smem_raw);
   launch_next();
   await_previous();
-  const int2 plan = make_plan(p, s, p.segments, true);
+  const int2 plan = make_plan<false>(p, s, p.segments, 0, true);
 #pragma unroll 1
   for (int i = threadIdx.x; i < p.slices; i += static_cast<int>(blockDim.x)) {
     Slice own = slice_of(p, plan, i);
@@ -448,7 +455,7 @@ struct SharedSmem {
   UnitInfo info[kInfos];
 };
 static_assert(sizeof(SharedSmem) <= 232448, "shared memory over the 227 KB limit");
-static_assert(sizeof(PlanOfFew) <= 2 * kStages * kTileBytes, "an own plan fits in the ring");
+static_assert(sizeof(OwnPlan<false>) <= 2 * kStages * kTileBytes, "an own plan fits in the ring");
 static_assert(kWeightsAt + 2 * kFewQBytes + kOwnPlanSegments * sizeof(Segment) <= 2 * kQBlockBytes,
               "its segments fit behind the small buffers");
 
@@ -468,8 +475,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int la
   return ok;
 }
 
-// kOwnPlan: the CTA makes its plan itself.
-template <bool kOwnPlan>
+template <Planned kPlanned>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, const SharedParams p) {
@@ -517,10 +523,12 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   await_previous();
   Slice plan;
   // segments of an own plan: in the Q buffer, behind what segments of few rows use of it
-  Segment* own_segments = reinterpret_cast<Segment*>(s.q + kWeightsAt + 2 * kFewQBytes);
-  if (kOwnPlan) {
-    PlanOfFew& ps = *reinterpret_cast<PlanOfFew*>(smem_raw);  // (in the ring, which is not in use yet)
-    const int2 all = make_plan(p, ps, own_segments, blockIdx.x == 0);
+  Segment* own_segments = kPlanned == kOwnFew ? reinterpret_cast<Segment*>(s.q + kWeightsAt + 2 * kFewQBytes)
+                                              : p.own_segments + static_cast<int64_t>(blockIdx.x) * kOwnPlanSegments;
+  if (kPlanned != kByKernel) {
+    using Smem = OwnPlan<kPlanned == kOwnFew>;
+    Smem& ps = *reinterpret_cast<Smem*>(smem_raw);  // (in the ring, which is not in use yet)
+    const int2 all = make_plan<true>(p, ps, own_segments, slice, blockIdx.x == 0);
     plan = slice_of(p, all, slice);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.slice[0] = plan;  // (for the merge)
     for (int i = threadIdx.x; i < all.x; i += kThreads)
@@ -556,9 +564,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     constexpr int kBatch = 32 / kTilePages;
     int seg = plan.segment, records = seg;
     Segment lane_record{};
-    if (!kOwnPlan) lane_record = p.segments[max(0, min(seg + lane, plan.segments - 1))];
+    if (kPlanned == kByKernel) lane_record = p.segments[max(0, min(seg + lane, plan.segments - 1))];
     auto record = [&](int i) {
-      if (kOwnPlan) return own_segments[i];
+      if (kPlanned != kByKernel) return own_segments[i];
       if (i >= records + 32) {
         records = i;
         lane_record = p.segments[min(i + lane, plan.segments - 1)];
@@ -1201,7 +1209,8 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 // ---------------------------------------------------------------------------------------------
 struct SharedLayout {
   int slices, tile_rows;
-  size_t slice, segments, rows, tile_parts, row_parts, total;
+  Planned planned;
+  size_t slice, segments, own_segments, rows, tile_parts, row_parts, total;
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1215,7 +1224,10 @@ bool shared_layout(SharedLayout& l, int hkv, int batch, int groups, int max_grou
   const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kTileRows : 0;
   l.slice = 0;
   l.segments = align256(sizeof(Slice) * l.slices);
-  l.rows = align256(l.segments + sizeof(Segment) * (tiles + batch));
+  l.planned = tiles + batch > kOwnPlanSegments ? kByKernel : max_group_rows <= kFewRows ? kOwnFew : kOwnAny;
+  l.own_segments = align256(l.segments + (l.planned == kByKernel ? sizeof(Segment) * (tiles + batch) : 0));
+  const size_t own = l.planned == kOwnAny ? sizeof(Segment) * kOwnPlanSegments : 0;
+  l.rows = align256(l.own_segments + own * l.slices * hkv);
   l.tile_parts = align256(l.rows + sizeof(RowPlan) * batch);
   const size_t per_row = static_cast<size_t>(hkv) * 2 * 2 * kRowFloats * sizeof(float);
   l.row_parts = align256(l.tile_parts + (groups > 0 ? (l.slices + tiles) * l.tile_rows * per_row : 0));
@@ -1286,7 +1298,8 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(shared_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
-    for (auto* kernel : {&shared_attention_kernel<false>, &shared_attention_kernel<true>}) {
+    for (auto* kernel : {&shared_attention_kernel<kByKernel>, &shared_attention_kernel<kOwnFew>,
+                         &shared_attention_kernel<kOwnAny>}) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(SharedSmem)));
       cudaFuncAttributes fa;
@@ -1322,21 +1335,24 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   p.status = status;
   p.slice = reinterpret_cast<Slice*>(ws + l.slice);
   p.segments = reinterpret_cast<Segment*>(ws + l.segments);
+  p.own_segments = reinterpret_cast<Segment*>(ws + l.own_segments);
   p.rows = reinterpret_cast<RowPlan*>(ws + l.rows);
   p.tile_parts = reinterpret_cast<float*>(ws + l.tile_parts);
   p.row_parts = reinterpret_cast<float*>(ws + l.row_parts);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(l.slices * hkv);
   cudaError_t e = cudaSuccess;
-  if (max_group_rows <= kFewRows && batch + groups <= kOwnPlanSegments) {
-    e = launch_dependent(shared_attention_kernel<true>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
+  if (l.planned == kOwnFew) {
+    e = launch_dependent(shared_attention_kernel<kOwnFew>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
+  } else if (l.planned == kOwnAny) {
+    e = launch_dependent(shared_attention_kernel<kOwnAny>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
   } else {
     // a thread per row, group and slice, in whole warps
     const unsigned plan_threads = static_cast<unsigned>(
         std::min(kPlanThreads, (std::max({static_cast<int>(batch), static_cast<int>(groups), l.slices}) + 31) / 32 * 32));
     e = launch_dependent(shared_plan_kernel, 1, plan_threads, sizeof(PlanOfAll), st, 0, p);
     if (e == cudaSuccess)
-      e = launch_dependent(shared_attention_kernel<false>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
+      e = launch_dependent(shared_attention_kernel<kByKernel>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
   }
   if (e == cudaSuccess)
     e = launch_dependent(shared_merge_kernel, static_cast<unsigned>(batch * hkv), kMergeThreads, 0, st, 0, p);
