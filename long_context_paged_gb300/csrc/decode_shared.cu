@@ -139,11 +139,10 @@ struct SharedParams {
 constexpr int kPlanThreads = 1024;  // at most: four rows a thread
 
 // Numbers of segments and their units travel as one word, segments above kShift bits of units.
-template <int kGroups, int kRows, class Word, int kShift, bool kFew>
+template <int kGroups, int kRows, class Word, int kShift>
 struct PlanSmem {
   using Packed = Word;
   static constexpr int kUnitBits = kShift;
-  static constexpr bool kFewOnly = kFew;  // no segments of many rows
   Packed warp_sums[3][kPlanThreads / 32];
   Packed totals[3];
   Slice own;  // of the CTA (a plan made by every CTA)
@@ -157,16 +156,14 @@ struct PlanSmem {
   int32_t own_seg[kRows + 1], own_unit[kRows + 1];
   int32_t unit[kGroups + kRows + kRows / kTileRows + 1];  // first unit of each segment
 };
-using PlanOfAll = PlanSmem<kMaxGroups, kMaxBatch, unsigned long long, 40, false>;
+using PlanOfAll = PlanSmem<kMaxGroups, kMaxBatch, unsigned long long, 40>;
 static_assert(sizeof(PlanOfAll) <= 232448, "shared memory over the 227 KB limit");
 
-// How a call is planned. One of no more segments than this is planned by every CTA for itself, which spares it
-// the launch of a plan kernel and the wait for it (8 rows or fewer per group over 1,000 keys 15.0 -> 13.8 us).
-// With few rows per group the segments stay in shared memory, else they go to the CTA's part of the workspace.
+// A call of no more segments than this is planned by every CTA for itself, its slice's segments kept in its part
+// of the workspace: that spares the launch of a plan kernel and the wait for it (4 rows over 1,000 keys 15.0 ->
+// 13.8 us, 307 rows 102 -> 94). Larger ones have the plan kernel.
 constexpr int kOwnPlanSegments = 512;
-enum Planned { kByKernel, kOwnFew, kOwnAny };
-template <bool kFew>
-using OwnPlan = PlanSmem<kOwnPlanSegments, kOwnPlanSegments, uint32_t, 20, kFew>;
+using OwnPlan = PlanSmem<kOwnPlanSegments, kOwnPlanSegments, uint32_t, 20>;
 static_assert(kOwnPlanSegments < 1 << 12 && kOwnPlanSegments * (kMaxKeys / kTileKeys) < 1 << 20, "fits in a word");
 
 template <class T>
@@ -179,23 +176,21 @@ __device__ __forceinline__ T warp_scan_sum(T v, int lane) {
   return v;
 }
 
-// Exclusive prefix sums over the CTA of packed numbers (from the first that can be other than 0), and their
-// totals.
+// Exclusive prefix sums over the CTA of three packed numbers, and their totals.
 template <class Smem>
 __device__ __forceinline__ void plan_scan(Smem& s, typename Smem::Packed (&v)[3]) {
   using T = typename Smem::Packed;
-  constexpr int kFrom = Smem::kFewOnly ? 1 : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T incl[3];
 #pragma unroll
-  for (int k = kFrom; k < 3; ++k) {
+  for (int k = 0; k < 3; ++k) {
     incl[k] = warp_scan_sum(v[k], lane);
     if (lane == 31) s.warp_sums[k][warp] = incl[k];
   }
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int k = kFrom; k < 3; ++k) {
+    for (int k = 0; k < 3; ++k) {
       const T w = lane < static_cast<int>(blockDim.x >> 5) ? s.warp_sums[k][lane] : 0;
       const T x = warp_scan_sum(w, lane);
       s.warp_sums[k][lane] = x - w;
@@ -204,7 +199,7 @@ __device__ __forceinline__ void plan_scan(Smem& s, typename Smem::Packed (&v)[3]
   }
   __syncthreads();
 #pragma unroll
-  for (int k = kFrom; k < 3; ++k) v[k] = s.warp_sums[k][warp] + incl[k] - v[k];
+  for (int k = 0; k < 3; ++k) v[k] = s.warp_sums[k][warp] + incl[k] - v[k];
 }
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
@@ -294,10 +289,8 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
     const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
-    if (!Smem::kFewOnly) {
-      const Packed many = (rows - few + kTileRows - 1) / kTileRows;
-      at[0] += many * kOne + many * units;
-    }
+    const Packed many = (rows - few + kTileRows - 1) / kTileRows;
+    at[0] += many * kOne + many * units;
     if (few > 0) at[1] += kOne + units;
   }
 #pragma unroll 1
@@ -306,8 +299,7 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
     if (units > 0) at[2] += kOne + units;
   }
   plan_scan(s, at);
-  const Packed many_total = Smem::kFewOnly ? 0 : s.totals[0];
-  const int many_tiles = count_of(many_total), many_units = units_in(many_total);
+  const int many_tiles = count_of(s.totals[0]), many_units = units_in(s.totals[0]);
   const int count = many_tiles + count_of(s.totals[1]) + count_of(s.totals[2]);
   const int units_all = many_units + units_in(s.totals[1]) + units_in(s.totals[2]);
   const Slice own = slice_of(p, make_int2(count, units_all), slice);
@@ -321,12 +313,10 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
-      if (!Smem::kFewOnly) {
-        s.many_seg[g] = seg;
-        s.many_unit[g] = unit;
-      }
+      s.many_seg[g] = seg;
+      s.many_unit[g] = unit;
 #pragma unroll 1
-      for (int r = 0; !Smem::kFewOnly && r < rows - few; r += kTileRows) {
+      for (int r = 0; r < rows - few; r += kTileRows) {
         put(seg, Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
                          s.shared[g] * kPage, seg});
         ++seg;
@@ -381,7 +371,7 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
         const int place = in_group / kTileRows;
         r.tile_units = units_of(start * kPage);
         r.in_tile = in_group % kTileRows;
-        if (!Smem::kFewOnly && in_group < rows - few) {
+        if (in_group < rows - few) {
           r.tile = s.many_seg[g] + place;
           r.tile_unit = s.many_unit[g] + place * r.tile_units;
         } else {
@@ -455,9 +445,7 @@ struct SharedSmem {
   UnitInfo info[kInfos];
 };
 static_assert(sizeof(SharedSmem) <= 232448, "shared memory over the 227 KB limit");
-static_assert(sizeof(OwnPlan<false>) <= 2 * kStages * kTileBytes, "an own plan fits in the ring");
-static_assert(kWeightsAt + 2 * kFewQBytes + kOwnPlanSegments * sizeof(Segment) <= 2 * kQBlockBytes,
-              "its segments fit behind the small buffers");
+static_assert(sizeof(OwnPlan) <= 2 * kStages * kTileBytes, "an own plan fits in the ring");
 
 __device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, int32_t* status) {
   if (mbar_wait_bounded(bar, parity)) return true;
@@ -475,7 +463,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int la
   return ok;
 }
 
-template <Planned kPlanned>
+// kOwnPlan: the CTA makes its plan itself.
+template <bool kOwnPlan>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, const SharedParams p) {
@@ -522,12 +511,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
                                       // S_t [0, 16) and two O_t at [64, 96) of the stream's S
   await_previous();
   Slice plan;
-  // segments of an own plan: in the Q buffer, behind what segments of few rows use of it
-  Segment* own_segments = kPlanned == kOwnFew ? reinterpret_cast<Segment*>(s.q + kWeightsAt + 2 * kFewQBytes)
-                                              : p.own_segments + static_cast<int64_t>(blockIdx.x) * kOwnPlanSegments;
-  if (kPlanned != kByKernel) {
-    using Smem = OwnPlan<kPlanned == kOwnFew>;
-    Smem& ps = *reinterpret_cast<Smem*>(smem_raw);  // (in the ring, which is not in use yet)
+  Segment* own_segments = p.own_segments + static_cast<int64_t>(blockIdx.x) * kOwnPlanSegments;
+  if (kOwnPlan) {
+    OwnPlan& ps = *reinterpret_cast<OwnPlan*>(smem_raw);  // (in the ring, which is not in use yet)
     const int2 all = make_plan<true>(p, ps, own_segments, slice, blockIdx.x == 0);
     plan = slice_of(p, all, slice);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.slice[0] = plan;  // (for the merge)
@@ -564,9 +550,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
     constexpr int kBatch = 32 / kTilePages;
     int seg = plan.segment, records = seg;
     Segment lane_record{};
-    if (kPlanned == kByKernel) lane_record = p.segments[max(0, min(seg + lane, plan.segments - 1))];
+    if (!kOwnPlan) lane_record = p.segments[max(0, min(seg + lane, plan.segments - 1))];
     auto record = [&](int i) {
-      if (kPlanned != kByKernel) return own_segments[i];
+      if (kOwnPlan) return own_segments[i];
       if (i >= records + 32) {
         records = i;
         lane_record = p.segments[min(i + lane, plan.segments - 1)];
@@ -1209,7 +1195,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 // ---------------------------------------------------------------------------------------------
 struct SharedLayout {
   int slices, tile_rows;
-  Planned planned;
+  bool own_plan;
   size_t slice, segments, own_segments, rows, tile_parts, row_parts, total;
 };
 
@@ -1224,10 +1210,9 @@ bool shared_layout(SharedLayout& l, int hkv, int batch, int groups, int max_grou
   const size_t tiles = groups > 0 ? static_cast<size_t>(groups) + batch / kTileRows : 0;
   l.slice = 0;
   l.segments = align256(sizeof(Slice) * l.slices);
-  l.planned = tiles + batch > kOwnPlanSegments ? kByKernel : max_group_rows <= kFewRows ? kOwnFew : kOwnAny;
-  l.own_segments = align256(l.segments + (l.planned == kByKernel ? sizeof(Segment) * (tiles + batch) : 0));
-  const size_t own = l.planned == kOwnAny ? sizeof(Segment) * kOwnPlanSegments : 0;
-  l.rows = align256(l.own_segments + own * l.slices * hkv);
+  l.own_plan = tiles + batch <= kOwnPlanSegments;
+  l.own_segments = align256(l.segments + (l.own_plan ? 0 : sizeof(Segment) * (tiles + batch)));
+  l.rows = align256(l.own_segments + (l.own_plan ? sizeof(Segment) * kOwnPlanSegments * l.slices * hkv : 0));
   l.tile_parts = align256(l.rows + sizeof(RowPlan) * batch);
   const size_t per_row = static_cast<size_t>(hkv) * 2 * 2 * kRowFloats * sizeof(float);
   l.row_parts = align256(l.tile_parts + (groups > 0 ? (l.slices + tiles) * l.tile_rows * per_row : 0));
@@ -1298,8 +1283,7 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(shared_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
-    for (auto* kernel : {&shared_attention_kernel<kByKernel>, &shared_attention_kernel<kOwnFew>,
-                         &shared_attention_kernel<kOwnAny>}) {
+    for (auto* kernel : {&shared_attention_kernel<false>, &shared_attention_kernel<true>}) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(SharedSmem)));
       cudaFuncAttributes fa;
@@ -1342,17 +1326,15 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(l.slices * hkv);
   cudaError_t e = cudaSuccess;
-  if (l.planned == kOwnFew) {
-    e = launch_dependent(shared_attention_kernel<kOwnFew>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
-  } else if (l.planned == kOwnAny) {
-    e = launch_dependent(shared_attention_kernel<kOwnAny>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
+  if (l.own_plan) {
+    e = launch_dependent(shared_attention_kernel<true>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
   } else {
     // a thread per row, group and slice, in whole warps
     const unsigned plan_threads = static_cast<unsigned>(
         std::min(kPlanThreads, (std::max({static_cast<int>(batch), static_cast<int>(groups), l.slices}) + 31) / 32 * 32));
     e = launch_dependent(shared_plan_kernel, 1, plan_threads, sizeof(PlanOfAll), st, 0, p);
     if (e == cudaSuccess)
-      e = launch_dependent(shared_attention_kernel<kByKernel>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
+      e = launch_dependent(shared_attention_kernel<false>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
   }
   if (e == cudaSuccess)
     e = launch_dependent(shared_merge_kernel, static_cast<unsigned>(batch * hkv), kMergeThreads, 0, st, 0, p);

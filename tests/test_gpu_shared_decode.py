@@ -273,8 +273,7 @@ def test_a_table_past_2_gib_of_entries_and_far_pages(cuda_lib):
 
 
 def test_a_larger_bound_gives_the_same_bits(cuda_lib):
-    """Few segments are planned by every CTA (with few rows per group in shared memory), others in a launch of
-    their own: the same plan."""
+    """The bound sizes the workspace; up to 512 segments are planned by every CTA, more in a launch of their own."""
     for x in (Inputs([(6, [100, 111, 97] * 30), (2, [33, 60]), (17, [300] * 70)], [12, 0, 700] * 40, seed=23),
               Inputs([(2, [40, 33])] * 150 + [(9, [150] * 66)], [30] * 60, hkv=2, seed=24),
               Inputs([(6, [100, 111, 97]), (2, [33, 60]), (0, []), (9, [150] * 8)], [12, 0, 700], seed=21),
