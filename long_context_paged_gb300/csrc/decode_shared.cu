@@ -33,7 +33,7 @@
 // Tried and left out: 64-key units (16 x 4 rows 216 -> 270 us: an issuing thread's waits and commits cost
 // more than its products); two row tiles on one K/V tile, a stream each, for 65 to 128 rows (4 groups of up to
 // 131 rows 112 -> 148 us: a stream's scores wait for its own weights and products, which two streams on
-// alternate units hide); a merge of 512 threads (8 rows 61.7 -> 60.8 us, 307 rows 101 -> 115).
+// alternate units hide).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -1087,18 +1087,25 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
 }
 
 // ---------------------------------------------------------------------------------------------
-// merge: a CTA per row and KV head. Its threads find the row's partial results and weigh them, then four
-// warps per query head add a quarter of them each, four dims a lane, eight results' loads in flight.
+// merge: a CTA per row and KV head. Its threads find the row's partial results and weigh them, then its
+// warps, half of them per query head, add a part of them each, four dims a lane, eight results' loads in flight.
 // (A warp per query head alone, in a CTA per row, took 15 us for 8 rows of 38 results each.)
+// The more rows, the fewer warps each: a row is a chain of four latencies however many, and rows that wait
+// for an SM add theirs. The whole call with 16, 8 and 2 warps: 8 rows of up to 38 results 59.7, 60.9 and 67.7 us;
+// 64 rows 159.7, 156.1 and 155.3; 307 rows 107, 94.7 and 84.9.
 // ---------------------------------------------------------------------------------------------
-constexpr int kMergeThreads = 256;
-constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMaxParts = 4 * kMaxSlices;  // two sets, two streams, every slice
+constexpr int kMergeWarpsFewRows = 16;  // up to a CTA per SM
+constexpr int kMergeWarps = 8;          // up to four
+constexpr int kMergeWarpsManyRows = 2;
 
-__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams p) {
-  __shared__ const float* where[kMaxParts];  // O of the row's first query head; the second's follows
-  __shared__ float4 stat[kMaxParts];         // (m, l) of both
-  __shared__ float4 sums[kMergeWarps][32];
+template <int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) shared_merge_kernel(const SharedParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  constexpr int kMergeThreads = kWarps * 32;
+  const int max_parts = 4 * p.slices;  // two sets, two streams, every slice
+  float4* stat = reinterpret_cast<float4*>(smem_raw);  // (m, l) of the row's two query heads
+  const float** where = reinterpret_cast<const float**>(stat + max_parts);  // O of the first; the second's follows
+  __shared__ float4 sums[kWarps][32];
   const int b = static_cast<int>(blockIdx.x) / p.hkv, head = static_cast<int>(blockIdx.x) % p.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   await_previous();
@@ -1133,7 +1140,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   __syncthreads();
   // each warp on its own: its first results' loads go out, then the row's maximum and sum over all results
   const int h = warp & 1;
-  constexpr int kStride = kMergeWarps / 2;
+  constexpr int kStride = kWarps / 2;
   float4 v[8];
   auto load = [&](int c0) {
 #pragma unroll
@@ -1280,9 +1287,10 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
     cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(sizeof(PlanOfAll)));
     // same carveout for the merge: no reconfiguration between them
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(shared_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
+    for (auto* kernel : {&shared_merge_kernel<kMergeWarpsFewRows>, &shared_merge_kernel<kMergeWarps>,
+                         &shared_merge_kernel<kMergeWarpsManyRows>})
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     for (auto* kernel : {&shared_attention_kernel<false>, &shared_attention_kernel<true>}) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(SharedSmem)));
@@ -1336,7 +1344,14 @@ extern "C" pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const
     if (e == cudaSuccess)
       e = launch_dependent(shared_attention_kernel<false>, grid, kThreads, sizeof(SharedSmem), st, 0, qm, km, vm, p);
   }
-  if (e == cudaSuccess)
-    e = launch_dependent(shared_merge_kernel, static_cast<unsigned>(batch * hkv), kMergeThreads, 0, st, 0, p);
+  if (e == cudaSuccess) {
+    const size_t smem = static_cast<size_t>(4 * l.slices) * (sizeof(float4) + sizeof(const float*));
+    const unsigned ctas = static_cast<unsigned>(batch * hkv);
+    auto merge = [&](auto* kernel, int warps) { return launch_dependent(kernel, ctas, 32 * warps, smem, st, 0, p); };
+    // the widest whose CTAs all run at once
+    e = batch <= l.slices       ? merge(shared_merge_kernel<kMergeWarpsFewRows>, kMergeWarpsFewRows)
+        : batch <= 4 * l.slices ? merge(shared_merge_kernel<kMergeWarps>, kMergeWarps)
+                                : merge(shared_merge_kernel<kMergeWarpsManyRows>, kMergeWarpsManyRows);
+  }
   return e == cudaSuccess ? PA_OK : record_cuda_error(e, "attn_decode_paged_shared");
 }

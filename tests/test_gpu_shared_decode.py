@@ -300,3 +300,11 @@ def test_no_lse_empty_batch_and_given_outputs(cuda_lib):
     assert got is out and lse is None and torch.equal(out, want)
     got, lse = cuda_lib.attn_decode_paged_shared(x.q[:0], x.k, x.v, dev(x.table), dev([]), dev([0]), dev([]), 1, SCALE)
     assert got.shape[0] == 0
+
+
+@pytest.mark.parametrize("rows", [19, 20, 76, 77])
+def test_rows_on_either_side_of_the_merge_s_widths(cuda_lib, rows):
+    """8 KV heads make 19 slices of a GB300: up to 19 rows, up to 76 and more are merged by CTAs of three sizes."""
+    one = rows // 2
+    Inputs([(40, [640 + (i * 37) % 400 for i in range(one)]), (3, [48 + (i * 53) % 300 for i in range(one)])],
+           [200] * (rows - 2 * one), seed=rows).check(cuda_lib)
