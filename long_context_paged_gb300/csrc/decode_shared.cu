@@ -9,18 +9,19 @@
 // costs 512 bytes of a KV head's cache and 4 * 128 * 2 R operations, so up to about 64 rows the call is
 // bound by HBM and reads the shared keys at its rate, R times fewer bytes than the plain decode.
 //
-// Measured on a GB300 (calls of a graph, 152 CTAs): 16 groups of 4 rows over 5,000 to 30,000 keys 157 us,
-// 6.2 TB/s of the bytes that have to be read (0.91 of a copy's rate; 64 rows read alone would be 3.7 GB);
-// 8 rows over 67,500 keys 61 us, of which the units take 41 (6.7 TB/s), the plan 3.5, the first copies 3.7,
-// the merge and its start 5.5 and the slowest CTA 2.5; 4 rows over 1,000 keys 13.8 us, a chain of latencies;
-// 307 rows in 4 groups 101 us (64 rows a pass: three passes over the keys of 131 rows).
+// Measured on a GB300 (calls of a graph, 152 CTAs): 16 groups of 4 rows over 5,000 to 30,000 keys 155 us,
+// 6.3 TB/s of the bytes that have to be read (0.93 of a copy's rate; 64 rows read alone would be 3.7 GB);
+// 8 rows over 67,500 keys 60 us, of which the units take 41 (6.7 TB/s), the plan 3.5, the first copies 3.7,
+// the merge and its start 5 and the slowest CTA 4; 4 rows over 1,000 keys 14 us, a chain of latencies;
+// 307 rows in 4 groups 85 us, of which the units take 62 (64 rows a pass: three passes over the keys of 131
+// rows; about 290 of the 955 units a head are of such tiles, the others of few or single rows), the plan 4, the slowest CTA 6, the merge 6.
 //
 // Work split. A segment is a run of keys with the rows that see all of it: (64 rows of a group, its
 // shared pages) or (one row, its own pages). Segments are cut into units of 128 keys, laid end to end
 // and divided into equal slices, one per CTA of a KV head; the Hkv CTAs of a slice read the heads of
 // the same pages at about the same time. A slice's part of a segment (a piece) leaves (m, l, O) in the
-// workspace; the merge joins a row's pieces of both sets. The segments are laid out by a plan kernel
-// of one CTA, from lengths that only the GPU knows.
+// workspace; the merge joins a row's pieces of both sets. The segments are laid out from lengths that only the
+// GPU knows: by every CTA for itself, or, where there are many, by a plan kernel of one CTA.
 //
 // Per unit, in a CTA: S = Q K^T (A = Q, B = K in shared memory, fp32 in TMEM), P = 2^(scale S - m) by a
 // thread per row, written over S as bf16, O += P V (A = P in TMEM, B = V in shared memory). With 8 rows or
@@ -161,7 +162,7 @@ static_assert(sizeof(PlanOfAll) <= 232448, "shared memory over the 227 KB limit"
 
 // A call of no more segments than this is planned by every CTA for itself, its slice's segments kept in its part
 // of the workspace: that spares the launch of a plan kernel and the wait for it (4 rows over 1,000 keys 15.0 ->
-// 13.8 us, 307 rows 102 -> 94). Larger ones have the plan kernel.
+// 13.8 us, 307 rows 102 -> 94, with the merge of then). Larger ones have the plan kernel.
 constexpr int kOwnPlanSegments = 512;
 using OwnPlan = PlanSmem<kOwnPlanSegments, kOwnPlanSegments, uint32_t, 20>;
 static_assert(kOwnPlanSegments < 1 << 12 && kOwnPlanSegments * (kMaxKeys / kTileKeys) < 1 << 20, "fits in a word");

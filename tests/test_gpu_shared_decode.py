@@ -308,3 +308,8 @@ def test_rows_on_either_side_of_the_merge_s_widths(cuda_lib, rows):
     one = rows // 2
     Inputs([(40, [640 + (i * 37) % 400 for i in range(one)]), (3, [48 + (i * 53) % 300 for i in range(one)])],
            [200] * (rows - 2 * one), seed=rows).check(cuda_lib)
+
+
+def test_many_results_of_many_rows(cuda_lib):
+    """One KV head: 152 slices, so 620 rows are merged by the smallest CTAs, 100 of them from dozens of results."""
+    Inputs([(1250, [20000 + 3 * i for i in range(100)])], [i % 40 for i in range(520)], hkv=1, seed=5).check(cuda_lib)
