@@ -17,6 +17,7 @@
 // launches of dependent loads. Candidate selection by k rounds of a block-wide maximum took 477 us for the
 // first of these; scores in fp64 in the second launch cost it 4 us of 14 (this GPU's fp64 rate is 1/60 of fp32's).
 #include <cuda_runtime.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -29,29 +30,32 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPickThreads = 512;
+constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxK = 64;
 constexpr int kMaxRows = 65535;
-constexpr int kList = 1024;  // candidates of a piece that the quick selection holds
-constexpr int kFound = 512;  // candidates of a request that the quick ranking holds
-// Pieces of a row: as many as give kTargetCtas CTAs in all (three rounds of what the GPU holds, so that one
-// CTA's selection runs beside another's loads), none of them below four vectors a thread.
+constexpr int kUnit = 128;   // 16-byte vectors of a unit: four a lane, 2 KB
+constexpr int kUnits = 512;  // units that the quick choice of them holds
+constexpr int kFound = 512;  // candidates that the quick ranking holds
+// Pieces of a row: as many as give kTargetCtas CTAs in all, none of them below a unit a warp.
 constexpr int kTargetCtas = 2736;
-constexpr int kMinVectors = 4 * kThreads;
 
 struct BeamParams {
   const void* logits;
   int64_t row_stride;
-  int32_t requests, beams, vocab, k, eos, pieces;
+  int32_t requests, beams, vocab, k, eos;
+  int32_t units, pieces;  // of a row
+  uint32_t over_units;    // (2^32 - 1) / units
   const float* scores;
   const int32_t* live;
   float* out_scores;
   int32_t* parents;
   int32_t* tokens;
   int32_t* live_out;
-  // workspace: of each row and piece, the k largest logits in order, and (maximum, sum of exp)
-  float2* best;   // [rows][pieces][k]: value, token as bits (-1: none)
-  float2* stats;  // [rows][pieces]
+  // workspace
+  float2* stats;  // [rows][pieces] maximum and sum of exponentials
+  float* tops;    // [rows][units] largest logit
 };
 
 // fp32 as an unsigned integer of the same order; -inf and NaN are 0, below everything else.
@@ -64,6 +68,11 @@ __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
+__device__ __forceinline__ uint64_t warp_min64(uint64_t v) {
+  const uint32_t hi = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : ~0u;
+  return static_cast<uint64_t>(hi) << 32 | __reduce_min_sync(0xffffffffu, lo);
+}
 __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
   const uint32_t lo = static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u;
@@ -88,6 +97,7 @@ struct Row {
     vectors = (n - head) / kVec;
     tail = n - head - vectors * kVec;
   }
+  __device__ int last_unit() const { return max(0, (vectors + kUnit - 1) / kUnit - 1); }
 };
 
 __device__ __forceinline__ void unpack(uint4 w, float (&x)[8]) {
@@ -100,12 +110,6 @@ __device__ __forceinline__ void unpack(uint4 w, float (&x)[4]) {
 }
 __device__ __forceinline__ float single(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ float single(float v) { return v; }
-
-// A logit's rank among a row's: by value, then the lower token.
-__device__ __forceinline__ uint64_t rank_of(float x, int token) {
-  const uint32_t o = order_of(x);
-  return o == 0 ? 0ull : static_cast<uint64_t>(o) << 32 | ~static_cast<uint32_t>(token);
-}
 
 // A thread's state over its logits: the largest, and the sum of exponentials against a reference that
 // follows the largest at a distance (40 at most: sums stay below 2^77), so that nothing is rescaled at
@@ -170,166 +174,78 @@ __device__ __forceinline__ float most_of(const uint4 (&w)[4], float) {
 template <class T>
 __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
   constexpr int kVec = Row<T>::kVec;
-  __shared__ uint64_t warp_best[kWarps], list[kList];
-  __shared__ uint32_t warp_bound[kWarps];
   __shared__ float2 warp_stats[kWarps];
-  __shared__ int found, holding;
-  __shared__ uint8_t holders[kThreads];
   const int row = static_cast<int>(blockIdx.y), piece = static_cast<int>(blockIdx.x);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found = holding = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   launch_next();
   await_previous();
   if (!expands(p, row)) return;
   const Row<T> r(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab);
   const uint4* body = reinterpret_cast<const uint4*>(r.base + r.head);
-  int per = (r.vectors + p.pieces - 1) / p.pieces;
-  // long pieces in whole rounds of four vectors a thread (the last one is shorter)
-  if (per > 3 * kMinVectors) per = (per + kMinVectors - 1) / kMinVectors * kMinVectors;
-  const int v0 = min(r.vectors, piece * per), v1 = min(r.vectors, v0 + per);
-  // the first piece has the single logits before the vectors, the last those after
-  const int lead = piece == 0 ? r.head : 0, trail = piece == p.pieces - 1 ? r.tail : 0;
-  const int trail_at = r.head + r.vectors * kVec;
+  const int per = (p.units + p.pieces - 1) / p.pieces, u1 = min(p.units, (piece + 1) * per);
+  float* tops = p.tops + static_cast<int64_t>(row) * p.units;
   Seen seen;
-  if (tid < lead) {
-    const float x = single(r.base[tid]);
-    seen.reach(x);
-    seen.take(x);
-  }
-  int v = v0 + tid;
-  for (; v + 3 * kThreads < v1; v += 4 * kThreads) {
-    uint4 w[4];
+  for (int u = piece * per + warp; u < u1; u += kWarps) {
+    const int v = u * kUnit + lane;
+    float most;
+    if ((u + 1) * kUnit <= r.vectors) {
+      uint4 w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = body[v + j * kThreads];
-    seen.reach(most_of(w, T()));
+      for (int j = 0; j < 4; ++j) w[j] = body[v + j * 32];
+      most = most_of(w, T());
+      seen.reach(most);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x[kVec];
-      unpack(w[j], x);
-      seen.take(x);
+      for (int j = 0; j < 4; ++j) {
+        float x[kVec];
+        unpack(w[j], x);
+        seen.take(x);
+      }
+    } else {  // the row's last unit
+      most = -INFINITY;
+      for (int i = v; i < min(r.vectors, (u + 1) * kUnit); i += 32) {
+        const uint4 w = body[i];
+        float x[kVec];
+        unpack(w, x);
+        const float m = most_of(w, T());
+        seen.reach(m);
+        seen.take(x);
+        most = fmaxf(most, m);
+      }
     }
-  }
-  for (; v < v1; v += kThreads) {
-    const uint4 w = body[v];
-    float x[kVec];
-    unpack(w, x);
-    seen.reach(most_of(w, T()));
-    seen.take(x);
-  }
-  if (tid < trail) {
-    const float x = single(r.base[trail_at + tid]);
-    seen.reach(x);
-    seen.take(x);
-  }
-  // A bound that k logits at least reach: the q-th best thread of each warp that has vectors (q of them
-  // make k; a thread counts by its largest logit), and of those the least.
-  const uint32_t mine = order_of(seen.top);
-  const int warps = min(kWarps, max(1, (v1 - v0 + 31) / 32));
-  uint32_t bound = 0;
-  if (warp < warps) {
-    uint32_t left = mine;
-    for (int q = (p.k + warps - 1) / warps; q > 0; --q) {
-      bound = __reduce_max_sync(0xffffffffu, left);
-      if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
+    // the single logits before the vectors are the first unit's, those after them the last one's
+    const int first = u == 0 && lane < r.head ? lane : -1;
+    const int last = u == r.last_unit() && lane < r.tail ? r.head + r.vectors * kVec + lane : -1;
+    if (first >= 0 || last >= 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = i == 0 ? first : last;
+        if (at < 0) continue;
+        const float x = single(r.base[at]);
+        seen.reach(x);
+        seen.take(x);
+        most = fmaxf(most, x);
+      }
     }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(most));
+    if (lane == 0) tops[u] = top > 0 ? value_of(top) : -INFINITY;
   }
   // maximum and sum of the CTA
-  float wm = seen.top;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+  const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(seen.top));
+  const float wm = top > 0 ? value_of(top) : -INFINITY;
   float ws = seen.ref == wm ? seen.sum : seen.sum * fast_exp2((seen.ref - wm) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-  if (lane == 0) {
-    warp_stats[warp] = make_float2(wm, ws);
-    warp_bound[warp] = bound;
-  }
+  if (lane == 0) warp_stats[warp] = make_float2(wm, ws);
   __syncthreads();
-  const int64_t out = static_cast<int64_t>(row) * p.pieces + piece;
-  if (tid == 0) {
-    float cm = -INFINITY, cs = 0.f;
+  if (warp != 0) return;
+  const float2 mine = lane < kWarps ? warp_stats[lane] : make_float2(-INFINITY, 0.f);
+  float cm = mine.x;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) cm = fmaxf(cm, warp_stats[w].x);
+  for (int o = 1; o < kWarps; o <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
+  float cs = mine.x == cm ? mine.y : mine.y * fast_exp2((mine.x - cm) * kLog2e);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      cs += warp_stats[w].x == cm ? warp_stats[w].y : warp_stats[w].y * fast_exp2((warp_stats[w].x - cm) * kLog2e);
-    p.stats[out] = make_float2(cm, cs);
-  }
-  bound = warp_bound[0];
-  for (int w = 1; w < warps; ++w) bound = min(bound, warp_bound[w]);
-  // Logits that reach the bound go to a list. Only threads whose own largest reaches it have one: they are
-  // listed, and all threads look through those threads' vectors (a second read of a small part of the
-  // piece, from L2 mostly).
-  const float least = bound > 0 ? value_of(bound) : -INFINITY;
-  const bool holds = mine > 0 && mine >= bound;
-  auto keep = [&](float x, int token) {
-    if (!(x >= least) || x == -INFINITY) return;
-    const int i = atomicAdd(&found, 1);
-    if (i < kList) list[i] = rank_of(x, token);
-  };
-  if (tid < lead) keep(single(r.base[tid]), tid);
-  if (tid < trail) keep(single(r.base[trail_at + tid]), trail_at + tid);
-  if (holds) holders[atomicAdd(&holding, 1)] = static_cast<uint8_t>(tid);
-  __syncthreads();
-  const int each = (v1 - v0 + kThreads - 1) / kThreads, looks = holding * each;
-  for (int i = tid; i < looks; i += kThreads) {
-    const int of = i / each, v = v0 + holders[of] + (i - of * each) * kThreads;
-    if (v >= v1) continue;
-    const uint4 w = body[v];
-    if (!(most_of(w, T()) >= least)) continue;  // most vectors
-    float x[kVec];
-    unpack(w, x);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) keep(x[j], r.head + v * kVec + j);
-  }
-  __syncthreads();
-  const int n = found;
-  if (n <= kList) {
-    // an entry's place is the number of those above it
-    for (int i = tid; i < max(n, p.k); i += kThreads) {
-      if (i >= n) {
-        p.best[out * p.k + i] = make_float2(-INFINITY, __int_as_float(-1));
-        continue;
-      }
-      const uint64_t c = list[i];
-      int place = 0;
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) place += list[j] > c ? 1 : 0;
-      if (place < p.k)
-        p.best[out * p.k + place] = make_float2(value_of(static_cast<uint32_t>(c >> 32)),
-                                                __int_as_float(static_cast<int>(~static_cast<uint32_t>(c))));
-    }
-    return;
-  }
-  // More than the list holds (most of a row's logits alike or banned, in a pattern that leaves a warp
-  // without a high one): the k largest one after the other, each found below the last.
-  uint64_t top = ~0ull;
-  for (int k = 0; k < p.k; ++k) {
-    uint64_t best = 0;
-    auto look = [&](float x, int token) {
-      const uint64_t c = rank_of(x, token);
-      if (c < top) best = max(best, c);
-    };
-    if (holds || lead > 0 || trail > 0) {
-      if (tid < lead) look(single(r.base[tid]), tid);
-      if (tid < trail) look(single(r.base[trail_at + tid]), trail_at + tid);
-      for (int v = v0 + tid; v < v1; v += kThreads) {
-        float x[kVec];
-        unpack(body[v], x);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) look(x[i], r.head + v * kVec + i);
-      }
-    }
-    best = warp_max64(best);
-    if (lane == 0) warp_best[warp] = best;
-    __syncthreads();
-    top = warp_best[0];
-    for (int w = 1; w < kWarps; ++w) top = max(top, warp_best[w]);
-    __syncthreads();
-    if (tid == 0)
-      p.best[out * p.k + k] = make_float2(value_of(static_cast<uint32_t>(top >> 32)),
-                                          __int_as_float(top == 0 ? -1 : static_cast<int>(~static_cast<uint32_t>(top))));
-  }
+  for (int o = 1; o < kWarps; o <<= 1) cs += __shfl_xor_sync(0xffffffffu, cs, o);
+  if (lane == 0) p.stats[static_cast<int64_t>(row) * p.pieces + piece] = make_float2(cm, cs);
 }
 
 // Scores as a pair of floats whose sum they are, lo at most half a step of hi (48 bits: fp64 is 50 times
@@ -368,19 +284,96 @@ __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
   return (a.score > b.score) | ((a.score == b.score) & (a.place > b.place));  // (no branches)
 }
 
-__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
+// The largest of the threads' candidates, to every thread. `scratch` may be used again after the next barrier.
+__device__ __forceinline__ Candidate best_of_all(Candidate c, Candidate* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Candidate other;
+    other.score = __shfl_xor_sync(0xffffffffu, c.score, o);
+    other.place = __shfl_xor_sync(0xffffffffu, c.place, o);
+    if (better(other, c)) c = other;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = c;
+  __syncthreads();
+  c = scratch[0];
+  for (int w = 1; w < kPickWarps; ++w)
+    if (better(scratch[w], c)) c = scratch[w];
+  return c;
+}
+
+// A score's order that at least k of the threads' `best` reach (0: fewer than k have one): the q-th best thread of
+// each of the first `warps` warps (q of them make k), and of those the least. (Threads of equal ones all count.)
+__device__ __forceinline__ uint64_t bound_of(uint64_t best, int k, int warps, uint64_t* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t bound = 0;
+  if (warp < warps) {
+    uint64_t left = best;
+    for (int q = (k + warps - 1) / warps; q > 0; --q) {
+      bound = warp_max64(left);
+      // one thread of those that have it
+      const uint32_t same = __ballot_sync(0xffffffffu, left == bound);
+      if (lane == __ffs(same) - 1) left = 0;
+    }
+  }
+  __syncthreads();
+  if (lane == 0) scratch[warp] = bound;
+  __syncthreads();
+  return warp_min64(lane < warps ? scratch[lane] : ~0ull);
+}
+
+// f(entry, its place among all by `better`) for the entries that are this thread's to write: kRankLanes threads
+// count for one.
+constexpr int kRankLanes = 8;
+template <class F>
+__device__ __forceinline__ void rank_all(const Candidate* list, int n, F f) {
+  const int part = threadIdx.x % kRankLanes;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kPickThreads / kRankLanes) {
+    const int i = i0 + threadIdx.x / kRankLanes;
+    const Candidate c = list[min(i, n - 1)];
+    int place = 0;
+#pragma unroll 4
+    for (int j = part; j < n; j += kRankLanes) place += better(list[j], c) ? 1 : 0;
+#pragma unroll
+    for (int o = 1; o < kRankLanes; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (i < n && part == 0) f(c, place);
+  }
+}
+
+// A chosen unit.
+struct Chosen {
+  const void* row;  // its row's logits
+  Pair shift;
+  int32_t beam, unit;  // unit: -1 for a beam that has ended
+  int32_t head, vectors, tail;
+};
+
+template <class T>
+__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParams p) {
+  constexpr int kVec = Row<T>::kVec;
+  constexpr int kHeld = 4;
   __shared__ Pair shift[kMaxBeams];    // score minus normaliser of a beam
   __shared__ uint8_t kind[kMaxBeams];  // 0: no candidates, 1: its tokens, 2: itself (finished)
-  __shared__ Candidate warp_best[kWarps];
-  __shared__ Candidate list[kFound];
-  __shared__ int found;
-  extern __shared__ uint8_t used[];    // [beams][pieces] candidates taken
+  __shared__ Candidate warp_best[kPickWarps];
+  __shared__ uint64_t warp_bound[kPickWarps], cut;
+  __shared__ Candidate list[kUnits > kFound ? kUnits : kFound];
+  __shared__ Chosen of[kMaxK];
+  __shared__ int units_found, found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = static_cast<int>(blockIdx.x), lists = p.beams * p.pieces;
+  const int n = static_cast<int>(blockIdx.x), units = p.beams * p.units;
   await_previous();
-  if (tid == 0) found = 0;
-  for (int i = tid; i < lists; i += kThreads) used[i] = 0;
-  for (int b = warp; b < p.beams; b += kWarps) {
+  if (tid == 0) {
+    units_found = found = 0;
+    cut = 1;
+  }
+  // units go round the warps, so that every warp has some of each beam; a thread's first ones are asked for now
+  const float* tops = p.tops + static_cast<int64_t>(n) * units;
+  const int mine0 = lane * kPickWarps + warp;
+  float held[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) held[j] = mine0 + j * kPickThreads < units ? tops[mine0 + j * kPickThreads] : 0.f;
+  for (int b = warp; b < p.beams; b += kPickWarps) {
     const int row = n * p.beams + b;
     const float2* stats = p.stats + static_cast<int64_t>(row) * p.pieces;
     // (read beside the score and the flag; of a row that is not expanded it is whatever was there)
@@ -421,26 +414,16 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
   }
   __syncthreads();
-  const float2* entries = p.best + static_cast<int64_t>(n) * lists * p.k;
-  auto candidate = [&](int b, float2 e) {
-    Candidate c{0, 0};
-    const int token = __float_as_int(e.y);
-    if (token >= 0) {
-      c.score = order_of(add(shift[b], e.x));
-      c.place = ~static_cast<uint32_t>(b * p.vocab + token);
-    }
-    return c;
+  // a unit's best score, by its largest logit
+  auto beam_of = [&](int i) {
+    const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(i), p.over_units));  // off by one at most
+    return i - q * p.units >= p.units ? q + 1 : q;
   };
-  auto entry = [&](int list, int at) {
-    const int b = list / p.pieces;
-    Candidate c{0, 0};
-    if (kind[b] == 1 && at < p.k) {
-      c = candidate(b, entries[static_cast<int64_t>(list) * p.k + at]);
-    } else if (kind[b] == 2 && at == 0 && list == b * p.pieces) {
-      c.score = order_of(shift[b]);
-      c.place = ~static_cast<uint32_t>(b * p.vocab + max(p.eos, 0));
-    }
-    return c;
+  auto unit_score = [&](int i, float top) {
+    const int b = beam_of(i), what = kind[b];
+    const bool own = what == 2 && i == b * p.units;
+    const uint64_t score = order_of(own ? shift[b] : add(shift[b], top));
+    return what == 1 || own ? score : uint64_t(0);
   };
   auto write = [&](int place, const Candidate& c) {
     const int at = n * p.k + place;
@@ -458,114 +441,137 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     p.tokens[at] = token;
     p.live_out[at] = kind[b] == 1 && token != p.eos ? 1 : 0;
   };
-  // A bound that k candidates at least reach, as in the first launch: from the best heads of each warp's
-  // lists (by score alone: equal ones all count). Candidates that reach it, in their lists' order, are ranked.
-  {
-    // (the lists go round the warps, so that every warp has some of each beam)
-    const int first = lane * kWarps + warp;
-    uint64_t best = 0;
-    for (int i = first; i < lists; i += kThreads) best = max(best, entry(i, 0).score);
-    const int warps = min(kWarps, lists);
-    uint64_t bound = 0;
-    if (warp < warps) {
-      uint64_t left = best;
-      for (int q = (p.k + warps - 1) / warps; q > 0; --q) {
-        bound = warp_max64(left);
-        // one thread of those that have it
-        const uint32_t same = __ballot_sync(0xffffffffu, left == bound);
-        if (lane == __ffs(same) - 1) left = 0;
-      }
-    }
-    if (lane == 0) warp_best[warp] = Candidate{bound, 0};
-    __syncthreads();
-    bound = warp_best[0].score;
-    for (int w = 1; w < warps; ++w) bound = min(bound, warp_best[w].score);
-    bound = max(bound, static_cast<uint64_t>(1));
-    if (best >= bound) {
-      for (int i = first; i < lists; i += kThreads) {
-        const int b = i / p.pieces;
-        auto keep = [&](const Candidate& c) {
-          if (c.score < bound) return false;
-          const int to = atomicAdd(&found, 1);
-          if (to < kFound) list[to] = c;
-          return true;
-        };
-        if (kind[b] != 1) {
-          keep(entry(i, 0));
-          continue;
-        }
-        // four entries' loads at a time
-        const float2* e = entries + static_cast<int64_t>(i) * p.k;
-        bool more = true;
-        for (int at = 0; at < p.k && more; at += 4) {
-          float2 v[4];
+  // The k best units, by their largest logit's score, equal ones in their order: the k best candidates are all in
+  // them, since each of them has one at least that is better than any of the other units, equal ones being earlier.
+  uint64_t key[kHeld], best = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = at + j < p.k ? e[at + j] : make_float2(0.f, __int_as_float(-1));
+  for (int j = 0; j < kHeld; ++j) {
+    key[j] = mine0 + j * kPickThreads < units ? unit_score(mine0 + j * kPickThreads, held[j]) : uint64_t(0);
+    best = max(best, key[j]);
+  }
+#pragma unroll 1
+  for (int i = mine0 + kHeld * kPickThreads; i < units; i += kPickThreads) best = max(best, unit_score(i, tops[i]));
+  const uint64_t bound = max(bound_of(best, p.k, min(kPickWarps, units), warp_bound), static_cast<uint64_t>(1));
+  if (best >= bound) {
+    auto keep = [&](int i, uint64_t score) {
+      if (score < bound) return;
+      const int to = atomicAdd(&units_found, 1);
+      if (to < kUnits) list[to] = Candidate{score, ~static_cast<uint32_t>(i)};
+    };
 #pragma unroll
-          for (int j = 0; j < 4; ++j) more = more && keep(candidate(b, v[j]));
-        }
+    for (int j = 0; j < kHeld; ++j) keep(mine0 + j * kPickThreads, key[j]);
+#pragma unroll 1
+    for (int i = mine0 + kHeld * kPickThreads; i < units; i += kPickThreads) keep(i, unit_score(i, tops[i]));
+  }
+  __syncthreads();
+  const int m = units_found, chosen = min(m, p.k);
+  auto choose = [&](const Candidate& c, int place) {
+    if (place >= p.k) return;
+    const int i = static_cast<int>(~c.place), b = beam_of(i);
+    const T* row = static_cast<const T*>(p.logits) + (static_cast<int64_t>(n) * p.beams + b) * p.row_stride;
+    const Row<T> r(row, p.vocab);
+    const int u = i - b * p.units;
+    of[place] = Chosen{row, shift[b], b, kind[b] == 2 ? -1 : u, r.head, r.vectors, r.tail};
+    if (place == p.k - 1) cut = c.score;
+  };
+  if (m <= kUnits) {
+    rank_all(list, m, choose);
+  } else {  // most units alike: one after the other
+    Candidate last{~0ull, ~0u};
+#pragma unroll 1
+    for (int k = 0; k < p.k; ++k) {
+      Candidate c{0, 0};
+#pragma unroll 1
+      for (int i = mine0; i < units; i += kPickThreads) {
+        const Candidate x{unit_score(i, tops[i]), ~static_cast<uint32_t>(i)};
+        if (better(last, x) && better(x, c)) c = x;
       }
-    }
-    __syncthreads();
-    const int m = found;
-    if (m <= kFound) {
-      for (int i = tid; i < max(m, p.k); i += kThreads) {
-        if (i >= m) {
-          write(i, Candidate{0, 0});
-          continue;
-        }
-        const Candidate c = list[i];
-        int place = 0;
-#pragma unroll 8
-        for (int j = 0; j < m; ++j) place += better(list[j], c) ? 1 : 0;
-        if (place < p.k) write(place, c);
-      }
-      return;
+      last = best_of_all(c, warp_best);
+      if (tid == 0) choose(last, k);
     }
   }
-  // More than the list holds: one after the other, each thread with the heads of its lists.
-  auto mine = [&](int& from) {
-    Candidate c{0, 0};
-    for (int i = tid; i < lists; i += kThreads) {
-      const Candidate h = entry(i, used[i]);
-      if (better(h, c)) {
-        c = h;
-        from = i;
+  __syncthreads();
+  // f(a candidate) for those of the chosen units that this thread looks at and that reach `least`: a vector at a
+  // time, the single logits beside the first and the last unit's vectors
+  auto each_candidate = [&](uint64_t least, auto f) {
+    // x + shift >= least: no x below the difference less its rounding
+    const float reach = value_of(static_cast<uint32_t>(least >> 32));
+#pragma unroll 1
+    for (int i = tid; i < chosen * kUnit; i += kPickThreads) {
+      const Chosen& c = of[i / kUnit];
+      const int at = i % kUnit, u = c.unit, v = u * kUnit + at;
+      const uint32_t place = static_cast<uint32_t>(c.beam) * p.vocab;
+      const Pair base = c.shift;
+      if (u < 0) {
+        if (at == 0) f(Candidate{order_of(base), ~(place + static_cast<uint32_t>(max(p.eos, 0)))});
+        continue;
+      }
+      const T* row = static_cast<const T*>(c.row);
+      float floor = (reach - base.hi) - (fabsf(reach) + fabsf(base.hi)) * 0x1p-21f;
+      if (!(floor < CUDART_INF_F)) floor = -CUDART_INF_F;
+      auto one = [&](float x, int token) {
+        if (x < floor) return;
+        const uint64_t score = order_of(add(base, x));
+        if (score >= least) f(Candidate{score, ~(place + token)});
+      };
+      if (v < c.vectors) {
+        const uint4 w = reinterpret_cast<const uint4*>(row + c.head)[v];
+        if (!(most_of(w, T()) < floor)) {
+          float x[kVec];
+          unpack(w, x);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) one(x[j], c.head + v * kVec + j);
+        }
+      }
+      if (u == 0 && at < c.head) one(single(row[at]), at);
+      if (at < c.tail && u == max(0, (c.vectors - 1) / kUnit)) {
+        const int token = c.head + c.vectors * kVec + at;
+        one(single(row[token]), token);
       }
     }
-    return c;
   };
-  int from = -1;
-  Candidate best = mine(from);
+  // Candidates that reach the worst of k units' best are ranked. (Fewer units: those that reach what k threads'
+  // best do.)
+  uint64_t least = cut;
+  if (chosen < p.k) {
+    best = 0;
+    each_candidate(1, [&](const Candidate& c) { best = max(best, c.score); });
+    least = max(least, bound_of(best, p.k, max(1, min(kPickWarps, chosen * (kUnit / 32))), warp_bound));
+  }
+  each_candidate(least, [&](const Candidate& c) {
+    const int to = atomicAdd(&found, 1);
+    if (to < kFound) list[to] = c;
+  });
+  __syncthreads();
+  const int all = found;
+  if (all <= kFound) {
+    rank_all(list, all, [&](const Candidate& c, int place) {
+      if (place < p.k) write(place, c);
+    });
+    if (tid >= all && tid < p.k) write(tid, Candidate{0, 0});
+    return;
+  }
+  // More than the list holds (most of the units' logits alike, or all high): one after the other.
+  Candidate last{~0ull, ~0u};
+#pragma unroll 1
   for (int k = 0; k < p.k; ++k) {
-    Candidate c = best;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Candidate other;
-      other.score = __shfl_xor_sync(0xffffffffu, c.score, o);
-      other.place = __shfl_xor_sync(0xffffffffu, c.place, o);
-      if (better(other, c)) c = other;
-    }
-    if (lane == 0) warp_best[warp] = c;
-    __syncthreads();
-    Candidate top = warp_best[0];
-    for (int w = 1; w < kWarps; ++w)
-      if (better(warp_best[w], top)) top = warp_best[w];
-    __syncthreads();
-    if (top.score == 0) {
-      if (tid == 0) write(k, top);
-    } else if (best.score == top.score && best.place == top.place) {
-      write(k, top);
-      ++used[from];
-      best = mine(from);
-    }
+    Candidate c{0, 0};
+    each_candidate(least, [&](const Candidate& x) {
+      if (better(last, x) && better(x, c)) c = x;
+    });
+    last = best_of_all(c, warp_best);
+    if (tid == 0) write(k, last);
   }
 }
 
-int pieces_of(int32_t requests, int32_t beams, int32_t vocab, int32_t logits_type) {
+int units_of(int32_t vocab, int32_t logits_type) {
+  const int vectors = vocab / (logits_type == PA_BF16 ? 8 : 4);  // of an aligned row: others have as many, or one less
+  return std::max(1, (vectors + kUnit - 1) / kUnit);
+}
+
+int pieces_of(int32_t requests, int32_t beams, int units) {
   const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(requests) * beams);
-  const int64_t most = std::max<int64_t>(1, vocab / (kMinVectors * (logits_type == PA_BF16 ? 8 : 4)));
-  return static_cast<int>(std::min(most, std::max<int64_t>(1, kTargetCtas / rows)));
+  return static_cast<int>(std::min<int64_t>((units + kWarps - 1) / kWarps, std::max<int64_t>(1, kTargetCtas / rows)));
 }
 
 bool beam_sizes_valid(int32_t requests, int32_t beams, int32_t vocab, int32_t k) {
@@ -583,8 +589,9 @@ bool beam_sizes_supported(int32_t requests, int32_t beams, int32_t vocab, int32_
 extern "C" size_t pa_beam_workspace_size(int32_t requests, int32_t beams, int32_t vocab, int32_t k) {
   using namespace pa;
   if (!beam_sizes_valid(requests, beams, vocab, k) || !beam_sizes_supported(requests, beams, vocab, k)) return 0;
-  const size_t lists = static_cast<size_t>(requests) * beams * pieces_of(requests, beams, vocab, PA_FP32);  // (the most)
-  return (lists * (k + 1) * sizeof(float2) + 255) / 256 * 256;
+  const size_t rows = static_cast<size_t>(requests) * beams;
+  const int units = units_of(vocab, PA_FP32);  // (the more)
+  return (rows * (pieces_of(requests, beams, units) * sizeof(float2) + units * sizeof(float)) + 255) / 256 * 256;
 }
 
 extern "C" pa_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride, int32_t requests,
@@ -608,17 +615,19 @@ extern "C" pa_status beam_select(const void* logits, int32_t logits_type, int64_
   if (workspace == nullptr || workspace_bytes < pa_beam_workspace_size(requests, beams, vocab, k))
     return PA_ERR_WORKSPACE_TOO_SMALL;
   if (reinterpret_cast<uintptr_t>(workspace) & 7u) return PA_ERR_INVALID_ARG;
-  const int pieces = pieces_of(requests, beams, vocab, logits_type);
-  const size_t lists = static_cast<size_t>(requests) * beams * pieces;
-  float2* best = static_cast<float2*>(workspace);
-  const BeamParams p{logits, row_stride, requests, beams, vocab, k, eos_token, pieces, scores, live, out_scores,
-                     parents, tokens, live_out, best, best + lists * k};
+  const int units = units_of(vocab, logits_type), pieces = pieces_of(requests, beams, units);
+  float2* stats = static_cast<float2*>(workspace);
+  const BeamParams p{logits, row_stride, requests, beams, vocab, k, eos_token, units, pieces,
+                     0xffffffffu / static_cast<uint32_t>(units), scores, live, out_scores,
+                     parents, tokens, live_out, stats,
+                     reinterpret_cast<float*>(stats + static_cast<size_t>(requests) * beams * pieces)};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(pieces), static_cast<unsigned>(requests * beams));
-  cudaError_t e = logits_type == PA_BF16 ? launch_dependent(beam_rows_kernel<uint16_t>, grid, kThreads, 0, st, 0, p)
-                                         : launch_dependent(beam_rows_kernel<float>, grid, kThreads, 0, st, 0, p);
-  if (e == cudaSuccess)
-    e = launch_dependent(beam_merge_kernel, static_cast<unsigned>(requests), kThreads,
-                         static_cast<size_t>(beams) * pieces, st, 0, p);
+  auto launch = [&](auto* rows_kernel, auto* pick_kernel) {
+    const cudaError_t e = launch_dependent(rows_kernel, grid, kThreads, 0, st, 0, p);
+    return e == cudaSuccess ? launch_dependent(pick_kernel, static_cast<unsigned>(requests), kPickThreads, 0, st, 0, p) : e;
+  };
+  const cudaError_t e = logits_type == PA_BF16 ? launch(beam_rows_kernel<uint16_t>, beam_pick_kernel<uint16_t>)
+                                               : launch(beam_rows_kernel<float>, beam_pick_kernel<float>);
   return e == cudaSuccess ? PA_OK : record_cuda_error(e, "beam_select");
 }

@@ -158,3 +158,33 @@ def test_in_place_on_a_stream_in_a_graph_and_with_a_workspace(cuda_lib):
 def test_no_requests(cuda_lib):
     got = cuda_lib.beam_select(torch.empty(0, 4, 100, device="cuda"), torch.empty(0, 4, device="cuda"), 4)
     assert got.scores.shape == (0, 4)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [511, 512, 513, 1023, 1024, 1025, 1032, 2049])
+def test_lengths_about_whole_units_at_every_offset(cuda_lib, dtype, V):
+    """Units of 512 or 1,024 logits, rows that start anywhere in 16 bytes, the best at both ends."""
+    wide = logits_of(1, 2, V + 8, dtype, V)
+    for cut in range(8):
+        x = wide[:, :, cut:cut + V].clone() if cut == 0 else wide[:, :, cut:cut + V]
+        x[0, 0, 0], x[0, 0, V - 1], x[0, 1, V // 2] = 14.0, 15.0, 14.5
+        check(cuda_lib, x, scores_of(1, 2, cut), 12)
+
+
+def test_more_units_alike_than_are_ranked_at_once(cuda_lib):
+    """The first step of a constrained search: three tokens allowed, the others at the type's lowest value."""
+    x = torch.full((1, 4, 300001), torch.finfo(torch.float32).min, device="cuda")
+    x[0, 0, [5, 170000, 300000]] = torch.tensor([1.0, 2.0, 3.0], device="cuda")
+    s = torch.tensor([[0.0, -INF, -INF, -INF]], device="cuda")
+    got = check(cuda_lib, x, s, 20)
+    assert got.tokens[0].tolist() == [300000, 170000, 5] + [i for i in range(18) if i != 5]
+
+
+def test_a_few_units_with_all_of_the_best(cuda_lib):
+    """More candidates than are ranked at once reach the worst of the k best units' largest."""
+    x = torch.full((2, 2, 40000), -4.0)
+    for u in range(8):
+        x[0, 0, 1024 * u: 1024 * u + 500] = torch.arange(500) / 500.0 + u % 3
+    x[1] = torch.randn(2, 40000, generator=torch.Generator().manual_seed(1))
+    check(cuda_lib, x.cuda(), torch.zeros(2, 2, device="cuda"), 8)
+    check(cuda_lib, x.to(torch.bfloat16).cuda(), torch.zeros(2, 2, device="cuda"), 64)
