@@ -3,19 +3,22 @@
 // Candidate (b, v) of a request has the score
 //     scores[b] + logits[b][v] - ln sum_u exp(logits[b][u])
 // and the k best are kept, equal scores in the order of (b, v). Within a beam the order is that of the
-// logits themselves, whatever the beam's score and normaliser: so one pass over a beam's logits finds
-// both its normaliser (running maximum and sum) and its k largest logits, and only those few meet the
-// other beams' in a second launch. Scores are formed as pairs of floats there (48 bits): what decides
-// between beams is the normalisers' precision (fp32 sums of exponentials), not the rounding of a sum
-// of large parts.
+// logits themselves, whatever the beam's score and normaliser. So one pass over a beam's logits finds its
+// normaliser (running maximum and sum) and the largest logit of every unit, 2 KB of the row. With all beams'
+// normalisers known the units are ordered by the scores of those (equal ones as they lie): the k best
+// candidates are all in the k best units, since each of these has one candidate at least that comes before
+// all of any other unit. The second launch looks through those k units alone. Scores are formed as pairs of
+// floats there (48 bits): what decides between beams is the normalisers' precision (fp32 sums of
+// exponentials), not the rounding of a sum of large parts.
 //
 // The logits are read once from memory. A row is cut into pieces so that a few rows still fill the GPU; a CTA
-// takes a piece, a thread 16-byte vectors kThreads apart. Measured on a GB300 (calls of a graph): 64 x 8 rows
-// of 151,936 in bf16 42 us (147 MB: 21.6 us at a copy's rate), the first launch 34 of them, bound by
-// instruction issue (64 % of the busy SMs' slots; 3.5 TB/s): 5 an element to unpack, exponentiate and add,
-// as many again per piece for the selection; 16 x 5 rows of 51,865 in fp32 14.8 us; one request 8.5 us, two
-// launches of dependent loads. Candidate selection by k rounds of a block-wide maximum took 477 us for the
-// first of these; scores in fp64 in the second launch cost it 4 us of 14 (this GPU's fp64 rate is 1/60 of fp32's).
+// takes a piece, a warp a unit, a lane four 16-byte vectors of it. Measured on a GB300 (calls of a graph): 64 x 8 rows
+// of 151,936 in bf16 35 us (147 MB: 21.6 us at a copy's rate), the first launch 25 of them, its instructions (5 an
+// element to unpack, exponentiate and add) half of what the SMs can issue; 16 x 5 rows of 51,865 in fp32 11.7 us; one
+// request 6.7 us. The second launch is a chain of some 1,000 instructions of each warp: normalisers 2 us, units 3,
+// candidates 2.5. Choosing each piece's k largest in the first launch, for the second to join, took 41.4, 14.6 and
+// 8.5 us (all of a piece's warps wait for its selection, three times); rounds of a block-wide maximum there 477 us
+// for the first of these; scores in fp64 in the second launch cost it 4 us (this GPU's fp64 rate is 1/60 of fp32's).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -30,13 +33,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPickThreads = 512;
-constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxK = 64;
 constexpr int kMaxRows = 65535;
 constexpr int kUnit = 128;   // 16-byte vectors of a unit: four a lane, 2 KB
 constexpr int kUnits = 512;  // units that the quick choice of them holds
+// Threads of the second launch: one for every vector of the k units that are looked through, at most 1,024. With 512
+// and 1,024: 10 kept of 16 x 5 rows 13.0 and 11.6 us (both launches), 8 of 64 x 8 37.3 and 35.6, 4 of one request 7.1
+// and 8.0; with 256 the last one 7.5.
+constexpr int kPickFew = 512, kPickMany = 1024;
 constexpr int kFound = 512;  // candidates that the quick ranking holds
 // Pieces of a row: as many as give kTargetCtas CTAs in all, none of them below a unit a warp.
 constexpr int kTargetCtas = 2736;
@@ -285,6 +290,7 @@ __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
 }
 
 // The largest of the threads' candidates, to every thread. `scratch` may be used again after the next barrier.
+template <int kPickWarps>
 __device__ __forceinline__ Candidate best_of_all(Candidate c, Candidate* scratch) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -325,7 +331,7 @@ __device__ __forceinline__ uint64_t bound_of(uint64_t best, int k, int warps, ui
 // f(entry, its place among all by `better`) for the entries that are this thread's to write: kRankLanes threads
 // count for one.
 constexpr int kRankLanes = 8;
-template <class F>
+template <int kPickThreads, class F>
 __device__ __forceinline__ void rank_all(const Candidate* list, int n, F f) {
   const int part = threadIdx.x % kRankLanes;
 #pragma unroll 1
@@ -349,10 +355,10 @@ struct Chosen {
   int32_t head, vectors, tail;
 };
 
-template <class T>
+template <class T, int kPickThreads>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParams p) {
-  constexpr int kVec = Row<T>::kVec;
-  constexpr int kHeld = 4;
+  constexpr int kVec = Row<T>::kVec, kPickWarps = kPickThreads / 32;
+  constexpr int kHeld = 2048 / kPickThreads;
   __shared__ Pair shift[kMaxBeams];    // score minus normaliser of a beam
   __shared__ uint8_t kind[kMaxBeams];  // 0: no candidates, 1: its tokens, 2: itself (finished)
   __shared__ Candidate warp_best[kPickWarps];
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     if (place == p.k - 1) cut = c.score;
   };
   if (m <= kUnits) {
-    rank_all(list, m, choose);
+    rank_all<kPickThreads>(list, m, choose);
   } else {  // most units alike: one after the other
     Candidate last{~0ull, ~0u};
 #pragma unroll 1
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
         const Candidate x{unit_score(i, tops[i]), ~static_cast<uint32_t>(i)};
         if (better(last, x) && better(x, c)) c = x;
       }
-      last = best_of_all(c, warp_best);
+      last = best_of_all<kPickWarps>(c, warp_best);
       if (tid == 0) choose(last, k);
     }
   }
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
   __syncthreads();
   const int all = found;
   if (all <= kFound) {
-    rank_all(list, all, [&](const Candidate& c, int place) {
+    rank_all<kPickThreads>(list, all, [&](const Candidate& c, int place) {
       if (place < p.k) write(place, c);
     });
     if (tid >= all && tid < p.k) write(tid, Candidate{0, 0});
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     each_candidate(least, [&](const Candidate& x) {
       if (better(last, x) && better(x, c)) c = x;
     });
-    last = best_of_all(c, warp_best);
+    last = best_of_all<kPickWarps>(c, warp_best);
     if (tid == 0) write(k, last);
   }
 }
@@ -623,11 +629,14 @@ extern "C" pa_status beam_select(const void* logits, int32_t logits_type, int64_
                      reinterpret_cast<float*>(stats + static_cast<size_t>(requests) * beams * pieces)};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(pieces), static_cast<unsigned>(requests * beams));
+  const bool few = k * kUnit <= kPickFew;
   auto launch = [&](auto* rows_kernel, auto* pick_kernel) {
     const cudaError_t e = launch_dependent(rows_kernel, grid, kThreads, 0, st, 0, p);
-    return e == cudaSuccess ? launch_dependent(pick_kernel, static_cast<unsigned>(requests), kPickThreads, 0, st, 0, p) : e;
+    return e == cudaSuccess ? launch_dependent(pick_kernel, static_cast<unsigned>(requests), few ? kPickFew : kPickMany, 0, st, 0, p) : e;
   };
-  const cudaError_t e = logits_type == PA_BF16 ? launch(beam_rows_kernel<uint16_t>, beam_pick_kernel<uint16_t>)
-                                               : launch(beam_rows_kernel<float>, beam_pick_kernel<float>);
+  const cudaError_t e =
+      logits_type == PA_BF16
+          ? launch(beam_rows_kernel<uint16_t>, few ? beam_pick_kernel<uint16_t, kPickFew> : beam_pick_kernel<uint16_t, kPickMany>)
+          : launch(beam_rows_kernel<float>, few ? beam_pick_kernel<float, kPickFew> : beam_pick_kernel<float, kPickMany>);
   return e == cudaSuccess ? PA_OK : record_cuda_error(e, "beam_select");
 }
