@@ -13,9 +13,9 @@
 //
 // The logits are read once from memory. A row is cut into pieces so that a few rows still fill the GPU; a CTA
 // takes a piece, a warp a unit, a lane four 16-byte vectors of it. Measured on a GB300 (calls of a graph): 64 x 8 rows
-// of 151,936 in bf16 35 us (147 MB: 21.6 us at a copy's rate), the first launch 25 of them, its instructions (5 an
-// element to unpack, exponentiate and add) half of what the SMs can issue; 16 x 5 rows of 51,865 in fp32 11.7 us; one
-// request 6.7 us. The second launch is a chain of some 1,000 instructions of each warp: normalisers 2 us, units 3,
+// of 151,936 in bf16 36 us (147 MB: 21.6 us at a copy's rate), the first launch 25 of them, its instructions (5 an
+// element to unpack, exponentiate and add) half of what the SMs can issue; 16 x 5 rows of 51,865 in fp32 12 us; one
+// request 7 us. The second launch is a chain of some 1,000 instructions of each warp: normalisers 2 us, units 3,
 // candidates 2.5. Choosing each piece's k largest in the first launch, for the second to join, took 41.4, 14.6 and
 // 8.5 us (all of a piece's warps wait for its selection, three times); rounds of a block-wide maximum there 477 us
 // for the first of these; scores in fp64 in the second launch cost it 4 us (this GPU's fp64 rate is 1/60 of fp32's).
@@ -43,6 +43,7 @@ constexpr int kUnits = 512;  // units that the quick choice of them holds
 // and 8.0; with 256 the last one 7.5.
 constexpr int kPickFew = 512, kPickMany = 1024;
 constexpr int kFound = 512;  // candidates that the quick ranking holds
+constexpr int kFewFound = 128;  // so few are ranked sooner than a closer bound is found
 // Pieces of a row: as many as give kTargetCtas CTAs in all, none of them below a unit a warp.
 constexpr int kTargetCtas = 2736;
 
@@ -365,12 +366,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
   __shared__ uint64_t warp_bound[kPickWarps], cut;
   __shared__ Candidate list[kUnits > kFound ? kUnits : kFound];
   __shared__ Chosen of[kMaxK];
-  __shared__ int units_found, found;
+  __shared__ int units_found, found, longest;  // longest: most vectors of a chosen unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = static_cast<int>(blockIdx.x), units = p.beams * p.units;
   await_previous();
   if (tid == 0) {
-    units_found = found = 0;
+    units_found = found = longest = 0;
     cut = 1;
   }
   // units go round the warps, so that every warp has some of each beam; a thread's first ones are asked for now
@@ -479,6 +480,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     const int u = i - b * p.units;
     of[place] = Chosen{row, shift[b], b, kind[b] == 2 ? -1 : u, r.head, r.vectors, r.tail};
     if (place == p.k - 1) cut = c.score;
+    atomicMax(&longest, max(1, min(kUnit, r.vectors - u * kUnit)));
   };
   if (m <= kUnits) {
     rank_all<kPickThreads>(list, m, choose);
@@ -497,15 +499,31 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     }
   }
   __syncthreads();
-  // f(a candidate) for those of the chosen units that this thread looks at and that reach `least`: a vector at a
-  // time, the single logits beside the first and the last unit's vectors
+  // This thread's vectors of the chosen units: the units take turns, so that every warp has some of each, however
+  // short they are and however far apart the beams' scores. (The first 8 places have the single logits too.)
+  const int places = chosen * max(longest, 8);
+  const uint32_t over_chosen = 0xffffffffu / static_cast<uint32_t>(max(chosen, 1));
+  auto unit_of = [&](int i, int& at) -> const Chosen& {
+    at = static_cast<int>(__umulhi(static_cast<uint32_t>(i), over_chosen));  // off by one at most
+    int which = i - at * chosen;
+    if (which >= chosen) {
+      ++at;
+      which -= chosen;
+    }
+    return of[which];
+  };
+  auto vector_of = [&](const Chosen& c, int v) {
+    return reinterpret_cast<const uint4*>(static_cast<const T*>(c.row) + c.head)[v];
+  };
+  // f(a candidate) for those that reach `least`
   auto each_candidate = [&](uint64_t least, auto f) {
     // x + shift >= least: no x below the difference less its rounding
     const float reach = value_of(static_cast<uint32_t>(least >> 32));
 #pragma unroll 1
-    for (int i = tid; i < chosen * kUnit; i += kPickThreads) {
-      const Chosen& c = of[i / kUnit];
-      const int at = i % kUnit, u = c.unit, v = u * kUnit + at;
+    for (int i = tid; i < places; i += kPickThreads) {
+      int at;
+      const Chosen& c = unit_of(i, at);
+      const int u = c.unit, v = u * kUnit + at;
       const uint32_t place = static_cast<uint32_t>(c.beam) * p.vocab;
       const Pair base = c.shift;
       if (u < 0) {
@@ -521,7 +539,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
         if (score >= least) f(Candidate{score, ~(place + token)});
       };
       if (v < c.vectors) {
-        const uint4 w = reinterpret_cast<const uint4*>(row + c.head)[v];
+        const uint4 w = vector_of(c, v);
         if (!(most_of(w, T()) < floor)) {
           float x[kVec];
           unpack(w, x);
@@ -536,21 +554,33 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
       }
     }
   };
-  // Candidates that reach the worst of k units' best are ranked. (Fewer units: those that reach what k threads'
-  // best do.)
+  // Candidates that reach the worst of k units' best are ranked. If there are fewer units, or many such candidates (a
+  // beam far ahead of the others that has fewer than k units, last units of a few logits), only those that reach what
+  // k threads' best vectors do. (That bound at once, always: 1.0 to 1.8 us more.)
   uint64_t least = cut;
-  if (chosen < p.k) {
-    best = 0;
-    each_candidate(1, [&](const Candidate& c) { best = max(best, c.score); });
-    least = max(least, bound_of(best, p.k, max(1, min(kPickWarps, chosen * (kUnit / 32))), warp_bound));
-  }
-  each_candidate(least, [&](const Candidate& c) {
-    const int to = atomicAdd(&found, 1);
-    if (to < kFound) list[to] = c;
-  });
-  __syncthreads();
-  const int all = found;
-  if (all <= kFound) {
+#pragma unroll 1
+  for (int pass = chosen < p.k ? 1 : 0; pass < 2; ++pass) {
+    if (pass == 1) {
+      best = 0;
+#pragma unroll 1
+      for (int i = tid; i < places; i += kPickThreads) {
+        int at;
+        const Chosen& c = unit_of(i, at);
+        const int v = c.unit * kUnit + at;
+        if (c.unit < 0 ? at == 0 : v < c.vectors)
+          best = max(best, order_of(c.unit < 0 ? c.shift : add(c.shift, most_of(vector_of(c, v), T()))));
+      }
+      least = max(least, bound_of(best, p.k, max(1, min(kPickWarps, chosen * longest / 32)), warp_bound));
+      if (tid == 0) found = 0;
+      __syncthreads();
+    }
+    each_candidate(least, [&](const Candidate& c) {
+      const int to = atomicAdd(&found, 1);
+      if (to < kFound) list[to] = c;
+    });
+    __syncthreads();
+    const int all = found;
+    if (all > (pass == 0 ? kFewFound : kFound)) continue;
     rank_all<kPickThreads>(list, all, [&](const Candidate& c, int place) {
       if (place < p.k) write(place, c);
     });

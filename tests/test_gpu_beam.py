@@ -188,3 +188,19 @@ def test_a_few_units_with_all_of_the_best(cuda_lib):
     x[1] = torch.randn(2, 40000, generator=torch.Generator().manual_seed(1))
     check(cuda_lib, x.cuda(), torch.zeros(2, 2, device="cuda"), 8)
     check(cuda_lib, x.to(torch.bfloat16).cuda(), torch.zeros(2, 2, device="cuda"), 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_beam_far_ahead_with_few_units(cuda_lib, dtype):
+    x, s = logits_of(3, 8, 9000, dtype, 31), scores_of(3, 8, 31)
+    s[:, 3] += 40
+    check(cuda_lib, x, s, 32)
+    live = torch.ones(3, 8, dtype=torch.int32, device="cuda")
+    live[1, 3] = live[2, 0] = 0
+    check(cuda_lib, x, s, 32, live, eos=3)
+
+
+@pytest.mark.parametrize("W,V", [(16, 2080), (3, 9000), (5, 1030), (2, 66)])
+def test_last_units_of_a_few_logits(cuda_lib, W, V):
+    for dtype in (torch.bfloat16, torch.float32):
+        check(cuda_lib, logits_of(2, W, V, dtype, V), scores_of(2, W, V), 31)
