@@ -126,7 +126,7 @@ struct Seen {
   // The largest of the next logits.
   __device__ __forceinline__ void reach(float most) {
     if (most > ref + 40.f) {
-      sum = ref == -INFINITY ? 0.f : sum * fast_exp2((ref - most) * kLog2e);
+      sum *= fast_exp2((ref - most) * kLog2e);  // (by 0 at first, which leaves a NaN)
       ref = most;
     }
     top = fmaxf(top, most);

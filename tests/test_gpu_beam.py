@@ -204,3 +204,13 @@ def test_one_beam_far_ahead_with_few_units(cuda_lib, dtype):
 def test_last_units_of_a_few_logits(cuda_lib, W, V):
     for dtype in (torch.bfloat16, torch.float32):
         check(cuda_lib, logits_of(2, W, V, dtype, V), scores_of(2, W, V), 31)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_before_anything_else_that_a_thread_reads(cuda_lib, dtype):
+    wide = logits_of(2, 2, 9000, dtype, 8)
+    for cut, V, where in [(3, 28, 0), (1, 7, 6), (0, 4, 3), (0, 8000, slice(0, 8)), (5, 8000, slice(3, 40)), (6, 30, 29)]:
+        x = wide.clone()[:, :, cut:cut + V]
+        x[0, 1, where] = NAN
+        got = check(cuda_lib, x, scores_of(2, 2, 8), 4)
+        assert (got.parents[0] <= 0).all()
