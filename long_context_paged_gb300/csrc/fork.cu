@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkParams p
     for (int k = tid; k < p.blocks; k += kThreads) differ = min(differ, p.differ[g * p.blocks + k]);
   block_sums(sums, scratch);
   const int before = sums[0], freed = sums[1], copies_before = sums[2], copies = sums[3];
-  const bool bad = sums[4] != 0, short_of = copies > count;
+  const bool bad = sums[4] != 0, short_of = !bad && copies > count;
   const bool full = static_cast<int64_t>(count) - copies + freed > p.free_capacity;
   if (at == 0 && tid == 0) {
     if (bad || full) flag_error(p.status, PA_DEV_ERR_LENGTH);

@@ -196,3 +196,13 @@ def test_copies_that_name_no_page(cuda_lib):
     assert cuda_lib.read_device_status(status) == 0 and torch.equal(pool, before)
     cuda_lib.paged_copy_pages(dev(np.zeros((0, 3))), [pool])
     cuda_lib.paged_copy_pages(dev([[0, 1, 3]]), [])
+
+
+def test_a_bad_parent_beside_groups_short_of_pages_is_one_error(cuda_lib):
+    """Two groups of a prompt handed to three beams need four pages and there is one; a third group's parent is bad."""
+    table = np.full((9, 2), -1, np.int32)
+    table[[0, 3, 6], 0] = [0, 1, 2]
+    lens = np.array([5, 0, 0, 7, 0, 0, 9, 0, 0])
+    parents = np.array([[0, 0, 0], [0, 0, 0], [0, 3, 0]])
+    want, _ = check(cuda_lib, parents, lens, table, np.array([3], np.int32), 1, 4)
+    assert want["flags"] == {"length"}
