@@ -465,7 +465,9 @@ pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t interleaved,
  * requests behind one instruction, have its pages in common. The pages describe no search over
  * hypotheses.
  *
- * The result is attn_decode_paged's up to rounding: row b attends to its seq_lens[b] keys.
+ * The result is attn_decode_paged's up to rounding: row b attends to its seq_lens[b] keys. Weights are held to
+ * 2^-15 of each, but those of shared pages that more than 8 rows have in common are rounded to bf16 (2^-8), as the
+ * prefill's are. (Rows of a group are taken 64 at a time; a last part of up to 8 counts as so few.)
  *   cu_group_rows  int32 [groups + 1]: group g is rows cu_group_rows[g] .. cu_group_rows[g+1]-1;
  *                  rows in no group share nothing
  *   shared_pages   int32 [groups]: leading pages that the group's rows have in common: the caller
@@ -479,8 +481,7 @@ pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t interleaved,
  *                  PA_DEV_ERR_LENGTH and no row shares anything.
  *   batch <= 4096, groups <= 4096; max_seq_len <= 131072, a longer sequence is flagged
  *   PA_DEV_ERR_LENGTH (and cut where it passes bt_stride * 16 or 131,072 keys); softmax_scale as
- *   attn_prefill_chunk; q, pools and out 16-byte aligned. Weights are rounded to bf16 before they meet V,
- *   as the prefill does.
+ *   attn_prefill_chunk; q, pools and out 16-byte aligned.
  *   workspace      at least pa_decode_shared_workspace_size(...) bytes, 256-byte aligned; calls that
  *                  share one must not overlap on the GPU.
  * A row without keys gets o = 0, lse = -inf; so does a row whose scores are all -inf. NaN and

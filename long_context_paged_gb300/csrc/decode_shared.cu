@@ -27,8 +27,10 @@
 // thread per row, written over S as bf16, O += P V (A = P in TMEM, B = V in shared memory). With 8 rows or
 // fewer most of those 128 matrix rows would be padding and one warp would do all exponentials, so the
 // products are turned round: S^T = K Q^T (A = K, 16 columns), a thread per key, O^T += V^T P^T (A = V, B = P
-// in shared memory). (16 x 4 rows: 190 us with a thread per row, 169 with a thread per key.) Units go to
-// two softmax warpgroups in turn, each with an S and an O of its own, so that one's exponentials run beside
+// in shared memory; 16 x 4 rows: 190 us with a thread per row, 169 with a thread per key). There the weights are
+// two bf16s each, 16 more columns that cost nothing measurable, so that beams' and single rows' results are
+// the plain decode's. Units go to two softmax warpgroups in turn, each with an S and an O of its own, so that one's
+// exponentials run beside
 // the other's products. K and V come by tiled TMA, a page per copy.
 //
 // Tried and left out: 64-key units (16 x 4 rows 216 -> 270 us: an issuing thread's waits and commits cost
@@ -74,11 +76,13 @@ constexpr uint32_t kGroupBytes = 8 * 256;          // of them 1 KB of the first 
 constexpr uint32_t kHalfBytes = 8 * 128;
 // The Q buffer: a segment of many rows has all of it. Those of few rows, which come after all of those,
 // have two small Q buffers in turn and, for each stream, their weights in it (bf16 [2 halves of the keys]
-// [kFew rows][64 keys]).
+// [kFew rows' high parts, then their low ones][64 keys]).
 constexpr uint32_t kFewHalfBytes = kFew * 128;
 constexpr uint32_t kFewQBytes = 2 * kFewHalfBytes;
 constexpr uint32_t kWeightsAt = 2 * kFewQBytes;
-static_assert(kWeightsAt + 2 * kFewQBytes <= 2 * kQBlockBytes, "the small buffers fit in the large one");
+constexpr uint32_t kWeightHalfBytes = 2 * kFewHalfBytes;
+constexpr uint32_t kWeightBytes = 2 * kWeightHalfBytes;
+static_assert(kWeightsAt + 2 * kWeightBytes <= 2 * kQBlockBytes, "the small buffers fit in the large one");
 constexpr float kRescaleThreshold = 8.0f;     // log2 units a row's maximum may lag behind
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroups = 4096;
@@ -509,7 +513,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem_base;  // S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); few rows:
-                                      // S_t [0, 16) and two O_t at [64, 96) of the stream's S
+                                      // S_t [0, 16) and two O_t of 32 columns at [64, 128) of the stream's S
   await_previous();
   Slice plan;
   Segment* own_segments = p.own_segments + static_cast<int64_t>(blockIdx.x) * kOwnPlanSegments;
@@ -756,17 +760,17 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         const uint32_t first = flags & kFirst ? 0u : 1u;
         const uint64_t v = dv + (st * kTileBytes >> 4);
         if (flags & kFewFlag) {  // O^T += V^T P^T
-          constexpr uint32_t id = tc::idesc_bf16(128, kFew, 1, 0);
-          const uint64_t w = dp + (t * kFewQBytes >> 4);
-          const uint32_t o = tmem + t * kTileKeys + 64 + buf * kFew;
+          constexpr uint32_t id = tc::idesc_bf16(128, 2 * kFew, 1, 0);
+          const uint64_t w = dp + (t * kWeightBytes >> 4);
+          const uint32_t o = tmem + t * kTileKeys + 64 + buf * 2 * kFew;
           tc::mma_ss(o, v, w, id, first);
           if (pages == kTilePages) {
 #pragma unroll
             for (int kk = 1; kk < kTilePages; ++kk)
-              tc::mma_ss_c<true>(o, v + kk * (kPageBytes >> 4), w + (((kk >> 2) * kFewHalfBytes + (kk & 3) * 32) >> 4), id);
+              tc::mma_ss_c<true>(o, v + kk * (kPageBytes >> 4), w + (((kk >> 2) * kWeightHalfBytes + (kk & 3) * 32) >> 4), id);
           } else {
             for (int kk = 1; kk < pages; ++kk)
-              tc::mma_ss_c<true>(o, v + kk * (kPageBytes >> 4), w + (((kk >> 2) * kFewHalfBytes + (kk & 3) * 32) >> 4), id);
+              tc::mma_ss_c<true>(o, v + kk * (kPageBytes >> 4), w + (((kk >> 2) * kWeightHalfBytes + (kk & 3) * 32) >> 4), id);
           }
         } else {  // O += P V
           constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
@@ -888,8 +892,10 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
             l *= alpha;
             m_used = m_new;
           }
-          // the weights go to bf16 for the product (their sum is of the unrounded ones): off by 2^-8 of
-          // each at most, which averages out over the keys; V's own precision is no better
+          // The weights go to one bf16 for the product (their sum is of the unrounded ones): off by 2^-8 of each
+          // at most, which averages out over the keys: 2.0e-3 of the output's norm against 1.7e-3 for two
+          // bf16s as below. Those would cost twice the products and half as many instructions again here: 307
+          // rows in 4 groups 85 -> 103 us.
           const float m_eff = m_used == -CUDART_INF_F ? 0.f : m_used;
           const float2 nm2 = make_float2(-m_eff, -m_eff);
           float2 ls[4];
@@ -962,13 +968,13 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         ok = warp_wait(&s.few_ready[stream][buf], (piece >> 1) & 1, lane, p.status);
         if (!ok) return;
         tc::fence_after_sync();
-        uint32_t o[kFew];
-        tc::tmem_ld16(t_s + 64 + buf * kFew, o);
+        uint32_t o[2 * kFew];
+        tc::tmem_ld32(t_s + 64 + buf * 2 * kFew, o);
         tc::tmem_wait_ld();
         hand_over(&s.few_free[stream][buf]);
 #pragma unroll
         for (int c = 0; c < kFew; ++c)
-          if (c < left_rows) left_part[c * kHeadDim + r] = __uint_as_float(o[c]);
+          if (c < left_rows) left_part[c * kHeadDim + r] = __uint_as_float(o[c]) + __uint_as_float(o[kFew + c]);
         // (a NaN among the scores: any finite maximum hands the NaN on)
         if (quarter == 0 && lane < left_rows)
           *reinterpret_cast<float2*>(left_part + left_stats + 2 * lane) = make_float2(left_l == left_l ? left_m : 0.f, left_l);
@@ -1021,30 +1027,38 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           const float alpha = m_used == -CUDART_INF_F ? 0.f : fast_exp2(m_used - m_new);
           m_used = m_new;
           if (!(flags & kFirst)) {
-            const uint32_t t_few = t_s + 64 + (few_pieces & 1) * kFew;
-            uint32_t o[kFew];
-            tc::tmem_ld16(t_few, o);
+            const uint32_t t_few = t_s + 64 + (few_pieces & 1) * 2 * kFew;
+            uint32_t o[2 * kFew];
+            tc::tmem_ld32(t_few, o);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < kFew; ++c) {
               const float a = __shfl_sync(0xffffffffu, alpha, c);
               l[c] *= a;
               o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
+              o[kFew + c] = __float_as_uint(__uint_as_float(o[kFew + c]) * a);
             }
-            tc::tmem_st16(t_few, o);
+            tc::tmem_st32(t_few, o);
             tc::tmem_wait_st();
           }
         }
         const float m_eff = m_used == -CUDART_INF_F ? 0.f : m_used;
-        uint8_t* w = s.q + kWeightsAt + stream * kFewQBytes + (r >> 6) * kFewHalfBytes + (r & 7) * 2;
+        // A weight is two bf16s: its high 16 bits, cut off, and the rest, rounded: 2^-8 of what is below 2^-7 of the
+        // weight, so 2^-15 of it at most (one bf16 alone: 2^-8, 2.35e-3 of the output's norm, of which the output's own
+        // rounding is 1.66e-3). The rest is taken of a weight 2^-20 larger, so that it is above 0 wherever the weight is:
+        // times an infinity of V the two then agree. (Rows four at a time, to overlap their latencies: 2 us of 62 at 8
+        // rows over 67,500 keys, which is what the second product had cost. Columns past the rows' are not used.)
+        uint8_t* w = s.q + kWeightsAt + stream * kWeightBytes + (r >> 6) * kWeightHalfBytes + (r & 7) * 2;
 #pragma unroll
         for (int c = 0; c < kFew; ++c) {
-          if (c >= rows) break;
+          if (c % 4 == 0 && c >= rows) break;
           const float m = __shfl_sync(0xffffffffu, m_eff, c);
           const float e = seen ? fast_exp2(fmaf(__uint_as_float(sb[c]), p.scale_log2, -m)) : 0.f;
           l[c] += e;
-          *reinterpret_cast<uint16_t*>(w + c * 128 + ((((r >> 3) & 7) ^ (c & 7)) << 4)) =
-              static_cast<uint16_t>(pack_bf16x2(e, 0.f));
+          const float high = __uint_as_float(__float_as_uint(e) & 0xffff0000u), rest = fmaf(e, 1.f + 0x1p-20f, -high);
+          uint16_t* to = reinterpret_cast<uint16_t*>(w + c * 128 + ((((r >> 3) & 7) ^ (c & 7)) << 4));
+          to[0] = static_cast<uint16_t>(__float_as_uint(e) >> 16);
+          to[kFewHalfBytes / 2] = static_cast<uint16_t>(pack_bf16x2(rest, 0.f));
         }
         tc::fence_proxy_async_smem();
         if (keys % kPage != 0) clear_tail(keys);
