@@ -522,7 +522,7 @@ pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const void* k_po
  *               k = beams.
  * A beam with a NaN or +inf among its logits, or nothing but -inf, has no candidates. Within a beam the
  * order is that of its logits; scores of different beams are compared as pairs of floats (48 bits) over
- * fp32 sums of exponentials (off by 3e-7).
+ * normalisers from fp32 exponentials, off by 2^-18 (4e-6) at most for vocabularies below 2^25.
  *   workspace   at least pa_beam_workspace_size(...) bytes, 8-byte aligned; calls that share one must not
  *               overlap on the GPU
  * ------------------------------------------------------------------------------------------ */

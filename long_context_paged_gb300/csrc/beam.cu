@@ -62,7 +62,7 @@ struct BeamParams {
   int32_t* tokens;
   int32_t* live_out;
   // workspace
-  float2* stats;  // [rows][pieces] maximum and sum of exponentials
+  float2* stats;  // [rows][pieces] reference and sum of exponentials
   float* tops;    // [rows][units] largest logit
 };
 
@@ -119,24 +119,37 @@ __device__ __forceinline__ void unpack(uint4 w, float (&x)[4]) {
 __device__ __forceinline__ float single(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ float single(float v) { return v; }
 
-// A thread's state over its logits: the largest, and the sum of exponentials against a reference that
-// follows the largest at a distance (40 at most: sums stay below 2^77), so that nothing is rescaled at
-// every new maximum.
+// e to the difference of two references: expf is off by 2^-23 at most, and the difference is exact.
+__device__ __forceinline__ float factor(float d) { return expf(d); }
+
+// A thread's sum of exponentials over its logits, against a reference that follows the largest of them at a distance
+// (kLag at most, so that little is rescaled). The distance is short because terms are formed from it: x - ref and
+// its product with log2 e are rounded by 2^-24 |x - ref| each, an error that terms alike have alike. (A lag of 40, by
+// which nothing is ever rescaled, left normalisers off by 5e-6, by what a thread happened to read first.) References are
+// whole numbers, so that differences between them are exact. The sum is a pair of floats: its error is that of one
+// vector's however many there are. In all a normaliser is off by at most 1.4e-7 y (y: distance below ref of the terms
+// that matter, at most the logarithm of their number) + 2.4e-7 (ex2) + 24 * 2^-24 (sums of vectors, lanes, warps and
+// pieces): 2^-18.
+constexpr float kLag = 4.f;
+
 struct Seen {
-  float top = -INFINITY, ref = -INFINITY, sum = 0.f;
+  float top = -INFINITY, ref = -INFINITY, sum = 0.f, low = 0.f;
 
   // The largest of the next logits.
   __device__ __forceinline__ void reach(float most) {
-    if (most > ref + 40.f) {
-      sum *= fast_exp2((ref - most) * kLog2e);  // (by 0 at first, which leaves a NaN)
-      ref = most;
+    if (most > ref + kLag) {
+      const float to = rintf(most), f = factor(ref - to);  // (0 at first, which leaves a NaN)
+      sum *= f;
+      low *= f;
+      ref = to;
     }
     top = fmaxf(top, most);
   }
-  // Those logits. (x - ref, then the factor: one rounding each, so no error that all terms share.)
-  __device__ __forceinline__ void take(float x) { sum += fast_exp2((x - (ref == -INFINITY ? 0.f : ref)) * kLog2e); }
+  // The sum of those logits' terms. (x - ref, then the factor: one rounding each; a product folded into the difference
+  // would overflow at the type's lowest value.)
+  __device__ __forceinline__ float term(float x) const { return fast_exp2((x - (ref == -INFINITY ? 0.f : ref)) * kLog2e); }
   template <int n>
-  __device__ __forceinline__ void take(const float (&x)[n]) {
+  __device__ __forceinline__ float terms(const float (&x)[n]) const {
     const float base = ref == -INFINITY ? 0.f : -ref;
     const float2 minus = make_float2(base, base), log2e = make_float2(kLog2e, kLog2e);
     float2 part = make_float2(0.f, 0.f);
@@ -145,7 +158,12 @@ struct Seen {
       const float2 e = mul2(add2(make_float2(x[i], x[i + 1]), minus), log2e);
       part = add2(part, make_float2(fast_exp2(e.x), fast_exp2(e.y)));
     }
-    sum += part.x + part.y;
+    return part.x + part.y;
+  }
+  __device__ __forceinline__ void add(float part) {
+    const float s = sum + part, t = s - sum;
+    low += (sum - (s - t)) + (part - t);
+    sum = s;
   }
 };
 
@@ -202,12 +220,14 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
       for (int j = 0; j < 4; ++j) w[j] = body[v + j * 32];
       most = most_of(w, T());
       seen.reach(most);
+      float part[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float x[kVec];
         unpack(w[j], x);
-        seen.take(x);
+        part[j] = seen.terms(x);
       }
+      seen.add((part[0] + part[1]) + (part[2] + part[3]));
     } else {  // the row's last unit
       most = -INFINITY;
       for (int i = v; i < min(r.vectors, (u + 1) * kUnit); i += 32) {
@@ -216,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
         unpack(w, x);
         const float m = most_of(w, T());
         seen.reach(m);
-        seen.take(x);
+        seen.add(seen.terms(x));
         most = fmaxf(most, m);
       }
     }
@@ -230,30 +250,32 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
         if (at < 0) continue;
         const float x = single(r.base[at]);
         seen.reach(x);
-        seen.take(x);
+        seen.add(seen.term(x));
         most = fmaxf(most, x);
       }
     }
     const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(most));
     if (lane == 0) tops[u] = top > 0 ? value_of(top) : -INFINITY;
   }
-  // maximum and sum of the CTA
+  // sum of the CTA, against its largest logit as a whole number (no thread's reference is above it): one that does not
+  // depend on which thread read what, so that rows alike have sums alike wherever they start
   const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(seen.top));
-  const float wm = top > 0 ? value_of(top) : -INFINITY;
-  float ws = seen.ref == wm ? seen.sum : seen.sum * fast_exp2((seen.ref - wm) * kLog2e);
+  const float wr = top > 0 ? rintf(value_of(top)) : -INFINITY;
+  float ws = seen.sum + seen.low;
+  if (seen.ref != wr) ws *= factor(seen.ref - wr);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-  if (lane == 0) warp_stats[warp] = make_float2(wm, ws);
+  if (lane == 0) warp_stats[warp] = make_float2(wr, ws);
   __syncthreads();
   if (warp != 0) return;
   const float2 mine = lane < kWarps ? warp_stats[lane] : make_float2(-INFINITY, 0.f);
-  float cm = mine.x;
+  float cr = mine.x;
 #pragma unroll
-  for (int o = 1; o < kWarps; o <<= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
-  float cs = mine.x == cm ? mine.y : mine.y * fast_exp2((mine.x - cm) * kLog2e);
+  for (int o = 1; o < kWarps; o <<= 1) cr = fmaxf(cr, __shfl_xor_sync(0xffffffffu, cr, o));
+  float cs = mine.x == cr ? mine.y : mine.y * factor(mine.x - cr);
 #pragma unroll
   for (int o = 1; o < kWarps; o <<= 1) cs += __shfl_xor_sync(0xffffffffu, cs, o);
-  if (lane == 0) p.stats[static_cast<int64_t>(row) * p.pieces + piece] = make_float2(cm, cs);
+  if (lane == 0) p.stats[static_cast<int64_t>(row) * p.pieces + piece] = make_float2(cr, cs);
 }
 
 // Scores as a pair of floats whose sum they are, lo at most half a step of hi (48 bits: fp64 is 50 times
@@ -269,7 +291,7 @@ __device__ __forceinline__ Pair add(Pair a, float b) {
   const Pair s = exact_sum(a.hi, b);
   return exact_sum(s.hi, s.lo + a.lo);
 }
-// ln x, of a normal x >= 2^-1 below 2^31: x = 2^e f with f in [3/4, 3/2), so that logf is off by half a step
+// ln x, of a normal x >= 2^-1 below 2^33: x = 2^e f with f in [3/4, 3/2), so that logf is off by half a step
 // of at most 0.41 (3e-8) and the rest is nearly exact; e times the high part of ln 2 (14 bits) is exact.
 __device__ __forceinline__ Pair natural_log(float x) {
   const int e = (__float_as_int(x) - 0x3f400000) >> 23;
@@ -399,10 +421,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     for (int i = 32 + lane; i < p.pieces; i += 32) m = fmaxf(m, stats[i].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    Pair sum{mine.x == m ? mine.y : mine.y * fast_exp2((mine.x - m) * kLog2e), 0.f};
+    Pair sum{mine.x == m ? mine.y : mine.y * factor(mine.x - m), 0.f};
     for (int i = 32 + lane; i < p.pieces; i += 32) {
       const float2 v = stats[i];
-      sum = add(sum, v.x == m ? v.y : v.y * fast_exp2((v.x - m) * kLog2e));
+      sum = add(sum, v.x == m ? v.y : v.y * factor(v.x - m));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -412,7 +434,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     }
     if (lane == 0) {
       // (a NaN or +inf among the logits, or nothing but -inf: no candidates)
-      const bool good = m > -INFINITY && m < INFINITY && sum.hi >= 0.5f && sum.hi < 2147483648.f;
+      // (m is within 0.5 of the largest logit: its term is e^-0.5 at least, and none is above e^0.5)
+      const bool good = m > -INFINITY && m < INFINITY && sum.hi >= 0.5f && sum.hi < 0x1p33f;
       kind[b] = good ? 1 : 0;
       if (good) {
         const Pair norm = natural_log(sum.hi);  // (sum.lo is below 2^-24 of it: ln moves by as much)
