@@ -520,9 +520,10 @@ pa_status attn_decode_paged_shared(pa_dims dims, const void* q, const void* k_po
  *               that has ended, 1 else: the new_lens of paged_step_plan when k is beams. Places without a
  *               candidate get -inf, -1, -1, 0. out_scores may be scores and live_out may be live where
  *               k = beams.
- * A beam with a NaN or +inf among its logits, or nothing but -inf, has no candidates. Within a beam the
- * order is that of its logits; scores of different beams are compared as pairs of floats (48 bits) over
- * normalisers from fp32 exponentials, off by 2^-18 (4e-6) at most for vocabularies below 2^25.
+ * A beam with a NaN or +inf among its logits, or nothing but -inf, has no candidates. Scores are compared
+ * as pairs of floats (48 bits): within a beam the order is that of its logits where they differ by more than
+ * 2^-45 of the score or of the normaliser, whichever is larger. A beam's normaliser, a sum of fp32
+ * exponentials, is off by 2^-18 (4e-6) at most for vocabularies below 2^25; that counts between beams alone.
  *   workspace   at least pa_beam_workspace_size(...) bytes, 8-byte aligned; calls that share one must not
  *               overlap on the GPU
  * ------------------------------------------------------------------------------------------ */

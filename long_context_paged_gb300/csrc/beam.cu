@@ -2,14 +2,15 @@
 //
 // Candidate (b, v) of a request has the score
 //     scores[b] + logits[b][v] - ln sum_u exp(logits[b][u])
-// and the k best are kept, equal scores in the order of (b, v). Within a beam the order is that of the
-// logits themselves, whatever the beam's score and normaliser. So one pass over a beam's logits finds its
-// normaliser (running maximum and sum) and the largest logit of every unit, 2 KB of the row. With all beams'
+// and the k best are kept, equal scores in the order of (b, v). Within a beam that is the order of the logits
+// themselves, whatever the beam's score and normaliser. So one pass over a beam's logits finds its
+// normaliser (a sum against a running reference) and the largest logit of every unit, 2 KB of the row. With all beams'
 // normalisers known the units are ordered by the scores of those (equal ones as they lie): the k best
 // candidates are all in the k best units, since each of these has one candidate at least that comes before
 // all of any other unit. The second launch looks through those k units alone. Scores are formed as pairs of
-// floats there (48 bits): what decides between beams is the normalisers' precision (fp32 sums of
-// exponentials), not the rounding of a sum of large parts.
+// floats there (48 bits; logits of a beam that differ by less than 2^-45 of its score may count as equal, or
+// change places): what decides between beams is the normalisers' precision (below: Seen), not the rounding of a sum of
+// large parts.
 //
 // The logits are read once from memory. A row is cut into pieces so that a few rows still fill the GPU; a CTA
 // takes a piece, a warp a unit, a lane four 16-byte vectors of it. Measured on a GB300 (calls of a graph): 64 x 8 rows
