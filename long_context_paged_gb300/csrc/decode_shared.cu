@@ -100,14 +100,14 @@ struct Segment {
   int32_t row, rows;         // query rows
   int32_t table_row;         // whose table entries are read
   int32_t first_key, end_key;
-  int32_t index;             // among the segments of shared pages; ~index among the rows' own
+  int32_t place;             // of its results among those of shared pages, in rows; ~place among those of the rows' own
 };
 
-// Where a row's partial results are: its segment of shared pages and its own, in units and as an index
-// into the results (units = 0: none).
+// Where a row's partial results are: its segment of shared pages and its own, in units and as places among
+// the results (units = 0: none).
 struct RowPlan {
-  int32_t tile_unit, tile_units, tile, in_tile;  // in_tile: the row's place in it
-  int32_t own_unit, own_units, own, pad;
+  int32_t tile_unit, tile_units, tile, in_tile;  // in_tile: the row's place in the segment
+  int32_t own_unit, own_units, own, tile_rows;   // tile_rows: the segment's rows
 };
 
 // A slice: its units, the segment of the first one, and what all slices have alike.
@@ -126,7 +126,7 @@ struct SharedParams {
   int64_t num_pages;
   float scale_log2;
   int32_t slices;       // CTAs per KV head
-  int32_t tile_rows;    // capacity of a shared segment's partial results, in rows
+  int32_t tile_rows;    // most rows of a shared segment
   uint16_t* out;
   float* lse;
   int32_t* status;
@@ -134,9 +134,16 @@ struct SharedParams {
   Segment* segments;
   Segment* own_segments;   // [CTAs][kOwnPlanSegments]
   RowPlan* rows;           // [batch]
-  float* tile_parts;       // [slices + tiles][hkv][2 streams][2 tile_rows][128], then (m, l)
-  float* row_parts;        // [slices + batch][hkv][2 streams][2][128], then (m, l)
+  // Partial results: of a piece of R rows [hkv][2 streams]([2 R][128], then (m, l) of each), where the results of
+  // (slice, place) begin, in rows. A segment of shared pages with many rows has its first row for its place, one
+  // with few rows that and `batch` (they come after all of those); a row's own segment, its number among those. Places
+  // go up by a segment's rows from one to the next, and the slices' starts by tile_rows, so pieces, which go up in
+  // both, do not overlap.
+  float* tile_parts;       // slices * tile_rows + 2 * batch rows
+  float* row_parts;        // slices + batch rows
 };
+
+constexpr int kPartFloats = 2 * 2 * kRowFloats;  // of a row and KV head: two streams, two query heads
 
 // ---------------------------------------------------------------------------------------------
 // plan
@@ -154,7 +161,7 @@ struct PlanSmem {
   // groups: first row, shared pages, first row that uses them; segments and units before the group's of
   // many rows, and before its one of few
   int32_t cu[kGroups + 1], shared[kGroups], first[kGroups];
-  int32_t many_seg[kGroups], many_unit[kGroups], few_seg[kGroups], few_unit[kGroups];
+  int32_t many_unit[kGroups], few_seg[kGroups], few_unit[kGroups];
   // rows: keys, last group that starts at or before the row (-1: none), pages that it shares; segments
   // and units of own pages before the row's
   int32_t len[kRows], group[kRows], start[kRows];
@@ -318,12 +325,11 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       const int rows = rows_of(g), few = few_of(rows), units = units_of(s.shared[g] * kPage);
-      s.many_seg[g] = seg;
       s.many_unit[g] = unit;
 #pragma unroll 1
       for (int r = 0; r < rows - few; r += kTileRows) {
         put(seg, Segment{unit, units, s.cu[g] + r, min(kTileRows, rows - few - r), s.first[g], 0,
-                         s.shared[g] * kPage, seg});
+                         s.shared[g] * kPage, s.cu[g] + r});
         ++seg;
         unit += units;
       }
@@ -361,7 +367,7 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
     const int row = s.cu[g], seg = many_tiles + s.few_seg[g] + s.own_seg[row];
     const int unit = many_units + s.few_unit[g] + s.own_unit[row];
     put(seg, Segment{unit, units_of(s.shared[g] * kPage), row + rows - few, few, s.first[g], 0,
-                     s.shared[g] * kPage, many_tiles + s.few_seg[g]});
+                     s.shared[g] * kPage, B + row + rows - few});
   }
 #pragma unroll 1
   for (int b = tid; b < B; b += threads) {
@@ -373,14 +379,16 @@ __device__ __forceinline__ int2 make_plan(const SharedParams& p, Smem& s, Segmen
       seg += s.few_seg[g] + (few > 0 ? 1 : 0);
       unit += s.few_unit[g] + (few > 0 ? units_of(s.shared[g] * kPage) : 0);
       if (rows_out && start > 0) {
-        const int place = in_group / kTileRows;
+        const int tile = in_group / kTileRows;
         r.tile_units = units_of(start * kPage);
         r.in_tile = in_group % kTileRows;
+        r.tile = b - r.in_tile;
         if (in_group < rows - few) {
-          r.tile = s.many_seg[g] + place;
-          r.tile_unit = s.many_unit[g] + place * r.tile_units;
+          r.tile_rows = min(kTileRows, rows - few - tile * kTileRows);
+          r.tile_unit = s.many_unit[g] + tile * r.tile_units;
         } else {
-          r.tile = many_tiles + s.few_seg[g];
+          r.tile += B;
+          r.tile_rows = few;
           r.tile_unit = many_units + s.few_unit[g] + s.own_unit[s.cu[g]];
         }
       }
@@ -571,7 +579,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
       g.table_row = __shfl_sync(0xffffffffu, lane_record.table_row, from);
       g.first_key = __shfl_sync(0xffffffffu, lane_record.first_key, from);
       g.end_key = __shfl_sync(0xffffffffu, lane_record.end_key, from);
-      g.index = __shfl_sync(0xffffffffu, lane_record.index, from);
+      g.place = __shfl_sync(0xffffffffu, lane_record.place, from);
       return g;
     };
     auto entries = [&](const Segment& g, int k) {
@@ -607,7 +615,7 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
         q_used |= 1u << qb;
       }
       if (few) next_q = qb ^ 1;
-      const bool is_tile = g.index >= 0;
+      const bool is_tile = g.place >= 0;
       for (int kb = k0; kb < k1 && ok; kb += kBatch) {
         const int ahead = kb + kBatch < k1 ? entries(g, kb + kBatch) : 0;
         for (int k = kb; k < min(kb + kBatch, k1); ++k, ++it) {
@@ -627,11 +635,9 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
           // before that one (it - 5; a slot serves every eighth).
           if (is_k && lane == 0) {
             UnitInfo& f = s.info[it % kInfos];
-            const int cap = is_tile ? 2 * p.tile_rows : 2;
-            const int64_t slot =
-                ((static_cast<int64_t>(slice) + (is_tile ? g.index : ~g.index)) * p.hkv + head) * 2;
-            f.part = slot * cap * kRowFloats;
-            f.stats = cap * kHeadDim;
+            const int from = is_tile ? slice * p.tile_rows + g.place : slice + ~g.place;  // (below 2^15)
+            f.part = (static_cast<int64_t>(from) * p.hkv + head * g.rows) * kPartFloats;
+            f.stats = 2 * g.rows * kHeadDim;
             f.keys = keys;
             f.flags = (k - k0 < 2 ? kFirst : 0) | (k1 - 1 - k < 2 ? kLast : 0) | (k == k0 ? kPieceStart : 0) |
                       (k == k1 - 1 ? kPieceEnd : 0) | (qb ? kQBuffer1 : 0) | (few ? kFewFlag : 0);
@@ -1141,15 +1147,16 @@ __global__ void __launch_bounds__(kWarps * 32) shared_merge_kernel(const SharedP
     const int set = c < count[0] ? 0 : 1, at = set == 0 ? c : c - count[0];
     const int i = (set == 0 ? i0[0] : i0[1]) + (at >> 1), stream = at & 1;
     const int unit = set == 0 ? row.tile_unit : row.own_unit, units = set == 0 ? row.tile_units : row.own_units;
-    const int cap = set == 0 ? 2 * p.tile_rows : 2, r = set == 0 ? 2 * row.in_tile : 0;
+    const int rows = set == 0 ? row.tile_rows : 1, r = set == 0 ? 2 * row.in_tile : 0;
     const int first = over(static_cast<uint64_t>(U) * i, n), end = over(static_cast<uint64_t>(U) * (i + 1), n);
     const int u0 = max(first, unit), u1 = min(end, unit + units);
     // units alternate between the streams, from the slice's first
     const bool there = u1 - u0 >= 2 || (u1 - u0 == 1 && ((u0 - first) & 1) == stream);
+    const int from = set == 0 ? i * p.tile_rows + row.tile : i + row.own;
     const float* part = (set == 0 ? p.tile_parts : p.row_parts) +
-                        (((static_cast<int64_t>(i) + (set == 0 ? row.tile : row.own)) * p.hkv + head) * 2 + stream) * cap * kRowFloats;
+                        (static_cast<int64_t>(from) * p.hkv + head * rows) * kPartFloats + stream * 2 * rows * kRowFloats;
     where[c] = there ? part + r * kHeadDim : nullptr;
-    stat[c] = there ? *reinterpret_cast<const float4*>(part + cap * kHeadDim + 2 * r)
+    stat[c] = there ? *reinterpret_cast<const float4*>(part + 2 * rows * kHeadDim + 2 * r)
                     : make_float4(-CUDART_INF_F, 0.f, -CUDART_INF_F, 0.f);
   }
   __syncthreads();
@@ -1236,9 +1243,9 @@ bool shared_layout(SharedLayout& l, int hkv, int batch, int groups, int max_grou
   l.own_segments = align256(l.segments + (l.own_plan ? 0 : sizeof(Segment) * (tiles + batch)));
   l.rows = align256(l.own_segments + (l.own_plan ? sizeof(Segment) * kOwnPlanSegments * l.slices * hkv : 0));
   l.tile_parts = align256(l.rows + sizeof(RowPlan) * batch);
-  const size_t per_row = static_cast<size_t>(hkv) * 2 * 2 * kRowFloats * sizeof(float);
-  l.row_parts = align256(l.tile_parts + (groups > 0 ? (l.slices + tiles) * l.tile_rows * per_row : 0));
-  l.total = align256(l.row_parts + (static_cast<size_t>(l.slices) + batch) * per_row);
+  const size_t per_row = static_cast<size_t>(hkv) * kPartFloats * sizeof(float), slices = static_cast<size_t>(l.slices);
+  l.row_parts = align256(l.tile_parts + (groups > 0 ? (slices * l.tile_rows + 2 * static_cast<size_t>(batch)) * per_row : 0));
+  l.total = align256(l.row_parts + (slices + batch) * per_row);
   return true;
 }
 
