@@ -483,7 +483,6 @@ shared_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_
                         const __grid_constant__ CUtensorMap v_map, const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  launch_next();
   SharedSmem& s = *reinterpret_cast<SharedSmem*>(smem_raw);
   const int head = static_cast<int>(blockIdx.x) % p.hkv, slice = static_cast<int>(blockIdx.x) / p.hkv;
   if ((smem_addr(smem_raw) & 1023u) != 0) {  // not the layout this kernel was built for
