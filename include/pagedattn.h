@@ -468,6 +468,8 @@ pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t interleaved,
  * The result is attn_decode_paged's up to rounding: row b attends to its seq_lens[b] keys. Weights are held to
  * 2^-15 of each, but those of shared pages that more than 8 rows have in common are rounded to bf16 (2^-8), as the
  * prefill's are. (Rows of a group are taken 64 at a time; a last part of up to 8 counts as so few.)
+ * attn_decode_paged takes the same tables, and is the quicker call for one group of R rows over n keys while
+ * (R - 1) n is below about 27,000. There are no score options and no pa_launch_opts here.
  *   cu_group_rows  int32 [groups + 1]: group g is rows cu_group_rows[g] .. cu_group_rows[g+1]-1;
  *                  rows in no group share nothing
  *   shared_pages   int32 [groups]: leading pages that the group's rows have in common: the caller

@@ -885,7 +885,10 @@ def attn_decode_paged_shared(q, k_pool, v_pool, block_table, seq_lens, cu_group_
     keys of those pages are read once for the group. q [B, Hq, D]; returns (out, lse).
 
     max_group_rows: host bound of a group's rows (default: B). Rows in no group share nothing; a row
-    with fewer keys than the shared pages hold reads its own entries alone."""
+    with fewer keys than the shared pages hold reads its own entries alone. Weights of pages that more
+    than 8 rows share are rounded to bf16, all others are kept as attn_decode_paged keeps them. That call takes
+    the same tables and is the quicker one for one group of R rows over n keys while (R - 1) n is below
+    about 27,000. No score options and no max_ctas here."""
     call, i32 = "attn_decode_paged_shared", torch.int32
     if _FAST is not None:
         o, l = _attn_outputs(q, out, lse, want_lse, stream)

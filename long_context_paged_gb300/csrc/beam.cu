@@ -14,9 +14,9 @@
 //
 // The logits are read once from memory. A row is cut into pieces so that a few rows still fill the GPU; a CTA
 // takes a piece, a warp a unit, a lane four 16-byte vectors of it. Measured on a GB300 (calls of a graph): 64 x 8 rows
-// of 151,936 in bf16 36 us (147 MB: 21.6 us at a copy's rate), the first launch 25 of them, its instructions (5 an
-// element to unpack, exponentiate and add) half of what the SMs can issue; 16 x 5 rows of 51,865 in fp32 12 us; one
-// request 7 us. The second launch is a chain of some 1,000 instructions of each warp: normalisers 2 us, units 3,
+// of 151,936 in bf16 36.5 us (147 MB: 21.6 us at a copy's rate), the first launch 25 of them, its instructions (5 an
+// element to unpack, exponentiate and add) 0.6 of what the SMs can issue; 16 x 5 rows of 51,865 in fp32 12.4 us; one
+// request 7.5 us. The second launch is a chain of some 1,000 instructions of each warp: normalisers 2 us, units 3,
 // candidates 2.5. Choosing each piece's k largest in the first launch, for the second to join, took 41.4, 14.6 and
 // 8.5 us (all of a piece's warps wait for its selection, three times); rounds of a block-wide maximum there 477 us
 // for the first of these; scores in fp64 in the second launch cost it 4 us (this GPU's fp64 rate is 1/60 of fp32's).
@@ -45,8 +45,8 @@ constexpr int kUnits = 512;  // units that the quick choice of them holds
 constexpr int kPickFew = 512, kPickMany = 1024;
 constexpr int kFound = 512;  // candidates that the quick ranking holds
 constexpr int kFewFound = 128;  // so few are ranked sooner than a closer bound is found
-// Pieces of a row: as many as give kTargetCtas CTAs in all (three rounds of the six that an SM holds), none of them
-// below a unit a warp. 64 x 8 rows with 912, 1,824, 2,736 and 5,472: 41.5, 39.4, 38.5 and 39.5 us at one stage of
+// Pieces of a row: as many as give kTargetCtas CTAs in all (three rounds of the six that an SM holds), and at most
+// one for every kWarps units or part of that many (9 units: pieces of 5 and 4, some warps without one). 64 x 8 rows with 912, 1,824, 2,736 and 5,472: 41.5, 39.4, 38.5 and 39.5 us at one stage of
 // this kernel; registers for seven or eight CTAs an SM: 36 -> 38.
 constexpr int kTargetCtas = 2736;
 

@@ -11,10 +11,13 @@
 //
 // Measured on a GB300 (calls of a graph, 152 CTAs): 16 groups of 4 rows over 5,000 to 30,000 keys 155 us,
 // 6.3 TB/s of the bytes that have to be read (0.93 of a copy's rate; 64 rows read alone would be 3.7 GB);
-// 8 rows over 67,500 keys 60 us, of which the units take 41 (6.7 TB/s), the plan 3.5, the first copies 3.7,
-// the merge and its start 5 and the slowest CTA 4; 4 rows over 1,000 keys 14 us, a chain of latencies;
+// 8 rows over 67,500 keys 59 us, of which the units take 41 (6.7 TB/s), the plan 3.5, the first copies 3.7,
+// the merge and its start 5 and the slowest CTA 4; 4 rows over 1,000 keys 13.4 us, a chain of latencies;
 // 307 rows in 4 groups 85 us, of which the units take 62 (64 rows a pass: three passes over the keys of 131
-// rows; about 290 of the 955 units a head are of such tiles, the others of few or single rows), the plan 4, the slowest CTA 6, the merge 6.
+// rows; about 290 of the 955 units a head are of such tiles, the others of few or single rows), the plan 4, the
+// slowest CTA 6, the merge 6. Short calls of few rows are quicker as attn_decode_paged, which reads a shared key
+// once a row, in one launch: for one group of R rows over n keys up to about (R - 1) n = 27,000 (4 rows over 1,000
+// keys 6.5 us, 2 over 16,000 22 and 24, 8 over 3,000 17 and 18).
 //
 // Work split. A segment is a run of keys with the rows that see all of it: (64 rows of a group, its
 // shared pages) or (one row, its own pages). Segments are cut into units of 128 keys, laid end to end
