@@ -488,7 +488,7 @@ pa_status rope_append_paged(pa_dims dims, int32_t rot_dim, int32_t interleaved,
  *                  share one must not overlap on the GPU.
  * A row without keys gets o = 0, lse = -inf; so does a row whose scores are all -inf. NaN and
  * infinities in keys that a row sees give what the formula gives (a weight of 0 times an infinity is
- * NaN); other rows are unmoved, those of the same group too unless the key is a shared one.
+ * NaN, one below 2^-90 of the row's largest may be); other rows are unmoved, those of the same group too unless the key is a shared one.
  * ------------------------------------------------------------------------------------------ */
 size_t pa_decode_shared_workspace_size(pa_dims dims, int32_t batch, int32_t groups,
                                        int32_t max_group_rows);

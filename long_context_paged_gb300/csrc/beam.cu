@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
     if (lane == 0) tops[u] = top > 0 ? value_of(top) : -INFINITY;
   }
   // sum of the CTA, against its largest logit as a whole number (no thread's reference is above it): one that does not
-  // depend on which thread read what, so that rows alike have sums alike wherever they start
+  // depend on which thread read what (rows alike that start elsewhere in 16 bytes then differ by roundings at most, and
+  // mostly not at all)
   const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(seen.top));
   const float wr = top > 0 ? rintf(value_of(top)) : -INFINITY;
   float ws = seen.sum + seen.low;
